@@ -304,6 +304,144 @@ int gpt_serve_tokens(gpt* h, int32_t* dst, int32_t cap, int32_t* n);
 int gpt_serve_end(gpt* h);
 
 /*
+ * Operators of one batched decode step, for programs that serve many sequences
+ * at once from a paged key-value cache (an addition of this library: the
+ * serving partition above decodes one sequence from a contiguous cache).  Each
+ * is one call on cuda_stream that does not synchronise, allocates nothing and
+ * may be captured into a CUDA graph; the current device is the one the pointers
+ * belong to.  Sums, softmax statistics and rotations are fp32; results are
+ * bitwise repeatable.  Errors: INVALID_ARG, UNSUPPORTED, CUDA (text via
+ * gpt_last_error(NULL)); nothing is launched on an error.
+ *
+ * Indices that live on the device (positions, sequence numbers, lengths, page
+ * and token ids) are checked by the kernels: what they name outside its range is
+ * neither read nor written, and its bit is OR-ed into *status (DEVICE uint32,
+ * may be NULL; the caller zeroes it and reads it when it wants to).
+ */
+#define GPT_STATUS_BAD_SEQ   1u  /* a sequence number >= n_seq                              */
+#define GPT_STATUS_BAD_POS   2u  /* a position or length outside the page table's reach,
+                                    or a negative length                                   */
+#define GPT_STATUS_BAD_PAGE  4u  /* a page id outside [0, n_pages)                          */
+#define GPT_STATUS_BAD_TOKEN 8u  /* a token id outside [0, vocab)                           */
+
+/*
+ * Keys and values of n_seq sequences in pages of page_size positions: position p
+ * of sequence s is slot p % page_size of page page_table[s*table_stride +
+ * p / page_size], and element i of head h of a slot is at
+ * page*page_stride + slot*slot_stride + head*head_stride + i (elements, k and v
+ * alike; any order of pages, slots and heads).  Base addresses and strides are
+ * multiples of 16 bytes, strides are not negative; head_dim is a multiple of 16
+ * bytes and <= 128.  Sequences may share pages.
+ */
+typedef struct gpt_paged_cache {
+  void *k, *v;               /* DEVICE, of type dtype                               */
+  const int32_t* page_table; /* DEVICE int32 [n_seq, max_pages]                     */
+  int64_t page_stride, slot_stride, head_stride, table_stride;
+  int32_t n_pages, page_size, n_seq, max_pages, n_kv_head, head_dim;
+  int32_t dtype;             /* GPT_DTYPE_FP32 or GPT_DTYPE_BF16: cache, q, k, v, outputs */
+} gpt_paged_cache;
+
+/*
+ * gpt_kv_append: writes the keys and values of n_tokens new tokens into the
+ * cache, rotating keys (and the queries, into q_out) on the way: the pairs
+ * (2i, 2i+1), i < rope_dims/2, of every head turn by positions[n] *
+ * rope_base^(-2i/rope_dims), the rotary form of the RTX 3090 page's model
+ * (gpt_config.rope); elements from rope_dims on, and the values, are copied.
+ * The rotation is fp32 with an angle accurate to 2^-23 of a turn at every
+ * position; one rounding to the cache's type.
+ *   k, v: DEVICE [n_tokens, n_kv_head, head_dim]; q, q_out [n_tokens, n_head,
+ *     head_dim], or NULL (both; n_head 0).  *_row, *_head: strides in elements
+ *     (multiples of 16 bytes), so one QKV projection's output serves as all
+ *     three.  q_out may be q itself with the same strides; otherwise no output
+ *     overlaps an input.
+ *   positions: DEVICE int32 [n_tokens]; seq: DEVICE int32 [n_tokens], the
+ *     sequence of each token, negative: a padding token, whose rows are neither
+ *     read nor written; NULL: token n belongs to sequence n.
+ *   Two tokens of one call at the same position of one sequence leave either's
+ *   values there.  A token with a bad index (status) is skipped whole.
+ */
+typedef struct gpt_kv_append_args {
+  const void *q, *k, *v;
+  void* q_out;
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head, qo_row, qo_head;
+  const int32_t *positions, *seq;
+  uint32_t* status;
+  double rope_base;          /* > 0; used when rope_dims > 0                        */
+  int32_t n_tokens, n_head;
+  int32_t rope_dims;         /* even, 0 (no rotation) .. head_dim                   */
+} gpt_kv_append_args;
+int gpt_kv_append(const gpt_paged_cache* cache, const gpt_kv_append_args* args, void* cuda_stream);
+
+/*
+ * gpt_decode_attention: attention of one new token of every sequence over the
+ * first lens[s] positions of its pages (the new token's own key among them):
+ * out[s, h] = softmax(scale q[s, h] . K) V with the keys and values of head
+ * h / (n_head / n_kv_head).  lens[s] == 0 gives a zero row and an lse of
+ * -infinity; a length past the table's reach is cut to it (status), keys on a
+ * bad page count as absent (status), and so do keys whose score is -infinity.
+ * Positions from lens[s] on may hold anything, NaN included.
+ *   q, out: DEVICE [n_seq, n_head, head_dim] with strides as in gpt_kv_append;
+ *   out does not overlap an input.  lse: DEVICE fp32 [n_seq, n_head] (natural
+ *   log of the sum of exponentials of the scaled scores) or NULL.
+ *   workspace: DEVICE scratch of gpt_decode_attention_workspace bytes, 16-byte
+ *     aligned, for this call alone until it has run; its content does not matter.
+ */
+typedef struct gpt_decode_attention_args {
+  const void* q;
+  void* out;
+  float* lse;
+  const int32_t* lens;       /* DEVICE int32 [n_seq]                                */
+  int64_t q_row, q_head, out_row, out_head;
+  void* workspace;
+  size_t workspace_bytes;
+  uint32_t* status;
+  float scale;
+  int32_t n_head;            /* a multiple of n_kv_head                             */
+} gpt_decode_attention_args;
+int gpt_decode_attention(const gpt_paged_cache* cache, const gpt_decode_attention_args* args, void* cuda_stream);
+
+/* Host-only: the workspace a gpt_decode_attention call with this cache and
+ * n_head needs (0 for arguments the call would refuse, or where none is needed). */
+size_t gpt_decode_attention_workspace(const gpt_paged_cache* cache, int32_t n_head);
+
+/*
+ * gpt_next_token: what stands between the logits and the choice of a token, for
+ * `rows` rows of `vocab` logits z.  For a token i of row b, each step rounded to
+ * fp32 on its own:
+ *   i in history[b][0 .. history_lens[b]):  z = z > 0 ? z / repetition[b] : z * repetition[b]
+ *   z = z - frequency[b] * c,  c: occurrences of i in history[b][prompt_lens[b] .. history_lens[b])
+ *   z = z - presence[b]        if c > 0
+ *   z = z + (the sum, in order of j, of bias_values[b][j] with bias_ids[b][j] == i)
+ *   z = -infinity              if bit i % 32 of allowed[b][i / 32] is 0
+ * out[b][i] = z; token[b] = the smallest id with the largest z (the serving
+ * partition's greedy choice; NaN is never chosen; -1 where no z is above
+ * -infinity); lse[b] = log sum_i exp(z_i) (-infinity where no z is above that).
+ *   logits: DEVICE [rows, vocab] of type dtype; out: DEVICE fp32 [rows, vocab],
+ *     may be logits itself (fp32, same stride).  Any of out, token and lse may
+ *     be NULL, not all.  *_stride: elements between rows; no alignment needed.
+ *   history, bias_ids: DEVICE int32, allowed: DEVICE uint32 [rows,
+ *     ceil(vocab / 32)]; history, repetition, presence, frequency, bias_ids,
+ *     allowed may be NULL: that step falls away.  history_lens NULL: max_history
+ *     each; prompt_lens NULL: 0 each.  Negative bias ids are unused entries;
+ *     ids >= vocab, and history ids outside [0, vocab), are skipped (status).
+ */
+typedef struct gpt_next_token_args {
+  const void* logits;
+  float* out;
+  int32_t* token;
+  float* lse;
+  const int32_t *history, *history_lens, *prompt_lens;
+  const float *repetition, *presence, *frequency;  /* DEVICE fp32 [rows]            */
+  const int32_t* bias_ids;
+  const float* bias_values;
+  const uint32_t* allowed;
+  uint32_t* status;
+  int64_t logits_stride, out_stride, history_stride, bias_stride, allowed_stride;
+  int32_t rows, vocab, dtype, max_history, n_bias;
+} gpt_next_token_args;
+int gpt_next_token(const gpt_next_token_args* args, void* cuda_stream);
+
+/*
  * Measurement hook (per-phase timing, after the per-family table of
  * "Coppelius training on the RTX 3090", section "Where a step's time goes"):
  * runs the operations op_first .. op_first + op_count - 1 of the handle's step

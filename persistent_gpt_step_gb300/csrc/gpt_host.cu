@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "../../include/gpt.h"
+#include "decode_ops.h"
 #include "graph.h"
 #include "launch.h"
 
@@ -1307,6 +1308,20 @@ int train_steps(gpt* h, const int32_t* tokens, const int32_t* targets, int32_t k
 // ============================================================================
 // C ABI
 // ============================================================================
+namespace pgs {
+int call_error(int code, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  g_create_error = buf;
+  return code;
+}
+
+void clear_call_error() { g_create_error.clear(); }
+}  // namespace pgs
+
 extern "C" {
 
 void gpt_default_config(gpt_config* c) {

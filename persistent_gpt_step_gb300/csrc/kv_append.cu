@@ -1,0 +1,140 @@
+// kv_append.cu — gpt_kv_append: keys and values of new tokens into a paged
+// cache, keys and queries rotated on the way.
+//
+// Pair i of a head turns by t = p base^(-2i/R) at position p.  In turns,
+// t / 2pi = p f with f = base^(-2i/R) / 2pi computed on the host in double and
+// passed as two floats f_hi + f_lo.  p is split into a multiple of 2^16 and the
+// rest, both exact floats; fma gives what the rounded products with f_hi leave
+// over, whole turns drop out of every term exactly, and sincospi needs no further
+// range reduction.  The angle is good to 2^-24 of a turn below position 2^24
+// (2^-20 up to 2^31), where the fp32 product p base^(-2i/R) is off by 2^-25 p.
+#include <cmath>
+
+#include "decode_ops.h"
+
+namespace pgs {
+namespace {
+
+constexpr int kMaxPairs = 64;  // head_dim <= 128
+
+struct AppendParams {
+  gpt_paged_cache c;
+  gpt_kv_append_args a;
+  float f_hi[kMaxPairs], f_lo[kMaxPairs];
+};
+
+__device__ __forceinline__ float part_turn(float x) { return x - rintf(x); }
+
+__device__ __forceinline__ void pair_angle(const AppendParams& p, int i, int pos, float* cs, float* sn) {
+  const float hi = (float)(pos & ~0xffff), lo = (float)(pos & 0xffff);
+  const float f = p.f_hi[i], a = hi * f, b = lo * f;
+  const float rest = part_turn(fmaf(hi, f, -a)) + fmaf(lo, f, -b) + (float)pos * p.f_lo[i];
+  const float t = part_turn(part_turn(a) + part_turn(b)) + rest;
+  sincospif(2.0f * t, sn, cs);
+}
+
+// One block per token; a thread per 16-byte piece of a head's row, looping over heads.
+template <typename T>
+__global__ void __launch_bounds__(128) kv_append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int kN = Piece<T>::kN;
+  const gpt_paged_cache& c = p.c;
+  const gpt_kv_append_args& a = p.a;
+  const int64_t n = blockIdx.x;
+  const int s = a.seq ? a.seq[n] : (int)n;
+  if (s < 0) return;  // padding
+  const int pos = a.positions[n];
+  const bool bad_seq = s >= c.n_seq;
+  const bool bad_pos = pos < 0 || pos >= c.max_pages * c.page_size;
+  int page = -1;
+  if (!bad_seq && !bad_pos) page = c.page_table[s * c.table_stride + pos / c.page_size];
+  const bool bad_page = !bad_seq && !bad_pos && (page < 0 || page >= c.n_pages);
+  if (bad_seq || bad_pos || bad_page) {
+    if (threadIdx.x == 0)
+      set_status(a.status, (bad_seq ? GPT_STATUS_BAD_SEQ : 0) | (bad_pos ? GPT_STATUS_BAD_POS : 0) |
+                               (bad_page ? GPT_STATUS_BAD_PAGE : 0));
+    return;
+  }
+  const int64_t slot = page * c.page_stride + (pos % c.page_size) * c.slot_stride;
+  const int pieces = c.head_dim / kN;
+  const int rows = a.n_head + 2 * c.n_kv_head;  // q heads, k heads, v heads
+  for (int w = threadIdx.x; w < rows * pieces; w += blockDim.x) {
+    const int row = w / pieces, e = (w % pieces) * kN;
+    const T* src;
+    T* dst;
+    int h = row;
+    bool turn = true;
+    if (h < a.n_head) {
+      src = (const T*)a.q + n * a.q_row + h * a.q_head;
+      dst = (T*)a.q_out + n * a.qo_row + h * a.qo_head;
+    } else if ((h -= a.n_head) < c.n_kv_head) {
+      src = (const T*)a.k + n * a.k_row + h * a.k_head;
+      dst = (T*)c.k + slot + h * c.head_stride;
+    } else {
+      h -= c.n_kv_head;
+      src = (const T*)a.v + n * a.v_row + h * a.v_head;
+      dst = (T*)c.v + slot + h * c.head_stride;
+      turn = false;
+    }
+    uint4 u = *reinterpret_cast<const uint4*>(src + e);
+    if (turn && e < a.rope_dims) {
+      float x[kN];
+      Piece<T>::unpack(u, x);
+#pragma unroll
+      for (int j = 0; j < kN; j += 2)
+        if (e + j < a.rope_dims) {
+          float cs, sn;
+          pair_angle(p, (e + j) / 2, pos, &cs, &sn);
+          const float x0 = x[j], x1 = x[j + 1];
+          x[j] = x0 * cs - x1 * sn;
+          x[j + 1] = x0 * sn + x1 * cs;
+        }
+      u = Piece<T>::pack(x);
+    }
+    *reinterpret_cast<uint4*>(dst + e) = u;
+  }
+}
+
+}  // namespace
+}  // namespace pgs
+
+using namespace pgs;
+
+extern "C" int gpt_kv_append(const gpt_paged_cache* c, const gpt_kv_append_args* a, void* cuda_stream) {
+  clear_call_error();
+  if (const int rc = check_cache(c)) return rc;
+  if (!a) return call_error(GPT_ERR_INVALID_ARG, "args must be non-NULL");
+  const int es = elem_size(c->dtype);
+  if (a->n_tokens < 0 || a->n_head < 0) return call_error(GPT_ERR_INVALID_ARG, "n_tokens and n_head must not be negative");
+  if (a->rope_dims < 0 || a->rope_dims > c->head_dim || (a->rope_dims & 1))
+    return call_error(GPT_ERR_INVALID_ARG, "rope_dims %d: even, from 0 to head_dim %d", a->rope_dims, c->head_dim);
+  if (a->rope_dims > 0 && !(a->rope_base > 0 && std::isfinite(a->rope_base)))
+    return call_error(GPT_ERR_INVALID_ARG, "rope_base must be positive and finite");
+  if (a->n_tokens == 0) return GPT_OK;
+  if (c->n_seq == 0) return call_error(GPT_ERR_INVALID_ARG, "the cache has no sequences");
+  if (!a->k || !a->v || !a->positions) return call_error(GPT_ERR_INVALID_ARG, "k, v and positions must be non-NULL");
+  if (!a->seq && a->n_tokens > c->n_seq)
+    return call_error(GPT_ERR_INVALID_ARG, "%d tokens without seq, but %d sequences", a->n_tokens, c->n_seq);
+  if (!aligned16(a->k) || !aligned16(a->v) || !stride16(a->k_row, es) || !stride16(a->k_head, es) ||
+      !stride16(a->v_row, es) || !stride16(a->v_head, es))
+    return call_error(GPT_ERR_INVALID_ARG, "k and v addresses and strides must be multiples of 16 bytes");
+  if ((a->n_head > 0) != (a->q != nullptr) || (a->n_head > 0) != (a->q_out != nullptr))
+    return call_error(GPT_ERR_INVALID_ARG, "q and q_out go with n_head > 0, and only with it");
+  if (a->n_head > 0 && (!aligned16(a->q) || !aligned16(a->q_out) || !stride16(a->q_row, es) || !stride16(a->q_head, es) ||
+                        !stride16(a->qo_row, es) || !stride16(a->qo_head, es)))
+    return call_error(GPT_ERR_INVALID_ARG, "q and q_out addresses and strides must be multiples of 16 bytes");
+  AppendParams p;
+  p.c = *c;
+  p.a = *a;
+  if (a->rope_dims > 0) {
+    const double step = std::pow(a->rope_base, -2.0 / a->rope_dims);
+    double f = 1.0 / 6.283185307179586476925;  // base^(-2i/R) / 2pi
+    for (int i = 0; i < a->rope_dims / 2; ++i, f *= step) {
+      p.f_hi[i] = (float)f;
+      p.f_lo[i] = (float)(f - (double)p.f_hi[i]);
+    }
+  }
+  const cudaStream_t st = (cudaStream_t)cuda_stream;
+  if (c->dtype == GPT_DTYPE_BF16) kv_append_kernel<__nv_bfloat16><<<a->n_tokens, 128, 0, st>>>(p);
+  else kv_append_kernel<float><<<a->n_tokens, 128, 0, st>>>(p);
+  return check_launch("gpt_kv_append");
+}
