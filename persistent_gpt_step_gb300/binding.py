@@ -141,10 +141,11 @@ SIGNATURES = [
                                    POINTER(c_int32), c_int32]),
     ("gpt_train_step_static", c_int, [POINTER(gpt_config), c_void_p, c_void_p, c_void_p, c_int64,
                                       c_void_p, c_void_p, POINTER(c_float), c_void_p]),
-    ("gpt_kv_append", c_int, [POINTER(gpt_paged_cache), POINTER(gpt_kv_append_args), c_void_p]),
-    ("gpt_decode_attention", c_int, [POINTER(gpt_paged_cache), POINTER(gpt_decode_attention_args), c_void_p]),
-    ("gpt_decode_attention_workspace", c_size_t, [POINTER(gpt_paged_cache), c_int32]),
-    ("gpt_next_token", c_int, [POINTER(gpt_next_token_args), c_void_p]),
+    # structs by address: a ctypes byref, or bytes packed by the decode module
+    ("gpt_kv_append", c_int, [c_void_p, c_void_p, c_void_p]),
+    ("gpt_decode_attention", c_int, [c_void_p, c_void_p, c_void_p]),
+    ("gpt_decode_attention_workspace", c_size_t, [c_void_p, c_int32]),
+    ("gpt_next_token", c_int, [c_void_p, c_void_p]),
     ("gpt_test_attention", c_int, [c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p, c_void_p,
                                    c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
     ("gpt_test_gemm", c_int, [c_int32, c_int32, c_int32, c_int32, c_void_p, c_int64, c_int32,
@@ -582,207 +583,13 @@ def test_attention(qkv, dout, B: int, T: int, H: int, d: int, stream=None):
     return o, lse, dqkv
 
 
-# -- operators of a batched decode step ---------------------------------------
-# Tensor arguments are checked here (device, type, shape, strides); indices that
-# live on the device are checked by the kernels (``status``).
-
-def _refuse(msg):
-    raise GptError(-1, msg)
+_DECODE = ("kv_append", "decode_attention", "next_token")
 
 
-def _op_tensor(name, t, dtype, shape, device):
-    """A CUDA tensor of this type and shape on ``device``, its elements side by side."""
-    if t.dtype is not dtype:
-        _refuse(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        _refuse(f"{name} is on {t.device}, not on {device}")
-    if t.shape != shape:
-        _refuse(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        _refuse(f"the last dimension of {name} must be contiguous")
-    return t.data_ptr()
-
-
-def _op_strides(t):
-    """Strides of all dimensions but the last; 0 where a dimension has one entry, whose stride says nothing."""
-    return [st if n > 1 else 0 for n, st in zip(t.shape[:-1], t.stride())]
-
-
-def _op_device(name, t):
-    """The device of a call: that of its first tensor, which must be the current one."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        _refuse(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        _refuse(f"{name} is on {t.device}, not the current device")
-    return t.device
-
-
-_OP_TYPES = {"torch.float32": DTYPE_FP32, "torch.bfloat16": DTYPE_BF16}
-
-
-def _op_dtype(name, t):
-    got = _OP_TYPES.get(str(t.dtype))
-    if got is None:
-        _refuse(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    return got
-
-
-def _op_cache(k_cache, v_cache, page_table, device):
-    import torch
-    if k_cache.dim() != 4:
-        _refuse("k_cache must be [pages, page size, heads, head size]")
-    shape, stride = k_cache.shape, _op_strides(k_cache)
-    if _op_strides(v_cache) != stride:
-        _refuse("k_cache and v_cache must have the same strides")
-    if page_table.dim() != 2:
-        _refuse("page_table must be [sequences, pages]")
-    c = gpt_paged_cache(k=_op_tensor("k_cache", k_cache, k_cache.dtype, shape, device),
-                        v=_op_tensor("v_cache", v_cache, k_cache.dtype, shape, device),
-                        page_table=_op_tensor("page_table", page_table, torch.int32, page_table.shape, device),
-                        page_stride=stride[0], slot_stride=stride[1], head_stride=stride[2],
-                        table_stride=page_table.stride(0), n_pages=shape[0], page_size=shape[1],
-                        n_seq=page_table.shape[0], max_pages=page_table.shape[1], n_kv_head=shape[2],
-                        head_dim=shape[3], dtype=_op_dtype("k_cache", k_cache))
-    return c
-
-
-def _op_run(fn, *args, stream):
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    rc = fn(*args, c_void_p(s.cuda_stream))
-    if rc != GPT_OK:
-        raise GptError(rc, _lib.gpt_last_error(None).decode())
-
-
-def _op_empty(shape, dtype, device, stream):
-    """Memory for ``stream``: the allocator reuses it in that stream's order."""
-    import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _op_status(status, device):
-    import torch
-    return None if status is None else _op_tensor("status", status, torch.int32, (1,), device)
-
-
-def kv_append(k, v, k_cache, v_cache, page_table, positions, seq=None, q=None, rope_dims: int = 0,
-              rope_base: float = 10000.0, q_out=None, status=None, stream=None):
-    """gpt_kv_append on CUDA tensors: k, v [tokens, kv heads, head size] into the paged cache
-    (k_cache, v_cache [pages, page size, kv heads, head size], page_table int32 [sequences, pages]) at
-    ``positions`` (int32 [tokens]) of sequences ``seq`` (int32 [tokens]; negative: padding; None: token n
-    is sequence n's), rotated by position over the first ``rope_dims`` elements of a head.
-
-    With q [tokens, heads, head size] returns the rotated queries (``q_out``, which may be q, or a new
-    tensor), else None.  ``status``: int32 [1] that collects STATUS_* bits."""
-    import torch
-    lib = load()
-    device = _op_device("k", k)
-    c = _op_cache(k_cache, v_cache, page_table, device)
-    n = k.shape[0]
-    kv = (n, c.n_kv_head, c.head_dim)
-    dtype = k_cache.dtype
-    a = gpt_kv_append_args(k=_op_tensor("k", k, dtype, kv, device), v=_op_tensor("v", v, dtype, kv, device),
-                           positions=_op_tensor("positions", positions, torch.int32, (n,), device),
-                           seq=None if seq is None else _op_tensor("seq", seq, torch.int32, (n,), device),
-                           status=_op_status(status, device), rope_base=rope_base, rope_dims=rope_dims, n_tokens=n)
-    (a.k_row, a.k_head), (a.v_row, a.v_head) = _op_strides(k), _op_strides(v)
-    if q is not None:
-        shape = (n, q.shape[1], c.head_dim)
-        if q_out is None:
-            q_out = _op_empty(shape, dtype, device, stream)
-        a.n_head = shape[1]
-        a.q, a.q_out = _op_tensor("q", q, dtype, shape, device), _op_tensor("q_out", q_out, dtype, shape, device)
-        (a.q_row, a.q_head), (a.qo_row, a.qo_head) = _op_strides(q), _op_strides(q_out)
-    elif q_out is not None:
-        _refuse("q_out goes with q")
-    _op_run(lib.gpt_kv_append, byref(c), byref(a), stream=stream)
-    return q_out
-
-
-def decode_attention(q, k_cache, v_cache, page_table, lens, scale: float | None = None, out=None, status=None,
-                     stream=None):
-    """gpt_decode_attention on CUDA tensors: attention of one new token of every sequence, q [sequences,
-    heads, head size], over the first ``lens`` (int32 [sequences]) positions of its pages (cache as in
-    kv_append).  ``scale``: 1/sqrt(head size) unless given.
-
-    Returns (out like q, lse float32 [sequences, heads])."""
-    import torch
-    lib = load()
-    device = _op_device("q", q)
-    c = _op_cache(k_cache, v_cache, page_table, device)
-    if q.dim() != 3:
-        _refuse("q must be [sequences, heads, head size]")
-    shape = (c.n_seq, q.shape[1], c.head_dim)
-    dtype = k_cache.dtype
-    if out is None:
-        out = _op_empty(shape, dtype, device, stream)
-    lse = _op_empty(shape[:2], torch.float32, device, stream)
-    a = gpt_decode_attention_args(q=_op_tensor("q", q, dtype, shape, device), out=_op_tensor("out", out, dtype, shape, device),
-                                  lse=lse.data_ptr(), lens=_op_tensor("lens", lens, torch.int32, (c.n_seq,), device),
-                                  status=_op_status(status, device),
-                                  scale=c.head_dim ** -0.5 if scale is None else scale, n_head=shape[1])
-    (a.q_row, a.q_head), (a.out_row, a.out_head) = _op_strides(q), _op_strides(out)
-    need = lib.gpt_decode_attention_workspace(byref(c), a.n_head)
-    if need:
-        scratch = _op_empty((need,), torch.uint8, device, stream)
-        a.workspace, a.workspace_bytes = scratch.data_ptr(), need
-    _op_run(lib.gpt_decode_attention, byref(c), byref(a), stream=stream)
-    return out, lse
-
-
-def next_token(logits, history=None, history_lens=None, prompt_lens=None, repetition=None, presence=None,
-               frequency=None, bias_ids=None, bias_values=None, allowed=None, out=None, status=None, stream=None):
-    """gpt_next_token on CUDA tensors: logits [rows, vocab] (float32 or bfloat16) with the penalties of
-    ``history`` (int32 [rows, n]; ``history_lens``, ``prompt_lens`` int32 [rows]; ``repetition``,
-    ``presence``, ``frequency`` float32 [rows]), the biases ``bias_values`` (float32 [rows, m]) of tokens
-    ``bias_ids`` (int32 [rows, m]) and the grammar mask ``allowed`` (int32 [rows, ceil(vocab/32)], one bit
-    per token) applied; every argument but logits may be None.
-
-    Returns (token int32 [rows], out float32 [rows, vocab], lse float32 [rows]); ``out`` may be float32
-    logits themselves."""
-    import torch
-    lib = load()
-    device = _op_device("logits", logits)
-    if logits.dim() != 2:
-        _refuse("logits must be [rows, vocab]")
-    rows, vocab = logits.shape
-    a = gpt_next_token_args(rows=rows, vocab=vocab, dtype=_op_dtype("logits", logits),
-                            logits=_op_tensor("logits", logits, logits.dtype, (rows, vocab), device),
-                            logits_stride=logits.stride(0), status=_op_status(status, device))
-    if history is not None:
-        if history.dim() != 2:
-            _refuse("history must be [rows, tokens]")
-        a.max_history, a.history_stride = history.shape[1], history.stride(0)
-        a.history = _op_tensor("history", history, torch.int32, (rows, a.max_history), device)
-    for name, t in (("history_lens", history_lens), ("prompt_lens", prompt_lens)):
-        if t is not None:
-            if history is None:
-                _refuse(f"{name} goes with history")
-            ptr = _op_tensor(name, t, torch.int32, (rows,), device)
-            if a.max_history:  # a history of no columns has no memory
-                setattr(a, name, ptr)
-    for name, t in (("repetition", repetition), ("presence", presence), ("frequency", frequency)):
-        if t is not None:
-            setattr(a, name, _op_tensor(name, t, torch.float32, (rows,), device))
-    if bias_ids is not None and bias_values is not None:
-        if bias_ids.dim() != 2 or _op_strides(bias_ids) != _op_strides(bias_values):
-            _refuse("bias_ids and bias_values must be [rows, entries] with the same strides")
-        a.n_bias, a.bias_stride = bias_ids.shape[1], bias_ids.stride(0)
-        a.bias_ids = _op_tensor("bias_ids", bias_ids, torch.int32, (rows, a.n_bias), device)
-        a.bias_values = _op_tensor("bias_values", bias_values, torch.float32, (rows, a.n_bias), device)
-    elif bias_ids is not None or bias_values is not None:
-        _refuse("bias_ids and bias_values go together")
-    if allowed is not None:
-        a.allowed = _op_tensor("allowed", allowed, torch.int32, (rows, (vocab + 31) // 32), device)
-        a.allowed_stride = allowed.stride(0)
-    if out is None:
-        out = _op_empty((rows, vocab), torch.float32, device, stream)
-    a.out, a.out_stride = _op_tensor("out", out, torch.float32, (rows, vocab), device), out.stride(0)
-    token, lse = _op_empty((rows,), torch.int32, device, stream), _op_empty((rows,), torch.float32, device, stream)
-    a.token, a.lse = token.data_ptr(), lse.data_ptr()
-    _op_run(lib.gpt_next_token, byref(a), stream=stream)
-    return token, out, lse
+def __getattr__(name):
+    """The decode-step operators, from ``decode`` (which imports torch) on first use."""
+    if name in _DECODE:
+        from . import decode
+        globals().update((n, getattr(decode, n)) for n in _DECODE)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

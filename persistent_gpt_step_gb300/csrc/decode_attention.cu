@@ -1,5 +1,34 @@
 // decode_attention.cu — gpt_decode_attention: attention of one new token of
 // every sequence over its pages of keys and values.
+//
+// Mathematics: with z_j = scale q.k_j, any set of keys reduces to (m, l, o) =
+// (reference m, sum 2^(z_j - m), sum 2^(z_j - m) v_j), and sets join by bringing
+// them to a common m; the output is o / l, the lse m + log l.  Scores are kept in
+// base 2 (scale log2 e folded in).
+//
+// Bound: every key and value is read once, 4 FLOP per element and query head, so
+// HBM bandwidth is the limit at any usual number of query heads per key head.
+// The kernel therefore keeps loads in flight and does as little as possible
+// between them:
+//  - Work is cut by keys, not by rows: the tiles of all (sequence, key heads)
+//    rows are one line, of which every block of a one-wave grid takes an equal
+//    part, whatever the lengths are (the host does not know them).  A row cut by
+//    block boundaries leaves (m, l, o) pieces in the workspace, which a second
+//    kernel joins; rows inside one block are finished there.  Few short rows are
+//    cut into one tile per block instead, so that no block has two parts.
+//  - Each warp reads its keys and values from global memory straight into the
+//    operand registers of its products; no shared memory, no barrier inside a
+//    row.  The values of a step are requested before its keys are used and the
+//    next step's keys before its values are used.
+//  - bf16: 16 keys at a time through mma.m16n8k16, keys (or the 16 value dims) as
+//    the 16-row operand and up to 8 query heads as its 8 columns.  An operand's
+//    16-byte pieces serve as they are: the order of the contraction index is free
+//    for the scores (the query is laid out to match) and the order of the output
+//    dims for the values.  The probabilities enter as two bf16 parts (p = hi + lo,
+//    2^-17 of p left over), so that their rounding does not show beside the
+//    output's own.
+//  - fp32: fused multiply-adds, four lanes to a key for the scores, a lane to
+//    four dims for the values.
 #include <cmath>
 
 #include "decode_ops.h"
@@ -7,95 +36,625 @@
 namespace pgs {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;      // of a block, at most; two blocks per SM
+constexpr int kTile = 32;      // keys of a unit of work
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct Meta { int32_t seq, row, last, pad; };  // a row begun in this block and ended in block `last`
 
 struct DecodeParams {
   gpt_paged_cache c;
   gpt_decode_attention_args a;
+  int32_t group;     // query heads per key head
+  int32_t chunk;     // query heads of a row per key head
+  int32_t chunks;    // rows of one key head
+  int32_t hc, ws;    // key heads per row, warps per key head
+  int32_t rows;      // rows per sequence
+  float scale2;      // scale log2 e
+  Meta* meta;        // [blocks]
+  float *piece_ml, *piece_o;  // [blocks][2][hc chunk][2], [...][head_dim]
 };
 
-// exp(x - m) for x <= m; nothing from x = -infinity, whatever m is.
-__device__ __forceinline__ float weight(float x, float m) { return x == -INFINITY ? 0.f : __expf(x - m); }
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 2^(x - m) for x <= m; nothing from x = -infinity, whatever m is.
+__device__ __forceinline__ float weight(float x, float m) { return x == -INFINITY ? 0.f : exp2_fast(x - m); }
 
-// One block per (sequence, query head); a warp per key in turn, one running
-// softmax (max m, sum l, weighted values o) per warp, the warps joined at the end.
-template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) decode_kernel(const __grid_constant__ DecodeParams p) {
-  constexpr int kN = Piece<T>::kN;
-  const gpt_paged_cache& c = p.c;
-  const gpt_decode_attention_args& a = p.a;
-  const int64_t s = blockIdx.y;
-  const int h = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t head = (int64_t)(h / (a.n_head / c.n_kv_head)) * c.head_stride;
-  int len = a.lens[s];
-  const int most = c.max_pages * c.page_size;
-  if (len < 0 || len > most) {
-    if (threadIdx.x == 0) set_status(a.status, GPT_STATUS_BAD_POS);
-    len = len < 0 ? 0 : most;
+__device__ __forceinline__ uint4 load16(const void* p, bool ok) {
+  uint4 u = make_uint4(0u, 0u, 0u, 0u);
+  if (ok) asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+  return u;
+}
+
+// Length of a sequence, cut to what its table can name.
+__device__ __forceinline__ int seq_len(const DecodeParams& p, int s, bool report) {
+  const int len = p.a.lens[s], most = p.c.max_pages * p.c.page_size;
+  if (len >= 0 && len <= most) return len;
+  if (report) set_status(p.a.status, GPT_STATUS_BAD_POS);
+  return len < 0 ? 0 : most;
+}
+
+// Page of a key, or -1 (past `end`, or a bad page).
+__device__ __forceinline__ int key_page(const DecodeParams& p, const int32_t* table, int key, int end) {
+  if (key >= end) return -1;
+  const int page = table[key / p.c.page_size];
+  if (page >= 0 && page < p.c.n_pages) return page;
+  set_status(p.a.status, GPT_STATUS_BAD_PAGE);
+  return -1;
+}
+// Offset (elements) of a key's row of head h; negative for no key.
+__device__ __forceinline__ int64_t key_offset(const DecodeParams& p, int page, int key, int64_t head) {
+  return page < 0 ? -1 : page * p.c.page_stride + (key % p.c.page_size) * p.c.slot_stride + head;
+}
+
+// What one warp leaves of its keys in shared memory: (m, l) of each head, then their o rows from left_o on.
+__host__ __device__ constexpr int left_o(int heads) { return (2 * heads + 3) / 4 * 4; }
+__host__ __device__ constexpr int left_floats(int heads, int dp) { return left_o(heads) + heads * dp; }
+
+// ---- bf16 ---------------------------------------------------------------------
+
+__device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <int NT_, int DP_>
+struct Bf16Path {
+  using T = __nv_bfloat16;
+  static constexpr int NT = NT_, DP = DP_, kHeads = 8 * NT;
+  static constexpr int KG = 128 / DP;           // 16-key groups of a step: 32 registers of keys, 32 of values
+  static constexpr int kQuery = NT * (DP / 32) * 128;  // a warp's queries: a 16-byte piece per lane, tile and 32 dims
+
+  // Lane (r, c): query head r of a tile, dims 32 i + 8 c .. + 7.
+  static __device__ __forceinline__ void stage_query(const DecodeParams& p, float* mine, int s, int h, int first, int n) {
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < DP / 32; ++i) {
+        const int qh = t * 8 + r;
+        reinterpret_cast<uint4*>(mine)[(t * (DP / 32) + i) * 32 + lane] =
+            load16((const T*)p.a.q + s * p.a.q_row + (int64_t)(h * p.group + first + qh) * p.a.q_head + i * 32 + c * 8,
+                   qh < n && i * 32 + c * 8 < p.c.head_dim);
+      }
   }
-  const bool mine = lane * kN < c.head_dim;  // head_dim <= 128: one piece per lane
-  float q[kN], o[kN], m = -INFINITY, l = 0.f;
+
+  // Keys [k0, k1) of sequence s for key head h, query heads first .. first + n of its group.
+  static __device__ __forceinline__ void run(const DecodeParams& p, const float* mine, float* left, int s, int h, int n, int k0, int k1) {
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const int d = p.c.head_dim;
+    const int32_t* table = p.c.page_table + s * p.c.table_stride;
+    const T *kb = (const T*)p.c.k + c * 8, *vb = (const T*)p.c.v + r * 8;
+    const int64_t head = (int64_t)h * p.c.head_stride;
+    const uint4* query = reinterpret_cast<const uint4*>(mine) + lane;
+    float o[NT][DP / 64][4][4], m[NT][2], l[NT][2];
 #pragma unroll
-  for (int i = 0; i < kN; ++i) q[i] = o[i] = 0.f;
-  if (mine)
-    Piece<T>::unpack(*reinterpret_cast<const uint4*>((const T*)a.q + s * a.q_row + h * a.q_head + lane * kN), q);
-  for (int j = warp; j < len; j += kWarps) {
-    const int page = c.page_table[s * c.table_stride + j / c.page_size];
-    if (page < 0 || page >= c.n_pages) {
-      if (lane == 0) set_status(a.status, GPT_STATUS_BAD_PAGE);
-      continue;
+    for (int t = 0; t < NT; ++t) {
+      m[t][0] = m[t][1] = -INFINITY, l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+      for (int b = 0; b < DP / 64; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[t][b][i / 4][i % 4] = 0.f;
     }
-    const int64_t at = page * c.page_stride + (j % c.page_size) * c.slot_stride + head + lane * kN;
-    float x[kN], z = 0.f;
-    if (mine) {
-      Piece<T>::unpack(*reinterpret_cast<const uint4*>((const T*)c.k + at), x);
+    const int key_of_lane = lane & (16 * KG - 1);
+    uint4 kr[KG][2][DP / 32], vr[KG][4][DP / 64];
+    auto load_keys = [&](int64_t off) {
 #pragma unroll
-      for (int i = 0; i < kN; ++i) z += q[i] * x[i];
+      for (int g = 0; g < KG; ++g)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int64_t at = __shfl_sync(0xffffffffu, off, g * 16 + u * 8 + r);
+#pragma unroll
+          for (int i = 0; i < DP / 32; ++i) kr[g][u][i] = load16(kb + at + i * 32, at >= 0 && i * 32 + c * 8 < d);
+        }
+    };
+    int64_t off = key_offset(p, key_page(p, table, k0 + key_of_lane, k1), k0 + key_of_lane, head);
+    int next_key = k0 + 16 * KG + key_of_lane;
+    int page = key_page(p, table, next_key, k1);
+    load_keys(off);
+    for (int k = k0; k < k1; k += 16 * KG) {
+      // this step's values
+#pragma unroll
+      for (int g = 0; g < KG; ++g)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int64_t at = __shfl_sync(0xffffffffu, off, g * 16 + (u >> 1) * 8 + 2 * c + (u & 1));
+#pragma unroll
+          for (int b = 0; b < DP / 64; ++b) vr[g][u][b] = load16(vb + at + b * 64, at >= 0 && b * 64 + r * 8 < d);
+        }
+      const uint32_t there = __ballot_sync(0xffffffffu, off >= 0);
+      off = key_offset(p, page, next_key, head);
+      next_key += 16 * KG;
+      page = key_page(p, table, next_key, k1);
+      // scores: 16 keys x 8 heads a tile
+      float z[KG][NT][4];
+#pragma unroll
+      for (int g = 0; g < KG; ++g)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[g][t][i] = 0.f;
+#pragma unroll
+          for (int i = 0; i < DP / 32; ++i) {
+            const uint4 q = query[(t * (DP / 32) + i) * 32];
+            mma16816(z[g][t], kr[g][0][i].x, kr[g][1][i].x, kr[g][0][i].y, kr[g][1][i].y, q.x, q.y);
+            mma16816(z[g][t], kr[g][0][i].z, kr[g][1][i].z, kr[g][0][i].w, kr[g][1][i].w, q.z, q.w);
+          }
+        }
+      load_keys(off);
+      // softmax: the reference of a head moves only when a score passes it by 2^8
+      bool move = false;
+#pragma unroll
+      for (int g = 0; g < KG; ++g) {
+        const bool low = (there >> (g * 16 + r)) & 1u, high = (there >> (g * 16 + 8 + r)) & 1u;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          z[g][t][0] = low ? z[g][t][0] * p.scale2 : -INFINITY, z[g][t][1] = low ? z[g][t][1] * p.scale2 : -INFINITY;
+          z[g][t][2] = high ? z[g][t][2] * p.scale2 : -INFINITY, z[g][t][3] = high ? z[g][t][3] * p.scale2 : -INFINITY;
+          move |= fmaxf(z[g][t][0], z[g][t][2]) > m[t][0] + 8.f || fmaxf(z[g][t][1], z[g][t][3]) > m[t][1] + 8.f;
+        }
+      }
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = m[t][e];
+#pragma unroll
+            for (int g = 0; g < KG; ++g) top = fmaxf(top, fmaxf(z[g][t][e], z[g][t][e + 2]));
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+            const float keep = weight(m[t][e], top);
+            m[t][e] = top;
+            l[t][e] *= keep;
+#pragma unroll
+            for (int b = 0; b < DP / 64; ++b)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[t][b][i][e] *= keep, o[t][b][i][e + 2] *= keep;
+          }
+      }
+#pragma unroll
+      for (int g = 0; g < KG; ++g)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const float m0 = m[t][0] == -INFINITY ? 0.f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+          const float p0 = exp2_fast(z[g][t][0] - m0), p1 = exp2_fast(z[g][t][1] - m1);
+          const float p2 = exp2_fast(z[g][t][2] - m0), p3 = exp2_fast(z[g][t][3] - m1);
+          l[t][0] += p0 + p2, l[t][1] += p1 + p3;
+          const uint32_t ha = pack2(p0, p1), hb = pack2(p2, p3);
+          const uint32_t la = pack2(p0 - __uint_as_float(ha << 16), p1 - __uint_as_float(ha & 0xffff0000u));
+          const uint32_t lb = pack2(p2 - __uint_as_float(hb << 16), p3 - __uint_as_float(hb & 0xffff0000u));
+          const uint32_t h0 = transpose8(ha), h1 = transpose8(hb), l0 = transpose8(la), l1 = transpose8(lb);
+#pragma unroll
+          for (int b = 0; b < DP / 64; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t va = (&vr[g][0][b].x)[i], vc = (&vr[g][1][b].x)[i], ve = (&vr[g][2][b].x)[i], vg = (&vr[g][3][b].x)[i];
+              const uint32_t a0 = __byte_perm(va, vc, 0x5410), a1 = __byte_perm(va, vc, 0x7632);
+              const uint32_t a2 = __byte_perm(ve, vg, 0x5410), a3 = __byte_perm(ve, vg, 0x7632);
+              mma16816(o[t][b][i], a0, a1, a2, a3, h0, h1);
+              mma16816(o[t][b][i], a0, a1, a2, a3, l0, l1);
+            }
+        }
     }
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) z += __shfl_xor_sync(0xffffffffu, z, w);
-    z *= a.scale;
-    const float top = fmaxf(m, z), keep = weight(m, top), e = weight(z, top);
-    m = top;
-    l = l * keep + e;
-    if (mine) {
-      Piece<T>::unpack(*reinterpret_cast<const uint4*>((const T*)c.v + at), x);
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int i = 0; i < kN; ++i) o[i] = o[i] * keep + e * x[i];
+      for (int e = 0; e < 2; ++e) {
+        const int qh = t * 8 + 2 * c + e;
+        float total = l[t][e];
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) total += __shfl_xor_sync(0xffffffffu, total, w);
+        if (qh >= n) continue;
+        if (r == 0) left[2 * qh] = m[t][e], left[2 * qh + 1] = total;
+#pragma unroll
+        for (int b = 0; b < DP / 64; ++b) {
+          float4* to = reinterpret_cast<float4*>(left + left_o(kHeads) + qh * DP + b * 64 + r * 8);
+          to[0] = make_float4(o[t][b][0][e], o[t][b][0][e + 2], o[t][b][1][e], o[t][b][1][e + 2]);
+          to[1] = make_float4(o[t][b][2][e], o[t][b][2][e + 2], o[t][b][3][e], o[t][b][3][e + 2]);
+        }
+      }
+  }
+};
+
+// ---- fp32 ---------------------------------------------------------------------
+
+template <int GH_, int DP_>
+struct Fp32Path {
+  using T = float;
+  static constexpr int DP = DP_, kHeads = GH_;
+  static constexpr int KG = 128 / DP;            // 8-key groups of a step: 32 registers of keys, 32 of values
+  static constexpr int kKeys = 8 * KG;
+  static constexpr int kLanes = DP / 4;          // lanes to a row of values
+  static constexpr int kRows = 32 / kLanes;      // rows of values a load covers
+  static constexpr int kQuery = kHeads * DP + kKeys * kHeads;  // a warp's queries and probabilities
+
+  static __device__ __forceinline__ void stage_query(const DecodeParams& p, float* mine, int s, int h, int first, int n) {
+    __syncwarp();
+    for (int i = threadIdx.x & 31; i < kHeads * DP; i += 32) {
+      const int qh = i / DP, e = i % DP;
+      mine[i] = qh < n && e < p.c.head_dim
+                    ? ((const float*)p.a.q)[s * p.a.q_row + (int64_t)(h * p.group + first + qh) * p.a.q_head + e] : 0.f;
+    }
+    __syncwarp();
+  }
+
+  static __device__ __forceinline__ void run(const DecodeParams& p, const float* mine, float* left, int s, int h, int n, int k0, int k1) {
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const int d = p.c.head_dim;
+    const int32_t* table = p.c.page_table + s * p.c.table_stride;
+    const int vd = (lane % kLanes) * 4, vrow = lane / kLanes;
+    const float *kb = (const float*)p.c.k + c * 4, *vb = (const float*)p.c.v + vd;
+    const int64_t head = (int64_t)h * p.c.head_stride;
+    const float* sq = mine;
+    float* sp = const_cast<float*>(mine) + kHeads * DP;  // [key][head]
+    float m[kHeads], l[kHeads];
+    float4 o[kHeads];
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) m[i] = -INFINITY, l[i] = 0.f, o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int key_of_lane = lane & (kKeys - 1);
+    uint4 kr[KG][DP / 16], vr[kKeys / kRows];
+    auto load_keys = [&](int64_t off) {
+#pragma unroll
+      for (int g = 0; g < KG; ++g) {
+        const int64_t at = __shfl_sync(0xffffffffu, off, g * 8 + r);
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i) kr[g][i] = load16(kb + at + i * 16, at >= 0 && i * 16 + c * 4 < d);
+      }
+    };
+    int64_t off = key_offset(p, key_page(p, table, k0 + key_of_lane, k1), k0 + key_of_lane, head);
+    int next_key = k0 + kKeys + key_of_lane;
+    int page = key_page(p, table, next_key, k1);
+    load_keys(off);
+    for (int k = k0; k < k1; k += kKeys) {
+#pragma unroll
+      for (int i = 0; i < kKeys / kRows; ++i) {
+        const int64_t at = __shfl_sync(0xffffffffu, off, i * kRows + vrow);
+        vr[i] = load16(vb + at, at >= 0 && vd < d);
+      }
+      const uint32_t there = __ballot_sync(0xffffffffu, off >= 0);
+      off = key_offset(p, page, next_key, head);
+      next_key += kKeys;
+      page = key_page(p, table, next_key, k1);
+      float z[KG][kHeads];
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i) {
+#pragma unroll
+        for (int g = 0; g < KG; ++g) z[g][i] = 0.f;
+#pragma unroll
+        for (int b = 0; b < DP / 16; ++b) {
+          const float4 x = *reinterpret_cast<const float4*>(sq + i * DP + b * 16 + c * 4);
+#pragma unroll
+          for (int g = 0; g < KG; ++g) {
+            const uint4 u = kr[g][b];
+            z[g][i] = fmaf(x.x, __uint_as_float(u.x), z[g][i]);
+            z[g][i] = fmaf(x.y, __uint_as_float(u.y), z[g][i]);
+            z[g][i] = fmaf(x.z, __uint_as_float(u.z), z[g][i]);
+            z[g][i] = fmaf(x.w, __uint_as_float(u.w), z[g][i]);
+          }
+        }
+      }
+      load_keys(off);
+      bool move = false;
+#pragma unroll
+      for (int g = 0; g < KG; ++g) {
+        const bool ok = (there >> (g * 8 + r)) & 1u;
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+          z[g][i] += __shfl_xor_sync(0xffffffffu, z[g][i], 1);
+          z[g][i] += __shfl_xor_sync(0xffffffffu, z[g][i], 2);
+          z[g][i] = ok ? z[g][i] * p.scale2 : -INFINITY;
+          move |= z[g][i] > m[i] + 8.f;
+        }
+      }
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+          float top = m[i];
+#pragma unroll
+          for (int g = 0; g < KG; ++g) top = fmaxf(top, z[g][i]);
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+          const float keep = weight(m[i], top);
+          m[i] = top;
+          l[i] *= keep;
+          o[i].x *= keep, o[i].y *= keep, o[i].z *= keep, o[i].w *= keep;
+        }
+      }
+      __syncwarp();  // the last step's probabilities have been read
+#pragma unroll
+      for (int g = 0; g < KG; ++g)
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+          const float e = exp2_fast(z[g][i] - (m[i] == -INFINITY ? 0.f : m[i]));
+          l[i] += e;
+          if ((i & 3) == c) sp[(g * 8 + r) * kHeads + i] = e;
+        }
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < kKeys / kRows; ++j) {
+        const float* e = sp + (j * kRows + vrow) * kHeads;
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+          o[i].x = fmaf(e[i], __uint_as_float(vr[j].x), o[i].x);
+          o[i].y = fmaf(e[i], __uint_as_float(vr[j].y), o[i].y);
+          o[i].z = fmaf(e[i], __uint_as_float(vr[j].z), o[i].z);
+          o[i].w = fmaf(e[i], __uint_as_float(vr[j].w), o[i].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+#pragma unroll
+      for (int w = 4; w < 32; w <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
+#pragma unroll
+      for (int w = kLanes; w < 32; w <<= 1) {
+        o[i].x += __shfl_xor_sync(0xffffffffu, o[i].x, w);
+        o[i].y += __shfl_xor_sync(0xffffffffu, o[i].y, w);
+        o[i].z += __shfl_xor_sync(0xffffffffu, o[i].z, w);
+        o[i].w += __shfl_xor_sync(0xffffffffu, o[i].w, w);
+      }
+      if (i >= n) continue;
+      if (lane == 0) left[2 * i] = m[i], left[2 * i + 1] = l[i];
+      if (vrow == 0) *reinterpret_cast<float4*>(left + left_o(kHeads) + i * DP + vd) = o[i];
     }
   }
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][128];
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
-  if (mine)
+};
+
+// ---- the kernels --------------------------------------------------------------
+
+__device__ __forceinline__ void store4(float* to, const float* x) { *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]); }
+__device__ __forceinline__ void store4(__nv_bfloat16* to, const float* x) {
+  *reinterpret_cast<uint2*>(to) = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
+}
+
+// Sum over the block, in a fixed order, to every thread.
+__device__ __forceinline__ int64_t block_total(int64_t v, int64_t* red) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) so[warp][lane * kN + i] = o[i];
+  for (int w = 16; w > 0; w >>= 1) v += __shfl_xor_sync(0xffffffffu, v, w);
   __syncthreads();
-  if (warp == 0) {
-    float top = sm[0], total = 0.f;
-    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm[w]);
-#pragma unroll
-    for (int i = 0; i < kN; ++i) o[i] = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-      const float keep = weight(sm[w], top);
-      total += sl[w] * keep;
-      if (mine)
-#pragma unroll
-        for (int i = 0; i < kN; ++i) o[i] += so[w][lane * kN + i] * keep;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0;
+  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) v += red[w];
+  return v;
+}
+
+template <class P>
+__global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(const __grid_constant__ DecodeParams p) {
+  using T = typename P::T;
+  constexpr int kLeft = left_floats(P::kHeads, P::DP);
+  extern __shared__ __align__(16) float sm[];
+  __shared__ int64_t red[kWarps], found_base;
+  __shared__ int found_seq;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n_seq = p.c.n_seq, d = p.c.head_dim;
+  const int blk = blockIdx.x, blocks = gridDim.x;
+
+  // the line of work: tiles of all sequences' rows
+  int64_t small = 0, large = 0;
+  const int large_tile = max(kTile, p.ws * 16);
+  for (int s = tid; s < n_seq; s += blockDim.x) {
+    const int len = seq_len(p, s, blk == 0);
+    small += (len + kTile - 1) / kTile;
+    large += (len + large_tile - 1) / large_tile;
+  }
+  small = block_total(small, red) * p.rows;
+  large = block_total(large, red) * p.rows;
+  const bool few = large <= blocks;  // a tile of 16 keys per warp for every block
+  const int tile = few ? large_tile : kTile;
+  const int64_t units = few ? large : small;
+  const int active = (int)min((int64_t)blocks, units);
+  const int64_t begin = blk < active ? blk * units / active : 0, end = blk < active ? (blk + 1) * units / active : 0;
+  if (tid == 0) p.meta[blk].seq = -1;
+
+  // sequences of no keys
+  for (int s = blk; s < n_seq; s += blocks)
+    if (seq_len(p, s, false) == 0) {
+      const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int i = tid; i < p.a.n_head * (d / 4); i += blockDim.x)
+        store4((T*)p.a.out + s * p.a.out_row + i / (d / 4) * p.a.out_head + i % (d / 4) * 4, zero);
+      if (p.a.lse)
+        for (int h = tid; h < p.a.n_head; h += blockDim.x) p.a.lse[(int64_t)s * p.a.n_head + h] = -INFINITY;
     }
-    if (mine) {
+  if (begin == end) return;
+
+  // the sequence that the block begins in
+  int64_t base = 0;
+  for (int s0 = 0; s0 < n_seq; s0 += blockDim.x) {
+    const int s = s0 + tid;
+    const int64_t mine = s < n_seq ? (int64_t)((seq_len(p, s, false) + tile - 1) / tile) * p.rows : 0;
+    int64_t sum = mine;  // inclusive, over the warp, then the block
 #pragma unroll
-      for (int i = 0; i < kN; ++i) o[i] = total == 0.f ? 0.f : o[i] / total;
-      *reinterpret_cast<uint4*>((T*)a.out + s * a.out_row + h * a.out_head + lane * kN) = Piece<T>::pack(o);
+    for (int w = 1; w < 32; w <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, sum, w);
+      if (lane >= w) sum += x;
     }
-    if (lane == 0 && a.lse) a.lse[s * a.n_head + h] = total == 0.f ? -INFINITY : top + logf(total);
+    __syncthreads();
+    if (lane == 31) red[warp] = sum;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
+      if (w == warp) sum += total;
+      total += red[w];
+    }
+    if (base + sum - mine <= begin && begin < base + sum) found_seq = s, found_base = base + sum - mine;
+    if (begin < base + total) break;
+    base += total;
+  }
+  __syncthreads();
+  int s = found_seq;
+  base = found_base;
+
+  const int heads = p.hc * p.chunk;  // query heads of a row
+  float* mine = sm + kWarps * kLeft + warp * P::kQuery;
+  for (int64_t u = begin; u < end;) {
+    const int len = seq_len(p, s, false), tiles = (len + tile - 1) / tile;
+    if (tiles == 0) { ++s; continue; }
+    const int row = (int)((u - base) / tiles), t0 = (int)((u - base) % tiles);
+    const int t1 = (int)min((int64_t)tiles, t0 + (end - u));
+    const int first = row % p.chunks * p.chunk, n = min(p.chunk, p.group - first);
+    const int h0 = row / p.chunks * p.hc;  // first key head of the row
+    {  // the warp's part of the keys, in steps of 16
+      const int steps = (min(len, t1 * tile) - t0 * tile + 15) / 16, each = (steps + p.ws - 1) / p.ws;
+      const int k0 = t0 * tile + (warp % p.ws) * each * 16, k1 = min(min(len, t1 * tile), k0 + each * 16);
+      P::stage_query(p, mine, s, h0 + warp / p.ws, first, n);
+      P::run(p, mine, sm + warp * kLeft, s, h0 + warp / p.ws, n, k0, k1);
+    }
+    __syncthreads();
+    // join the warps of a key head; finish the row, or leave a piece of it
+    const bool whole = t0 == 0 && t1 == tiles;
+    const int64_t slot = 2 * blk + (t0 == 0 ? 1 : 0);
+    for (int i = tid; i < p.hc * n * (d / 4); i += blockDim.x) {
+      const int e = i % (d / 4) * 4, qh = i / (d / 4) % n, hl = i / (d / 4) / n;
+      float top = -INFINITY, total = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int w = hl * p.ws; w < (hl + 1) * p.ws; ++w) top = fmaxf(top, sm[w * kLeft + 2 * qh]);
+      for (int w = hl * p.ws; w < (hl + 1) * p.ws; ++w) {
+        const float* from = sm + w * kLeft;
+        const float keep = weight(from[2 * qh], top);
+        total += from[2 * qh + 1] * keep;
+        const float4 y = *reinterpret_cast<const float4*>(from + left_o(P::kHeads) + qh * P::DP + e);
+        x[0] += y.x * keep, x[1] += y.y * keep, x[2] += y.z * keep, x[3] += y.w * keep;
+      }
+      const int hq = (h0 + hl) * p.group + first + qh;
+      if (whole) {
+        const float inv = total == 0.f ? 0.f : 1.0f / total;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] *= inv;
+        store4((T*)p.a.out + s * p.a.out_row + hq * p.a.out_head + e, x);
+        if (e == 0 && p.a.lse) p.a.lse[(int64_t)s * p.a.n_head + hq] = total == 0.f ? -INFINITY : top * kLn2 + logf(total);
+      } else {
+        const int64_t at = slot * heads + hl * p.chunk + qh;
+        if (e == 0) p.piece_ml[2 * at] = top, p.piece_ml[2 * at + 1] = total;
+        store4(p.piece_o + at * d + e, x);
+      }
+    }
+    u += t1 - t0;
+    if (t0 == 0 && t1 < tiles && tid == 0) {  // the row goes on: where does it end?
+      const int64_t stop = base + (int64_t)(row + 1) * tiles;
+      int last = (int)((stop * active - 1) / units);
+      while (last + 1 < active && (last + 1) * units / active < stop) ++last;
+      while (last > blk && last * units / active >= stop) --last;
+      p.meta[blk] = Meta{s, row, last, 0};
+    }
+    if (u - base == (int64_t)tiles * p.rows) base = u, ++s;
+    __syncthreads();
   }
 }
+
+// A row that several blocks worked on: the pieces of its blocks, joined; a warp
+// per query head.
+template <typename T>
+__global__ void __launch_bounds__(256) decode_join_kernel(const __grid_constant__ DecodeParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int blk = blockIdx.x, lane = threadIdx.x & 31, d = p.c.head_dim;
+  const Meta mt = p.meta[blk];
+  if (mt.seq < 0) return;
+  const int first = mt.row % p.chunks * p.chunk, n = min(p.chunk, p.group - first), h0 = mt.row / p.chunks * p.hc;
+  const int heads = p.hc * p.chunk, pieces = mt.last - blk + 1;
+  for (int i = threadIdx.x >> 5; i < p.hc * n; i += 8) {
+    const int hl = i / n, qh = i % n;
+    auto at = [&](int j) { return (int64_t)(j == 0 ? 2 * blk + 1 : 2 * (blk + j)) * heads + hl * p.chunk + qh; };
+    float top = -INFINITY;
+    for (int j = lane; j < pieces; j += 32) top = fmaxf(top, p.piece_ml[2 * at(j)]);
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+    float total = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int j = 0; j < pieces; ++j) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.piece_ml + 2 * at(j));
+      const float keep = weight(ml.x, top);
+      total += ml.y * keep;
+      if (lane * 4 < d) {
+        const float4 y = *reinterpret_cast<const float4*>(p.piece_o + at(j) * d + lane * 4);
+        x[0] += y.x * keep, x[1] += y.y * keep, x[2] += y.z * keep, x[3] += y.w * keep;
+      }
+    }
+    const int hq = (h0 + hl) * p.group + first + qh;
+    const float inv = total == 0.f ? 0.f : 1.0f / total;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] *= inv;
+    if (lane * 4 < d) store4((T*)p.a.out + mt.seq * p.a.out_row + hq * p.a.out_head + lane * 4, x);
+    if (lane == 0 && p.a.lse) p.a.lse[(int64_t)mt.seq * p.a.n_head + hq] = total == 0.f ? -INFINITY : top * kLn2 + logf(total);
+  }
+}
+
+// ---- host ---------------------------------------------------------------------
 
 int check_args(const gpt_paged_cache* c, int32_t n_head) {
   if (const int rc = check_cache(c)) return rc;
   if (n_head < 1 || n_head % c->n_kv_head)
     return call_error(GPT_ERR_INVALID_ARG, "n_head %d must be a multiple of n_kv_head %d", n_head, c->n_kv_head);
   return GPT_OK;
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 152;
+  }
+  return sms;
+}
+
+struct Plan { int blocks, hc, ws, chunk, chunks; size_t ml_at, o_at, bytes; };
+
+// How rows are formed and how many blocks share them.
+Plan make_plan(const gpt_paged_cache* c, int32_t n_head) {
+  Plan pl;
+  pl.blocks = 2 * sm_count();
+  const int group = n_head / c->n_kv_head;
+  pl.chunk = group <= 8 ? group : c->dtype == GPT_DTYPE_BF16 ? (group < 16 ? group : 16) : 8;
+  pl.chunks = (group + pl.chunk - 1) / pl.chunk;
+  // Key heads of a row, a warp or more each: as many as leave two rows per block.
+  // More rows than that only add ends (a join in shared memory, a pipeline that
+  // runs empty); fewer leave pieces to join.
+  pl.hc = 1;
+  for (int hc = 2; hc <= kWarps; ++hc)
+    if (c->n_kv_head % hc == 0 && (int64_t)c->n_seq * (c->n_kv_head / hc) * pl.chunks >= 2 * pl.blocks) pl.hc = hc;
+  pl.ws = kWarps / pl.hc;
+  const size_t records = (size_t)pl.blocks * 2 * pl.hc * pl.chunk;
+  pl.ml_at = (pl.blocks * sizeof(Meta) + 15) / 16 * 16;
+  pl.o_at = (pl.ml_at + records * 8 + 15) / 16 * 16;
+  pl.bytes = pl.o_at + records * c->head_dim * 4;
+  return pl;
+}
+
+template <class P>
+int launch(const DecodeParams& p, const Plan& pl, cudaStream_t st) {
+  const size_t smem = (size_t)kWarps * (left_floats(P::kHeads, P::DP) + P::kQuery) * sizeof(float);
+  static thread_local int ready = -1;  // device whose limit has been raised
+  int dev = -1;
+  cudaGetDevice(&dev);
+  if (ready != dev) {
+    if (cudaFuncSetAttribute(decode_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+      return check_launch("gpt_decode_attention");
+    ready = dev;
+  }
+  decode_kernel<P><<<pl.blocks, pl.hc * pl.ws * 32, smem, st>>>(p);
+  if (const int rc = check_launch("gpt_decode_attention")) return rc;
+  // the second kernel may start while the first one ends; it waits for its results itself
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(pl.blocks), cfg.blockDim = dim3(256), cfg.stream = st, cfg.attrs = &attr, cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, decode_join_kernel<typename P::T>, p);
+  return check_launch("gpt_decode_attention (join)");
 }
 
 }  // namespace
@@ -105,7 +664,8 @@ using namespace pgs;
 
 extern "C" size_t gpt_decode_attention_workspace(const gpt_paged_cache* c, int32_t n_head) {
   clear_call_error();
-  return 0;
+  if (check_args(c, n_head) != GPT_OK || c->n_seq == 0) return 0;
+  return make_plan(c, n_head).bytes;
 }
 
 extern "C" int gpt_decode_attention(const gpt_paged_cache* c, const gpt_decode_attention_args* a, void* cuda_stream) {
@@ -119,11 +679,26 @@ extern "C" int gpt_decode_attention(const gpt_paged_cache* c, const gpt_decode_a
       !stride16(a->out_row, es) || !stride16(a->out_head, es))
     return call_error(GPT_ERR_INVALID_ARG, "q and out addresses and strides must be multiples of 16 bytes");
   if (!std::isfinite(a->scale)) return call_error(GPT_ERR_INVALID_ARG, "scale must be finite");
-  if (c->n_seq > 65535) return call_error(GPT_ERR_UNSUPPORTED, "at most 65535 sequences");
-  const DecodeParams p{*c, *a};
-  const dim3 grid(a->n_head, c->n_seq);
+  const Plan pl = make_plan(c, a->n_head);
+  if (!a->workspace || a->workspace_bytes < pl.bytes || !aligned16(a->workspace))
+    return call_error(GPT_ERR_INVALID_ARG, "workspace: %zu bytes on a 16-byte boundary", pl.bytes);
+  DecodeParams p;
+  p.c = *c;
+  p.a = *a;
+  p.group = a->n_head / c->n_kv_head;
+  p.chunk = pl.chunk, p.chunks = pl.chunks, p.hc = pl.hc, p.ws = pl.ws;
+  p.rows = c->n_kv_head / pl.hc * pl.chunks;
+  p.scale2 = a->scale * kLog2e;
+  p.meta = (Meta*)a->workspace;
+  p.piece_ml = (float*)((char*)a->workspace + pl.ml_at);
+  p.piece_o = (float*)((char*)a->workspace + pl.o_at);
   const cudaStream_t st = (cudaStream_t)cuda_stream;
-  if (c->dtype == GPT_DTYPE_BF16) decode_kernel<__nv_bfloat16><<<grid, kWarps * 32, 0, st>>>(p);
-  else decode_kernel<float><<<grid, kWarps * 32, 0, st>>>(p);
-  return check_launch("gpt_decode_attention");
+  const bool wide = c->head_dim > 64;
+  if (c->dtype == GPT_DTYPE_BF16) {
+    if (pl.chunk <= 8) return wide ? launch<Bf16Path<1, 128>>(p, pl, st) : launch<Bf16Path<1, 64>>(p, pl, st);
+    return wide ? launch<Bf16Path<2, 128>>(p, pl, st) : launch<Bf16Path<2, 64>>(p, pl, st);
+  }
+  if (pl.chunk == 1) return wide ? launch<Fp32Path<1, 128>>(p, pl, st) : launch<Fp32Path<1, 64>>(p, pl, st);
+  if (pl.chunk <= 4) return wide ? launch<Fp32Path<4, 128>>(p, pl, st) : launch<Fp32Path<4, 64>>(p, pl, st);
+  return wide ? launch<Fp32Path<8, 128>>(p, pl, st) : launch<Fp32Path<8, 64>>(p, pl, st);
 }

@@ -31,8 +31,8 @@ inline int check_cache(const gpt_paged_cache* c) {
   const int es = elem_size(c->dtype);
   if (c->head_dim > 128 || (c->head_dim * es) % 16)
     return call_error(GPT_ERR_UNSUPPORTED, "head_dim %d: a multiple of 16 bytes, at most 128 elements", c->head_dim);
-  if ((int64_t)c->max_pages * c->page_size > INT32_MAX)
-    return call_error(GPT_ERR_UNSUPPORTED, "max_pages * page_size does not fit in 32 bits");
+  if ((int64_t)c->max_pages * c->page_size > INT32_MAX - 4096)  // tiles that end past the last position still count in 32 bits
+    return call_error(GPT_ERR_UNSUPPORTED, "max_pages * page_size must stay 4096 below 2^31 for 32 bits");
   if (c->n_seq == 0) return GPT_OK;
   if (!c->k || !c->v || !c->page_table) return call_error(GPT_ERR_INVALID_ARG, "cache pointers must be non-NULL");
   if (!aligned16(c->k) || !aligned16(c->v) || !stride16(c->page_stride, es) || !stride16(c->slot_stride, es) ||

@@ -107,7 +107,8 @@ def test_append_refusals(lib, change, word):
 @pytest.mark.parametrize("change,word", [
     (dict(n_head=6), "multiple"), (dict(n_head=0), "multiple"), (dict(q=None), "NULL"), (dict(out=None), "NULL"),
     (dict(lens=None), "NULL"), (dict(q=FAKE + 4), "16 bytes"), (dict(out_row=508), "16 bytes"),
-    (dict(scale=math.nan), "scale"), (dict(scale=math.inf), "scale")])
+    (dict(scale=math.nan), "scale"), (dict(scale=math.inf), "scale"), (dict(workspace=None), "workspace"),
+    (dict(workspace=FAKE + 8), "workspace"), (dict(workspace_bytes=64), "workspace")])
 def test_attention_refusals(lib, change, word):
     assert lib.gpt_decode_attention(ctypes.byref(_cache()), ctypes.byref(_attend(**change)), None) == -1
     assert word in lib.gpt_last_error(None).decode()
