@@ -63,7 +63,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // 2^(x - m) for x <= m; nothing from x = -infinity, whatever m is.
 __device__ __forceinline__ float weight(float x, float m) { return x == -INFINITY ? 0.f : exp2_fast(x - m); }
 
-__device__ __forceinline__ uint4 load16(const void* p, bool ok) {
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 u;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+  return u;
+}
+__device__ __forceinline__ uint4 load16_if(const void* p, bool ok) {
   uint4 u = make_uint4(0u, 0u, 0u, 0u);
   if (ok) asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
   return u;
@@ -77,18 +82,46 @@ __device__ __forceinline__ int seq_len(const DecodeParams& p, int s, bool report
   return len < 0 ? 0 : most;
 }
 
-// Page of a key, or -1 (past `end`, or a bad page).
-__device__ __forceinline__ int key_page(const DecodeParams& p, const int32_t* table, int key, int end) {
-  if (key >= end) return -1;
-  const int page = table[key / p.c.page_size];
-  if (page >= 0 && page < p.c.n_pages) return page;
-  set_status(p.a.status, GPT_STATUS_BAD_PAGE);
-  return -1;
-}
-// Offset (elements) of a key's row of head h; negative for no key.
-__device__ __forceinline__ int64_t key_offset(const DecodeParams& p, int page, int key, int64_t head) {
-  return page < 0 ? -1 : page * p.c.page_stride + (key % p.c.page_size) * p.c.slot_stride + head;
-}
+// Where a warp's keys are.  kWhole (pages of whole 16-key groups): lane i holds the
+// offset (elements) of group i of the next 32, one division and one table entry a
+// group; rows of a group are slot_stride apart.  Otherwise a lane holds the offset
+// of its own key of the step, one of each a key.  Table entries are read one round
+// ahead.  An offset of -1: no such key, or a bad page.
+template <bool kWhole, int kKeys>
+struct Walk {
+  const DecodeParams& p;
+  const int32_t* table;
+  int64_t head, off;
+  int next, end, page, at;
+
+  __device__ __forceinline__ Walk(const DecodeParams& p_, int s, int h, int k0, int k1)
+      : p(p_), table(p_.c.page_table + s * p_.c.table_stride), head((int64_t)h * p_.c.head_stride), end(k1), at(0) {
+    const int lane = threadIdx.x & 31;
+    next = k0 + (kWhole ? lane * 16 : lane & (kKeys - 1));
+    page = fetch();
+    turn();
+  }
+  __device__ __forceinline__ int fetch() const {
+    if (next >= end) return -1;
+    const int id = table[next / p.c.page_size];
+    if (id >= 0 && id < p.c.n_pages) return id;
+    set_status(p.a.status, GPT_STATUS_BAD_PAGE);
+    return -1;
+  }
+  __device__ __forceinline__ void turn() {
+    off = page < 0 ? -1 : page * p.c.page_stride + (next % p.c.page_size) * p.c.slot_stride + head;
+    next += kWhole ? 512 : kKeys;
+    page = fetch();
+  }
+  // kWhole: offset of key `at` (a multiple of 8) of the 512 in hand; then `by` keys on.
+  __device__ __forceinline__ int64_t step(int by) {
+    int64_t x = __shfl_sync(0xffffffffu, off, at >> 4);
+    if (x >= 0) x += (at & 15) * p.c.slot_stride;
+    at += by;
+    if (at == 512) turn(), at = 0;
+    return x;
+  }
+};
 
 // What one warp leaves of its keys in shared memory: (m, l) of each head, then their o rows from left_o on.
 __host__ __device__ constexpr int left_o(int heads) { return (2 * heads + 3) / 4 * 4; }
@@ -112,10 +145,14 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-template <int NT_, int DP_>
+// kMode: query heads of a row.  4: up to 4, columns 4..7 of the scores repeat them, so
+// that one product takes hi from columns 0..3 and lo from 4..7; 8, 16: up to that
+// many, hi and lo in products of their own.
+template <int kMode, int DP_, bool kFast>
 struct Bf16Path {
   using T = __nv_bfloat16;
-  static constexpr int NT = NT_, DP = DP_, kHeads = 8 * NT;
+  static constexpr int NT = kMode == 16 ? 2 : 1, DP = DP_, kHeads = kMode;
+  static constexpr bool kTwice = kMode == 4;
   static constexpr int KG = 128 / DP;           // 16-key groups of a step: 32 registers of keys, 32 of values
   static constexpr int kQuery = NT * (DP / 32) * 128;  // a warp's queries: a 16-byte piece per lane, tile and 32 dims
 
@@ -126,20 +163,20 @@ struct Bf16Path {
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int i = 0; i < DP / 32; ++i) {
-        const int qh = t * 8 + r;
+        const int qh = kTwice ? r & 3 : t * 8 + r;
         reinterpret_cast<uint4*>(mine)[(t * (DP / 32) + i) * 32 + lane] =
-            load16((const T*)p.a.q + s * p.a.q_row + (int64_t)(h * p.group + first + qh) * p.a.q_head + i * 32 + c * 8,
-                   qh < n && i * 32 + c * 8 < p.c.head_dim);
+            load16_if((const T*)p.a.q + s * p.a.q_row + (int64_t)(h * p.group + first + qh) * p.a.q_head + i * 32 + c * 8,
+                      qh < n && i * 32 + c * 8 < p.c.head_dim);
       }
   }
 
-  // Keys [k0, k1) of sequence s for key head h, query heads first .. first + n of its group.
+  // Keys [k0, k1) of sequence s for key head h and the n staged query heads.
   static __device__ __forceinline__ void run(const DecodeParams& p, const float* mine, float* left, int s, int h, int n, int k0, int k1) {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const int d = p.c.head_dim;
-    const int32_t* table = p.c.page_table + s * p.c.table_stride;
-    const T *kb = (const T*)p.c.k + c * 8, *vb = (const T*)p.c.v + r * 8;
-    const int64_t head = (int64_t)h * p.c.head_stride;
+    const int64_t row = p.c.slot_stride;
+    const T* kb = (const T*)p.c.k + c * 8 + (kFast ? r * row : 0);
+    const T* vb = (const T*)p.c.v + r * 8 + (kFast ? 2 * c * row : 0);
     const uint4* query = reinterpret_cast<const uint4*>(mine) + lane;
     float o[NT][DP / 64][4][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -150,64 +187,115 @@ struct Bf16Path {
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[t][b][i / 4][i % 4] = 0.f;
     }
-    const int key_of_lane = lane & (16 * KG - 1);
     uint4 kr[KG][2][DP / 32], vr[KG][4][DP / 64];
-    auto load_keys = [&](int64_t off) {
+    Walk<kFast, 16 * KG> walk(p, s, h, k0, k1);
+    int64_t off[KG];  // of the step's groups (kFast); of the lane's key
+    auto advance = [&] {
+      if constexpr (kFast) {
 #pragma unroll
-      for (int g = 0; g < KG; ++g)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int64_t at = __shfl_sync(0xffffffffu, off, g * 16 + u * 8 + r);
-#pragma unroll
-          for (int i = 0; i < DP / 32; ++i) kr[g][u][i] = load16(kb + at + i * 32, at >= 0 && i * 32 + c * 8 < d);
-        }
+        for (int g = 0; g < KG; ++g) off[g] = walk.step(16);
+      } else {
+        off[0] = walk.off;
+        walk.turn();
+      }
     };
-    int64_t off = key_offset(p, key_page(p, table, k0 + key_of_lane, k1), k0 + key_of_lane, head);
-    int next_key = k0 + 16 * KG + key_of_lane;
-    int page = key_page(p, table, next_key, k1);
-    load_keys(off);
-    for (int k = k0; k < k1; k += 16 * KG) {
-      // this step's values
+    auto load_keys = [&] {
 #pragma unroll
-      for (int g = 0; g < KG; ++g)
+      for (int g = 0; g < KG; ++g) {
+        if constexpr (kFast) {
+          const T* at = kb + max(off[g], (int64_t)0);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int64_t at = __shfl_sync(0xffffffffu, off, g * 16 + (u >> 1) * 8 + 2 * c + (u & 1));
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int b = 0; b < DP / 64; ++b) vr[g][u][b] = load16(vb + at + b * 64, at >= 0 && b * 64 + r * 8 < d);
+            for (int i = 0; i < DP / 32; ++i) kr[g][u][i] = load16(at + u * 8 * row + i * 32);
+        } else {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int64_t at = __shfl_sync(0xffffffffu, off[0], g * 16 + u * 8 + r);
+#pragma unroll
+            for (int i = 0; i < DP / 32; ++i) kr[g][u][i] = load16_if(kb + at + i * 32, at >= 0 && i * 32 + c * 8 < d);
+          }
         }
-      const uint32_t there = __ballot_sync(0xffffffffu, off >= 0);
-      off = key_offset(p, page, next_key, head);
-      next_key += 16 * KG;
-      page = key_page(p, table, next_key, k1);
+      }
+    };
+    advance();
+    load_keys();
+    for (int k = k0; k < k1; k += 16 * KG) {
+      // the step's values
+      uint32_t there = 0xffffffffu;  // keys that count
+#pragma unroll
+      for (int g = 0; g < KG; ++g) {
+        if constexpr (kFast) {
+          const T* at = vb + max(off[g], (int64_t)0);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int b = 0; b < DP / 64; ++b) vr[g][u][b] = load16(at + ((u >> 1) * 8 + (u & 1)) * row + b * 64);
+          if (off[g] < 0) there &= ~(0xffffu << (g * 16));
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int64_t at = __shfl_sync(0xffffffffu, off[0], g * 16 + (u >> 1) * 8 + 2 * c + (u & 1));
+#pragma unroll
+            for (int b = 0; b < DP / 64; ++b) vr[g][u][b] = load16_if(vb + at + b * 64, at >= 0 && b * 64 + r * 8 < d);
+          }
+        }
+      }
+      if constexpr (kFast) {
+        if (k1 - k < 16 * KG) there &= (1u << (k1 - k)) - 1u;
+      } else {
+        there = __ballot_sync(0xffffffffu, off[0] >= 0);
+      }
+      advance();
       // scores: 16 keys x 8 heads a tile
       float z[KG][NT][4];
 #pragma unroll
       for (int g = 0; g < KG; ++g)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i) z[g][t][i] = 0.f;
 #pragma unroll
-          for (int i = 0; i < DP / 32; ++i) {
-            const uint4 q = query[(t * (DP / 32) + i) * 32];
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < DP / 32; ++i) {
+          const uint4 q = query[(t * (DP / 32) + i) * 32];
+#pragma unroll
+          for (int g = 0; g < KG; ++g) {
             mma16816(z[g][t], kr[g][0][i].x, kr[g][1][i].x, kr[g][0][i].y, kr[g][1][i].y, q.x, q.y);
             mma16816(z[g][t], kr[g][0][i].z, kr[g][1][i].z, kr[g][0][i].w, kr[g][1][i].w, q.z, q.w);
           }
         }
-      load_keys(off);
+      load_keys();
+#pragma unroll
+      for (int g = 0; g < KG; ++g)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[g][t][i] *= p.scale2;
+      if (__builtin_expect(there != 0xffffffffu >> (32 - 16 * KG) && there != 0xffffffffu, 0)) {
+#pragma unroll
+        for (int g = 0; g < KG; ++g) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (!((there >> (g * 16 + (i >> 1) * 8 + r)) & 1u)) z[g][t][i] = -INFINITY;
+          if constexpr (kFast)  // what such a slot holds may be NaN
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (!((there >> (g * 16 + (u >> 1) * 8 + 2 * c + (u & 1))) & 1u))
+#pragma unroll
+                for (int b = 0; b < DP / 64; ++b) vr[g][u][b] = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
       // softmax: the reference of a head moves only when a score passes it by 2^8
       bool move = false;
 #pragma unroll
-      for (int g = 0; g < KG; ++g) {
-        const bool low = (there >> (g * 16 + r)) & 1u, high = (there >> (g * 16 + 8 + r)) & 1u;
+      for (int g = 0; g < KG; ++g)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          z[g][t][0] = low ? z[g][t][0] * p.scale2 : -INFINITY, z[g][t][1] = low ? z[g][t][1] * p.scale2 : -INFINITY;
-          z[g][t][2] = high ? z[g][t][2] * p.scale2 : -INFINITY, z[g][t][3] = high ? z[g][t][3] * p.scale2 : -INFINITY;
+        for (int t = 0; t < NT; ++t)
           move |= fmaxf(z[g][t][0], z[g][t][2]) > m[t][0] + 8.f || fmaxf(z[g][t][1], z[g][t][3]) > m[t][1] + 8.f;
-        }
-      }
       if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -235,10 +323,13 @@ struct Bf16Path {
           const float p0 = exp2_fast(z[g][t][0] - m0), p1 = exp2_fast(z[g][t][1] - m1);
           const float p2 = exp2_fast(z[g][t][2] - m0), p3 = exp2_fast(z[g][t][3] - m1);
           l[t][0] += p0 + p2, l[t][1] += p1 + p3;
-          const uint32_t ha = pack2(p0, p1), hb = pack2(p2, p3);
+          uint32_t ha = pack2(p0, p1), hb = pack2(p2, p3);
           const uint32_t la = pack2(p0 - __uint_as_float(ha << 16), p1 - __uint_as_float(ha & 0xffff0000u));
           const uint32_t lb = pack2(p2 - __uint_as_float(hb << 16), p3 - __uint_as_float(hb & 0xffff0000u));
-          const uint32_t h0 = transpose8(ha), h1 = transpose8(hb), l0 = transpose8(la), l1 = transpose8(lb);
+          if (kTwice) ha = c < 2 ? ha : la, hb = c < 2 ? hb : lb;
+          const uint32_t h0 = transpose8(ha), h1 = transpose8(hb);
+          uint32_t l0, l1;
+          if (!kTwice) l0 = transpose8(la), l1 = transpose8(lb);
 #pragma unroll
           for (int b = 0; b < DP / 64; ++b)
 #pragma unroll
@@ -247,7 +338,7 @@ struct Bf16Path {
               const uint32_t a0 = __byte_perm(va, vc, 0x5410), a1 = __byte_perm(va, vc, 0x7632);
               const uint32_t a2 = __byte_perm(ve, vg, 0x5410), a3 = __byte_perm(ve, vg, 0x7632);
               mma16816(o[t][b][i], a0, a1, a2, a3, h0, h1);
-              mma16816(o[t][b][i], a0, a1, a2, a3, l0, l1);
+              if (!kTwice) mma16816(o[t][b][i], a0, a1, a2, a3, l0, l1);
             }
         }
     }
@@ -259,6 +350,14 @@ struct Bf16Path {
         float total = l[t][e];
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) total += __shfl_xor_sync(0xffffffffu, total, w);
+        if (kTwice)
+#pragma unroll
+          for (int b = 0; b < DP / 64; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              o[t][b][i][e] += __shfl_xor_sync(0xffffffffu, o[t][b][i][e], 2);
+              o[t][b][i][e + 2] += __shfl_xor_sync(0xffffffffu, o[t][b][i][e + 2], 2);
+            }
         if (qh >= n) continue;
         if (r == 0) left[2 * qh] = m[t][e], left[2 * qh + 1] = total;
 #pragma unroll
@@ -273,7 +372,7 @@ struct Bf16Path {
 
 // ---- fp32 ---------------------------------------------------------------------
 
-template <int GH_, int DP_>
+template <int GH_, int DP_, bool kFast>
 struct Fp32Path {
   using T = float;
   static constexpr int DP = DP_, kHeads = GH_;
@@ -296,40 +395,63 @@ struct Fp32Path {
   static __device__ __forceinline__ void run(const DecodeParams& p, const float* mine, float* left, int s, int h, int n, int k0, int k1) {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const int d = p.c.head_dim;
-    const int32_t* table = p.c.page_table + s * p.c.table_stride;
+    const int64_t row = p.c.slot_stride;
     const int vd = (lane % kLanes) * 4, vrow = lane / kLanes;
-    const float *kb = (const float*)p.c.k + c * 4, *vb = (const float*)p.c.v + vd;
-    const int64_t head = (int64_t)h * p.c.head_stride;
+    const float* kb = (const float*)p.c.k + c * 4 + (kFast ? r * row : 0);
+    const float* vb = (const float*)p.c.v + vd + (kFast ? vrow * row : 0);
     const float* sq = mine;
     float* sp = const_cast<float*>(mine) + kHeads * DP;  // [key][head]
     float m[kHeads], l[kHeads];
     float4 o[kHeads];
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) m[i] = -INFINITY, l[i] = 0.f, o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int key_of_lane = lane & (kKeys - 1);
     uint4 kr[KG][DP / 16], vr[kKeys / kRows];
-    auto load_keys = [&](int64_t off) {
-#pragma unroll
-      for (int g = 0; g < KG; ++g) {
-        const int64_t at = __shfl_sync(0xffffffffu, off, g * 8 + r);
-#pragma unroll
-        for (int i = 0; i < DP / 16; ++i) kr[g][i] = load16(kb + at + i * 16, at >= 0 && i * 16 + c * 4 < d);
+    Walk<kFast, kKeys> walk(p, s, h, k0, k1);
+    int64_t off;  // of the step's first key (kFast); of the lane's key
+    auto advance = [&] {
+      if constexpr (kFast) {
+        off = walk.step(kKeys);
+      } else {
+        off = walk.off;
+        walk.turn();
       }
     };
-    int64_t off = key_offset(p, key_page(p, table, k0 + key_of_lane, k1), k0 + key_of_lane, head);
-    int next_key = k0 + kKeys + key_of_lane;
-    int page = key_page(p, table, next_key, k1);
-    load_keys(off);
-    for (int k = k0; k < k1; k += kKeys) {
+    auto load_keys = [&] {
 #pragma unroll
-      for (int i = 0; i < kKeys / kRows; ++i) {
-        const int64_t at = __shfl_sync(0xffffffffu, off, i * kRows + vrow);
-        vr[i] = load16(vb + at, at >= 0 && vd < d);
+      for (int g = 0; g < KG; ++g) {
+        if constexpr (kFast) {
+          const float* at = kb + max(off, (int64_t)0) + g * 8 * row;
+#pragma unroll
+          for (int i = 0; i < DP / 16; ++i) kr[g][i] = load16(at + i * 16);
+        } else {
+          const int64_t at = __shfl_sync(0xffffffffu, off, g * 8 + r);
+#pragma unroll
+          for (int i = 0; i < DP / 16; ++i) kr[g][i] = load16_if(kb + at + i * 16, at >= 0 && i * 16 + c * 4 < d);
+        }
       }
-      const uint32_t there = __ballot_sync(0xffffffffu, off >= 0);
-      off = key_offset(p, page, next_key, head);
-      next_key += kKeys;
-      page = key_page(p, table, next_key, k1);
+    };
+    advance();
+    load_keys();
+    for (int k = k0; k < k1; k += kKeys) {
+      uint32_t there;
+      if constexpr (kFast) {
+        const float* at = vb + max(off, (int64_t)0);
+#pragma unroll
+        for (int i = 0; i < kKeys / kRows; ++i) vr[i] = load16(at + i * kRows * row);
+        there = off < 0 ? 0u : k1 - k < kKeys ? (1u << (k1 - k)) - 1u : (1u << kKeys) - 1u;
+        if (there != (1u << kKeys) - 1u)  // what a slot past the end holds may be NaN
+#pragma unroll
+          for (int i = 0; i < kKeys / kRows; ++i)
+            if (!((there >> (i * kRows + vrow)) & 1u)) vr[i] = make_uint4(0u, 0u, 0u, 0u);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kKeys / kRows; ++i) {
+          const int64_t at = __shfl_sync(0xffffffffu, off, i * kRows + vrow);
+          vr[i] = load16_if(vb + at, at >= 0 && vd < d);
+        }
+        there = __ballot_sync(0xffffffffu, off >= 0);
+      }
+      advance();
       float z[KG][kHeads];
 #pragma unroll
       for (int i = 0; i < kHeads; ++i) {
@@ -348,7 +470,7 @@ struct Fp32Path {
           }
         }
       }
-      load_keys(off);
+      load_keys();
       bool move = false;
 #pragma unroll
       for (int g = 0; g < KG; ++g) {
@@ -693,12 +815,13 @@ extern "C" int gpt_decode_attention(const gpt_paged_cache* c, const gpt_decode_a
   p.piece_ml = (float*)((char*)a->workspace + pl.ml_at);
   p.piece_o = (float*)((char*)a->workspace + pl.o_at);
   const cudaStream_t st = (cudaStream_t)cuda_stream;
-  const bool wide = c->head_dim > 64;
-  if (c->dtype == GPT_DTYPE_BF16) {
-    if (pl.chunk <= 8) return wide ? launch<Bf16Path<1, 128>>(p, pl, st) : launch<Bf16Path<1, 64>>(p, pl, st);
-    return wide ? launch<Bf16Path<2, 128>>(p, pl, st) : launch<Bf16Path<2, 64>>(p, pl, st);
-  }
-  if (pl.chunk == 1) return wide ? launch<Fp32Path<1, 128>>(p, pl, st) : launch<Fp32Path<1, 64>>(p, pl, st);
-  if (pl.chunk <= 4) return wide ? launch<Fp32Path<4, 128>>(p, pl, st) : launch<Fp32Path<4, 64>>(p, pl, st);
-  return wide ? launch<Fp32Path<8, 128>>(p, pl, st) : launch<Fp32Path<8, 64>>(p, pl, st);
+  // the fast form: pages of whole 16-key groups, heads of exactly 64 or 128
+  const bool wide = c->head_dim > 64, fast = c->page_size % 16 == 0 && c->head_dim % 64 == 0;
+#define PGS_LAUNCH(PATH, N)                                                                               \
+  (wide ? fast ? launch<PATH<N, 128, true>>(p, pl, st) : launch<PATH<N, 128, false>>(p, pl, st)           \
+        : fast ? launch<PATH<N, 64, true>>(p, pl, st) : launch<PATH<N, 64, false>>(p, pl, st))
+  if (c->dtype == GPT_DTYPE_BF16)
+    return pl.chunk <= 4 ? PGS_LAUNCH(Bf16Path, 4) : pl.chunk <= 8 ? PGS_LAUNCH(Bf16Path, 8) : PGS_LAUNCH(Bf16Path, 16);
+  return pl.chunk == 1 ? PGS_LAUNCH(Fp32Path, 1) : pl.chunk <= 4 ? PGS_LAUNCH(Fp32Path, 4) : PGS_LAUNCH(Fp32Path, 8);
+#undef PGS_LAUNCH
 }
