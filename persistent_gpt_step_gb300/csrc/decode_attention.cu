@@ -10,16 +10,17 @@
 // HBM bandwidth is the limit at any usual number of query heads per key head.
 // The kernel therefore keeps loads in flight and does as little as possible
 // between them:
-//  - Work is cut by keys, not by rows: the tiles of all (sequence, key heads)
-//    rows are one line, of which every block of a one-wave grid takes an equal
-//    part, whatever the lengths are (the host does not know them).  A row cut by
-//    block boundaries leaves (m, l, o) pieces in the workspace, which a second
-//    kernel joins; rows inside one block are finished there.  Few short rows are
-//    cut into one tile per block instead, so that no block has two parts.
+//  - Work is cut by keys, not by rows: the 16-key tiles of all (sequence, key
+//    head) rows are one line, of which every warp of a one-wave grid takes an equal
+//    part, whatever the lengths are (the host does not know them).  Rows inside one
+//    warp's part are finished from its registers; a row cut by part boundaries
+//    leaves (m, l, o) pieces in shared memory, which the block joins once at its
+//    end, and one cut by block boundaries pieces in the workspace, which a second
+//    kernel joins.
 //  - Each warp reads its keys and values from global memory straight into the
-//    operand registers of its products; no shared memory, no barrier inside a
-//    row.  The values of a step are requested before its keys are used and the
-//    next step's keys before its values are used.
+//    operand registers of its products; no barrier until the warp's part is done.
+//    The values of a step are requested before its keys are used and the next
+//    step's keys before its values are used.
 //  - bf16: 16 keys at a time through mma.m16n8k16, keys (or the 16 value dims) as
 //    the 16-row operand and up to 8 query heads as its 8 columns.  An operand's
 //    16-byte pieces serve as they are: the order of the contraction index is free
@@ -36,8 +37,8 @@
 namespace pgs {
 namespace {
 
-constexpr int kWarps = 8;      // of a block, at most; two blocks per SM
-constexpr int kTile = 32;      // keys of a unit of work
+constexpr int kWarps = 8;      // of a block
+constexpr int kTile = 16;      // keys of a unit of work
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Meta { int32_t seq, row, last, pad; };  // a row begun in this block and ended in block `last`
@@ -46,13 +47,13 @@ struct DecodeParams {
   gpt_paged_cache c;
   gpt_decode_attention_args a;
   int32_t group;     // query heads per key head
-  int32_t chunk;     // query heads of a row per key head
+  int32_t chunk;     // query heads of a row
   int32_t chunks;    // rows of one key head
-  int32_t hc, ws;    // key heads per row, warps per key head
-  int32_t rows;      // rows per sequence
+  int32_t team;      // warps that take the same keys, a key head each
+  int32_t rows;      // rows (of `team` key heads) of one sequence
   float scale2;      // scale log2 e
   Meta* meta;        // [blocks]
-  float *piece_ml, *piece_o;  // [blocks][2][hc chunk][2], [...][head_dim]
+  float *piece_ml, *piece_o;  // [blocks][2][team chunk][2], [...][head_dim]
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -123,9 +124,20 @@ struct Walk {
   }
 };
 
-// What one warp leaves of its keys in shared memory: (m, l) of each head, then their o rows from left_o on.
+// A piece of a row in shared memory: (m, l) of each head, then their o rows from left_o on.
 __host__ __device__ constexpr int left_o(int heads) { return (2 * heads + 3) / 4 * 4; }
 __host__ __device__ constexpr int left_floats(int heads, int dp) { return left_o(heads) + heads * dp; }
+
+__device__ __forceinline__ void store_lse(const DecodeParams& p, int s, int hq, float m, float total) {
+  if (p.a.lse) p.a.lse[(int64_t)s * p.a.n_head + hq] = total == 0.f ? -INFINITY : m * kLn2 + logf(total);
+}
+
+// A warp's part of a row: keys [k0, k1) of sequence s for key head h, query heads
+// hq .. hq + n; left: where its piece goes, or null to finish the row.
+struct Part {
+  int s, h, hq, n, k0, k1;
+  float* left;
+};
 
 // ---- bf16 ---------------------------------------------------------------------
 
@@ -152,12 +164,13 @@ template <int kMode, int DP_, bool kFast>
 struct Bf16Path {
   using T = __nv_bfloat16;
   static constexpr int NT = kMode == 16 ? 2 : 1, DP = DP_, kHeads = kMode;
+  static constexpr int kBlocks = kMode == 16 ? 1 : 2;  // of an SM
   static constexpr bool kTwice = kMode == 4;
   static constexpr int KG = 128 / DP;           // 16-key groups of a step: 32 registers of keys, 32 of values
   static constexpr int kQuery = NT * (DP / 32) * 128;  // a warp's queries: a 16-byte piece per lane, tile and 32 dims
 
   // Lane (r, c): query head r of a tile, dims 32 i + 8 c .. + 7.
-  static __device__ __forceinline__ void stage_query(const DecodeParams& p, float* mine, int s, int h, int first, int n) {
+  static __device__ __forceinline__ void stage_query(const DecodeParams& p, float* mine, const Part& w) {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -165,13 +178,13 @@ struct Bf16Path {
       for (int i = 0; i < DP / 32; ++i) {
         const int qh = kTwice ? r & 3 : t * 8 + r;
         reinterpret_cast<uint4*>(mine)[(t * (DP / 32) + i) * 32 + lane] =
-            load16_if((const T*)p.a.q + s * p.a.q_row + (int64_t)(h * p.group + first + qh) * p.a.q_head + i * 32 + c * 8,
-                      qh < n && i * 32 + c * 8 < p.c.head_dim);
+            load16_if((const T*)p.a.q + w.s * p.a.q_row + (w.hq + qh) * p.a.q_head + i * 32 + c * 8,
+                      qh < w.n && i * 32 + c * 8 < p.c.head_dim);
       }
   }
 
-  // Keys [k0, k1) of sequence s for key head h and the n staged query heads.
-  static __device__ __forceinline__ void run(const DecodeParams& p, const float* mine, float* left, int s, int h, int n, int k0, int k1) {
+  static __device__ __forceinline__ void run(const DecodeParams& p, const float* mine, const Part& w) {
+    const int k0 = w.k0, k1 = w.k1;
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const int d = p.c.head_dim;
     const int64_t row = p.c.slot_stride;
@@ -188,7 +201,7 @@ struct Bf16Path {
         for (int i = 0; i < 16; ++i) o[t][b][i / 4][i % 4] = 0.f;
     }
     uint4 kr[KG][2][DP / 32], vr[KG][4][DP / 64];
-    Walk<kFast, 16 * KG> walk(p, s, h, k0, k1);
+    Walk<kFast, 16 * KG> walk(p, w.s, w.h, k0, k1);
     int64_t off[KG];  // of the step's groups (kFast); of the lane's key
     auto advance = [&] {
       if constexpr (kFast) {
@@ -305,7 +318,7 @@ struct Bf16Path {
 #pragma unroll
             for (int g = 0; g < KG; ++g) top = fmaxf(top, fmaxf(z[g][t][e], z[g][t][e + 2]));
 #pragma unroll
-            for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
             const float keep = weight(m[t][e], top);
             m[t][e] = top;
             l[t][e] *= keep;
@@ -349,7 +362,7 @@ struct Bf16Path {
         const int qh = t * 8 + 2 * c + e;
         float total = l[t][e];
 #pragma unroll
-        for (int w = 4; w < 32; w <<= 1) total += __shfl_xor_sync(0xffffffffu, total, w);
+        for (int x = 4; x < 32; x <<= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
         if (kTwice)
 #pragma unroll
           for (int b = 0; b < DP / 64; ++b)
@@ -358,13 +371,24 @@ struct Bf16Path {
               o[t][b][i][e] += __shfl_xor_sync(0xffffffffu, o[t][b][i][e], 2);
               o[t][b][i][e + 2] += __shfl_xor_sync(0xffffffffu, o[t][b][i][e + 2], 2);
             }
-        if (qh >= n) continue;
-        if (r == 0) left[2 * qh] = m[t][e], left[2 * qh + 1] = total;
+        if (qh >= w.n) continue;
+        if (w.left) {
+          if (r == 0) w.left[2 * qh] = m[t][e], w.left[2 * qh + 1] = total;
 #pragma unroll
-        for (int b = 0; b < DP / 64; ++b) {
-          float4* to = reinterpret_cast<float4*>(left + left_o(kHeads) + qh * DP + b * 64 + r * 8);
-          to[0] = make_float4(o[t][b][0][e], o[t][b][0][e + 2], o[t][b][1][e], o[t][b][1][e + 2]);
-          to[1] = make_float4(o[t][b][2][e], o[t][b][2][e + 2], o[t][b][3][e], o[t][b][3][e + 2]);
+          for (int b = 0; b < DP / 64; ++b) {
+            float4* to = reinterpret_cast<float4*>(w.left + left_o(kHeads) + qh * DP + b * 64 + r * 8);
+            to[0] = make_float4(o[t][b][0][e], o[t][b][0][e + 2], o[t][b][1][e], o[t][b][1][e + 2]);
+            to[1] = make_float4(o[t][b][2][e], o[t][b][2][e + 2], o[t][b][3][e], o[t][b][3][e + 2]);
+          }
+        } else {
+          const float inv = total == 0.f ? 0.f : 1.0f / total;
+          T* to = (T*)p.a.out + w.s * p.a.out_row + (w.hq + qh) * p.a.out_head + r * 8;
+#pragma unroll
+          for (int b = 0; b < DP / 64; ++b)
+            if (kFast || b * 64 + r * 8 < d)
+              *reinterpret_cast<uint4*>(to + b * 64) = make_uint4(pack2(o[t][b][0][e] * inv, o[t][b][0][e + 2] * inv), pack2(o[t][b][1][e] * inv, o[t][b][1][e + 2] * inv),
+                                                                  pack2(o[t][b][2][e] * inv, o[t][b][2][e + 2] * inv), pack2(o[t][b][3][e] * inv, o[t][b][3][e + 2] * inv));
+          if (r == 0) store_lse(p, w.s, w.hq + qh, m[t][e], total);
         }
       }
   }
@@ -375,24 +399,24 @@ struct Bf16Path {
 template <int GH_, int DP_, bool kFast>
 struct Fp32Path {
   using T = float;
-  static constexpr int DP = DP_, kHeads = GH_;
+  static constexpr int DP = DP_, kHeads = GH_, kBlocks = 2;
   static constexpr int KG = 128 / DP;            // 8-key groups of a step: 32 registers of keys, 32 of values
   static constexpr int kKeys = 8 * KG;
   static constexpr int kLanes = DP / 4;          // lanes to a row of values
   static constexpr int kRows = 32 / kLanes;      // rows of values a load covers
   static constexpr int kQuery = kHeads * DP + kKeys * kHeads;  // a warp's queries and probabilities
 
-  static __device__ __forceinline__ void stage_query(const DecodeParams& p, float* mine, int s, int h, int first, int n) {
+  static __device__ __forceinline__ void stage_query(const DecodeParams& p, float* mine, const Part& w) {
     __syncwarp();
     for (int i = threadIdx.x & 31; i < kHeads * DP; i += 32) {
       const int qh = i / DP, e = i % DP;
-      mine[i] = qh < n && e < p.c.head_dim
-                    ? ((const float*)p.a.q)[s * p.a.q_row + (int64_t)(h * p.group + first + qh) * p.a.q_head + e] : 0.f;
+      mine[i] = qh < w.n && e < p.c.head_dim ? ((const float*)p.a.q)[w.s * p.a.q_row + (w.hq + qh) * p.a.q_head + e] : 0.f;
     }
     __syncwarp();
   }
 
-  static __device__ __forceinline__ void run(const DecodeParams& p, const float* mine, float* left, int s, int h, int n, int k0, int k1) {
+  static __device__ __forceinline__ void run(const DecodeParams& p, const float* mine, const Part& w) {
+    const int k0 = w.k0, k1 = w.k1;
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const int d = p.c.head_dim;
     const int64_t row = p.c.slot_stride;
@@ -406,7 +430,7 @@ struct Fp32Path {
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) m[i] = -INFINITY, l[i] = 0.f, o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     uint4 kr[KG][DP / 16], vr[kKeys / kRows];
-    Walk<kFast, kKeys> walk(p, s, h, k0, k1);
+    Walk<kFast, kKeys> walk(p, w.s, w.h, k0, k1);
     int64_t off;  // of the step's first key (kFast); of the lane's key
     auto advance = [&] {
       if constexpr (kFast) {
@@ -490,7 +514,7 @@ struct Fp32Path {
 #pragma unroll
           for (int g = 0; g < KG; ++g) top = fmaxf(top, z[g][i]);
 #pragma unroll
-          for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+          for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
           const float keep = weight(m[i], top);
           m[i] = top;
           l[i] *= keep;
@@ -522,17 +546,25 @@ struct Fp32Path {
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
 #pragma unroll
-      for (int w = 4; w < 32; w <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
+      for (int x = 4; x < 32; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
 #pragma unroll
-      for (int w = kLanes; w < 32; w <<= 1) {
-        o[i].x += __shfl_xor_sync(0xffffffffu, o[i].x, w);
-        o[i].y += __shfl_xor_sync(0xffffffffu, o[i].y, w);
-        o[i].z += __shfl_xor_sync(0xffffffffu, o[i].z, w);
-        o[i].w += __shfl_xor_sync(0xffffffffu, o[i].w, w);
+      for (int x = kLanes; x < 32; x <<= 1) {
+        o[i].x += __shfl_xor_sync(0xffffffffu, o[i].x, x);
+        o[i].y += __shfl_xor_sync(0xffffffffu, o[i].y, x);
+        o[i].z += __shfl_xor_sync(0xffffffffu, o[i].z, x);
+        o[i].w += __shfl_xor_sync(0xffffffffu, o[i].w, x);
       }
-      if (i >= n) continue;
-      if (lane == 0) left[2 * i] = m[i], left[2 * i + 1] = l[i];
-      if (vrow == 0) *reinterpret_cast<float4*>(left + left_o(kHeads) + i * DP + vd) = o[i];
+      if (i >= w.n) continue;
+      if (w.left) {
+        if (lane == 0) w.left[2 * i] = m[i], w.left[2 * i + 1] = l[i];
+        if (vrow == 0) *reinterpret_cast<float4*>(w.left + left_o(kHeads) + i * DP + vd) = o[i];
+      } else {
+        const float inv = l[i] == 0.f ? 0.f : 1.0f / l[i];
+        if (vrow == 0 && vd < d)
+          *reinterpret_cast<float4*>((float*)p.a.out + w.s * p.a.out_row + (w.hq + i) * p.a.out_head + vd) =
+              make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv);
+        if (lane == 0) store_lse(p, w.s, w.hq + i, m[i], l[i]);
+      }
     }
   }
 };
@@ -557,162 +589,221 @@ __device__ __forceinline__ int64_t block_total(int64_t v, int64_t* red) {
 }
 
 template <class P>
-__global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, P::kBlocks) decode_kernel(const __grid_constant__ DecodeParams p) {
   using T = typename P::T;
   constexpr int kLeft = left_floats(P::kHeads, P::DP);
-  extern __shared__ __align__(16) float sm[];
-  __shared__ int64_t red[kWarps], found_base;
-  __shared__ int found_seq;
+  extern __shared__ __align__(16) float sm[];  // [kWarps][2] pieces, [kWarps] queries
+  __shared__ int64_t red[kWarps], total_before[kWarps * 32];
+  __shared__ struct { int s, row, valid, ends, tiles; } info[kWarps][2];  // a team's pieces: that continues a row, that begins one
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n_seq = p.c.n_seq, d = p.c.head_dim;
   const int blk = blockIdx.x, blocks = gridDim.x;
+  if (tid < 2 * kWarps) info[tid >> 1][tid & 1].valid = 0;
+  if (tid == 0) p.meta[blk].seq = -1;
 
   // the line of work: tiles of all sequences' rows
-  int64_t small = 0, large = 0;
-  const int large_tile = max(kTile, p.ws * 16);
-  for (int s = tid; s < n_seq; s += blockDim.x) {
-    const int len = seq_len(p, s, blk == 0);
-    small += (len + kTile - 1) / kTile;
-    large += (len + large_tile - 1) / large_tile;
-  }
-  small = block_total(small, red) * p.rows;
-  large = block_total(large, red) * p.rows;
-  const bool few = large <= blocks;  // a tile of 16 keys per warp for every block
-  const int tile = few ? large_tile : kTile;
-  const int64_t units = few ? large : small;
-  const int active = (int)min((int64_t)blocks, units);
-  const int64_t begin = blk < active ? blk * units / active : 0, end = blk < active ? (blk + 1) * units / active : 0;
-  if (tid == 0) p.meta[blk].seq = -1;
+  int64_t units = 0;
+  for (int s = tid; s < n_seq; s += kWarps * 32) units += (seq_len(p, s, blk == 0) + kTile - 1) / kTile;
+  units = block_total(units, red) * p.rows;
+  const int teams = kWarps / p.team, team = warp / p.team, hl = warp % p.team;
+  const int64_t active = min((int64_t)blocks * teams, units), gt = (int64_t)blk * teams + team;
+  const int64_t begin = gt < active ? gt * units / active : 0, end = gt < active ? (gt + 1) * units / active : 0;
 
   // sequences of no keys
   for (int s = blk; s < n_seq; s += blocks)
     if (seq_len(p, s, false) == 0) {
       const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int i = tid; i < p.a.n_head * (d / 4); i += blockDim.x)
+      for (int i = tid; i < p.a.n_head * (d / 4); i += kWarps * 32)
         store4((T*)p.a.out + s * p.a.out_row + i / (d / 4) * p.a.out_head + i % (d / 4) * 4, zero);
-      if (p.a.lse)
-        for (int h = tid; h < p.a.n_head; h += blockDim.x) p.a.lse[(int64_t)s * p.a.n_head + h] = -INFINITY;
+      for (int h = tid; h < p.a.n_head; h += kWarps * 32) store_lse(p, s, h, 0.f, 0.f);
     }
-  if (begin == end) return;
+  if ((int64_t)blk * teams >= active) return;
 
-  // the sequence that the block begins in
+  // the sequence that each warp begins in, and its units before that
+  int s = 0;
+  int64_t into = 0;
   int64_t base = 0;
-  for (int s0 = 0; s0 < n_seq; s0 += blockDim.x) {
-    const int s = s0 + tid;
-    const int64_t mine = s < n_seq ? (int64_t)((seq_len(p, s, false) + tile - 1) / tile) * p.rows : 0;
+  for (int s0 = 0; s0 < n_seq; s0 += kWarps * 32) {
+    const int64_t mine = s0 + tid < n_seq ? (int64_t)((seq_len(p, s0 + tid, false) + kTile - 1) / kTile) * p.rows : 0;
     int64_t sum = mine;  // inclusive, over the warp, then the block
 #pragma unroll
-    for (int w = 1; w < 32; w <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, sum, w);
-      if (lane >= w) sum += x;
+    for (int x = 1; x < 32; x <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, sum, x);
+      if (lane >= x) sum += y;
     }
     __syncthreads();
     if (lane == 31) red[warp] = sum;
     __syncthreads();
-    int64_t total = 0;
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
-      if (w == warp) sum += total;
-      total += red[w];
+    int64_t total = base;
+#pragma unroll
+    for (int x = 0; x < kWarps; ++x) {
+      if (x == warp) sum += total;
+      total += red[x];
     }
-    if (base + sum - mine <= begin && begin < base + sum) found_seq = s, found_base = base + sum - mine;
-    if (begin < base + total) break;
-    base += total;
+    total_before[tid] = sum - mine;
+    __syncthreads();
+    if (begin >= base && begin < total) {  // the last sequence that starts at or before `begin`
+      int at = 0;
+#pragma unroll
+      for (int x = kWarps * 16; x > 0; x >>= 1)
+        if (at + x < min(kWarps * 32, n_seq - s0) && total_before[at + x] <= begin) at += x;
+      s = s0 + at;
+      into = begin - total_before[at];
+    }
+    base = total;
+  }
+
+  float* mine = sm + kWarps * 2 * kLeft + warp * P::kQuery;
+  int64_t left = end - begin;
+  if (left > 0) {
+    int len = seq_len(p, s, false), tiles = (len + kTile - 1) / kTile;
+    int row = (int)(into / tiles), t0 = (int)(into % tiles);
+    while (true) {
+      const int t1 = (int)min((int64_t)tiles, t0 + left);
+      const bool whole = t0 == 0 && t1 == tiles;
+      Part w;
+      w.s = s, w.h = row / p.chunks * p.team + hl;
+      w.hq = w.h * p.group + row % p.chunks * p.chunk, w.n = min(p.chunk, (w.h + 1) * p.group - w.hq);
+      w.k0 = t0 * kTile, w.k1 = min(len, t1 * kTile);
+      w.left = whole ? nullptr : sm + (warp * 2 + (t0 == 0)) * kLeft;
+      P::stage_query(p, mine, w);
+      P::run(p, mine, w);
+      if (!whole && hl == 0 && lane == 0) {
+        auto& f = info[team][t0 == 0];
+        f.s = s, f.row = row, f.valid = 1, f.ends = t1 == tiles, f.tiles = tiles - t1;
+      }
+      left -= t1 - t0;
+      if (left == 0) break;
+      t0 = 0;
+      if (++row == p.rows) {
+        row = 0;
+        do len = seq_len(p, ++s, false); while (len == 0);
+        tiles = (len + kTile - 1) / kTile;
+      }
+    }
   }
   __syncthreads();
-  int s = found_seq;
-  base = found_base;
 
-  const int heads = p.hc * p.chunk;  // query heads of a row
-  float* mine = sm + kWarps * kLeft + warp * P::kQuery;
-  for (int64_t u = begin; u < end;) {
-    const int len = seq_len(p, s, false), tiles = (len + tile - 1) / tile;
-    if (tiles == 0) { ++s; continue; }
-    const int row = (int)((u - base) / tiles), t0 = (int)((u - base) % tiles);
-    const int t1 = (int)min((int64_t)tiles, t0 + (end - u));
+  // Join the pieces of each row: one that begins a row or comes from the block
+  // before, then the next teams' continuations.
+  for (int j = 0; j < 2 * teams;) {
+    if (!info[j >> 1][j & 1].valid) { ++j; continue; }
+    int last = j;  // pieces j, then 2 (j / 2 + 1), ... last
+    while (!info[last >> 1][last & 1].ends && (last | 1) + 1 < 2 * teams && info[(last >> 1) + 1][0].valid) last = (last | 1) + 1;
+    const int ps = info[j >> 1][j & 1].s, row = info[j >> 1][j & 1].row;
+    const bool begins = j & 1, ends = info[last >> 1][last & 1].ends;
     const int first = row % p.chunks * p.chunk, n = min(p.chunk, p.group - first);
-    const int h0 = row / p.chunks * p.hc;  // first key head of the row
-    {  // the warp's part of the keys, in steps of 16
-      const int steps = (min(len, t1 * tile) - t0 * tile + 15) / 16, each = (steps + p.ws - 1) / p.ws;
-      const int k0 = t0 * tile + (warp % p.ws) * each * 16, k1 = min(min(len, t1 * tile), k0 + each * 16);
-      P::stage_query(p, mine, s, h0 + warp / p.ws, first, n);
-      P::run(p, mine, sm + warp * kLeft, s, h0 + warp / p.ws, n, k0, k1);
-    }
-    __syncthreads();
-    // join the warps of a key head; finish the row, or leave a piece of it
-    const bool whole = t0 == 0 && t1 == tiles;
-    const int64_t slot = 2 * blk + (t0 == 0 ? 1 : 0);
-    for (int i = tid; i < p.hc * n * (d / 4); i += blockDim.x) {
-      const int e = i % (d / 4) * 4, qh = i / (d / 4) % n, hl = i / (d / 4) / n;
+    const int64_t slot = 2 * blk + begins;
+    for (int i = tid; i < p.team * n * (d / 4); i += kWarps * 32) {
+      const int e = i % (d / 4) * 4, qh = i / (d / 4) % n, g = i / (d / 4) / n;
+      const int hq = (row / p.chunks * p.team + g) * p.group + first + qh;
       float top = -INFINITY, total = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int w = hl * p.ws; w < (hl + 1) * p.ws; ++w) top = fmaxf(top, sm[w * kLeft + 2 * qh]);
-      for (int w = hl * p.ws; w < (hl + 1) * p.ws; ++w) {
-        const float* from = sm + w * kLeft;
+      auto piece = [&](int k) { return sm + (((k >> 1) * p.team + g) * 2 + (k & 1)) * kLeft; };
+      for (int k = j; k <= last; k = (k | 1) + 1) top = fmaxf(top, piece(k)[2 * qh]);
+      for (int k = j; k <= last; k = (k | 1) + 1) {
+        const float* from = piece(k);
         const float keep = weight(from[2 * qh], top);
         total += from[2 * qh + 1] * keep;
         const float4 y = *reinterpret_cast<const float4*>(from + left_o(P::kHeads) + qh * P::DP + e);
         x[0] += y.x * keep, x[1] += y.y * keep, x[2] += y.z * keep, x[3] += y.w * keep;
       }
-      const int hq = (h0 + hl) * p.group + first + qh;
-      if (whole) {
+      if (begins && ends) {
         const float inv = total == 0.f ? 0.f : 1.0f / total;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] *= inv;
-        store4((T*)p.a.out + s * p.a.out_row + hq * p.a.out_head + e, x);
-        if (e == 0 && p.a.lse) p.a.lse[(int64_t)s * p.a.n_head + hq] = total == 0.f ? -INFINITY : top * kLn2 + logf(total);
+        for (int k = 0; k < 4; ++k) x[k] *= inv;
+        store4((T*)p.a.out + ps * p.a.out_row + hq * p.a.out_head + e, x);
+        if (e == 0) store_lse(p, ps, hq, top, total);
       } else {
-        const int64_t at = slot * heads + hl * p.chunk + qh;
+        const int64_t at = (slot * p.team + g) * p.chunk + qh;
         if (e == 0) p.piece_ml[2 * at] = top, p.piece_ml[2 * at + 1] = total;
         store4(p.piece_o + at * d + e, x);
       }
     }
-    u += t1 - t0;
-    if (t0 == 0 && t1 < tiles && tid == 0) {  // the row goes on: where does it end?
-      const int64_t stop = base + (int64_t)(row + 1) * tiles;
-      int last = (int)((stop * active - 1) / units);
-      while (last + 1 < active && (last + 1) * units / active < stop) ++last;
-      while (last > blk && last * units / active >= stop) --last;
-      p.meta[blk] = Meta{s, row, last, 0};
+    if (begins && !ends && tid == 0) {  // the row goes on in later blocks: where does it end?
+      const int64_t stop = ((int64_t)blk * teams + (j >> 1) + 1) * units / active + info[j >> 1][1].tiles;
+      int64_t to = (stop * active - 1) / units;
+      while ((to + 1) * units / active < stop) ++to;
+      while (to * units / active >= stop) --to;
+      p.meta[blk] = Meta{ps, row, (int)(to / teams), 0};
     }
-    if (u - base == (int64_t)tiles * p.rows) base = u, ++s;
-    __syncthreads();
+    j = last + 1;
   }
 }
 
-// A row that several blocks worked on: the pieces of its blocks, joined; a warp
-// per query head.
+// A row that several blocks worked on: the pieces of its blocks, joined.  Block
+// (b, y): the row begun in block b, its query heads from 8 y on; the warps share
+// the heads and, where these are fewer, the pieces.
 template <typename T>
 __global__ void __launch_bounds__(256) decode_join_kernel(const __grid_constant__ DecodeParams p) {
+  __shared__ float sm_ml[8][2], sm_o[8][128];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int blk = blockIdx.x, lane = threadIdx.x & 31, d = p.c.head_dim;
+  const int blk = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = p.c.head_dim;
   const Meta mt = p.meta[blk];
   if (mt.seq < 0) return;
-  const int first = mt.row % p.chunks * p.chunk, n = min(p.chunk, p.group - first), h0 = mt.row / p.chunks * p.hc;
-  const int heads = p.hc * p.chunk, pieces = mt.last - blk + 1;
-  for (int i = threadIdx.x >> 5; i < p.hc * n; i += 8) {
-    const int hl = i / n, qh = i % n;
-    auto at = [&](int j) { return (int64_t)(j == 0 ? 2 * blk + 1 : 2 * (blk + j)) * heads + hl * p.chunk + qh; };
-    float top = -INFINITY;
-    for (int j = lane; j < pieces; j += 32) top = fmaxf(top, p.piece_ml[2 * at(j)]);
+  const int first = mt.row % p.chunks * p.chunk, n = min(p.chunk, p.group - first), pieces = mt.last - blk + 1;
+  const int heads = min(8, p.team * n - 8 * (int)blockIdx.y);
+  if (heads <= 0) return;
+  const int share = pieces > 2 ? 8 / heads : 1;  // warps of a head
+  const int i = 8 * blockIdx.y + warp / share, sub = warp % share, g = i / n, qh = i % n;
+  const bool mine = warp / share < heads;
+  float top = -INFINITY, total = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+  if (mine) {
+    const int e = min(lane * 4, d - 4);
+    auto at = [&](int j) { return ((int64_t)(j == 0 ? 2 * blk + 1 : 2 * (blk + j)) * p.team + g) * p.chunk + qh; };
+    for (int j0 = sub; j0 < pieces; j0 += 32 * share) {  // a piece per lane at a time
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (j0 + lane * share < pieces) ml = *reinterpret_cast<const float2*>(p.piece_ml + 2 * at(j0 + lane * share));
+      float best = fmaxf(top, ml.x);
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-    float total = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int j = 0; j < pieces; ++j) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.piece_ml + 2 * at(j));
-      const float keep = weight(ml.x, top);
-      total += ml.y * keep;
-      if (lane * 4 < d) {
-        const float4 y = *reinterpret_cast<const float4*>(p.piece_o + at(j) * d + lane * 4);
-        x[0] += y.x * keep, x[1] += y.y * keep, x[2] += y.z * keep, x[3] += y.w * keep;
+      for (int w = 16; w > 0; w >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, w));
+      const float keep = weight(top, best), factor = weight(ml.x, best);
+      float sum = ml.y * factor;
+#pragma unroll
+      for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+      total = total * keep + sum;
+      top = best;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] *= keep;
+      const int count = min(32, (pieces - j0 + share - 1) / share);
+      for (int j = 0; j < count; j += 8) {
+        float4 y[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) y[u] = *reinterpret_cast<const float4*>(p.piece_o + at(j0 + min(j + u, count - 1) * share) * d + e);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const float f = __shfl_sync(0xffffffffu, factor, (j + u) & 31);
+          if (j + u < count) x[0] += y[u].x * f, x[1] += y[u].y * f, x[2] += y[u].z * f, x[3] += y[u].w * f;
+        }
       }
     }
-    const int hq = (h0 + hl) * p.group + first + qh;
-    const float inv = total == 0.f ? 0.f : 1.0f / total;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] *= inv;
-    if (lane * 4 < d) store4((T*)p.a.out + mt.seq * p.a.out_row + hq * p.a.out_head + lane * 4, x);
-    if (lane == 0 && p.a.lse) p.a.lse[(int64_t)mt.seq * p.a.n_head + hq] = total == 0.f ? -INFINITY : top * kLn2 + logf(total);
   }
+  if (share > 1) {  // the first warp of a head adds the others'
+    if (lane == 0) sm_ml[warp][0] = top, sm_ml[warp][1] = total;
+    store4(&sm_o[warp][lane * 4], x);
+    __syncthreads();
+    if (!mine || sub) return;
+    float best = top;
+    for (int w = 1; w < share; ++w) best = fmaxf(best, sm_ml[warp + w][0]);
+    const float keep = weight(top, best);
+    total *= keep;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] *= keep;
+    for (int w = 1; w < share; ++w) {
+      const float f = weight(sm_ml[warp + w][0], best);
+      total += sm_ml[warp + w][1] * f;
+      const float4 y = *reinterpret_cast<const float4*>(&sm_o[warp + w][lane * 4]);
+      x[0] += y.x * f, x[1] += y.y * f, x[2] += y.z * f, x[3] += y.w * f;
+    }
+    top = best;
+  } else if (!mine) {
+    return;
+  }
+  const int hq = (mt.row / p.chunks * p.team + g) * p.group + first + qh;
+  const float inv = total == 0.f ? 0.f : 1.0f / total;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] *= inv;
+  if (lane * 4 < d) store4((T*)p.a.out + mt.seq * p.a.out_row + hq * p.a.out_head + lane * 4, x);
+  if (lane == 0) store_lse(p, mt.seq, hq, top, total);
 }
 
 // ---- host ---------------------------------------------------------------------
@@ -733,23 +824,21 @@ int sm_count() {
   return sms;
 }
 
-struct Plan { int blocks, hc, ws, chunk, chunks; size_t ml_at, o_at, bytes; };
+struct Plan { int blocks, chunk, chunks, team; size_t ml_at, o_at, bytes; };
 
-// How rows are formed and how many blocks share them.
+// Blocks of the grid, query heads of a row, and the workspace.
 Plan make_plan(const gpt_paged_cache* c, int32_t n_head) {
   Plan pl;
-  pl.blocks = 2 * sm_count();
   const int group = n_head / c->n_kv_head;
   pl.chunk = group <= 8 ? group : c->dtype == GPT_DTYPE_BF16 ? (group < 16 ? group : 16) : 8;
   pl.chunks = (group + pl.chunk - 1) / pl.chunk;
-  // Key heads of a row, a warp or more each: as many as leave two rows per block.
-  // More rows than that only add ends (a join in shared memory, a pipeline that
-  // runs empty); fewer leave pieces to join.
-  pl.hc = 1;
-  for (int hc = 2; hc <= kWarps; ++hc)
-    if (c->n_kv_head % hc == 0 && (int64_t)c->n_seq * (c->n_kv_head / hc) * pl.chunks >= 2 * pl.blocks) pl.hc = hc;
-  pl.ws = kWarps / pl.hc;
-  const size_t records = (size_t)pl.blocks * 2 * pl.hc * pl.chunk;
+  pl.blocks = sm_count() * (pl.chunk > 8 ? 1 : 2);
+#ifndef PGS_TEAM
+#define PGS_TEAM 1
+#endif
+  pl.team = 1;
+  while (pl.team < PGS_TEAM && c->n_kv_head % (2 * pl.team) == 0) pl.team *= 2;
+  const size_t records = (size_t)pl.blocks * 2 * pl.team * pl.chunk;
   pl.ml_at = (pl.blocks * sizeof(Meta) + 15) / 16 * 16;
   pl.o_at = (pl.ml_at + records * 8 + 15) / 16 * 16;
   pl.bytes = pl.o_at + records * c->head_dim * 4;
@@ -758,7 +847,7 @@ Plan make_plan(const gpt_paged_cache* c, int32_t n_head) {
 
 template <class P>
 int launch(const DecodeParams& p, const Plan& pl, cudaStream_t st) {
-  const size_t smem = (size_t)kWarps * (left_floats(P::kHeads, P::DP) + P::kQuery) * sizeof(float);
+  const size_t smem = (size_t)kWarps * (2 * left_floats(P::kHeads, P::DP) + P::kQuery) * sizeof(float);
   static thread_local int ready = -1;  // device whose limit has been raised
   int dev = -1;
   cudaGetDevice(&dev);
@@ -767,14 +856,14 @@ int launch(const DecodeParams& p, const Plan& pl, cudaStream_t st) {
       return check_launch("gpt_decode_attention");
     ready = dev;
   }
-  decode_kernel<P><<<pl.blocks, pl.hc * pl.ws * 32, smem, st>>>(p);
+  decode_kernel<P><<<pl.blocks, kWarps * 32, smem, st>>>(p);
   if (const int rc = check_launch("gpt_decode_attention")) return rc;
   // the second kernel may start while the first one ends; it waits for its results itself
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(pl.blocks), cfg.blockDim = dim3(256), cfg.stream = st, cfg.attrs = &attr, cfg.numAttrs = 1;
+  cfg.gridDim = dim3(pl.blocks, (pl.team * pl.chunk + 7) / 8), cfg.blockDim = dim3(256), cfg.stream = st, cfg.attrs = &attr, cfg.numAttrs = 1;
   cudaLaunchKernelEx(&cfg, decode_join_kernel<typename P::T>, p);
   return check_launch("gpt_decode_attention (join)");
 }
@@ -808,8 +897,8 @@ extern "C" int gpt_decode_attention(const gpt_paged_cache* c, const gpt_decode_a
   p.c = *c;
   p.a = *a;
   p.group = a->n_head / c->n_kv_head;
-  p.chunk = pl.chunk, p.chunks = pl.chunks, p.hc = pl.hc, p.ws = pl.ws;
-  p.rows = c->n_kv_head / pl.hc * pl.chunks;
+  p.chunk = pl.chunk, p.chunks = pl.chunks, p.team = pl.team;
+  p.rows = c->n_kv_head / pl.team * pl.chunks;
   p.scale2 = a->scale * kLog2e;
   p.meta = (Meta*)a->workspace;
   p.piece_ml = (float*)((char*)a->workspace + pl.ml_at);
