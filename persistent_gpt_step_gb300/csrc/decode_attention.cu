@@ -30,6 +30,7 @@
 //    output's own.
 //  - fp32: fused multiply-adds, four lanes to a key for the scores, a lane to
 //    four dims for the values.
+#include <algorithm>
 #include <cmath>
 
 #include "decode_ops.h"
@@ -39,6 +40,11 @@ namespace {
 
 constexpr int kWarps = 8;      // of a block
 constexpr int kTile = 16;      // keys of a unit of work
+// What the start of a row costs a warp, in tiles (the first loads' latencies and the
+// row's end): without it warps with many short rows end last.  200 sequences of 1 to
+// 1,024 keys, 16 heads of 64: 91 us with 0, 85 with 2, 82 with 4, 85 with 8; 256 of 1
+// to 256 keys: 44, 36, 35, 34.
+constexpr int kStart = 4;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Meta { int32_t seq, row, last, pad; };  // a row begun in this block and ended in block `last`
@@ -100,7 +106,6 @@ struct Walk {
     const int lane = threadIdx.x & 31;
     next = k0 + (kWhole ? lane * 16 : lane & (kKeys - 1));
     page = fetch();
-    turn();
   }
   __device__ __forceinline__ int fetch() const {
     if (next >= end) return -1;
@@ -183,7 +188,7 @@ struct Bf16Path {
       }
   }
 
-  static __device__ __forceinline__ void run(const DecodeParams& p, const float* mine, const Part& w) {
+  static __device__ __forceinline__ void run(const DecodeParams& p, float* mine, const Part& w) {
     const int k0 = w.k0, k1 = w.k1;
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const int d = p.c.head_dim;
@@ -231,6 +236,8 @@ struct Bf16Path {
         }
       }
     };
+    stage_query(p, mine, w);
+    walk.turn();
     advance();
     load_keys();
     for (int k = k0; k < k1; k += 16 * KG) {
@@ -415,7 +422,7 @@ struct Fp32Path {
     __syncwarp();
   }
 
-  static __device__ __forceinline__ void run(const DecodeParams& p, const float* mine, const Part& w) {
+  static __device__ __forceinline__ void run(const DecodeParams& p, float* mine, const Part& w) {
     const int k0 = w.k0, k1 = w.k1;
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const int d = p.c.head_dim;
@@ -424,7 +431,7 @@ struct Fp32Path {
     const float* kb = (const float*)p.c.k + c * 4 + (kFast ? r * row : 0);
     const float* vb = (const float*)p.c.v + vd + (kFast ? vrow * row : 0);
     const float* sq = mine;
-    float* sp = const_cast<float*>(mine) + kHeads * DP;  // [key][head]
+    float* sp = mine + kHeads * DP;  // [key][head]
     float m[kHeads], l[kHeads];
     float4 o[kHeads];
 #pragma unroll
@@ -454,6 +461,8 @@ struct Fp32Path {
         }
       }
     };
+    stage_query(p, mine, w);
+    walk.turn();
     advance();
     load_keys();
     for (int k = k0; k < k1; k += kKeys) {
@@ -576,105 +585,107 @@ __device__ __forceinline__ void store4(__nv_bfloat16* to, const float* x) {
   *reinterpret_cast<uint2*>(to) = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
 }
 
-// Sum over the block, in a fixed order, to every thread.
-__device__ __forceinline__ int64_t block_total(int64_t v, int64_t* red) {
-#pragma unroll
-  for (int w = 16; w > 0; w >>= 1) v += __shfl_xor_sync(0xffffffffu, v, w);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0;
-  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) v += red[w];
-  return v;
-}
-
 template <class P>
 __global__ void __launch_bounds__(kWarps * 32, P::kBlocks) decode_kernel(const __grid_constant__ DecodeParams p) {
   using T = typename P::T;
   constexpr int kLeft = left_floats(P::kHeads, P::DP);
   extern __shared__ __align__(16) float sm[];  // [kWarps][2] pieces, [kWarps] queries
-  __shared__ int64_t red[kWarps], total_before[kWarps * 32];
   __shared__ struct { int s, row, valid, ends, tiles; } info[kWarps][2];  // a team's pieces: that continues a row, that begins one
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n_seq = p.c.n_seq, d = p.c.head_dim;
   const int blk = blockIdx.x, blocks = gridDim.x;
+  const int teams = kWarps / p.team, team = warp / p.team, hl = warp % p.team;
   if (tid < 2 * kWarps) info[tid >> 1][tid & 1].valid = 0;
   if (tid == 0) p.meta[blk].seq = -1;
 
-  // the line of work: tiles of all sequences' rows
-  int64_t units = 0;
-  for (int s = tid; s < n_seq; s += kWarps * 32) units += (seq_len(p, s, blk == 0) + kTile - 1) / kTile;
-  units = block_total(units, red) * p.rows;
-  const int teams = kWarps / p.team, team = warp / p.team, hl = warp % p.team;
-  const int64_t active = min((int64_t)blocks * teams, units), gt = (int64_t)blk * teams + team;
-  const int64_t begin = gt < active ? gt * units / active : 0, end = gt < active ? (gt + 1) * units / active : 0;
-
-  // sequences of no keys
-  for (int s = blk; s < n_seq; s += blocks)
-    if (seq_len(p, s, false) == 0) {
-      const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int i = tid; i < p.a.n_head * (d / 4); i += kWarps * 32)
-        store4((T*)p.a.out + s * p.a.out_row + i / (d / 4) * p.a.out_head + i % (d / 4) * 4, zero);
-      for (int h = tid; h < p.a.n_head; h += kWarps * 32) store_lse(p, s, h, 0.f, 0.f);
+  // The line of work: for every row its start (as long as kStart tiles), then its
+  // tiles.  Every warp looks at the sequences for itself, 256 at a time, 8 a lane.
+  constexpr int kLook = 8;
+  int keys[kLook];          // of the lane's sequences
+  int64_t before, total;    // units before them among those looked at, and of all of these
+  auto look_at = [&](int s0) {
+    int64_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < kLook; ++i) {
+      const int s = s0 + lane * kLook + i;
+      keys[i] = s < n_seq ? seq_len(p, s, tid == lane && blk == 0) : 0;
     }
-  if ((int64_t)blk * teams >= active) return;
-
-  // the sequence that each warp begins in, and its units before that
-  int s = 0;
-  int64_t into = 0;
-  int64_t base = 0;
-  for (int s0 = 0; s0 < n_seq; s0 += kWarps * 32) {
-    const int64_t mine = s0 + tid < n_seq ? (int64_t)((seq_len(p, s0 + tid, false) + kTile - 1) / kTile) * p.rows : 0;
-    int64_t sum = mine;  // inclusive, over the warp, then the block
+#pragma unroll
+    for (int i = 0; i < kLook; ++i) sum += keys[i] > 0 ? (keys[i] + kTile - 1) / kTile + kStart : 0;
+    sum *= p.rows;
+    before = sum;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, sum, x);
-      if (lane >= x) sum += y;
+      const int64_t y = __shfl_up_sync(0xffffffffu, before, x);
+      if (lane >= x) before += y;
     }
-    __syncthreads();
-    if (lane == 31) red[warp] = sum;
-    __syncthreads();
-    int64_t total = base;
+    total = __shfl_sync(0xffffffffu, before, 31);
+    before -= sum;
+  };
+  int64_t units = 0;
+  for (int s0 = 0; s0 < n_seq; s0 += 32 * kLook) look_at(s0), units += total;
+  const int64_t active = min((int64_t)blocks * teams, units), gt = (int64_t)blk * teams + team;
+  auto cut = [&](int64_t i) {  // where part i of the line begins
+    return (uint64_t)(i * units) >> 32 ? i * units / active : (int64_t)((uint32_t)(i * units) / (uint32_t)active);
+  };
+  const int64_t begin = gt < active ? cut(gt) : 0, end = gt < active ? cut(gt + 1) : 0;
+
+  auto empty_rows = [&] {  // sequences of no keys
+    for (int s = blk; s < n_seq; s += blocks)
+      if (seq_len(p, s, false) == 0) {
+        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int i = tid; i < p.a.n_head * (d / 4); i += kWarps * 32)
+          store4((T*)p.a.out + s * p.a.out_row + i / (d / 4) * p.a.out_head + i % (d / 4) * 4, zero);
+        for (int h = tid; h < p.a.n_head; h += kWarps * 32) store_lse(p, s, h, 0.f, 0.f);
+      }
+  };
+  if ((int64_t)blk * teams >= active) return empty_rows();
+
+  // the sequence that the team begins in, its keys and the units of it before that
+  int s = 0, len = 0;
+  int64_t into = 0, base = 0;
+  for (int s0 = 0; s0 < n_seq; s0 += 32 * kLook) {
+    if (n_seq > 32 * kLook) look_at(s0);
+    if (begin >= base && begin < base + total) {
+      const int owner = 31 - __clz(__ballot_sync(0xffffffffu, base + before <= begin));  // the last lane at or before `begin`
+      int64_t at = begin - base - before;
 #pragma unroll
-    for (int x = 0; x < kWarps; ++x) {
-      if (x == warp) sum += total;
-      total += red[x];
+      for (int i = 0; i < kLook; ++i) {
+        const int64_t here = keys[i] > 0 ? (int64_t)((keys[i] + kTile - 1) / kTile + kStart) * p.rows : 0;
+        if (at >= 0 && at < here) s = s0 + lane * kLook + i, len = keys[i], into = at;
+        at -= here;
+      }
+      s = __shfl_sync(0xffffffffu, s, owner), len = __shfl_sync(0xffffffffu, len, owner);
+      into = __shfl_sync(0xffffffffu, into, owner);
+      break;
     }
-    total_before[tid] = sum - mine;
-    __syncthreads();
-    if (begin >= base && begin < total) {  // the last sequence that starts at or before `begin`
-      int at = 0;
-#pragma unroll
-      for (int x = kWarps * 16; x > 0; x >>= 1)
-        if (at + x < min(kWarps * 32, n_seq - s0) && total_before[at + x] <= begin) at += x;
-      s = s0 + at;
-      into = begin - total_before[at];
-    }
-    base = total;
+    base += total;
   }
 
   float* mine = sm + kWarps * 2 * kLeft + warp * P::kQuery;
   int64_t left = end - begin;
   if (left > 0) {
-    int len = seq_len(p, s, false), tiles = (len + kTile - 1) / kTile;
-    int row = (int)(into / tiles), t0 = (int)(into % tiles);
+    int tiles = (len + kTile - 1) / kTile;
+    int row, at;  // units of the row before the team's
+    if (into >> 32) row = (int)(into / (tiles + kStart)), at = (int)(into % (tiles + kStart));
+    else row = (uint32_t)into / (uint32_t)(tiles + kStart), at = (uint32_t)into % (uint32_t)(tiles + kStart);
     while (true) {
-      const int t1 = (int)min((int64_t)tiles, t0 + left);
+      const int stop = (int)min((int64_t)(tiles + kStart), at + left);
+      const int t0 = max(at - kStart, 0), t1 = max(stop - kStart, 0);
       const bool whole = t0 == 0 && t1 == tiles;
       Part w;
       w.s = s, w.h = row / p.chunks * p.team + hl;
       w.hq = w.h * p.group + row % p.chunks * p.chunk, w.n = min(p.chunk, (w.h + 1) * p.group - w.hq);
       w.k0 = t0 * kTile, w.k1 = min(len, t1 * kTile);
       w.left = whole ? nullptr : sm + (warp * 2 + (t0 == 0)) * kLeft;
-      P::stage_query(p, mine, w);
-      P::run(p, mine, w);
-      if (!whole && hl == 0 && lane == 0) {
+      if (t1 > t0) P::run(p, mine, w);
+      if (t1 > t0 && !whole && hl == 0 && lane == 0) {
         auto& f = info[team][t0 == 0];
         f.s = s, f.row = row, f.valid = 1, f.ends = t1 == tiles, f.tiles = tiles - t1;
       }
-      left -= t1 - t0;
+      left -= stop - at;
       if (left == 0) break;
-      t0 = 0;
+      at = 0;
       if (++row == p.rows) {
         row = 0;
         do len = seq_len(p, ++s, false); while (len == 0);
@@ -685,49 +696,57 @@ __global__ void __launch_bounds__(kWarps * 32, P::kBlocks) decode_kernel(const _
   __syncthreads();
 
   // Join the pieces of each row: one that begins a row or comes from the block
-  // before, then the next teams' continuations.
-  for (int j = 0; j < 2 * teams;) {
-    if (!info[j >> 1][j & 1].valid) { ++j; continue; }
+  // before, then the next teams' continuations.  Piece 2 t + b: of team t.
+  uint32_t valid, ends;
+  {
+    const bool there = lane < 2 * teams && info[(lane & 15) >> 1][lane & 1].valid;
+    valid = __ballot_sync(0xffffffffu, there);
+    ends = __ballot_sync(0xffffffffu, there && info[(lane & 15) >> 1][lane & 1].ends);
+  }
+  while (valid) {
+    const int j = __ffs(valid) - 1;
     int last = j;  // pieces j, then 2 (j / 2 + 1), ... last
-    while (!info[last >> 1][last & 1].ends && (last | 1) + 1 < 2 * teams && info[(last >> 1) + 1][0].valid) last = (last | 1) + 1;
+    while (!((ends >> last) & 1u) && (valid >> ((last | 1) + 1)) & 1u) last = (last | 1) + 1;
+    valid &= ~((2u << last) - 1u);
     const int ps = info[j >> 1][j & 1].s, row = info[j >> 1][j & 1].row;
-    const bool begins = j & 1, ends = info[last >> 1][last & 1].ends;
+    const bool begins = j & 1, done = begins && (ends >> last) & 1u;
     const int first = row % p.chunks * p.chunk, n = min(p.chunk, p.group - first);
     const int64_t slot = 2 * blk + begins;
-    for (int i = tid; i < p.team * n * (d / 4); i += kWarps * 32) {
-      const int e = i % (d / 4) * 4, qh = i / (d / 4) % n, g = i / (d / 4) / n;
-      const int hq = (row / p.chunks * p.team + g) * p.group + first + qh;
-      float top = -INFINITY, total = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i = tid; i < p.team * p.chunk * (d / 4); i += kWarps * 32) {
+      const int e = i % (d / 4) * 4, qh = i / (d / 4) % p.chunk, g = i / (d / 4) / p.chunk;
+      if (qh >= n) continue;
+      float top = -INFINITY, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
       auto piece = [&](int k) { return sm + (((k >> 1) * p.team + g) * 2 + (k & 1)) * kLeft; };
       for (int k = j; k <= last; k = (k | 1) + 1) top = fmaxf(top, piece(k)[2 * qh]);
       for (int k = j; k <= last; k = (k | 1) + 1) {
         const float* from = piece(k);
         const float keep = weight(from[2 * qh], top);
-        total += from[2 * qh + 1] * keep;
+        sum += from[2 * qh + 1] * keep;
         const float4 y = *reinterpret_cast<const float4*>(from + left_o(P::kHeads) + qh * P::DP + e);
         x[0] += y.x * keep, x[1] += y.y * keep, x[2] += y.z * keep, x[3] += y.w * keep;
       }
-      if (begins && ends) {
-        const float inv = total == 0.f ? 0.f : 1.0f / total;
+      if (done) {
+        const int hq = (row / p.chunks * p.team + g) * p.group + first + qh;
+        const float inv = sum == 0.f ? 0.f : 1.0f / sum;
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[k] *= inv;
         store4((T*)p.a.out + ps * p.a.out_row + hq * p.a.out_head + e, x);
-        if (e == 0) store_lse(p, ps, hq, top, total);
+        if (e == 0) store_lse(p, ps, hq, top, sum);
       } else {
         const int64_t at = (slot * p.team + g) * p.chunk + qh;
-        if (e == 0) p.piece_ml[2 * at] = top, p.piece_ml[2 * at + 1] = total;
+        if (e == 0) p.piece_ml[2 * at] = top, p.piece_ml[2 * at + 1] = sum;
         store4(p.piece_o + at * d + e, x);
       }
     }
-    if (begins && !ends && tid == 0) {  // the row goes on in later blocks: where does it end?
-      const int64_t stop = ((int64_t)blk * teams + (j >> 1) + 1) * units / active + info[j >> 1][1].tiles;
-      int64_t to = (stop * active - 1) / units;
-      while ((to + 1) * units / active < stop) ++to;
-      while (to * units / active >= stop) --to;
-      p.meta[blk] = Meta{ps, row, (int)(to / teams), 0};
+    if (begins && !done && tid == 0) {  // the row goes on in later blocks: which team ends it?
+      const int64_t stop = cut((int64_t)blk * teams + (j >> 1) + 1) + info[j >> 1][1].tiles;
+      int64_t to = (int64_t)((float)stop * (float)active / (float)units);  // then exactly: begins before stop, the next does not
+      while ((to + 1) * units < stop * active) ++to;
+      while (to * units >= stop * active) --to;
+      p.meta[blk] = Meta{ps, row, (int)to / teams, 0};
     }
-    j = last + 1;
   }
+  empty_rows();
 }
 
 // A row that several blocks worked on: the pieces of its blocks, joined.  Block
@@ -833,11 +852,15 @@ Plan make_plan(const gpt_paged_cache* c, int32_t n_head) {
   pl.chunk = group <= 8 ? group : c->dtype == GPT_DTYPE_BF16 ? (group < 16 ? group : 16) : 8;
   pl.chunks = (group + pl.chunk - 1) / pl.chunk;
   pl.blocks = sm_count() * (pl.chunk > 8 ? 1 : 2);
-#ifndef PGS_TEAM
-#define PGS_TEAM 1
-#endif
+  // Teams: warps that read the same keys' neighbouring heads keep DRAM pages open
+  // where a head's row is short (200 sequences of 16 heads of 64: 86 us with teams of
+  // 1, 81 with 4, 82 with 8); but a row of a team is cut into that many more pieces
+  // (one sequence of 131,071 keys and 8 heads: 93 us with 1, 98 with 2, 105 with 4).
+  // So: up to 4, as long as a row does not have more than 16 pieces.
+  const int64_t tiles = ((int64_t)c->max_pages * c->page_size + kTile - 1) / kTile, rows = (int64_t)c->n_kv_head * pl.chunks * c->n_seq;
+  const int64_t used = std::min<int64_t>(pl.blocks, (rows * (tiles + kStart) + kWarps - 1) / kWarps);
   pl.team = 1;
-  while (pl.team < PGS_TEAM && c->n_kv_head % (2 * pl.team) == 0) pl.team *= 2;
+  while (pl.team < 4 && c->n_kv_head % (2 * pl.team) == 0 && used * 2 * pl.team <= 16 * rows) pl.team *= 2;
   const size_t records = (size_t)pl.blocks * 2 * pl.team * pl.chunk;
   pl.ml_at = (pl.blocks * sizeof(Meta) + 15) / 16 * 16;
   pl.o_at = (pl.ml_at + records * 8 + 15) / 16 * 16;
