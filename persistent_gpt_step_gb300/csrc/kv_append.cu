@@ -33,9 +33,15 @@ __device__ __forceinline__ void pair_angle(const AppendParams& p, int i, int pos
   sincospif(2.0f * t, sn, cs);
 }
 
-// One block per token; a thread per 16-byte piece of a head's row, looping over heads.
+constexpr int kThreads = 128;
+constexpr int kUnroll = 4;  // rows of a thread in flight
+
+// Bound: HBM (every element is read and written once).  One block per token.  A
+// thread has one 16-byte piece of the head, whose sines and
+// cosines it computes once, and every kThreads / pieces-th row of the token's q, k
+// and v heads.
 template <typename T>
-__global__ void __launch_bounds__(128) kv_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kN = Piece<T>::kN;
   const gpt_paged_cache& c = p.c;
   const gpt_kv_append_args& a = p.a;
@@ -43,54 +49,60 @@ __global__ void __launch_bounds__(128) kv_append_kernel(const __grid_constant__ 
   const int s = a.seq ? a.seq[n] : (int)n;
   if (s < 0) return;  // padding
   const int pos = a.positions[n];
+  const int pieces = c.head_dim / kN, groups = kThreads / pieces;
+  const int group = threadIdx.x / pieces, e = threadIdx.x % pieces * kN;
+  const int rows = a.n_head + 2 * c.n_kv_head;  // q heads, k heads, v heads
+  uint4 u[kUnroll];
+  auto load = [&](int row0) {
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      int row = row0 + i * groups;
+      if (group >= groups || row >= rows) continue;
+      const T* from;
+      if (row < a.n_head) from = (const T*)a.q + n * a.q_row + row * a.q_head;
+      else if ((row -= a.n_head) < c.n_kv_head) from = (const T*)a.k + n * a.k_row + row * a.k_head;
+      else from = (const T*)a.v + n * a.v_row + (row - c.n_kv_head) * a.v_head;
+      u[i] = __ldcs(reinterpret_cast<const uint4*>(from + e));
+    }
+  };
+  load(group);  // under way while the page is looked up
   const bool bad_seq = s >= c.n_seq;
   const bool bad_pos = pos < 0 || pos >= c.max_pages * c.page_size;
   int page = -1;
   if (!bad_seq && !bad_pos) page = c.page_table[s * c.table_stride + pos / c.page_size];
-  const bool bad_page = !bad_seq && !bad_pos && (page < 0 || page >= c.n_pages);
-  if (bad_seq || bad_pos || bad_page) {
-    if (threadIdx.x == 0)
-      set_status(a.status, (bad_seq ? GPT_STATUS_BAD_SEQ : 0) | (bad_pos ? GPT_STATUS_BAD_POS : 0) |
-                               (bad_page ? GPT_STATUS_BAD_PAGE : 0));
+  float cs[kN / 2], sn[kN / 2];
+#pragma unroll
+  for (int j = 0; j < kN / 2; ++j)
+    if (e + 2 * j < a.rope_dims) pair_angle(p, e / 2 + j, pos, &cs[j], &sn[j]);
+  if (page < 0 || page >= c.n_pages) {
+    if (threadIdx.x == 0) set_status(a.status, bad_seq ? GPT_STATUS_BAD_SEQ : bad_pos ? GPT_STATUS_BAD_POS : GPT_STATUS_BAD_PAGE);
     return;
   }
   const int64_t slot = page * c.page_stride + (pos % c.page_size) * c.slot_stride;
-  const int pieces = c.head_dim / kN;
-  const int rows = a.n_head + 2 * c.n_kv_head;  // q heads, k heads, v heads
-  for (int w = threadIdx.x; w < rows * pieces; w += blockDim.x) {
-    const int row = w / pieces, e = (w % pieces) * kN;
-    const T* src;
-    T* dst;
-    int h = row;
-    bool turn = true;
-    if (h < a.n_head) {
-      src = (const T*)a.q + n * a.q_row + h * a.q_head;
-      dst = (T*)a.q_out + n * a.qo_row + h * a.qo_head;
-    } else if ((h -= a.n_head) < c.n_kv_head) {
-      src = (const T*)a.k + n * a.k_row + h * a.k_head;
-      dst = (T*)c.k + slot + h * c.head_stride;
-    } else {
-      h -= c.n_kv_head;
-      src = (const T*)a.v + n * a.v_row + h * a.v_head;
-      dst = (T*)c.v + slot + h * c.head_stride;
-      turn = false;
-    }
-    uint4 u = *reinterpret_cast<const uint4*>(src + e);
-    if (turn && e < a.rope_dims) {
-      float x[kN];
-      Piece<T>::unpack(u, x);
+  for (int row0 = group; group < groups && row0 < rows; row0 += kUnroll * groups) {
+    if (row0 > group) load(row0);
 #pragma unroll
-      for (int j = 0; j < kN; j += 2)
-        if (e + j < a.rope_dims) {
-          float cs, sn;
-          pair_angle(p, (e + j) / 2, pos, &cs, &sn);
-          const float x0 = x[j], x1 = x[j + 1];
-          x[j] = x0 * cs - x1 * sn;
-          x[j + 1] = x0 * sn + x1 * cs;
-        }
-      u = Piece<T>::pack(x);
+    for (int i = 0; i < kUnroll; ++i) {
+      int row = row0 + i * groups;
+      if (row >= rows) break;
+      if (row < a.n_head + c.n_kv_head && e < a.rope_dims) {
+        float x[kN];
+        Piece<T>::unpack(u[i], x);
+#pragma unroll
+        for (int j = 0; j < kN / 2; ++j)
+          if (e + 2 * j < a.rope_dims) {
+            const float x0 = x[2 * j], x1 = x[2 * j + 1];
+            x[2 * j] = x0 * cs[j] - x1 * sn[j];
+            x[2 * j + 1] = x0 * sn[j] + x1 * cs[j];
+          }
+        u[i] = Piece<T>::pack(x);
+      }
+      T* to;
+      if (row < a.n_head) to = (T*)a.q_out + n * a.qo_row + row * a.qo_head;
+      else if ((row -= a.n_head) < c.n_kv_head) to = (T*)c.k + slot + row * c.head_stride;
+      else to = (T*)c.v + slot + (row - c.n_kv_head) * c.head_stride;
+      *reinterpret_cast<uint4*>(to + e) = u[i];
     }
-    *reinterpret_cast<uint4*>(dst + e) = u;
   }
 }
 
@@ -134,7 +146,7 @@ extern "C" int gpt_kv_append(const gpt_paged_cache* c, const gpt_kv_append_args*
     }
   }
   const cudaStream_t st = (cudaStream_t)cuda_stream;
-  if (c->dtype == GPT_DTYPE_BF16) kv_append_kernel<__nv_bfloat16><<<a->n_tokens, 128, 0, st>>>(p);
-  else kv_append_kernel<float><<<a->n_tokens, 128, 0, st>>>(p);
+  if (c->dtype == GPT_DTYPE_BF16) kv_append_kernel<__nv_bfloat16><<<a->n_tokens, kThreads, 0, st>>>(p);
+  else kv_append_kernel<float><<<a->n_tokens, kThreads, 0, st>>>(p);
   return check_launch("gpt_kv_append");
 }

@@ -122,7 +122,8 @@ def test_attention_refusals(lib, change, word):
     (dict(out_stride=99), "stride"), (dict(history=FAKE, max_history=9, history_stride=8), "stride"),
     (dict(allowed=FAKE, allowed_stride=3), "stride"), (dict(history_lens=FAKE), "history"),
     (dict(prompt_lens=FAKE), "history"), (dict(bias_ids=FAKE), "together"), (dict(bias_values=FAKE), "together"),
-    (dict(out=FAKE, dtype=1), "in place"), (dict(out=FAKE, out_stride=104), "in place")])
+    (dict(out=FAKE, dtype=1), "in place"), (dict(out=FAKE, out_stride=104), "in place"),
+    (dict(logits=FAKE + 2), "boundaries"), (dict(logits=FAKE + 1, dtype=1), "boundaries"), (dict(out=FAKE + 4098), "boundaries")])
 def test_next_token_refusals(lib, change, word):
     change = {"out": FAKE + 4096, **change}
     assert lib.gpt_next_token(ctypes.byref(_token(**change)), None) == -1
