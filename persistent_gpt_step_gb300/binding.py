@@ -141,11 +141,10 @@ SIGNATURES = [
                                    POINTER(c_int32), c_int32]),
     ("gpt_train_step_static", c_int, [POINTER(gpt_config), c_void_p, c_void_p, c_void_p, c_int64,
                                       c_void_p, c_void_p, POINTER(c_float), c_void_p]),
-    # structs by address: a ctypes byref, or bytes packed by the decode module
-    ("gpt_kv_append", c_int, [c_void_p, c_void_p, c_void_p]),
-    ("gpt_decode_attention", c_int, [c_void_p, c_void_p, c_void_p]),
-    ("gpt_decode_attention_workspace", c_size_t, [c_void_p, c_int32]),
-    ("gpt_next_token", c_int, [c_void_p, c_void_p]),
+    ("gpt_kv_append", c_int, [POINTER(gpt_paged_cache), POINTER(gpt_kv_append_args), c_void_p]),
+    ("gpt_decode_attention", c_int, [POINTER(gpt_paged_cache), POINTER(gpt_decode_attention_args), c_void_p]),
+    ("gpt_decode_attention_workspace", c_size_t, [POINTER(gpt_paged_cache), c_int32]),
+    ("gpt_next_token", c_int, [POINTER(gpt_next_token_args), c_void_p]),
     ("gpt_test_attention", c_int, [c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p, c_void_p,
                                    c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
     ("gpt_test_gemm", c_int, [c_int32, c_int32, c_int32, c_int32, c_void_p, c_int64, c_int32,
