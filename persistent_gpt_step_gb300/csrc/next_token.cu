@@ -6,8 +6,11 @@
 // SMs and the row's maximum and sum are joined through shared memory: one launch,
 // no workspace.  Few ids have a penalty or a bias.  Each block marks those of its
 // range in a bitmap, gives them places in a compact table by the bitmap's running
-// popcounts, and counts occurrences and adds biases there; the pass over the logits
-// then looks at one byte of the bitmap per eight ids.
+// popcounts, counts occurrences and adds biases there, works them off one a thread,
+// and writes them over what the pass over the logits left: that pass looks at one
+// byte of the bitmap per eight ids and has no branch for them.  (With the penalties,
+// or only separate stores, inside the pass 512 rows of 131,072 logits and 2,048 tokens
+// took 150 us: nearly every warp has a marked id among its 256.)
 #include <cooperative_groups.h>
 
 #include <cmath>
@@ -22,13 +25,20 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMarked = 4096;            // places of the compact table
-constexpr int kRange = 32768;            // ids marked at once, where the history and the biases fit the table
+constexpr int kRange = 32768;            // ids of a range at most
+constexpr int kMarked = 2048;            // places of the compact table; a range with more marked ids ends before them
+constexpr int kBatch = 8;                // history ids of a thread at a time
+constexpr int kHistory = kBatch * kThreads;
 constexpr int kNoToken = 0x7fffffff;
 constexpr float kLog2e = 1.4426950408889634f;
 
+__device__ __forceinline__ float exp_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * kLog2e));
+  return y;
+}
 // exp(x - m) between partial maxima: 1 where both are the same, infinities too.
-__device__ __forceinline__ float rescale(float x, float m) { return x == m ? 1.0f : exp2f((x - m) * kLog2e); }
+__device__ __forceinline__ float rescale(float x, float m) { return x == m ? 1.0f : exp_fast(x - m); }
 
 struct Best {  // maximum, sum of exp(z - m), smallest id of the maximum
   float m, sum;
@@ -39,27 +49,35 @@ __device__ __forceinline__ Best join(const Best& a, const Best& b) {
   return Best{top, a.sum * rescale(a.m, top) + b.sum * rescale(b.m, top), a.m == b.m ? min(a.id, b.id) : a.m > b.m ? a.id : b.id};
 }
 
-// Eight logits on a 16-byte boundary as floats.
+// Eight logits in one load (fp32: on a 32-byte, bf16: on a 16-byte boundary) as floats.
 __device__ __forceinline__ void load8(const float* z, float* x) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(z)), b = __ldcs(reinterpret_cast<const float4*>(z) + 1);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  asm volatile("ld.global.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+               : "l"(z) : "memory");
 }
 __device__ __forceinline__ void load8(const __nv_bfloat16* z, float* x) {
   Piece<__nv_bfloat16>::unpack(__ldcs(reinterpret_cast<const uint4*>(z)), x);
+}
+__device__ __forceinline__ void store8(float* z, const float* x) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(z), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]),
+               "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+               : "memory");
 }
 __device__ __forceinline__ void load1(const float* z, float* x) { *x = *z; }
 __device__ __forceinline__ void load1(const __nv_bfloat16* z, float* x) { *x = __bfloat162float(*z); }
 
 // Units of eight ids: unit u holds ids 8 u - shift .., the shift chosen so that
-// units of the logits lie on 16-byte boundaries whatever the row's address is.
+// units of the logits lie on boundaries of their size whatever the row's address is.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) next_token_kernel(const __grid_constant__ gpt_next_token_args a) {
+__global__ void __launch_bounds__(kThreads, 4) next_token_kernel(const __grid_constant__ gpt_next_token_args a) {
   __shared__ uint32_t bitmap[kRange / 32];
   __shared__ uint16_t place[kRange / 32];   // marked ids before a word's
-  __shared__ uint32_t seen[kMarked];        // in the history: 2^31; occurrences after the prompt
+  __shared__ uint16_t where[kMarked];       // the marked id of a place, from the range's first on
+  __shared__ uint32_t seen[kMarked];        // occurrences after the prompt; 2^31: in the prompt
   __shared__ float bias[kMarked];
   __shared__ Best warp_best[kWarps], block_best[8];
   __shared__ uint32_t scan[kWarps];
+  __shared__ int fit;
   cg::cluster_group cluster = cg::this_cluster();
   auto started = cluster.barrier_arrive();  // waited for before another block's memory is written
   const int blocks = cluster.num_blocks(), part = cluster.block_rank();
@@ -69,47 +87,106 @@ __global__ void __launch_bounds__(kThreads) next_token_kernel(const __grid_const
   float* z_out = a.out ? a.out + b * a.out_stride : nullptr;
   const uint32_t* allowed = a.allowed ? a.allowed + b * a.allowed_stride : nullptr;
   const int32_t* bias_ids = a.bias_ids ? a.bias_ids + b * a.bias_stride : nullptr;
-  const int32_t* hist = a.history ? a.history + b * a.history_stride : nullptr;
-  int n_hist = 0, n_prompt = 0;
-  if (hist) {
-    n_hist = a.history_lens ? a.history_lens[b] : a.max_history;
-    n_prompt = a.prompt_lens ? a.prompt_lens[b] : 0;
-    if (n_hist < 0 || n_hist > a.max_history) {
-      if (tid == 0) set_status(a.status, GPT_STATUS_BAD_POS);
-      n_hist = n_hist < 0 ? 0 : a.max_history;
-    }
-  }
-  const int n_bias = bias_ids ? a.n_bias : 0;
-  const bool marks = n_hist > 0 || n_bias > 0;
-  const float rep = a.repetition ? a.repetition[b] : 1.f, pres = a.presence ? a.presence[b] : 0.f;
-  const float freq = a.frequency ? a.frequency[b] : 0.f;
-
-  const int shift = (int)((reinterpret_cast<uintptr_t>(z_in) & 15) / sizeof(T));
-  const bool wide_out = z_out && ((reinterpret_cast<uintptr_t>(z_out) / 4 - shift) & 3) == 0;
+  const int shift = (int)((reinterpret_cast<uintptr_t>(z_in) / sizeof(T)) & 7);
+  const bool wide_out = z_out && ((reinterpret_cast<uintptr_t>(z_out) / 4 - shift) & 7) == 0;
   const int units = (int)(((int64_t)a.vocab + shift + 7) / 8);
   const int u0 = (int)((int64_t)part * units / blocks), u1 = (int)((int64_t)(part + 1) * units / blocks);
-  const int step = ((int64_t)n_hist + n_bias <= kMarked ? kRange : kMarked) / 8;  // units marked at once: a place for each id in any case
+  const int32_t* hist = a.history ? a.history + b * a.history_stride : nullptr;
+  const int most = hist ? a.max_history : 0;
+  int n_hist = hist && a.history_lens ? a.history_lens[b] : most;
+  const int n_prompt = hist && a.prompt_lens ? a.prompt_lens[b] : 0;
+
+  // Units w, w + kThreads of the logits, and the mask's bits of their ids.
+  constexpr int kUnroll = 2;
+  float x[kUnroll][8];
+  uint32_t open[kUnroll];
+  auto load = [&](int w0, int v1) {
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int w = w0 + k * kThreads;
+      const int64_t id0 = (int64_t)w * 8 - shift;
+      open[k] = 0xffu;
+      if (w >= v1) continue;
+      if (id0 >= 0 && id0 + 8 <= a.vocab) {
+        load8(z_in + id0, x[k]);
+        if (allowed) {
+          open[k] = allowed[id0 >> 5] >> (id0 & 31);
+          if ((id0 & 31) > 24) open[k] |= allowed[(id0 >> 5) + 1] << (32 - (id0 & 31));
+        }
+      } else {
+        open[k] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int64_t id = id0 + i;
+          const bool there = id >= 0 && id < a.vocab;
+          x[k][i] = -INFINITY;
+          if (there) load1(z_in + id, &x[k][i]);
+          if (there && (!allowed || (allowed[id >> 5] >> (id & 31)) & 1u)) open[k] |= 1u << i;
+        }
+      }
+    }
+  };
+  load(u0 + tid, u1);  // the first of every thread's, under way while the ids are marked
+
+  // The history, kBatch ids of a thread at a time.  One that fits is read once, before
+  // its length is known.
+  const bool at_once = most <= kHistory;
+  int recent[kBatch];
+  auto read_history = [&](int j0, int n) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int j = j0 + i * kThreads + tid;
+      recent[i] = j < n ? hist[j] : -1;
+    }
+  };
+  if (at_once) read_history(0, most);
+  const int n_bias = bias_ids ? a.n_bias : 0;
+  int bias_id = -1;  // the first 32 entries, a lane of warp 0 each
+  float bias_value = 0.f;
+  if (warp == 0 && lane < n_bias) bias_id = bias_ids[lane], bias_value = a.bias_values[b * a.bias_stride + lane];
+  const float rep = a.repetition ? a.repetition[b] : 1.f, pres = a.presence ? a.presence[b] : 0.f;
+  const float freq = a.frequency ? a.frequency[b] : 0.f;
+  if (n_hist < 0 || n_hist > most) {
+    if (tid == 0) set_status(a.status, GPT_STATUS_BAD_POS);
+    n_hist = n_hist < 0 ? 0 : most;
+  }
+  const bool marks = n_hist > 0 || n_bias > 0;
+  uint32_t bad = 0;
 
   Best best{-INFINITY, 0.f, kNoToken};
-  for (int v0 = u0; v0 < u1; v0 += step) {
-    const int v1 = min(u1, v0 + step), words = (v1 - v0 + 3) / 4;
-    const int64_t first = (int64_t)v0 * 8 - shift;  // the id of bit 0
-    const int ids = (v1 - v0) * 8;
+  for (int v0 = u0, v1; v0 < u1; v0 = v1) {
+    v1 = min(u1, v0 + kRange / 8);
+    const int words = (v1 - v0 + 3) / 4;
+    const int first = (int)((int64_t)v0 * 8 - shift);  // the id of bit 0
+    uint32_t ids = (v1 - v0) * 8, marked = 0;
+    auto inside = [&](int id) { return (uint32_t)id < (uint32_t)a.vocab && (uint32_t)(id - first) < ids; };
+    if (v0 > u0) load(v0 + tid, v1);
     if (marks) {
       for (int i = tid; i < words; i += kThreads) bitmap[i] = 0;
+      const int places = (int)min((uint64_t)kMarked, (uint64_t)n_hist + n_bias);
+      for (int i = tid; i < places; i += kThreads) seen[i] = 0, bias[i] = 0.f;
+      if (tid == 0) fit = kRange / 32;
       __syncthreads();
-      for (int j = tid; j < n_hist; j += kThreads) {
-        const int id = hist[j];
-        if (id < 0 || id >= a.vocab) { set_status(a.status, GPT_STATUS_BAD_TOKEN); continue; }
-        const int64_t i = id - first;
-        if (i >= 0 && i < ids) atomicOr(&bitmap[i >> 5], 1u << (i & 31));
+      auto mark = [&](int id) {
+        if (inside(id)) atomicOr(&bitmap[(id - first) >> 5], 1u << ((id - first) & 31));
+      };
+      for (int j0 = 0; j0 < n_hist; j0 += kHistory) {
+        if (!at_once) read_history(j0, n_hist);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int j = j0 + i * kThreads;
+          if (j >= n_hist) break;
+          const bool there = j + tid < n_hist;
+          bad |= there && (uint32_t)recent[i] >= (uint32_t)a.vocab;
+          if (there) mark(recent[i]);
+        }
       }
-      for (int j = tid; j < n_bias; j += kThreads) {
-        const int id = bias_ids[j];
-        if (id >= a.vocab) { set_status(a.status, GPT_STATUS_BAD_TOKEN); continue; }
-        const int64_t i = id - first;
-        if (id >= 0 && i >= 0 && i < ids) atomicOr(&bitmap[i >> 5], 1u << (i & 31));
-      }
+      if (warp == 0)
+        for (int j = lane; j < n_bias; j += 32) {
+          const int id = j < 32 ? bias_id : bias_ids[j];
+          bad |= id >= a.vocab;
+          mark(id);
+        }
       __syncthreads();
       // places: running popcounts, kRange / 32 / kThreads words a thread
       constexpr int kPer = kRange / 32 / kThreads;
@@ -118,14 +195,13 @@ __global__ void __launch_bounds__(kThreads) next_token_kernel(const __grid_const
       for (int i = 0; i < kPer; ++i) mine += tid * kPer + i < words ? __popc(bitmap[tid * kPer + i]) : 0;
       sum = mine;
 #pragma unroll
-      for (int x = 1; x < 32; x <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, sum, x);
-        if (lane >= x) sum += y;
+      for (int y = 1; y < 32; y <<= 1) {
+        const uint32_t z = __shfl_up_sync(0xffffffffu, sum, y);
+        if (lane >= y) sum += z;
       }
       if (lane == 31) scan[warp] = sum;
       __syncthreads();
       sum -= mine;
-      uint32_t marked = 0;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         if (w == warp) sum += marked;
@@ -135,110 +211,112 @@ __global__ void __launch_bounds__(kThreads) next_token_kernel(const __grid_const
       for (int i = 0; i < kPer; ++i)
         if (tid * kPer + i < words) {
           place[tid * kPer + i] = (uint16_t)sum;
+          if (sum <= kMarked && sum + __popc(bitmap[tid * kPer + i]) > kMarked) fit = tid * kPer + i;  // the first word without places
           sum += __popc(bitmap[tid * kPer + i]);
         }
-      for (uint32_t i = tid; i < marked; i += kThreads) seen[i] = 0, bias[i] = 0.f;
       __syncthreads();
-      auto place_of = [&](int64_t i) { return place[i >> 5] + __popc(bitmap[i >> 5] & ((1u << (i & 31)) - 1u)); };
-      for (int j = tid; j < n_hist; j += kThreads) {
-        const int64_t i = hist[j] - first;
-        if (hist[j] < 0 || hist[j] >= a.vocab || i < 0 || i >= ids) continue;
-        atomicOr(&seen[place_of(i)], 0x80000000u);
-        if (j >= n_prompt) atomicAdd(&seen[place_of(i)], 1u);
+      if (marked > kMarked) {  // the range ends before that word
+        marked = place[fit];
+        v1 = v0 + fit * 4;
+        ids = fit * 32;
+      }
+      auto place_of = [&](int id) {
+        const int i = id - first;
+        return place[i >> 5] + __popc(bitmap[i >> 5] & ((1u << (i & 31)) - 1u));
+      };
+      for (int j0 = 0; j0 < n_hist; j0 += kHistory) {  // integer sums: the same in any order
+        if (!at_once) read_history(j0, n_hist);
+#pragma unroll
+        for (int i0 = 0; i0 < kBatch; i0 += 4) {  // lookups before updates, so that they do not wait for one another
+          if (j0 + i0 * kThreads >= n_hist) break;
+          int at[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            at[i] = j0 + (i0 + i) * kThreads + tid < n_hist && inside(recent[i0 + i]) ? place_of(recent[i0 + i]) : -1;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (at[i] >= 0) {
+              where[at[i]] = (uint16_t)(recent[i0 + i] - first);
+              if (j0 + (i0 + i) * kThreads + tid >= n_prompt) atomicAdd(&seen[at[i]], 1u);
+              else atomicOr(&seen[at[i]], 0x80000000u);
+            }
+        }
       }
       if (warp == 0)  // biases of one id in the order of their entries: the entry's rank among the equal ones takes turns
         for (int j0 = 0; j0 < n_bias; j0 += 32) {
-          const int id = j0 + lane < n_bias ? bias_ids[j0 + lane] : -1;
-          const int64_t i = id - first;
-          const bool mine_too = id >= 0 && id < a.vocab && i >= 0 && i < ids;
-          const float v = mine_too ? a.bias_values[b * a.bias_stride + j0 + lane] : 0.f;
-          const uint32_t same = __match_any_sync(0xffffffffu, id);
-          const int rank = mine_too ? __popc(same & ((1u << lane) - 1u)) : -1;
+          if (j0 > 0) {
+            bias_id = j0 + lane < n_bias ? bias_ids[j0 + lane] : -1;
+            bias_value = j0 + lane < n_bias ? a.bias_values[b * a.bias_stride + j0 + lane] : 0.f;
+          }
+          const uint32_t same = __match_any_sync(0xffffffffu, bias_id);
+          const int rank = inside(bias_id) ? __popc(same & ((1u << lane) - 1u)) : -1;
+          if (rank >= 0) where[place_of(bias_id)] = (uint16_t)(bias_id - first);
           for (int r = 0; __any_sync(0xffffffffu, rank >= r); ++r) {
-            if (rank == r) bias[place_of(i)] += v;
+            if (rank == r) bias[place_of(bias_id)] += bias_value;
             __syncwarp();
           }
         }
+      if (warp == 0 && n_bias > 32 && v1 < u1) bias_id = bias_ids[lane], bias_value = a.bias_values[b * a.bias_stride + lane];
       __syncthreads();
+      // The marked ids themselves, one a thread.  The pass over the logits leaves them
+      // out of the maximum and the sum, and their values are written over its own.
+      for (uint32_t k = tid; k < marked; k += kThreads) {
+        const int id = first + where[k];
+        const uint32_t c = seen[k];
+        float z;
+        load1(z_in + id, &z);
+        if (c) z = z > 0.f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
+        if (c & 0x7fffffffu) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, (float)(c & 0x7fffffffu))), pres);
+        z = __fadd_rn(z, bias[k]);
+        if (allowed && !((allowed[id >> 5] >> (id & 31)) & 1u)) z = -INFINITY;
+        bias[k] = z;
+        const float top = fmaxf(z, -INFINITY);  // NaN is never the maximum
+        best = join(best, Best{top, top > -INFINITY ? 1.f : isnan(z) ? z : 0.f, top > -INFINITY ? id : kNoToken});
+      }
+      __syncthreads();  // (in place: before anything is written)
     }
 
-    constexpr int kUnroll = 2;
     for (int w0 = v0 + tid; w0 < v1; w0 += kUnroll * kThreads) {
-      float x[kUnroll][8];
-      uint32_t open[kUnroll];
-#pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const int w = w0 + k * kThreads;
-        const int64_t id0 = (int64_t)w * 8 - shift;
-        open[k] = 0xffu;
-        if (w >= v1) continue;
-        if (id0 >= 0 && id0 + 8 <= a.vocab) {
-          load8(z_in + id0, x[k]);
-          if (allowed) {
-            open[k] = allowed[id0 >> 5] >> (id0 & 31);
-            if ((id0 & 31) > 24) open[k] |= allowed[(id0 >> 5) + 1] << (32 - (id0 & 31));
-          }
-        } else {
-          open[k] = 0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int64_t id = id0 + i;
-            const bool there = id >= 0 && id < a.vocab;
-            x[k][i] = -INFINITY;
-            if (there) load1(z_in + id, &x[k][i]);
-            if (there && (!allowed || (allowed[id >> 5] >> (id & 31)) & 1u)) open[k] |= 1u << i;
-          }
-        }
-      }
+      if (w0 > v0 + tid) load(w0, v1);
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
         const int w = w0 + k * kThreads;
         if (w >= v1) continue;
         const int64_t id0 = (int64_t)w * 8 - shift;
-        if (marks) {
-          const int i0 = (w - v0) * 8;
-          const uint32_t word = bitmap[i0 >> 5];
-          if ((word >> (i0 & 31)) & 0xffu) {
-            uint32_t at = place[i0 >> 5] + __popc(word & ((1u << (i0 & 31)) - 1u));
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if ((word >> ((i0 & 31) + i)) & 1u) {
-                const uint32_t c = seen[at];
-                float z = x[k][i];
-                if (c) z = z > 0.f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
-                if (c & 0x7fffffffu) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, (float)(c & 0x7fffffffu))), pres);
-                x[k][i] = __fadd_rn(z, bias[at]);
-                ++at;
-              }
-          }
-        }
+        const int i0 = (w - v0) * 8;
+        const uint32_t done = marks ? (bitmap[i0 >> 5] >> (i0 & 31)) & 0xffu : 0u;  // not this pass's
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (!((open[k] >> i) & 1u)) x[k][i] = -INFINITY;
+          if (!((open[k] & ~done) >> i & 1u)) x[k][i] = -INFINITY;
           top = fmaxf(top, x[k][i]);
         }
         if (z_out) {
           if (wide_out && id0 >= 0 && id0 + 8 <= a.vocab) {
-            __stcs(reinterpret_cast<float4*>(z_out + id0), make_float4(x[k][0], x[k][1], x[k][2], x[k][3]));
-            __stcs(reinterpret_cast<float4*>(z_out + id0) + 1, make_float4(x[k][4], x[k][5], x[k][6], x[k][7]));
+            store8(z_out + id0, x[k]);
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               if (id0 + i >= 0 && id0 + i < a.vocab) z_out[id0 + i] = x[k][i];
           }
         }
-        if (top > best.m) {  // ids only rise here: the first of equal maxima stays
+        if (top >= best.m && top > -INFINITY) {
           best.sum *= rescale(best.m, top);
-          best.m = top;
+          int id = kNoToken;  // the first of equal maxima
 #pragma unroll
           for (int i = 7; i >= 0; --i)
-            if (x[k][i] == top) best.id = (int)id0 + i;
+            if (x[k][i] == top) id = (int)id0 + i;
+          best.id = top == best.m ? min(best.id, id) : id;
+          best.m = top;
         }
         const float off = isinf(best.m) ? 0.f : best.m;  // of an infinite maximum: sums of infinities, as log-sum-exp has them
 #pragma unroll
-        for (int i = 0; i < 8; ++i) best.sum += exp2f((x[k][i] - off) * kLog2e);
+        for (int i = 0; i < 8; ++i) best.sum += exp_fast(x[k][i] - off);
       }
+    }
+    if (marks && z_out) {
+      __syncthreads();
+      for (uint32_t k = tid; k < marked; k += kThreads) z_out[first + where[k]] = bias[k];
     }
     if (v1 < u1) __syncthreads();
   }
@@ -246,6 +324,7 @@ __global__ void __launch_bounds__(kThreads) next_token_kernel(const __grid_const
 #pragma unroll
   for (int w = 16; w > 0; w >>= 1)
     best = join(best, Best{__shfl_xor_sync(0xffffffffu, best.m, w), __shfl_xor_sync(0xffffffffu, best.sum, w), __shfl_xor_sync(0xffffffffu, best.id, w)});
+  if (bad) set_status(a.status, GPT_STATUS_BAD_TOKEN);
   if (lane == 0) warp_best[warp] = best;
   __syncthreads();
   cluster.barrier_wait(std::move(started));
@@ -273,6 +352,8 @@ extern "C" int gpt_next_token(const gpt_next_token_args* a, void* cuda_stream) {
     return call_error(GPT_ERR_INVALID_ARG, "dtype must be GPT_DTYPE_FP32 or GPT_DTYPE_BF16");
   if (a->rows < 0 || a->vocab < 1 || a->max_history < 0 || a->n_bias < 0)
     return call_error(GPT_ERR_INVALID_ARG, "sizes must not be negative, vocab must be positive");
+  if (a->max_history > (1 << 30) || a->n_bias > (1 << 30) || a->vocab > (1 << 30))
+    return call_error(GPT_ERR_UNSUPPORTED, "max_history, n_bias and vocab must not exceed 2^30");
   if (a->rows == 0) return GPT_OK;
   if (!a->out && !a->token && !a->lse) return call_error(GPT_ERR_INVALID_ARG, "out, token and lse are all NULL");
   if (!a->logits) return call_error(GPT_ERR_INVALID_ARG, "logits must be non-NULL");
@@ -291,7 +372,7 @@ extern "C" int gpt_next_token(const gpt_next_token_args* a, void* cuda_stream) {
     return call_error(GPT_ERR_INVALID_ARG, "in place needs fp32 logits and equal strides");
   // Blocks of a row: as many as fill the GPU a few times over, with 1,024 ids each at least.
   int blocks = 8;
-  while (blocks > 1 && ((int64_t)a->rows * blocks > 1216 || a->vocab / blocks < 1024)) blocks /= 2;
+  while (blocks > 1 && ((int64_t)a->rows * blocks > 2432 || a->vocab / blocks < 1024)) blocks /= 2;
   if ((int64_t)a->rows * blocks > INT32_MAX) return call_error(GPT_ERR_UNSUPPORTED, "too many rows");
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;

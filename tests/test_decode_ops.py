@@ -584,11 +584,11 @@ def _next(z, hist=None, hl=None, pl=None, rep=None, pres=None, freq=None, ids=No
             if hist is not None:
                 n, first = (len(hist[b]) if hl is None else hl[b]), (0 if pl is None else pl[b])
                 h = [t for t in hist[b][:n] if 0 <= t < vocab]
-                made = [t for t in hist[b][first:n] if 0 <= t < vocab]
+                made = np.bincount([t for t in hist[b][first:n] if 0 <= t < vocab], minlength=vocab)
                 for t in sorted(set(h)):
                     if rep is not None:
                         z[b, t] = z[b, t] / f(rep[b]) if z[b, t] > 0 else z[b, t] * f(rep[b])
-                    c = made.count(t)
+                    c = made[t]
                     if c:
                         z[b, t] = f(z[b, t] - f(f(freq[b] if freq is not None else 0) * f(c))) - f(pres[b] if pres is not None else 0)
             if ids is not None:
@@ -649,6 +649,20 @@ def _run_next(x, kind, **kw):
 def test_next_token(cuda, kind, rows, vocab, most):
     x = _token_inputs(_rng(kind, rows, vocab), rows, vocab, most, kind)
     _check_next(_run_next(x, kind), _next(**x))
+
+
+@gpu
+@pytest.mark.parametrize("rows,vocab,most,n_bias", [(2, 50304, 30000, 40), (1, 131072, 9000, 5000), (3, 4096, 4096, 3000),
+                                                    (1, 65, 5000, 65)])
+def test_next_token_many_marked_ids(cuda, rows, vocab, most, n_bias):
+    """Long histories and bias lists spread evenly over the vocabulary: more marked ids than a block's table has places."""
+    rng = _rng(rows, vocab, most)
+    x = _token_inputs(rng, rows, vocab, most, "fp32")
+    x["hist"] = rng.integers(0, vocab, (rows, most)).astype(np.int32)
+    x["hl"] = np.array([most - i for i in range(rows)])
+    x["ids"] = rng.integers(0, vocab, (rows, n_bias))
+    x["vals"] = rng.standard_normal((rows, n_bias)).astype(np.float32)
+    _check_next(_run_next(x, "fp32"), _next(**x))
 
 
 @gpu
