@@ -13,6 +13,7 @@
 // took 150 us: nearly every warp has a marked id among its 256.)
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <cmath>
 #include <utility>
 
@@ -69,7 +70,7 @@ __device__ __forceinline__ void load1(const __nv_bfloat16* z, float* x) { *x = _
 // Units of eight ids: unit u holds ids 8 u - shift .., the shift chosen so that
 // units of the logits lie on boundaries of their size whatever the row's address is.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) next_token_kernel(const __grid_constant__ gpt_next_token_args a) {
+__global__ void __launch_bounds__(kThreads, 5) next_token_kernel(const __grid_constant__ gpt_next_token_args a) {
   __shared__ uint32_t bitmap[kRange / 32];
   __shared__ uint16_t place[kRange / 32];   // marked ids before a word's
   __shared__ uint16_t where[kMarked];       // the marked id of a place, from the range's first on
@@ -96,37 +97,32 @@ __global__ void __launch_bounds__(kThreads, 4) next_token_kernel(const __grid_co
   int n_hist = hist && a.history_lens ? a.history_lens[b] : most;
   const int n_prompt = hist && a.prompt_lens ? a.prompt_lens[b] : 0;
 
-  // Units w, w + kThreads of the logits, and the mask's bits of their ids.
-  constexpr int kUnroll = 2;
-  float x[kUnroll][8];
-  uint32_t open[kUnroll];
-  auto load = [&](int w0, int v1) {
+  // Unit w of the logits, and the mask's bits of its ids.
+  float x[8];
+  uint32_t open;
+  auto load = [&](int w) {
+    const int64_t id0 = (int64_t)w * 8 - shift;
+    open = 0xffu;
+    if (w >= u1) return;
+    if (id0 >= 0 && id0 + 8 <= a.vocab) {
+      load8(z_in + id0, x);
+      if (allowed) {
+        open = allowed[id0 >> 5] >> (id0 & 31);
+        if ((id0 & 31) > 24) open |= allowed[(id0 >> 5) + 1] << (32 - (id0 & 31));
+      }
+    } else {
+      open = 0;
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const int w = w0 + k * kThreads;
-      const int64_t id0 = (int64_t)w * 8 - shift;
-      open[k] = 0xffu;
-      if (w >= v1) continue;
-      if (id0 >= 0 && id0 + 8 <= a.vocab) {
-        load8(z_in + id0, x[k]);
-        if (allowed) {
-          open[k] = allowed[id0 >> 5] >> (id0 & 31);
-          if ((id0 & 31) > 24) open[k] |= allowed[(id0 >> 5) + 1] << (32 - (id0 & 31));
-        }
-      } else {
-        open[k] = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int64_t id = id0 + i;
-          const bool there = id >= 0 && id < a.vocab;
-          x[k][i] = -INFINITY;
-          if (there) load1(z_in + id, &x[k][i]);
-          if (there && (!allowed || (allowed[id >> 5] >> (id & 31)) & 1u)) open[k] |= 1u << i;
-        }
+      for (int i = 0; i < 8; ++i) {
+        const int64_t id = id0 + i;
+        const bool there = id >= 0 && id < a.vocab;
+        x[i] = -INFINITY;
+        if (there) load1(z_in + id, &x[i]);
+        if (there && (!allowed || (allowed[id >> 5] >> (id & 31)) & 1u)) open |= 1u << i;
       }
     }
   };
-  load(u0 + tid, u1);  // the first of every thread's, under way while the ids are marked
+  load(u0 + tid);  // every thread's first, under way while the ids are marked
 
   // The history, kBatch ids of a thread at a time.  One that fits is read once, before
   // its length is known.
@@ -160,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 4) next_token_kernel(const __grid_co
     const int first = (int)((int64_t)v0 * 8 - shift);  // the id of bit 0
     uint32_t ids = (v1 - v0) * 8, marked = 0;
     auto inside = [&](int id) { return (uint32_t)id < (uint32_t)a.vocab && (uint32_t)(id - first) < ids; };
-    if (v0 > u0) load(v0 + tid, v1);
+    if (v0 > u0) load(v0 + tid);
     if (marks) {
       for (int i = tid; i < words; i += kThreads) bitmap[i] = 0;
       const int places = (int)min((uint64_t)kMarked, (uint64_t)n_hist + n_bias);
@@ -276,43 +272,38 @@ __global__ void __launch_bounds__(kThreads, 4) next_token_kernel(const __grid_co
       __syncthreads();  // (in place: before anything is written)
     }
 
-    for (int w0 = v0 + tid; w0 < v1; w0 += kUnroll * kThreads) {
-      if (w0 > v0 + tid) load(w0, v1);
+    for (int w = v0 + tid; w < v1; w += kThreads) {
+      if (w > v0 + tid) load(w);
+      const int64_t id0 = (int64_t)w * 8 - shift;
+      const int i0 = (w - v0) * 8;
+      if (marks) open &= ~(bitmap[i0 >> 5] >> (i0 & 31));
+      float top = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const int w = w0 + k * kThreads;
-        if (w >= v1) continue;
-        const int64_t id0 = (int64_t)w * 8 - shift;
-        const int i0 = (w - v0) * 8;
-        const uint32_t done = marks ? (bitmap[i0 >> 5] >> (i0 & 31)) & 0xffu : 0u;  // not this pass's
-        float top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (!((open[k] & ~done) >> i & 1u)) x[k][i] = -INFINITY;
-          top = fmaxf(top, x[k][i]);
-        }
-        if (z_out) {
-          if (wide_out && id0 >= 0 && id0 + 8 <= a.vocab) {
-            store8(z_out + id0, x[k]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (id0 + i >= 0 && id0 + i < a.vocab) z_out[id0 + i] = x[k][i];
-          }
-        }
-        if (top >= best.m && top > -INFINITY) {
-          best.sum *= rescale(best.m, top);
-          int id = kNoToken;  // the first of equal maxima
-#pragma unroll
-          for (int i = 7; i >= 0; --i)
-            if (x[k][i] == top) id = (int)id0 + i;
-          best.id = top == best.m ? min(best.id, id) : id;
-          best.m = top;
-        }
-        const float off = isinf(best.m) ? 0.f : best.m;  // of an infinite maximum: sums of infinities, as log-sum-exp has them
-#pragma unroll
-        for (int i = 0; i < 8; ++i) best.sum += exp_fast(x[k][i] - off);
+      for (int i = 0; i < 8; ++i) {
+        if (!((open >> i) & 1u)) x[i] = -INFINITY;
+        top = fmaxf(top, x[i]);
       }
+      if (z_out) {
+        if (wide_out && id0 >= 0 && id0 + 8 <= a.vocab) {
+          store8(z_out + id0, x);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (id0 + i >= 0 && id0 + i < a.vocab) z_out[id0 + i] = x[i];
+        }
+      }
+      if (top >= best.m && top > -INFINITY) {
+        best.sum *= rescale(best.m, top);
+        int id = kNoToken;  // the first of equal maxima
+#pragma unroll
+        for (int i = 7; i >= 0; --i)
+          if (x[i] == top) id = (int)id0 + i;
+        best.id = top == best.m ? min(best.id, id) : id;
+        best.m = top;
+      }
+      const float off = isinf(best.m) ? 0.f : best.m;  // of an infinite maximum: sums of infinities, as log-sum-exp has them
+#pragma unroll
+      for (int i = 0; i < 8; ++i) best.sum += exp_fast(x[i] - off);
     }
     if (marks && z_out) {
       __syncthreads();
@@ -370,9 +361,11 @@ extern "C" int gpt_next_token(const gpt_next_token_args* a, void* cuda_stream) {
     return call_error(GPT_ERR_INVALID_ARG, "bias_ids and bias_values go together");
   if ((const void*)a->out == a->logits && (a->dtype != GPT_DTYPE_FP32 || (a->rows > 1 && a->out_stride != a->logits_stride)))
     return call_error(GPT_ERR_INVALID_ARG, "in place needs fp32 logits and equal strides");
-  // Blocks of a row: as many as fill the GPU a few times over, with 1,024 ids each at least.
-  int blocks = 8;
-  while (blocks > 1 && ((int64_t)a->rows * blocks > 2432 || a->vocab / blocks < 1024)) blocks /= 2;
+  // Blocks of a row: as many as all run at once (four an SM; clusters leave the fifth
+  // place empty here and there), for a second wave repeats the marking of ids: 200 rows
+  // of 50,304 took 23 us in clusters of 2, 29 of 4, 35 of 8; 64 rows of 131,072 42, 25
+  // and 19 us; one row 13, 10 and 9.  A block has 512 ids at least.
+  const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>({8, 608 / a->rows, a->vocab / 512}));
   if ((int64_t)a->rows * blocks > INT32_MAX) return call_error(GPT_ERR_UNSUPPORTED, "too many rows");
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
