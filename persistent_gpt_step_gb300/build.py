@@ -21,7 +21,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgpt.so")
 MODULE = os.path.join(HERE, "_decode.so")
 SOURCES = ["gpt_host.cu", "kernel_fp32.cu", "kernel_bf16.cu", "kernel_bf16_ext.cu",
-           "kv_append.cu", "decode_attention.cu", "next_token.cu"]
+           "kv_append.cu", "decode_attention.cu", "decode_bf16_64.cu", "decode_bf16_128.cu", "decode_fp32_64.cu",
+           "decode_fp32_128.cu", "next_token.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
          "-I" + os.path.join(ROOT, "include")]

@@ -1,831 +1,12 @@
-// decode_attention.cu — gpt_decode_attention: attention of one new token of
-// every sequence over its pages of keys and values.
-//
-// Mathematics: with z_j = scale q.k_j, any set of keys reduces to (m, l, o) =
-// (reference m, sum 2^(z_j - m), sum 2^(z_j - m) v_j), and sets join by bringing
-// them to a common m; the output is o / l, the lse m + log l.  Scores are kept in
-// base 2 (scale log2 e folded in).
-//
-// Bound: every key and value is read once, 4 FLOP per element and query head, so
-// HBM bandwidth is the limit at any usual number of query heads per key head.
-// The kernel therefore keeps loads in flight and does as little as possible
-// between them:
-//  - Work is cut by keys, not by rows: the 16-key tiles of all (sequence, key
-//    head) rows are one line, of which every warp of a one-wave grid takes an equal
-//    part, whatever the lengths are (the host does not know them).  Rows inside one
-//    warp's part are finished from its registers; a row cut by part boundaries
-//    leaves (m, l, o) pieces in shared memory, which the block joins once at its
-//    end, and one cut by block boundaries pieces in the workspace, which a second
-//    kernel joins.
-//  - Each warp reads its keys and values from global memory straight into the
-//    operand registers of its products; no barrier until the warp's part is done.
-//    The values of a step are requested before its keys are used and the next
-//    step's keys before its values are used.
-//  - bf16: 16 keys at a time through mma.m16n8k16, keys (or the 16 value dims) as
-//    the 16-row operand and up to 8 query heads as its 8 columns.  An operand's
-//    16-byte pieces serve as they are: the order of the contraction index is free
-//    for the scores (the query is laid out to match) and the order of the output
-//    dims for the values.  The probabilities enter as two bf16 parts (p = hi + lo,
-//    2^-17 of p left over), so that their rounding does not show beside the
-//    output's own.
-//  - fp32: fused multiply-adds, four lanes to a key for the scores, a lane to
-//    four dims for the values.
+// decode_attention.cu — gpt_decode_attention: argument checks, the choice of a
+// kernel and its grid, the workspace.
 #include <algorithm>
 #include <cmath>
 
-#include "decode_ops.h"
+#include "decode_attention.h"
 
 namespace pgs {
 namespace {
-
-constexpr int kWarps = 8;      // of a block
-constexpr int kTile = 16;      // keys of a unit of work
-// What the start of a row costs a warp, in tiles (the first loads' latencies and the
-// row's end): without it warps with many short rows end last.  200 sequences of 1 to
-// 1,024 keys, 16 heads of 64: 91 us with 0, 85 with 2, 82 with 4, 85 with 8; 256 of 1
-// to 256 keys: 44, 36, 35, 34.
-constexpr int kStart = 4;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-struct Meta { int32_t seq, row, last, pad; };  // a row begun in this block and ended in block `last`
-
-struct DecodeParams {
-  gpt_paged_cache c;
-  gpt_decode_attention_args a;
-  int32_t group;     // query heads per key head
-  int32_t chunk;     // query heads of a row
-  int32_t chunks;    // rows of one key head
-  int32_t team;      // warps that take the same keys, a key head each
-  int32_t rows;      // rows (of `team` key heads) of one sequence
-  float scale2;      // scale log2 e
-  Meta* meta;        // [blocks]
-  float *piece_ml, *piece_o;  // [blocks][2][team chunk][2], [...][head_dim]
-};
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// 2^(x - m) for x <= m; nothing from x = -infinity, whatever m is.
-__device__ __forceinline__ float weight(float x, float m) { return x == -INFINITY ? 0.f : exp2_fast(x - m); }
-
-__device__ __forceinline__ uint4 load16(const void* p) {
-  uint4 u;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
-  return u;
-}
-__device__ __forceinline__ uint4 load16_if(const void* p, bool ok) {
-  uint4 u = make_uint4(0u, 0u, 0u, 0u);
-  if (ok) asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
-  return u;
-}
-
-// Length of a sequence, cut to what its table can name.
-__device__ __forceinline__ int seq_len(const DecodeParams& p, int s, bool report) {
-  const int len = p.a.lens[s], most = p.c.max_pages * p.c.page_size;
-  if (len >= 0 && len <= most) return len;
-  if (report) set_status(p.a.status, GPT_STATUS_BAD_POS);
-  return len < 0 ? 0 : most;
-}
-
-// Where a warp's keys are.  kWhole (pages of whole 16-key groups): lane i holds the
-// offset (elements) of group i of the next 32, one division and one table entry a
-// group; rows of a group are slot_stride apart.  Otherwise a lane holds the offset
-// of its own key of the step, one of each a key.  Table entries are read one round
-// ahead.  An offset of -1: no such key, or a bad page.
-template <bool kWhole, int kKeys>
-struct Walk {
-  const DecodeParams& p;
-  const int32_t* table;
-  int64_t head, off;
-  int next, end, page, at;
-
-  __device__ __forceinline__ Walk(const DecodeParams& p_, int s, int h, int k0, int k1)
-      : p(p_), table(p_.c.page_table + s * p_.c.table_stride), head((int64_t)h * p_.c.head_stride), end(k1), at(0) {
-    const int lane = threadIdx.x & 31;
-    next = k0 + (kWhole ? lane * 16 : lane & (kKeys - 1));
-    page = fetch();
-  }
-  __device__ __forceinline__ int fetch() const {
-    if (next >= end) return -1;
-    const int id = table[next / p.c.page_size];
-    if (id >= 0 && id < p.c.n_pages) return id;
-    set_status(p.a.status, GPT_STATUS_BAD_PAGE);
-    return -1;
-  }
-  __device__ __forceinline__ void turn() {
-    off = page < 0 ? -1 : page * p.c.page_stride + (next % p.c.page_size) * p.c.slot_stride + head;
-    next += kWhole ? 512 : kKeys;
-    page = fetch();
-  }
-  // kWhole: offset of key `at` (a multiple of 8) of the 512 in hand; then `by` keys on.
-  __device__ __forceinline__ int64_t step(int by) {
-    int64_t x = __shfl_sync(0xffffffffu, off, at >> 4);
-    if (x >= 0) x += (at & 15) * p.c.slot_stride;
-    at += by;
-    if (at == 512) turn(), at = 0;
-    return x;
-  }
-};
-
-// A piece of a row in shared memory: (m, l) of each head, then their o rows from left_o on.
-__host__ __device__ constexpr int left_o(int heads) { return (2 * heads + 3) / 4 * 4; }
-__host__ __device__ constexpr int left_floats(int heads, int dp) { return left_o(heads) + heads * dp; }
-
-__device__ __forceinline__ void store_lse(const DecodeParams& p, int s, int hq, float m, float total) {
-  if (p.a.lse) p.a.lse[(int64_t)s * p.a.n_head + hq] = total == 0.f ? -INFINITY : m * kLn2 + logf(total);
-}
-
-// A warp's part of a row: keys [k0, k1) of sequence s for key head h, query heads
-// hq .. hq + n; left: where its piece goes, or null to finish the row.
-struct Part {
-  int s, h, hq, n, k0, k1;
-  float* left;
-};
-
-// ---- bf16 ---------------------------------------------------------------------
-
-__device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// kMode: query heads of a row.  4: up to 4, columns 4..7 of the scores repeat them, so
-// that one product takes hi from columns 0..3 and lo from 4..7; 8, 16: up to that
-// many, hi and lo in products of their own.
-template <int kMode, int DP_, bool kFast>
-struct Bf16Path {
-  using T = __nv_bfloat16;
-  static constexpr int NT = kMode == 16 ? 2 : 1, DP = DP_, kHeads = kMode;
-  static constexpr int kBlocks = kMode == 16 ? 1 : 2;  // of an SM
-  static constexpr bool kTwice = kMode == 4;
-  static constexpr int KG = 128 / DP;           // 16-key groups of a step: 32 registers of keys, 32 of values
-  static constexpr int kQuery = NT * (DP / 32) * 128;  // a warp's queries: a 16-byte piece per lane, tile and 32 dims
-
-  // Lane (r, c): query head r of a tile, dims 32 i + 8 c .. + 7.
-  static __device__ __forceinline__ void stage_query(const DecodeParams& p, float* mine, const Part& w) {
-    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < DP / 32; ++i) {
-        const int qh = kTwice ? r & 3 : t * 8 + r;
-        reinterpret_cast<uint4*>(mine)[(t * (DP / 32) + i) * 32 + lane] =
-            load16_if((const T*)p.a.q + w.s * p.a.q_row + (w.hq + qh) * p.a.q_head + i * 32 + c * 8,
-                      qh < w.n && i * 32 + c * 8 < p.c.head_dim);
-      }
-  }
-
-  static __device__ __forceinline__ void run(const DecodeParams& p, float* mine, const Part& w) {
-    const int k0 = w.k0, k1 = w.k1;
-    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const int d = p.c.head_dim;
-    const int64_t row = p.c.slot_stride;
-    const T* kb = (const T*)p.c.k + c * 8 + (kFast ? r * row : 0);
-    const T* vb = (const T*)p.c.v + r * 8 + (kFast ? 2 * c * row : 0);
-    const uint4* query = reinterpret_cast<const uint4*>(mine) + lane;
-    float o[NT][DP / 64][4][4], m[NT][2], l[NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      m[t][0] = m[t][1] = -INFINITY, l[t][0] = l[t][1] = 0.f;
-#pragma unroll
-      for (int b = 0; b < DP / 64; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[t][b][i / 4][i % 4] = 0.f;
-    }
-    uint4 kr[KG][2][DP / 32], vr[KG][4][DP / 64];
-    Walk<kFast, 16 * KG> walk(p, w.s, w.h, k0, k1);
-    int64_t off[KG];  // of the step's groups (kFast); of the lane's key
-    auto advance = [&] {
-      if constexpr (kFast) {
-#pragma unroll
-        for (int g = 0; g < KG; ++g) off[g] = walk.step(16);
-      } else {
-        off[0] = walk.off;
-        walk.turn();
-      }
-    };
-    auto load_keys = [&] {
-#pragma unroll
-      for (int g = 0; g < KG; ++g) {
-        if constexpr (kFast) {
-          const T* at = kb + max(off[g], (int64_t)0);
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < DP / 32; ++i) kr[g][u][i] = load16(at + u * 8 * row + i * 32);
-        } else {
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int64_t at = __shfl_sync(0xffffffffu, off[0], g * 16 + u * 8 + r);
-#pragma unroll
-            for (int i = 0; i < DP / 32; ++i) kr[g][u][i] = load16_if(kb + at + i * 32, at >= 0 && i * 32 + c * 8 < d);
-          }
-        }
-      }
-    };
-    stage_query(p, mine, w);
-    walk.turn();
-    advance();
-    load_keys();
-    for (int k = k0; k < k1; k += 16 * KG) {
-      // the step's values
-      uint32_t there = 0xffffffffu;  // keys that count
-#pragma unroll
-      for (int g = 0; g < KG; ++g) {
-        if constexpr (kFast) {
-          const T* at = vb + max(off[g], (int64_t)0);
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int b = 0; b < DP / 64; ++b) vr[g][u][b] = load16(at + ((u >> 1) * 8 + (u & 1)) * row + b * 64);
-          if (off[g] < 0) there &= ~(0xffffu << (g * 16));
-        } else {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int64_t at = __shfl_sync(0xffffffffu, off[0], g * 16 + (u >> 1) * 8 + 2 * c + (u & 1));
-#pragma unroll
-            for (int b = 0; b < DP / 64; ++b) vr[g][u][b] = load16_if(vb + at + b * 64, at >= 0 && b * 64 + r * 8 < d);
-          }
-        }
-      }
-      if constexpr (kFast) {
-        if (k1 - k < 16 * KG) there &= (1u << (k1 - k)) - 1u;
-      } else {
-        there = __ballot_sync(0xffffffffu, off[0] >= 0);
-      }
-      advance();
-      // scores: 16 keys x 8 heads a tile
-      float z[KG][NT][4];
-#pragma unroll
-      for (int g = 0; g < KG; ++g)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) z[g][t][i] = 0.f;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < DP / 32; ++i) {
-          const uint4 q = query[(t * (DP / 32) + i) * 32];
-#pragma unroll
-          for (int g = 0; g < KG; ++g) {
-            mma16816(z[g][t], kr[g][0][i].x, kr[g][1][i].x, kr[g][0][i].y, kr[g][1][i].y, q.x, q.y);
-            mma16816(z[g][t], kr[g][0][i].z, kr[g][1][i].z, kr[g][0][i].w, kr[g][1][i].w, q.z, q.w);
-          }
-        }
-      load_keys();
-#pragma unroll
-      for (int g = 0; g < KG; ++g)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) z[g][t][i] *= p.scale2;
-      if (__builtin_expect(there != 0xffffffffu >> (32 - 16 * KG) && there != 0xffffffffu, 0)) {
-#pragma unroll
-        for (int g = 0; g < KG; ++g) {
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (!((there >> (g * 16 + (i >> 1) * 8 + r)) & 1u)) z[g][t][i] = -INFINITY;
-          if constexpr (kFast)  // what such a slot holds may be NaN
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              if (!((there >> (g * 16 + (u >> 1) * 8 + 2 * c + (u & 1))) & 1u))
-#pragma unroll
-                for (int b = 0; b < DP / 64; ++b) vr[g][u][b] = make_uint4(0u, 0u, 0u, 0u);
-        }
-      }
-      // softmax: the reference of a head moves only when a score passes it by 2^8
-      bool move = false;
-#pragma unroll
-      for (int g = 0; g < KG; ++g)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          move |= fmaxf(z[g][t][0], z[g][t][2]) > m[t][0] + 8.f || fmaxf(z[g][t][1], z[g][t][3]) > m[t][1] + 8.f;
-      if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float top = m[t][e];
-#pragma unroll
-            for (int g = 0; g < KG; ++g) top = fmaxf(top, fmaxf(z[g][t][e], z[g][t][e + 2]));
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-            const float keep = weight(m[t][e], top);
-            m[t][e] = top;
-            l[t][e] *= keep;
-#pragma unroll
-            for (int b = 0; b < DP / 64; ++b)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[t][b][i][e] *= keep, o[t][b][i][e + 2] *= keep;
-          }
-      }
-#pragma unroll
-      for (int g = 0; g < KG; ++g)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const float m0 = m[t][0] == -INFINITY ? 0.f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
-          const float p0 = exp2_fast(z[g][t][0] - m0), p1 = exp2_fast(z[g][t][1] - m1);
-          const float p2 = exp2_fast(z[g][t][2] - m0), p3 = exp2_fast(z[g][t][3] - m1);
-          l[t][0] += p0 + p2, l[t][1] += p1 + p3;
-          uint32_t ha = pack2(p0, p1), hb = pack2(p2, p3);
-          const uint32_t la = pack2(p0 - __uint_as_float(ha << 16), p1 - __uint_as_float(ha & 0xffff0000u));
-          const uint32_t lb = pack2(p2 - __uint_as_float(hb << 16), p3 - __uint_as_float(hb & 0xffff0000u));
-          if (kTwice) ha = c < 2 ? ha : la, hb = c < 2 ? hb : lb;
-          const uint32_t h0 = transpose8(ha), h1 = transpose8(hb);
-          uint32_t l0, l1;
-          if (!kTwice) l0 = transpose8(la), l1 = transpose8(lb);
-#pragma unroll
-          for (int b = 0; b < DP / 64; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t va = (&vr[g][0][b].x)[i], vc = (&vr[g][1][b].x)[i], ve = (&vr[g][2][b].x)[i], vg = (&vr[g][3][b].x)[i];
-              const uint32_t a0 = __byte_perm(va, vc, 0x5410), a1 = __byte_perm(va, vc, 0x7632);
-              const uint32_t a2 = __byte_perm(ve, vg, 0x5410), a3 = __byte_perm(ve, vg, 0x7632);
-              mma16816(o[t][b][i], a0, a1, a2, a3, h0, h1);
-              if (!kTwice) mma16816(o[t][b][i], a0, a1, a2, a3, l0, l1);
-            }
-        }
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int qh = t * 8 + 2 * c + e;
-        float total = l[t][e];
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
-        if (kTwice)
-#pragma unroll
-          for (int b = 0; b < DP / 64; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              o[t][b][i][e] += __shfl_xor_sync(0xffffffffu, o[t][b][i][e], 2);
-              o[t][b][i][e + 2] += __shfl_xor_sync(0xffffffffu, o[t][b][i][e + 2], 2);
-            }
-        if (qh >= w.n) continue;
-        if (w.left) {
-          if (r == 0) w.left[2 * qh] = m[t][e], w.left[2 * qh + 1] = total;
-#pragma unroll
-          for (int b = 0; b < DP / 64; ++b) {
-            float4* to = reinterpret_cast<float4*>(w.left + left_o(kHeads) + qh * DP + b * 64 + r * 8);
-            to[0] = make_float4(o[t][b][0][e], o[t][b][0][e + 2], o[t][b][1][e], o[t][b][1][e + 2]);
-            to[1] = make_float4(o[t][b][2][e], o[t][b][2][e + 2], o[t][b][3][e], o[t][b][3][e + 2]);
-          }
-        } else {
-          const float inv = total == 0.f ? 0.f : 1.0f / total;
-          T* to = (T*)p.a.out + w.s * p.a.out_row + (w.hq + qh) * p.a.out_head + r * 8;
-#pragma unroll
-          for (int b = 0; b < DP / 64; ++b)
-            if (kFast || b * 64 + r * 8 < d)
-              *reinterpret_cast<uint4*>(to + b * 64) = make_uint4(pack2(o[t][b][0][e] * inv, o[t][b][0][e + 2] * inv), pack2(o[t][b][1][e] * inv, o[t][b][1][e + 2] * inv),
-                                                                  pack2(o[t][b][2][e] * inv, o[t][b][2][e + 2] * inv), pack2(o[t][b][3][e] * inv, o[t][b][3][e + 2] * inv));
-          if (r == 0) store_lse(p, w.s, w.hq + qh, m[t][e], total);
-        }
-      }
-  }
-};
-
-// ---- fp32 ---------------------------------------------------------------------
-
-template <int GH_, int DP_, bool kFast>
-struct Fp32Path {
-  using T = float;
-  static constexpr int DP = DP_, kHeads = GH_, kBlocks = 2;
-  static constexpr int KG = 128 / DP;            // 8-key groups of a step: 32 registers of keys, 32 of values
-  static constexpr int kKeys = 8 * KG;
-  static constexpr int kLanes = DP / 4;          // lanes to a row of values
-  static constexpr int kRows = 32 / kLanes;      // rows of values a load covers
-  static constexpr int kQuery = kHeads * DP + kKeys * kHeads;  // a warp's queries and probabilities
-
-  static __device__ __forceinline__ void stage_query(const DecodeParams& p, float* mine, const Part& w) {
-    __syncwarp();
-    for (int i = threadIdx.x & 31; i < kHeads * DP; i += 32) {
-      const int qh = i / DP, e = i % DP;
-      mine[i] = qh < w.n && e < p.c.head_dim ? ((const float*)p.a.q)[w.s * p.a.q_row + (w.hq + qh) * p.a.q_head + e] : 0.f;
-    }
-    __syncwarp();
-  }
-
-  static __device__ __forceinline__ void run(const DecodeParams& p, float* mine, const Part& w) {
-    const int k0 = w.k0, k1 = w.k1;
-    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const int d = p.c.head_dim;
-    const int64_t row = p.c.slot_stride;
-    const int vd = (lane % kLanes) * 4, vrow = lane / kLanes;
-    const float* kb = (const float*)p.c.k + c * 4 + (kFast ? r * row : 0);
-    const float* vb = (const float*)p.c.v + vd + (kFast ? vrow * row : 0);
-    const float* sq = mine;
-    float* sp = mine + kHeads * DP;  // [key][head]
-    float m[kHeads], l[kHeads];
-    float4 o[kHeads];
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) m[i] = -INFINITY, l[i] = 0.f, o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    uint4 kr[KG][DP / 16], vr[kKeys / kRows];
-    Walk<kFast, kKeys> walk(p, w.s, w.h, k0, k1);
-    int64_t off;  // of the step's first key (kFast); of the lane's key
-    auto advance = [&] {
-      if constexpr (kFast) {
-        off = walk.step(kKeys);
-      } else {
-        off = walk.off;
-        walk.turn();
-      }
-    };
-    auto load_keys = [&] {
-#pragma unroll
-      for (int g = 0; g < KG; ++g) {
-        if constexpr (kFast) {
-          const float* at = kb + max(off, (int64_t)0) + g * 8 * row;
-#pragma unroll
-          for (int i = 0; i < DP / 16; ++i) kr[g][i] = load16(at + i * 16);
-        } else {
-          const int64_t at = __shfl_sync(0xffffffffu, off, g * 8 + r);
-#pragma unroll
-          for (int i = 0; i < DP / 16; ++i) kr[g][i] = load16_if(kb + at + i * 16, at >= 0 && i * 16 + c * 4 < d);
-        }
-      }
-    };
-    stage_query(p, mine, w);
-    walk.turn();
-    advance();
-    load_keys();
-    for (int k = k0; k < k1; k += kKeys) {
-      uint32_t there;
-      if constexpr (kFast) {
-        const float* at = vb + max(off, (int64_t)0);
-#pragma unroll
-        for (int i = 0; i < kKeys / kRows; ++i) vr[i] = load16(at + i * kRows * row);
-        there = off < 0 ? 0u : k1 - k < kKeys ? (1u << (k1 - k)) - 1u : (1u << kKeys) - 1u;
-        if (there != (1u << kKeys) - 1u)  // what a slot past the end holds may be NaN
-#pragma unroll
-          for (int i = 0; i < kKeys / kRows; ++i)
-            if (!((there >> (i * kRows + vrow)) & 1u)) vr[i] = make_uint4(0u, 0u, 0u, 0u);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kKeys / kRows; ++i) {
-          const int64_t at = __shfl_sync(0xffffffffu, off, i * kRows + vrow);
-          vr[i] = load16_if(vb + at, at >= 0 && vd < d);
-        }
-        there = __ballot_sync(0xffffffffu, off >= 0);
-      }
-      advance();
-      float z[KG][kHeads];
-#pragma unroll
-      for (int i = 0; i < kHeads; ++i) {
-#pragma unroll
-        for (int g = 0; g < KG; ++g) z[g][i] = 0.f;
-#pragma unroll
-        for (int b = 0; b < DP / 16; ++b) {
-          const float4 x = *reinterpret_cast<const float4*>(sq + i * DP + b * 16 + c * 4);
-#pragma unroll
-          for (int g = 0; g < KG; ++g) {
-            const uint4 u = kr[g][b];
-            z[g][i] = fmaf(x.x, __uint_as_float(u.x), z[g][i]);
-            z[g][i] = fmaf(x.y, __uint_as_float(u.y), z[g][i]);
-            z[g][i] = fmaf(x.z, __uint_as_float(u.z), z[g][i]);
-            z[g][i] = fmaf(x.w, __uint_as_float(u.w), z[g][i]);
-          }
-        }
-      }
-      load_keys();
-      bool move = false;
-#pragma unroll
-      for (int g = 0; g < KG; ++g) {
-        const bool ok = (there >> (g * 8 + r)) & 1u;
-#pragma unroll
-        for (int i = 0; i < kHeads; ++i) {
-          z[g][i] += __shfl_xor_sync(0xffffffffu, z[g][i], 1);
-          z[g][i] += __shfl_xor_sync(0xffffffffu, z[g][i], 2);
-          z[g][i] = ok ? z[g][i] * p.scale2 : -INFINITY;
-          move |= z[g][i] > m[i] + 8.f;
-        }
-      }
-      if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-        for (int i = 0; i < kHeads; ++i) {
-          float top = m[i];
-#pragma unroll
-          for (int g = 0; g < KG; ++g) top = fmaxf(top, z[g][i]);
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-          const float keep = weight(m[i], top);
-          m[i] = top;
-          l[i] *= keep;
-          o[i].x *= keep, o[i].y *= keep, o[i].z *= keep, o[i].w *= keep;
-        }
-      }
-      __syncwarp();  // the last step's probabilities have been read
-#pragma unroll
-      for (int g = 0; g < KG; ++g)
-#pragma unroll
-        for (int i = 0; i < kHeads; ++i) {
-          const float e = exp2_fast(z[g][i] - (m[i] == -INFINITY ? 0.f : m[i]));
-          l[i] += e;
-          if ((i & 3) == c) sp[(g * 8 + r) * kHeads + i] = e;
-        }
-      __syncwarp();
-#pragma unroll
-      for (int j = 0; j < kKeys / kRows; ++j) {
-        const float* e = sp + (j * kRows + vrow) * kHeads;
-#pragma unroll
-        for (int i = 0; i < kHeads; ++i) {
-          o[i].x = fmaf(e[i], __uint_as_float(vr[j].x), o[i].x);
-          o[i].y = fmaf(e[i], __uint_as_float(vr[j].y), o[i].y);
-          o[i].z = fmaf(e[i], __uint_as_float(vr[j].z), o[i].z);
-          o[i].w = fmaf(e[i], __uint_as_float(vr[j].w), o[i].w);
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-#pragma unroll
-      for (int x = 4; x < 32; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
-#pragma unroll
-      for (int x = kLanes; x < 32; x <<= 1) {
-        o[i].x += __shfl_xor_sync(0xffffffffu, o[i].x, x);
-        o[i].y += __shfl_xor_sync(0xffffffffu, o[i].y, x);
-        o[i].z += __shfl_xor_sync(0xffffffffu, o[i].z, x);
-        o[i].w += __shfl_xor_sync(0xffffffffu, o[i].w, x);
-      }
-      if (i >= w.n) continue;
-      if (w.left) {
-        if (lane == 0) w.left[2 * i] = m[i], w.left[2 * i + 1] = l[i];
-        if (vrow == 0) *reinterpret_cast<float4*>(w.left + left_o(kHeads) + i * DP + vd) = o[i];
-      } else {
-        const float inv = l[i] == 0.f ? 0.f : 1.0f / l[i];
-        if (vrow == 0 && vd < d)
-          *reinterpret_cast<float4*>((float*)p.a.out + w.s * p.a.out_row + (w.hq + i) * p.a.out_head + vd) =
-              make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv);
-        if (lane == 0) store_lse(p, w.s, w.hq + i, m[i], l[i]);
-      }
-    }
-  }
-};
-
-// ---- the kernels --------------------------------------------------------------
-
-__device__ __forceinline__ void store4(float* to, const float* x) { *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]); }
-__device__ __forceinline__ void store4(__nv_bfloat16* to, const float* x) {
-  *reinterpret_cast<uint2*>(to) = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
-}
-
-template <class P>
-__global__ void __launch_bounds__(kWarps * 32, P::kBlocks) decode_kernel(const __grid_constant__ DecodeParams p) {
-  using T = typename P::T;
-  constexpr int kLeft = left_floats(P::kHeads, P::DP);
-  extern __shared__ __align__(16) float sm[];  // [kWarps][2] pieces, [kWarps] queries
-  __shared__ struct { int s, row, valid, ends, tiles; } info[kWarps][2];  // a team's pieces: that continues a row, that begins one
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n_seq = p.c.n_seq, d = p.c.head_dim;
-  const int blk = blockIdx.x, blocks = gridDim.x;
-  const int teams = kWarps / p.team, team = warp / p.team, hl = warp % p.team;
-  if (tid < 2 * kWarps) info[tid >> 1][tid & 1].valid = 0;
-  if (tid == 0) p.meta[blk].seq = -1;
-
-  // The line of work: for every row its start (as long as kStart tiles), then its
-  // tiles.  Every warp looks at the sequences for itself, 256 at a time, 8 a lane.
-  constexpr int kLook = 8;
-  int keys[kLook];          // of the lane's sequences
-  int64_t before, total;    // units before them among those looked at, and of all of these
-  auto look_at = [&](int s0) {
-    int64_t sum = 0;
-#pragma unroll
-    for (int i = 0; i < kLook; ++i) {
-      const int s = s0 + lane * kLook + i;
-      keys[i] = s < n_seq ? seq_len(p, s, tid == lane && blk == 0) : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < kLook; ++i) sum += keys[i] > 0 ? (keys[i] + kTile - 1) / kTile + kStart : 0;
-    sum *= p.rows;
-    before = sum;
-#pragma unroll
-    for (int x = 1; x < 32; x <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, before, x);
-      if (lane >= x) before += y;
-    }
-    total = __shfl_sync(0xffffffffu, before, 31);
-    before -= sum;
-  };
-  int64_t units = 0;
-  for (int s0 = 0; s0 < n_seq; s0 += 32 * kLook) look_at(s0), units += total;
-  const int64_t active = min((int64_t)blocks * teams, units), gt = (int64_t)blk * teams + team;
-  auto cut = [&](int64_t i) {  // where part i of the line begins
-    return (uint64_t)(i * units) >> 32 ? i * units / active : (int64_t)((uint32_t)(i * units) / (uint32_t)active);
-  };
-  const int64_t begin = gt < active ? cut(gt) : 0, end = gt < active ? cut(gt + 1) : 0;
-
-  auto empty_rows = [&] {  // sequences of no keys
-    for (int s = blk; s < n_seq; s += blocks)
-      if (seq_len(p, s, false) == 0) {
-        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int i = tid; i < p.a.n_head * (d / 4); i += kWarps * 32)
-          store4((T*)p.a.out + s * p.a.out_row + i / (d / 4) * p.a.out_head + i % (d / 4) * 4, zero);
-        for (int h = tid; h < p.a.n_head; h += kWarps * 32) store_lse(p, s, h, 0.f, 0.f);
-      }
-  };
-  if ((int64_t)blk * teams >= active) return empty_rows();
-
-  // the sequence that the team begins in, its keys and the units of it before that
-  int s = 0, len = 0;
-  int64_t into = 0, base = 0;
-  for (int s0 = 0; s0 < n_seq; s0 += 32 * kLook) {
-    if (n_seq > 32 * kLook) look_at(s0);
-    if (begin >= base && begin < base + total) {
-      const int owner = 31 - __clz(__ballot_sync(0xffffffffu, base + before <= begin));  // the last lane at or before `begin`
-      int64_t at = begin - base - before;
-#pragma unroll
-      for (int i = 0; i < kLook; ++i) {
-        const int64_t here = keys[i] > 0 ? (int64_t)((keys[i] + kTile - 1) / kTile + kStart) * p.rows : 0;
-        if (at >= 0 && at < here) s = s0 + lane * kLook + i, len = keys[i], into = at;
-        at -= here;
-      }
-      s = __shfl_sync(0xffffffffu, s, owner), len = __shfl_sync(0xffffffffu, len, owner);
-      into = __shfl_sync(0xffffffffu, into, owner);
-      break;
-    }
-    base += total;
-  }
-
-  float* mine = sm + kWarps * 2 * kLeft + warp * P::kQuery;
-  int64_t left = end - begin;
-  if (left > 0) {
-    int tiles = (len + kTile - 1) / kTile;
-    int row, at;  // units of the row before the team's
-    if (into >> 32) row = (int)(into / (tiles + kStart)), at = (int)(into % (tiles + kStart));
-    else row = (uint32_t)into / (uint32_t)(tiles + kStart), at = (uint32_t)into % (uint32_t)(tiles + kStart);
-    while (true) {
-      const int stop = (int)min((int64_t)(tiles + kStart), at + left);
-      const int t0 = max(at - kStart, 0), t1 = max(stop - kStart, 0);
-      const bool whole = t0 == 0 && t1 == tiles;
-      Part w;
-      w.s = s, w.h = row / p.chunks * p.team + hl;
-      w.hq = w.h * p.group + row % p.chunks * p.chunk, w.n = min(p.chunk, (w.h + 1) * p.group - w.hq);
-      w.k0 = t0 * kTile, w.k1 = min(len, t1 * kTile);
-      w.left = whole ? nullptr : sm + (warp * 2 + (t0 == 0)) * kLeft;
-      if (t1 > t0) P::run(p, mine, w);
-      if (t1 > t0 && !whole && hl == 0 && lane == 0) {
-        auto& f = info[team][t0 == 0];
-        f.s = s, f.row = row, f.valid = 1, f.ends = t1 == tiles, f.tiles = tiles - t1;
-      }
-      left -= stop - at;
-      if (left == 0) break;
-      at = 0;
-      if (++row == p.rows) {
-        row = 0;
-        do len = seq_len(p, ++s, false); while (len == 0);
-        tiles = (len + kTile - 1) / kTile;
-      }
-    }
-  }
-  __syncthreads();
-
-  // Join the pieces of each row: one that begins a row or comes from the block
-  // before, then the next teams' continuations.  Piece 2 t + b: of team t.
-  uint32_t valid, ends;
-  {
-    const bool there = lane < 2 * teams && info[(lane & 15) >> 1][lane & 1].valid;
-    valid = __ballot_sync(0xffffffffu, there);
-    ends = __ballot_sync(0xffffffffu, there && info[(lane & 15) >> 1][lane & 1].ends);
-  }
-  while (valid) {
-    const int j = __ffs(valid) - 1;
-    int last = j;  // pieces j, then 2 (j / 2 + 1), ... last
-    while (!((ends >> last) & 1u) && (valid >> ((last | 1) + 1)) & 1u) last = (last | 1) + 1;
-    valid &= ~((2u << last) - 1u);
-    const int ps = info[j >> 1][j & 1].s, row = info[j >> 1][j & 1].row;
-    const bool begins = j & 1, done = begins && (ends >> last) & 1u;
-    const int first = row % p.chunks * p.chunk, n = min(p.chunk, p.group - first);
-    const int64_t slot = 2 * blk + begins;
-    for (int i = tid; i < p.team * p.chunk * (d / 4); i += kWarps * 32) {
-      const int e = i % (d / 4) * 4, qh = i / (d / 4) % p.chunk, g = i / (d / 4) / p.chunk;
-      if (qh >= n) continue;
-      float top = -INFINITY, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-      auto piece = [&](int k) { return sm + (((k >> 1) * p.team + g) * 2 + (k & 1)) * kLeft; };
-      for (int k = j; k <= last; k = (k | 1) + 1) top = fmaxf(top, piece(k)[2 * qh]);
-      for (int k = j; k <= last; k = (k | 1) + 1) {
-        const float* from = piece(k);
-        const float keep = weight(from[2 * qh], top);
-        sum += from[2 * qh + 1] * keep;
-        const float4 y = *reinterpret_cast<const float4*>(from + left_o(P::kHeads) + qh * P::DP + e);
-        x[0] += y.x * keep, x[1] += y.y * keep, x[2] += y.z * keep, x[3] += y.w * keep;
-      }
-      if (done) {
-        const int hq = (row / p.chunks * p.team + g) * p.group + first + qh;
-        const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] *= inv;
-        store4((T*)p.a.out + ps * p.a.out_row + hq * p.a.out_head + e, x);
-        if (e == 0) store_lse(p, ps, hq, top, sum);
-      } else {
-        const int64_t at = (slot * p.team + g) * p.chunk + qh;
-        if (e == 0) p.piece_ml[2 * at] = top, p.piece_ml[2 * at + 1] = sum;
-        store4(p.piece_o + at * d + e, x);
-      }
-    }
-    if (begins && !done && tid == 0) {  // the row goes on in later blocks: which team ends it?
-      const int64_t stop = cut((int64_t)blk * teams + (j >> 1) + 1) + info[j >> 1][1].tiles;
-      int64_t to = (int64_t)((float)stop * (float)active / (float)units);  // then exactly: begins before stop, the next does not
-      while ((to + 1) * units < stop * active) ++to;
-      while (to * units >= stop * active) --to;
-      p.meta[blk] = Meta{ps, row, (int)to / teams, 0};
-    }
-  }
-  empty_rows();
-}
-
-// A row that several blocks worked on: the pieces of its blocks, joined.  Block
-// (b, y): the row begun in block b, its query heads from 8 y on; the warps share
-// the heads and, where these are fewer, the pieces.
-template <typename T>
-__global__ void __launch_bounds__(256) decode_join_kernel(const __grid_constant__ DecodeParams p) {
-  __shared__ float sm_ml[8][2], sm_o[8][128];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int blk = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = p.c.head_dim;
-  const Meta mt = p.meta[blk];
-  if (mt.seq < 0) return;
-  const int first = mt.row % p.chunks * p.chunk, n = min(p.chunk, p.group - first), pieces = mt.last - blk + 1;
-  const int heads = min(8, p.team * n - 8 * (int)blockIdx.y);
-  if (heads <= 0) return;
-  const int share = pieces > 2 ? 8 / heads : 1;  // warps of a head
-  const int i = 8 * blockIdx.y + warp / share, sub = warp % share, g = i / n, qh = i % n;
-  const bool mine = warp / share < heads;
-  float top = -INFINITY, total = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-  if (mine) {
-    const int e = min(lane * 4, d - 4);
-    auto at = [&](int j) { return ((int64_t)(j == 0 ? 2 * blk + 1 : 2 * (blk + j)) * p.team + g) * p.chunk + qh; };
-    for (int j0 = sub; j0 < pieces; j0 += 32 * share) {  // a piece per lane at a time
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (j0 + lane * share < pieces) ml = *reinterpret_cast<const float2*>(p.piece_ml + 2 * at(j0 + lane * share));
-      float best = fmaxf(top, ml.x);
-#pragma unroll
-      for (int w = 16; w > 0; w >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, w));
-      const float keep = weight(top, best), factor = weight(ml.x, best);
-      float sum = ml.y * factor;
-#pragma unroll
-      for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-      total = total * keep + sum;
-      top = best;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] *= keep;
-      const int count = min(32, (pieces - j0 + share - 1) / share);
-      for (int j = 0; j < count; j += 8) {
-        float4 y[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) y[u] = *reinterpret_cast<const float4*>(p.piece_o + at(j0 + min(j + u, count - 1) * share) * d + e);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const float f = __shfl_sync(0xffffffffu, factor, (j + u) & 31);
-          if (j + u < count) x[0] += y[u].x * f, x[1] += y[u].y * f, x[2] += y[u].z * f, x[3] += y[u].w * f;
-        }
-      }
-    }
-  }
-  if (share > 1) {  // the first warp of a head adds the others'
-    if (lane == 0) sm_ml[warp][0] = top, sm_ml[warp][1] = total;
-    store4(&sm_o[warp][lane * 4], x);
-    __syncthreads();
-    if (!mine || sub) return;
-    float best = top;
-    for (int w = 1; w < share; ++w) best = fmaxf(best, sm_ml[warp + w][0]);
-    const float keep = weight(top, best);
-    total *= keep;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] *= keep;
-    for (int w = 1; w < share; ++w) {
-      const float f = weight(sm_ml[warp + w][0], best);
-      total += sm_ml[warp + w][1] * f;
-      const float4 y = *reinterpret_cast<const float4*>(&sm_o[warp + w][lane * 4]);
-      x[0] += y.x * f, x[1] += y.y * f, x[2] += y.z * f, x[3] += y.w * f;
-    }
-    top = best;
-  } else if (!mine) {
-    return;
-  }
-  const int hq = (mt.row / p.chunks * p.team + g) * p.group + first + qh;
-  const float inv = total == 0.f ? 0.f : 1.0f / total;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) x[k] *= inv;
-  if (lane * 4 < d) store4((T*)p.a.out + mt.seq * p.a.out_row + hq * p.a.out_head + lane * 4, x);
-  if (lane == 0) store_lse(p, mt.seq, hq, top, total);
-}
-
-// ---- host ---------------------------------------------------------------------
 
 int check_args(const gpt_paged_cache* c, int32_t n_head) {
   if (const int rc = check_cache(c)) return rc;
@@ -843,8 +24,6 @@ int sm_count() {
   return sms;
 }
 
-struct Plan { int blocks, chunk, chunks, team; size_t ml_at, o_at, bytes; };
-
 // Blocks of the grid, query heads of a row, and the workspace.
 Plan make_plan(const gpt_paged_cache* c, int32_t n_head) {
   Plan pl;
@@ -861,34 +40,28 @@ Plan make_plan(const gpt_paged_cache* c, int32_t n_head) {
   const int64_t used = std::min<int64_t>(pl.blocks, (rows * (tiles + kStart) + kWarps - 1) / kWarps);
   pl.team = 1;
   while (pl.team < 4 && c->n_kv_head % (2 * pl.team) == 0 && used * 2 * pl.team <= 16 * rows) pl.team *= 2;
+  // Rows that all get a block or a cluster at once, of at most 8 tiles a warp, take
+  // decode_row_kernel: one sequence of 513 keys, 12 heads of 64 in fp32 6.3 us (the
+  // line and its join 10.2), 4,096 keys of 8 heads of 128 11.3 (16.8), 32 sequences up
+  // to 500 keys of 12 heads of 64 14.5 (17.2); with 16 tiles a warp it loses, 16,000
+  // keys of 8 heads 33.7 (25.0).
+  pl.cluster = 0;
+  if (rows <= 2 * pl.blocks) {
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(8, pl.blocks / rows));
+    if (tiles <= 8 * most * kWarps) pl.cluster = (int)std::min<int64_t>(most, (tiles + kWarps - 1) / kWarps);
+  }
+  if (pl.cluster) {
+    pl.team = pl.join_heads = 1, pl.bytes = 0;
+    return pl;
+  }
+  // Pieces of a row, about: the more, the fewer heads for a block of the second kernel.
+  const int64_t pieces = used * pl.team / rows;
+  pl.join_heads = pieces > 32 ? 1 : pieces > 16 ? 2 : pieces > 8 ? 4 : 8;
   const size_t records = (size_t)pl.blocks * 2 * pl.team * pl.chunk;
   pl.ml_at = (pl.blocks * sizeof(Meta) + 15) / 16 * 16;
   pl.o_at = (pl.ml_at + records * 8 + 15) / 16 * 16;
   pl.bytes = pl.o_at + records * c->head_dim * 4;
   return pl;
-}
-
-template <class P>
-int launch(const DecodeParams& p, const Plan& pl, cudaStream_t st) {
-  const size_t smem = (size_t)kWarps * (2 * left_floats(P::kHeads, P::DP) + P::kQuery) * sizeof(float);
-  static thread_local int ready = -1;  // device whose limit has been raised
-  int dev = -1;
-  cudaGetDevice(&dev);
-  if (ready != dev) {
-    if (cudaFuncSetAttribute(decode_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-      return check_launch("gpt_decode_attention");
-    ready = dev;
-  }
-  decode_kernel<P><<<pl.blocks, kWarps * 32, smem, st>>>(p);
-  if (const int rc = check_launch("gpt_decode_attention")) return rc;
-  // the second kernel may start while the first one ends; it waits for its results itself
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(pl.blocks, (pl.team * pl.chunk + 7) / 8), cfg.blockDim = dim3(256), cfg.stream = st, cfg.attrs = &attr, cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, decode_join_kernel<typename P::T>, p);
-  return check_launch("gpt_decode_attention (join)");
 }
 
 }  // namespace
@@ -914,26 +87,20 @@ extern "C" int gpt_decode_attention(const gpt_paged_cache* c, const gpt_decode_a
     return call_error(GPT_ERR_INVALID_ARG, "q and out addresses and strides must be multiples of 16 bytes");
   if (!std::isfinite(a->scale)) return call_error(GPT_ERR_INVALID_ARG, "scale must be finite");
   const Plan pl = make_plan(c, a->n_head);
-  if (!a->workspace || a->workspace_bytes < pl.bytes || !aligned16(a->workspace))
+  if (pl.bytes && (!a->workspace || a->workspace_bytes < pl.bytes || !aligned16(a->workspace)))
     return call_error(GPT_ERR_INVALID_ARG, "workspace: %zu bytes on a 16-byte boundary", pl.bytes);
   DecodeParams p;
   p.c = *c;
   p.a = *a;
   p.group = a->n_head / c->n_kv_head;
-  p.chunk = pl.chunk, p.chunks = pl.chunks, p.team = pl.team;
+  p.chunk = pl.chunk, p.chunks = pl.chunks, p.team = pl.team, p.join_heads = pl.join_heads;
   p.rows = c->n_kv_head / pl.team * pl.chunks;
   p.scale2 = a->scale * kLog2e;
   p.meta = (Meta*)a->workspace;
   p.piece_ml = (float*)((char*)a->workspace + pl.ml_at);
   p.piece_o = (float*)((char*)a->workspace + pl.o_at);
   const cudaStream_t st = (cudaStream_t)cuda_stream;
-  // the fast form: pages of whole 16-key groups, heads of exactly 64 or 128
-  const bool wide = c->head_dim > 64, fast = c->page_size % 16 == 0 && c->head_dim % 64 == 0;
-#define PGS_LAUNCH(PATH, N)                                                                               \
-  (wide ? fast ? launch<PATH<N, 128, true>>(p, pl, st) : launch<PATH<N, 128, false>>(p, pl, st)           \
-        : fast ? launch<PATH<N, 64, true>>(p, pl, st) : launch<PATH<N, 64, false>>(p, pl, st))
-  if (c->dtype == GPT_DTYPE_BF16)
-    return pl.chunk <= 4 ? PGS_LAUNCH(Bf16Path, 4) : pl.chunk <= 8 ? PGS_LAUNCH(Bf16Path, 8) : PGS_LAUNCH(Bf16Path, 16);
-  return pl.chunk == 1 ? PGS_LAUNCH(Fp32Path, 1) : pl.chunk <= 4 ? PGS_LAUNCH(Fp32Path, 4) : PGS_LAUNCH(Fp32Path, 8);
-#undef PGS_LAUNCH
+  const bool wide = c->head_dim > 64;
+  if (c->dtype == GPT_DTYPE_BF16) return wide ? decode_bf16_128(p, pl, st) : decode_bf16_64(p, pl, st);
+  return wide ? decode_fp32_128(p, pl, st) : decode_fp32_64(p, pl, st);
 }

@@ -110,6 +110,12 @@ def test_append_refusals(lib, change, word):
     (dict(scale=math.nan), "scale"), (dict(scale=math.inf), "scale"), (dict(workspace=None), "workspace"),
     (dict(workspace=FAKE + 8), "workspace"), (dict(workspace_bytes=64), "workspace")])
 def test_attention_refusals(lib, change, word):
+    if word == "workspace":  # a table that reaches far enough for one to be needed
+        c = _cache(max_pages=10000, table_stride=10000)
+        assert lib.gpt_decode_attention_workspace(ctypes.byref(c), 8) > 64
+        assert lib.gpt_decode_attention(ctypes.byref(c), ctypes.byref(_attend(**change)), None) == -1
+        assert word in lib.gpt_last_error(None).decode()
+        return
     assert lib.gpt_decode_attention(ctypes.byref(_cache()), ctypes.byref(_attend(**change)), None) == -1
     assert word in lib.gpt_last_error(None).decode()
     assert lib.gpt_decode_attention(None, ctypes.byref(_attend()), None) == -1
@@ -405,8 +411,9 @@ def _attention(q, keys, values, scale):
     return out, (m + np.log(l))[:, 0], spread * (2 * dw + (n + 8) * U)[:, None], dz + (n + 8) * U + 4 * U * np.abs(m[:, 0])
 
 
-def _run_attention(rng, lens, heads, kv, dim, page, kind, order="slot", scale=None, fill=math.nan, strided=False):
-    table, n_pages = _pages(rng, lens, page)
+def _run_attention(rng, lens, heads, kv, dim, page, kind, order="slot", scale=None, fill=math.nan, strided=False, reach=0):
+    """``reach``: positions that the table has room for, if more than the lengths need; the kernel is chosen by it."""
+    table, n_pages = _pages(rng, lens, page, width=-(-reach // page))
     kc, vc = _pool(n_pages, page, kv, dim, kind, order, fill)
     parts = _fill(rng, lens, table, kc, vc, page)
     q = _t(rng.standard_normal((len(lens), heads, dim)), kind)
@@ -442,11 +449,12 @@ ATTENDS = [  # lengths, heads, kv heads, dim, page, order
 
 
 @gpu
+@pytest.mark.parametrize("reach", [0, 400000])
 @pytest.mark.parametrize("kind", ["fp32", "bf16"])
 @pytest.mark.parametrize("lens,heads,kv,dim,page,order", ATTENDS)
-def test_attention(cuda, kind, lens, heads, kv, dim, page, order):
+def test_attention(cuda, kind, lens, heads, kv, dim, page, order, reach):
     """Everything that no sequence's length covers is NaN, and table entries past it name no page."""
-    _run_attention(_rng(kind, dim, len(lens), heads), lens, heads, kv, dim, page, kind, order)
+    _run_attention(_rng(kind, dim, len(lens), heads), lens, heads, kv, dim, page, kind, order, reach=reach)
 
 
 @gpu
@@ -454,26 +462,41 @@ def test_attention(cuda, kind, lens, heads, kv, dim, page, order):
 def test_attention_strided_and_scaled(cuda, kind):
     _run_attention(_rng(kind), [70, 0, 9], 6, 2, 64, 16, kind, "gaps", scale=0.3, strided=True)
     _run_attention(_rng(kind), [70, 3], 6, 2, 64, 16, kind, scale=0.0)
-    _run_attention(_rng(kind), [70, 3], 6, 2, 64, 16, kind, scale=-0.7, fill=math.inf)
+    for reach in (0, 400000):
+        _run_attention(_rng(kind), [70, 3], 6, 2, 64, 16, kind, scale=-0.7, fill=math.inf, reach=reach)
 
 
 @gpu
+@pytest.mark.parametrize("reach", [0, 400000])
 @pytest.mark.parametrize("kind", ["fp32", "bf16"])
-def test_attention_every_length_near_a_split(cuda, kind):
+@pytest.mark.parametrize("page", [16, 8, 5])
+def test_attention_every_length_near_a_split(cuda, kind, page, reach):
     """Lengths around every power of two and tile: one launch, a sequence each."""
     lens = sorted({max(0, (1 << e) + d) for e in range(0, 12) for d in (-1, 0, 1)})
-    _run_attention(_rng(kind, 3), lens, 4, 2, 64, 16, kind)
+    _run_attention(_rng(kind, 3), lens, 4, 2, 64, page, kind, reach=reach)
 
 
 @gpu
 @pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("n_seq,kv", [(700, 1), (300, 4), (2000, 2)])
+def test_attention_many_sequences(cuda, kind, n_seq, kv):
+    """More sequences than are looked at at a time, most of them short or empty, a few long."""
+    rng = _rng(kind, n_seq)
+    lens = np.where(rng.random(n_seq) < 0.3, 0, (rng.random(n_seq) ** 6 * 900).astype(np.int64) + 1)
+    lens[[0, n_seq // 2, n_seq - 1]] = [0, 1500, 7]
+    _run_attention(rng, lens.tolist(), 2 * kv, kv, 32, 16, kind)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("reach", [10000, 400000])
 @pytest.mark.parametrize("where", [0, 1, 127, 128, 4095, 5000, 9999])
-def test_attention_finds_one_key(cuda, kind, where):
+def test_attention_finds_one_key(cuda, kind, where, reach):
     """One key of 10,000 carries nearly all of the weight, wherever it stands; far smaller and far larger
     scores before and after it (the running maximum jumps by more than exp's range)."""
     rng = _rng(where)
     n, page, dim = 10000, 16, 64
-    table, n_pages = _pages(rng, [n], page)
+    table, n_pages = _pages(rng, [n], page, width=reach // page)
     kc, vc = _pool(n_pages, page, 2, dim, kind, "slot", math.nan)
     k = rng.standard_normal((n, 2, dim)) * 0.01
     k[: where // 2, :, 0] -= 300.0
@@ -491,9 +514,10 @@ def test_attention_finds_one_key(cuda, kind, where):
 
 
 @gpu
-def test_attention_infinite_scores_are_absent_keys(cuda):
+@pytest.mark.parametrize("reach", [0, 400000])
+def test_attention_infinite_scores_are_absent_keys(cuda, reach):
     rng = _rng(9)
-    table, n_pages = _pages(rng, [40, 3], 16)
+    table, n_pages = _pages(rng, [40, 3], 16, width=reach // 16)
     kc, vc = _pool(n_pages, 16, 1, 64, "fp32", "slot", math.nan)
     parts = _fill(rng, [40, 3], table, kc, vc, 16)
     q = _t(np.abs(rng.standard_normal((2, 1, 64))) + 0.1)
