@@ -31,6 +31,10 @@ Plan make_plan(const gpt_paged_cache* c, int32_t n_head) {
   pl.chunk = group <= 8 ? group : c->dtype == GPT_DTYPE_BF16 ? (group < 16 ? group : 16) : 8;
   pl.chunks = (group + pl.chunk - 1) / pl.chunk;
   pl.blocks = sm_count() * (pl.chunk > 8 ? 1 : 2);
+  const int es = elem_size(c->dtype);
+  const double span = ((double)(c->n_pages - 1) * c->page_stride + (double)(c->page_size - 1) * c->slot_stride +
+                       (double)(c->n_kv_head - 1) * c->head_stride + c->head_dim) * es;
+  pl.fast = c->page_size % 8 == 0 && span < 16.0 * 0xffffffffu;
   // Teams: warps that read the same keys' neighbouring heads keep DRAM pages open
   // where a head's row is short (200 sequences of 16 heads of 64: 86 us with teams of
   // 1, 81 with 4, 82 with 8); but a row of a team is cut into that many more pieces
@@ -95,6 +99,10 @@ extern "C" int gpt_decode_attention(const gpt_paged_cache* c, const gpt_decode_a
   p.group = a->n_head / c->n_kv_head;
   p.chunk = pl.chunk, p.chunks = pl.chunks, p.team = pl.team, p.join_heads = pl.join_heads;
   p.rows = c->n_kv_head / pl.team * pl.chunks;
+  if (pl.fast) {
+    p.page16 = (uint32_t)(c->page_stride * es / 16), p.slot16 = (uint32_t)(c->slot_stride * es / 16);
+    p.head16 = (uint32_t)(c->head_stride * es / 16);
+  }
   p.scale2 = a->scale * kLog2e;
   p.meta = (Meta*)a->workspace;
   p.piece_ml = (float*)((char*)a->workspace + pl.ml_at);

@@ -33,6 +33,8 @@
 #pragma once
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "decode_attention.h"
 
 namespace pgs {
@@ -67,21 +69,24 @@ __device__ __forceinline__ int seq_len(const DecodeParams& p, int s, bool report
   return len < 0 ? 0 : most;
 }
 
-// Where a warp's keys are.  kFast (pages of whole 8-key groups): lane i holds the
-// offset (elements) of group i of the next 32, one division and one table entry a
-// group; rows of a group are slot_stride apart.  Otherwise a lane holds the offset
-// of its own key of the step, one of each a key.  Table entries are read one round
-// ahead.  An offset of -1: no such key, or a bad page.
+// Where a warp's keys are.  kFast (pages of whole 8-key groups, everything within
+// 64 GB): lane i holds the offset, in 16 bytes, of group i of the next 32, one division
+// and one table entry a group; rows of a group are slot_stride apart.  Otherwise a lane
+// holds the offset, in elements, of its own key of the step, one of each a key.  Table
+// entries are read one round ahead.  kNoKey: no such key, or a bad page.
 template <bool kFast, int kKeys>
 struct Walk {
+  using Off = std::conditional_t<kFast, uint32_t, int64_t>;
+  static constexpr Off kNoKey = (Off)-1;
   const DecodeParams& p;
   const int32_t* table;
-  int64_t head, off;
+  Off head, off;
   int next, end, page, at;
 
   __device__ __forceinline__ Walk(const DecodeParams& p_, int s, int h, int k0, int k1)
-      : p(p_), table(p_.c.page_table + s * p_.c.table_stride), head((int64_t)h * p_.c.head_stride), end(k1), at(0) {
+      : p(p_), table(p_.c.page_table + s * p_.c.table_stride), end(k1), at(0) {
     const int lane = threadIdx.x & 31;
+    head = kFast ? h * p.head16 : h * p.c.head_stride;
     next = k0 + (kFast ? lane * 8 : lane & (kKeys - 1));
     page = fetch();
   }
@@ -93,17 +98,24 @@ struct Walk {
     return -1;
   }
   __device__ __forceinline__ void turn() {
-    off = page < 0 ? -1 : page * p.c.page_stride + (next % p.c.page_size) * p.c.slot_stride + head;
+    if constexpr (kFast) off = page < 0 ? kNoKey : page * p.page16 + (next % p.c.page_size) * p.slot16 + head;
+    else off = page < 0 ? kNoKey : page * p.c.page_stride + (next % p.c.page_size) * p.c.slot_stride + head;
     next += kFast ? 256 : kKeys;
     page = fetch();
   }
   // kFast: offset of the next group of 8 keys.
-  __device__ __forceinline__ int64_t group() {
-    const int64_t x = __shfl_sync(0xffffffffu, off, at);
+  __device__ __forceinline__ Off group() {
+    const Off x = __shfl_sync(0xffffffffu, off, at);
     if (++at == 32) turn(), at = 0;
     return x;
   }
 };
+
+// A group's address (its first slot's); one that is not there reads the pool's first slots.
+template <typename T>
+__device__ __forceinline__ const T* group_at(const T* base, uint32_t off) {
+  return reinterpret_cast<const T*>(reinterpret_cast<const char*>(base) + (off == ~0u ? 0ull : (unsigned long long)off * 16));
+}
 
 // A piece of a row in shared memory: (m, l) of each head, then their o rows from left_o on.
 __host__ __device__ constexpr int left_o(int heads) { return (2 * heads + 3) / 4 * 4; }
@@ -146,6 +158,9 @@ struct Bf16Path {
   using T = __nv_bfloat16;
   static constexpr int NT = kMode == 16 ? 2 : 1, DP = DP_, kHeads = kMode;
   static constexpr int kBlocks = kMode == 16 ? 1 : 2;  // of an SM
+  // A unit of the line is a step (in tiles of 16 where a step is 32 keys: 38.2 instead
+  // of 36.6 us for 256 sequences of 1 to 256 keys).
+  static constexpr int kUnit = 16 * (128 / DP_), kUnitStart = DP_ == 64 ? 3 : kStart;
   static constexpr bool kTwice = kMode == 4;
   static constexpr int KG = 128 / DP;           // 16-key groups of a step: 32 registers of keys, 32 of values
   static constexpr int kQuery = NT * (DP / 32) * 128;  // a warp's queries: a 16-byte piece per lane, tile and 32 dims
@@ -183,7 +198,7 @@ struct Bf16Path {
     }
     uint4 kr[KG][2][DP / 32], vr[KG][4][DP / 64];
     Walk<kFast, 16 * KG> walk(p, w.s, w.h, k0, k1);
-    int64_t off[KG][2];  // of the step's groups of 8 (kFast); off[0][0]: of the lane's key
+    typename Walk<kFast, 16 * KG>::Off off[KG][2];  // of the step's groups of 8 (kFast); off[0][0]: of the lane's key
     auto advance = [&] {
       if constexpr (kFast) {
 #pragma unroll
@@ -199,7 +214,7 @@ struct Bf16Path {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
           if constexpr (kFast) {
-            const T* at = kb + max(off[g][u], (int64_t)0);
+            const T* at = group_at(kb, off[g][u]);
 #pragma unroll
             for (int i = 0; i < DP / 32; ++i) kr[g][u][i] = kExact ? load16(at + i * 32) : load16_if(at + i * 32, i * 32 + c * 8 < d);
           } else {
@@ -220,10 +235,10 @@ struct Bf16Path {
 #pragma unroll
         for (int u = 0; u < 4; ++u)
           if constexpr (kFast) {
-            const T* at = vb + max(off[g][u >> 1], (int64_t)0) + (u & 1) * row;
+            const T* at = group_at(vb, off[g][u >> 1]) + (u & 1) * row;
 #pragma unroll
             for (int b = 0; b < DP / 64; ++b) vr[g][u][b] = kExact ? load16(at + b * 64) : load16_if(at + b * 64, b * 64 + r * 8 < d);
-            if ((u & 1) && off[g][u >> 1] < 0) there &= ~(0xffu << (g * 16 + (u >> 1) * 8));
+            if ((u & 1) && off[g][u >> 1] == ~0u) there &= ~(0xffu << (g * 16 + (u >> 1) * 8));
           } else {
             const int64_t at = __shfl_sync(0xffffffffu, off[0][0], g * 16 + (u >> 1) * 8 + 2 * c + (u & 1));
 #pragma unroll
@@ -374,7 +389,7 @@ struct Bf16Path {
 template <int GH_, int DP_, bool kFast, bool kExact>
 struct Fp32Path {
   using T = float;
-  static constexpr int DP = DP_, kHeads = GH_, kBlocks = 2;
+  static constexpr int DP = DP_, kHeads = GH_, kBlocks = 2, kUnit = kTile, kUnitStart = kStart;
   static constexpr int KG = 128 / DP;            // 8-key groups of a step: 32 registers of keys, 32 of values
   static constexpr int kKeys = 8 * KG;
   static constexpr int kLanes = DP / 4;          // lanes to a row of values
@@ -406,7 +421,7 @@ struct Fp32Path {
     for (int i = 0; i < kHeads; ++i) m[i] = -INFINITY, l[i] = 0.f, o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     uint4 kr[KG][DP / 16], vr[kKeys / kRows];
     Walk<kFast, kKeys> walk(p, w.s, w.h, k0, k1);
-    int64_t off[KG];  // of the step's groups of 8 (kFast); off[0]: of the lane's key
+    typename Walk<kFast, kKeys>::Off off[KG];  // of the step's groups of 8 (kFast); off[0]: of the lane's key
     auto advance = [&] {
       if constexpr (kFast) {
 #pragma unroll
@@ -420,7 +435,7 @@ struct Fp32Path {
 #pragma unroll
       for (int g = 0; g < KG; ++g)
         if constexpr (kFast) {
-          const float* at = kb + max(off[g], (int64_t)0);
+          const float* at = group_at(kb, off[g]);
 #pragma unroll
           for (int i = 0; i < DP / 16; ++i) kr[g][i] = kExact ? load16(at + i * 16) : load16_if(at + i * 16, i * 16 + c * 4 < d);
         } else {
@@ -438,11 +453,11 @@ struct Fp32Path {
       if constexpr (kFast) {
 #pragma unroll
         for (int g = 0; g < KG; ++g) {
-          const float* at = vb + max(off[g], (int64_t)0);
+          const float* at = group_at(vb, off[g]);
 #pragma unroll
           for (int i = 0; i < 8 / kRows; ++i)
             vr[g * (8 / kRows) + i] = kExact ? load16(at + i * kRows * row) : load16_if(at + i * kRows * row, vd < d);
-          if (off[g] < 0) there &= ~(0xffu << (g * 8));
+          if (off[g] == ~0u) there &= ~(0xffu << (g * 8));
         }
         if (k1 - k < kKeys) there &= (1u << (k1 - k)) - 1u;
         if (there != (1u << kKeys) - 1u)  // what a slot that does not count holds may be NaN
@@ -571,7 +586,7 @@ __global__ void __launch_bounds__(kWarps * 32, P::kBlocks) decode_kernel(const _
   if (tid < 2 * kWarps) info[tid >> 1][tid & 1].valid = 0;
   if (tid == 0) p.meta[blk].seq = -1;
 
-  // The line of work: for every row its start (as long as kStart tiles), then its
+  // The line of work: for every row its start (as long as P::kUnitStart tiles), then its
   // tiles.  Every warp looks at the sequences for itself, 256 at a time, 8 a lane.
   constexpr int kLook = 8;
   int keys[kLook];          // of the lane's sequences
@@ -584,7 +599,7 @@ __global__ void __launch_bounds__(kWarps * 32, P::kBlocks) decode_kernel(const _
       keys[i] = s < n_seq ? seq_len(p, s, tid == lane && blk == 0) : 0;
     }
 #pragma unroll
-    for (int i = 0; i < kLook; ++i) sum += keys[i] > 0 ? (keys[i] + kTile - 1) / kTile + kStart : 0;
+    for (int i = 0; i < kLook; ++i) sum += keys[i] > 0 ? (keys[i] + P::kUnit - 1) / P::kUnit + P::kUnitStart : 0;
     sum *= p.rows;
     before = sum;
 #pragma unroll
@@ -624,7 +639,7 @@ __global__ void __launch_bounds__(kWarps * 32, P::kBlocks) decode_kernel(const _
       int64_t at = begin - base - before;
 #pragma unroll
       for (int i = 0; i < kLook; ++i) {
-        const int64_t here = keys[i] > 0 ? (int64_t)((keys[i] + kTile - 1) / kTile + kStart) * p.rows : 0;
+        const int64_t here = keys[i] > 0 ? (int64_t)((keys[i] + P::kUnit - 1) / P::kUnit + P::kUnitStart) * p.rows : 0;
         if (at >= 0 && at < here) s = s0 + lane * kLook + i, len = keys[i], into = at;
         at -= here;
       }
@@ -638,18 +653,18 @@ __global__ void __launch_bounds__(kWarps * 32, P::kBlocks) decode_kernel(const _
   float* mine = sm + kWarps * 2 * kLeft + warp * P::kQuery;
   int64_t left = end - begin;
   if (left > 0) {
-    int tiles = (len + kTile - 1) / kTile;
+    int tiles = (len + P::kUnit - 1) / P::kUnit;
     int row, at;  // units of the row before the team's
-    if (into >> 32) row = (int)(into / (tiles + kStart)), at = (int)(into % (tiles + kStart));
-    else row = (uint32_t)into / (uint32_t)(tiles + kStart), at = (uint32_t)into % (uint32_t)(tiles + kStart);
+    if (into >> 32) row = (int)(into / (tiles + P::kUnitStart)), at = (int)(into % (tiles + P::kUnitStart));
+    else row = (uint32_t)into / (uint32_t)(tiles + P::kUnitStart), at = (uint32_t)into % (uint32_t)(tiles + P::kUnitStart);
     while (true) {
-      const int stop = (int)min((int64_t)(tiles + kStart), at + left);
-      const int t0 = max(at - kStart, 0), t1 = max(stop - kStart, 0);
+      const int stop = (int)min((int64_t)(tiles + P::kUnitStart), at + left);
+      const int t0 = max(at - P::kUnitStart, 0), t1 = max(stop - P::kUnitStart, 0);
       const bool whole = t0 == 0 && t1 == tiles;
       Part w;
       w.s = s, w.h = row / p.chunks * p.team + hl;
       w.hq = w.h * p.group + row % p.chunks * p.chunk, w.n = min(p.chunk, (w.h + 1) * p.group - w.hq);
-      w.k0 = t0 * kTile, w.k1 = min(len, t1 * kTile);
+      w.k0 = t0 * P::kUnit, w.k1 = min(len, t1 * P::kUnit);
       w.left = whole ? nullptr : sm + (warp * 2 + (t0 == 0)) * kLeft;
       if (t1 > t0) P::run(p, mine, w);
       if (t1 > t0 && !whole && hl == 0 && lane == 0) {
@@ -662,7 +677,7 @@ __global__ void __launch_bounds__(kWarps * 32, P::kBlocks) decode_kernel(const _
       if (++row == p.rows) {
         row = 0;
         do len = seq_len(p, ++s, false); while (len == 0);
-        tiles = (len + kTile - 1) / kTile;
+        tiles = (len + P::kUnit - 1) / P::kUnit;
       }
     }
   }
@@ -898,10 +913,10 @@ int launch(const DecodeParams& p, const Plan& pl, cudaStream_t st) {
 }
 
 // The launch for a head size of at most DP: the fast forms need pages of whole 8-key
-// groups, the exact one heads of exactly DP.
+// groups within 64 GB, the exact one heads of exactly DP.
 template <template <int, int, bool, bool> class Path, int N, int DP>
 int launch_form(const DecodeParams& p, const Plan& pl, cudaStream_t st) {
-  if (p.c.page_size % 8) return launch<Path<N, DP, false, false>>(p, pl, st);
+  if (!pl.fast) return launch<Path<N, DP, false, false>>(p, pl, st);
   return p.c.head_dim == DP ? launch<Path<N, DP, true, true>>(p, pl, st) : launch<Path<N, DP, true, false>>(p, pl, st);
 }
 

@@ -25,6 +25,7 @@ struct DecodeParams {
   int32_t team;      // warps that take the same keys, a key head each
   int32_t rows;      // rows (of `team` key heads) of one sequence
   int32_t join_heads;  // query heads of a block of the second kernel, 1 to 8
+  uint32_t page16, slot16, head16;  // the cache's strides in 16 bytes (fast forms)
   float scale2;      // scale log2 e
   Meta* meta;        // [blocks]
   float *piece_ml, *piece_o;  // [blocks][2][team chunk][2], [...][head_dim]
@@ -36,6 +37,7 @@ struct Plan {
   int team;            // warps that take the same keys
   int cluster;         // blocks of a row (decode_row_kernel); 0: the line
   int join_heads;      // query heads of a block of the second kernel
+  bool fast;           // pages of whole 8-key groups, offsets in 16 bytes within 32 bits
   size_t ml_at, o_at, bytes;  // the workspace: pieces' (m, l), their o, its size
 };
 

@@ -559,13 +559,13 @@ def test_attention_bad_pages_and_lengths(cuda, kind):
 
 
 @gpu
-def test_attention_offsets_past_32_bits(cuda):
-    """Pages 2^32 bytes and more apart in one pool."""
+@pytest.mark.parametrize("step", [(1 << 31) + 4096, (1 << 33) + 4096])
+def test_attention_offsets_past_32_bits(cuda, step):
+    """Pages 2^32 bytes and more apart in one pool (of more than 2^36 bytes, the second time); `step`: elements between pages."""
     rng = _rng(4)
     page, dim, n_pages = 16, 128, 5
-    step = (1 << 31) + 4096  # elements between pages
-    pools = [torch.empty((n_pages - 1) * step + page * dim, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
-    kc, vc = (x.as_strided((n_pages, page, 1, dim), (step, dim, dim, 1)) for x in pools)
+    pool = torch.empty((n_pages - 1) * step + 2 * page * dim, dtype=torch.bfloat16, device="cuda")
+    kc, vc = (x.as_strided((n_pages, page, 1, dim), (step, dim, dim, 1), at) for x, at in ((pool, 0), (pool, page * dim)))
     kc.fill_(math.nan), vc.fill_(math.nan)
     table = np.array([[4, 0, 3]], dtype=np.int32)
     parts = _fill(rng, [41], table, kc, vc, page)
