@@ -30,7 +30,7 @@ Plan make_plan(const gpt_paged_cache* c, int32_t n_head) {
   const int group = n_head / c->n_kv_head;
   pl.chunk = group <= 8 ? group : c->dtype == GPT_DTYPE_BF16 ? (group < 16 ? group : 16) : 8;
   pl.chunks = (group + pl.chunk - 1) / pl.chunk;
-  pl.blocks = sm_count() * (pl.chunk > 8 ? 1 : 2);
+  pl.blocks = sm_count() * (pl.chunk > (c->dtype == GPT_DTYPE_BF16 ? 8 : 4) ? 1 : 2);  // as the kernels' kBlocks
   const int es = elem_size(c->dtype);
   const double span = ((double)(c->n_pages - 1) * c->page_stride + (double)(c->page_size - 1) * c->slot_stride +
                        (double)(c->n_kv_head - 1) * c->head_stride + c->head_dim) * es;
@@ -44,15 +44,18 @@ Plan make_plan(const gpt_paged_cache* c, int32_t n_head) {
   const int64_t used = std::min<int64_t>(pl.blocks, (rows * (tiles + kStart) + kWarps - 1) / kWarps);
   pl.team = 1;
   while (pl.team < 4 && c->n_kv_head % (2 * pl.team) == 0 && used * 2 * pl.team <= 16 * rows) pl.team *= 2;
-  // Rows that all get a block or a cluster at once, of at most 8 tiles a warp, take
-  // decode_row_kernel: one sequence of 513 keys, 12 heads of 64 in fp32 6.3 us (the
-  // line and its join 10.2), 4,096 keys of 8 heads of 128 11.3 (16.8), 32 sequences up
-  // to 500 keys of 12 heads of 64 14.5 (17.2); with 16 tiles a warp it loses, 16,000
-  // keys of 8 heads 33.7 (25.0).
+  // Rows that all get a block or a cluster at once take decode_row_kernel: no line to
+  // look up, no second kernel.  One sequence of 513 keys, 12 heads of 64 in fp32 6.3 us
+  // (the line and its join 10.2), 4,096 keys of 8 heads of 128 11.8 (19.4), 304 rows of
+  // 2,048 keys of 128 54 (60).  The line is better where the lengths' spread weighs
+  // more than its few us (over 16 tiles a warp), where clusters of 8 leave half the GPU
+  // idle (16,000 keys of 8 heads 33.7 against 25.0) and, with more rows than blocks at
+  // once, over 2 tiles a warp (384 rows of 512 keys 31.0 against 29.4).
   pl.cluster = 0;
   if (rows <= 2 * pl.blocks) {
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>(8, pl.blocks / rows));
-    if (tiles <= 8 * most * kWarps) pl.cluster = (int)std::min<int64_t>(most, (tiles + kWarps - 1) / kWarps);
+    const int deep = rows > pl.blocks ? 2 : most == 8 && 16 * rows < pl.blocks ? 8 : 16;
+    if (tiles <= deep * most * kWarps) pl.cluster = (int)std::min<int64_t>(most, (tiles + kWarps - 1) / kWarps);
   }
   if (pl.cluster) {
     pl.team = pl.join_heads = 1, pl.bytes = 0;

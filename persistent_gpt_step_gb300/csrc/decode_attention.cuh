@@ -389,9 +389,13 @@ struct Bf16Path {
 template <int GH_, int DP_, bool kFast, bool kExact>
 struct Fp32Path {
   using T = float;
-  static constexpr int DP = DP_, kHeads = GH_, kBlocks = 2, kUnit = kTile, kUnitStart = kStart;
-  static constexpr int KG = 128 / DP;            // 8-key groups of a step: 32 registers of keys, 32 of values
+  static constexpr int DP = DP_, kHeads = GH_, kUnit = kTile, kUnitStart = kStart;
+  // With 8 heads the reads of the queries in shared memory bound it: twice the keys of a
+  // step use each, with the registers of a block alone on its SM.
+  static constexpr int kBlocks = GH_ == 8 ? 1 : 2;
+  static constexpr int KG = (GH_ == 8 ? 256 : 128) / DP;  // 8-key groups of a step: 32 registers of keys, 32 of values (64 each)
   static constexpr int kKeys = 8 * KG;
+  static constexpr uint32_t kAll = 0xffffffffu >> (32 - kKeys);
   static constexpr int kLanes = DP / 4;          // lanes to a row of values
   static constexpr int kRows = 32 / kLanes;      // rows of values a load covers
   static constexpr int kQuery = kHeads * DP + kKeys * kHeads;  // a warp's queries and probabilities
@@ -449,7 +453,7 @@ struct Fp32Path {
     advance();
     load_keys();
     for (int k = k0; k < k1; k += kKeys) {
-      uint32_t there = (1u << kKeys) - 1u;  // keys that count
+      uint32_t there = kAll;  // keys that count
       if constexpr (kFast) {
 #pragma unroll
         for (int g = 0; g < KG; ++g) {
@@ -460,7 +464,7 @@ struct Fp32Path {
           if (off[g] == ~0u) there &= ~(0xffu << (g * 8));
         }
         if (k1 - k < kKeys) there &= (1u << (k1 - k)) - 1u;
-        if (there != (1u << kKeys) - 1u)  // what a slot that does not count holds may be NaN
+        if (there != kAll)  // what a slot that does not count holds may be NaN
 #pragma unroll
           for (int i = 0; i < kKeys / kRows; ++i)
             if (!((there >> (i * kRows + vrow)) & 1u)) vr[i] = make_uint4(0u, 0u, 0u, 0u);

@@ -13,7 +13,6 @@
 // took 150 us: nearly every warp has a marked id among its 256.)
 #include <cooperative_groups.h>
 
-#include <algorithm>
 #include <cmath>
 #include <utility>
 
@@ -361,11 +360,13 @@ extern "C" int gpt_next_token(const gpt_next_token_args* a, void* cuda_stream) {
     return call_error(GPT_ERR_INVALID_ARG, "bias_ids and bias_values go together");
   if ((const void*)a->out == a->logits && (a->dtype != GPT_DTYPE_FP32 || (a->rows > 1 && a->out_stride != a->logits_stride)))
     return call_error(GPT_ERR_INVALID_ARG, "in place needs fp32 logits and equal strides");
-  // Blocks of a row: as many as all run at once (four an SM; clusters leave the fifth
-  // place empty here and there), for a second wave repeats the marking of ids: 200 rows
-  // of 50,304 took 23 us in clusters of 2, 29 of 4, 35 of 8; 64 rows of 131,072 42, 25
-  // and 19 us; one row 13, 10 and 9.  A block has 512 ids at least.
-  const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>({8, 608 / a->rows, a->vocab / 512}));
+  // Blocks of a row: a power of two such that all run at once (four an SM; clusters
+  // leave the fifth place empty here and there), for a second wave repeats the marking
+  // of ids: 200 rows of 50,304 took 23 us in clusters of 2, 29 of 4, 35 of 8; 64 rows of
+  // 131,072 42, 25 and 19 us; one row 13, 10 and 9; 100 rows of 12,288 9.6 us in
+  // clusters of 4, 11.4 of 6.  A block has 512 ids at least.
+  int blocks = 1;
+  while (blocks < 8 && 2 * blocks * (int64_t)a->rows <= 608 && a->vocab / (2 * blocks) >= 512) blocks *= 2;
   if ((int64_t)a->rows * blocks > INT32_MAX) return call_error(GPT_ERR_UNSUPPORTED, "too many rows");
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
