@@ -1,7 +1,9 @@
-"""Throughput of the serving partition on a workload's model (162M by default).
+"""Throughput of the serving partition on a workload's model (162M by default), or,
+with --decode, of the batched decode-step operators on its heads and vocabulary.
 
 python -m persistent_gpt_step_gb300.serve_bench [--config main] [--blocks 24] [--tokens 256]
                                                 [--per-step 8] [--steps 20]
+python -m persistent_gpt_step_gb300.serve_bench --decode 64 [--config 57m] [--context 512]
 
 1. Serving alone: one launch in which `blocks` blocks generate `tokens` tokens
    greedily (batch 1) after a 16-token prompt; tokens/s = generated tokens /
@@ -13,6 +15,10 @@ python -m persistent_gpt_step_gb300.serve_bench [--config main] [--blocks 24] [-
    all blocks for comparison.  ("Open Flapping Airplanes" record, section "What
    ran": training, serving and Doom share one kernel by SM role; "How one
    persistent kernel runs three jobs": the B200 run gives serving 24 SMs.)
+3. --decode B: what a decode step of B sequences spends outside its matrix products:
+   per layer kv_append (rotating, for a rotary model) and decode_attention over a paged
+   cache of `context` positions a sequence, then next_token with repetition penalties;
+   microseconds per call and per step, from CUDA events.
 """
 
 from __future__ import annotations
@@ -26,6 +32,48 @@ from . import binding as B
 from . import inputs as I
 
 
+def decode_bench(cfg, batch: int, context: int, page: int = 16, reps: int = 20) -> dict:
+    """Microseconds per call of the decode-step operators and of a step's calls together, `batch` sequences
+    of `context` positions, every layer with a cache of its own."""
+    dev, heads, dim = "cuda", cfg.n_head, cfg.head_dim
+    pages = -(-context // page)
+    table = torch.randperm(batch * pages, device=dev).to(torch.int32).view(batch, pages)
+    caches = [[torch.randn(batch * pages, page, heads, dim, device=dev).to(torch.bfloat16) for _ in range(2)]
+              for _ in range(cfg.n_layer)]
+    q, k, v = torch.randn(batch, 3 * heads * dim, device=dev).to(torch.bfloat16).unflatten(1, (3 * heads, dim)).split(heads, dim=1)
+    lens = torch.full((batch,), context, dtype=torch.int32, device=dev)
+    positions = lens - 1
+    logits = torch.randn(batch, cfg.vocab, device=dev)
+    history = torch.randint(0, cfg.vocab, (batch, context), device=dev).to(torch.int32)
+    penalty = torch.full((batch,), 1.1, device=dev)
+    rope = dim if cfg.rope else 0
+
+    def append():
+        return [B.kv_append(k, v, kc, vc, table, positions, q=q, rope_dims=rope) for kc, vc in caches]
+
+    def attend():
+        return [B.decode_attention(q, kc, vc, table, lens) for kc, vc in caches]
+
+    def token():
+        return B.next_token(logits, history=history, history_lens=lens, repetition=penalty)
+
+    def timed(fn):
+        fn()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        e0.record()
+        for _ in range(reps):
+            fn()
+        e1.record()
+        torch.cuda.synchronize()
+        return 1e3 * e0.elapsed_time(e1) / reps
+
+    us = {"kv_append_us": timed(append) / cfg.n_layer, "decode_attention_us": timed(attend) / cfg.n_layer, "next_token_us": timed(token)}
+    us["step_us"] = timed(lambda: (append(), attend(), token()))
+    us["cache_gb_per_s"] = 4e-3 * batch * context * heads * dim / us["decode_attention_us"]
+    return us
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--config", default="main")
@@ -33,9 +81,15 @@ def main():
     ap.add_argument("--tokens", type=int, default=256)
     ap.add_argument("--per-step", type=int, default=8)
     ap.add_argument("--steps", type=int, default=20)
+    ap.add_argument("--decode", type=int, default=0, help="time the decode-step operators for this many sequences instead")
+    ap.add_argument("--context", type=int, default=512)
     args = ap.parse_args()
     cfg = I.CONFIGS[args.config]
     torch.cuda.set_device(0)
+    if args.decode:
+        print(json.dumps({"config": args.config, "sequences": args.decode, "context": args.context,
+                          **decode_bench(cfg, args.decode, args.context)}))
+        return
     batches = [tuple(torch.from_numpy(x).cuda() for x in I.batch(cfg, 1234, s)) for s in range(args.steps + 3)]
     prompt = I.batch(cfg, 77, 0)[0][0, :16]
     out = {"config": args.config, "blocks": args.blocks}

@@ -950,3 +950,12 @@ def test_given_stream(cuda):
     qo = B.kv_append(late_q[:, :2], late_q[:, :2], kc, vc, tab, _i([0, 0]), q=late_q, stream=st)
     st.synchronize()
     assert torch.equal(out, want) and torch.equal(tok, tok2) and torch.equal(qo, q)
+
+
+@gpu
+@pytest.mark.parametrize("name", ["tiny", "small_gated"])
+def test_serve_bench_times_the_operators(cuda, name):
+    from persistent_gpt_step_gb300 import inputs, serve_bench
+    got = serve_bench.decode_bench(inputs.CONFIGS[name], 3, 40, reps=2)
+    assert all(v > 0 for v in got.values())
+    assert set(got) == {"kv_append_us", "decode_attention_us", "next_token_us", "step_us", "cache_gb_per_s"}
