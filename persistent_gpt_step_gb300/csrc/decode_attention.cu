@@ -44,18 +44,25 @@ Plan make_plan(const gpt_paged_cache* c, int32_t n_head) {
   const int64_t used = std::min<int64_t>(pl.blocks, (rows * (tiles + kStart) + kWarps - 1) / kWarps);
   pl.team = 1;
   while (pl.team < 4 && c->n_kv_head % (2 * pl.team) == 0 && used * 2 * pl.team <= 16 * rows) pl.team *= 2;
-  // Rows that all get a block or a cluster at once take decode_row_kernel: no line to
-  // look up, no second kernel.  One sequence of 513 keys, 12 heads of 64 in fp32 6.3 us
-  // (the line and its join 10.2), 4,096 keys of 8 heads of 128 11.8 (19.4), 304 rows of
-  // 2,048 keys of 128 54 (60).  The line is better where the lengths' spread weighs
-  // more than its few us (over 16 tiles a warp), where clusters of 8 leave half the GPU
-  // idle (16,000 keys of 8 heads 33.7 against 25.0) and, with more rows than blocks at
-  // once, over 2 tiles a warp (384 rows of 512 keys 31.0 against 29.4).
-  pl.cluster = 0;
-  if (rows <= 2 * pl.blocks) {
-    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(8, pl.blocks / rows));
-    const int deep = rows > pl.blocks ? 2 : most == 8 && 16 * rows < pl.blocks ? 8 : 16;
-    if (tiles <= deep * most * kWarps) pl.cluster = (int)std::min<int64_t>(most, (tiles + kWarps - 1) / kWarps);
+  // Rows of few tiles a warp take decode_row_kernel: no line to look up, no second
+  // kernel.  Up to a block per row at once: a cluster of blocks for each (one sequence
+  // of 513 keys, 12 heads of 64 in fp32 6.3 us, the line and its join 10.2; 4,096 keys
+  // of 8 heads of 128 11.8 and 19.4; 304 rows of 2,048 keys of 64 33 and 38), but a few
+  // rows in clusters of 8 leave half the GPU idle (16,000 keys of 8 heads of 128 33.7
+  // and 25.0).  More rows: as many to a block as all run at once, down to a warp for a
+  // row (768 rows of 512 keys of 64 25.1 and 29.8, 2,400 of 128 20.4 and 29.2), then in
+  // several waves (8,192 rows of 1 to 128 44 and 53).  With more tiles a warp the spread
+  // of lengths weighs more than the line's few us (768 rows of 1 to 1,024 36 and 31),
+  // with longer rows of keys earlier (heads of 128: 768 rows of 1 to 512 34 and 30).
+  pl.cluster = 0, pl.pack = 1;
+  const int deep = c->head_dim * es <= 128 ? 16 : 12;
+  if (rows <= pl.blocks) {
+    const int64_t most = std::min<int64_t>(8, pl.blocks / rows);
+    if (tiles <= (most == 8 && 16 * rows < pl.blocks ? 8 : deep) * most * kWarps) pl.cluster = (int)std::min<int64_t>(most, (tiles + kWarps - 1) / kWarps);
+  } else {
+    while (pl.pack < kWarps && (rows + pl.pack - 1) / pl.pack > pl.blocks) pl.pack = pl.pack == 4 ? kWarps : pl.pack + 1;
+    const bool waves = (rows + pl.pack - 1) / pl.pack > pl.blocks;
+    if ((rows + pl.pack - 1) / pl.pack <= INT32_MAX && tiles <= (waves && deep == 12 ? 8 : deep) * (kWarps / pl.pack)) pl.cluster = 1;
   }
   if (pl.cluster) {
     pl.team = pl.join_heads = 1, pl.bytes = 0;
@@ -100,7 +107,7 @@ extern "C" int gpt_decode_attention(const gpt_paged_cache* c, const gpt_decode_a
   p.c = *c;
   p.a = *a;
   p.group = a->n_head / c->n_kv_head;
-  p.chunk = pl.chunk, p.chunks = pl.chunks, p.team = pl.team, p.join_heads = pl.join_heads;
+  p.chunk = pl.chunk, p.chunks = pl.chunks, p.team = pl.team, p.pack = pl.pack, p.join_heads = pl.join_heads;
   p.rows = c->n_kv_head / pl.team * pl.chunks;
   if (pl.fast) {
     p.page16 = (uint32_t)(c->page_stride * es / 16), p.slot16 = (uint32_t)(c->slot_stride * es / 16);

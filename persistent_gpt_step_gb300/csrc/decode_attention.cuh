@@ -750,9 +750,9 @@ __global__ void __launch_bounds__(kWarps * 32, P::kBlocks) decode_kernel(const _
   empty_rows();
 }
 
-// Few short rows: a cluster of blocks per row, its keys in equal parts over their
-// warps, the warps joined in shared memory, the blocks through each other's.  One
-// launch, no line of work to look up, no workspace.
+// Few or short rows: a cluster of blocks per row, or a block for `pack` rows, the keys
+// of a row in equal parts over its warps; these are joined in shared memory, blocks
+// through each other's.  One launch, no line of work to look up, no workspace.
 template <class P>
 __global__ void __launch_bounds__(kWarps * 32, P::kBlocks) decode_row_kernel(const __grid_constant__ DecodeParams p) {
   using T = typename P::T;
@@ -762,29 +762,26 @@ __global__ void __launch_bounds__(kWarps * 32, P::kBlocks) decode_row_kernel(con
   const int blocks = cluster.num_blocks(), rank = cluster.block_rank();
   after_stream();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, d = p.c.head_dim;
-  const int s = blockIdx.x / blocks / p.rows, row = blockIdx.x / blocks % p.rows;
-  const int len = seq_len(p, s, tid == 0), tiles = (len + kTile - 1) / kTile;
-  Part w;
-  w.s = s, w.h = row / p.chunks;
-  w.hq = w.h * p.group + row % p.chunks * p.chunk, w.n = min(p.chunk, (w.h + 1) * p.group - w.hq);
-  const int part = rank * kWarps + warp, parts = blocks * kWarps;
-  w.k0 = (int)((int64_t)part * tiles / parts) * kTile, w.k1 = min(len, (int)((int64_t)(part + 1) * tiles / parts) * kTile);
-  w.left = sm + warp * kLeft;
-  if (w.k0 < w.k1) P::run(p, sm + (kWarps + 1) * kLeft + warp * P::kQuery, w);
-  else if (lane < w.n) w.left[2 * lane] = -INFINITY, w.left[2 * lane + 1] = 0.f;
-  __syncthreads();
-  float* whole = sm + kWarps * kLeft;
-  auto finish = [&](int i, float top, float sum, float* x) {
-    const int e = i % (d / 4) * 4, hq = w.hq + i / (d / 4);
-    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] *= inv;
-    store4((T*)p.a.out + s * p.a.out_row + hq * p.a.out_head + e, x);
-    if (e == 0) store_lse(p, s, hq, top, sum);
+  const int each = kWarps / p.pack;  // warps of a row
+  const int64_t row0 = (int64_t)(blockIdx.x / blocks) * p.pack, all = (int64_t)p.c.n_seq * p.rows;
+  auto part_of = [&](int64_t r) {  // sequence and heads of a row
+    Part w;
+    w.s = (int)r / p.rows, w.h = (int)r % p.rows / p.chunks;
+    w.hq = w.h * p.group + (int)r % p.rows % p.chunks * p.chunk, w.n = min(p.chunk, (w.h + 1) * p.group - w.hq);
+    return w;
   };
+  if (warp < each * p.pack && row0 + warp / each < all) {
+    Part w = part_of(row0 + warp / each);
+    const int len = seq_len(p, w.s, true), tiles = (len + kTile - 1) / kTile;
+    const int part = rank * each + warp % each, parts = blocks * each;
+    w.k0 = (int)((int64_t)part * tiles / parts) * kTile, w.k1 = min(len, (int)((int64_t)(part + 1) * tiles / parts) * kTile);
+    w.left = sm + warp * kLeft;
+    if (w.k0 < w.k1) P::run(p, sm + (kWarps + 1) * kLeft + warp * P::kQuery, w);
+    else if (lane < w.n) w.left[2 * lane] = -INFINITY, w.left[2 * lane + 1] = 0.f;
+  }
+  __syncthreads();
   // (m, l, o) of one head and four dims over n pieces, those without keys left out
-  auto join = [&](int i, int n, auto piece, float& top, float& sum, float* x) {
-    const int e = i % (d / 4) * 4, qh = i / (d / 4);
+  auto join = [&](int qh, int e, int n, auto piece, float& top, float& sum, float* x) {
     top = -INFINITY, sum = 0.f, x[0] = x[1] = x[2] = x[3] = 0.f;
     for (int k = 0; k < n; ++k) top = fmaxf(top, piece(k)[2 * qh]);
     for (int k = 0; k < n; ++k) {
@@ -796,22 +793,35 @@ __global__ void __launch_bounds__(kWarps * 32, P::kBlocks) decode_row_kernel(con
       x[0] += y.x * keep, x[1] += y.y * keep, x[2] += y.z * keep, x[3] += y.w * keep;
     }
   };
+  auto finish = [&](const Part& w, int qh, int e, float top, float sum, float* x) {
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] *= inv;
+    store4((T*)p.a.out + w.s * p.a.out_row + (w.hq + qh) * p.a.out_head + e, x);
+    if (e == 0) store_lse(p, w.s, w.hq + qh, top, sum);
+  };
   float top, sum, x[4];
-  for (int i = tid; i < w.n * (d / 4); i += kWarps * 32) {
-    join(i, kWarps, [&](int k) { return sm + k * kLeft; }, top, sum, x);
+  float* whole = sm + kWarps * kLeft;
+  for (int i = tid; i < p.pack * p.chunk * (d / 4); i += kWarps * 32) {
+    const int e = i % (d / 4) * 4, qh = i / (d / 4) % p.chunk, g = i / (d / 4) / p.chunk;
+    if (row0 + g >= all) break;
+    const Part w = part_of(row0 + g);
+    if (qh >= w.n) continue;
+    join(qh, e, each, [&](int k) { return sm + (g * each + k) * kLeft; }, top, sum, x);
     if (blocks == 1) {
-      finish(i, top, sum, x);
+      finish(w, qh, e, top, sum, x);
     } else {
-      const int qh = i / (d / 4);
-      if (i % (d / 4) == 0) whole[2 * qh] = top, whole[2 * qh + 1] = sum;
-      store4(whole + left_o(P::kHeads) + qh * P::DP + i % (d / 4) * 4, x);
+      if (e == 0) whole[2 * qh] = top, whole[2 * qh + 1] = sum;
+      store4(whole + left_o(P::kHeads) + qh * P::DP + e, x);
     }
   }
   if (blocks == 1) return;
   cluster.sync();
+  const Part w = part_of(row0);
   for (int i = rank * kWarps * 32 + tid; i < w.n * (d / 4); i += blocks * kWarps * 32) {
-    join(i, blocks, [&](int k) { return (const float*)cluster.map_shared_rank(whole, k); }, top, sum, x);
-    finish(i, top, sum, x);
+    const int e = i % (d / 4) * 4, qh = i / (d / 4);
+    join(qh, e, blocks, [&](int k) { return (const float*)cluster.map_shared_rank(whole, k); }, top, sum, x);
+    finish(w, qh, e, top, sum, x);
   }
   cluster.sync();  // a block's memory stays until the others have read it
 }
@@ -913,7 +923,7 @@ int launch(const DecodeParams& p, const Plan& pl, cudaStream_t st) {
   if (pl.cluster) {
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = pl.cluster, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(p.c.n_seq * p.rows * pl.cluster), cfg.dynamicSmemBytes = kRowBytes, cfg.numAttrs = 2;
+    cfg.gridDim = dim3((unsigned)(((int64_t)p.c.n_seq * p.rows + pl.pack - 1) / pl.pack * pl.cluster)), cfg.dynamicSmemBytes = kRowBytes, cfg.numAttrs = 2;
     cudaLaunchKernelEx(&cfg, decode_row_kernel<P>, p);
     return check_launch("gpt_decode_attention");
   }

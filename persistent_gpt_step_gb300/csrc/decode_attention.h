@@ -23,6 +23,7 @@ struct DecodeParams {
   int32_t chunk;     // query heads of a row
   int32_t chunks;    // rows of one key head
   int32_t team;      // warps that take the same keys, a key head each
+  int32_t pack;      // rows of a block (decode_row_kernel)
   int32_t rows;      // rows (of `team` key heads) of one sequence
   int32_t join_heads;  // query heads of a block of the second kernel, 1 to 8
   uint32_t page16, slot16, head16;  // the cache's strides in 16 bytes (fast forms)
@@ -35,7 +36,7 @@ struct Plan {
   int blocks;          // of the line's grid
   int chunk, chunks;   // query heads of a row, rows of a key head
   int team;            // warps that take the same keys
-  int cluster;         // blocks of a row (decode_row_kernel); 0: the line
+  int cluster, pack;   // decode_row_kernel: blocks of a row, rows of a block (one is 1); 0: the line
   int join_heads;      // query heads of a block of the second kernel
   bool fast;           // pages of whole 8-key groups, offsets in 16 bytes within 32 bits
   size_t ml_at, o_at, bytes;  // the workspace: pieces' (m, l), their o, its size
