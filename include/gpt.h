@@ -308,8 +308,8 @@ int gpt_serve_end(gpt* h);
  * at once from a paged key-value cache (an addition of this library: the
  * serving partition above decodes one sequence from a contiguous cache).  Each
  * is one call on cuda_stream that does not synchronise, allocates nothing and
- * may be captured into a CUDA graph; the current device is the one the pointers
- * belong to.  Sums, softmax statistics and rotations are fp32; results are
+ * may be captured into a CUDA graph; calls may overlap on different streams and
+ * threads.  The current device is the one the pointers belong to.  Sums, softmax statistics and rotations are fp32; results are
  * bitwise repeatable.  Errors: INVALID_ARG, UNSUPPORTED, CUDA (text via
  * gpt_last_error(NULL)); nothing is launched on an error.
  *
@@ -331,7 +331,8 @@ int gpt_serve_end(gpt* h);
  * page*page_stride + slot*slot_stride + head*head_stride + i (elements, k and v
  * alike; any order of pages, slots and heads).  Base addresses and strides are
  * multiples of 16 bytes, strides are not negative; head_dim is a multiple of 16
- * bytes and <= 128.  Sequences may share pages.
+ * bytes and <= 128; max_pages * page_size stays 4096 below 2^31.  Sequences may
+ * share pages (table_stride 0: all of them one row of the table).
  */
 typedef struct gpt_paged_cache {
   void *k, *v;               /* DEVICE, of type dtype                               */
@@ -347,8 +348,8 @@ typedef struct gpt_paged_cache {
  * (2i, 2i+1), i < rope_dims/2, of every head turn by positions[n] *
  * rope_base^(-2i/rope_dims), the rotary form of the RTX 3090 page's model
  * (gpt_config.rope); elements from rope_dims on, and the values, are copied.
- * The rotation is fp32 with an angle accurate to 2^-23 of a turn at every
- * position; one rounding to the cache's type.
+ * The rotation is fp32 with an angle accurate to 2^-24 of a turn below position
+ * 2^24 (2^-20 from there on); one rounding to the cache's type.
  *   k, v: DEVICE [n_tokens, n_kv_head, head_dim]; q, q_out [n_tokens, n_head,
  *     head_dim], or NULL (both; n_head 0).  *_row, *_head: strides in elements
  *     (multiples of 16 bytes), so one QKV projection's output serves as all
@@ -366,7 +367,7 @@ typedef struct gpt_kv_append_args {
   int64_t q_row, q_head, k_row, k_head, v_row, v_head, qo_row, qo_head;
   const int32_t *positions, *seq;
   uint32_t* status;
-  double rope_base;          /* > 0; used when rope_dims > 0                        */
+  double rope_base;          /* >= 1; used when rope_dims > 0                       */
   int32_t n_tokens, n_head;
   int32_t rope_dims;         /* even, 0 (no rotation) .. head_dim                   */
 } gpt_kv_append_args;
@@ -381,7 +382,7 @@ int gpt_kv_append(const gpt_paged_cache* cache, const gpt_kv_append_args* args, 
  * bad page count as absent (status), and so do keys whose score is -infinity.
  * Positions from lens[s] on may hold anything, NaN included.
  *   q, out: DEVICE [n_seq, n_head, head_dim] with strides as in gpt_kv_append;
- *   out does not overlap an input.  lse: DEVICE fp32 [n_seq, n_head] (natural
+ *   out does not overlap an input (nor q).  lse: DEVICE fp32 [n_seq, n_head] (natural
  *   log of the sum of exponentials of the scaled scores) or NULL.
  *   workspace: DEVICE scratch of gpt_decode_attention_workspace bytes, 16-byte
  *     aligned, for this call alone until it has run; its content does not matter.
@@ -418,9 +419,11 @@ size_t gpt_decode_attention_workspace(const gpt_paged_cache* cache, int32_t n_he
  * -infinity); lse[b] = log sum_i exp(z_i) (-infinity where no z is above that).
  *   logits: DEVICE [rows, vocab] of type dtype; out: DEVICE fp32 [rows, vocab],
  *     may be logits itself (fp32, same stride).  Any of out, token and lse may
- *     be NULL, not all.  *_stride: elements between rows; no alignment needed.
- *   history, bias_ids: DEVICE int32, allowed: DEVICE uint32 [rows,
- *     ceil(vocab / 32)]; history, repetition, presence, frequency, bias_ids,
+ *     be NULL, not all.  *_stride: elements between rows, at least a row's width
+ *     or, but for out, 0 (all rows read one); no alignment needed.
+ *   history: DEVICE int32 [rows, max_history] (all of it is readable, whatever
+ *     history_lens is); bias_ids: DEVICE int32, bias_values: DEVICE fp32 [rows,
+ *     n_bias]; allowed: DEVICE uint32 [rows, ceil(vocab / 32)]; history, repetition, presence, frequency, bias_ids,
  *     allowed may be NULL: that step falls away.  history_lens NULL: max_history
  *     each; prompt_lens NULL: 0 each.  Negative bias ids are unused entries;
  *     ids >= vocab, and history ids outside [0, vocab), are skipped (status).

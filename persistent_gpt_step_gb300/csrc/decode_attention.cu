@@ -62,7 +62,7 @@ Plan make_plan(const gpt_paged_cache* c, int32_t n_head) {
   } else {
     while (pl.pack < kWarps && (rows + pl.pack - 1) / pl.pack > pl.blocks) pl.pack = pl.pack == 4 ? kWarps : pl.pack + 1;
     const bool waves = (rows + pl.pack - 1) / pl.pack > pl.blocks;
-    if ((rows + pl.pack - 1) / pl.pack <= INT32_MAX && tiles <= (waves && deep == 12 ? 8 : deep) * (kWarps / pl.pack)) pl.cluster = 1;
+    if (rows <= (1 << 28) && tiles <= (waves && deep == 12 ? 8 : deep) * (kWarps / pl.pack)) pl.cluster = 1;
   }
   if (pl.cluster) {
     pl.team = pl.join_heads = 1, pl.bytes = 0;
@@ -99,6 +99,7 @@ extern "C" int gpt_decode_attention(const gpt_paged_cache* c, const gpt_decode_a
   if (!aligned16(a->q) || !aligned16(a->out) || !stride16(a->q_row, es) || !stride16(a->q_head, es) ||
       !stride16(a->out_row, es) || !stride16(a->out_head, es))
     return call_error(GPT_ERR_INVALID_ARG, "q and out addresses and strides must be multiples of 16 bytes");
+  if (a->out == a->q) return call_error(GPT_ERR_INVALID_ARG, "out must not be q");
   if (!std::isfinite(a->scale)) return call_error(GPT_ERR_INVALID_ARG, "scale must be finite");
   const Plan pl = make_plan(c, a->n_head);
   if (pl.bytes && (!a->workspace || a->workspace_bytes < pl.bytes || !aligned16(a->workspace)))

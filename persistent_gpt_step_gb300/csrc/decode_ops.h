@@ -38,7 +38,7 @@ inline int check_cache(const gpt_paged_cache* c) {
   if (!aligned16(c->k) || !aligned16(c->v) || !stride16(c->page_stride, es) || !stride16(c->slot_stride, es) ||
       !stride16(c->head_stride, es))
     return call_error(GPT_ERR_INVALID_ARG, "cache addresses and strides must be multiples of 16 bytes");
-  if (c->table_stride < c->max_pages && c->n_seq > 1)
+  if (c->table_stride < c->max_pages && c->table_stride != 0 && c->n_seq > 1)
     return call_error(GPT_ERR_INVALID_ARG, "table_stride is smaller than max_pages");
   return GPT_OK;
 }

@@ -119,8 +119,8 @@ extern "C" int gpt_kv_append(const gpt_paged_cache* c, const gpt_kv_append_args*
   if (a->n_tokens < 0 || a->n_head < 0) return call_error(GPT_ERR_INVALID_ARG, "n_tokens and n_head must not be negative");
   if (a->rope_dims < 0 || a->rope_dims > c->head_dim || (a->rope_dims & 1))
     return call_error(GPT_ERR_INVALID_ARG, "rope_dims %d: even, from 0 to head_dim %d", a->rope_dims, c->head_dim);
-  if (a->rope_dims > 0 && !(a->rope_base > 0 && std::isfinite(a->rope_base)))
-    return call_error(GPT_ERR_INVALID_ARG, "rope_base must be positive and finite");
+  if (a->rope_dims > 0 && !(a->rope_base >= 1 && std::isfinite(a->rope_base)))
+    return call_error(GPT_ERR_INVALID_ARG, "rope_base must be finite and at least 1");
   if (a->n_tokens == 0) return GPT_OK;
   if (c->n_seq == 0) return call_error(GPT_ERR_INVALID_ARG, "the cache has no sequences");
   if (!a->k || !a->v || !a->positions) return call_error(GPT_ERR_INVALID_ARG, "k, v and positions must be non-NULL");

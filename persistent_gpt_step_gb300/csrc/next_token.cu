@@ -349,10 +349,10 @@ extern "C" int gpt_next_token(const gpt_next_token_args* a, void* cuda_stream) {
   if (!a->logits) return call_error(GPT_ERR_INVALID_ARG, "logits must be non-NULL");
   if (reinterpret_cast<uintptr_t>(a->logits) % elem_size(a->dtype) || reinterpret_cast<uintptr_t>(a->out) % 4)
     return call_error(GPT_ERR_INVALID_ARG, "logits and out must lie on their elements' boundaries");
-  if (a->rows > 1 && (a->logits_stride < a->vocab || (a->out && a->out_stride < a->vocab) ||
-                      (a->history && a->history_stride < a->max_history) ||
-                      (a->bias_ids && a->bias_stride < a->n_bias) ||
-                      (a->allowed && a->allowed_stride < (a->vocab + 31) / 32)))
+  auto narrow = [&](int64_t stride, int64_t width) { return a->rows > 1 && stride != 0 && stride < width; };  // 0: all rows read the same
+  if (narrow(a->logits_stride, a->vocab) || (a->out && a->rows > 1 && a->out_stride < a->vocab) ||
+      (a->history && narrow(a->history_stride, a->max_history)) || (a->bias_ids && narrow(a->bias_stride, a->n_bias)) ||
+      (a->allowed && narrow(a->allowed_stride, (a->vocab + 31) / 32)))
     return call_error(GPT_ERR_INVALID_ARG, "a row stride is smaller than its row");
   if (!a->history && (a->history_lens || a->prompt_lens))
     return call_error(GPT_ERR_INVALID_ARG, "history_lens and prompt_lens go with history");

@@ -57,7 +57,7 @@ def _append(**kw):
 
 
 def _attend(**kw):
-    a = B.gpt_decode_attention_args(q=FAKE, out=FAKE, lens=FAKE, q_row=512, q_head=64, out_row=512, out_head=64,
+    a = B.gpt_decode_attention_args(q=FAKE, out=FAKE + 4096, lens=FAKE, q_row=512, q_head=64, out_row=512, out_head=64,
                                     workspace=FAKE, workspace_bytes=1 << 40, scale=0.125, n_head=8)
     for k, v in kw.items():
         setattr(a, k, v)
@@ -91,7 +91,7 @@ def test_bad_caches_are_refused(lib, change, code, word):
 
 @pytest.mark.parametrize("change,word", [
     (dict(n_tokens=-1), "negative"), (dict(n_head=-1), "negative"), (dict(rope_dims=63), "rope_dims"),
-    (dict(rope_dims=66), "rope_dims"), (dict(rope_dims=-2), "rope_dims"), (dict(rope_base=0.0), "rope_base"),
+    (dict(rope_dims=66), "rope_dims"), (dict(rope_dims=-2), "rope_dims"), (dict(rope_base=0.5), "rope_base"),
     (dict(rope_base=math.inf), "rope_base"), (dict(rope_base=math.nan), "rope_base"), (dict(k=None), "NULL"),
     (dict(positions=None), "NULL"), (dict(n_tokens=4), "sequences"), (dict(k_row=250), "16 bytes"),
     (dict(v=FAKE + 2), "16 bytes"), (dict(q=None), "n_head"), (dict(q_out=None), "n_head"), (dict(n_head=0), "n_head"),
@@ -107,7 +107,7 @@ def test_append_refusals(lib, change, word):
 @pytest.mark.parametrize("change,word", [
     (dict(n_head=6), "multiple"), (dict(n_head=0), "multiple"), (dict(q=None), "NULL"), (dict(out=None), "NULL"),
     (dict(lens=None), "NULL"), (dict(q=FAKE + 4), "16 bytes"), (dict(out_row=508), "16 bytes"),
-    (dict(scale=math.nan), "scale"), (dict(scale=math.inf), "scale"), (dict(workspace=None), "workspace"),
+    (dict(scale=math.nan), "scale"), (dict(scale=math.inf), "scale"), (dict(out=FAKE), "q"), (dict(workspace=None), "workspace"),
     (dict(workspace=FAKE + 8), "workspace"), (dict(workspace_bytes=64), "workspace")])
 def test_attention_refusals(lib, change, word):
     if word == "workspace":  # a table that reaches far enough for one to be needed
@@ -142,6 +142,15 @@ def test_nothing_to_do_is_no_error(lib):
     assert lib.gpt_kv_append(c, ctypes.byref(_append(n_tokens=0)), None) == 0
     assert lib.gpt_decode_attention(ctypes.byref(_cache(n_seq=0)), ctypes.byref(_attend()), None) == 0
     assert lib.gpt_next_token(ctypes.byref(_token(rows=0, out=FAKE + 4096)), None) == 0
+
+
+def test_calls_without_a_gpu_fail_cleanly(lib):
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    c = ctypes.byref(_cache())
+    for rc in (lib.gpt_kv_append(c, ctypes.byref(_append()), None), lib.gpt_decode_attention(c, ctypes.byref(_attend()), None),
+               lib.gpt_next_token(ctypes.byref(_token(out=FAKE + 4096)), None)):
+        assert rc == -2 and lib.gpt_last_error(None)
 
 
 def test_structs_match_the_header():
@@ -816,6 +825,107 @@ def test_empty_batches(cuda):
     x = _token_inputs(_rng(3), 2, 50, 4, "fp32")
     token, _, _ = B.next_token(_t(x["z"]), history=z(2, 0, t=i32), history_lens=z(2, t=i32), bias_ids=z(2, 0, t=i32), bias_values=z(2, 0))
     assert token.tolist() == x["z"].argmax(axis=1).tolist()
+
+
+@gpu
+def test_broadcast_inputs(cuda):
+    """Inputs expanded over rows, sequences and heads (stride 0)."""
+    rng = _rng(21)
+    x = _token_inputs(rng, 4, 700, 30, "fp32")
+    for k in ("z", "hist", "ids", "vals", "allowed"):
+        x[k] = np.repeat(x[k][:1], 4, axis=0)
+    want = _next(**x)
+    wide = {k: (_t(x[k][:1]) if k in ("z", "vals") else _i(x[k][:1])).expand(4, -1) for k in ("z", "hist", "ids", "vals", "allowed")}
+    got = B.next_token(wide["z"], history=wide["hist"], history_lens=_i(x["hl"]), prompt_lens=_i(x["pl"]), repetition=_t(x["rep"]),
+                       presence=_t(x["pres"]), frequency=_t(x["freq"]), bias_ids=wide["ids"], bias_values=wide["vals"], allowed=wide["allowed"])
+    _check_next(got, want)
+    table, n_pages = _pages(rng, [77], 16)
+    kc, vc = _pool(n_pages, 16, 1, 64, "bf16", "slot", math.nan)
+    (k, v), = _fill(rng, [77], table, kc, vc, 16)
+    q = _t(rng.standard_normal((3, 1, 64)), "bf16").expand(3, 6, 64)
+    out, lse = B.decode_attention(q, kc.expand(-1, -1, 2, -1), vc.expand(-1, -1, 2, -1), _i(table).expand(3, -1), _i([77, 30, 1]))
+    for s, n in enumerate((77, 30, 1)):
+        w, wl, tol, tl = _attention(_np(q)[s], k[:n], v[:n], 0.125)
+        _check(out[s], w, tol + (np.abs(w) + tol) * 2.0 ** -8)
+        _check(lse[s], wl, tl)
+    new = _t(rng.standard_normal((2, 1, 64)), "bf16").expand(2, 3, 64)
+    kc, vc = _pool(4, 16, 3, 64, "bf16", "slot", 0.0)
+    assert B.kv_append(new, new, kc, vc, _i([[1, 2]]), _i([3, 20]), seq=_i([0, 0])) is None
+    assert torch.equal(kc[1, 3], new[0]) and torch.equal(vc[2, 4], new[1])
+
+
+@gpu
+@pytest.mark.parametrize("reach", [0, 400000])
+def test_captured_behind_a_join_and_copies(cuda, reach):
+    """Captured where the stream has just joined another and copied, replayed with other inputs, beside eager calls."""
+    rng = _rng(31)
+    table, n_pages = _pages(rng, [300, 40, 0], 16, width=reach // 16)
+    kc, vc = _pool(n_pages, 16, 2, 64, "bf16", "slot", math.nan)
+    _fill(rng, [300, 40, 0], table, kc, vc, 16)
+    tab, lens = _i(table), _i([300, 40, 0])
+    qs = [_t(rng.standard_normal((3, 8, 64)), "bf16") for _ in range(3)]
+    zs = [_t(rng.standard_normal((3, 999))) for _ in range(3)]
+    want = [(*B.decode_attention(q, kc, vc, tab, lens), *B.next_token(z)) for q, z in zip(qs, zs)]
+    q, z, side = torch.zeros_like(qs[0]), torch.zeros_like(zs[0]), torch.cuda.Stream()
+    q_in, z_in = torch.zeros_like(q), torch.zeros_like(z)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            z.copy_(z_in)
+            token = B.next_token(z)
+        q.copy_(q_in)
+        main.wait_stream(side)
+        att = B.decode_attention(q, kc, vc, tab, lens)
+        again = B.decode_attention(q, kc, vc, tab, lens)
+    for i in (1, 2, 0):
+        q_in.copy_(qs[i])
+        z_in.copy_(zs[i])
+        g.replay()
+        eager = B.decode_attention(qs[i], kc, vc, tab, lens)
+        torch.cuda.synchronize()
+        for a, b in zip((*att, *token), want[i]):
+            assert torch.equal(a, b)
+        for other in (again, eager):
+            assert torch.equal(other[0], want[i][0]) and torch.equal(other[1], want[i][1])
+
+
+@gpu
+def test_calls_from_threads_on_their_own_streams(cuda):
+    """Four threads, a stream each, calling at once."""
+    import threading
+    rng = _rng(41)
+    lens = [2000, 1, 555, 90]
+    table, n_pages = _pages(rng, lens, 16, width=30000)
+    kc, vc = _pool(n_pages, 16, 2, 128, "bf16", "slot", math.nan)
+    _fill(rng, lens, table, kc, vc, 16)
+    tab, ln = _i(table), _i(lens)
+    qs = [_t(rng.standard_normal((4, 8, 128)), "bf16") for _ in range(4)]
+    x = _token_inputs(rng, 4, 3000, 64, "fp32")
+    z, hist, rep = _t(x["z"]), _i(x["hist"]), _t(x["rep"])
+    want = [B.decode_attention(q, kc, vc, tab, ln) for q in qs]
+    token = B.next_token(z, history=hist, repetition=rep)
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            for _ in range(50):
+                out, lse = B.decode_attention(qs[i], kc, vc, tab, ln)
+                t = B.next_token(z, history=hist, repetition=rep)
+                st.synchronize()
+                if not (torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1]) and all(torch.equal(a, b) for a, b in zip(t, token))):
+                    bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
 
 
 class _Layer:
