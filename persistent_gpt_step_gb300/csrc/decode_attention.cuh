@@ -572,15 +572,6 @@ struct Fp32Path {
 
 // ---- the kernels --------------------------------------------------------------
 
-// The kernels are launched with programmatic stream serialization: their blocks may
-// take free places while the kernel before them in the stream still runs, and wait
-// here, before their first access to memory, until it is complete.  Worth 2 to 3 us of
-// a line and its join, about 1 us of a cluster kernel.
-__device__ __forceinline__ void after_stream() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 __device__ __forceinline__ void store4(float* to, const float* x) { *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]); }
 __device__ __forceinline__ void store4(__nv_bfloat16* to, const float* x) {
   *reinterpret_cast<uint2*>(to) = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
@@ -915,24 +906,13 @@ int launch(const DecodeParams& p, const Plan& pl, cudaStream_t st) {
     if (const int rc = check_launch("gpt_decode_attention")) return rc;
     ready = dev;
   }
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kWarps * 32), cfg.stream = st, cfg.attrs = attr, cfg.numAttrs = 1;
   if (pl.cluster) {
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = pl.cluster, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)(((int64_t)p.c.n_seq * p.rows + pl.pack - 1) / pl.pack * pl.cluster)), cfg.dynamicSmemBytes = kRowBytes, cfg.numAttrs = 2;
-    cudaLaunchKernelEx(&cfg, decode_row_kernel<P>, p);
-    return check_launch("gpt_decode_attention");
+    const dim3 grid((unsigned)(((int64_t)p.c.n_seq * p.rows + pl.pack - 1) / pl.pack * pl.cluster));
+    return launch_after("gpt_decode_attention", decode_row_kernel<P>, grid, kWarps * 32, kRowBytes, pl.cluster, st, p);
   }
-  cfg.gridDim = dim3(pl.blocks), cfg.dynamicSmemBytes = kLineBytes;
-  cudaLaunchKernelEx(&cfg, decode_kernel<P>, p);
-  if (const int rc = check_launch("gpt_decode_attention")) return rc;
-  cfg.gridDim = dim3(pl.blocks, (pl.team * pl.chunk + pl.join_heads - 1) / pl.join_heads), cfg.dynamicSmemBytes = 0;
-  cudaLaunchKernelEx(&cfg, decode_join_kernel<typename P::T>, p);
-  return check_launch("gpt_decode_attention (join)");
+  if (const int rc = launch_after("gpt_decode_attention", decode_kernel<P>, dim3(pl.blocks), kWarps * 32, kLineBytes, 0, st, p)) return rc;
+  const dim3 grid(pl.blocks, (pl.team * pl.chunk + pl.join_heads - 1) / pl.join_heads);
+  return launch_after("gpt_decode_attention (join)", decode_join_kernel<typename P::T>, grid, kWarps * 32, 0, 0, st, p);
 }
 
 // The launch for a head size of at most DP: the fast forms need pages of whole 8-key

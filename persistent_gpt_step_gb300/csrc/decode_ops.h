@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "../../include/gpt.h"
 
 namespace pgs {
@@ -49,6 +51,29 @@ inline int check_launch(const char* what) {
 }
 
 #ifdef __CUDACC__
+// Launches an operator's kernel with programmatic stream serialization: its blocks may
+// take their places while the kernel before it in the stream ends, and wait in
+// after_stream() for that kernel's completion.  `cluster` blocks to a cluster, if not 0.
+template <typename... P>
+inline int launch_after(const char* what, void (*kernel)(P...), dim3 grid, int threads, int smem, int cluster, cudaStream_t st,
+                        std::common_type_t<P>... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid, cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = st;
+  cfg.attrs = attr, cfg.numAttrs = cluster ? 2 : 1;
+  cudaLaunchKernelEx(&cfg, kernel, args...);
+  return check_launch(what);
+}
+// Every thread's first statement, before any access to memory that another kernel
+// writes or reads.  The kernels do not let their successors in early themselves: with
+// that, the successor's blocks crowd the SMs that are done first (next token of 33 rows
+// 20.7 us instead of 14.4; 16.5 without any of this).
+__device__ __forceinline__ void after_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ void set_status(uint32_t* status, uint32_t bit) {
   if (status) atomicOr(status, bit);
 }

@@ -46,6 +46,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
   __shared__ __align__(16) float2 turn[kMaxPairs];  // cosine, sine
   const gpt_paged_cache& c = p.c;
   const gpt_kv_append_args& a = p.a;
+  after_stream();
   const int64_t n = blockIdx.x;
   const int s = a.seq ? a.seq[n] : (int)n;
   if (s < 0) return;  // padding
@@ -134,7 +135,7 @@ extern "C" int gpt_kv_append(const gpt_paged_cache* c, const gpt_kv_append_args*
   if (a->n_head > 0 && (!aligned16(a->q) || !aligned16(a->q_out) || !stride16(a->q_row, es) || !stride16(a->q_head, es) ||
                         !stride16(a->qo_row, es) || !stride16(a->qo_head, es)))
     return call_error(GPT_ERR_INVALID_ARG, "q and q_out addresses and strides must be multiples of 16 bytes");
-  AppendParams p;
+  AppendParams p = {};
   p.c = *c;
   p.a = *a;
   if (a->rope_dims > 0) {
@@ -150,12 +151,10 @@ extern "C" int gpt_kv_append(const gpt_paged_cache* c, const gpt_kv_append_args*
   // us with 256 threads, 4.4 with 128); many: fewer, for the throughput (32,768: 129 us
   // with 128, 149 with 256).
   const bool few = a->n_tokens <= 608;
-  if (c->dtype == GPT_DTYPE_BF16) {
-    if (few) kv_append_kernel<__nv_bfloat16, 256, 3><<<a->n_tokens, 256, 0, st>>>(p);
-    else kv_append_kernel<__nv_bfloat16, 128, 6><<<a->n_tokens, 128, 0, st>>>(p);
-  } else {
-    if (few) kv_append_kernel<float, 256, 3><<<a->n_tokens, 256, 0, st>>>(p);
-    else kv_append_kernel<float, 128, 6><<<a->n_tokens, 128, 0, st>>>(p);
-  }
-  return check_launch("gpt_kv_append");
+  const dim3 grid(a->n_tokens);
+  auto launch = [&](auto few_kernel, auto many_kernel) {
+    return launch_after("gpt_kv_append", few ? few_kernel : many_kernel, grid, few ? 256 : 128, 0, 0, st, p);
+  };
+  if (c->dtype == GPT_DTYPE_BF16) return launch(kv_append_kernel<__nv_bfloat16, 256, 3>, kv_append_kernel<__nv_bfloat16, 128, 6>);
+  return launch(kv_append_kernel<float, 256, 3>, kv_append_kernel<float, 128, 6>);
 }

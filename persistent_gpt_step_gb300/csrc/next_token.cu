@@ -79,6 +79,7 @@ __global__ void __launch_bounds__(kThreads, 5) next_token_kernel(const __grid_co
   __shared__ uint32_t scan[kWarps];
   __shared__ int fit;
   cg::cluster_group cluster = cg::this_cluster();
+  after_stream();
   auto started = cluster.barrier_arrive();  // waited for before another block's memory is written
   const int blocks = cluster.num_blocks(), part = cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -368,13 +369,8 @@ extern "C" int gpt_next_token(const gpt_next_token_args* a, void* cuda_stream) {
   int blocks = 1;
   while (blocks < 8 && 2 * blocks * (int64_t)a->rows <= 608 && a->vocab / (2 * blocks) >= 512) blocks *= 2;
   if ((int64_t)a->rows * blocks > INT32_MAX) return call_error(GPT_ERR_UNSUPPORTED, "too many rows");
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = blocks, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a->rows * blocks), cfg.blockDim = dim3(kThreads), cfg.stream = (cudaStream_t)cuda_stream;
-  cfg.attrs = &attr, cfg.numAttrs = 1;
-  if (a->dtype == GPT_DTYPE_BF16) cudaLaunchKernelEx(&cfg, next_token_kernel<__nv_bfloat16>, *a);
-  else cudaLaunchKernelEx(&cfg, next_token_kernel<float>, *a);
-  return check_launch("gpt_next_token");
+  const dim3 grid(a->rows * blocks);
+  const cudaStream_t st = (cudaStream_t)cuda_stream;
+  if (a->dtype == GPT_DTYPE_BF16) return launch_after("gpt_next_token", next_token_kernel<__nv_bfloat16>, grid, kThreads, 0, blocks, st, *a);
+  return launch_after("gpt_next_token", next_token_kernel<float>, grid, kThreads, 0, blocks, st, *a);
 }
