@@ -14,7 +14,6 @@
 #include <cooperative_groups.h>
 
 #include <cmath>
-#include <utility>
 
 #include "decode_ops.h"
 
@@ -27,7 +26,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRange = 32768;            // ids of a range at most
 constexpr int kMarked = 2048;            // places of the compact table; a range with more marked ids ends before them
-constexpr int kBatch = 8;                // history ids of a thread at a time
+constexpr int kBatch = 16;               // history ids of a thread at a time
 constexpr int kHistory = kBatch * kThreads;
 constexpr int kNoToken = 0x7fffffff;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -69,19 +68,19 @@ __device__ __forceinline__ void load1(const __nv_bfloat16* z, float* x) { *x = _
 // Units of eight ids: unit u holds ids 8 u - shift .., the shift chosen so that
 // units of the logits lie on boundaries of their size whatever the row's address is.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 5) next_token_kernel(const __grid_constant__ gpt_next_token_args a) {
-  __shared__ uint32_t bitmap[kRange / 32];
+__global__ void __launch_bounds__(kThreads, 4) next_token_kernel(const __grid_constant__ gpt_next_token_args a) {
+  __shared__ __align__(16) uint32_t bitmap[kRange / 32];
   __shared__ uint16_t place[kRange / 32];   // marked ids before a word's
   __shared__ uint16_t where[kMarked];       // the marked id of a place, from the range's first on
-  __shared__ uint32_t seen[kMarked];        // occurrences after the prompt; 2^31: in the prompt
-  __shared__ float bias[kMarked];
+  __shared__ __align__(16) uint32_t seen[kMarked];  // occurrences after the prompt; 2^31: in the prompt
+  __shared__ __align__(16) float bias[kMarked];
   __shared__ Best warp_best[kWarps], block_best[8];
   __shared__ uint32_t scan[kWarps];
   __shared__ int fit;
   cg::cluster_group cluster = cg::this_cluster();
   after_stream();
-  auto started = cluster.barrier_arrive();  // waited for before another block's memory is written
   const int blocks = cluster.num_blocks(), part = cluster.block_rank();
+  if (blocks > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");  // waited for before another block's memory is written
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t b = blockIdx.x / blocks;
   const T* z_in = (const T*)a.logits + b * a.logits_stride;
@@ -123,6 +122,13 @@ __global__ void __launch_bounds__(kThreads, 5) next_token_kernel(const __grid_co
     }
   };
   load(u0 + tid);  // every thread's first, under way while the ids are marked
+  auto clear = [&] {
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = tid; i < kRange / 128; i += kThreads) reinterpret_cast<uint4*>(bitmap)[i] = zero;
+    for (int i = tid; i < kMarked / 4; i += kThreads) reinterpret_cast<uint4*>(seen)[i] = reinterpret_cast<uint4*>(bias)[i] = zero;
+    if (tid == 0) fit = kRange / 32;
+    __syncthreads();
+  };
 
   // The history, kBatch ids of a thread at a time.  One that fits is read once, before
   // its length is known.
@@ -137,9 +143,11 @@ __global__ void __launch_bounds__(kThreads, 5) next_token_kernel(const __grid_co
   };
   if (at_once) read_history(0, most);
   const int n_bias = bias_ids ? a.n_bias : 0;
-  int bias_id = -1;  // the first 32 entries, a lane of warp 0 each
+  int bias_id = -1;  // the first 32 entries, a lane of the last warp each
   float bias_value = 0.f;
-  if (warp == 0 && lane < n_bias) bias_id = bias_ids[lane], bias_value = a.bias_values[b * a.bias_stride + lane];
+  const bool adds = warp == kWarps - 1;
+  if (adds && lane < n_bias) bias_id = bias_ids[lane], bias_value = a.bias_values[b * a.bias_stride + lane];
+  if (hist || n_bias > 0) clear();  // (before the loads above are waited for)
   const float rep = a.repetition ? a.repetition[b] : 1.f, pres = a.presence ? a.presence[b] : 0.f;
   const float freq = a.frequency ? a.frequency[b] : 0.f;
   if (n_hist < 0 || n_hist > most) {
@@ -158,11 +166,7 @@ __global__ void __launch_bounds__(kThreads, 5) next_token_kernel(const __grid_co
     auto inside = [&](int id) { return (uint32_t)id < (uint32_t)a.vocab && (uint32_t)(id - first) < ids; };
     if (v0 > u0) load(v0 + tid);
     if (marks) {
-      for (int i = tid; i < words; i += kThreads) bitmap[i] = 0;
-      const int places = (int)min((uint64_t)kMarked, (uint64_t)n_hist + n_bias);
-      for (int i = tid; i < places; i += kThreads) seen[i] = 0, bias[i] = 0.f;
-      if (tid == 0) fit = kRange / 32;
-      __syncthreads();
+      if (v0 > u0) clear();
       auto mark = [&](int id) {
         if (inside(id)) atomicOr(&bitmap[(id - first) >> 5], 1u << ((id - first) & 31));
       };
@@ -177,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 5) next_token_kernel(const __grid_co
           if (there) mark(recent[i]);
         }
       }
-      if (warp == 0)
+      if (adds)
         for (int j = lane; j < n_bias; j += 32) {
           const int id = j < 32 ? bias_id : bias_ids[j];
           bad |= id >= a.vocab;
@@ -238,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 5) next_token_kernel(const __grid_co
             }
         }
       }
-      if (warp == 0)  // biases of one id in the order of their entries: the entry's rank among the equal ones takes turns
+      if (adds)  // biases of one id in the order of their entries: the entry's rank among the equal ones takes turns
         for (int j0 = 0; j0 < n_bias; j0 += 32) {
           if (j0 > 0) {
             bias_id = j0 + lane < n_bias ? bias_ids[j0 + lane] : -1;
@@ -252,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 5) next_token_kernel(const __grid_co
             __syncwarp();
           }
         }
-      if (warp == 0 && n_bias > 32 && v1 < u1) bias_id = bias_ids[lane], bias_value = a.bias_values[b * a.bias_stride + lane];
+      if (adds && n_bias > 32 && v1 < u1) bias_id = bias_ids[lane], bias_value = a.bias_values[b * a.bias_stride + lane];
       __syncthreads();
       // The marked ids themselves, one a thread.  The pass over the logits leaves them
       // out of the maximum and the sum, and their values are written over its own.
@@ -269,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 5) next_token_kernel(const __grid_co
         const float top = fmaxf(z, -INFINITY);  // NaN is never the maximum
         best = join(best, Best{top, top > -INFINITY ? 1.f : isnan(z) ? z : 0.f, top > -INFINITY ? id : kNoToken});
       }
-      __syncthreads();  // (in place: before anything is written)
+      if ((const void*)z_out == (const void*)z_in) __syncthreads();  // before anything is written over
     }
 
     for (int w = v0 + tid; w < v1; w += kThreads) {
@@ -318,14 +322,17 @@ __global__ void __launch_bounds__(kThreads, 5) next_token_kernel(const __grid_co
   if (bad) set_status(a.status, GPT_STATUS_BAD_TOKEN);
   if (lane == 0) warp_best[warp] = best;
   __syncthreads();
-  cluster.barrier_wait(std::move(started));
-  if (tid == 0) {
+  if (tid == 0)
     for (int w = 1; w < kWarps; ++w) best = join(best, warp_best[w]);
-    cluster.map_shared_rank(block_best, 0)[part] = best;
+  if (blocks > 1) {
+    asm volatile("barrier.cluster.wait;" ::: "memory");
+    if (tid == 0) cluster.map_shared_rank(block_best, 0)[part] = best;
+    cluster.sync();
+    if (part > 0) return;
+    if (tid == 0)
+      for (int r = 1; r < blocks; ++r) best = join(best, block_best[r]);
   }
-  cluster.sync();
-  if (part == 0 && tid == 0) {
-    for (int r = 1; r < blocks; ++r) best = join(best, block_best[r]);
+  if (tid == 0) {
     if (a.token) a.token[b] = best.id == kNoToken ? -1 : best.id;
     if (a.lse) a.lse[b] = best.m + logf(best.sum);
   }
@@ -361,13 +368,19 @@ extern "C" int gpt_next_token(const gpt_next_token_args* a, void* cuda_stream) {
     return call_error(GPT_ERR_INVALID_ARG, "bias_ids and bias_values go together");
   if ((const void*)a->out == a->logits && (a->dtype != GPT_DTYPE_FP32 || (a->rows > 1 && a->out_stride != a->logits_stride)))
     return call_error(GPT_ERR_INVALID_ARG, "in place needs fp32 logits and equal strides");
-  // Blocks of a row: a power of two such that all run at once (four an SM; clusters
-  // leave the fifth place empty here and there), for a second wave repeats the marking
-  // of ids: 200 rows of 50,304 took 23 us in clusters of 2, 29 of 4, 35 of 8; 64 rows of
-  // 131,072 42, 25 and 19 us; one row 13, 10 and 9; 100 rows of 12,288 9.6 us in
-  // clusters of 4, 11.4 of 6.  A block has 512 ids at least.
+  // Blocks of a row, a power of two of 512 ids at least each.  Up to two blocks an SM
+  // more blocks are better (one row of 50,304 13, 10 and 9 us in clusters of 2, 4 and 8);
+  // up to four, where a block keeps 8,192 ids (140 rows of 50,304 16.6 us in clusters of
+  // 4, 19.5 of 2, but 64 rows 12.0 of 8, 10.7 of 4; 70 rows of 131,072 18.3 of 8, 22.9 of
+  // 4).  Never a second wave, which repeats the marking of ids (200 rows of 50,304 23 us
+  // in clusters of 2, 29 of 4, 35 of 8; 75 rows 12.3 of 4, 16.7 of 8: larger clusters do
+  // not fill every place).
   int blocks = 1;
-  while (blocks < 8 && 2 * blocks * (int64_t)a->rows <= 608 && a->vocab / (2 * blocks) >= 512) blocks *= 2;
+  auto fits = [&](int n) {
+    const int64_t all = (int64_t)a->rows * n;
+    return n <= 8 && a->vocab / n >= 512 && (all <= 304 || (all <= (n == 2 ? 608 : 568) && a->vocab / n >= 8192));
+  };
+  while (fits(2 * blocks)) blocks *= 2;
   if ((int64_t)a->rows * blocks > INT32_MAX) return call_error(GPT_ERR_UNSUPPORTED, "too many rows");
   const dim3 grid(a->rows * blocks);
   const cudaStream_t st = (cudaStream_t)cuda_stream;
