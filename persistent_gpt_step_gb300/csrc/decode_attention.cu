@@ -35,6 +35,8 @@ Plan make_plan(const gpt_paged_cache* c, int32_t n_head) {
   const double span = ((double)(c->n_pages - 1) * c->page_stride + (double)(c->page_size - 1) * c->slot_stride +
                        (double)(c->n_kv_head - 1) * c->head_stride + c->head_dim) * es;
   pl.fast = c->page_size % 8 == 0 && span < 16.0 * 0xffffffffu;
+  pl.exact = pl.fast && c->head_dim % 64 == 0 && reinterpret_cast<uintptr_t>(c->k) % 32 == 0 && c->page_stride * es % 32 == 0 &&
+             c->slot_stride * es % 32 == 0 && c->head_stride * es % 32 == 0;
   // Teams: warps that read the same keys' neighbouring heads keep DRAM pages open
   // where a head's row is short (200 sequences of 16 heads of 64: 86 us with teams of
   // 1, 81 with 4, 82 with 8); but a row of a team is cut into that many more pieces

@@ -55,6 +55,11 @@ __device__ __forceinline__ uint4 load16(const void* p) {
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
   return u;
 }
+// Two neighbouring 16-byte pieces in one load, on a 32-byte boundary.
+__device__ __forceinline__ void load32(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w) : "l"(p));
+}
 __device__ __forceinline__ uint4 load16_if(const void* p, bool ok) {
   uint4 u = make_uint4(0u, 0u, 0u, 0u);
   if (ok) asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
@@ -165,7 +170,11 @@ struct Bf16Path {
   static constexpr int KG = 128 / DP;           // 16-key groups of a step: 32 registers of keys, 32 of values
   static constexpr int kQuery = NT * (DP / 32) * 128;  // a warp's queries: a 16-byte piece per lane, tile and 32 dims
 
-  // Lane (r, c): query head r of a tile, dims 32 i + 8 c .. + 7.
+  // Dims of a lane's piece i of a key or query: lane c has 16 of every 64, in two pieces
+  // for one load (4,096 keys of 8 heads of 128 12.6 us, with 16-byte loads 13.5).
+  static __device__ __forceinline__ int piece_dim(int i, int c) { return i / 2 * 64 + c * 16 + i % 2 * 8; }
+
+  // Lane (r, c): query head r of a tile, its pieces.
   static __device__ __forceinline__ void stage_query(const DecodeParams& p, float* mine, const Part& w) {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
 #pragma unroll
@@ -174,8 +183,8 @@ struct Bf16Path {
       for (int i = 0; i < DP / 32; ++i) {
         const int qh = kTwice ? r & 3 : t * 8 + r;
         reinterpret_cast<uint4*>(mine)[(t * (DP / 32) + i) * 32 + lane] =
-            load16_if((const T*)p.a.q + w.s * p.a.q_row + (w.hq + qh) * p.a.q_head + i * 32 + c * 8,
-                      qh < w.n && i * 32 + c * 8 < p.c.head_dim);
+            load16_if((const T*)p.a.q + w.s * p.a.q_row + (w.hq + qh) * p.a.q_head + piece_dim(i, c),
+                      qh < w.n && piece_dim(i, c) < p.c.head_dim);
       }
   }
 
@@ -184,7 +193,7 @@ struct Bf16Path {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const int d = p.c.head_dim;
     const int64_t row = p.c.slot_stride;
-    const T* kb = (const T*)p.c.k + c * 8 + (kFast ? r * row : 0);
+    const T* kb = (const T*)p.c.k + (kFast ? r * row : 0);
     const T* vb = (const T*)p.c.v + r * 8 + (kFast ? 2 * c * row : 0);
     const uint4* query = reinterpret_cast<const uint4*>(mine) + lane;
     float o[NT][DP / 64][4][4], m[NT][2], l[NT][2];
@@ -216,11 +225,13 @@ struct Bf16Path {
           if constexpr (kFast) {
             const T* at = group_at(kb, off[g][u]);
 #pragma unroll
-            for (int i = 0; i < DP / 32; ++i) kr[g][u][i] = kExact ? load16(at + i * 32) : load16_if(at + i * 32, i * 32 + c * 8 < d);
+            for (int i = 0; i < DP / 32; i += 2)
+              if constexpr (kExact) load32(at + piece_dim(i, c), kr[g][u][i], kr[g][u][i + 1]);
+              else kr[g][u][i] = load16_if(at + piece_dim(i, c), piece_dim(i, c) < d), kr[g][u][i + 1] = load16_if(at + piece_dim(i + 1, c), piece_dim(i + 1, c) < d);
           } else {
             const int64_t at = __shfl_sync(0xffffffffu, off[0][0], g * 16 + u * 8 + r);
 #pragma unroll
-            for (int i = 0; i < DP / 32; ++i) kr[g][u][i] = load16_if(kb + at + i * 32, at >= 0 && i * 32 + c * 8 < d);
+            for (int i = 0; i < DP / 32; ++i) kr[g][u][i] = load16_if(kb + at + piece_dim(i, c), at >= 0 && piece_dim(i, c) < d);
           }
     };
     stage_query(p, mine, w);
@@ -398,6 +409,11 @@ struct Fp32Path {
   static constexpr uint32_t kAll = 0xffffffffu >> (32 - kKeys);
   static constexpr int kLanes = DP / 4;          // lanes to a row of values
   static constexpr int kRows = 32 / kLanes;      // rows of values a load covers
+  // Dims of a lane's piece i of a key: in heads up to 64 lane c has 8 of every 32, in two
+  // pieces for one load; in larger ones 4 of every 16 (the wide loads' register groups
+  // spill there: 16 over 8 heads of 128, 48.7 us instead of 42.9).
+  static constexpr bool kPairs = DP == 64;
+  static __device__ __forceinline__ int piece_dim(int i, int c) { return kPairs ? i / 2 * 32 + c * 8 + i % 2 * 4 : i * 16 + c * 4; }
   static constexpr int kQuery = kHeads * DP + kKeys * kHeads;  // a warp's queries and probabilities
 
   static __device__ __forceinline__ void stage_query(const DecodeParams& p, float* mine, const Part& w) {
@@ -415,7 +431,7 @@ struct Fp32Path {
     const int d = p.c.head_dim;
     const int64_t row = p.c.slot_stride;
     const int vd = (lane % kLanes) * 4, vrow = lane / kLanes;
-    const float* kb = (const float*)p.c.k + c * 4 + (kFast ? r * row : 0);
+    const float* kb = (const float*)p.c.k + (kFast ? r * row : 0);
     const float* vb = (const float*)p.c.v + vd + (kFast ? vrow * row : 0);
     const float* sq = mine;
     float* sp = mine + kHeads * DP;  // [key][head]
@@ -441,11 +457,14 @@ struct Fp32Path {
         if constexpr (kFast) {
           const float* at = group_at(kb, off[g]);
 #pragma unroll
-          for (int i = 0; i < DP / 16; ++i) kr[g][i] = kExact ? load16(at + i * 16) : load16_if(at + i * 16, i * 16 + c * 4 < d);
+          for (int i = 0; i < DP / 16; i += 2)
+            if constexpr (kExact && kPairs) load32(at + piece_dim(i, c), kr[g][i], kr[g][i + 1]);
+            else if constexpr (kExact) kr[g][i] = load16(at + piece_dim(i, c)), kr[g][i + 1] = load16(at + piece_dim(i + 1, c));
+            else kr[g][i] = load16_if(at + piece_dim(i, c), piece_dim(i, c) < d), kr[g][i + 1] = load16_if(at + piece_dim(i + 1, c), piece_dim(i + 1, c) < d);
         } else {
           const int64_t at = __shfl_sync(0xffffffffu, off[0], g * 8 + r);
 #pragma unroll
-          for (int i = 0; i < DP / 16; ++i) kr[g][i] = load16_if(kb + at + i * 16, at >= 0 && i * 16 + c * 4 < d);
+          for (int i = 0; i < DP / 16; ++i) kr[g][i] = load16_if(kb + at + piece_dim(i, c), at >= 0 && piece_dim(i, c) < d);
         }
     };
     stage_query(p, mine, w);
@@ -484,7 +503,7 @@ struct Fp32Path {
         for (int g = 0; g < KG; ++g) z[g][i] = 0.f;
 #pragma unroll
         for (int b = 0; b < DP / 16; ++b) {
-          const float4 x = *reinterpret_cast<const float4*>(sq + i * DP + b * 16 + c * 4);
+          const float4 x = *reinterpret_cast<const float4*>(sq + i * DP + piece_dim(b, c));
 #pragma unroll
           for (int g = 0; g < KG; ++g) {
             const uint4 u = kr[g][b];
@@ -916,11 +935,11 @@ int launch(const DecodeParams& p, const Plan& pl, cudaStream_t st) {
 }
 
 // The launch for a head size of at most DP: the fast forms need pages of whole 8-key
-// groups within 64 GB, the exact one heads of exactly DP.
+// groups within 64 GB, the exact one also heads of exactly DP, keys on 32-byte boundaries.
 template <template <int, int, bool, bool> class Path, int N, int DP>
 int launch_form(const DecodeParams& p, const Plan& pl, cudaStream_t st) {
   if (!pl.fast) return launch<Path<N, DP, false, false>>(p, pl, st);
-  return p.c.head_dim == DP ? launch<Path<N, DP, true, true>>(p, pl, st) : launch<Path<N, DP, true, false>>(p, pl, st);
+  return pl.exact ? launch<Path<N, DP, true, true>>(p, pl, st) : launch<Path<N, DP, true, false>>(p, pl, st);
 }
 
 }  // namespace

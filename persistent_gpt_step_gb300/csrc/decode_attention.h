@@ -39,6 +39,7 @@ struct Plan {
   int cluster, pack;   // decode_row_kernel: blocks of a row, rows of a block (one is 1); 0: the line
   int join_heads;      // query heads of a block of the second kernel
   bool fast;           // pages of whole 8-key groups, offsets in 16 bytes within 32 bits
+  bool exact;          // fast, heads of 64 or 128, keys on 32-byte boundaries
   size_t ml_at, o_at, bytes;  // the workspace: pieces' (m, l), their o, its size
 };
 

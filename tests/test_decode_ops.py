@@ -468,6 +468,27 @@ def test_attention(cuda, kind, lens, heads, kv, dim, page, order, reach):
 
 @gpu
 @pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("offset,gap", [(1, 0), (0, 1), (1, 1), (2, 2)])
+def test_attention_cache_on_16_byte_boundaries(cuda, kind, offset, gap):
+    """Bases and strides that are odd multiples of 16 bytes."""
+    rng = _rng(kind, offset, gap)
+    e, page, heads, dim = 16 // (2 if kind == "bf16" else 4), 16, 2, 64
+    lens = [100, 33]
+    table, n_pages = _pages(rng, lens, page)
+    row = dim + gap * e
+    pools = [torch.full((offset * e + n_pages * page * heads * row,), math.nan, dtype=DT[kind], device="cuda") for _ in range(2)]
+    kc, vc = (x[offset * e:].view(n_pages, page, heads, row)[..., :dim] for x in pools)
+    parts = _fill(rng, lens, table, kc, vc, page)
+    q = _t(rng.standard_normal((2, 4, dim)), kind)
+    out, lse = B.decode_attention(q, kc, vc, _i(table), _i(lens))
+    for s, (k, v) in enumerate(parts):
+        want, wl, tol, tl = _attention(_np(q)[s], k, v, dim ** -0.5)
+        _check(out[s], want, tol + ((np.abs(want) + tol) * 2.0 ** -8 if kind == "bf16" else 0))
+        _check(lse[s], wl, tl)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
 def test_attention_strided_and_scaled(cuda, kind):
     _run_attention(_rng(kind), [70, 0, 9], 6, 2, 64, 16, kind, "gaps", scale=0.3, strided=True)
     _run_attention(_rng(kind), [70, 3], 6, 2, 64, 16, kind, scale=0.0)
