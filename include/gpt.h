@@ -309,9 +309,11 @@ int gpt_serve_end(gpt* h);
  * serving partition above decodes one sequence from a contiguous cache).  Each
  * is one call on cuda_stream that does not synchronise, allocates nothing and
  * may be captured into a CUDA graph; calls may overlap on different streams and
- * threads.  The current device is the one the pointers belong to.  Sums, softmax statistics and rotations are fp32; results are
- * bitwise repeatable.  Errors: INVALID_ARG, UNSUPPORTED, CUDA (text via
- * gpt_last_error(NULL)); nothing is launched on an error.
+ * threads.  The current device is the one the pointers belong to.  Sums,
+ * softmax statistics and rotations are fp32; results are bitwise repeatable.
+ * Outputs do not overlap inputs, but where it is said.  Errors: INVALID_ARG,
+ * UNSUPPORTED, CUDA (text via gpt_last_error(NULL)); nothing is launched on an
+ * error.
  *
  * Indices that live on the device (positions, sequence numbers, lengths, page
  * and token ids) are checked by the kernels: what they name outside its range is
@@ -331,8 +333,9 @@ int gpt_serve_end(gpt* h);
  * page*page_stride + slot*slot_stride + head*head_stride + i (elements, k and v
  * alike; any order of pages, slots and heads).  Base addresses and strides are
  * multiples of 16 bytes, strides are not negative; head_dim is a multiple of 16
- * bytes and <= 128; max_pages * page_size stays 4096 below 2^31.  Sequences may
- * share pages (table_stride 0: all of them one row of the table).
+ * bytes and <= 128, n_kv_head <= 65536; max_pages * page_size stays 4096 below
+ * 2^31.  Sequences may share pages (table_stride 0: all of them one row of the
+ * table).
  */
 typedef struct gpt_paged_cache {
   void *k, *v;               /* DEVICE, of type dtype                               */
@@ -348,18 +351,19 @@ typedef struct gpt_paged_cache {
  * (2i, 2i+1), i < rope_dims/2, of every head turn by positions[n] *
  * rope_base^(-2i/rope_dims), the rotary form of the RTX 3090 page's model
  * (gpt_config.rope); elements from rope_dims on, and the values, are copied.
- * The rotation is fp32 with an angle accurate to 2^-24 of a turn below position
- * 2^24 (2^-20 from there on); one rounding to the cache's type.
+ * The rotation is fp32 with an angle accurate to 2^-23 of a turn below position
+ * 2^24 (2^-18 from there on); one rounding to the cache's type.
  *   k, v: DEVICE [n_tokens, n_kv_head, head_dim]; q, q_out [n_tokens, n_head,
  *     head_dim], or NULL (both; n_head 0).  *_row, *_head: strides in elements
  *     (multiples of 16 bytes), so one QKV projection's output serves as all
- *     three.  q_out may be q itself with the same strides; otherwise no output
- *     overlaps an input.
+ *     three.  q_out may be q itself with the same strides.  Strides of the
+ *     cache and of q_out are at least head_dim (dimensions of one entry aside).
  *   positions: DEVICE int32 [n_tokens]; seq: DEVICE int32 [n_tokens], the
  *     sequence of each token, negative: a padding token, whose rows are neither
  *     read nor written; NULL: token n belongs to sequence n.
- *   Two tokens of one call at the same position of one sequence leave either's
- *   values there.  A token with a bad index (status) is skipped whole.
+ *   Two tokens of one call at the same place (a position of one sequence, a
+ *   shared page) leave either's values there, 16 bytes by 16 bytes.  A token with
+ *   a bad index (status) is skipped whole, its row of q_out too.
  */
 typedef struct gpt_kv_append_args {
   const void *q, *k, *v;
@@ -381,9 +385,9 @@ int gpt_kv_append(const gpt_paged_cache* cache, const gpt_kv_append_args* args, 
  * -infinity; a length past the table's reach is cut to it (status), keys on a
  * bad page count as absent (status), and so do keys whose score is -infinity.
  * Positions from lens[s] on may hold anything, NaN included.
- *   q, out: DEVICE [n_seq, n_head, head_dim] with strides as in gpt_kv_append;
- *   out does not overlap an input (nor q).  lse: DEVICE fp32 [n_seq, n_head] (natural
- *   log of the sum of exponentials of the scaled scores) or NULL.
+ *   q, out: DEVICE [n_seq, n_head, head_dim] with strides as q and q_out of
+ *   gpt_kv_append; out is not q.  lse: DEVICE fp32 [n_seq, n_head] (natural log of
+ *   the sum of exponentials of the scaled scores) or NULL.
  *   workspace: DEVICE scratch of gpt_decode_attention_workspace bytes, 16-byte
  *     aligned, for this call alone until it has run; its content does not matter.
  */
@@ -423,10 +427,11 @@ size_t gpt_decode_attention_workspace(const gpt_paged_cache* cache, int32_t n_he
  *     or, but for out, 0 (all rows read one); no alignment needed.
  *   history: DEVICE int32 [rows, max_history] (all of it is readable, whatever
  *     history_lens is); bias_ids: DEVICE int32, bias_values: DEVICE fp32 [rows,
- *     n_bias]; allowed: DEVICE uint32 [rows, ceil(vocab / 32)]; history, repetition, presence, frequency, bias_ids,
- *     allowed may be NULL: that step falls away.  history_lens NULL: max_history
- *     each; prompt_lens NULL: 0 each.  Negative bias ids are unused entries;
- *     ids >= vocab, and history ids outside [0, vocab), are skipped (status).
+ *     n_bias]; allowed: DEVICE uint32 [rows, ceil(vocab / 32)]; history,
+ *     repetition, presence, frequency, bias_ids, allowed may be NULL: that step
+ *     falls away.  history_lens NULL: max_history each; prompt_lens NULL: 0 each.
+ *     Negative bias ids are unused entries; ids >= vocab, and history ids outside
+ *     [0, vocab), are skipped (status).
  */
 typedef struct gpt_next_token_args {
   const void* logits;

@@ -12,6 +12,7 @@ int check_args(const gpt_paged_cache* c, int32_t n_head) {
   if (const int rc = check_cache(c)) return rc;
   if (n_head < 1 || n_head % c->n_kv_head)
     return call_error(GPT_ERR_INVALID_ARG, "n_head %d must be a multiple of n_kv_head %d", n_head, c->n_kv_head);
+  if (n_head > kMostHeads) return call_error(GPT_ERR_UNSUPPORTED, "n_head %d: at most %d", n_head, kMostHeads);
   return GPT_OK;
 }
 
@@ -102,7 +103,9 @@ extern "C" int gpt_decode_attention(const gpt_paged_cache* c, const gpt_decode_a
       !stride16(a->out_row, es) || !stride16(a->out_head, es))
     return call_error(GPT_ERR_INVALID_ARG, "q and out addresses and strides must be multiples of 16 bytes");
   if (a->out == a->q) return call_error(GPT_ERR_INVALID_ARG, "out must not be q");
-  if (!std::isfinite(a->scale)) return call_error(GPT_ERR_INVALID_ARG, "scale must be finite");
+  if (!apart(a->out_row, c->n_seq, c->head_dim) || !apart(a->out_head, a->n_head, c->head_dim))
+    return call_error(GPT_ERR_INVALID_ARG, "strides of out are smaller than a head");
+  if (!std::isfinite(a->scale * kLog2e)) return call_error(GPT_ERR_INVALID_ARG, "scale must be finite");
   const Plan pl = make_plan(c, a->n_head);
   if (pl.bytes && (!a->workspace || a->workspace_bytes < pl.bytes || !aligned16(a->workspace)))
     return call_error(GPT_ERR_INVALID_ARG, "workspace: %zu bytes on a 16-byte boundary", pl.bytes);

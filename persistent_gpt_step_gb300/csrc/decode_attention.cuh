@@ -16,11 +16,11 @@
 //    warp's part are finished from its registers; a row cut by part boundaries
 //    leaves (m, l, o) pieces in shared memory, which the block joins once at its
 //    end, and one cut by block boundaries pieces in the workspace, which a second
-//    kernel joins.
+//    kernel joins.  (Rows of few tiles a warp do without the line: decode_row_kernel.)
 //  - Each warp reads its keys and values from global memory straight into the
 //    operand registers of its products; no barrier until the warp's part is done.
 //    The values of a step are requested before its keys are used and the next
-//    step's keys before its values are used.
+//    step's keys before its values are used: 4 KB of each, 16 warps an SM.
 //  - bf16: 16 keys at a time through mma.m16n8k16, keys (or the 16 value dims) as
 //    the 16-row operand and up to 8 query heads as its 8 columns.  An operand's
 //    16-byte pieces serve as they are: the order of the contraction index is free
@@ -30,6 +30,9 @@
 //    output's own.
 //  - fp32: fused multiply-adds, four lanes to a key for the scores, a lane to
 //    four dims for the values.
+// Measured (HBM copy 6.7 TB/s): 64 sequences of 17 to 8,192 keys, 32 query over 8 key
+// heads of 128, bf16, 174 us (6.2 TB/s); 131,071 keys of one sequence 93 us (5.7); 200
+// sequences of 1 to 1,024 keys, 16 heads of 64, 82 us (5.1).
 #pragma once
 #include <cooperative_groups.h>
 
@@ -920,9 +923,9 @@ int launch(const DecodeParams& p, const Plan& pl, cudaStream_t st) {
   int dev = -1;
   cudaGetDevice(&dev);
   if (ready != dev) {
-    cudaFuncSetAttribute(decode_row_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowBytes);
-    cudaFuncSetAttribute(decode_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLineBytes);
-    if (const int rc = check_launch("gpt_decode_attention")) return rc;
+    cudaError_t e = cudaFuncSetAttribute(decode_row_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowBytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(decode_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLineBytes);
+    if (const int rc = check_cuda("gpt_decode_attention", e)) return rc;
     ready = dev;
   }
   if (pl.cluster) {

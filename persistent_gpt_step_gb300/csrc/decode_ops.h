@@ -22,6 +22,9 @@ inline int elem_size(int32_t dtype) { return dtype == GPT_DTYPE_BF16 ? 2 : 4; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 // A stride (elements of es bytes) that keeps 16-byte alignment and is not negative.
 inline bool stride16(int64_t s, int es) { return s >= 0 && (s * es) % 16 == 0; }
+// The strides of a written dimension of n entries keep its rows of `width` apart.
+inline bool apart(int64_t s, int64_t n, int64_t width) { return n <= 1 || s >= width; }
+constexpr int kMostHeads = 1 << 16;  // head counts and their products stay in 32 bits
 
 // GPT_OK, or the refusal of a cache that the header does not allow.
 inline int check_cache(const gpt_paged_cache* c) {
@@ -31,6 +34,7 @@ inline int check_cache(const gpt_paged_cache* c) {
   if (c->n_pages < 1 || c->page_size < 1 || c->n_seq < 0 || c->max_pages < 1 || c->n_kv_head < 1 || c->head_dim < 1)
     return call_error(GPT_ERR_INVALID_ARG, "cache sizes must be positive");
   const int es = elem_size(c->dtype);
+  if (c->n_kv_head > kMostHeads) return call_error(GPT_ERR_UNSUPPORTED, "n_kv_head %d: at most %d", c->n_kv_head, kMostHeads);
   if (c->head_dim > 128 || (c->head_dim * es) % 16)
     return call_error(GPT_ERR_UNSUPPORTED, "head_dim %d: a multiple of 16 bytes, at most 128 elements", c->head_dim);
   if ((int64_t)c->max_pages * c->page_size > INT32_MAX - 4096)  // tiles that end past the last position still count in 32 bits
@@ -45,9 +49,11 @@ inline int check_cache(const gpt_paged_cache* c) {
   return GPT_OK;
 }
 
-inline int check_launch(const char* what) {
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? GPT_OK : call_error(GPT_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(e));
+// What a CUDA call of ours returned; its error does not stay for the caller's next cudaGetLastError.
+inline int check_cuda(const char* what, cudaError_t e) {
+  if (e == cudaSuccess) return GPT_OK;
+  cudaGetLastError();
+  return call_error(GPT_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(e));
 }
 
 #ifdef __CUDACC__
@@ -65,8 +71,7 @@ inline int launch_after(const char* what, void (*kernel)(P...), dim3 grid, int t
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid, cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = st;
   cfg.attrs = attr, cfg.numAttrs = cluster ? 2 : 1;
-  cudaLaunchKernelEx(&cfg, kernel, args...);
-  return check_launch(what);
+  return check_cuda(what, cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 // Every thread's first statement, before any access to memory that another kernel
 // writes or reads.  The kernels do not let their successors in early themselves: with

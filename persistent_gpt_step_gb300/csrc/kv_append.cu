@@ -6,8 +6,10 @@
 // passed as two floats f_hi + f_lo.  p is split into a multiple of 2^16 and the
 // rest, both exact floats; fma gives what the rounded products with f_hi leave
 // over, whole turns drop out of every term exactly, and sincospi needs no further
-// range reduction.  The angle is good to 2^-24 of a turn below position 2^24
-// (2^-20 up to 2^31), where the fp32 product p base^(-2i/R) is off by 2^-25 p.
+// range reduction.  Errors in turns: f's double products 2^-49 p f, f_lo's rounding
+// 2^-50 p f, and the roundings of the sums, 2^-26 each: 2^-23 below position 2^24.
+// From there on the product p f_lo has whole turns as well: 2^-18 up to 2^31.  (The
+// fp32 product p base^(-2i/R) would be off by 2^-25 p.)
 #include <cmath>
 
 #include "decode_ops.h"
@@ -32,7 +34,6 @@ __device__ __forceinline__ void pair_angle(const AppendParams& p, int i, int pos
   const float t = part_turn(part_turn(a) + part_turn(b)) + rest;
   sincospif(2.0f * t, sn, cs);
 }
-
 
 // Bound: HBM (every element is read and written once).  One block per token, whose
 // sines and cosines are computed once for all of its heads, a pair a thread: with a
@@ -122,6 +123,7 @@ extern "C" int gpt_kv_append(const gpt_paged_cache* c, const gpt_kv_append_args*
     return call_error(GPT_ERR_INVALID_ARG, "rope_dims %d: even, from 0 to head_dim %d", a->rope_dims, c->head_dim);
   if (a->rope_dims > 0 && !(a->rope_base >= 1 && std::isfinite(a->rope_base)))
     return call_error(GPT_ERR_INVALID_ARG, "rope_base must be finite and at least 1");
+  if (a->n_head > kMostHeads) return call_error(GPT_ERR_UNSUPPORTED, "n_head %d: at most %d", a->n_head, kMostHeads);
   if (a->n_tokens == 0) return GPT_OK;
   if (c->n_seq == 0) return call_error(GPT_ERR_INVALID_ARG, "the cache has no sequences");
   if (!a->k || !a->v || !a->positions) return call_error(GPT_ERR_INVALID_ARG, "k, v and positions must be non-NULL");
@@ -135,16 +137,21 @@ extern "C" int gpt_kv_append(const gpt_paged_cache* c, const gpt_kv_append_args*
   if (a->n_head > 0 && (!aligned16(a->q) || !aligned16(a->q_out) || !stride16(a->q_row, es) || !stride16(a->q_head, es) ||
                         !stride16(a->qo_row, es) || !stride16(a->qo_head, es)))
     return call_error(GPT_ERR_INVALID_ARG, "q and q_out addresses and strides must be multiples of 16 bytes");
+  if (!apart(c->page_stride, c->n_pages, c->head_dim) || !apart(c->slot_stride, c->page_size, c->head_dim) ||
+      !apart(c->head_stride, c->n_kv_head, c->head_dim) ||
+      (a->n_head > 0 && (!apart(a->qo_row, a->n_tokens, c->head_dim) || !apart(a->qo_head, a->n_head, c->head_dim))))
+    return call_error(GPT_ERR_INVALID_ARG, "strides of the cache or q_out are smaller than a head");
   AppendParams p = {};
   p.c = *c;
   p.a = *a;
   if (a->rope_dims > 0) {
-    const double step = std::pow(a->rope_base, -2.0 / a->rope_dims);
-    double f = 1.0 / 6.283185307179586476925;  // base^(-2i/R) / 2pi
-    for (int i = 0; i < a->rope_dims / 2; ++i, f *= step) {
-      p.f_hi[i] = (float)f;
-      p.f_lo[i] = (float)(f - (double)p.f_hi[i]);
+    double f[kMaxPairs] = {1.0 / 6.283185307179586476925};  // base^(-2i/R) / 2pi, at most six products each
+    const int pairs = a->rope_dims / 2;
+    for (int n = 1; n < pairs; n *= 2) {
+      const double step = std::pow(a->rope_base, -2.0 * n / a->rope_dims);
+      for (int i = n; i < pairs && i < 2 * n; ++i) f[i] = f[i - n] * step;
     }
+    for (int i = 0; i < pairs; ++i) p.f_hi[i] = (float)f[i], p.f_lo[i] = (float)(f[i] - (double)p.f_hi[i]);
   }
   const cudaStream_t st = (cudaStream_t)cuda_stream;
   // Few tokens: more threads each, for the latency (256 tokens of 48 heads of 128: 3.8

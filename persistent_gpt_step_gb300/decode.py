@@ -4,8 +4,8 @@ gpt_next_token of the C ABI (also reached as ``binding.kv_append`` and so on).
 Every tensor's device, type, shape and strides are checked before the call; a mismatch raises
 GptError(INVALID_ARG).  Indices that live on the device are checked by the kernels and reported in
 ``status`` (int32 [1], STATUS_* bits of ``binding``, zeroed by the caller).  Calls run on ``stream`` (default:
-the current stream) without synchronising; what they return belongs to that stream.  The checks and the
-call itself are the ``_decode`` module (csrc/decode_py.cpp); if it is missing this module raises.
+the current stream) without synchronising; what they return belongs to that stream.  They have no gradients.
+The checks and the call itself are the ``_decode`` module (csrc/decode_py.cpp); if it is missing this module raises.
 """
 
 from __future__ import annotations
@@ -35,7 +35,7 @@ def kv_append(k, v, k_cache, v_cache, page_table, positions, seq=None, q=None, r
     over the first ``rope_dims`` elements of a head.
 
     With q [tokens, heads, head size] returns the rotated queries (``q_out``, which may be q, or a new
-    tensor), else None."""
+    tensor, whose rows of padding and of bad indices hold nothing), else None."""
     return _C.kv_append(k, v, k_cache, v_cache, page_table, positions, seq, q, rope_dims, rope_base, q_out, status, stream)
 
 

@@ -95,7 +95,7 @@ def test_bad_caches_are_refused(lib, change, code, word):
     (dict(rope_base=math.inf), "rope_base"), (dict(rope_base=math.nan), "rope_base"), (dict(k=None), "NULL"),
     (dict(positions=None), "NULL"), (dict(n_tokens=4), "sequences"), (dict(k_row=250), "16 bytes"),
     (dict(v=FAKE + 2), "16 bytes"), (dict(q=None), "n_head"), (dict(q_out=None), "n_head"), (dict(n_head=0), "n_head"),
-    (dict(qo_head=60), "16 bytes"), (dict(q_row=-512), "16 bytes")])
+    (dict(qo_head=60), "16 bytes"), (dict(q_row=-512), "16 bytes"), (dict(qo_row=0), "smaller"), (dict(qo_head=56), "smaller")])
 def test_append_refusals(lib, change, word):
     assert lib.gpt_kv_append(ctypes.byref(_cache()), ctypes.byref(_append(**change)), None) == -1
     assert word in lib.gpt_last_error(None).decode()
@@ -106,7 +106,8 @@ def test_append_refusals(lib, change, word):
 
 @pytest.mark.parametrize("change,word", [
     (dict(n_head=6), "multiple"), (dict(n_head=0), "multiple"), (dict(q=None), "NULL"), (dict(out=None), "NULL"),
-    (dict(lens=None), "NULL"), (dict(q=FAKE + 4), "16 bytes"), (dict(out_row=508), "16 bytes"),
+    (dict(lens=None), "NULL"), (dict(q=FAKE + 4), "16 bytes"), (dict(out_row=508), "16 bytes"), (dict(out_row=0), "smaller"),
+    (dict(out_head=0), "smaller"), (dict(scale=3e38), "scale"),
     (dict(scale=math.nan), "scale"), (dict(scale=math.inf), "scale"), (dict(out=FAKE), "q"), (dict(workspace=None), "workspace"),
     (dict(workspace=FAKE + 8), "workspace"), (dict(workspace_bytes=64), "workspace")])
 def test_attention_refusals(lib, change, word):
@@ -135,6 +136,20 @@ def test_next_token_refusals(lib, change, word):
     assert lib.gpt_next_token(ctypes.byref(_token(**change)), None) == -1
     assert word in lib.gpt_last_error(None).decode()
     assert lib.gpt_next_token(None, None) == -1
+
+
+@pytest.mark.parametrize("change", [dict(page_stride=0), dict(slot_stride=56), dict(head_stride=0)])
+def test_append_into_overlapping_slots_is_refused(lib, change):
+    assert lib.gpt_kv_append(ctypes.byref(_cache(**change)), ctypes.byref(_append()), None) == -1
+    assert "smaller" in lib.gpt_last_error(None).decode()
+
+
+def test_head_counts_beyond_32_bits_of_work_are_refused(lib):
+    heads = 1 << 17
+    assert lib.gpt_kv_append(ctypes.byref(_cache()), ctypes.byref(_append(n_head=heads)), None) == -8
+    assert lib.gpt_decode_attention(ctypes.byref(_cache()), ctypes.byref(_attend(n_head=heads)), None) == -8
+    for fn, a in ((lib.gpt_kv_append, _append()), (lib.gpt_decode_attention, _attend(n_head=heads))):
+        assert fn(ctypes.byref(_cache(n_kv_head=heads)), ctypes.byref(a), None) == -8
 
 
 def test_nothing_to_do_is_no_error(lib):
@@ -335,6 +350,23 @@ def test_append_far_positions(cuda, pos, turn):
 
 
 @gpu
+@pytest.mark.parametrize("pos,turn", [((1 << 24) - 1, 2.0 ** -23), ((1 << 31) - 4200, 2.0 ** -18)])
+@pytest.mark.parametrize("base", [1.0, 1.0003, 4.0])
+def test_append_slow_rates_at_far_positions(cuda, base, pos, turn):
+    """Rates that hardly fall off leave every pair with millions of turns: the bounds of the header hold for all of them."""
+    page, dim = 1 << 14, 128
+    rng = _rng(int(base * 1000), pos % 1000)
+    table = torch.full((1, (1 << 31) // page - 1), -1, dtype=torch.int32, device="cuda")
+    pos = min(pos, table.shape[1] * page - 1)
+    table[0, pos // page] = 0
+    kc, vc = _pool(1, page, 1, dim, "fp32", "slot", 0.0)
+    k = _t(rng.standard_normal((1, 1, dim)))
+    B.kv_append(k, k, kc, vc, table, _i([pos]), rope_dims=dim, rope_base=base)
+    want = _turned(_np(k), np.array([pos]), dim, base)
+    _check(_np(kc[0, pos % page])[None], want, _turn_tolerance(_np(k), want, dim, "fp32", turn))
+
+
+@gpu
 def test_append_in_place_queries_and_no_seq(cuda):
     rng = _rng(5)
     n, dim = 6, 64
@@ -504,6 +536,16 @@ def test_attention_every_length_near_a_split(cuda, kind, page, reach):
     """Lengths around every power of two and tile: one launch, a sequence each."""
     lens = sorted({max(0, (1 << e) + d) for e in range(0, 12) for d in (-1, 0, 1)})
     _run_attention(_rng(kind, 3), lens, 4, 2, 64, page, kind, reach=reach)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("n_seq", [19, 37, 43, 50, 60, 76, 101, 152, 153, 304, 305, 609, 913, 2433])
+def test_attention_rows_per_block(cuda, kind, n_seq):
+    """Rows from a few to many: every number of blocks to a row and of rows to a block, whole waves and one row more."""
+    rng = _rng(kind, n_seq)
+    lens = rng.integers(0, 300 if n_seq > 300 else 1200, n_seq).tolist()
+    _run_attention(rng, lens, 2, 1, 64, 16, kind)
 
 
 @gpu
