@@ -38,9 +38,9 @@ __device__ __forceinline__ void pair_angle(const AppendParams& p, int i, int pos
 // Bound: HBM (every element is read and written once).  One block per token, whose
 // sines and cosines are computed once for all of its heads, a pair a thread: with a
 // thread's own four pairs instead 32,768 tokens of 32 + 8 + 8 heads of 128 took 165 us
-// (the sincospi), without any rotation 120.  A thread has one 16-byte piece of the
-// head, and every kThreads / pieces-th row of the token's q, k and v heads, kUnroll
-// of them in flight.
+// (the sincospi), without any rotation 120; now 127, 6.3 TB/s.  A thread has one
+// 16-byte piece of the head, and every kThreads / pieces-th row of the token's q, k and
+// v heads, kUnroll of them in flight.
 template <typename T, int kThreads, int kUnroll>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kN = Piece<T>::kN;

@@ -6,6 +6,9 @@ fp32 operation, half a step of bf16 (2^-8 of the value) for the one rounding of 
 
 import ctypes
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -1123,6 +1126,48 @@ def test_given_stream(cuda):
     qo = B.kv_append(late_q[:, :2], late_q[:, :2], kc, vc, tab, _i([0, 0]), q=late_q, stream=st)
     st.synchronize()
     assert torch.equal(out, want) and torch.equal(tok, tok2) and torch.equal(qo, q)
+
+
+@gpu
+def test_default_stream_given_from_another(cuda):
+    side = torch.cuda.Stream()
+    z = _t(_rng(13).standard_normal((3, 500)))
+    want = B.next_token(z)[0]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        got = B.next_token(z, stream=torch.cuda.default_stream())[0]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+FIRST_CALLS = """
+import torch
+from persistent_gpt_step_gb300 import binding as B
+i = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+kc, vc = (torch.zeros(40, 16, 2, 64, device="cuda") for _ in range(2))
+q, k, z = (torch.randn(s, device="cuda") for s in ((2, 4, 64), (2, 2, 64), (2, 300)))
+table, pos, lens = torch.arange(40, dtype=torch.int32, device="cuda").view(2, 20), i(0, 0), i(1, 1)
+far = torch.zeros(2, 9000, dtype=torch.int32, device="cuda")  # room for so many keys that the other kernel is taken
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    B.kv_append(k, k, kc, vc, table, pos)
+    near = B.decode_attention(q, kc, vc, table, lens)[0]
+    wide = B.decode_attention(q, kc, vc, far[:, :9000], lens)[0]
+    token = B.next_token(z)[0]
+g.replay()
+torch.cuda.synchronize()
+want = k.repeat_interleave(2, 1)
+assert torch.equal(near, want) and torch.equal(wide[0], want[0]) and torch.equal(token, z.argmax(1).int())
+"""
+
+
+@gpu
+def test_first_calls_of_a_process_are_captured(cuda):
+    """No call has to run eagerly before it can be captured."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 @gpu
