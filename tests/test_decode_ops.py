@@ -1129,6 +1129,28 @@ def test_given_stream(cuda):
 
 
 @gpu
+def test_append_and_next_token_offsets_past_32_bits(cuda):
+    """Pages, token rows, logits and histories 2^31 elements and more apart."""
+    step = (1 << 31) + 64
+    rng = _rng(15)
+    kc, vc = (torch.zeros(step + 4096, dtype=torch.bfloat16, device="cuda").as_strided((2, 4, 2, 64), (step, 128, 64, 1))
+              for _ in range(2))
+    x = torch.zeros(step + 4096, dtype=torch.bfloat16, device="cuda").as_strided((2, 2, 64), (step, 64, 1))
+    x.copy_(_t(rng.standard_normal((2, 2, 64)), "bf16"))
+    B.kv_append(x, x, kc, vc, _i([[0, 1], [1, 0]]), _i([3, 1]))
+    want = torch.zeros(2, 4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    want[0, 3], want[1, 1] = x[0], x[1]
+    assert torch.equal(kc, want) and torch.equal(vc, want)
+    x = _token_inputs(rng, 2, 1000, 40, "fp32")
+    z, out = (torch.full((step + 2000,), 2.0, device="cuda").as_strided((2, 1000), (step, 1)) for _ in range(2))
+    z.copy_(_t(x["z"]))
+    hist = torch.zeros(step + 100, dtype=torch.int32, device="cuda").as_strided((2, 40), (step, 1))
+    hist.copy_(_i(x["hist"]))
+    got = B.next_token(z, history=hist, history_lens=_i(x["hl"]), repetition=_t(x["rep"]), out=out)
+    _check_next(got, _next(x["z"], hist=x["hist"], hl=x["hl"], rep=x["rep"]))
+
+
+@gpu
 def test_default_stream_given_from_another(cuda):
     side = torch.cuda.Stream()
     z = _t(_rng(13).standard_normal((3, 500)))
