@@ -81,8 +81,9 @@ __device__ __forceinline__ int seq_len(const DecodeParams& p, int s, bool report
 // 64 GB): lane i holds the offset, in 16 bytes, of group i of the next 32, one division
 // and one table entry a group; rows of a group are slot_stride apart.  Otherwise a lane
 // holds the offset, in elements, of its own key of the step, one of each a key.  Table
-// entries are read one round ahead.  kNoKey: no such key, or a bad page.
-template <bool kFast, int kKeys>
+// entries are read one round ahead.  kNoKey: no such key, or a bad page.  kLast: groups
+// past the end are the last one again instead.
+template <bool kFast, int kKeys, bool kLast = false>
 struct Walk {
   using Off = std::conditional_t<kFast, uint32_t, int64_t>;
   static constexpr Off kNoKey = (Off)-1;
@@ -98,15 +99,16 @@ struct Walk {
     next = k0 + (kFast ? lane * 8 : lane & (kKeys - 1));
     page = fetch();
   }
+  __device__ __forceinline__ int here() const { return kLast ? min(next, (end - 1) & ~7) : next; }
   __device__ __forceinline__ int fetch() const {
-    if (next >= end) return -1;
-    const int id = table[next / p.c.page_size];
+    if (!kLast && next >= end) return -1;
+    const int id = table[here() / p.c.page_size];
     if (id >= 0 && id < p.c.n_pages) return id;
     set_status(p.a.status, GPT_STATUS_BAD_PAGE);
     return -1;
   }
   __device__ __forceinline__ void turn() {
-    if constexpr (kFast) off = page < 0 ? kNoKey : page * p.page16 + (next % p.c.page_size) * p.slot16 + head;
+    if constexpr (kFast) off = page < 0 ? kNoKey : page * p.page16 + (here() % p.c.page_size) * p.slot16 + head;
     else off = page < 0 ? kNoKey : page * p.c.page_stride + (next % p.c.page_size) * p.c.slot_stride + head;
     next += kFast ? 256 : kKeys;
     page = fetch();
@@ -171,6 +173,12 @@ struct Bf16Path {
   static constexpr int kUnit = 16 * (128 / DP_), kUnitStart = DP_ == 64 ? 3 : kStart;
   static constexpr bool kTwice = kMode == 4;
   static constexpr int KG = 128 / DP;           // 16-key groups of a step: 32 registers of keys, 32 of values
+  // Heads of 65 to 127: no keys are read past the last step, and none of the pool's first
+  // slots in place of groups past the end (104 sequences of 13 to 878 keys, 8 heads of 96,
+  // 38.3 us instead of 43.8; 10 of 2,596 to 18,383, 6 over 2 heads of 80, 26.2 instead of
+  // 35.8).  Elsewhere the conditions cost more than such reads: 111 to 233 sequences of 32
+  // over 8 heads of 128 2 %, 64 of 12 heads of 32 2.5 %.
+  static constexpr bool kEdge = kFast && !kExact && DP == 128;
   static constexpr int kQuery = NT * (DP / 32) * 128;  // a warp's queries: a 16-byte piece per lane, tile and 32 dims
 
   // Dims of a lane's piece i of a key or query: lane c has 16 of every 64, in two pieces
@@ -209,8 +217,9 @@ struct Bf16Path {
         for (int i = 0; i < 16; ++i) o[t][b][i / 4][i % 4] = 0.f;
     }
     uint4 kr[KG][2][DP / 32], vr[KG][4][DP / 64];
-    Walk<kFast, 16 * KG> walk(p, w.s, w.h, k0, k1);
-    typename Walk<kFast, 16 * KG>::Off off[KG][2];  // of the step's groups of 8 (kFast); off[0][0]: of the lane's key
+    using Keys = Walk<kFast, 16 * KG, kEdge>;
+    Keys walk(p, w.s, w.h, k0, k1);
+    typename Keys::Off off[KG][2];  // of the step's groups of 8 (kFast); off[0][0]: of the lane's key
     auto advance = [&] {
       if constexpr (kFast) {
 #pragma unroll
@@ -283,7 +292,7 @@ struct Bf16Path {
             mma16816(z[g][t], kr[g][0][i].z, kr[g][1][i].z, kr[g][0][i].w, kr[g][1][i].w, q.z, q.w);
           }
         }
-      load_keys();
+      if (!kEdge || k + 16 * KG < k1) load_keys();
 #pragma unroll
       for (int g = 0; g < KG; ++g)
 #pragma unroll
@@ -527,7 +536,9 @@ struct Fp32Path {
           }
         }
       }
-      load_keys();
+      // (keys past the last step left out: 177 sequences of 32 to 52 keys, 16 heads of 128,
+      // 28.4 us instead of 29.7)
+      if (!kFast || k + kKeys < k1) load_keys();
       bool move = false;
 #pragma unroll
       for (int g = 0; g < KG; ++g) {
