@@ -18,11 +18,13 @@ namespace pgs {
 namespace {
 
 constexpr int kMaxPairs = 64;  // head_dim <= 128
+constexpr int kMaxTokens = 8;  // of a block
 
 struct AppendParams {
   gpt_paged_cache c;
   gpt_kv_append_args a;
   float f_hi[kMaxPairs], f_lo[kMaxPairs];
+  int32_t share;  // threads of a token are the block's >> share
 };
 
 __device__ __forceinline__ float part_turn(float x) { return x - rintf(x); }
@@ -35,25 +37,28 @@ __device__ __forceinline__ void pair_angle(const AppendParams& p, int i, int pos
   sincospif(2.0f * t, sn, cs);
 }
 
-// Bound: HBM (every element is read and written once).  One block per token, whose
+// Bound: HBM (every element is read and written once).  A block has one token, or up to
+// 8 where these are small, each with a part of its threads.  A token's
 // sines and cosines are computed once for all of its heads, a pair a thread: with a
 // thread's own four pairs instead 32,768 tokens of 32 + 8 + 8 heads of 128 took 165 us
 // (the sincospi), without any rotation 120; now 127, 6.3 TB/s.  A thread has one
 // 16-byte piece of the head, and every kThreads / pieces-th row of the token's q, k and
 // v heads, kUnroll of them in flight.
-template <typename T, int kThreads, int kUnroll>
+template <typename T, int kThreads, int kUnroll, bool kShared>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kN = Piece<T>::kN;
-  __shared__ __align__(16) float2 turn[kMaxPairs];  // cosine, sine
+  __shared__ __align__(16) float2 turns[kShared ? kMaxTokens : 1][kMaxPairs];  // cosine, sine
   const gpt_paged_cache& c = p.c;
   const gpt_kv_append_args& a = p.a;
   after_stream();
-  const int64_t n = blockIdx.x;
-  const int s = a.seq ? a.seq[n] : (int)n;
-  if (s < 0) return;  // padding
-  const int pos = a.positions[n];
-  const int pieces = c.head_dim / kN, groups = kThreads / pieces;
-  const int group = threadIdx.x / pieces, e = threadIdx.x % pieces * kN;
+  const int share = kShared ? p.share : 0, threads = kThreads >> share;
+  const int tid = threadIdx.x % threads, sub = threadIdx.x / threads;
+  float2* turn = turns[sub];
+  const int64_t n = ((int64_t)blockIdx.x << share) + sub;
+  const int s = kShared && n >= a.n_tokens ? -1 : a.seq ? a.seq[n] : (int)n;
+  if (!kShared && s < 0) return;
+  const int pieces = c.head_dim / kN, groups = threads / pieces;
+  const int group = tid / pieces, e = tid % pieces * kN;
   const int rows = a.n_head + 2 * c.n_kv_head;  // q heads, k heads, v heads
   uint4 u[kUnroll];
   auto load = [&](int row0) {
@@ -68,17 +73,25 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
       u[i] = __ldcs(reinterpret_cast<const uint4*>(from + e));
     }
   };
-  load(group);  // under way while the page is looked up
-  const bool bad_seq = s >= c.n_seq;
-  const bool bad_pos = pos < 0 || pos >= c.max_pages * c.page_size;
-  int page = -1;
-  if (!bad_seq && !bad_pos) page = c.page_table[s * c.table_stride + pos / c.page_size];
-  if (threadIdx.x < a.rope_dims / 2) pair_angle(p, threadIdx.x, pos, &turn[threadIdx.x].x, &turn[threadIdx.x].y);
-  if (page < 0 || page >= c.n_pages) {
-    if (threadIdx.x == 0) set_status(a.status, bad_seq ? GPT_STATUS_BAD_SEQ : bad_pos ? GPT_STATUS_BAD_POS : GPT_STATUS_BAD_PAGE);
-    return;
+  int pos = 0, page = -1;
+  if (s >= 0) {  // not padding
+    pos = a.positions[n];
+    load(group);  // under way while the page is looked up
+    const bool bad_seq = s >= c.n_seq;
+    const bool bad_pos = pos < 0 || pos >= c.max_pages * c.page_size;
+    if (!bad_seq && !bad_pos) page = c.page_table[s * c.table_stride + pos / c.page_size];
+    for (int i = tid; i < a.rope_dims / 2; i += threads) {
+      pair_angle(p, i, pos, &turn[i].x, &turn[i].y);
+      if (!kShared) break;  // at most 64 pairs
+    }
+    if (page < 0 || page >= c.n_pages) {
+      if (tid == 0) set_status(a.status, bad_seq ? GPT_STATUS_BAD_SEQ : bad_pos ? GPT_STATUS_BAD_POS : GPT_STATUS_BAD_PAGE);
+      page = -1;
+      if (!kShared) return;
+    }
   }
   __syncthreads();
+  if (kShared && page < 0) return;
   const int64_t slot = page * c.page_stride + (pos % c.page_size) * c.slot_stride;
   for (int row0 = group; group < groups && row0 < rows; row0 += kUnroll * groups) {
     if (row0 > group) load(row0);
@@ -158,10 +171,22 @@ extern "C" int gpt_kv_append(const gpt_paged_cache* c, const gpt_kv_append_args*
   // us with 256 threads, 4.4 with 128); many: fewer, for the throughput (32,768: 129 us
   // with 128, 149 with 256).
   const bool few = a->n_tokens <= 608;
-  const dim3 grid(a->n_tokens);
-  auto launch = [&](auto few_kernel, auto many_kernel) {
-    return launch_after("gpt_kv_append", few ? few_kernel : many_kernel, grid, few ? 256 : 128, 0, 0, st, p);
+  // Small tokens: as many to a block as its threads keep in flight and as leave four
+  // blocks an SM (20,471 tokens of 2 + 1 + 1 heads of 96 8.0 us, one to a block 26; 7,880
+  // of 16 + 4 + 4 of 32 5.1 and 11.4; 16,384 of 12 + 12 + 12 of 64 31.6 and 36.8; with
+  // half as many in flight 43).  Its own kernel, for the registers: with a variable share
+  // the large tokens above take 136 us.
+  const int pieces = c->head_dim * es / 16, work = (a->n_head + 2 * c->n_kv_head) * pieces;
+  p.share = 0;
+  while (!few && (1 << p.share) < kMaxTokens && (work << (p.share + 1)) <= 128 * 6 && (128 >> (p.share + 1)) >= pieces &&
+         (a->n_tokens >> (p.share + 1)) >= 608)
+    ++p.share;
+  const dim3 grid((unsigned)(((int64_t)a->n_tokens + (1 << p.share) - 1) >> p.share));
+  auto launch = [&](auto few_kernel, auto many_kernel, auto shared_kernel) {
+    return launch_after("gpt_kv_append", few ? few_kernel : p.share ? shared_kernel : many_kernel, grid, few ? 256 : 128, 0, 0, st, p);
   };
-  if (c->dtype == GPT_DTYPE_BF16) return launch(kv_append_kernel<__nv_bfloat16, 256, 3>, kv_append_kernel<__nv_bfloat16, 128, 6>);
-  return launch(kv_append_kernel<float, 256, 3>, kv_append_kernel<float, 128, 6>);
+  if (c->dtype == GPT_DTYPE_BF16)
+    return launch(kv_append_kernel<__nv_bfloat16, 256, 3, false>, kv_append_kernel<__nv_bfloat16, 128, 6, false>,
+                  kv_append_kernel<__nv_bfloat16, 128, 6, true>);
+  return launch(kv_append_kernel<float, 256, 3, false>, kv_append_kernel<float, 128, 6, false>, kv_append_kernel<float, 128, 6, true>);
 }

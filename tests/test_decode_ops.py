@@ -281,7 +281,10 @@ def _check(got, want, tol):
 APPENDS = [  # tokens, heads, kv heads, dim, rope, page, order of the cache
     (1, 8, 8, 64, 64, 16, "slot"), (1, 1, 1, 8, 2, 1, "slot"), (37, 12, 4, 64, 32, 24, "head"),
     (130, 4, 4, 128, 128, 16, "gaps"), (65, 14, 2, 96, 24, 7, "slot"), (9, 0, 3, 80, 80, 64, "head"),
-    (33, 32, 1, 128, 0, 16, "slot"), (515, 6, 6, 16, 10, 33, "head")]
+    (33, 32, 1, 128, 0, 16, "slot"), (515, 6, 6, 16, 10, 33, "head"),
+    # more tokens than blocks run at once: of many heads one, of few heads two to eight in a block
+    (611, 12, 12, 64, 64, 16, "slot"), (1301, 8, 4, 64, 48, 16, "gaps"), (2437, 4, 1, 80, 80, 24, "slot"),
+    (4869, 2, 1, 96, 6, 7, "head"), (4871, 0, 1, 8, 8, 16, "slot")]
 
 
 @gpu
@@ -415,6 +418,34 @@ def test_append_bad_indices_are_skipped_and_reported(cuda, what, bit):
     assert bool((qo[1] == 4.0).all()) and torch.equal(qo[[0, 2, 3]], q[[0, 2, 3]])
     B.kv_append(k, v, kc, vc, _i(table), _i(pos), seq=_i(seq))  # without a status word
     assert torch.equal(vc, want)
+
+
+@gpu
+def test_append_bad_tokens_beside_others_in_a_block(cuda):
+    """Every way to be bad or padding, next to good tokens: those are written, nothing else is."""
+    rng = _rng(16)
+    n, dim, page = 5001, 32, 8
+    lens = np.full(10, 600)
+    table, n_pages = _pages(rng, lens, page)
+    seq, pos = np.arange(n) % 10, np.arange(n) // 10
+    kinds = rng.integers(0, 8, n)
+    bad_seq, bad_pos = seq.copy(), pos.copy()
+    bad_seq[kinds == 0], bad_seq[kinds == 1] = -5, 10
+    bad_pos[kinds == 2], bad_pos[kinds == 3] = -1, 10 ** 9
+    table[3, 7] = n_pages
+    good = (kinds > 3) & ~((seq == 3) & (pos // page == 7))
+    kc, vc = _pool(n_pages, page, 1, dim, "bf16", "slot", 9.0)
+    q, k, v = (_t(rng.standard_normal((n, 1, dim)), "bf16") for _ in range(3))
+    qo = torch.full_like(q, 4.0)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.kv_append(k, v, kc, vc, _i(table), _i(bad_pos), seq=_i(bad_seq), q=q, rope_dims=0, q_out=qo, status=status)
+    assert int(status) == 7
+    for pool, x in ((kc, k), (vc, v)):
+        want = torch.full_like(pool, 9.0)
+        want[_i(table[seq[good], pos[good] // page]).long(), _i(pos[good] % page).long()] = x[torch.from_numpy(good).cuda()]
+        assert torch.equal(pool, want)
+    want = torch.where(torch.from_numpy(good).cuda()[:, None, None], q, torch.full_like(q, 4.0))
+    assert torch.equal(qo, want)
 
 
 # ----------------------------------------------------------------- decode_attention
