@@ -10,7 +10,7 @@
 // and writes them over what the pass over the logits left: that pass looks at one
 // byte of the bitmap per eight ids and has no branch for them.  (With the penalties,
 // or only separate stores, inside the pass 512 rows of 131,072 logits and 2,048 tokens
-// took 150 us: nearly every warp has a marked id among its 256; now 119, 4.6 TB/s.)
+// took 150 us: nearly every warp has a marked id among its 256; now 113, 4.9 TB/s.)
 #include <cooperative_groups.h>
 
 #include <cmath>
@@ -53,7 +53,7 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162f
 
 // Eight logits as loaded (fp32: on a 32-byte, bf16: on a 16-byte boundary), unpacked
 // where they are used: nothing waits for them before, nor for the mask's words after
-// them (unpacked at once 512 rows of 131,072 in bf16 118 us, now 112).
+// them (unpacked at once 512 rows of 131,072 in bf16 118 us, so 112).
 template <typename T> struct Eight;
 template <> struct Eight<float> {
   float x[8];
@@ -88,7 +88,8 @@ __device__ __forceinline__ void store8(float* z, const float* x) {
 
 // Units of eight ids: unit u holds ids 8 u - shift .., the shift chosen so that
 // units of the logits lie on boundaries of their size whatever the row's address is.
-template <typename T>
+// kAhead: a thread has its next two units under way instead of one.
+template <typename T, bool kAhead>
 __global__ void __launch_bounds__(kThreads, 4) next_token_kernel(const __grid_constant__ gpt_next_token_args a) {
   __shared__ __align__(16) uint32_t bitmap[kRange / 32];
   __shared__ uint16_t place[kRange / 32];   // marked ids before a word's
@@ -297,8 +298,7 @@ __global__ void __launch_bounds__(kThreads, 4) next_token_kernel(const __grid_co
       if ((const void*)z_out == (const void*)z_in) __syncthreads();  // before anything is written over
     }
 
-    for (int w = v0 + tid; w < v1; w += kThreads) {
-      if (w > v0 + tid) load(w, raw, m0, m1);
+    auto process = [&](int w, Eight<T>& raw, uint32_t m0, uint32_t m1) {
       const int64_t id0 = (int64_t)w * 8 - shift;
       const int i0 = (w - v0) * 8;
       const bool inside_row = inner(w);
@@ -332,6 +332,24 @@ __global__ void __launch_bounds__(kThreads, 4) next_token_kernel(const __grid_co
       const float off = isinf(best.m) ? 0.f : best.m;  // of an infinite maximum: sums of infinities, as log-sum-exp has them
 #pragma unroll
       for (int i = 0; i < 8; ++i) best.sum += exp_fast(x[i] - off);
+    };
+    if constexpr (kAhead) {
+      Eight<T> raw2;
+      uint32_t n0, n1;
+      if (v0 + tid + kThreads < v1) load(v0 + tid + kThreads, raw2, n0, n1);
+      for (int w = v0 + tid; w < v1; w += 2 * kThreads) {
+        process(w, raw, m0, m1);
+        if (w + 2 * kThreads < v1) load(w + 2 * kThreads, raw, m0, m1);
+        if (w + kThreads < v1) {
+          process(w + kThreads, raw2, n0, n1);
+          if (w + 3 * kThreads < v1) load(w + 3 * kThreads, raw2, n0, n1);
+        }
+      }
+    } else {
+      for (int w = v0 + tid; w < v1; w += kThreads) {
+        if (w > v0 + tid) load(w, raw, m0, m1);
+        process(w, raw, m0, m1);
+      }
     }
     if (marks && z_out) {
       __syncthreads();
@@ -408,6 +426,13 @@ extern "C" int gpt_next_token(const gpt_next_token_args* a, void* cuda_stream) {
   if ((int64_t)a->rows * blocks > INT32_MAX) return call_error(GPT_ERR_UNSUPPORTED, "too many rows");
   const dim3 grid(a->rows * blocks);
   const cudaStream_t st = (cudaStream_t)cuda_stream;
-  if (a->dtype == GPT_DTYPE_BF16) return launch_after("gpt_next_token", next_token_kernel<__nv_bfloat16>, grid, kThreads, 0, blocks, st, *a);
-  return launch_after("gpt_next_token", next_token_kernel<float>, grid, kThreads, 0, blocks, st, *a);
+  // Two units under way where a thread has eight or more (512 rows of 131,072 112.8 us and
+  // 118.8, in bf16 106 and 112; 198 of 102,855 in bf16 38.0 and 40.5); below, the registers
+  // it costs weigh more (64 rows of 50,304 in clusters of 4 11.7 and 11.4).
+  const bool ahead = a->vocab / blocks >= 8 * 8 * kThreads;
+  auto launch = [&](auto kernel, auto ahead_kernel) {
+    return launch_after("gpt_next_token", ahead ? ahead_kernel : kernel, grid, kThreads, 0, blocks, st, *a);
+  };
+  if (a->dtype == GPT_DTYPE_BF16) return launch(next_token_kernel<__nv_bfloat16, false>, next_token_kernel<__nv_bfloat16, true>);
+  return launch(next_token_kernel<float, false>, next_token_kernel<float, true>);
 }

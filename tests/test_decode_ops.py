@@ -1160,6 +1160,22 @@ def test_given_stream(cuda):
 
 
 @gpu
+@pytest.mark.parametrize("rows,vocab,pad", [(1, 140000, 3), (305, 20011, 0)])
+def test_next_token_in_place_on_long_rows(cuda, rows, vocab, pad):
+    """Rows of several loads a thread and ranges a block, read and written over; what lies between rows stays."""
+    x = _token_inputs(_rng(rows, vocab), rows, vocab, 2500, "fp32")
+    wide = torch.full((rows, vocab + pad), 5.0, device="cuda")
+    z = wide[:, :vocab]
+    z.copy_(_t(x["z"]))
+    got = B.next_token(z, history=_i(x["hist"]), history_lens=_i(x["hl"]), prompt_lens=_i(x["pl"]), repetition=_t(x["rep"]),
+                       presence=_t(x["pres"]), frequency=_t(x["freq"]), bias_ids=_i(x["ids"]), bias_values=_t(x["vals"]),
+                       allowed=_i(x["allowed"]), out=z)
+    assert got[1] is z
+    _check_next(got, _next(**x))
+    assert bool((wide[:, vocab:] == 5.0).all())
+
+
+@gpu
 def test_append_and_next_token_offsets_past_32_bits(cuda):
     """Pages, token rows, logits and histories 2^31 elements and more apart."""
     step = (1 << 31) + 64
