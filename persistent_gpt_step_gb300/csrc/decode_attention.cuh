@@ -630,7 +630,8 @@ __global__ void __launch_bounds__(kWarps * 32, P::kBlocks) decode_kernel(const _
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n_seq = p.c.n_seq, d = p.c.head_dim;
   const int blk = blockIdx.x, blocks = gridDim.x;
   const int teams = kWarps / p.team, team = warp / p.team, hl = warp % p.team;
-  if (tid < 2 * kWarps) info[tid >> 1][tid & 1].valid = 0;
+  if (hl == 0 && lane < 2) info[team][lane].valid = 0;  // by the warp that sets it: no block barrier before the join
+  __syncwarp();
   if (tid == 0) p.meta[blk].seq = -1;
 
   // The line of work: for every row its start (as long as P::kUnitStart tiles), then its

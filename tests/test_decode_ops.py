@@ -1246,3 +1246,18 @@ def test_serve_bench_times_the_operators(cuda, name):
     got = serve_bench.decode_bench(inputs.CONFIGS[name], 3, 40, reps=2)
     assert all(v > 0 for v in got.values())
     assert set(got) == {"kv_append_us", "decode_attention_us", "next_token_us", "step_us", "cache_gb_per_s"}
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("kv,n_seq", [(1, 90), (2, 45), (4, 25), (8, 12)])
+def test_attention_short_rows_in_a_wide_table(cuda, kind, kv, n_seq):
+    """Rows of a few keys cut by the parts of the line, in teams of one, two and four warps: a warp's piece is there
+    however soon it is done, and again in every repeat of the call."""
+    def once():
+        rng = _rng(kind, kv, n_seq)
+        return _run_attention(rng, rng.integers(1, 200, n_seq).tolist(), 2 * kv, kv, 64, 16, kind, reach=400000)
+    got, lse = once()
+    for _ in range(4):
+        again, lse2 = once()
+        assert torch.equal(got, again) and torch.equal(lse, lse2)
