@@ -383,8 +383,11 @@ int gpt_kv_append(const gpt_paged_cache* cache, const gpt_kv_append_args* args, 
  * out[s, h] = softmax(scale q[s, h] . K) V with the keys and values of head
  * h / (n_head / n_kv_head).  lens[s] == 0 gives a zero row and an lse of
  * -infinity; a length past the table's reach is cut to it (status), keys on a
- * bad page count as absent (status), and so do keys whose score is -infinity.
- * Positions from lens[s] on may hold anything, NaN included.
+ * bad page count as absent (status), and so do keys whose score is -infinity,
+ * whatever their values are.  Positions from lens[s] on may hold anything, NaN
+ * included.  A value of infinity or NaN at a key that counts is in the result
+ * however small the key's weight is (such heads are computed once more, by a block
+ * each: 0.3 ms for 8,000 keys).
  *   q, out: DEVICE [n_seq, n_head, head_dim] with strides as q and q_out of
  *   gpt_kv_append; out is not q.  lse: DEVICE fp32 [n_seq, n_head] (natural log of
  *   the sum of exponentials of the scaled scores) or NULL.

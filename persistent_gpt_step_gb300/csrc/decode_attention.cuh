@@ -135,6 +135,109 @@ __device__ __forceinline__ void store_lse(const DecodeParams& p, int s, int hq, 
   if (p.a.lse) p.a.lse[(int64_t)s * p.a.n_head + hq] = total == 0.f ? -INFINITY : m * kLn2 + logf(total);
 }
 
+__device__ __forceinline__ void store4(float* to, const float* x) { *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]); }
+__device__ __forceinline__ void store4(__nv_bfloat16* to, const float* x) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+  *reinterpret_cast<uint2*>(to) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+__device__ __forceinline__ void load4(const float* from, float* x) {
+  const float4 y = *reinterpret_cast<const float4*>(from);
+  x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* from, float* x) {
+  const uint2 y = *reinterpret_cast<const uint2*>(from);
+  x[0] = __uint_as_float(y.x << 16), x[1] = __uint_as_float(y.x & 0xffff0000u);
+  x[2] = __uint_as_float(y.y << 16), x[3] = __uint_as_float(y.y & 0xffff0000u);
+}
+__device__ __forceinline__ bool finite4(const float* x) { return x[0] * 0.f + x[1] * 0.f + (x[2] * 0.f + x[3] * 0.f) == 0.f; }
+
+// Results that are not finite.  A value of infinity or NaN at a key that counts belongs in
+// the result however small the key's weight is, and one at a key with a score of -infinity
+// does not; the products make NaN of both where a weight, or the low part of one, is zero (or
+// negative) beside an infinity.  Weights of up to 2^8, and sums of many, also overflow where
+// the result does not.  So a head whose results are not all finite is computed once more by
+// a block, key by key, with weights of at most 2^-31 (whose sum over a row is at most 1).
+// 131,071 keys take 5 ms.
+constexpr int kCarefulFloats = kWarps * 130;
+__device__ __forceinline__ float scaled(float x, float f) { return x * 0.f == 0.f ? x * f : x; }
+__device__ __forceinline__ float with_value(float x, float w, float v) { return v * 0.f == 0.f ? fmaf(w, v, x) : x + v; }
+
+// Query head hq, which reads key head h, of sequence s, by all threads of a block, if what
+// is there is not finite.
+template <typename T>
+__device__ __noinline__ void careful_head(const DecodeParams& p, int s, int h, int hq, float* scratch) {
+  constexpr int kAtOnce = 16 / sizeof(T);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = p.c.head_dim, e = lane * 4, len = seq_len(p, s, false);
+  T* out = (T*)p.a.out + s * p.a.out_row + hq * p.a.out_head + e;
+  float q[4] = {0.f, 0.f, 0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
+  __syncthreads();
+  if (e < d) load4(out, o);
+  if (__all_sync(0xffffffffu, finite4(o))) return;
+  if (p.a.lse && isnan(p.a.lse[(int64_t)s * p.a.n_head + hq])) return;  // of NaN or infinite scores: everything is NaN
+  const int32_t* table = p.c.page_table + s * p.c.table_stride;
+  const T *kb = (const T*)p.c.k + h * p.c.head_stride + e, *vb = (const T*)p.c.v + h * p.c.head_stride + e;
+  if (e < d) load4((const T*)p.a.q + s * p.a.q_row + hq * p.a.q_head + e, q);
+  o[0] = o[1] = o[2] = o[3] = 0.f;
+  for (int64_t k = warp * 32; k < len; k += kWarps * 32) {
+    int64_t at = -1;  // in elements; -1: no such key, or a bad page
+    if (k + lane < len) {
+      const int id = table[(int)(k + lane) / p.c.page_size];
+      if (id >= 0 && id < p.c.n_pages) at = id * p.c.page_stride + ((int)(k + lane) % p.c.page_size) * p.c.slot_stride;
+    }
+    for (int j0 = 0; j0 < 32; j0 += kAtOnce) {
+      float x[kAtOnce][4], v[kAtOnce][4], z[kAtOnce], top = m;
+      bool there[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int64_t from = __shfl_sync(0xffffffffu, at, j0 + j);
+        there[j] = from >= 0;
+        x[j][0] = x[j][1] = x[j][2] = x[j][3] = v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0.f;
+        if (there[j] && e < d) load4(kb + from, x[j]), load4(vb + from, v[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        z[j] = fmaf(x[j][3], q[3], fmaf(x[j][2], q[2], fmaf(x[j][1], q[1], x[j][0] * q[0])));
+#pragma unroll
+        for (int y = 16; y > 0; y >>= 1) z[j] += __shfl_xor_sync(0xffffffffu, z[j], y);
+        z[j] = there[j] ? z[j] * p.scale2 : -INFINITY;
+        top = fmaxf(top, z[j]);
+      }
+      const float keep = weight(m, top);
+      m = top;
+      l *= keep;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) o[u] = scaled(o[u], keep);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        if (z[j] == -INFINITY) continue;
+        const float w = weight(z[j], m);
+        l += w;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) o[u] = with_value(o[u], w * 0x1p-31f, v[j][u]);
+      }
+    }
+  }
+  float* mine = scratch + warp * 130;
+  if (lane == 0) mine[128] = m, mine[129] = l;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) mine[lane * 4 + u] = o[u];
+  __syncthreads();
+  if (warp > 0) return;
+  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, scratch[w * 130 + 128]);
+  l = o[0] = o[1] = o[2] = o[3] = 0.f;
+  for (int w = 0; w < kWarps; ++w) {
+    const float keep = weight(scratch[w * 130 + 128], m);
+    l += scratch[w * 130 + 129] * keep;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) o[u] = with_value(o[u], keep, scratch[w * 130 + lane * 4 + u]);
+  }
+  const float inv = l == 0.f ? 0.f : 1.0f / (l * 0x1p-31f);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) o[u] = l * 0.f == 0.f ? scaled(o[u], inv) : NAN;  // NaN of NaN or infinite scores
+  if (e < d) store4(out, o);
+  if (lane == 0) store_lse(p, s, hq, m, l);
+}
+
 // A warp's part of a row: keys [k0, k1) of sequence s for key head h, query heads
 // hq .. hq + n; left: where its piece goes, or null to finish the row.
 struct Part {
@@ -615,11 +718,6 @@ struct Fp32Path {
 
 // ---- the kernels --------------------------------------------------------------
 
-__device__ __forceinline__ void store4(float* to, const float* x) { *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]); }
-__device__ __forceinline__ void store4(__nv_bfloat16* to, const float* x) {
-  *reinterpret_cast<uint2*>(to) = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
-}
-
 template <class P>
 __global__ void __launch_bounds__(kWarps * 32, P::kBlocks) decode_kernel(const __grid_constant__ DecodeParams p) {
   using T = typename P::T;
@@ -785,6 +883,16 @@ __global__ void __launch_bounds__(kWarps * 32, P::kBlocks) decode_kernel(const _
   empty_rows();
 }
 
+// The query heads of this block's rows in decode_row_kernel, once more.
+template <typename T>
+__device__ __noinline__ void careful_rows(const DecodeParams& p, float* scratch) {
+  const int64_t row0 = (int64_t)(blockIdx.x / cg::this_cluster().num_blocks()) * p.pack, all = (int64_t)p.c.n_seq * p.rows;
+  for (int i = 0; i < p.pack * p.chunk && row0 + i / p.chunk < all; ++i) {
+    const int row = (int)((row0 + i / p.chunk) % p.rows), h = row / p.chunks, hq = h * p.group + row % p.chunks * p.chunk + i % p.chunk;
+    if (hq < (h + 1) * p.group) careful_head<T>(p, (int)((row0 + i / p.chunk) / p.rows), h, hq, scratch);
+  }
+}
+
 // Few or short rows: a cluster of blocks per row, or a block for `pack` rows, the keys
 // of a row in equal parts over its warps; these are joined in shared memory, blocks
 // through each other's.  One launch, no line of work to look up, no workspace.
@@ -793,10 +901,12 @@ __global__ void __launch_bounds__(kWarps * 32, P::kBlocks) decode_row_kernel(con
   using T = typename P::T;
   constexpr int kLeft = left_floats(P::kHeads, P::DP);
   extern __shared__ __align__(16) float sm[];  // [kWarps] pieces, the block's piece, [kWarps] queries
+  __shared__ int infinite;  // a result of the block's, or in the first block of the cluster's, is not finite
   cg::cluster_group cluster = cg::this_cluster();
   const int blocks = cluster.num_blocks(), rank = cluster.block_rank();
   after_stream();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, d = p.c.head_dim;
+  if (tid == 0) infinite = 0;
   const int each = kWarps / p.pack;  // warps of a row
   const int64_t row0 = (int64_t)(blockIdx.x / blocks) * p.pack, all = (int64_t)p.c.n_seq * p.rows;
   auto part_of = [&](int64_t r) {  // sequence and heads of a row
@@ -834,6 +944,7 @@ __global__ void __launch_bounds__(kWarps * 32, P::kBlocks) decode_row_kernel(con
     for (int k = 0; k < 4; ++k) x[k] *= inv;
     store4((T*)p.a.out + w.s * p.a.out_row + (w.hq + qh) * p.a.out_head + e, x);
     if (e == 0) store_lse(p, w.s, w.hq + qh, top, sum);
+    if (!finite4(x) && sum * 0.f == 0.f) *cluster.map_shared_rank(&infinite, 0) = 1;
   };
   float top, sum, x[4];
   float* whole = sm + kWarps * kLeft;
@@ -850,24 +961,28 @@ __global__ void __launch_bounds__(kWarps * 32, P::kBlocks) decode_row_kernel(con
       store4(whole + left_o(P::kHeads) + qh * P::DP + e, x);
     }
   }
-  if (blocks == 1) return;
-  cluster.sync();
-  const Part w = part_of(row0);
-  for (int i = rank * kWarps * 32 + tid; i < w.n * (d / 4); i += blocks * kWarps * 32) {
-    const int e = i % (d / 4) * 4, qh = i / (d / 4);
-    join(qh, e, blocks, [&](int k) { return (const float*)cluster.map_shared_rank(whole, k); }, top, sum, x);
-    finish(w, qh, e, top, sum, x);
+  if (blocks == 1) {
+    __syncthreads();
+  } else {
+    cluster.sync();
+    const Part w = part_of(row0);
+    for (int i = rank * kWarps * 32 + tid; i < w.n * (d / 4); i += blocks * kWarps * 32) {
+      const int e = i % (d / 4) * 4, qh = i / (d / 4);
+      join(qh, e, blocks, [&](int k) { return (const float*)cluster.map_shared_rank(whole, k); }, top, sum, x);
+      finish(w, qh, e, top, sum, x);
+    }
+    cluster.sync();  // a block's memory stays until the others have read it
   }
-  cluster.sync();  // a block's memory stays until the others have read it
+  if (infinite) careful_rows<T>(p, sm);
 }
 
 // A row that several blocks worked on: the pieces of its blocks, joined.  Block
 // (b, y): the row begun in block b, its query heads from join_heads y on; the warps
-// share the heads and, where these are fewer, the pieces.
+// share the heads and, where these are fewer, the pieces.  The last y: look_at_heads.
 template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) decode_join_kernel(const __grid_constant__ DecodeParams p) {
+__device__ __forceinline__ void join_row(const DecodeParams& p, float* scratch) {
   __shared__ float sm_ml[kWarps][2], sm_o[kWarps][128];
-  after_stream();
+  __shared__ int again[kWarps];  // heads whose results are not finite, or -1
   const int blk = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = p.c.head_dim;
   const Meta mt = p.meta[blk];
   if (mt.seq < 0) return;
@@ -912,7 +1027,9 @@ __global__ void __launch_bounds__(kWarps * 32) decode_join_kernel(const __grid_c
     if (lane == 0) sm_ml[warp][0] = top, sm_ml[warp][1] = total;
     store4(&sm_o[warp][lane * 4], x);
     __syncthreads();
-    if (!mine || sub) return;
+  }
+  const bool ends = mine && sub == 0;
+  if (share > 1 && ends) {
     float best = top;
     for (int w = 1; w < share; ++w) best = fmaxf(best, sm_ml[warp + w][0]);
     const float keep = weight(top, best);
@@ -926,21 +1043,76 @@ __global__ void __launch_bounds__(kWarps * 32) decode_join_kernel(const __grid_c
       x[0] += y.x * f, x[1] += y.y * f, x[2] += y.z * f, x[3] += y.w * f;
     }
     top = best;
-  } else if (!mine) {
-    return;
   }
-  const int hq = (mt.row / p.chunks * p.team + g) * p.group + first + qh;
-  const float inv = total == 0.f ? 0.f : 1.0f / total;
+  int infinite = -1;
+  if (ends) {
+    const int hq = (mt.row / p.chunks * p.team + g) * p.group + first + qh;
+    const float inv = total == 0.f ? 0.f : 1.0f / total;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) x[k] *= inv;
-  if (lane * 4 < d) store4((T*)p.a.out + mt.seq * p.a.out_row + hq * p.a.out_head + lane * 4, x);
-  if (lane == 0) store_lse(p, mt.seq, hq, top, total);
+    for (int k = 0; k < 4; ++k) x[k] *= inv;
+    if (lane * 4 < d) store4((T*)p.a.out + mt.seq * p.a.out_row + hq * p.a.out_head + lane * 4, x);
+    if (lane == 0) store_lse(p, mt.seq, hq, top, total);
+    if (!__all_sync(0xffffffffu, finite4(x))) infinite = hq;
+  }
+  if (lane == 0) again[warp] = infinite;
+  if (__syncthreads_and(infinite < 0)) return;
+  for (int w = 0; w < kWarps; ++w)
+    if (again[w] >= 0) careful_head<T>(p, mt.seq, again[w] / p.group, again[w], scratch);
+}
+
+// The heads that the line kernel ended itself, looked at for results that are not finite.
+template <typename T>
+__device__ __forceinline__ void look_at_heads(const DecodeParams& p, float* scratch) {
+  constexpr int kAtOnce = 4;
+  __shared__ uint32_t found[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = p.c.head_dim, e = min(lane * 4, d - 4);
+  const int64_t heads = (int64_t)p.c.n_seq * p.a.n_head, warps = (int64_t)gridDim.x * kWarps;
+  auto sequence = [&](int64_t at) { return at >> 32 ? (int)(at / p.a.n_head) : (int)((uint32_t)at / (uint32_t)p.a.n_head); };
+  for (int64_t head0 = (int64_t)blockIdx.x * kWarps; head0 < heads; head0 += kAtOnce * warps) {
+    float x[kAtOnce][4];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int64_t at = min(head0 + warp + i * warps, heads - 1);
+      const int s = sequence(at);
+      load4((const T*)p.a.out + s * p.a.out_row + (at - (int64_t)s * p.a.n_head) * p.a.out_head + e, x[i]);
+    }
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) bits |= !finite4(x[i]) && head0 + warp + i * warps < heads ? 1u << i : 0u;
+    if (__syncthreads_and(bits == 0)) continue;
+    bits = __reduce_or_sync(0xffffffffu, bits);
+    if (lane == 0) found[warp] = bits;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w)
+      for (uint32_t b = found[w]; b; b &= b - 1) {
+        const int64_t at = head0 + w + (__ffs(b) - 1) * warps;
+        const int s = sequence(at), hq = (int)(at - (int64_t)s * p.a.n_head), h = hq / p.group;
+        bool joined = false;  // in another block, which looks at what it has written itself
+        for (int i = lane; i < gridDim.x; i += 32)
+          joined |= p.meta[i].seq == s && p.meta[i].row == h / p.team * p.chunks + hq % p.group / p.chunk;
+        if (!__any_sync(0xffffffffu, joined)) careful_head<T>(p, s, h, hq, scratch);
+      }
+    __syncthreads();
+  }
+}
+
+// Looking at the heads here takes 0.2 to 1.3 us (200 sequences of 1 to 1,024 keys, 16 heads of
+// 64, 81.8 us with it and 80.4 without; 131,071 keys 93.1 and 92.3); in the line kernel, where
+// a row ends, it takes as much, and with heads of 96 5 us (104 sequences of 13 to 878 keys, 8
+// heads, 42.7, here 38.2).
+template <typename T>
+__global__ void __launch_bounds__(kWarps * 32, 3) decode_join_kernel(const __grid_constant__ DecodeParams p) {
+  __shared__ float scratch[kCarefulFloats];
+  after_stream();
+  if (blockIdx.y + 1 < gridDim.y) join_row<T>(p, scratch);
+  else look_at_heads<T>(p, scratch);
 }
 
 template <class P>
 int launch(const DecodeParams& p, const Plan& pl, cudaStream_t st) {
   constexpr int kLeft = left_floats(P::kHeads, P::DP);
   constexpr int kRowBytes = ((kWarps + 1) * kLeft + kWarps * P::kQuery) * 4, kLineBytes = kWarps * (2 * kLeft + P::kQuery) * 4;
+  static_assert(kRowBytes >= kCarefulFloats * 4, "careful_head's scratch");
   static thread_local int ready = -1;  // device whose shared-memory limits have been raised
   int dev = -1;
   cudaGetDevice(&dev);
@@ -955,7 +1127,7 @@ int launch(const DecodeParams& p, const Plan& pl, cudaStream_t st) {
     return launch_after("gpt_decode_attention", decode_row_kernel<P>, grid, kWarps * 32, kRowBytes, pl.cluster, st, p);
   }
   if (const int rc = launch_after("gpt_decode_attention", decode_kernel<P>, dim3(pl.blocks), kWarps * 32, kLineBytes, 0, st, p)) return rc;
-  const dim3 grid(pl.blocks, (pl.team * pl.chunk + pl.join_heads - 1) / pl.join_heads);
+  const dim3 grid(pl.blocks, (pl.team * pl.chunk + pl.join_heads - 1) / pl.join_heads + 1);
   return launch_after("gpt_decode_attention (join)", decode_join_kernel<typename P::T>, grid, kWarps * 32, 0, 0, st, p);
 }
 

@@ -1261,3 +1261,101 @@ def test_attention_short_rows_in_a_wide_table(cuda, kind, kv, n_seq):
     for _ in range(4):
         again, lse2 = once()
         assert torch.equal(got, again) and torch.equal(lse, lse2)
+
+
+def _weighed(q, keys, values, scale):
+    """Definition for one sequence and values that need not be finite: keys of a score of -infinity are absent, every
+    other value belongs in the result.  (out, the largest finite |value| per head and dim, lse)."""
+    heads, dim = q.shape
+    g = heads // keys.shape[1]
+    K, V = np.repeat(keys, g, axis=1), np.repeat(values, g, axis=1)
+    out, lse = np.zeros((heads, dim)), np.full(heads, -np.inf)
+    with np.errstate(all="ignore"):
+        for h in range(heads):
+            z = (K[:, h] * q[h]).sum(axis=1) * scale
+            on = z > -np.inf
+            if not on.any():
+                continue
+            w = np.exp(z[on] - z[on].max())
+            lse[h] = z[on].max() + np.log(w.sum())
+            w = w / w.sum()
+            v = V[on, h]
+            out[h] = np.where(np.isfinite(v), w[:, None] * np.where(np.isfinite(v), v, 0), v).sum(axis=0)
+    return out, lse
+
+
+def _check_infinite(got, want, rel):
+    got = _np(got)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    ok = ~np.isnan(want)
+    assert np.array_equal(np.isinf(got) & ok, np.isinf(want) & ok) and np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
+    f = np.isfinite(want)
+    off = np.abs(got[f] - want[f]) - rel(np.where(f, want, 0))[f]
+    assert (off <= 0).all(), float(off.max())
+
+
+@gpu
+@pytest.mark.parametrize("reach", [0, 400000])
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("lens,heads,kv,dim,page", [([40, 3, 700], 4, 1, 64, 16), ([2500, 60], 8, 8, 128, 16), ([300, 9, 9], 6, 2, 96, 24),
+                                                    ([90, 5000], 12, 1, 64, 5), ([100] * 40, 4, 4, 64, 16)])
+def test_attention_values_of_infinity_and_nan(cuda, kind, reach, lens, heads, kv, dim, page):
+    """A value of infinity or NaN belongs in the result at any key that counts, however small its weight is, and in none where the
+    key's score is -infinity; the other dims and heads are what they are without it."""
+    rng = _rng(kind, dim, len(lens), heads)
+    table, n_pages = _pages(rng, lens, page, width=-(-reach // page))
+    kc, vc = _pool(n_pages, page, kv, dim, kind, "slot", math.nan)
+    parts = _fill(rng, lens, table, kc, vc, page)
+    q = _t(np.abs(rng.standard_normal((len(lens), heads, dim))) + 0.1, kind)
+
+    def put(pool, which, s, j, h, e, x):
+        pool[int(table[s, j // page]), j % page, h, e] = x
+        parts[s][which][j, h, e] = x
+    inf, nan = math.inf, math.nan
+    for s, n in enumerate(lens):
+        put(vc, 1, s, 0, 0, 3, inf)
+        put(vc, 1, s, n - 1, kv - 1, 5, -inf)
+        put(vc, 1, s, n // 2, 0, 7, nan)
+        put(vc, 1, s, n - 1, 0, 9, inf), put(vc, 1, s, 0, 0, 9, -inf)
+        if n > 30:
+            put(kc, 0, s, 11, 0, 0, -inf), put(vc, 1, s, 11, 0, 11, nan), put(vc, 1, s, 11, 0, 12, inf)  # absent
+            put(kc, 0, s, 20, 0, 1, -3000.0), put(vc, 1, s, 20, 0, 13, inf)  # a weight far below fp32
+            parts[s][0][20, 0, 1] = _np(kc[int(table[s, 20 // page]), 20 % page, 0, 1])
+    out, lse = B.decode_attention(q, kc, vc, _i(table), _i(lens))
+    for s, (k, v) in enumerate(parts):
+        want, wl = _weighed(_np(q)[s], k, v, dim ** -0.5)
+        g = heads // kv
+        spread = np.repeat(np.where(np.isfinite(v), np.abs(v), 0).max(axis=0), g, axis=0)
+        # weights as in _attention, with scores of at most 300 in size where they count: their bound there, and of the mean of the values
+        z = np.einsum("hd,nhd->hn", _np(q)[s], np.repeat(np.where(np.abs(k) < 100, np.abs(k), 0), g, axis=1)).max() * dim ** -0.5
+        dw = ((dim + 4) * U + 4 * U) * z + 2.0 ** -15 + (len(k) + 8) * U
+        _check_infinite(out[s], want, lambda w: 2 * dw * spread + (2.0 ** -8 * (np.abs(w) + 2 * dw * spread) if kind == "bf16" else 0))
+        _check(lse[s], wl, dw + 4 * U * np.abs(wl))
+
+
+@gpu
+@pytest.mark.parametrize("reach", [0, 400000])
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("lens,heads,kv", [([700, 3], 4, 1), ([6000], 2, 2), ([64] * 50, 2, 2), ([2000], 8, 1)])
+def test_attention_of_the_largest_values(cuda, kind, reach, lens, heads, kv):
+    """Values at half of the type's range: their mean is finite, whatever their sum is."""
+    rng = _rng(kind, len(lens), heads)
+    page, dim = 16, 64
+    table, n_pages = _pages(rng, lens, page, width=reach // page)
+    kc, vc = _pool(n_pages, page, kv, dim, kind, "slot", math.nan)
+    parts = _fill(rng, lens, table, kc, vc, page)
+    q = _t(rng.standard_normal((len(lens), heads, dim)), kind)
+    big = 2.0 ** 127
+    for s, n in enumerate(lens):
+        j = np.arange(n)
+        at = torch.from_numpy(table[s, j // page].astype(np.int64)).cuda(), torch.from_numpy(j % page).cuda()
+        sign = np.where(np.arange(dim) % 3 == 0, -1.0, 1.0) * np.ones((n, kv, dim))
+        sign[:, :, 1::5] = rng.integers(0, 2, (n, kv, len(range(1, dim, 5)))) * 2.0 - 1
+        vc[at] = (_t(sign) * big).to(vc.dtype)
+        parts[s][1] = sign
+    out, lse = B.decode_attention(q, kc, vc, _i(table), _i(lens))
+    assert torch.isfinite(out).all()
+    for s, (k, v) in enumerate(parts):
+        want, wl, tol, tl = _attention(_np(q)[s], k, v, dim ** -0.5)
+        _check(_np(out[s]) / big, want, tol + ((np.abs(want) + tol) * 2.0 ** -8 if kind == "bf16" else 0))
+        _check(lse[s], wl, tl + 2.0 ** -20)
