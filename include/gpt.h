@@ -356,8 +356,10 @@ typedef struct gpt_paged_cache {
  *   k, v: DEVICE [n_tokens, n_kv_head, head_dim]; q, q_out [n_tokens, n_head,
  *     head_dim], or NULL (both; n_head 0).  *_row, *_head: strides in elements
  *     (multiples of 16 bytes), so one QKV projection's output serves as all
- *     three.  q_out may be q itself with the same strides.  Strides of the
- *     cache and of q_out are at least head_dim (dimensions of one entry aside).
+ *     three.  q_out may be q itself with the same strides.  The dimensions of
+ *     the cache and of q_out lie inside one another: ordered by size, each stride
+ *     is at least what those before it take up, the first at least head_dim
+ *     (dimensions of one entry aside).
  *   positions: DEVICE int32 [n_tokens]; seq: DEVICE int32 [n_tokens], the
  *     sequence of each token, negative: a padding token, whose rows are neither
  *     read nor written; NULL: token n belongs to sequence n.

@@ -103,8 +103,8 @@ extern "C" int gpt_decode_attention(const gpt_paged_cache* c, const gpt_decode_a
       !stride16(a->out_row, es) || !stride16(a->out_head, es))
     return call_error(GPT_ERR_INVALID_ARG, "q and out addresses and strides must be multiples of 16 bytes");
   if (a->out == a->q) return call_error(GPT_ERR_INVALID_ARG, "out must not be q");
-  if (!apart(a->out_row, c->n_seq, c->head_dim) || !apart(a->out_head, a->n_head, c->head_dim))
-    return call_error(GPT_ERR_INVALID_ARG, "strides of out are smaller than a head");
+  if (!apart({{a->out_row, c->n_seq}, {a->out_head, a->n_head}}, c->head_dim))
+    return call_error(GPT_ERR_INVALID_ARG, "strides of out are smaller than a head or the dimension inside");
   if (!std::isfinite(a->scale * kLog2e)) return call_error(GPT_ERR_INVALID_ARG, "scale must be finite");
   const Plan pl = make_plan(c, a->n_head);
   if (pl.bytes && (!a->workspace || a->workspace_bytes < pl.bytes || !aligned16(a->workspace)))

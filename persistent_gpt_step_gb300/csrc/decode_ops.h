@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <initializer_list>
 #include <type_traits>
 
 #include "../../include/gpt.h"
@@ -22,8 +24,24 @@ inline int elem_size(int32_t dtype) { return dtype == GPT_DTYPE_BF16 ? 2 : 4; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 // A stride (elements of es bytes) that keeps 16-byte alignment and is not negative.
 inline bool stride16(int64_t s, int es) { return s >= 0 && (s * es) % 16 == 0; }
-// The strides of a written dimension of n entries keep its rows of `width` apart.
-inline bool apart(int64_t s, int64_t n, int64_t width) { return n <= 1 || s >= width; }
+// A written dimension: its stride and its entries.
+struct Dim { int64_t stride, n; };
+// No two indices of these dimensions of rows of `width` name one element: from the smallest
+// stride on, each is at least what the dimensions before it take up.  (Doubles: exact up to
+// 2^53 elements.)
+inline bool apart(std::initializer_list<Dim> dims, int64_t width) {
+  Dim d[3];
+  size_t n = 0;
+  for (const Dim& x : dims)
+    if (x.n > 1) d[n++] = x;
+  std::sort(d, d + n, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  double extent = (double)width;
+  for (size_t i = 0; i < n; ++i) {
+    if ((double)d[i].stride < extent) return false;
+    extent += (double)d[i].stride * (double)(d[i].n - 1);
+  }
+  return true;
+}
 constexpr int kMostHeads = 1 << 16;  // head counts and their products stay in 32 bits
 
 // GPT_OK, or the refusal of a cache that the header does not allow.

@@ -150,10 +150,12 @@ extern "C" int gpt_kv_append(const gpt_paged_cache* c, const gpt_kv_append_args*
   if (a->n_head > 0 && (!aligned16(a->q) || !aligned16(a->q_out) || !stride16(a->q_row, es) || !stride16(a->q_head, es) ||
                         !stride16(a->qo_row, es) || !stride16(a->qo_head, es)))
     return call_error(GPT_ERR_INVALID_ARG, "q and q_out addresses and strides must be multiples of 16 bytes");
-  if (!apart(c->page_stride, c->n_pages, c->head_dim) || !apart(c->slot_stride, c->page_size, c->head_dim) ||
-      !apart(c->head_stride, c->n_kv_head, c->head_dim) ||
-      (a->n_head > 0 && (!apart(a->qo_row, a->n_tokens, c->head_dim) || !apart(a->qo_head, a->n_head, c->head_dim))))
-    return call_error(GPT_ERR_INVALID_ARG, "strides of the cache or q_out are smaller than a head");
+  if (!apart({{c->page_stride, c->n_pages}, {c->slot_stride, c->page_size}, {c->head_stride, c->n_kv_head}}, c->head_dim) ||
+      (a->n_head > 0 && !apart({{a->qo_row, a->n_tokens}, {a->qo_head, a->n_head}}, c->head_dim)))
+    return call_error(GPT_ERR_INVALID_ARG, "strides of the cache or q_out are smaller than a head or the dimensions inside");
+  if (a->n_head > 0 && a->q_out == a->q &&
+      ((a->n_tokens > 1 && a->qo_row != a->q_row) || (a->n_head > 1 && a->qo_head != a->q_head)))
+    return call_error(GPT_ERR_INVALID_ARG, "q_out that is q needs its strides");
   AppendParams p = {};
   p.c = *c;
   p.a = *a;

@@ -1359,3 +1359,44 @@ def test_attention_of_the_largest_values(cuda, kind, reach, lens, heads, kv):
         want, wl, tol, tl = _attention(_np(q)[s], k, v, dim ** -0.5)
         _check(_np(out[s]) / big, want, tol + ((np.abs(want) + tol) * 2.0 ** -8 if kind == "bf16" else 0))
         _check(lse[s], wl, tl + 2.0 ** -20)
+
+
+@pytest.mark.parametrize("change", [
+    dict(page_stride=256, slot_stride=256), dict(page_stride=16 * 256 - 64), dict(slot_stride=64, head_stride=64),
+    dict(slot_stride=192), dict(head_stride=16 * 64, slot_stride=64, page_stride=4096 - 64), dict(page_stride=64, slot_stride=64 * 31, head_stride=64 * 31 * 16)])
+def test_append_into_dimensions_on_top_of_one_another_is_refused(lib, change):
+    """Strides of a head and more each, but together two indices for one address."""
+    assert lib.gpt_kv_append(ctypes.byref(_cache(**change)), ctypes.byref(_append()), None) == -1
+    assert "smaller" in lib.gpt_last_error(None).decode()
+
+
+@pytest.mark.parametrize("row,head", [(64, 64), (448, 64), (64, 128), (512, 512)])
+def test_outputs_on_top_of_one_another_are_refused(lib, row, head):
+    assert lib.gpt_kv_append(ctypes.byref(_cache()), ctypes.byref(_append(qo_row=row, qo_head=head)), None) == -1
+    assert "smaller" in lib.gpt_last_error(None).decode()
+    assert lib.gpt_decode_attention(ctypes.byref(_cache()), ctypes.byref(_attend(out_row=row, out_head=head)), None) == -1
+    assert "smaller" in lib.gpt_last_error(None).decode()
+
+
+@pytest.mark.parametrize("change", [dict(qo_row=1024), dict(qo_head=128, qo_row=1024)])
+def test_queries_in_place_with_other_strides_are_refused(lib, change):
+    args = {"q": FAKE, "q_out": FAKE, **change}
+    assert lib.gpt_kv_append(ctypes.byref(_cache()), ctypes.byref(_append(**args)), None) == -1
+    assert "strides" in lib.gpt_last_error(None).decode()
+
+
+@pytest.mark.parametrize("cache,out", [
+    (dict(page_stride=64, slot_stride=64 * 32, head_stride=64 * 32 * 16), (64, 192)),  # pages innermost; heads outermost
+    (dict(head_stride=80, slot_stride=80 * 4 - 16, page_stride=(80 * 4 - 16) * 16), (72 * 8, 72)),  # gaps, but for the last
+    (dict(page_stride=8, n_pages=1), (0, 64)), (dict(slot_stride=0, page_size=1), (512, 64))])
+def test_layouts_that_do_not_overlap_are_taken(lib, cache, out):
+    """Any order of the dimensions, gaps between them, any stride of a dimension of one entry: refused by nothing but the
+    missing device (or, where there is one, not called)."""
+    row, head = out
+    n_seq = 1 if row == 0 else 3
+    a, t = _append(q_out=FAKE + 65536, qo_row=row, qo_head=head, n_tokens=n_seq), _attend(out_row=row, out_head=head)
+    c = _cache(n_seq=n_seq, **cache)
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are not real ones")
+    assert lib.gpt_kv_append(ctypes.byref(c), ctypes.byref(a), None) == -2
+    assert lib.gpt_decode_attention(ctypes.byref(c), ctypes.byref(t), None) == -2
