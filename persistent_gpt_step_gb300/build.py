@@ -1,5 +1,6 @@
 """Builds libgpt.so in-tree with nvcc for sm_103a (one -gencode, parallel TUs), and
-_decode.so, the CPython module through which decode.py hands torch tensors to it.
+_decode.so, the CPython module through which decode.py hands torch tensors to it (where
+torch is installed: the library does not need it).
 
 Usage: python -m persistent_gpt_step_gb300.build [--force]
 """
@@ -42,11 +43,37 @@ def _deps() -> list[str]:
     return out
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(MODULE):
+def _newer_than_sources(path: str) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in _deps())
+
+
+def _torch() -> str | None:
+    """Folder of the installed torch, without importing it."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec else None
+
+
+def _built_for() -> str:
+    """What _decode.so is compiled against: the Python ABI and the torch that is installed."""
+    with open(os.path.join(_torch(), "version.py")) as f:
+        return f"{sysconfig.get_config_var('SOABI')}\n{_torch()}\n{f.read()}"
+
+
+def _stamp() -> str:
+    return os.path.join(BUILD, "_decode.built_for")
+
+
+def _module_up_to_date() -> bool:
+    if _torch() is None:
+        return True
+    if not _newer_than_sources(MODULE) or not os.path.exists(_stamp()):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(MODULE))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    with open(_stamp()) as f:
+        return f.read() == _built_for()
+
+
+def up_to_date() -> bool:
+    return _newer_than_sources(LIB) and _module_up_to_date()
 
 
 def _compile(src: str) -> tuple[str, str]:
@@ -60,7 +87,7 @@ def _compile(src: str) -> tuple[str, str]:
 
 def _module() -> None:
     """Compiles _decode.so (g++) against the installed torch's headers and libraries."""
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch = _torch()
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
@@ -72,17 +99,14 @@ def _module() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for decode_py.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, MODULE)
+    with open(_stamp(), "w") as f:
+        f.write(_built_for())
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compiles every translation unit and links libgpt.so; returns its path."""
-    if not force and up_to_date():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        module = ex.submit(_module)
+def _library(verbose: bool) -> None:
+    """Compiles every translation unit and links libgpt.so."""
+    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
         results = list(ex.map(_compile, SOURCES))
-        module.result()
     report = "\n".join(r[1] for r in results)
     with open(os.path.join(BUILD, "ptxas.txt"), "w") as f:
         f.write(report)
@@ -94,6 +118,21 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Builds what is missing or out of date (``force``: everything); returns the path of libgpt.so.
+    A module that cannot be built is reported after the library has been."""
+    library = force or not _newer_than_sources(LIB)
+    module = _torch() is not None and (force or not _module_up_to_date())
+    if library or module:
+        os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(1) as ex:
+        made = ex.submit(_module) if module else None
+        if library:
+            _library(verbose)
+        if made:
+            made.result()
     return LIB
 
 

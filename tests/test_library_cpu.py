@@ -325,3 +325,64 @@ def test_trace_window_shares_synthetic():
     assert s1["gemm"] == pytest.approx((1.0 / 4.0, 0.0))
     assert s1["adamw"] == pytest.approx((1.5 / 4.0, 0.5 / 4.0))
 
+
+
+# ----------------------------------------------------------------- build.py with stand-ins for the compilers
+
+FAKE_COMPILER = """#!/bin/sh
+case "$*" in *decode_py.cpp*) [ -n "$FAKE_GPP_FAILS" ] && { echo "no such header" >&2; exit 1; };; esac
+while [ $# -gt 0 ]; do [ "$1" = -o ] && { echo built > "$2"; exit 0; }; shift; done
+exit 1
+"""
+
+
+@pytest.fixture
+def fake_build(monkeypatch, tmp_path):
+    tools = tmp_path / "bin"
+    tools.mkdir()
+    for name in ("nvcc", "g++"):
+        (tools / name).write_text(FAKE_COMPILER)
+        (tools / name).chmod(0o755)
+    monkeypatch.setenv("PATH", f"{tools}{os.pathsep}{os.environ['PATH']}")
+    monkeypatch.setattr(build_mod, "LIB", str(tmp_path / "libgpt.so"))
+    monkeypatch.setattr(build_mod, "MODULE", str(tmp_path / "_decode.so"))
+    monkeypatch.setattr(build_mod, "BUILD", str(tmp_path / "_build"))
+    return tmp_path
+
+
+def test_build_without_torch_makes_the_library(fake_build, monkeypatch):
+    """libgpt.so needs nvcc alone; only the torch module needs torch."""
+    real = build_mod.importlib.util.find_spec
+    monkeypatch.setattr(build_mod.importlib.util, "find_spec", lambda n, *a: None if n == "torch" else real(n, *a))
+    assert build_mod.build() == build_mod.LIB and os.path.exists(build_mod.LIB)
+    assert not os.path.exists(build_mod.MODULE)
+    assert build_mod.up_to_date()
+
+
+def test_build_links_the_library_before_it_reports_a_failed_module(fake_build, monkeypatch):
+    monkeypatch.setenv("FAKE_GPP_FAILS", "1")
+    with pytest.raises(RuntimeError, match="no such header"):
+        build_mod.build()
+    assert os.path.exists(build_mod.LIB) and not os.path.exists(build_mod.MODULE)
+    assert not build_mod.up_to_date()
+
+
+def test_build_makes_the_module_again_for_another_torch(fake_build, monkeypatch, tmp_path):
+    """Found through what is installed, not through --force."""
+    torch_dir = tmp_path / "torch"
+    torch_dir.mkdir()
+    (torch_dir / "version.py").write_text("__version__ = '1'")
+    spec = type("Spec", (), {"submodule_search_locations": [str(torch_dir)]})
+    real = build_mod.importlib.util.find_spec
+    monkeypatch.setattr(build_mod.importlib.util, "find_spec", lambda n, *a: spec if n == "torch" else real(n, *a))
+    build_mod.build()
+    assert build_mod.up_to_date()
+    for p in (build_mod.LIB, build_mod.MODULE):
+        open(p, "w").write("kept")
+    build_mod.build()
+    assert open(build_mod.MODULE).read() == "kept"
+    (torch_dir / "version.py").write_text("__version__ = '2'")
+    assert not build_mod.up_to_date()
+    build_mod.build()
+    assert open(build_mod.MODULE).read() == "built\n" and open(build_mod.LIB).read() == "kept"
+    assert build_mod.up_to_date()
