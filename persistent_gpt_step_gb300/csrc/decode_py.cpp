@@ -8,6 +8,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -93,10 +94,19 @@ const at::Tensor& expect(const Place& at, const at::Tensor& t, const char* name,
   if (!t.is_cuda() || t.get_device() != at.device) refuse(name, " is on ", t.device(), ", not on cuda:", (int)at.device);
   if (t.sizes() != shape) refuse(name, " has shape ", t.sizes(), ", expected ", shape);
   if (shape.back() > 1 && t.strides().back() != 1) refuse("the last dimension of ", name, " must be contiguous");
+  if (t.requires_grad() && c10::GradMode::is_enabled())
+    refuse(name, " requires a gradient, which this operator does not have: call it under torch.no_grad()");
   return t;
 }
 const at::Tensor& expect(const Place& at, PyObject* o, const char* name, at::ScalarType type, at::IntArrayRef shape) {
   return expect(at, tensor(o, name), name, type, shape);
+}
+// A tensor that the call has written: what autograd saved of it before no longer holds.
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(PyObject* o) {
+  if (given(o)) written(THPVariable_Unpack(o));
 }
 template <typename T>
 T* data(const at::Tensor& t) { return static_cast<T*>(t.data_ptr()); }
@@ -176,6 +186,7 @@ PyObject* kv_append(PyObject*, PyObject* const* o, Py_ssize_t count) {
     refuse("q_out goes with q");
   }
   check(f_kv_append(&c, &a, at.stream));
+  written(o[2]), written(o[3]), written(o[10]), written(o[11]);
   if (!q_out.defined()) Py_RETURN_NONE;
   if (given(o[10])) { Py_INCREF(o[10]); return o[10]; }
   return THPVariable_Wrap(std::move(q_out));
@@ -210,6 +221,7 @@ PyObject* decode_attention(PyObject*, PyObject* const* o, Py_ssize_t count) {
     a.workspace = scratch.data_ptr();
   }
   check(f_decode_attention(&c, &a, at.stream));
+  written(o[6]), written(o[7]);
   PyObject* result = PyTuple_New(2);
   if (!result) throw python_error();
   if (given(o[6])) { Py_INCREF(o[6]); PyTuple_SET_ITEM(result, 0, o[6]); }
@@ -268,6 +280,7 @@ PyObject* next_token(PyObject*, PyObject* const* o, Py_ssize_t count) {
   at::Tensor token = at.empty({rows}, at::kInt), lse = at.empty({rows}, at::kFloat);
   a.token = data<int32_t>(token), a.lse = data<float>(lse);
   check(f_next_token(&a, at.stream));
+  written(o[10]), written(o[11]);
   PyObject* result = PyTuple_New(3);
   if (!result) throw python_error();
   PyTuple_SET_ITEM(result, 0, THPVariable_Wrap(std::move(token)));

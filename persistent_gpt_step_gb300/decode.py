@@ -4,7 +4,10 @@ gpt_next_token of the C ABI (also reached as ``binding.kv_append`` and so on).
 Every tensor's device, type, shape and strides are checked before the call; a mismatch raises
 GptError(INVALID_ARG).  Indices that live on the device are checked by the kernels and reported in
 ``status`` (int32 [1], STATUS_* bits of ``binding``, zeroed by the caller).  Calls run on ``stream`` (default:
-the current stream) without synchronising; what they return belongs to that stream.  They have no gradients.
+the current stream) without synchronising; what they return belongs to that stream.  Inputs are not recorded on
+it: with a stream other than their own, keep them (or call ``record_stream``) until the call has run.  They have
+no gradients: a tensor that requires one is refused while gradients are recorded, and the versions of the tensors
+that they write move as those of torch's in-place operations do.
 The checks and the call itself are the ``_decode`` module (csrc/decode_py.cpp); if it is missing this module raises.
 """
 

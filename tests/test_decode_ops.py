@@ -1400,3 +1400,53 @@ def test_layouts_that_do_not_overlap_are_taken(lib, cache, out):
         pytest.skip("the addresses are not real ones")
     assert lib.gpt_kv_append(ctypes.byref(c), ctypes.byref(a), None) == -2
     assert lib.gpt_decode_attention(ctypes.byref(c), ctypes.byref(t), None) == -2
+
+
+def _small(dtype=torch.float32):
+    z = lambda *s, t=dtype: torch.zeros(*s, dtype=t, device="cuda")  # noqa: E731
+    i32 = torch.int32
+    return dict(k=z(2, 4, 64), v=z(2, 4, 64), kc=z(8, 16, 4, 64), vc=z(8, 16, 4, 64), table=z(2, 4, t=i32) + torch.tensor([[0], [1]], dtype=i32, device="cuda"),
+                at=z(2, t=i32), q=z(2, 8, 64), out=z(2, 8, 64), logits=z(3, 50), status=z(1, t=i32))
+
+
+def _small_calls(x):
+    return [("k", lambda: B.kv_append(x["k"], x["v"], x["kc"], x["vc"], x["table"], x["at"], q=x["q"], q_out=x["out"])),
+            ("q", lambda: B.decode_attention(x["q"], x["kc"], x["vc"], x["table"], x["at"] + 1, out=x["out"])),
+            ("logits", lambda: B.next_token(x["logits"], repetition=x["rep"], out=x["z"]))]
+
+
+@gpu
+@pytest.mark.parametrize("who", ["k", "v", "kc", "vc", "q", "out", "logits", "rep", "z"])
+def test_tensors_that_require_gradients_are_refused_while_these_are_recorded(cuda, who):
+    x = {**_small(), "rep": torch.ones(3, device="cuda"), "z": torch.zeros(3, 50, device="cuda")}
+    x[who].requires_grad_()
+    refused = 0
+    for _, call in _small_calls(x):
+        with torch.no_grad():
+            call()
+        try:
+            call()
+        except B.GptError as e:
+            assert e.name == "INVALID_ARG" and "gradient" in str(e)
+            refused += 1
+    assert refused == {"kc": 2, "vc": 2, "q": 2, "out": 2}.get(who, 1)
+
+
+@gpu
+def test_written_tensors_are_new_versions(cuda):
+    """Autograd finds a tensor that it has saved and a call has written since."""
+    x = {**_small(), "rep": torch.ones(3, device="cuda"), "z": torch.zeros(3, 50, device="cuda")}
+    for names, (_, call) in zip((("kc", "vc", "out"), ("out",), ("z",)), _small_calls(x)):
+        before = {n: t._version for n, t in x.items()}
+        call()
+        assert {n for n, t in x.items() if t._version != before[n]} == set(names)
+    w = torch.ones(64, device="cuda", requires_grad=True)
+    loss = (x["kc"] * w).sum()
+    B.kv_append(x["k"], x["v"], x["kc"][2:], x["vc"][2:], x["table"], x["at"])  # a view of the same memory
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        y = _small()
+        B.kv_append(y["k"], y["v"], y["kc"], y["vc"], y["table"], y["at"], status=y["status"])
+        B.decode_attention(y["q"], y["kc"], y["vc"], y["table"], y["at"] + 1, status=y["status"])
+        B.next_token(y["logits"], status=y["status"])
