@@ -126,7 +126,7 @@ int32_t type_code(const at::Tensor& t, const char* name) {
 }
 
 int32_t to_int(int64_t x, const char* what) {
-  if (x > INT32_MAX) refuse(what, " does not fit in 32 bits");
+  if (x > INT32_MAX || x < INT32_MIN) refuse(what, " does not fit in 32 bits");
   return (int32_t)x;
 }
 
@@ -170,7 +170,9 @@ PyObject* kv_append(PyObject*, PyObject* const* o, Py_ssize_t count) {
   a.positions = data<int32_t>(expect(at, o[5], "positions", at::kInt, {n}));
   a.seq = data_or_null<int32_t>(at, o[6], "seq", at::kInt, {n});
   a.status = status_word(at, o[11]);
-  a.rope_dims = to_int(PyLong_AsLongLong(o[8]), "rope_dims");
+  const int64_t rope_dims = PyLong_AsLongLong(o[8]);
+  if (PyErr_Occurred()) throw python_error();
+  a.rope_dims = to_int(rope_dims, "rope_dims");
   a.rope_base = PyFloat_AsDouble(o[9]);
   if (PyErr_Occurred()) throw python_error();
   at::Tensor q_out;

@@ -1450,3 +1450,22 @@ def test_written_tensors_are_new_versions(cuda):
         B.kv_append(y["k"], y["v"], y["kc"], y["vc"], y["table"], y["at"], status=y["status"])
         B.decode_attention(y["q"], y["kc"], y["vc"], y["table"], y["at"] + 1, status=y["status"])
         B.next_token(y["logits"], status=y["status"])
+
+
+@gpu
+@pytest.mark.parametrize("rope", [-(1 << 32), -(1 << 33) + 2, 1 << 32, (1 << 32) + 64, -(1 << 63)])
+def test_rope_dims_past_32_bits_are_refused(cuda, rope):
+    x = _small()
+    with pytest.raises(B.GptError) as e:
+        B.kv_append(x["k"], x["v"], x["kc"], x["vc"], x["table"], x["at"], rope_dims=rope)
+    assert e.value.name == "INVALID_ARG"
+
+
+@gpu
+def test_arguments_that_are_no_numbers(cuda):
+    x = _small()
+    for kw in (dict(rope_dims="8"), dict(rope_dims=1 << 70), dict(rope_dims=8, rope_base="x"), dict(stream=3)):
+        with pytest.raises((TypeError, OverflowError, AttributeError)):
+            B.kv_append(x["k"], x["v"], x["kc"], x["vc"], x["table"], x["at"], **kw)
+    with pytest.raises(TypeError):
+        B.decode_attention(x["q"], x["kc"], x["vc"], x["table"], x["at"], scale="x")
