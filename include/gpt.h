@@ -434,7 +434,8 @@ size_t gpt_decode_attention_workspace(const gpt_paged_cache* cache, int32_t n_he
  *     history_lens is); bias_ids: DEVICE int32, bias_values: DEVICE fp32 [rows,
  *     n_bias]; allowed: DEVICE uint32 [rows, ceil(vocab / 32)]; history,
  *     repetition, presence, frequency, bias_ids, allowed may be NULL: that step
- *     falls away.  history_lens NULL: max_history each; prompt_lens NULL: 0 each.
+ *     falls away.  history_lens NULL: max_history each; prompt_lens NULL: 0 each
+ *     (negative: 0, and status; past the history: all of it is prompt).
  *     Negative bias ids are unused entries; ids >= vocab, and history ids outside
  *     [0, vocab), are skipped (status).
  */

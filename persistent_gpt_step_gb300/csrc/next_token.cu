@@ -173,9 +173,9 @@ __global__ void __launch_bounds__(kThreads, 4) next_token_kernel(const __grid_co
   if (hist || n_bias > 0) clear();  // (before the loads above are waited for)
   const float rep = a.repetition ? a.repetition[b] : 1.f, pres = a.presence ? a.presence[b] : 0.f;
   const float freq = a.frequency ? a.frequency[b] : 0.f;
-  if (n_hist < 0 || n_hist > most) {
+  if (n_hist < 0 || n_hist > most || n_prompt < 0) {  // (a prompt longer than the history: none of that counts)
     if (tid == 0) set_status(a.status, GPT_STATUS_BAD_POS);
-    n_hist = n_hist < 0 ? 0 : most;
+    n_hist = min(max(n_hist, 0), most);
   }
   const bool marks = n_hist > 0 || n_bias > 0;
   uint32_t bad = 0;

@@ -1469,3 +1469,19 @@ def test_arguments_that_are_no_numbers(cuda):
             B.kv_append(x["k"], x["v"], x["kc"], x["vc"], x["table"], x["at"], **kw)
     with pytest.raises(TypeError):
         B.decode_attention(x["q"], x["kc"], x["vc"], x["table"], x["at"], scale="x")
+
+
+@gpu
+@pytest.mark.parametrize("vocab", [60, 40000])
+def test_next_token_prompt_lengths_out_of_range(cuda, vocab):
+    """A negative prompt length is reported and counts as none; one past the history leaves nothing behind it, and is no error."""
+    x = _token_inputs(_rng(vocab), 3, vocab, 20, "fp32")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x["pl"][:] = [20, 21, 1 << 30]
+    _check_next(_run_next(x, "fp32", status=status), _next(**x))
+    assert int(status) == 0
+    x["pl"][:] = [3, -1, -(1 << 31)]
+    got = _run_next(x, "fp32", status=status)
+    x["pl"][:] = [3, 0, 0]
+    _check_next(got, _next(**x))
+    assert int(status) == B.STATUS_BAD_POS
