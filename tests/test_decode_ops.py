@@ -1485,3 +1485,55 @@ def test_next_token_prompt_lengths_out_of_range(cuda, vocab):
     x["pl"][:] = [3, 0, 0]
     _check_next(got, _next(**x))
     assert int(status) == B.STATUS_BAD_POS
+
+
+@gpu
+@pytest.mark.parametrize("reach", [0, 400000])
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("page", [16, 24, 5])
+@pytest.mark.parametrize("dim,heads", [(64, 4), (96, 10), (128, 6), (128, 34)])
+def test_attention_bad_pages_and_lengths_in_every_form(cuda, kind, reach, page, dim, heads):
+    """Bad pages at the start, inside and at the end of rows, rows of bad pages only, lengths below zero and past the
+    table: both kernels, whole-group and other pages, exact and other heads."""
+    rng = _rng(kind, reach, page, dim, heads)
+    width = max(12, reach // page)
+    lens = [5 * page + 3, 7 * page, 4 * page + 1, 3 * page, -3, 10 ** 9, 0, 6 * page - 1, 9 * page + 2, -(1 << 31)]
+    there = [n if 0 <= n < 10 ** 9 else 0 for n in lens]
+    table, n_pages = _pages(rng, [9 * page + 2] * len(lens), page, spare=2, width=width)
+    bad = np.array([-1, n_pages, 1 << 30, -(1 << 31), (1 << 31) - 1])
+    used = np.zeros((len(lens), width), dtype=bool)
+    for s, n in enumerate(there):
+        used[s, :-(-n // page)] = True
+    used[5, [0, width - 1]] = True  # of the longest: the first page and the last that the table has
+    table[5, width - 1] = table[5, 1]
+    used[0, 0] = used[1, 3] = used[2, 4] = False
+    used[3, :] = used[8, 4:7] = False
+    table = np.where(used, table, bad[rng.integers(0, len(bad), table.shape)])
+    kc, vc = _pool(n_pages, page, 2, dim, kind, "slot", math.nan)
+    keep = []
+    for s, n in enumerate(there):
+        n = width * page if s == 5 else n
+        rows = [j for i in np.nonzero(used[s])[0] for j in range(i * page, min((i + 1) * page, n))]
+        j = np.array(rows, dtype=np.int64)
+        at = torch.from_numpy(table[s, j // page].astype(np.int64)).cuda(), torch.from_numpy(j % page).cuda()
+        kv = [_t(rng.standard_normal((len(j), 2, dim)), kind) for _ in range(2)]
+        kc[at], vc[at] = kv
+        keep.append([_np(x) for x in kv])
+    q = _t(rng.standard_normal((len(lens), heads, dim)), kind)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = B.decode_attention(q, kc, vc, _i(table), _i(lens), status=status)
+    assert int(status) == B.STATUS_BAD_PAGE | B.STATUS_BAD_POS
+    for s, (k, v) in enumerate(keep):
+        want, wl, tol, tl = _attention(_np(q)[s], k, v, dim ** -0.5)
+        _check(out[s], want, tol + ((np.abs(want) + tol) * 2.0 ** -8 if kind == "bf16" else 0))
+        if len(k):
+            _check(lse[s], wl, tl)
+        else:
+            assert bool((lse[s] == -math.inf).all())
+    # each kind of fault by itself, and no status word
+    one = lambda rows, n: (B.decode_attention(q[rows], kc, vc, _i(table[rows]), _i(n), status=status.zero_())[0], int(status))  # noqa: E731
+    assert one([7], [-1])[1] == B.STATUS_BAD_POS and one([0], [1])[1] == B.STATUS_BAD_PAGE
+    got, bits = one([7], [6 * page - 1])
+    assert bits == 0 and torch.equal(got[0], B.decode_attention(q[7:8], kc, vc, _i(table[7:8]), _i([6 * page - 1]))[0][0])
+    again = B.decode_attention(q, kc, vc, _i(table), _i(lens))
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
