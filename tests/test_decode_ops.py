@@ -1537,3 +1537,27 @@ def test_attention_bad_pages_and_lengths_in_every_form(cuda, kind, reach, page, 
     assert bits == 0 and torch.equal(got[0], B.decode_attention(q[7:8], kc, vc, _i(table[7:8]), _i([6 * page - 1]))[0][0])
     again = B.decode_attention(q, kc, vc, _i(table), _i(lens))
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@gpu
+@pytest.mark.parametrize("reach", [0, 400000])
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("lens,heads,kv", [([700, 3], 4, 2), ([5000], 4, 4), ([64] * 50, 2, 2)])
+def test_attention_scores_that_are_no_numbers(cuda, kind, reach, lens, heads, kv):
+    """A key of NaN, or a score of +infinity, makes its head NaN, lse too; the other heads and sequences do not see it."""
+    rng = _rng(kind, reach, len(lens), heads)
+    table, n_pages = _pages(rng, lens, 16, width=reach // 16)
+    kc, vc = _pool(n_pages, 16, kv, 64, kind, "slot", math.nan)
+    parts = _fill(rng, lens, table, kc, vc, 16)
+    q = _t(np.abs(rng.standard_normal((len(lens), heads, 64))) + 0.1, kind)
+    clean = B.decode_attention(q, kc, vc, _i(table), _i(lens))
+    j = lens[0] // 2
+    kc[int(table[0, j // 16]), j % 16, 0, 3] = math.nan
+    last = lens[-1] - 1
+    kc[int(table[-1, last // 16]), last % 16, kv - 1, 5] = math.inf
+    out, lse = B.decode_attention(q, kc, vc, _i(table), _i(lens))
+    gone = torch.zeros(len(lens), heads, dtype=torch.bool, device="cuda")
+    gone[0, :heads // kv] = True
+    gone[-1, heads - heads // kv:] = True
+    assert torch.equal(torch.isnan(lse), gone) and torch.equal(torch.isnan(out).all(-1), gone) and torch.equal(torch.isnan(out).any(-1), gone)
+    assert torch.equal(out[~gone], clean[0][~gone]) and torch.equal(lse[~gone], clean[1][~gone])
