@@ -271,9 +271,10 @@ struct Bf16Path {
   using T = __nv_bfloat16;
   static constexpr int NT = kMode == 16 ? 2 : 1, DP = DP_, kHeads = kMode;
   static constexpr int kBlocks = kMode == 16 ? 1 : 2;  // of an SM
-  // A unit of the line is a step (in tiles of 16 where a step is 32 keys: 38.2 instead
-  // of 36.6 us for 256 sequences of 1 to 256 keys).
-  static constexpr int kUnit = 16 * (128 / DP_), kUnitStart = DP_ == 64 ? 3 : kStart;
+  // A unit of the line is a step, of 32 keys in heads up to 64, where a row's start counts
+  // as one of them (200 sequences of 1 to 1,024 keys, 16 heads of 64: 87.4 us with 0, 80.2
+  // with 1, 81.7 with 2, 83.2 with 3, 87.9 with 6).
+  static constexpr int kUnit = 16 * (128 / DP_), kUnitStart = DP_ == 64 ? 1 : kStart;
   static constexpr bool kTwice = kMode == 4;
   static constexpr int KG = 128 / DP;           // 16-key groups of a step: 32 registers of keys, 32 of values
   // Heads of 65 to 127: no keys are read past the last step, and none of the pool's first

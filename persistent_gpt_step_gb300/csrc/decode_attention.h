@@ -8,10 +8,12 @@ namespace pgs {
 constexpr int kWarps = 8;      // of a block
 constexpr int kTile = 16;      // keys of a unit of work
 // What the start of a row costs a warp, in tiles (the first loads' latencies and the
-// row's end): without it warps with many short rows end last.  200 sequences of 1 to
-// 1,024 keys, 16 heads of 64: 91 us with 0, 85 with 2, 82 with 4, 85 with 8; 256 of 1
-// to 256 keys: 44, 36, 35, 34.
-constexpr int kStart = 4;
+// row's end): without it warps with many short rows end last.  In tables of 8,192
+// positions, 200 sequences of 1 to 512 keys, 8 heads of 128 in fp32: 75.1 us with 0, 73.3
+// with 1, 73.2 with 2, 74.3 with 4, 75.6 with 8; 256 of 1 to 256 keys, 8 over 4 heads of
+// 128 in bf16: 27.5, 24.1, 24.5, 25.9, 27.1; 16 of 500 to 4,000, 32 over 4 heads of 128 in
+// fp32: 43.6, 41.4, 39.3, 39.6, 39.3.
+constexpr int kStart = 2;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Meta { int32_t seq, row, last, pad; };  // a row begun in this block and ended in block `last`
