@@ -336,6 +336,13 @@ int gpt_serve_end(gpt* h);
  * bytes and <= 128, n_kv_head <= 65536; max_pages * page_size stays 4096 below
  * 2^31.  Sequences may share pages (table_stride 0: all of them one row of the
  * table).
+ *
+ * The attention's kernel is chosen by what the table can name, max_pages *
+ * page_size, so that a captured call holds for any lengths.  Where all sequences
+ * are known to be shorter, a smaller max_pages with the same table_stride (a view
+ * of the table's first columns) is faster: one sequence of 513 keys, 12 heads of
+ * 64, 6.8 us, in a table of 65,536 positions 9.8; 256 of 1 to 256 keys, 8 over 4
+ * heads of 128, 22.2 and 24.5; 200 of 1 to 1,024, 16 heads of 64, the same.
  */
 typedef struct gpt_paged_cache {
   void *k, *v;               /* DEVICE, of type dtype                               */

@@ -49,7 +49,7 @@ Plan make_plan(const gpt_paged_cache* c, int32_t n_head) {
   while (pl.team < 4 && c->n_kv_head % (2 * pl.team) == 0 && used * 2 * pl.team <= 16 * rows) pl.team *= 2;
   // Rows of few tiles a warp take decode_row_kernel: no line to look up, no second
   // kernel.  Up to a block per row at once: a cluster of blocks for each (one sequence
-  // of 513 keys, 12 heads of 64 in fp32 6.3 us, the line and its join 10.2; 4,096 keys
+  // of 513 keys, 12 heads of 64 in fp32 6.8 us, the line and its join 9.8; 4,096 keys
   // of 8 heads of 128 11.8 and 19.4; 304 rows of 2,048 keys of 64 33 and 38), but a few
   // rows in clusters of 8 leave half the GPU idle (16,000 keys of 8 heads of 128 33.7
   // and 25.0).  More rows: as many to a block as all run at once, down to a warp for a

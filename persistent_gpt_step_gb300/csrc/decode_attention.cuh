@@ -31,8 +31,8 @@
 //  - fp32: fused multiply-adds, four lanes to a key for the scores, a lane to
 //    four dims for the values.
 // Measured (HBM copy 6.7 TB/s): 64 sequences of 17 to 8,192 keys, 32 query over 8 key
-// heads of 128, bf16, 174 us (6.2 TB/s); 131,071 keys of one sequence 93 us (5.7); 200
-// sequences of 1 to 1,024 keys, 16 heads of 64, 82 us (5.1).
+// heads of 128, bf16, 175 us (6.1 TB/s); 131,071 keys of one sequence 94 us (5.7); 200
+// sequences of 1 to 1,024 keys, 16 heads of 64, 80 us (5.2).
 #pragma once
 #include <cooperative_groups.h>
 

@@ -171,7 +171,7 @@ extern "C" int gpt_kv_append(const gpt_paged_cache* c, const gpt_kv_append_args*
   const cudaStream_t st = (cudaStream_t)cuda_stream;
   // Few tokens: more threads each, for the latency (256 tokens of 48 heads of 128: 3.8
   // us with 256 threads, 4.4 with 128); many: fewer, for the throughput (32,768: 129 us
-  // with 128, 149 with 256).
+  // with 128, 149 with 256).  608: four blocks on each of the GPU's 152 SMs, here and below.
   const bool few = a->n_tokens <= 608;
   // Small tokens: as many to a block as its threads keep in flight and as leave four
   // blocks an SM (20,471 tokens of 2 + 1 + 1 heads of 96 8.0 us, one to a block 26; 7,880

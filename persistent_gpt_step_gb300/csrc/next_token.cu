@@ -410,11 +410,11 @@ extern "C" int gpt_next_token(const gpt_next_token_args* a, void* cuda_stream) {
     return call_error(GPT_ERR_INVALID_ARG, "bias_ids and bias_values go together");
   if ((const void*)a->out == a->logits && (a->dtype != GPT_DTYPE_FP32 || (a->rows > 1 && a->out_stride != a->logits_stride)))
     return call_error(GPT_ERR_INVALID_ARG, "in place needs fp32 logits and equal strides");
-  // Blocks of a row, a power of two of 512 ids at least each.  Up to two blocks an SM
-  // more blocks are better (one row of 50,304 13, 10 and 9 us in clusters of 2, 4 and 8);
-  // up to four, where a block keeps 8,192 ids (140 rows of 50,304 16.6 us in clusters of
-  // 4, 19.5 of 2, but 64 rows 12.0 of 8, 10.7 of 4; 70 rows of 131,072 18.3 of 8, 22.9 of
-  // 4).  Never a second wave, which repeats the marking of ids (200 rows of 50,304 23 us
+  // Blocks of a row, a power of two of 512 ids at least each.  Up to two blocks an SM (304
+  // on 152 SMs) more blocks are better (one row of 50,304 13, 10 and 9 us in clusters of 2,
+  // 4 and 8); up to four (608), where a block keeps 8,192 ids (140 rows of 50,304 16.6 us in
+  // clusters of 4, 19.5 of 2, but 64 rows 12.0 of 8, 10.7 of 4; 70 rows of 131,072 18.3 of
+  // 8, 22.9 of 4).  Never a second wave, which repeats the marking of ids (200 rows of 50,304 23 us
   // in clusters of 2, 29 of 4, 35 of 8; 75 rows 12.3 of 4, 16.7 of 8: larger clusters do
   // not fill every place).
   int blocks = 1;
