@@ -463,6 +463,111 @@ typedef struct gpt_next_token_args {
 int gpt_next_token(const gpt_next_token_args* args, void* cuda_stream);
 
 /*
+ * A paged cache in 8 bits: keys and values as e4m3 numbers (float8_e4m3fn: 4
+ * exponent bits of bias 7, 3 fraction bits, no infinities, NaN 0x7f and 0xff),
+ * each page and key head with one fp32 scale for its keys and one for its values; an
+ * element is number * scale.  pages: as above, k and v e4m3 (strides in elements,
+ * that is bytes), head_dim a multiple of 16; pages.dtype is the type of q, k, v
+ * and the outputs.  The scales of page p and key head h are k_scale and
+ * v_scale[p*scale_page + h*scale_head]; they are finite and not negative.
+ */
+typedef struct gpt_fp8_cache {
+  gpt_paged_cache pages;
+  float *k_scale, *v_scale;  /* DEVICE fp32                                         */
+  int64_t scale_page, scale_head;
+} gpt_fp8_cache;
+
+/*
+ * gpt_kv_append_fp8: gpt_kv_append into such a cache.  The new tokens of a sequence
+ * are neighbouring rows of k, v and q, in order: rows starts[s] .. starts[s+1] - 1
+ * are the tokens at positions before[s], before[s] + 1, ... of sequence s.  For each
+ * page, key head and side (keys, values) that gets new rows, with a the largest
+ * finite magnitude of these rows (of the keys before they are rotated) and
+ *   s_new = 2^(max(floor(log2 a), -119) - 7),
+ *  - a page whose slot 0 gets a row starts anew: its scale becomes s_new;
+ *  - otherwise it becomes the larger, s', of s_new and the scale s that is there,
+ *    and the numbers in the slots before the first new one become e4m3(number * s / s');
+ * then each new element x (keys: rotated, in fp32) is written as e4m3(x / scale),
+ * rounded to nearest, ties to even; infinities and NaN become NaN.  With s_new all
+ * elements lie below 2^8 (rotated ones below 2^8.5) and none reaches 448, the largest
+ * number; scales are powers of two, so that bringing numbers to a larger one loses nothing
+ * but what falls under the smallest number, 2^-9.  Slots behind the new rows are left
+ * as they are.  Rows before starts[0] and from starts[n_seq] on are neither read nor
+ * written (rows of q_out too), nor are the rows of a sequence of negative before[s].
+ *   before: DEVICE int32 [n_seq]; starts: DEVICE int32 [n_seq + 1], not decreasing, in
+ *     [0, n_tokens], or NULL: row s is the one new token of sequence s (n_tokens <=
+ *     n_seq).  Other arguments as in gpt_kv_append; the scales' strides name no scale
+ *     twice.
+ *   A row at a position past the table's reach (status), on a bad page (status) or at
+ *   a place where starts decreases or leaves its range (status BAD_SEQ) is skipped
+ *   whole.  Two sequences that write to one page in a call leave it unspecified.
+ */
+typedef struct gpt_kv_append_fp8_args {
+  const void *q, *k, *v;
+  void* q_out;
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head, qo_row, qo_head;
+  const int32_t *before, *starts;
+  uint32_t* status;
+  double rope_base;          /* >= 1; used when rope_dims > 0                       */
+  int32_t n_tokens, n_head;
+  int32_t rope_dims;         /* even, 0 (no rotation) .. head_dim                   */
+} gpt_kv_append_fp8_args;
+int gpt_kv_append_fp8(const gpt_fp8_cache* cache, const gpt_kv_append_fp8_args* args, void* cuda_stream);
+
+/*
+ * gpt_decode_attention_fp8: gpt_decode_attention over such a cache (the same
+ * arguments, q and out of type pages.dtype; strides of the scales may be 0: one scale
+ * for all).  A NaN among the values of a key that counts is in the result however
+ * small the key's weight is.  Weights enter the product with the values as fp16 numbers
+ * (two of them for fp32 outputs), to 2^-32 of the largest; sums are fp32.
+ */
+int gpt_decode_attention_fp8(const gpt_fp8_cache* cache, const gpt_decode_attention_args* args, void* cuda_stream);
+
+/* Host-only: the workspace a gpt_decode_attention_fp8 call with this cache and
+ * n_head needs (0 for arguments the call would refuse, or where none is needed). */
+size_t gpt_decode_attention_fp8_workspace(const gpt_fp8_cache* cache, int32_t n_head);
+
+/*
+ * gpt_sample_token: draws a token from each of `rows` rows of `vocab` logits z (those
+ * that gpt_next_token left, for instance) with the row's number uniform[b] in [0, 1).
+ * Tokens whose z is -infinity or NaN are not there.  With m the largest z of the row
+ * and T = temperature[b], a token's weight is w = exp((z - m) / T).  Of the tokens in
+ * order of falling z (equal ones: the smaller id first) these are kept:
+ *   top_k[b] >= 1: the first top_k[b];
+ *   top_p[b] < 1: of these the fewest whose weights sum to at least top_p[b] times the
+ *     sum of them all, one at least;
+ *   min_p[b] > 0: of these the ones with w >= min_p[b], the first in any case;
+ * (NULL or a value outside these ranges: no such limit).  The token is the first, by
+ * id, at which the running sum of the kept tokens' weights exceeds uniform[b] times
+ * their whole sum (uniform < 0 or NaN: 0; >= 1: the last of them with a weight).
+ * T not above 0 (NaN too): the first in that order alone, gpt_next_token's choice.  m of
+ * +infinity: the tokens of +infinity weigh 1 each, the others nothing.
+ * logprob = log(w / sum) of the token among the kept ones; kept: their number.  A row
+ * without tokens gives token -1, logprob -infinity, kept 0.
+ * Weights are summed as 64-bit integers in units of 2^(ceil(log2 vocab) - 63) of the
+ * largest, each off by 2^-40 of itself and a unit at most: the choices are those of the
+ * definition in 64 bits but where a limit or the number lies that close to a border, and
+ * do not depend on how a row is split.
+ *   logits: DEVICE [rows, vocab] of type dtype; logits_stride: elements between rows, at
+ *     least vocab or 0 (all rows read one); no alignment needed.  uniform,
+ *     temperature (NULL: 1 each), top_p, min_p: DEVICE fp32 [rows]; top_k: DEVICE int32
+ *     [rows].  token, kept: DEVICE int32 [rows]; logprob: DEVICE fp32 [rows]; any of the
+ *     three may be NULL, not all.
+ */
+typedef struct gpt_sample_token_args {
+  const void* logits;
+  const float *uniform, *temperature;
+  const int32_t* top_k;
+  const float *top_p, *min_p;
+  int32_t* token;
+  float* logprob;
+  int32_t* kept;
+  int64_t logits_stride;
+  int32_t rows, vocab, dtype;
+} gpt_sample_token_args;
+int gpt_sample_token(const gpt_sample_token_args* args, void* cuda_stream);
+
+/*
  * Measurement hook (per-phase timing, after the per-family table of
  * "Coppelius training on the RTX 3090", section "Where a step's time goes"):
  * runs the operations op_first .. op_first + op_count - 1 of the handle's step

@@ -98,6 +98,25 @@ class gpt_next_token_args(ctypes.Structure):
                 ("n_bias", c_int32)]
 
 
+class gpt_fp8_cache(ctypes.Structure):
+    _fields_ = [("pages", gpt_paged_cache), ("k_scale", c_void_p), ("v_scale", c_void_p), ("scale_page", c_int64),
+                ("scale_head", c_int64)]
+
+
+class gpt_kv_append_fp8_args(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("q_out", c_void_p),
+                ("q_row", c_int64), ("q_head", c_int64), ("k_row", c_int64), ("k_head", c_int64),
+                ("v_row", c_int64), ("v_head", c_int64), ("qo_row", c_int64), ("qo_head", c_int64),
+                ("before", c_void_p), ("starts", c_void_p), ("status", c_void_p), ("rope_base", c_double),
+                ("n_tokens", c_int32), ("n_head", c_int32), ("rope_dims", c_int32)]
+
+
+class gpt_sample_token_args(ctypes.Structure):
+    _fields_ = [("logits", c_void_p), ("uniform", c_void_p), ("temperature", c_void_p), ("top_k", c_void_p),
+                ("top_p", c_void_p), ("min_p", c_void_p), ("token", c_void_p), ("logprob", c_void_p), ("kept", c_void_p),
+                ("logits_stride", c_int64), ("rows", c_int32), ("vocab", c_int32), ("dtype", c_int32)]
+
+
 # bits of the decode-step operators' status word
 STATUS_BAD_SEQ, STATUS_BAD_POS, STATUS_BAD_PAGE, STATUS_BAD_TOKEN = 1, 2, 4, 8
 
@@ -145,6 +164,10 @@ SIGNATURES = [
     ("gpt_decode_attention", c_int, [POINTER(gpt_paged_cache), POINTER(gpt_decode_attention_args), c_void_p]),
     ("gpt_decode_attention_workspace", c_size_t, [POINTER(gpt_paged_cache), c_int32]),
     ("gpt_next_token", c_int, [POINTER(gpt_next_token_args), c_void_p]),
+    ("gpt_kv_append_fp8", c_int, [POINTER(gpt_fp8_cache), POINTER(gpt_kv_append_fp8_args), c_void_p]),
+    ("gpt_decode_attention_fp8", c_int, [POINTER(gpt_fp8_cache), POINTER(gpt_decode_attention_args), c_void_p]),
+    ("gpt_decode_attention_fp8_workspace", c_size_t, [POINTER(gpt_fp8_cache), c_int32]),
+    ("gpt_sample_token", c_int, [POINTER(gpt_sample_token_args), c_void_p]),
     ("gpt_test_attention", c_int, [c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p, c_void_p,
                                    c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
     ("gpt_test_gemm", c_int, [c_int32, c_int32, c_int32, c_int32, c_void_p, c_int64, c_int32,
@@ -582,7 +605,7 @@ def test_attention(qkv, dout, B: int, T: int, H: int, d: int, stream=None):
     return o, lse, dqkv
 
 
-_DECODE = ("kv_append", "decode_attention", "next_token")
+_DECODE = ("kv_append", "decode_attention", "next_token", "kv_append_fp8", "decode_attention_fp8", "sample_token")
 
 
 def __getattr__(name):

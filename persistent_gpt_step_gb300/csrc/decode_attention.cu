@@ -1,5 +1,5 @@
-// decode_attention.cu — gpt_decode_attention: argument checks, the choice of a
-// kernel and its grid, the workspace.
+// decode_attention.cu — gpt_decode_attention and gpt_decode_attention_fp8: argument
+// checks, the choice of a kernel and its grid, the workspace.
 #include <algorithm>
 #include <cmath>
 
@@ -8,8 +8,7 @@
 namespace pgs {
 namespace {
 
-int check_args(const gpt_paged_cache* c, int32_t n_head) {
-  if (const int rc = check_cache(c)) return rc;
+int check_heads(const gpt_paged_cache* c, int32_t n_head) {
   if (n_head < 1 || n_head % c->n_kv_head)
     return call_error(GPT_ERR_INVALID_ARG, "n_head %d must be a multiple of n_kv_head %d", n_head, c->n_kv_head);
   if (n_head > kMostHeads) return call_error(GPT_ERR_UNSUPPORTED, "n_head %d: at most %d", n_head, kMostHeads);
@@ -25,14 +24,14 @@ int sm_count() {
   return sms;
 }
 
-// Blocks of the grid, query heads of a row, and the workspace.
-Plan make_plan(const gpt_paged_cache* c, int32_t n_head) {
+// Blocks of the grid, query heads of a row, and the workspace; es: bytes of an element of
+// the cache.
+Plan make_plan(const gpt_paged_cache* c, int32_t n_head, int es) {
   Plan pl;
   const int group = n_head / c->n_kv_head;
   pl.chunk = group <= 8 ? group : c->dtype == GPT_DTYPE_BF16 ? (group < 16 ? group : 16) : 8;
   pl.chunks = (group + pl.chunk - 1) / pl.chunk;
-  pl.blocks = sm_count() * (pl.chunk > (c->dtype == GPT_DTYPE_BF16 ? 8 : 4) ? 1 : 2);  // as the kernels' kBlocks
-  const int es = elem_size(c->dtype);
+  pl.blocks = sm_count() * (pl.chunk > (c->dtype == GPT_DTYPE_BF16 || es == 1 ? 8 : 4) ? 1 : 2);  // as the kernels' kBlocks
   const double span = ((double)(c->n_pages - 1) * c->page_stride + (double)(c->page_size - 1) * c->slot_stride +
                        (double)(c->n_kv_head - 1) * c->head_stride + c->head_dim) * es;
   pl.fast = c->page_size % 8 == 0 && span < 16.0 * 0xffffffffu;
@@ -81,23 +80,11 @@ Plan make_plan(const gpt_paged_cache* c, int32_t n_head) {
   return pl;
 }
 
-}  // namespace
-}  // namespace pgs
-
-using namespace pgs;
-
-extern "C" size_t gpt_decode_attention_workspace(const gpt_paged_cache* c, int32_t n_head) {
-  clear_call_error();
-  if (check_args(c, n_head) != GPT_OK || c->n_seq == 0) return 0;
-  return make_plan(c, n_head).bytes;
-}
-
-extern "C" int gpt_decode_attention(const gpt_paged_cache* c, const gpt_decode_attention_args* a, void* cuda_stream) {
-  clear_call_error();
-  if (!a) return call_error(GPT_ERR_INVALID_ARG, "args must be non-NULL");
-  if (const int rc = check_args(c, a->n_head)) return rc;
+// Both entries: over a cache of dtype's elements, or over one in 8 bits with these scales.
+int attend(const gpt_paged_cache* c, const gpt_fp8_cache* scales, const gpt_decode_attention_args* a, cudaStream_t st) {
+  if (const int rc = check_heads(c, a->n_head)) return rc;
   if (c->n_seq == 0) return GPT_OK;
-  const int es = elem_size(c->dtype);
+  const int es = elem_size(c->dtype), cache_es = scales ? 1 : es;
   if (!a->q || !a->out || !a->lens) return call_error(GPT_ERR_INVALID_ARG, "q, out and lens must be non-NULL");
   if (!aligned16(a->q) || !aligned16(a->out) || !stride16(a->q_row, es) || !stride16(a->q_head, es) ||
       !stride16(a->out_row, es) || !stride16(a->out_head, es))
@@ -106,25 +93,58 @@ extern "C" int gpt_decode_attention(const gpt_paged_cache* c, const gpt_decode_a
   if (!apart({{a->out_row, c->n_seq}, {a->out_head, a->n_head}}, c->head_dim))
     return call_error(GPT_ERR_INVALID_ARG, "strides of out are smaller than a head or the dimension inside");
   if (!std::isfinite(a->scale * kLog2e)) return call_error(GPT_ERR_INVALID_ARG, "scale must be finite");
-  const Plan pl = make_plan(c, a->n_head);
+  const Plan pl = make_plan(c, a->n_head, cache_es);
   if (pl.bytes && (!a->workspace || a->workspace_bytes < pl.bytes || !aligned16(a->workspace)))
     return call_error(GPT_ERR_INVALID_ARG, "workspace: %zu bytes on a 16-byte boundary", pl.bytes);
-  DecodeParams p;
+  DecodeParams p = {};
   p.c = *c;
   p.a = *a;
   p.group = a->n_head / c->n_kv_head;
   p.chunk = pl.chunk, p.chunks = pl.chunks, p.team = pl.team, p.pack = pl.pack, p.join_heads = pl.join_heads;
   p.rows = c->n_kv_head / pl.team * pl.chunks;
+  if (scales) p.k_scale = scales->k_scale, p.v_scale = scales->v_scale, p.scale_page = scales->scale_page, p.scale_head = scales->scale_head;
   if (pl.fast) {
-    p.page16 = (uint32_t)(c->page_stride * es / 16), p.slot16 = (uint32_t)(c->slot_stride * es / 16);
-    p.head16 = (uint32_t)(c->head_stride * es / 16);
+    p.page16 = (uint32_t)(c->page_stride * cache_es / 16), p.slot16 = (uint32_t)(c->slot_stride * cache_es / 16);
+    p.head16 = (uint32_t)(c->head_stride * cache_es / 16);
   }
   p.scale2 = a->scale * kLog2e;
   p.meta = (Meta*)a->workspace;
   p.piece_ml = (float*)((char*)a->workspace + pl.ml_at);
   p.piece_o = (float*)((char*)a->workspace + pl.o_at);
-  const cudaStream_t st = (cudaStream_t)cuda_stream;
-  const bool wide = c->head_dim > 64;
-  if (c->dtype == GPT_DTYPE_BF16) return wide ? decode_bf16_128(p, pl, st) : decode_bf16_64(p, pl, st);
+  const bool wide = c->head_dim > 64, bf16 = c->dtype == GPT_DTYPE_BF16;
+  if (scales && bf16) return wide ? decode_fp8_bf16_128(p, pl, st) : decode_fp8_bf16_64(p, pl, st);
+  if (scales) return wide ? decode_fp8_fp32_128(p, pl, st) : decode_fp8_fp32_64(p, pl, st);
+  if (bf16) return wide ? decode_bf16_128(p, pl, st) : decode_bf16_64(p, pl, st);
   return wide ? decode_fp32_128(p, pl, st) : decode_fp32_64(p, pl, st);
+}
+
+}  // namespace
+}  // namespace pgs
+
+using namespace pgs;
+
+extern "C" size_t gpt_decode_attention_workspace(const gpt_paged_cache* c, int32_t n_head) {
+  clear_call_error();
+  if (check_cache(c) != GPT_OK || check_heads(c, n_head) != GPT_OK || c->n_seq == 0) return 0;
+  return make_plan(c, n_head, elem_size(c->dtype)).bytes;
+}
+
+extern "C" int gpt_decode_attention(const gpt_paged_cache* c, const gpt_decode_attention_args* a, void* cuda_stream) {
+  clear_call_error();
+  if (!a) return call_error(GPT_ERR_INVALID_ARG, "args must be non-NULL");
+  if (const int rc = check_cache(c)) return rc;
+  return attend(c, nullptr, a, (cudaStream_t)cuda_stream);
+}
+
+extern "C" size_t gpt_decode_attention_fp8_workspace(const gpt_fp8_cache* c, int32_t n_head) {
+  clear_call_error();
+  if (check_cache(c, false) != GPT_OK || check_heads(&c->pages, n_head) != GPT_OK || c->pages.n_seq == 0) return 0;
+  return make_plan(&c->pages, n_head, 1).bytes;
+}
+
+extern "C" int gpt_decode_attention_fp8(const gpt_fp8_cache* c, const gpt_decode_attention_args* a, void* cuda_stream) {
+  clear_call_error();
+  if (!a) return call_error(GPT_ERR_INVALID_ARG, "args must be non-NULL");
+  if (const int rc = check_cache(c, false)) return rc;
+  return attend(&c->pages, c, a, (cudaStream_t)cuda_stream);
 }

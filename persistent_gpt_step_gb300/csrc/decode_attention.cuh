@@ -162,9 +162,22 @@ constexpr int kCarefulFloats = kWarps * 130;
 __device__ __forceinline__ float scaled(float x, float f) { return x * 0.f == 0.f ? x * f : x; }
 __device__ __forceinline__ float with_value(float x, float w, float v) { return v * 0.f == 0.f ? fmaf(w, v, x) : x + v; }
 
+// Four dims of a key or value of type C, times the scale of its page in a cache in 8 bits.
+template <typename C>
+__device__ __forceinline__ void load_values(const C* from, float, float* x) { load4(from, x); }
+__device__ __forceinline__ void load_values(const E4m3* from, float scale, float* x) {
+  uint32_t a, b;
+  asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h;}"
+      : "=r"(a), "=r"(b) : "r"(*reinterpret_cast<const uint32_t*>(from)));
+  asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(x[0]), "=f"(x[1]) : "r"(a));
+  asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(x[2]), "=f"(x[3]) : "r"(b));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] *= scale;
+}
+
 // Query head hq, which reads key head h, of sequence s, by all threads of a block, if what
-// is there is not finite.
-template <typename T>
+// is there is not finite.  T: of the queries and results, C: of the cache.
+template <typename T, typename C>
 __device__ __noinline__ void careful_head(const DecodeParams& p, int s, int h, int hq, float* scratch) {
   constexpr int kAtOnce = 16 / sizeof(T);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = p.c.head_dim, e = lane * 4, len = seq_len(p, s, false);
@@ -175,14 +188,18 @@ __device__ __noinline__ void careful_head(const DecodeParams& p, int s, int h, i
   if (__all_sync(0xffffffffu, finite4(o))) return;
   if (p.a.lse && isnan(p.a.lse[(int64_t)s * p.a.n_head + hq])) return;  // of NaN or infinite scores: everything is NaN
   const int32_t* table = p.c.page_table + s * p.c.table_stride;
-  const T *kb = (const T*)p.c.k + h * p.c.head_stride + e, *vb = (const T*)p.c.v + h * p.c.head_stride + e;
+  const C *kb = (const C*)p.c.k + h * p.c.head_stride + e, *vb = (const C*)p.c.v + h * p.c.head_stride + e;
   if (e < d) load4((const T*)p.a.q + s * p.a.q_row + hq * p.a.q_head + e, q);
   o[0] = o[1] = o[2] = o[3] = 0.f;
   for (int64_t k = warp * 32; k < len; k += kWarps * 32) {
     int64_t at = -1;  // in elements; -1: no such key, or a bad page
+    float ks = 1.f, vs = 1.f;
     if (k + lane < len) {
       const int id = table[(int)(k + lane) / p.c.page_size];
-      if (id >= 0 && id < p.c.n_pages) at = id * p.c.page_stride + ((int)(k + lane) % p.c.page_size) * p.c.slot_stride;
+      if (id >= 0 && id < p.c.n_pages) {
+        at = id * p.c.page_stride + ((int)(k + lane) % p.c.page_size) * p.c.slot_stride;
+        if constexpr (std::is_same_v<C, E4m3>) ks = p.k_scale[id * p.scale_page + h * p.scale_head], vs = p.v_scale[id * p.scale_page + h * p.scale_head];
+      }
     }
     for (int j0 = 0; j0 < 32; j0 += kAtOnce) {
       float x[kAtOnce][4], v[kAtOnce][4], z[kAtOnce], top = m;
@@ -190,9 +207,11 @@ __device__ __noinline__ void careful_head(const DecodeParams& p, int s, int h, i
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) {
         const int64_t from = __shfl_sync(0xffffffffu, at, j0 + j);
+        float k_scale = 1.f, v_scale = 1.f;
+        if constexpr (std::is_same_v<C, E4m3>) k_scale = __shfl_sync(0xffffffffu, ks, j0 + j), v_scale = __shfl_sync(0xffffffffu, vs, j0 + j);
         there[j] = from >= 0;
         x[j][0] = x[j][1] = x[j][2] = x[j][3] = v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0.f;
-        if (there[j] && e < d) load4(kb + from, x[j]), load4(vb + from, v[j]);
+        if (there[j] && e < d) load_values(kb + from, k_scale, x[j]), load_values(vb + from, v_scale, v[j]);
       }
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) {
@@ -269,6 +288,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 template <int kMode, int DP_, bool kFast, bool kExact>
 struct Bf16Path {
   using T = __nv_bfloat16;
+  using Cache = T;
   static constexpr int NT = kMode == 16 ? 2 : 1, DP = DP_, kHeads = kMode;
   static constexpr int kBlocks = kMode == 16 ? 1 : 2;  // of an SM
   // A unit of the line is a step, of 32 keys in heads up to 64, where a row's start counts
@@ -516,6 +536,7 @@ struct Bf16Path {
 template <int GH_, int DP_, bool kFast, bool kExact>
 struct Fp32Path {
   using T = float;
+  using Cache = T;
   static constexpr int DP = DP_, kHeads = GH_, kUnit = kTile, kUnitStart = kStart;
   // With 8 heads the reads of the queries in shared memory bound it: twice the keys of a
   // step use each, with the registers of a block alone on its SM.
@@ -885,12 +906,12 @@ __global__ void __launch_bounds__(kWarps * 32, P::kBlocks) decode_kernel(const _
 }
 
 // The query heads of this block's rows in decode_row_kernel, once more.
-template <typename T>
+template <typename T, typename C>
 __device__ __noinline__ void careful_rows(const DecodeParams& p, float* scratch) {
   const int64_t row0 = (int64_t)(blockIdx.x / cg::this_cluster().num_blocks()) * p.pack, all = (int64_t)p.c.n_seq * p.rows;
   for (int i = 0; i < p.pack * p.chunk && row0 + i / p.chunk < all; ++i) {
     const int row = (int)((row0 + i / p.chunk) % p.rows), h = row / p.chunks, hq = h * p.group + row % p.chunks * p.chunk + i % p.chunk;
-    if (hq < (h + 1) * p.group) careful_head<T>(p, (int)((row0 + i / p.chunk) / p.rows), h, hq, scratch);
+    if (hq < (h + 1) * p.group) careful_head<T, C>(p, (int)((row0 + i / p.chunk) / p.rows), h, hq, scratch);
   }
 }
 
@@ -974,13 +995,13 @@ __global__ void __launch_bounds__(kWarps * 32, P::kBlocks) decode_row_kernel(con
     }
     cluster.sync();  // a block's memory stays until the others have read it
   }
-  if (infinite) careful_rows<T>(p, sm);
+  if (infinite) careful_rows<T, typename P::Cache>(p, sm);
 }
 
 // A row that several blocks worked on: the pieces of its blocks, joined.  Block
 // (b, y): the row begun in block b, its query heads from join_heads y on; the warps
 // share the heads and, where these are fewer, the pieces.  The last y: look_at_heads.
-template <typename T>
+template <typename T, typename C>
 __device__ __forceinline__ void join_row(const DecodeParams& p, float* scratch) {
   __shared__ float sm_ml[kWarps][2], sm_o[kWarps][128];
   __shared__ int again[kWarps];  // heads whose results are not finite, or -1
@@ -1058,11 +1079,11 @@ __device__ __forceinline__ void join_row(const DecodeParams& p, float* scratch) 
   if (lane == 0) again[warp] = infinite;
   if (__syncthreads_and(infinite < 0)) return;
   for (int w = 0; w < kWarps; ++w)
-    if (again[w] >= 0) careful_head<T>(p, mt.seq, again[w] / p.group, again[w], scratch);
+    if (again[w] >= 0) careful_head<T, C>(p, mt.seq, again[w] / p.group, again[w], scratch);
 }
 
 // The heads that the line kernel ended itself, looked at for results that are not finite.
-template <typename T>
+template <typename T, typename C>
 __device__ __forceinline__ void look_at_heads(const DecodeParams& p, float* scratch) {
   constexpr int kAtOnce = 4;
   __shared__ uint32_t found[kWarps];
@@ -1091,7 +1112,7 @@ __device__ __forceinline__ void look_at_heads(const DecodeParams& p, float* scra
         bool joined = false;  // in another block, which looks at what it has written itself
         for (int i = lane; i < gridDim.x; i += 32)
           joined |= p.meta[i].seq == s && p.meta[i].row == h / p.team * p.chunks + hq % p.group / p.chunk;
-        if (!__any_sync(0xffffffffu, joined)) careful_head<T>(p, s, h, hq, scratch);
+        if (!__any_sync(0xffffffffu, joined)) careful_head<T, C>(p, s, h, hq, scratch);
       }
     __syncthreads();
   }
@@ -1101,12 +1122,12 @@ __device__ __forceinline__ void look_at_heads(const DecodeParams& p, float* scra
 // 64, 81.8 us with it and 80.4 without; 131,071 keys 93.1 and 92.3); in the line kernel, where
 // a row ends, it takes as much, and with heads of 96 5 us (104 sequences of 13 to 878 keys, 8
 // heads, 42.7, here 38.2).
-template <typename T>
+template <typename T, typename C>
 __global__ void __launch_bounds__(kWarps * 32, 3) decode_join_kernel(const __grid_constant__ DecodeParams p) {
   __shared__ float scratch[kCarefulFloats];
   after_stream();
-  if (blockIdx.y + 1 < gridDim.y) join_row<T>(p, scratch);
-  else look_at_heads<T>(p, scratch);
+  if (blockIdx.y + 1 < gridDim.y) join_row<T, C>(p, scratch);
+  else look_at_heads<T, C>(p, scratch);
 }
 
 template <class P>
@@ -1129,7 +1150,7 @@ int launch(const DecodeParams& p, const Plan& pl, cudaStream_t st) {
   }
   if (const int rc = launch_after("gpt_decode_attention", decode_kernel<P>, dim3(pl.blocks), kWarps * 32, kLineBytes, 0, st, p)) return rc;
   const dim3 grid(pl.blocks, (pl.team * pl.chunk + pl.join_heads - 1) / pl.join_heads + 1);
-  return launch_after("gpt_decode_attention (join)", decode_join_kernel<typename P::T>, grid, kWarps * 32, 0, 0, st, p);
+  return launch_after("gpt_decode_attention (join)", decode_join_kernel<typename P::T, typename P::Cache>, grid, kWarps * 32, 0, 0, st, p);
 }
 
 // The launch for a head size of at most DP: the fast forms need pages of whole 8-key

@@ -1,5 +1,5 @@
-// decode_attention.h — what the host side of gpt_decode_attention and its kernels
-// share; the kernels are compiled by type and head size, a translation unit each.
+// decode_attention.h — what the host side of gpt_decode_attention, gpt_decode_attention_fp8 and
+// their kernels share; the kernels are compiled by type and head size, a translation unit each.
 #pragma once
 #include "decode_ops.h"
 
@@ -16,6 +16,8 @@ constexpr int kTile = 16;      // keys of a unit of work
 constexpr int kStart = 2;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+struct E4m3 { uint8_t bits; };  // an element of a cache in 8 bits
+
 struct Meta { int32_t seq, row, last, pad; };  // a row begun in this block and ended in block `last`
 
 struct DecodeParams {
@@ -28,6 +30,8 @@ struct DecodeParams {
   int32_t pack;      // rows of a block (decode_row_kernel)
   int32_t rows;      // rows (of `team` key heads) of one sequence
   int32_t join_heads;  // query heads of a block of the second kernel, 1 to 8
+  const float *k_scale, *v_scale;  // of a cache in 8 bits
+  int64_t scale_page, scale_head;
   uint32_t page16, slot16, head16;  // the cache's strides in 16 bytes (fast forms)
   float scale2;      // scale log2 e
   Meta* meta;        // [blocks]
@@ -50,5 +54,9 @@ int decode_bf16_64(const DecodeParams& p, const Plan& pl, cudaStream_t st);
 int decode_bf16_128(const DecodeParams& p, const Plan& pl, cudaStream_t st);
 int decode_fp32_64(const DecodeParams& p, const Plan& pl, cudaStream_t st);
 int decode_fp32_128(const DecodeParams& p, const Plan& pl, cudaStream_t st);
+int decode_fp8_bf16_64(const DecodeParams& p, const Plan& pl, cudaStream_t st);
+int decode_fp8_bf16_128(const DecodeParams& p, const Plan& pl, cudaStream_t st);
+int decode_fp8_fp32_64(const DecodeParams& p, const Plan& pl, cudaStream_t st);
+int decode_fp8_fp32_128(const DecodeParams& p, const Plan& pl, cudaStream_t st);
 
 }  // namespace pgs

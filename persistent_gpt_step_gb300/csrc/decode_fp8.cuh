@@ -1,0 +1,443 @@
+// decode_fp8.cuh — attention of one new token over a cache in 8 bits: the part of a
+// row that a warp does, for the kernels of decode_attention.cuh.
+//
+// Keys and values are e4m3 numbers, a scale each per page and head.  A number is exact in
+// fp16, so both products are mma.m16n8k16 on fp16 with fp32 sums:
+//  - scores: 16 keys x 8 query heads, four dims of a lane to a product as they lie in
+//    memory; the key scale of a page multiplies the score.  A query is brought below 2^15 by
+//    a power of two of its own (what falls under 2^-25 there is 2^-39 of its largest): bf16
+//    queries are then exact, fp32 ones enter as two fp16 parts (2^-23).
+//  - values: the weights enter as fp16 numbers below 2^15 (their reference lies 7 under the
+//    maximum, so that what falls under fp16's smallest number is 2^-32 of the largest), for
+//    fp32 results as two parts.  A product of 16 keys is summed apart and joined to the row's
+//    sums with the value scale of its page; where its keys have two scales, the smaller one's
+//    weights are brought to the larger.
+// Bound: HBM, half the bytes of a bf16 cache; the conversions (a number of a key and a value
+// each, two at a time) are the pipe that is busiest beside it.
+#pragma once
+#include "decode_attention.cuh"
+
+namespace pgs {
+namespace {
+
+__device__ __forceinline__ void mma16816_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The four numbers of a word as fp16 pairs.
+__device__ __forceinline__ void to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h;}" : "=r"(lo), "=r"(hi) : "r"(w));
+}
+__device__ __forceinline__ uint32_t pack2_f16(float lo, float hi) {
+  uint32_t u;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
+  return u;
+}
+__device__ __forceinline__ float2 unpack2_f16(uint32_t u) {
+  float2 x;
+  asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(x.x), "=f"(x.y) : "r"(u));
+  return x;
+}
+// What two numbers leave over of their fp16 parts; nothing of an infinity.
+__device__ __forceinline__ uint32_t rest2_f16(float lo, float hi, uint32_t parts) {
+  const float2 x = unpack2_f16(parts);
+  return pack2_f16(fabsf(x.x) == INFINITY ? 0.f : lo - x.x, fabsf(x.y) == INFINITY ? 0.f : hi - x.y);
+}
+__device__ __forceinline__ uint2 load8(const void* p) {
+  uint2 u;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(u.x), "=r"(u.y) : "l"(p));
+  return u;
+}
+
+// As Walk, with the scales of each group's (or key's) page: table entries are read two
+// rounds ahead, the scales one.
+template <bool kFast>
+struct ScaledWalk {
+  using Off = std::conditional_t<kFast, uint32_t, int64_t>;
+  static constexpr Off kNoKey = (Off)-1;
+  static constexpr int kRound = kFast ? 256 : 32;  // keys
+  const DecodeParams& p;
+  const int32_t* table;
+  const float *ks_at, *vs_at;  // of the head
+  Off head, off;
+  float ks, vs, ks1, vs1;
+  int at1, page1, page2, end, lane_at;
+
+  __device__ __forceinline__ ScaledWalk(const DecodeParams& p_, int s, int h, int k0, int k1)
+      : p(p_), table(p_.c.page_table + s * p_.c.table_stride), ks_at(p_.k_scale + h * p_.scale_head), vs_at(p_.v_scale + h * p_.scale_head),
+        end(k1), lane_at(0) {
+    const int lane = threadIdx.x & 31;
+    head = kFast ? h * p.head16 : h * p.c.head_stride;
+    at1 = k0 + (kFast ? lane * 8 : lane);
+    page1 = fetch(at1);
+    scales();
+    page2 = fetch(at1 + kRound);
+  }
+  __device__ __forceinline__ int fetch(int at) const {
+    if (at >= end) return -1;
+    const int id = table[at / p.c.page_size];
+    if (id >= 0 && id < p.c.n_pages) return id;
+    set_status(p.a.status, GPT_STATUS_BAD_PAGE);
+    return -1;
+  }
+  __device__ __forceinline__ void scales() {
+    ks1 = vs1 = 0.f;
+    if (page1 >= 0) ks1 = __ldg(ks_at + page1 * p.scale_page), vs1 = __ldg(vs_at + page1 * p.scale_page);
+  }
+  __device__ __forceinline__ void turn() {
+    if constexpr (kFast) off = page1 < 0 ? kNoKey : page1 * p.page16 + (at1 % p.c.page_size) * p.slot16 + head;
+    else off = page1 < 0 ? kNoKey : page1 * p.c.page_stride + (at1 % p.c.page_size) * p.c.slot_stride + head;
+    ks = ks1, vs = vs1;
+    at1 += kRound, page1 = page2;
+    scales();
+    page2 = fetch(at1 + kRound);
+  }
+  // kFast: the next group of 8 keys.
+  __device__ __forceinline__ void group(Off& o, float& k, float& v) {
+    o = __shfl_sync(0xffffffffu, off, lane_at), k = __shfl_sync(0xffffffffu, ks, lane_at), v = __shfl_sync(0xffffffffu, vs, lane_at);
+    if (++lane_at == 32) turn(), lane_at = 0;
+  }
+};
+
+// kMode: query heads of a row.  fp32 with 4: columns 4..7 of the products take the low parts
+// of queries and weights; with 8: products of their own.  bf16: 8, or 16 in two tiles.
+template <typename T_, int kMode, int DP_, bool kFast, bool kExact>
+struct Fp8Path {
+  using T = T_;
+  using Cache = E4m3;
+  static constexpr bool kFull = std::is_same_v<T, float>;
+  static constexpr int NT = kMode == 16 ? 2 : 1, DP = DP_, kHeads = kMode;
+  static constexpr bool kTwice = kFull && kMode == 4;
+  static constexpr int kParts = kFull && !kTwice ? 2 : 1;  // products for a tile
+  static constexpr int kBlocks = kMode == 16 ? 1 : 2;      // of an SM
+  static constexpr int KG = 2, kKeys = 16 * KG, kUnit = kKeys, kUnitStart = kStart;
+  static constexpr int KP = DP / 64;                       // a lane's 16-byte pieces of a key
+  static constexpr int VW = DP / 32;                       // a lane's words of a value
+  static constexpr int kQuery = NT * kParts * KP * 256;    // a warp's queries: 32 bytes per lane, tile, part and piece
+
+  // Dims of a lane's piece i of a key or query; those of its part of a value begin at r * 4 VW.
+  static __device__ __forceinline__ int piece_dim(int i, int c) { return c * 16 * KP + i * 16; }
+
+  // Lane (r, c): query head r of a tile, its pieces, in fp16.  Returns 2^e of the head, by which
+  // its scores are to be multiplied.
+  static __device__ __forceinline__ float stage_query(const DecodeParams& p, uint4* query, const Part& w, int t) {
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const int qh = kTwice ? r & 3 : t * 8 + r;
+    constexpr int kN = Piece<T>::kN, kLoads = 16 / kN;
+    uint4 u[KP][kLoads];
+#pragma unroll
+    for (int i = 0; i < KP; ++i)
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j)
+        u[i][j] = load16_if((const T*)p.a.q + w.s * p.a.q_row + (w.hq + qh) * p.a.q_head + piece_dim(i, c) + j * kN,
+                            qh < w.n && piece_dim(i, c) < p.c.head_dim);
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < KP; ++i)
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        float x[kN];
+        Piece<T>::unpack(u[i][j], x);
+#pragma unroll
+        for (int k = 0; k < kN; ++k) top = fabsf(x[k]) < INFINITY ? fmaxf(top, fabsf(x[k])) : top;
+      }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int e = max((int)(__float_as_uint(top) >> 23) - 127 - 14, -126);  // top 2^-e is below 2^15
+    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < KP; ++i)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8 / kN; ++k) Piece<T>::unpack(u[i][half * (8 / kN) + k], x + k * kN);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] *= down;
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          h[k] = pack2_f16(x[2 * k], x[2 * k + 1]);
+          if (kFull) l[k] = rest2_f16(x[2 * k], x[2 * k + 1], h[k]);
+          if (kTwice && r >= 4) h[k] = l[k];
+        }
+        query[((t * kParts * KP + i) * 2 + half) * 32] = make_uint4(h[0], h[1], h[2], h[3]);
+        if (kParts == 2) query[(((t * kParts + 1) * KP + i) * 2 + half) * 32] = make_uint4(l[0], l[1], l[2], l[3]);
+      }
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+  }
+
+  static __device__ __forceinline__ void run(const DecodeParams& p, float* mine, const Part& w) {
+    const int k0 = w.k0, k1 = w.k1;
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const int d = p.c.head_dim;
+    const int64_t row = p.c.slot_stride;
+    const uint8_t* kb = (const uint8_t*)p.c.k + (kFast ? r * row : 0);
+    const uint8_t* vb = (const uint8_t*)p.c.v + r * 4 * VW + (kFast ? 2 * c * row : 0);
+    uint4* query = reinterpret_cast<uint4*>(mine) + lane;
+    float o[NT][VW][2][4], m[NT][2], l[NT][2], factor[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      m[t][0] = m[t][1] = -INFINITY, l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+      for (int b = 0; b < VW; ++b)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[t][b][i / 4][i % 4] = 0.f;
+    }
+    uint4 kr[KG][2][KP];
+    uint32_t vr[KG][4][VW];
+    using Keys = ScaledWalk<kFast>;
+    Keys walk(p, w.s, w.h, k0, k1);
+    // Of the step's groups of 8: offsets, scales.  Without kFast: off[0][0] of the lane's key,
+    // the scales of key g * 16 + u * 8 + r.
+    typename Keys::Off off[KG][2];
+    float ks[KG][2], vs[KG][2];
+    auto advance = [&] {
+      if constexpr (kFast) {
+#pragma unroll
+        for (int g = 0; g < KG; ++g)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) walk.group(off[g][u], ks[g][u], vs[g][u]);
+      } else {
+        off[0][0] = walk.off;
+#pragma unroll
+        for (int g = 0; g < KG; ++g)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            ks[g][u] = __shfl_sync(0xffffffffu, walk.ks, g * 16 + u * 8 + r);
+            vs[g][u] = __shfl_sync(0xffffffffu, walk.vs, g * 16 + u * 8 + r);
+          }
+        walk.turn();
+      }
+    };
+    auto load_keys = [&] {
+#pragma unroll
+      for (int g = 0; g < KG; ++g)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if constexpr (kFast) {
+            const uint8_t* at = group_at(kb, off[g][u]);
+            if constexpr (kExact && KP == 2) load32(at + piece_dim(0, c), kr[g][u][0], kr[g][u][KP - 1]);
+            else
+#pragma unroll
+              for (int i = 0; i < KP; ++i) kr[g][u][i] = kExact ? load16(at + piece_dim(i, c)) : load16_if(at + piece_dim(i, c), piece_dim(i, c) < d);
+          } else {
+            const int64_t at = __shfl_sync(0xffffffffu, off[0][0], g * 16 + u * 8 + r);
+#pragma unroll
+            for (int i = 0; i < KP; ++i) kr[g][u][i] = load16_if(kb + at + piece_dim(i, c), at >= 0 && piece_dim(i, c) < d);
+          }
+    };
+    auto load_value = [&](const uint8_t* at, bool ok, uint32_t* to) {
+      if constexpr (VW == 4) {
+        const uint4 u = kExact ? load16(at) : load16_if(at, ok && r * 16 < d);
+        to[0] = u.x, to[1] = u.y, to[2] = u.z, to[3] = u.w;
+      } else {
+        const uint2 u = kExact || (ok && r * 8 < d) ? load8(at) : make_uint2(0u, 0u);
+        to[0] = u.x, to[1] = u.y;
+      }
+    };
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float up = stage_query(p, query, w, t);
+      factor[t][0] = __shfl_sync(0xffffffffu, up, 8 * c);
+      factor[t][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
+    }
+    walk.turn();
+    advance();
+    load_keys();
+    for (int k = k0; k < k1; k += kKeys) {
+      uint32_t there = 0xffffffffu;  // keys that count
+#pragma unroll
+      for (int g = 0; g < KG; ++g)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if constexpr (kFast) {
+            load_value(group_at(vb, off[g][u >> 1]) + (u & 1) * row, true, vr[g][u]);
+            if ((u & 1) && off[g][u >> 1] == ~0u) there &= ~(0xffu << (g * 16 + (u >> 1) * 8));
+          } else {
+            const int64_t at = __shfl_sync(0xffffffffu, off[0][0], g * 16 + (u >> 1) * 8 + 2 * c + (u & 1));
+            load_value(vb + at, at >= 0, vr[g][u]);
+          }
+      if constexpr (kFast) {
+        if (k1 - k < kKeys) there &= (1u << (k1 - k)) - 1u;
+      } else {
+        there = __ballot_sync(0xffffffffu, off[0][0] >= 0);
+      }
+      // the step's scales: of the scores; of a product of 16 keys, and what brings weights to it
+      float key_scale[KG][2], value_scale[KG], bring[KG][2];
+#pragma unroll
+      for (int g = 0; g < KG; ++g) {
+        key_scale[g][0] = ks[g][0], key_scale[g][1] = ks[g][1];
+        float top = fmaxf(vs[g][0], vs[g][1]);
+        if constexpr (!kFast)
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        value_scale[g] = top;
+        bring[g][0] = vs[g][0] == top ? 1.f : vs[g][0] / top, bring[g][1] = vs[g][1] == top ? 1.f : vs[g][1] / top;
+      }
+      advance();
+      // scores: 16 keys x 8 columns a tile
+      float z[KG][NT][4];
+#pragma unroll
+      for (int g = 0; g < KG; ++g)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[g][t][i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < KP; ++i)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint4 q[NT][kParts];
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int x = 0; x < kParts; ++x) q[t][x] = query[(((t * kParts + x) * KP + i) * 2 + half) * 32];
+#pragma unroll
+          for (int g = 0; g < KG; ++g)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint32_t a0, a1, a2, a3;
+              to_f16((&kr[g][0][i].x)[half * 2 + j], a0, a2);
+              to_f16((&kr[g][1][i].x)[half * 2 + j], a1, a3);
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int x = 0; x < kParts; ++x) mma16816_f16(z[g][t], a0, a1, a2, a3, j ? q[t][x].z : q[t][x].x, j ? q[t][x].w : q[t][x].y);
+            }
+        }
+      load_keys();
+#pragma unroll
+      for (int g = 0; g < KG; ++g)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (kTwice) z[g][t][i] += __shfl_xor_sync(0xffffffffu, z[g][t][i], 2);
+            z[g][t][i] *= factor[t][i & 1] * key_scale[g][i >> 1] * p.scale2;
+          }
+      if (__builtin_expect(there != 0xffffffffu, 0)) {
+#pragma unroll
+        for (int g = 0; g < KG; ++g) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (!((there >> (g * 16 + (i >> 1) * 8 + r)) & 1u)) z[g][t][i] = -INFINITY;
+          if constexpr (kFast)  // what such a slot holds may be NaN
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (!((there >> (g * 16 + (u >> 1) * 8 + 2 * c + (u & 1))) & 1u))
+#pragma unroll
+                for (int b = 0; b < VW; ++b) vr[g][u][b] = 0u;
+        }
+      }
+      // softmax: the reference of a head moves only when a score passes the maximum by 2^8
+      bool move = false;
+#pragma unroll
+      for (int g = 0; g < KG; ++g)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          move |= fmaxf(z[g][t][0], z[g][t][2]) > m[t][0] + 15.f || fmaxf(z[g][t][1], z[g][t][3]) > m[t][1] + 15.f;
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = m[t][e] + 7.f;
+#pragma unroll
+            for (int g = 0; g < KG; ++g) top = fmaxf(top, fmaxf(z[g][t][e], z[g][t][e + 2]));
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            top -= 7.f;
+            const float keep = weight(m[t][e], top);
+            m[t][e] = top;
+            l[t][e] *= keep;
+#pragma unroll
+            for (int b = 0; b < VW; ++b)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) o[t][b][i][e] *= keep, o[t][b][i][e + 2] *= keep;
+          }
+      }
+#pragma unroll
+      for (int g = 0; g < KG; ++g) {
+        uint32_t h0[NT], h1[NT], l0[NT], l1[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const float m0 = m[t][0] == -INFINITY ? 0.f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+          float p0 = exp2_fast(z[g][t][0] - m0), p1 = exp2_fast(z[g][t][1] - m1);
+          float p2 = exp2_fast(z[g][t][2] - m0), p3 = exp2_fast(z[g][t][3] - m1);
+          l[t][0] += p0 + p2, l[t][1] += p1 + p3;
+          p0 *= bring[g][0], p1 *= bring[g][0], p2 *= bring[g][1], p3 *= bring[g][1];
+          uint32_t ha = pack2_f16(p0, p1), hb = pack2_f16(p2, p3), la = 0u, lb = 0u;
+          if (kFull) la = rest2_f16(p0, p1, ha), lb = rest2_f16(p2, p3, hb);
+          if (kTwice) ha = c < 2 ? ha : la, hb = c < 2 ? hb : lb;
+          h0[t] = transpose8(ha), h1[t] = transpose8(hb);
+          if (kParts == 2) l0[t] = transpose8(la), l1[t] = transpose8(lb);
+        }
+#pragma unroll
+        for (int b = 0; b < VW; ++b)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t a0, a1, a2, a3;
+            to_f16(__byte_perm(vr[g][0][b], vr[g][1][b], i ? 0x7362 : 0x5140), a0, a1);
+            to_f16(__byte_perm(vr[g][2][b], vr[g][3][b], i ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              float x[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16816_f16(x, a0, a1, a2, a3, h0[t], h1[t]);
+              if (kParts == 2) mma16816_f16(x, a0, a1, a2, a3, l0[t], l1[t]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[t][b][i][j] = fmaf(value_scale[g], x[j], o[t][b][i][j]);
+            }
+          }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int qh = t * 8 + 2 * c + e;
+        float total = l[t][e];
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
+        float y[VW][4];
+#pragma unroll
+        for (int b = 0; b < VW; ++b)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            y[b][i] = o[t][b][i >> 1][e + 2 * (i & 1)];
+            if (kTwice) y[b][i] += __shfl_xor_sync(0xffffffffu, y[b][i], 2);
+          }
+        if (qh >= w.n) continue;
+        if (w.left) {
+          if (r == 0) w.left[2 * qh] = m[t][e], w.left[2 * qh + 1] = total;
+          float* to = w.left + left_o(kHeads) + qh * DP + r * 4 * VW;
+#pragma unroll
+          for (int b = 0; b < VW; ++b) store4(to + 4 * b, y[b]);
+        } else {
+          const float inv = total == 0.f ? 0.f : 1.0f / total;
+          T* to = (T*)p.a.out + w.s * p.a.out_row + (w.hq + qh) * p.a.out_head + r * 4 * VW;
+#pragma unroll
+          for (int b = 0; b < VW; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[b][i] *= inv;
+          if (kExact || r * 4 * VW < d)
+#pragma unroll
+            for (int b = 0; b < VW; ++b) store4(to + 4 * b, y[b]);
+          if (r == 0) store_lse(p, w.s, w.hq + qh, m[t][e], total);
+        }
+      }
+  }
+};
+
+template <typename T, int N, int DP>
+int launch_fp8(const DecodeParams& p, const Plan& pl, cudaStream_t st) {
+  if (!pl.fast) return launch<Fp8Path<T, N, DP, false, false>>(p, pl, st);
+  return pl.exact ? launch<Fp8Path<T, N, DP, true, true>>(p, pl, st) : launch<Fp8Path<T, N, DP, true, false>>(p, pl, st);
+}
+
+}  // namespace
+}  // namespace pgs

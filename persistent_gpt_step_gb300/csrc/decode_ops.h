@@ -1,5 +1,5 @@
-// decode_ops.h — what the operators of a batched decode step (kv_append.cu,
-// decode_attention.cu, next_token.cu) share: error texts, argument checks, the
+// decode_ops.h — what the operators of a batched decode step (kv_append.cu, kv_append_fp8.cu,
+// decode_attention.cu, decode_attention_fp8.cu, next_token.cu, sample_token.cu) share: error texts, argument checks, the
 // device view of a paged cache and element conversions.
 #pragma once
 #include <cuda_bf16.h>
@@ -44,14 +44,15 @@ inline bool apart(std::initializer_list<Dim> dims, int64_t width) {
 }
 constexpr int kMostHeads = 1 << 16;  // head counts and their products stay in 32 bits
 
-// GPT_OK, or the refusal of a cache that the header does not allow.
-inline int check_cache(const gpt_paged_cache* c) {
+// GPT_OK, or the refusal of a cache that the header does not allow; es: bytes of an element
+// of the cache, 0 for those of its dtype.
+inline int check_cache(const gpt_paged_cache* c, int es = 0) {
   if (!c) return call_error(GPT_ERR_INVALID_ARG, "cache must be non-NULL");
   if (c->dtype != GPT_DTYPE_FP32 && c->dtype != GPT_DTYPE_BF16)
     return call_error(GPT_ERR_INVALID_ARG, "cache dtype must be GPT_DTYPE_FP32 or GPT_DTYPE_BF16");
   if (c->n_pages < 1 || c->page_size < 1 || c->n_seq < 0 || c->max_pages < 1 || c->n_kv_head < 1 || c->head_dim < 1)
     return call_error(GPT_ERR_INVALID_ARG, "cache sizes must be positive");
-  const int es = elem_size(c->dtype);
+  if (es == 0) es = elem_size(c->dtype);
   if (c->n_kv_head > kMostHeads) return call_error(GPT_ERR_UNSUPPORTED, "n_kv_head %d: at most %d", c->n_kv_head, kMostHeads);
   if (c->head_dim > 128 || (c->head_dim * es) % 16)
     return call_error(GPT_ERR_UNSUPPORTED, "head_dim %d: a multiple of 16 bytes, at most 128 elements", c->head_dim);
@@ -64,6 +65,20 @@ inline int check_cache(const gpt_paged_cache* c) {
     return call_error(GPT_ERR_INVALID_ARG, "cache addresses and strides must be multiples of 16 bytes");
   if (c->table_stride < c->max_pages && c->table_stride != 0 && c->n_seq > 1)
     return call_error(GPT_ERR_INVALID_ARG, "table_stride is smaller than max_pages");
+  return GPT_OK;
+}
+
+// The same for a cache in 8 bits with scales; `written`: no scale may be named twice.
+inline int check_cache(const gpt_fp8_cache* c, bool written) {
+  if (!c) return call_error(GPT_ERR_INVALID_ARG, "cache must be non-NULL");
+  if (const int rc = check_cache(&c->pages, 1)) return rc;
+  if (c->pages.n_seq == 0) return GPT_OK;
+  if (!c->k_scale || !c->v_scale) return call_error(GPT_ERR_INVALID_ARG, "k_scale and v_scale must be non-NULL");
+  if (reinterpret_cast<uintptr_t>(c->k_scale) % 4 || reinterpret_cast<uintptr_t>(c->v_scale) % 4)
+    return call_error(GPT_ERR_INVALID_ARG, "k_scale and v_scale must lie on 4-byte boundaries");
+  if (c->scale_page < 0 || c->scale_head < 0) return call_error(GPT_ERR_INVALID_ARG, "strides of the scales must not be negative");
+  if (written && !apart({{c->scale_page, c->pages.n_pages}, {c->scale_head, c->pages.n_kv_head}}, 1))
+    return call_error(GPT_ERR_INVALID_ARG, "strides of the scales are smaller than the dimension inside");
   return GPT_OK;
 }
 

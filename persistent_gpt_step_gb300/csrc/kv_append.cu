@@ -1,41 +1,18 @@
 // kv_append.cu — gpt_kv_append: keys and values of new tokens into a paged
-// cache, keys and queries rotated on the way.
-//
-// Pair i of a head turns by t = p base^(-2i/R) at position p.  In turns,
-// t / 2pi = p f with f = base^(-2i/R) / 2pi computed on the host in double and
-// passed as two floats f_hi + f_lo.  p is split into a multiple of 2^16 and the
-// rest, both exact floats; fma gives what the rounded products with f_hi leave
-// over, whole turns drop out of every term exactly, and sincospi needs no further
-// range reduction.  Errors in turns: f's double products 2^-49 p f, f_lo's rounding
-// 2^-50 p f, and the roundings of the sums, 2^-26 each: 2^-23 below position 2^24.
-// From there on the product p f_lo has whole turns as well: 2^-18 up to 2^31.  (The
-// fp32 product p base^(-2i/R) would be off by 2^-25 p.)
-#include <cmath>
-
-#include "decode_ops.h"
+// cache, keys and queries rotated on the way (rotary.h).
+#include "rotary.h"
 
 namespace pgs {
 namespace {
 
-constexpr int kMaxPairs = 64;  // head_dim <= 128
 constexpr int kMaxTokens = 8;  // of a block
 
 struct AppendParams {
   gpt_paged_cache c;
   gpt_kv_append_args a;
-  float f_hi[kMaxPairs], f_lo[kMaxPairs];
+  RotaryRates rates;
   int32_t share;  // threads of a token are the block's >> share
 };
-
-__device__ __forceinline__ float part_turn(float x) { return x - rintf(x); }
-
-__device__ __forceinline__ void pair_angle(const AppendParams& p, int i, int pos, float* cs, float* sn) {
-  const float hi = (float)(pos & ~0xffff), lo = (float)(pos & 0xffff);
-  const float f = p.f_hi[i], a = hi * f, b = lo * f;
-  const float rest = part_turn(fmaf(hi, f, -a)) + fmaf(lo, f, -b) + (float)pos * p.f_lo[i];
-  const float t = part_turn(part_turn(a) + part_turn(b)) + rest;
-  sincospif(2.0f * t, sn, cs);
-}
 
 // Bound: HBM (every element is read and written once).  A block has one token, or up to
 // 8 where these are small, each with a part of its threads.  A token's
@@ -81,7 +58,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     const bool bad_pos = pos < 0 || pos >= c.max_pages * c.page_size;
     if (!bad_seq && !bad_pos) page = c.page_table[s * c.table_stride + pos / c.page_size];
     for (int i = tid; i < a.rope_dims / 2; i += threads) {
-      pair_angle(p, i, pos, &turn[i].x, &turn[i].y);
+      pair_angle(p.rates, i, pos, &turn[i].x, &turn[i].y);
       if (!kShared) break;  // at most 64 pairs
     }
     if (page < 0 || page >= c.n_pages) {
@@ -159,15 +136,7 @@ extern "C" int gpt_kv_append(const gpt_paged_cache* c, const gpt_kv_append_args*
   AppendParams p = {};
   p.c = *c;
   p.a = *a;
-  if (a->rope_dims > 0) {
-    double f[kMaxPairs] = {1.0 / 6.283185307179586476925};  // base^(-2i/R) / 2pi, at most six products each
-    const int pairs = a->rope_dims / 2;
-    for (int n = 1; n < pairs; n *= 2) {
-      const double step = std::pow(a->rope_base, -2.0 * n / a->rope_dims);
-      for (int i = n; i < pairs && i < 2 * n; ++i) f[i] = f[i - n] * step;
-    }
-    for (int i = 0; i < pairs; ++i) p.f_hi[i] = (float)f[i], p.f_lo[i] = (float)(f[i] - (double)p.f_hi[i]);
-  }
+  if (a->rope_dims > 0) set_rates(&p.rates, a->rope_base, a->rope_dims);
   const cudaStream_t st = (cudaStream_t)cuda_stream;
   // Few tokens: more threads each, for the latency (256 tokens of 48 heads of 128: 3.8
   // us with 256 threads, 4.4 with 128); many: fewer, for the throughput (32,768: 129 us

@@ -1,5 +1,6 @@
 """The operators of a batched decode step on torch CUDA tensors: gpt_kv_append, gpt_decode_attention and
-gpt_next_token of the C ABI (also reached as ``binding.kv_append`` and so on).
+gpt_next_token of the C ABI (also reached as ``binding.kv_append`` and so on), the first two over a cache in 8 bits
+(gpt_kv_append_fp8, gpt_decode_attention_fp8), and gpt_sample_token.
 
 Every tensor's device, type, shape and strides are checked before the call; a mismatch raises
 GptError(INVALID_ARG).  Indices that live on the device are checked by the kernels and reported in
@@ -27,6 +28,7 @@ except ImportError as e:
 
 _C.init(*(ctypes.cast(getattr(B.load(), f), ctypes.c_void_p).value
           for f in ("gpt_kv_append", "gpt_decode_attention", "gpt_decode_attention_workspace", "gpt_next_token",
+                    "gpt_kv_append_fp8", "gpt_decode_attention_fp8", "gpt_decode_attention_fp8_workspace", "gpt_sample_token",
                     "gpt_last_error")), B.GptError)
 
 
@@ -65,3 +67,33 @@ def next_token(logits, history=None, history_lens=None, prompt_lens=None, repeti
     logits themselves."""
     return _C.next_token(logits, history, history_lens, prompt_lens, repetition, presence, frequency, bias_ids, bias_values,
                          allowed, out, status, stream)
+
+
+def kv_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, before, starts=None, q=None, rope_dims: int = 0,
+                  rope_base: float = 10000.0, q_out=None, status=None, stream=None):
+    """gpt_kv_append_fp8: k, v [tokens, kv heads, head size] into the paged cache in 8 bits (k_cache, v_cache
+    float8_e4m3fn [pages, page size, kv heads, head size], k_scale, v_scale float32 [pages, kv heads], page_table as in
+    kv_append).  The tokens of sequence s are rows starts[s] .. starts[s+1] - 1 (``starts`` int32 [sequences + 1]; None: row
+    s alone), at positions from ``before[s]`` on (int32 [sequences]; negative: none of them is written).  A page that gets a
+    token at its first position starts anew; its old scales do not matter.
+
+    q, ``q_out`` and the result as in kv_append."""
+    return _C.kv_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, before, starts, q, rope_dims, rope_base, q_out,
+                            status, stream)
+
+
+def decode_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, scale: float | None = None, out=None,
+                         status=None, stream=None):
+    """gpt_decode_attention_fp8: decode_attention over a cache in 8 bits (as in kv_append_fp8; q float32 or bfloat16).
+
+    Returns (out like q, lse float32 [sequences, heads])."""
+    return _C.decode_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, scale, out, status, stream)
+
+
+def sample_token(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
+    """gpt_sample_token: a token of each row of logits [rows, vocab] (float32 or bfloat16) drawn with ``uniform`` (float32
+    [rows], in [0, 1)), ``temperature``, ``top_p``, ``min_p`` (float32 [rows]) and ``top_k`` (int32 [rows]); None, top_k < 1,
+    top_p >= 1 and min_p <= 0: no such limit; temperature 0: the greedy choice.
+
+    Returns (token int32 [rows], logprob float32 [rows]: of the token among those kept, kept int32 [rows]: their number)."""
+    return _C.sample_token(logits, uniform, temperature, top_k, top_p, min_p, stream)
