@@ -8,6 +8,10 @@
 // rising id; with the composite key (z's order, ~id) of a token, which is its own, the kept
 // tokens are those at or above the last kept one's.
 //
+// Rows without limits need one pass and no exact sum of all weights: their sums in fp32, good to
+// 2^-21, name the token unless the number falls that near a border between two; only then
+// the weights are summed as integers.
+//
 // A row is the work of a cluster of blocks, each with a range of its ids, each warp with a
 // part of that.  The logits are read again in each pass (from L2; nothing is written):
 //  1. the largest z;
@@ -34,6 +38,7 @@ constexpr int kBlocks = 8;        // of a cluster at most
 constexpr int kBins = 1024;
 constexpr int kList = 1024;
 constexpr int kTable = 1024;
+constexpr int kPieces = 8;        // of a warp's range, where sums are in fp32
 using u64 = unsigned long long;
 
 struct SampleParams {
@@ -116,6 +121,79 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* z, float* x) {
   Piece<__nv_bfloat16>::unpack(u, x);
 }
 
+// 2^n, 0 and the largest power where that is too small or large.
+__device__ __forceinline__ float power(int n) { return __uint_as_float((uint32_t)min(max(n + 127, 0), 254) << 23); }
+
+// A sum of 2^(c z) over a thread's tokens, as (sum + rest) 2^ref.
+// c z is split into an integer and a fraction of at most 1/2 (a product with c in two floats: good
+// to 2^-25), powers of the integer part are exact, and of the rounded sums of eight only the three
+// roundings inside are not carried along.  Together with ex2.approx (2^-22): 2^-21.
+struct FastSum {
+  float c_hi, c_lo, inv_c;
+  float sum, rest, top;
+  float low, high;   // z outside change nothing, or need another ref
+  int ref, missing;  // missing: of the units, what is no token
+  bool bad;          // too large for the split
+  __device__ __forceinline__ void start(float hi, float lo) {
+    c_hi = hi, c_lo = lo, inv_c = 1.f / hi;
+    clear(), missing = 0, top = -INFINITY, bad = false;
+  }
+  __device__ __forceinline__ void clear() { sum = rest = 0.f, low = high = -INFINITY, ref = -(1 << 24); }
+  __device__ __forceinline__ void add(const float* x) {
+    float m = x[0], all = x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = fmaxf(m, x[i]), all += x[i];
+    if (!(all > -INFINITY))
+#pragma unroll
+      for (int i = 0; i < 8; ++i) missing += !(x[i] > -INFINITY);
+    if (!(m > low)) return;
+    top = fmaxf(top, m);
+    if (m > high) {
+      const float at = m * c_hi;
+      if (!(fabsf(at) < 0x1p21f)) {
+        bad = true;
+        return;
+      }
+      const int now = __float2int_rn(at);
+      const float keep = power(ref - now);
+      sum *= keep, rest *= keep, ref = now;
+      low = (float)(now - 100) * inv_c, high = (float)(now + 40) * inv_c;
+    }
+    constexpr float kMagic = 12582912.f;  // 1.5 2^23
+    const int less = __float_as_int(kMagic) + ref;
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float z = fmaxf(x[i], low), up = __fmaf_rn(z, c_hi, kMagic), n = __fsub_rn(up, kMagic);
+      const float r = __fmaf_rn(z, c_lo, __fmaf_rn(z, c_hi, -n));
+      float f;
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(r));
+      w[i] = __int_as_float(__float_as_int(f) + ((__float_as_int(up) - less) << 23));
+    }
+#pragma unroll
+    for (int k = 1; k < 8; k *= 2)
+#pragma unroll
+      for (int i = 0; i < 8; i += 2 * k) w[i] += w[i + k];
+    two_sum(w[0], 0.f);
+  }
+  __device__ __forceinline__ void two_sum(float v, float more) {  // sum + rest += v + more, exactly but for the rests' roundings
+    const float s = __fadd_rn(sum, v), t = __fsub_rn(s, sum);
+    rest = __fadd_rn(rest, __fadd_rn(more, __fadd_rn(__fsub_rn(sum, __fsub_rn(s, t)), __fsub_rn(v, t))));
+    sum = s;
+  }
+  // The warp's sum in every lane, with one ref.
+  __device__ __forceinline__ void join_warp() {
+    const int all = __reduce_max_sync(0xffffffffu, ref);
+    const float keep = power(ref - all);
+    sum *= keep, rest *= keep, ref = all;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) {
+      const float v = __shfl_xor_sync(0xffffffffu, sum, x), more = __shfl_xor_sync(0xffffffffu, rest, x);
+      two_sum(v, more);
+    }
+  }
+};
+
 template <typename T>
 struct RowView {
   const T* z;
@@ -153,6 +231,9 @@ struct Shared {
   };
   u64 list[kList];
   u64 scratch[kWarps], parts[kWarps];
+  struct { float sum, rest; int ref; u64 upto; } pieces[kWarps * kPieces];  // of the warps' ranges
+  struct { u64 before, below, under; int piece; } fast;  // where the number falls
+  double drop;
   u64 slots[2][3][kBlocks];  // values of the cluster's blocks, in turns
   struct { u64 before; uint32_t bin, count; int way; } found;  // (the first block's)
   uint32_t listed;
@@ -253,9 +334,148 @@ __global__ void __launch_bounds__(kThreads, 3) sample_token_kernel(const __grid_
   };
   if (blocks > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
 
-  // 1. the first token in order
+  auto make_table = [&] {
+    for (int i = tid; i < kTable; i += kThreads) sm.table[i] = __umul64hi(p.coarse[i >> 5], p.fine[i & 31]) << 1;
+  };
+  auto log_of = [&](float w, float sum) { return logf(__fdiv_rn(w, sum)); };
+  // c = log2 e / T in two floats
+  float c_hi = 0.f, c_lo = 0.f;
+  if (temperature < INFINITY) {
+    constexpr double kLog2e = 1.442695040888963407;
+    constexpr float kHi = (float)kLog2e, kLo = (float)(kLog2e - (double)kHi);
+    const float t = fmaxf(temperature, 0x1p-126f);
+    c_hi = __fdiv_rn(kHi, t), c_lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-c_hi, t, kHi), kLo), t);
+  }
+  Weigher weight;
+  weight.table = sm.table, weight.unit = p.unit;
+  auto set_top = [&](float m) { weight.mh = 0.5f * m, weight.c_hi = 2.f * c_hi, weight.c_lo = 2.f * c_lo, weight.infinite = m == INFINITY; };
+
   u64 best = 0;
+  const bool limits = (top_k >= 1 && top_k < a.vocab) || top_p < 1.f || min_p > 0.f;
+  if (temperature > 0.f && !limits && c_hi > 1e-30f) {
+    FastSum f;
+    f.start(c_hi, c_lo);
+    const int steps = (w1 - w0 + 31) / 32, each = (steps + 2 * kPieces - 1) / (2 * kPieces) * 64;  // units of a piece
+    {
+      float x[2][8];
+      if (w0 + lane < w1) row.load(w0 + lane, x[0]);
+      for (int i = 0; i < kPieces; ++i) {
+        const int end = min(w1, w0 + (i + 1) * each);
+        f.clear();
+        for (int w = w0 + i * each + lane; w < end; w += 64) {
+          if (w + 32 < w1) row.load(w + 32, x[1]);
+          f.add(x[0]);
+          if (w + 64 < w1) row.load(w + 64, x[0]);
+          if (w + 32 < end) f.add(x[1]);
+        }
+        __syncwarp();
+        f.join_warp();
+        auto& piece = sm.pieces[warp * kPieces + i];
+        if (lane == 0) piece.sum = f.sum, piece.rest = f.rest, piece.ref = f.ref;
+      }
+    }
+    const uint32_t gone = __reduce_add_sync(0xffffffffu, f.missing), bad = __any_sync(0xffffffffu, f.bad);
+    const u64 top = warp_max(composite(f.top, 0));
+    if (lane == 0) sm.scratch[warp] = top, sm.parts[warp] = (u64)bad << 32 | gone;
+    __syncthreads();
+    u64 first = 0, flags = 0, sum = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) first = max(first, sm.scratch[i]), flags += sm.parts[i];
+    // the pieces as integers, in units of 2^(1 - U) of 2^mine: with the largest weight about 1
+    const int mine = first && flags >> 32 == 0 ? __float2int_rn(value_of((uint32_t)(first >> 32)) * c_hi) : -(1 << 22);
+    if (warp == 0) {
+      auto whole = [&](const auto& piece) {
+        const int up = piece.ref - mine + p.unit - 1;  // in two factors: up to 2^48 and more down than a float goes
+        const float a = power(min(up, 0)), b = power(max(up, 0));
+        return (u64)(__float2ll_rn(piece.sum * a * b) + __float2ll_rn(piece.rest * a * b));
+      };
+      const u64 v0 = whole(sm.pieces[2 * lane]), v1 = whole(sm.pieces[2 * lane + 1]);
+      u64 upto = v0 + v1;
+#pragma unroll
+      for (int y = 1; y < 32; y <<= 1) {
+        const u64 t = __shfl_up_sync(0xffffffffu, upto, y);
+        if (lane >= y) upto += t;
+      }
+      sm.pieces[2 * lane].upto = upto - v1, sm.pieces[2 * lane + 1].upto = upto;
+      sum = __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (blocks > 1) asm volatile("barrier.cluster.wait;" ::: "memory");
+    const u64(*got)[kBlocks] = share(sum, (u64)(uint32_t)mine << 32 | (uint32_t)(first >> 32), flags);  // (by the first warp's threads)
+    uint32_t top_key = 0;
+    int ref = -(1 << 22);
+    flags = 0;
+    for (int i = 0; i < blocks; ++i) top_key = max(top_key, (uint32_t)got[1][i]), ref = max(ref, (int)(got[1][i] >> 32)), flags += got[2][i];
+    if (top_key == 0) {
+      if (part == 0 && tid == 0) answer(-1, -INFINITY, 0);
+      return;
+    }
+    const float m = value_of(top_key);
+    set_top(m);
+    int accepted = 0;
+    if (flags >> 32 == 0) {
+      auto moved = [&](u64 v, int from) { return ref - from < 64 ? v >> (ref - from) : 0ull; };
+      u64 all = 0, before = 0;
+      for (int i = 0; i < blocks; ++i) {
+        if (i == part) before = all;
+        all += moved(got[0][i], (int)(got[1][i] >> 32));
+      }
+      // The piece in which the number falls, surely: each sum is off by 2^-21 of itself and
+      // some units.
+      if (tid == 0) sm.fast.piece = -1;
+      __syncthreads();
+      const u64 goal = u >= 1.f ? all : u > 0.f ? part_of(u, all, false) : 0;
+      if (tid < kWarps * kPieces) {
+        const u64 from = before + (tid ? moved(sm.pieces[tid - 1].upto, mine) : 0), to = before + moved(sm.pieces[tid].upto, mine);
+        const u64 off = ((from + goal) >> 21) + 256;
+        if (goal >= from + off) {
+          const u64 local = goal - from;
+          const u64 off_to = ((to + goal) >> 21) + 256;
+          if (to > goal + off_to) sm.fast.piece = tid, sm.fast.before = from, sm.fast.below = local - min(local, off), sm.fast.under = local + off;
+        }
+      }
+      __syncthreads();
+      const int piece = sm.fast.piece;
+      if (piece >= 0) {
+        make_table();
+        __syncthreads();
+        const int s = b0 + (int)((int64_t)(piece / kPieces) * (b1 - b0) / kWarps), e = b0 + (int)((int64_t)(piece / kPieces + 1) * (b1 - b0) / kWarps);
+        const int piece_units = ((e - s + 31) / 32 + 2 * kPieces - 1) / (2 * kPieces) * 64;
+        const int s0 = s + piece % kPieces * piece_units, s1 = min(e, s0 + piece_units);
+        const int per = (s1 - s0 + kThreads - 1) / kThreads, t0 = min(s1, s0 + tid * per), t1 = min(s1, t0 + per);
+        u64 own = 0, total;
+        row.each(t0, t1, 0, 1, [&](const float* x, int) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) own += weight(x[i]);
+        });
+        u64 upto = block_scan(own, sm.scratch, &total) - own;
+        // from these sums' units to the weights', 2^-U of 2^(c m): to 2^-20
+        const float up = exp2f(1.f - fmaf(m, c_lo, fmaf(m, c_hi, -(float)ref)));
+        const u64 below = (u64)((float)sm.fast.below * up * (1.f - 0x1p-20f)), under = (u64)((float)sm.fast.under * up * (1.f + 0x1p-20f)) + 1;
+        if (upto <= below && upto + own > under)
+          row.each(t0, t1, 0, 1, [&](const float* x, int id) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const u64 w = weight(x[i]);
+              if (upto <= below && upto + w > under) {
+                answer(id + i, log_of((float)w, (float)all * up), units * 8 - (int)flags);
+                accepted = 1;
+              }
+              upto += w;
+            }
+          });
+      }
+      accepted = __syncthreads_or(accepted);
+    }
+    const u64(*verdict)[kBlocks] = share(accepted, 0, 0);
+    for (int i = 0; i < blocks; ++i) accepted |= (int)verdict[0][i];
+    if (accepted) return;
+    make_table();
+    __syncthreads();
+  } else {
+  // 1. the first token in order
   {
+    // (doubles are slow: by one warp, while the logits are under way)
+    if (min_p > 0.f && min_p <= 1.f && warp == kWarps - 1) sm.drop = log((double)min_p) * (double)temperature;
     float top = -INFINITY;
     int at = 0;
     row.each(w0, w1, lane, 32, [&](const float* x, int id) {
@@ -271,11 +491,11 @@ __global__ void __launch_bounds__(kThreads, 3) sample_token_kernel(const __grid_
     });
     best = warp_max(composite(top, at));
     if (lane == 0) sm.scratch[warp] = best;
-    for (int i = tid; i < kTable; i += kThreads) sm.table[i] = __umul64hi(p.coarse[i >> 5], p.fine[i & 31]) << 1;
+    make_table();
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) best = max(best, sm.scratch[w]);
-    if (blocks > 1) asm volatile("barrier.cluster.wait;" ::: "memory");  // the others have begun
+    if (blocks > 1) asm volatile("barrier.cluster.wait;" ::: "memory");
     const u64(*got)[kBlocks] = share(best, 0, 0);
     for (int i = 0; i < blocks; ++i) best = max(best, got[0][i]);
   }
@@ -283,19 +503,15 @@ __global__ void __launch_bounds__(kThreads, 3) sample_token_kernel(const __grid_
     if (part == 0 && tid == 0) best == 0 ? answer(-1, -INFINITY, 0) : answer(id_of(best), 0.f, 1);
     return;
   }
-  const float m = value_of((uint32_t)(best >> 32));
-  Weigher weight;
-  {
-    const double c = 2.885390081777926815 / (double)fmaxf(temperature, 0x1p-126f);  // of halves
-    weight.table = sm.table, weight.mh = 0.5f * m, weight.c_hi = (float)c, weight.c_lo = (float)(c - (double)weight.c_hi);
-    weight.unit = p.unit, weight.infinite = m == INFINITY;
+  set_top(value_of((uint32_t)(best >> 32)));
   }
+  const float m = 2.f * weight.mh;
   // what min_p keeps
   u64 least = 1;
   if (min_p > 1.f) {
     least = best;
   } else if (min_p > 0.f) {
-    const float from = m == INFINITY ? m : __double2float_ru((double)m + log((double)min_p) * (double)temperature);
+    const float from = m == INFINITY ? m : __double2float_ru((double)m + sm.drop);
     least = min((u64)key_of(from) << 32, best);
     if (least == 0) least = 1;
   }
@@ -308,7 +524,6 @@ __global__ void __launch_bounds__(kThreads, 3) sample_token_kernel(const __grid_
     const uint32_t at = atomicAdd(listed, 1u);
     if (at < kList) cluster.map_shared_rank(sm.list, 0)[at] = comp;
   };
-  auto log_of = [&](u64 w, u64 sum) { return (float)log((double)w / (double)sum); };
 
   // By the first block: the draw among the list's first n, in falling order, whose weights are in sm.weights.
   auto draw_from_list = [&](int n, u64 sum) {
@@ -329,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_token_kernel(const __grid_
     u64 upto = block_scan(mine, sm.scratch, &total) - mine;
     for (int i = tid * each; i < min(n, (tid + 1) * each); ++i) {
       const u64 w = sm.weights[(uint32_t)by_id[i]];
-      if (upto < goal && upto + w >= goal) answer((int)~(uint32_t)(by_id[i] >> 32), log_of(w, sum), n);
+      if (upto < goal && upto + w >= goal) answer((int)~(uint32_t)(by_id[i] >> 32), log_of((float)w, (float)sum), n);
       upto += w;
     }
   };
@@ -529,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_token_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const u64 w = weigh(x, id, i);
-      if (upto < goal && upto + w >= goal) answer(id + i, log_of(w, sum), (int)kept);
+      if (upto < goal && upto + w >= goal) answer(id + i, log_of((float)w, (float)sum), (int)kept);
       upto += w;
     }
   });
