@@ -8,19 +8,18 @@
 // rising id; with the composite key (z's order, ~id) of a token, which is its own, the kept
 // tokens are those at or above the last kept one's.
 //
-// Rows without limits need one pass and no exact sum of all weights: their sums in fp32, good to
-// 2^-21, name the token unless the number falls that near a border between two; only then
-// the weights are summed as integers.
-//
 // A row is the work of a cluster of blocks, each with a range of its ids, each warp with a
-// part of that.  The logits are read again in each pass (from L2; nothing is written):
-//  1. the largest z;
-//  2. for a limit, counts (and weights) in 1,024 bins of equal width below it, of which one
-//     holds the limit's last token;
-//  3. what lies in that bin, or, where it is few, all above its end, into a list that the
-//     first block sorts: where the list holds all, it draws from it;
-//  4. otherwise the weights of the kept tokens, a sum for each warp, then the warp's range in
-//     which the number falls, a token after the other.
+// part of that.  Nothing is written; the logits are read again (from L2) where a row needs
+// more than one pass:
+//  - without limits: one pass of sums in fp32, good to 2^-21, names the token unless the number
+//    falls that near a border between two; only then the weights are summed as integers;
+//  - with a limit: a first pass takes the largest logit of each thread.  The n-th largest of these
+//    has at least n tokens at or above it, so that the tokens at or above its bin (1,024 of equal
+//    width below the row's largest) hold the first top_k, or, of 160, mostly what top_p keeps.  A
+//    second pass lists them (and sums all weights for top_p alone); the first block takes the
+//    limits and draws from the list, by counting for each entry what lies before it;
+//  - where a list does not hold what it must: slow_row, bins of counts and sums of all tokens, as
+//    many rounds as it takes, then the sums of the kept ones by warp.
 #include <cooperative_groups.h>
 
 #include <cmath>
@@ -37,6 +36,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBlocks = 8;        // of a cluster at most
 constexpr int kBins = 1024;
 constexpr int kList = 1024;
+constexpr int kShort = 256;       // entries of a list that need no sorting
+constexpr int kGuess = 160;       // of the largest logits, for top_p alone
 constexpr int kTable = 1024;
 constexpr int kPieces = 8;        // of a warp's range, where sums are in fp32
 using u64 = unsigned long long;
@@ -78,11 +79,9 @@ struct Weigher {
     constexpr float kL = (float)kLn2, kL42 = (float)(kL * kUp), kRest42 = (float)((kLn2 - (double)kL) * kUp);
     constexpr float kC2 = (float)(kLn2 * kLn2 / 2 * kUp), kC3 = (float)(kLn2 * kLn2 * kLn2 / 6 * kUp);
     constexpr float kMagic = 12288.f;  // 1.5 2^13: sums with it are multiples of 2^-10
-    if (infinite) return z == INFINITY ? 1ull << unit : 0ull;
     const float zh = __fmul_rn(z, 0.5f), s = __fsub_rn(zh, mh), t = __fsub_rn(s, zh);
     const float e = __fsub_rn(__fsub_rn(zh, __fsub_rn(s, t)), __fadd_rn(mh, t));
-    const float p = __fmul_rn(s, c_hi);
-    if (!(p > -64.f)) return 0ull;
+    const float p = fmaxf(__fmul_rn(s, c_hi), -100.f);  // (NaN too) nothing is left of 2^-100
     const float up = __fadd_rn(p, kMagic), r = __fsub_rn(p, __fsub_rn(up, kMagic));
     const float low = __fmaf_rn(s, c_lo, __fmaf_rn(e, c_hi, __fmaf_rn(s, c_hi, -p)));
     const int J = (int)(__float_as_uint(up) - __float_as_uint(kMagic));
@@ -91,8 +90,8 @@ struct Weigher {
     const int more = __float2int_rn(a) + __float2int_rn(rest);
     const u64 base = table[J & (kTable - 1)];
     const u64 w = base + (u64)(((int64_t)more * (int)(base >> 32)) >> 10);
-    const int shift = 61 - unit - (J >> 10);
-    return shift < 64 ? ((w >> shift) + 1) >> 1 : 0ull;
+    const u64 rounded = ((w >> min(61 - unit - (J >> 10), 63)) + 1) >> 1;
+    return infinite ? (z == INFINITY ? 1ull << unit : 0ull) : rounded;
   }
 };
 
@@ -223,20 +222,40 @@ struct RowView {
   }
 };
 
+// The tokens at or above a composite key (of 1: all of them).
+struct Kept {
+  float z;
+  int id;
+  __device__ __forceinline__ explicit Kept(u64 last) : z(last > 1 ? value_of((uint32_t)(last >> 32)) : -INFINITY), id(last > 1 ? id_of(last) : -1) {}
+  __device__ __forceinline__ bool has(float x, int i) const { return x > z || (x == z && i <= id); }
+  __device__ __forceinline__ bool none(const float* x) const {  // of eight
+    float m = x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = fmaxf(m, x[i]);
+    return !(m >= z);
+  }
+};
+
 struct Shared {
   u64 table[kTable];
   union {
     struct { u64 mass[kBins]; uint32_t count[kBins]; } bins;
-    u64 weights[kList];
+    u64 weights[kList];  // of the entries of `all`
   };
-  u64 list[kList];
+  union {
+    float maxima[kBlocks * kThreads];  // of the cluster's threads (in the first block)
+    u64 all[kList];                    // its blocks' lists, side by side (in the first block)
+  };
+  u64 list[kList];                     // of this block
   u64 scratch[kWarps], parts[kWarps];
   struct { float sum, rest; int ref; u64 upto; } pieces[kWarps * kPieces];  // of the warps' ranges
-  struct { u64 before, below, under; int piece; } fast;  // where the number falls
+  u64 slots[2][3][kBlocks];            // values of the cluster's blocks, in turns
+  union {
+    struct { u64 before, below, under; int piece; } fast;       // where the number falls
+    struct { u64 before, all; uint32_t bin, count; int way; } found;  // (the first block's)
+  };
   double drop;
-  u64 slots[2][3][kBlocks];  // values of the cluster's blocks, in turns
-  struct { u64 before; uint32_t bin, count; int way; } found;  // (the first block's)
-  uint32_t listed;
+  uint32_t listed, gathered, base;
   int chosen;
 };
 
@@ -287,37 +306,64 @@ __device__ __forceinline__ void sort_falling(u64* x, int n) {
   __syncthreads();
 }
 
+// What a thread knows of its row.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) sample_token_kernel(const __grid_constant__ SampleParams p) {
-  __shared__ Shared sm;
-  cg::cluster_group cluster = cg::this_cluster();
-  const gpt_sample_token_args& a = p.a;
-  const int blocks = cluster.num_blocks(), part = cluster.block_rank();
-  after_stream();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t b = blockIdx.x / blocks;
+struct Sampler {
+  const gpt_sample_token_args& a;
+  Shared& sm;
+  cg::cluster_group cluster;
   RowView<T> row;
-  row.z = (const T*)a.logits + b * a.logits_stride, row.vocab = a.vocab;
-  row.shift = (int)((reinterpret_cast<uintptr_t>(row.z) / sizeof(T)) & 7);
-  const int units = (int)(((int64_t)a.vocab + row.shift + 7) / 8);
-  const int b0 = (int)((int64_t)part * units / blocks), b1 = (int)((int64_t)(part + 1) * units / blocks);
-  const int w0 = b0 + (int)((int64_t)warp * (b1 - b0) / kWarps), w1 = b0 + (int)((int64_t)(warp + 1) * (b1 - b0) / kWarps);
-  const float temperature = a.temperature ? a.temperature[b] : 1.f, u = a.uniform[b];
-  const int top_k = a.top_k ? a.top_k[b] : 0;
-  const float top_p = a.top_p ? a.top_p[b] : 1.f, min_p = a.min_p ? a.min_p[b] : 0.f;
+  int tid, lane, warp, blocks, part;
+  int units, b0, b1, w0, w1;  // of the row; the block's and the warp's
+  int64_t b;
+  float u, temperature, top_p, min_p, c_hi, c_lo;
+  int top_k;
+  int turn;
+  Weigher weight;
+
+  __device__ __forceinline__ Sampler(const SampleParams& p, Shared& shared) : a(p.a), sm(shared), cluster(cg::this_cluster()) {
+    tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    blocks = cluster.num_blocks(), part = cluster.block_rank(), turn = 0;
+    b = blockIdx.x / blocks;
+    row.z = (const T*)a.logits + b * a.logits_stride, row.vocab = a.vocab;
+    row.shift = (int)((reinterpret_cast<uintptr_t>(row.z) / sizeof(T)) & 7);
+    units = (int)(((int64_t)a.vocab + row.shift + 7) / 8);
+    b0 = (int)((int64_t)part * units / blocks), b1 = (int)((int64_t)(part + 1) * units / blocks);
+    w0 = warp_begin(warp), w1 = warp_begin(warp + 1);
+    u = a.uniform[b], temperature = a.temperature ? a.temperature[b] : 1.f;
+    top_k = a.top_k ? a.top_k[b] : 0;
+    if (top_k < 1 || top_k >= a.vocab) top_k = 0;
+    top_p = a.top_p ? a.top_p[b] : 1.f, min_p = a.min_p ? a.min_p[b] : 0.f;
+    // c = log2 e / T in two floats
+    c_hi = c_lo = 0.f;
+    if (temperature < INFINITY) {
+      constexpr double kLog2e = 1.442695040888963407;
+      constexpr float kHi = (float)kLog2e, kLo = (float)(kLog2e - (double)kHi);
+      const float t = fmaxf(temperature, 0x1p-126f);
+      c_hi = __fdiv_rn(kHi, t), c_lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-c_hi, t, kHi), kLo), t);
+    }
+    weight.table = sm.table, weight.unit = p.unit;
+  }
+  __device__ __forceinline__ int warp_begin(int w) const { return b0 + (int)((int64_t)w * (b1 - b0) / kWarps); }
+  __device__ __forceinline__ void set_top(float m) {
+    weight.mh = 0.5f * m, weight.c_hi = 2.f * c_hi, weight.c_lo = 2.f * c_lo, weight.infinite = m == INFINITY;
+  }
+  __device__ __forceinline__ float top() const { return 2.f * weight.mh; }
 
   // A value of each block to all of them; what the cluster's blocks wrote before is visible after it.
-  int turn = 0;
-  auto share = [&](u64 x, u64 y, u64 z) {  // by all threads of the block alike
+  __device__ __forceinline__ const u64 (*share(u64 x, u64 y, u64 z))[kBlocks] {  // (the first warp's threads' values)
     if (tid < blocks) {
       u64(*to)[kBlocks] = cluster.map_shared_rank(sm.slots[turn & 1], tid);
       to[0][part] = x, to[1][part] = y, to[2][part] = z;
     }
+    sync_all();
+    return sm.slots[turn++ & 1];
+  }
+  __device__ __forceinline__ void sync_all() {
     if (blocks > 1) cluster.sync();
     else __syncthreads();
-    return sm.slots[turn++ & 1];
-  };
-  auto block_sum = [&](u64 v) {
+  }
+  __device__ __forceinline__ u64 block_sum(u64 v) {
     v = warp_sum(v);
     __syncthreads();
     if (lane == 0) sm.scratch[warp] = v;
@@ -326,36 +372,141 @@ __global__ void __launch_bounds__(kThreads, 3) sample_token_kernel(const __grid_
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) v += sm.scratch[w];
     return v;
-  };
-  auto answer = [&](int token, float logprob, int kept) {
+  }
+  __device__ __forceinline__ void answer(int token, float logprob, int kept) {
     if (a.token) a.token[b] = token;
     if (a.logprob) a.logprob[b] = logprob;
     if (a.kept) a.kept[b] = kept;
-  };
-  if (blocks > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
-
-  auto make_table = [&] {
-    for (int i = tid; i < kTable; i += kThreads) sm.table[i] = __umul64hi(p.coarse[i >> 5], p.fine[i & 31]) << 1;
-  };
-  auto log_of = [&](float w, float sum) { return logf(__fdiv_rn(w, sum)); };
-  // c = log2 e / T in two floats
-  float c_hi = 0.f, c_lo = 0.f;
-  if (temperature < INFINITY) {
-    constexpr double kLog2e = 1.442695040888963407;
-    constexpr float kHi = (float)kLog2e, kLo = (float)(kLog2e - (double)kHi);
-    const float t = fmaxf(temperature, 0x1p-126f);
-    c_hi = __fdiv_rn(kHi, t), c_lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-c_hi, t, kHi), kLo), t);
   }
-  Weigher weight;
-  weight.table = sm.table, weight.unit = p.unit;
-  auto set_top = [&](float m) { weight.mh = 0.5f * m, weight.c_hi = 2.f * c_hi, weight.c_lo = 2.f * c_lo, weight.infinite = m == INFINITY; };
+  __device__ __forceinline__ float log_of(float w, float sum) { return logf(__fdiv_rn(w, sum)); }
 
-  u64 best = 0;
-  const bool limits = (top_k >= 1 && top_k < a.vocab) || top_p < 1.f || min_p > 0.f;
-  if (temperature > 0.f && !limits && c_hi > 1e-30f) {
+  // Bins of equal width from the largest logit down; the last one goes on to the end.
+  __device__ __forceinline__ float per_bin() const { return kBins / (32.f * fmaxf(1.f, fminf(temperature, 1e30f))); }
+  __device__ __forceinline__ int bin_of(float z, float each) const { return (int)fminf((top() - z) * each, (float)(kBins - 1)); }
+
+  // The least composite key that min_p keeps.
+  __device__ __forceinline__ u64 least(u64 best) const {
+    if (min_p > 1.f) return best;
+    if (!(min_p > 0.f)) return 1;
+    const uint32_t key = key_of(top() == INFINITY ? INFINITY : __double2float_ru((double)top() + sm.drop));
+    return key ? min((u64)key << 32 | 0x80000000u, best) : 1;  // (any id)
+  }
+
+  // A pass that lists the tokens that f names (f(eight logits, the first's id, name)), then all
+  // blocks' lists in the first block's sm.all, sm.gathered of them; those behind kList are lost.
+  template <typename F>
+  __device__ __forceinline__ void gather(F f) {
+    if (tid == 0) sm.listed = 0;
+    __syncthreads();
+    row.each(w0, w1, lane, 32, [&](const float* x, int id) {
+      f(x, id, [&](float z, int i) {
+        const uint32_t at = atomicAdd(&sm.listed, 1u);
+        if (at < kList) sm.list[at] = composite(z, i);
+      });
+    });
+    __syncthreads();
+    const uint32_t n = sm.listed;
+    if (tid == 0 && n) sm.base = atomicAdd(cluster.map_shared_rank(&sm.gathered, 0), n);
+    __syncthreads();
+    u64* all = cluster.map_shared_rank(sm.all, 0);
+    for (uint32_t i = tid; i < min(n, (uint32_t)kList); i += kThreads)
+      if (sm.base + i < kList) all[sm.base + i] = sm.list[i];
+  }
+
+  // By the first block, of the n <= kShort entries of sm.all: the limits, and the draw among what
+  // they keep.  whole: the sum of all tokens' weights, for top_p alone; false: the entries do not reach it.
+  __device__ __forceinline__ bool finish_short(int n, u64 best, u64 whole) {
+    const u64 mine = tid < n ? sm.all[tid] : 0, from = least(best);
+    u64 w = tid < n ? weight(value_of((uint32_t)(mine >> 32))) : 0;
+    if (tid < n) sm.weights[tid] = w;
+    __syncthreads();
+    u64 above = 0;
+    int rank = 0;
+    if (tid < n)
+      for (int i = 0; i < n; ++i)
+        if (sm.all[i] > mine) ++rank, above += sm.weights[i];
+    bool keep = tid < n && mine >= from && (top_k == 0 || rank < top_k);
+    if (top_p < 1.f) {
+      const u64 sum = block_sum(tid < n && (top_k == 0 || rank < top_k) ? w : 0);
+      const u64 goal = max(top_p > 0.f ? part_of(top_p, top_k ? sum : whole, true) : 0, 1ull);
+      if (sum < goal) return false;
+      keep = keep && above < goal;
+    }
+    if (!keep) w = 0;
+    const u64 sum = block_sum(w), kept = block_sum(keep);
+    if (tid < n) sm.weights[tid] = w;
+    __syncthreads();
+    const u64 goal = goal_of(u, sum);
+    u64 upto = 0;
+    if (w)
+      for (int i = 0; i < n; ++i)
+        if ((uint32_t)sm.all[i] > (uint32_t)mine) upto += sm.weights[i];  // a smaller id
+    if (w && upto < goal && upto + w >= goal) answer(id_of(mine), log_of((float)w, (float)sum), (int)kept);
+    return true;
+  }
+
+  // The entries of sm.all sorted, weights of the first n, and their sum.
+  __device__ __forceinline__ u64 weigh_list(int n) {
+    u64 sum = 0;
+    for (int i = tid; i < n; i += kThreads) {
+      const u64 w = weight(value_of((uint32_t)(sm.all[i] >> 32)));
+      sm.weights[i] = w, sum += w;
+    }
+    return block_sum(sum);
+  }
+  // How many of the first n it takes for a sum of at least `goal`.
+  __device__ __forceinline__ int fewest(int n, u64 goal) {
+    const int each = (n + kThreads - 1) / kThreads;
+    u64 mine = 0, total;
+    for (int i = tid * each; i < min(n, (tid + 1) * each); ++i) mine += sm.weights[i];
+    u64 upto = block_scan(mine, sm.scratch, &total) - mine;
+    for (int i = tid * each; i < min(n, (tid + 1) * each); ++i) {
+      if (upto < goal && upto + sm.weights[i] >= goal) sm.chosen = i + 1;
+      upto += sm.weights[i];
+    }
+    __syncthreads();
+    return sm.chosen;
+  }
+  // As finish_short, for up to kList entries.
+  __device__ __forceinline__ bool finish_long(int n, u64 best, u64 whole) {
+    sort_falling(sm.all, n);
+    int keep = top_k ? min(top_k, n) : n;
+    u64 sum = weigh_list(keep);
+    if (top_p < 1.f) {
+      const u64 goal = max(top_p > 0.f ? part_of(top_p, top_k ? sum : whole, true) : 0, 1ull);
+      if (sum < goal) return false;
+      keep = fewest(keep, goal);
+    }
+    const u64 from = least(best);
+    int above = 0;
+    for (int i = tid; i < keep; i += kThreads) above += sm.all[i] >= from;
+    keep = (int)block_sum(above);
+    sum = 0;
+    for (int i = tid; i < keep; i += kThreads) sum += sm.weights[i];
+    sum = block_sum(sum);
+    // by rising ids: falling ~id
+    for (int i = tid; i < keep; i += kThreads) sm.all[i] = (u64)(uint32_t)sm.all[i] << 32 | (uint32_t)i;
+    __syncthreads();
+    sort_falling(sm.all, keep);
+    const u64 goal = goal_of(u, sum);
+    const int each = (keep + kThreads - 1) / kThreads;
+    u64 mine = 0, total;
+    for (int i = tid * each; i < min(keep, (tid + 1) * each); ++i) mine += sm.weights[(uint32_t)sm.all[i]];
+    u64 upto = block_scan(mine, sm.scratch, &total) - mine;
+    for (int i = tid * each; i < min(keep, (tid + 1) * each); ++i) {
+      const u64 w = sm.weights[(uint32_t)sm.all[i]];
+      if (upto < goal && upto + w >= goal) answer((int)~(uint32_t)(sm.all[i] >> 32), log_of((float)w, (float)sum), keep);
+      upto += w;
+    }
+    return true;
+  }
+  __device__ __forceinline__ bool finish(int n, u64 best, u64 whole) { return n <= kShort ? finish_short(n, best, whole) : finish_long(n, best, whole); }
+
+  // Rows without limits.  True: done; otherwise set_top is.
+  __device__ __forceinline__ bool without_limits() {
     FastSum f;
     f.start(c_hi, c_lo);
-    const int steps = (w1 - w0 + 31) / 32, each = (steps + 2 * kPieces - 1) / (2 * kPieces) * 64;  // units of a piece
+    const int each = ((w1 - w0 + 31) / 32 + 2 * kPieces - 1) / (2 * kPieces) * 64;  // units of a piece
     {
       float x[2][8];
       if (w0 + lane < w1) row.load(w0 + lane, x[0]);
@@ -369,25 +520,25 @@ __global__ void __launch_bounds__(kThreads, 3) sample_token_kernel(const __grid_
           if (w + 32 < end) f.add(x[1]);
         }
         __syncwarp();
-        f.join_warp();
+        if (w0 + i * each < w1) f.join_warp();
         auto& piece = sm.pieces[warp * kPieces + i];
         if (lane == 0) piece.sum = f.sum, piece.rest = f.rest, piece.ref = f.ref;
       }
     }
     const uint32_t gone = __reduce_add_sync(0xffffffffu, f.missing), bad = __any_sync(0xffffffffu, f.bad);
-    const u64 top = warp_max(composite(f.top, 0));
-    if (lane == 0) sm.scratch[warp] = top, sm.parts[warp] = (u64)bad << 32 | gone;
+    const uint32_t key = __reduce_max_sync(0xffffffffu, key_of(f.top));
+    if (lane == 0) sm.scratch[warp] = key, sm.parts[warp] = (u64)bad << 32 | gone;
     __syncthreads();
     u64 first = 0, flags = 0, sum = 0;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) first = max(first, sm.scratch[i]), flags += sm.parts[i];
     // the pieces as integers, in units of 2^(1 - U) of 2^mine: with the largest weight about 1
-    const int mine = first && flags >> 32 == 0 ? __float2int_rn(value_of((uint32_t)(first >> 32)) * c_hi) : -(1 << 22);
+    const int mine = first && flags >> 32 == 0 ? __float2int_rn(value_of((uint32_t)first) * c_hi) : -(1 << 22);
     if (warp == 0) {
       auto whole = [&](const auto& piece) {
-        const int up = piece.ref - mine + p.unit - 1;  // in two factors: up to 2^48 and more down than a float goes
-        const float a = power(min(up, 0)), b = power(max(up, 0));
-        return (u64)(__float2ll_rn(piece.sum * a * b) + __float2ll_rn(piece.rest * a * b));
+        const int up = piece.ref - mine + weight.unit - 1;  // in two factors: up to 2^48 and more, down to nothing
+        const float x = power(min(up, 0)), y = power(max(up, 0));
+        return (u64)(__float2ll_rn(piece.sum * x * y) + __float2ll_rn(piece.rest * x * y));
       };
       const u64 v0 = whole(sm.pieces[2 * lane]), v1 = whole(sm.pieces[2 * lane + 1]);
       u64 upto = v0 + v1;
@@ -400,180 +551,172 @@ __global__ void __launch_bounds__(kThreads, 3) sample_token_kernel(const __grid_
       sum = __shfl_sync(0xffffffffu, upto, 31);
     }
     if (blocks > 1) asm volatile("barrier.cluster.wait;" ::: "memory");
-    const u64(*got)[kBlocks] = share(sum, (u64)(uint32_t)mine << 32 | (uint32_t)(first >> 32), flags);  // (by the first warp's threads)
+    const u64(*got)[kBlocks] = share(sum, (u64)(uint32_t)mine << 32 | (uint32_t)first, flags);
     uint32_t top_key = 0;
     int ref = -(1 << 22);
     flags = 0;
     for (int i = 0; i < blocks; ++i) top_key = max(top_key, (uint32_t)got[1][i]), ref = max(ref, (int)(got[1][i] >> 32)), flags += got[2][i];
     if (top_key == 0) {
       if (part == 0 && tid == 0) answer(-1, -INFINITY, 0);
-      return;
+      return true;
     }
     const float m = value_of(top_key);
     set_top(m);
+    if (flags >> 32) return false;
     int accepted = 0;
-    if (flags >> 32 == 0) {
-      auto moved = [&](u64 v, int from) { return ref - from < 64 ? v >> (ref - from) : 0ull; };
-      u64 all = 0, before = 0;
-      for (int i = 0; i < blocks; ++i) {
-        if (i == part) before = all;
-        all += moved(got[0][i], (int)(got[1][i] >> 32));
-      }
-      // The piece in which the number falls, surely: each sum is off by 2^-21 of itself and
-      // some units.
-      if (tid == 0) sm.fast.piece = -1;
-      __syncthreads();
-      const u64 goal = u >= 1.f ? all : u > 0.f ? part_of(u, all, false) : 0;
-      if (tid < kWarps * kPieces) {
-        const u64 from = before + (tid ? moved(sm.pieces[tid - 1].upto, mine) : 0), to = before + moved(sm.pieces[tid].upto, mine);
-        const u64 off = ((from + goal) >> 21) + 256;
-        if (goal >= from + off) {
-          const u64 local = goal - from;
-          const u64 off_to = ((to + goal) >> 21) + 256;
-          if (to > goal + off_to) sm.fast.piece = tid, sm.fast.before = from, sm.fast.below = local - min(local, off), sm.fast.under = local + off;
-        }
-      }
-      __syncthreads();
-      const int piece = sm.fast.piece;
-      if (piece >= 0) {
-        make_table();
-        __syncthreads();
-        const int s = b0 + (int)((int64_t)(piece / kPieces) * (b1 - b0) / kWarps), e = b0 + (int)((int64_t)(piece / kPieces + 1) * (b1 - b0) / kWarps);
-        const int piece_units = ((e - s + 31) / 32 + 2 * kPieces - 1) / (2 * kPieces) * 64;
-        const int s0 = s + piece % kPieces * piece_units, s1 = min(e, s0 + piece_units);
-        const int per = (s1 - s0 + kThreads - 1) / kThreads, t0 = min(s1, s0 + tid * per), t1 = min(s1, t0 + per);
-        u64 own = 0, total;
-        row.each(t0, t1, 0, 1, [&](const float* x, int) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) own += weight(x[i]);
-        });
-        u64 upto = block_scan(own, sm.scratch, &total) - own;
-        // from these sums' units to the weights', 2^-U of 2^(c m): to 2^-20
-        const float up = exp2f(1.f - fmaf(m, c_lo, fmaf(m, c_hi, -(float)ref)));
-        const u64 below = (u64)((float)sm.fast.below * up * (1.f - 0x1p-20f)), under = (u64)((float)sm.fast.under * up * (1.f + 0x1p-20f)) + 1;
-        if (upto <= below && upto + own > under)
-          row.each(t0, t1, 0, 1, [&](const float* x, int id) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const u64 w = weight(x[i]);
-              if (upto <= below && upto + w > under) {
-                answer(id + i, log_of((float)w, (float)all * up), units * 8 - (int)flags);
-                accepted = 1;
-              }
-              upto += w;
-            }
-          });
-      }
-      accepted = __syncthreads_or(accepted);
+    auto moved = [&](u64 v, int from) { return ref - from < 64 ? v >> (ref - from) : 0ull; };
+    u64 all = 0, before = 0;
+    for (int i = 0; i < blocks; ++i) {
+      if (i == part) before = all;
+      all += moved(got[0][i], (int)(got[1][i] >> 32));
     }
+    // The piece in which the number falls, surely: each sum is off by 2^-21 of itself and
+    // some units.
+    if (tid == 0) sm.fast.piece = -1;
+    __syncthreads();
+    const u64 goal = u >= 1.f ? all : u > 0.f ? part_of(u, all, false) : 0;
+    if (tid < kWarps * kPieces) {
+      const u64 from = before + (tid ? moved(sm.pieces[tid - 1].upto, mine) : 0), to = before + moved(sm.pieces[tid].upto, mine);
+      const u64 off = ((from + goal) >> 21) + 256, off_to = ((to + goal) >> 21) + 256;
+      if (goal >= from + off && to > goal + off_to)
+        sm.fast.piece = tid, sm.fast.below = goal - from - off, sm.fast.under = goal - from + off;
+    }
+    __syncthreads();
+    const int piece = sm.fast.piece;
+    if (piece >= 0) {
+      // its tokens one after the other, 2,048 at a time
+      const int s = warp_begin(piece / kPieces), e = warp_begin(piece / kPieces + 1);
+      const int piece_units = ((e - s + 31) / 32 + 2 * kPieces - 1) / (2 * kPieces) * 64;
+      const int s0 = s + piece % kPieces * piece_units, s1 = min(e, s0 + piece_units);
+      // from these sums' units to the weights', 2^-U of 2^(c m): to 2^-20
+      const float up = exp2f(1.f - fmaf(m, c_lo, fmaf(m, c_hi, -(float)ref)));
+      const u64 below = (u64)((float)sm.fast.below * up * (1.f - 0x1p-20f)), under = (u64)((float)sm.fast.under * up * (1.f + 0x1p-20f)) + 1;
+      u64 upto = 0;
+      for (int w = s0; w < s1; w += kThreads) {
+        float x[8];
+        u64 v[8], own = 0, total;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = -INFINITY;
+        if (w + tid < s1) row.load(w + tid, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = weight(x[i]), own += v[i];
+        u64 at = upto + block_scan(own, sm.scratch, &total) - own;
+        if (at <= below && at + own > under)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (at <= below && at + v[i] > under) {
+              answer((w + tid) * 8 - row.shift + i, log_of((float)v[i], (float)all * up), units * 8 - (int)flags);
+              accepted = 1;
+            }
+            at += v[i];
+          }
+        upto += total;
+      }
+    }
+    accepted = __syncthreads_or(accepted);
     const u64(*verdict)[kBlocks] = share(accepted, 0, 0);
     for (int i = 0; i < blocks; ++i) accepted |= (int)verdict[0][i];
-    if (accepted) return;
-    make_table();
-    __syncthreads();
-  } else {
-  // 1. the first token in order
-  {
-    // (doubles are slow: by one warp, while the logits are under way)
-    if (min_p > 0.f && min_p <= 1.f && warp == kWarps - 1) sm.drop = log((double)min_p) * (double)temperature;
-    float top = -INFINITY;
+    return accepted;
+  }
+
+  // 1. of the other rows: the first token in order, and each thread's largest logit.
+  __device__ __forceinline__ u64 first_token() {
+    float m = -INFINITY;
     int at = 0;
     row.each(w0, w1, lane, 32, [&](const float* x, int id) {
-      float m = x[0];
+      float y = x[0];
 #pragma unroll
-      for (int i = 1; i < 8; ++i) m = fmaxf(m, x[i]);
-      if (m > top) {
-        top = m;
+      for (int i = 1; i < 8; ++i) y = fmaxf(y, x[i]);
+      if (y > m) {
+        m = y;
 #pragma unroll
         for (int i = 7; i >= 0; --i)
-          if (x[i] == m) at = id + i;
+          if (x[i] == y) at = id + i;
       }
     });
-    best = warp_max(composite(top, at));
+    u64 best = warp_max(composite(m, at));
     if (lane == 0) sm.scratch[warp] = best;
-    make_table();
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) best = max(best, sm.scratch[w]);
     if (blocks > 1) asm volatile("barrier.cluster.wait;" ::: "memory");
+    cluster.map_shared_rank(sm.maxima, 0)[part * kThreads + tid] = m;
     const u64(*got)[kBlocks] = share(best, 0, 0);
     for (int i = 0; i < blocks; ++i) best = max(best, got[0][i]);
-  }
-  if (best == 0 || !(temperature > 0.f)) {
-    if (part == 0 && tid == 0) best == 0 ? answer(-1, -INFINITY, 0) : answer(id_of(best), 0.f, 1);
-    return;
-  }
-  set_top(value_of((uint32_t)(best >> 32)));
-  }
-  const float m = 2.f * weight.mh;
-  // what min_p keeps
-  u64 least = 1;
-  if (min_p > 1.f) {
-    least = best;
-  } else if (min_p > 0.f) {
-    const float from = m == INFINITY ? m : __double2float_ru((double)m + sm.drop);
-    least = min((u64)key_of(from) << 32, best);
-    if (least == 0) least = 1;
+    return best;
   }
 
-  // Bins of equal width from m down; the last one goes on to the end.
-  const float per_bin = kBins / (32.f * fmaxf(1.f, fminf(temperature, 1e30f)));
-  auto bin_of = [&](float z) { return (int)fminf((m - z) * per_bin, (float)(kBins - 1)); };
-  auto push = [&](u64 comp) {
-    uint32_t* listed = cluster.map_shared_rank(&sm.listed, 0);
-    const uint32_t at = atomicAdd(listed, 1u);
-    if (at < kList) cluster.map_shared_rank(sm.list, 0)[at] = comp;
-  };
-
-  // By the first block: the draw among the list's first n, in falling order, whose weights are in sm.weights.
-  auto draw_from_list = [&](int n, u64 sum) {
-    const u64 goal = goal_of(u, sum);
-    u64* by_id = sm.list;
-    u64 comps[kList / kThreads];
+  // Rows with limits by a list of the largest logits; false: it does not hold what it must.
+  __device__ __forceinline__ bool by_list(u64 best) {
+    const float each = per_bin();
+    const bool ranked = top_k || top_p < 1.f;
+    int bin = kBins;
+    if (ranked) {
+      const int n = top_k ? top_k : kGuess;
+      int way = 0;
+      if (part == 0) {
+        for (int i = tid; i < kBins; i += kThreads) sm.bins.count[i] = 0;
+        if (tid == 0) sm.chosen = kBins;
+        __syncthreads();
+        for (int i = tid; i < blocks * kThreads; i += kThreads)
+          if (sm.maxima[i] > -INFINITY) atomicAdd(&sm.bins.count[bin_of(sm.maxima[i], each)], 1u);
+        __syncthreads();
+        constexpr int kPer = kBins / kThreads;
+        u64 count = 0, total;
 #pragma unroll
-    for (int i = 0; i < kList / kThreads; ++i) comps[i] = tid + i * kThreads < n ? sm.list[tid + i * kThreads] : 0;
-    __syncthreads();
+        for (int i = 0; i < kPer; ++i) count += sm.bins.count[tid * kPer + i];
+        u64 to = block_scan(count, sm.scratch, &total) - count;
 #pragma unroll
-    for (int i = 0; i < kList / kThreads; ++i)  // rising ids: falling ~id
-      if (tid + i * kThreads < n) by_id[tid + i * kThreads] = (u64)(uint32_t)comps[i] << 32 | (uint32_t)(tid + i * kThreads);
-    __syncthreads();
-    sort_falling(by_id, n);
-    const int each = (n + kThreads - 1) / kThreads;
-    u64 mine = 0, total;
-    for (int i = tid * each; i < min(n, (tid + 1) * each); ++i) mine += sm.weights[(uint32_t)by_id[i]];
-    u64 upto = block_scan(mine, sm.scratch, &total) - mine;
-    for (int i = tid * each; i < min(n, (tid + 1) * each); ++i) {
-      const u64 w = sm.weights[(uint32_t)by_id[i]];
-      if (upto < goal && upto + w >= goal) answer((int)~(uint32_t)(by_id[i] >> 32), log_of((float)w, (float)sum), n);
-      upto += w;
+        for (int i = 0; i < kPer; ++i) {
+          if (to < n && to + sm.bins.count[tid * kPer + i] >= n) sm.chosen = tid * kPer + i;
+          to += sm.bins.count[tid * kPer + i];
+        }
+        __syncthreads();
+        way = sm.chosen;
+      }
+      bin = (int)share(way, 0, 0)[0][0];
+      if (bin >= kBins - 1 && blocks * kThreads < a.vocab) return false;  // (fewer threads than vocab: the last bin holds any number)
     }
-  };
-  // By the first block: the list sorted, weights of its first n, and their sum.
-  auto weigh_list = [&](int n) {
-    u64 sum = 0;
-    for (int i = tid; i < n; i += kThreads) {
-      const u64 w = weight(value_of((uint32_t)(sm.list[i] >> 32)));
-      sm.weights[i] = w, sum += w;
-    }
-    return block_sum(sum);
-  };
-  // How many of the list's first n, whose weights are in sm.weights, it takes for a sum of at least `goal`.
-  auto fewest = [&](int n, u64 goal) {
-    const int each = (n + kThreads - 1) / kThreads;
-    u64 mine = 0, total;
-    for (int i = tid * each; i < min(n, (tid + 1) * each); ++i) mine += sm.weights[i];
-    u64 upto = block_scan(mine, sm.scratch, &total) - mine;
-    for (int i = tid * each; i < min(n, (tid + 1) * each); ++i) {
-      if (upto < goal && upto + sm.weights[i] >= goal) sm.chosen = i + 1;
-      upto += sm.weights[i];
-    }
-    __syncthreads();
-    return sm.chosen;
-  };
+    const Kept limit(ranked ? 1 : least(best));
+    const bool sums = top_k == 0 && top_p < 1.f;
+    u64 whole = 0;
+    gather([&](const float* x, int id, auto name) {
+      if (sums) {
+        u64 w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = weight(x[i]);
+        whole += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+      }
+      if (limit.none(x)) return;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (limit.has(x[i], id + i) && (!ranked || bin_of(x[i], each) <= bin)) name(x[i], id + i);
+    });
+    if (sums) whole = block_sum(whole);
+    const u64(*got)[kBlocks] = share(whole, 0, 0);
+    whole = 0;
+    for (int i = 0; i < blocks; ++i) whole += got[0][i];
+    bool done = true;
+    if (part == 0) done = sm.gathered <= kList && finish((int)sm.gathered, best, whole);
+    return share(done, 0, 0)[0][0];
+  }
+};
 
-  // The last token of the prefix of `target` tokens, or of the fewest whose weights sum to at
-  // least that, among those at or above `floor`.  0: the row is done (all that counts was in
-  // the list).  kMass: target is top_p of all weights; kCount: `floor` where there are not as many.
+// Any row whose first token is known (without limits: whose largest logit is): rounds of bins for
+// each limit, then the sums of the kept tokens.
+template <typename T>
+__device__ __noinline__ void slow_row(const SampleParams& p, Shared& sm, int turn, u64 best, float m) {
+  Sampler<T> s(p, sm);
+  s.turn = turn;
+  s.set_top(m);
+  const Weigher weight = s.weight;
+  const auto& row = s.row;
+  const int tid = s.tid, lane = s.lane, warp = s.warp, blocks = s.blocks, part = s.part, w0 = s.w0, w1 = s.w1;
+  const float each = s.per_bin();
+
+  // The last token of the prefix of `target` tokens, or (kMass) of the fewest whose weights sum
+  // to top_p of the sum of all, among those at or above `floor`; `floor` where there are not as many.
+  // 0: the row is done (all that counts was in the list).
   enum { kCount, kMass };
   enum { kBin, kWhole, kNoLimit };
   auto select = [&](int by, u64 target, u64 floor) -> u64 {
@@ -581,32 +724,42 @@ __global__ void __launch_bounds__(kThreads, 3) sample_token_kernel(const __grid_
     int shift = -1, bin = 0;
     u64 before = 0;
     for (int round = 0;; ++round) {
-      for (int i = tid; i < kBins; i += kThreads) sm.bins.mass[i] = 0, sm.bins.count[i] = 0;
-      if (tid == 0) sm.listed = 0;
       __syncthreads();
-      auto place = [&](float z, u64 comp) {  // the bin, -1: none
-        if (comp < floor) return -1;
-        if (shift < 0) return bin_of(z);
+      for (int i = tid; i < kBins; i += kThreads) sm.bins.mass[i] = 0, sm.bins.count[i] = 0;
+      if (tid == 0) sm.gathered = 0;
+      __syncthreads();
+      const Kept from(floor);
+      auto place = [&](float z, int id) {  // the bin, -1: none
+        if (!from.has(z, id)) return -1;
+        if (shift < 0) return s.bin_of(z, each);
+        const u64 comp = composite(z, id);
         return comp >= lo && comp <= hi ? (int)((hi - comp) >> shift) : -1;
       };
       row.each(w0, w1, lane, 32, [&](const float* x, int id) {
+        if (from.none(x)) return;
+        int at[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int at = place(x[i], composite(x[i], id + i));
-          if (at < 0) continue;
-          atomicAdd(&sm.bins.count[at], 1u);
-          if (by == kMass) atomicAdd(&sm.bins.mass[at], weight(x[i]));
+        for (int i = 0; i < 8; ++i) at[i] = place(x[i], id + i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (at[i] >= 0) atomicAdd(&sm.bins.count[at[i]], 1u);
+        if (by == kMass) {
+          u64 w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = weight(x[i]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (at[i] >= 0 && w[i]) atomicAdd(&sm.bins.mass[at[i]], w[i]);
         }
       });
-      __syncthreads();
+      s.sync_all();  // (the first block's bins have been cleared and filled)
       if (blocks > 1) {
-        cluster.sync();  // the first block's bins have been cleared and filled
         if (part > 0)
           for (int i = tid; i < kBins; i += kThreads) {
-            if (sm.bins.count[i]) atomicAdd(cluster.map_shared_rank(sm.bins.count, 0) + i, sm.bins.count[i]);
-            if (sm.bins.mass[i]) atomicAdd(cluster.map_shared_rank(sm.bins.mass, 0) + i, sm.bins.mass[i]);
+            if (sm.bins.count[i]) atomicAdd(s.cluster.map_shared_rank(sm.bins.count, 0) + i, sm.bins.count[i]);
+            if (sm.bins.mass[i]) atomicAdd(s.cluster.map_shared_rank(sm.bins.mass, 0) + i, sm.bins.mass[i]);
           }
-        cluster.sync();
+        s.cluster.sync();
       }
       if (part == 0) {
         constexpr int kPer = kBins / kThreads;
@@ -615,8 +768,8 @@ __global__ void __launch_bounds__(kThreads, 3) sample_token_kernel(const __grid_
         for (int i = 0; i < kPer; ++i) mass += sm.bins.mass[tid * kPer + i], count += sm.bins.count[tid * kPer + i];
         u64 mass_to = block_scan(mass, sm.scratch, &all_mass) - mass;
         u64 count_to = block_scan(count, sm.scratch, &all_count) - count;
-        if (round == 0 && by == kMass) target = max(part_of(top_p, all_mass, true), 1ull);
-        if (tid == 0) sm.found.way = round == 0 && by == kCount && target >= all_count ? kNoLimit : kBin;
+        if (round == 0 && by == kMass) target = max(part_of(s.top_p, all_mass, true), 1ull);
+        if (tid == 0) sm.found.all = all_mass, sm.found.way = round == 0 && by == kCount && target >= all_count ? kNoLimit : kBin;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -631,85 +784,90 @@ __global__ void __launch_bounds__(kThreads, 3) sample_token_kernel(const __grid_
         __syncthreads();
       }
       // the choice, to all blocks: the bin, and whether the list takes all above its end
-      const u64(*got)[kBlocks] = share((u64)sm.found.bin << 32 | sm.found.count, sm.found.way, sm.found.before);
+      const u64(*got)[kBlocks] = s.share((u64)sm.found.bin << 32 | sm.found.count, sm.found.way, sm.found.before);
       if (got[1][0] == kNoLimit) return floor;
       bin = (int)(got[0][0] >> 32), before = got[2][0];
       const bool take_all = got[1][0] == kWhole;
-      const uint32_t count = (uint32_t)got[0][0];
-      u64 low = ~0ull, high = 0;
-      row.each(w0, w1, lane, 32, [&](const float* x, int id) {
+      if (!take_all && (uint32_t)got[0][0] > kList) {  // once more, in this bin
+        u64 low = ~0ull, high = 0;
+        row.each(w0, w1, lane, 32, [&](const float* x, int id) {
+          if (from.none(x)) return;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const u64 comp = composite(x[i], id + i);
-          const int at = place(x[i], comp);
-          if (at < 0 || (take_all ? at > bin : at != bin)) continue;
-          if (take_all || count <= kList) push(comp);
-          else low = min(low, comp), high = max(high, comp);
-        }
-      });
-      if (!take_all && count > kList) {  // once more, in this bin
+          for (int i = 0; i < 8; ++i)
+            if (place(x[i], id + i) == bin) low = min(low, composite(x[i], id + i)), high = max(high, composite(x[i], id + i));
+        });
         low = ~warp_max(~low), high = warp_max(high);
         __syncthreads();
         if (lane == 0) sm.parts[warp] = low, sm.scratch[warp] = high;
         __syncthreads();
         for (int w = 0; w < kWarps; ++w) low = min(low, sm.parts[w]), high = max(high, sm.scratch[w]);
-        const u64(*ends)[kBlocks] = share(low, high, 0);
+        const u64(*ends)[kBlocks] = s.share(low, high, 0);
         for (int i = 0; i < blocks; ++i) low = min(low, ends[0][i]), high = max(high, ends[1][i]);
         lo = low, hi = high, shift = 0;
         while ((hi - lo) >> shift >= kBins) ++shift;
         continue;
       }
-      if (blocks > 1) cluster.sync();
-      else __syncthreads();
+      s.gather([&](const float* x, int id, auto name) {
+        if (from.none(x)) return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int at = place(x[i], id + i);
+          if (at >= 0 && (take_all ? at <= bin : at == bin)) name(x[i], id + i);
+        }
+      });
+      s.sync_all();
       u64 last = 0;
       if (part == 0) {
-        const int n = (int)sm.listed;
-        sort_falling(sm.list, n);
-        if (!take_all) {
-          if (by == kCount) {
-            last = sm.list[target - before - 1];
-          } else {
-            weigh_list(n);
-            last = sm.list[fewest(n, target - before) - 1];
-          }
+        const int n = (int)sm.gathered;
+        if (take_all) {
+          // (top_p of the tokens at or above `floor`, which top_k has cut: the list is of these alone)
+          s.top_k = by == kCount ? s.top_k : 0;
+          s.finish(n, best, sm.found.all);
         } else {
-          int keep = n;
-          if (by == kCount) keep = (int)target;
-          u64 sum = weigh_list(keep);
-          if (by == kMass) keep = fewest(keep, target);
-          else if (top_p < 1.f) keep = fewest(keep, max(top_p > 0.f ? part_of(top_p, sum, true) : 0, 1ull));
-          int above = 0;  // min_p
-          for (int i = tid; i < keep; i += kThreads) above += sm.list[i] >= least;
-          keep = (int)block_sum(above);
-          sum = 0;
-          for (int i = tid; i < keep; i += kThreads) sum += sm.weights[i];
-          draw_from_list(keep, block_sum(sum));
+          sort_falling(sm.all, n);
+          if (by == kCount) {
+            last = sm.all[target - before - 1];
+          } else {
+            s.weigh_list(n);
+            last = sm.all[s.fewest(n, target - before) - 1];
+          }
         }
       }
       if (take_all) return 0;
-      return share(last, 0, 0)[0][0];
+      return s.share(last, 0, 0)[0][0];
     }
   };
 
   u64 last = 1;  // the kept tokens are those at or above it
-  if (top_k >= 1 && top_k < a.vocab) {
-    last = top_k == 1 ? best : select(kCount, top_k, 1);
+  if (s.top_k) {
+    last = s.top_k == 1 ? best : select(kCount, s.top_k, 1);
     if (last == 0) return;
   }
-  if (top_p <= 0.f) {
+  if (s.top_p <= 0.f) {
     last = best;
-  } else if (top_p < 1.f && last != best) {
+  } else if (s.top_p < 1.f && last != best) {
     last = select(kMass, 0, last);
     if (last == 0) return;
   }
-  last = max(last, least);
+  last = max(last, s.least(best));
 
-  // 4. the kept tokens' weights
+  // the kept tokens' weights
+  const Kept limit(last);
+  auto weigh = [&](const float* x, int id, u64* w) {  // eight, 0 for those that are not kept; how many are
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool in = limit.has(x[i], id + i);
+      w[i] = in ? weight(x[i]) : 0ull, n += in;
+    }
+    return n;
+  };
   u64 sum = 0, kept = 0;
   row.each(w0, w1, lane, 32, [&](const float* x, int id) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (composite(x[i], id + i) >= last) sum += weight(x[i]), ++kept;
+    if (limit.none(x)) return;
+    u64 w[8];
+    kept += weigh(x, id, w);
+    sum += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
   });
   sum = warp_sum(sum), kept = warp_sum(kept);
   __syncthreads();
@@ -718,36 +876,67 @@ __global__ void __launch_bounds__(kThreads, 3) sample_token_kernel(const __grid_
   sum = kept = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) sum += sm.parts[w], kept += sm.scratch[w];
-  const u64(*got)[kBlocks] = share(sum, kept, 0);
+  const u64(*got)[kBlocks] = s.share(sum, kept, 0);
   u64 before = 0;
   sum = kept = 0;
   for (int i = 0; i < blocks; ++i) {
     if (i == part) before = sum;
     sum += got[0][i], kept += got[1][i];
   }
-  const u64 goal = goal_of(u, sum);
+  const u64 goal = goal_of(s.u, sum);
   if (before >= goal || before + got[0][part] < goal) return;  // another block's
   int w = 0;
   while (before + sm.parts[w] < goal) before += sm.parts[w++];
-  const int s0 = b0 + (int)((int64_t)w * (b1 - b0) / kWarps), s1 = b0 + (int)((int64_t)(w + 1) * (b1 - b0) / kWarps);
-  const int each = (s1 - s0 + kThreads - 1) / kThreads;  // units of a thread, side by side
-  auto weigh = [&](const float* x, int id, int i) { return composite(x[i], id + i) >= last ? weight(x[i]) : 0ull; };
-  u64 mine = 0, total;
-  const int t0 = min(s1, s0 + tid * each), t1 = min(s1, t0 + each);
-  row.each(t0, t1, 0, 1, [&](const float* x, int id) {
+  // the warp's tokens one after the other, 2,048 at a time
+  const int s0 = s.warp_begin(w), s1 = s.warp_begin(w + 1);
+  for (int v = s0; v < s1; v += kThreads) {
+    float x[8];
+    u64 y[8], own = 0, total;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) mine += weigh(x, id, i);
-  });
-  u64 upto = before + block_scan(mine, sm.scratch, &total) - mine;
-  if (upto >= goal || upto + mine < goal) return;
-  row.each(t0, t1, 0, 1, [&](const float* x, int id) {
+    for (int i = 0; i < 8; ++i) x[i] = -INFINITY;
+    if (v + tid < s1) row.load(v + tid, x);
+    const int id = (v + tid) * 8 - row.shift;
+    weigh(x, id, y);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const u64 w = weigh(x, id, i);
-      if (upto < goal && upto + w >= goal) answer(id + i, log_of((float)w, (float)sum), (int)kept);
-      upto += w;
+    for (int i = 0; i < 8; ++i) own += y[i];
+    u64 upto = before + block_scan(own, sm.scratch, &total) - own;
+    if (upto < goal && upto + own >= goal)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (upto < goal && upto + y[i] >= goal) s.answer(id + i, s.log_of((float)y[i], (float)sum), (int)kept);
+        upto += y[i];
+      }
+    before += total;
+    if (before >= goal) return;
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 3) sample_token_kernel(const __grid_constant__ SampleParams p) {
+  __shared__ Shared sm;
+  // what needs nothing of the stream before
+  const u64 fine = p.fine[threadIdx.x & 31];
+  for (int i = threadIdx.x; i < kTable; i += kThreads) sm.table[i] = __umul64hi(p.coarse[i >> 5], fine) << 1;
+  if (threadIdx.x == 0) sm.gathered = 0;
+  __syncthreads();
+  after_stream();
+  Sampler<T> s(p, sm);
+  if (s.blocks > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");  // waited for before another block's memory is touched
+  u64 best = 0;
+  if (s.temperature > 0.f && s.top_k == 0 && !(s.top_p < 1.f) && !(s.min_p > 0.f) && s.c_hi > 1e-30f) {
+    if (s.without_limits()) return;
+  } else {
+    // (doubles are slow: by one warp, while the logits are under way)
+    if (s.min_p > 0.f && s.min_p <= 1.f && s.warp == kWarps - 1) sm.drop = log((double)s.min_p) * (double)s.temperature;
+    best = s.first_token();
+    if (best == 0 || !(s.temperature > 0.f) || s.top_k == 1 || s.top_p <= 0.f || s.min_p > 1.f) {
+      if (s.part == 0 && s.tid == 0) best == 0 ? s.answer(-1, -INFINITY, 0) : s.answer(id_of(best), 0.f, 1);
+      return;
     }
-  });
+    s.set_top(value_of((uint32_t)(best >> 32)));
+    if ((s.top_k || s.top_p < 1.f || s.min_p > 0.f) && s.by_list(best)) return;
+  }
+  slow_row<T>(p, sm, s.turn, best, s.top());
 }
 
 }  // namespace
