@@ -13,11 +13,12 @@
 // more than one pass:
 //  - without limits: one pass of sums in fp32, good to 2^-21, names the token unless the number
 //    falls that near a border between two; only then the weights are summed as integers;
-//  - with a limit: a first pass takes the largest logit of each thread.  The n-th largest of these
-//    has at least n tokens at or above it, so that the tokens at or above its bin (1,024 of equal
-//    width below the row's largest) hold the first top_k, or, of 160, mostly what top_p keeps.  A
-//    second pass lists them (and sums all weights for top_p alone); the first block takes the
-//    limits and draws from the list, by counting for each entry what lies before it;
+//  - with top_k, or min_p alone: a first pass takes the largest logit of each thread.  The n-th
+//    largest of these has at least n tokens at or above it, so that the tokens at or above its bin
+//    (1,024 of equal width below the row's largest) hold the first top_k.  A second pass lists
+//    them; the first block takes the limits and draws from the list, by counting for each entry
+//    what lies before it;
+//  - with top_p alone: by_sums;
 //  - where a list does not hold what it must: slow_row, bins of counts and sums of all tokens, as
 //    many rounds as it takes, then the sums of the kept ones by warp.
 #include <cooperative_groups.h>
@@ -37,7 +38,6 @@ constexpr int kBlocks = 8;        // of a cluster at most
 constexpr int kBins = 1024;
 constexpr int kList = 1024;
 constexpr int kShort = 256;       // entries of a list that need no sorting
-constexpr int kGuess = 160;       // of the largest logits, for top_p alone
 constexpr int kTable = 1024;
 constexpr int kPieces = 8;        // of a warp's range, where sums are in fp32
 using u64 = unsigned long long;
@@ -47,9 +47,6 @@ struct SampleParams {
   int32_t unit;               // U
   u64 coarse[32], fine[32];   // 2^62 2^(i/32), 2^63 2^(i/1024)
 };
-
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 // Ascends with z; 0: no token.  Both zeros are one value.
 __device__ __forceinline__ uint32_t key_of(float z) {
@@ -108,17 +105,33 @@ __device__ __forceinline__ u64 part_of(float f, u64 x, bool up) {
 // The first of the running sums that the number u falls under, as the least such sum.
 __device__ __forceinline__ u64 goal_of(float u, u64 sum) { return u >= 1.f ? sum : (u > 0.f ? part_of(u, sum, false) : 0) + 1; }
 
-// Eight logits of a row from a boundary of their size on.
-__device__ __forceinline__ void load8(const float* z, float* x) {
-  asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
-               : "l"(z) : "memory");
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* z, float* x) {
+// Eight logits as loaded from a boundary of their size on, unpacked where they are used.
+template <typename T> struct Unit;
+template <> struct Unit<float> {
+  float x[8];
+  __device__ __forceinline__ void load(const float* z) {
+    asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                 : "l"(z));
+  }
+  __device__ __forceinline__ void set(int i, const float* z, bool there) { x[i] = there ? *z : -INFINITY; }
+  __device__ __forceinline__ const float* values(float*) const { return x; }
+};
+template <> struct Unit<__nv_bfloat16> {
   uint4 u;
-  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(z) : "memory");
-  Piece<__nv_bfloat16>::unpack(u, x);
-}
+  __device__ __forceinline__ void load(const __nv_bfloat16* z) {
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(z));
+  }
+  __device__ __forceinline__ void set(int i, const __nv_bfloat16* z, bool there) {
+    const uint32_t bits = there ? *reinterpret_cast<const uint16_t*>(z) : 0xff80u;
+    uint32_t& w = (&u.x)[i / 2];
+    w = i & 1 ? w | bits << 16 : bits;
+  }
+  __device__ __forceinline__ const float* values(float* to) const {
+    Piece<__nv_bfloat16>::unpack(u, to);
+    return to;
+  }
+};
 
 // 2^n, 0 and the largest power where that is too small or large.
 __device__ __forceinline__ float power(int n) { return __uint_as_float((uint32_t)min(max(n + 127, 0), 254) << 23); }
@@ -197,28 +210,42 @@ template <typename T>
 struct RowView {
   const T* z;
   int vocab, shift;  // unit w: ids 8 w - shift ..
-  __device__ __forceinline__ void load(int w, float* x) const {
+  __device__ __forceinline__ void load(int w, Unit<T>& x) const {
     const int64_t id = (int64_t)w * 8 - shift;
     if (id >= 0 && id + 8 <= vocab) {
-      load8(z + id, x);
+      x.load(z + id);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = id + i >= 0 && id + i < vocab ? to_float(z[id + i]) : -INFINITY;
+      for (int i = 0; i < 8; ++i) x.set(i, z + id + i, id + i >= 0 && id + i < vocab);
     }
   }
-  // f(8 logits, the first's id) for units w0 + first, w0 + first + step, ... below w1, two of them under way.
+  // f(8 logits, the first's id) for units w0 + lane, w0 + lane + 32, ... below w1, four under way.
   template <typename F>
-  __device__ __forceinline__ void each(int w0, int w1, int first, int step, F f) const {
-    float x[2][8];
-    int w = w0 + first;
-    if (w < w1) load(w, x[0]);
-    for (; w < w1; w += 2 * step) {
-      if (w + step < w1) load(w + step, x[1]);
-      f(x[0], w * 8 - shift);
-      if (w + step >= w1) break;
-      if (w + 2 * step < w1) load(w + 2 * step, x[0]);
-      f(x[1], (w + step) * 8 - shift);
-    }
+  __device__ __forceinline__ void each(int w0, int w1, F f) const {
+    constexpr int kAhead = 4;
+    Unit<T> x[kAhead];
+    int w = w0 + (threadIdx.x & 31);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (w + 32 * i < w1) load(w + 32 * i, x[i]);
+    for (; w < w1; w += 32 * kAhead)
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (w + 32 * i < w1) {
+          float y[8];
+          f(x[i].values(y), (w + 32 * i) * 8 - shift);
+        }
+        if (w + 32 * (kAhead + i) < w1) load(w + 32 * (kAhead + i), x[i]);
+      }
+  }
+  // Unit w, nothing from w1 on.
+  __device__ __forceinline__ void one(int w, int w1, float* to) const {
+    Unit<T> x;
+    float y[8];
+    if (w < w1) load(w, x);
+    const float* v = x.values(y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) to[i] = w < w1 ? v[i] : -INFINITY;
   }
 };
 
@@ -241,6 +268,8 @@ struct Shared {
   union {
     struct { u64 mass[kBins]; uint32_t count[kBins]; } bins;
     u64 weights[kList];  // of the entries of `all`
+    ulonglong2 entries[kShort];
+    uint32_t share[kBins];  // of a bin's weights, in units of its first
   };
   union {
     float maxima[kBlocks * kThreads];  // of the cluster's threads (in the first block)
@@ -253,6 +282,7 @@ struct Shared {
   union {
     struct { u64 before, below, under; int piece; } fast;       // where the number falls
     struct { u64 before, all; uint32_t bin, count; int way; } found;  // (the first block's)
+    struct { int low, high; uint32_t upto; } ends;                     // (the first block's)
   };
   double drop;
   uint32_t listed, gathered, base;
@@ -398,7 +428,7 @@ struct Sampler {
   __device__ __forceinline__ void gather(F f) {
     if (tid == 0) sm.listed = 0;
     __syncthreads();
-    row.each(w0, w1, lane, 32, [&](const float* x, int id) {
+    row.each(w0, w1, [&](const float* x, int id) {
       f(x, id, [&](float z, int i) {
         const uint32_t at = atomicAdd(&sm.listed, 1u);
         if (at < kList) sm.list[at] = composite(z, i);
@@ -418,13 +448,18 @@ struct Sampler {
   __device__ __forceinline__ bool finish_short(int n, u64 best, u64 whole) {
     const u64 mine = tid < n ? sm.all[tid] : 0, from = least(best);
     u64 w = tid < n ? weight(value_of((uint32_t)(mine >> 32))) : 0;
-    if (tid < n) sm.weights[tid] = w;
+    ulonglong2* entries = sm.entries;
+    if (tid < n) entries[tid] = make_ulonglong2(mine, w);
     __syncthreads();
     u64 above = 0;
     int rank = 0;
-    if (tid < n)
-      for (int i = 0; i < n; ++i)
-        if (sm.all[i] > mine) ++rank, above += sm.weights[i];
+    if (tid < n) {
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) {
+        const ulonglong2 x = entries[i];
+        if (x.x > mine) ++rank, above += x.y;
+      }
+    }
     bool keep = tid < n && mine >= from && (top_k == 0 || rank < top_k);
     if (top_p < 1.f) {
       const u64 sum = block_sum(tid < n && (top_k == 0 || rank < top_k) ? w : 0);
@@ -433,15 +468,21 @@ struct Sampler {
       keep = keep && above < goal;
     }
     if (!keep) w = 0;
-    const u64 sum = block_sum(w), kept = block_sum(keep);
-    if (tid < n) sm.weights[tid] = w;
+    const u64 sum = block_sum(w);
+    const int kept = __syncthreads_count(keep);
+    // the kept ones alone, side by side: the first of them in order
+    if (keep) entries[rank] = make_ulonglong2(mine, w);
     __syncthreads();
     const u64 goal = goal_of(u, sum);
     u64 upto = 0;
-    if (w)
-      for (int i = 0; i < n; ++i)
-        if ((uint32_t)sm.all[i] > (uint32_t)mine) upto += sm.weights[i];  // a smaller id
-    if (w && upto < goal && upto + w >= goal) answer(id_of(mine), log_of((float)w, (float)sum), (int)kept);
+    if (w) {
+#pragma unroll 8
+      for (int i = 0; i < kept; ++i) {
+        const ulonglong2 x = entries[i];
+        if ((uint32_t)x.x > (uint32_t)mine) upto += x.y;  // a smaller id
+      }
+    }
+    if (w && upto < goal && upto + w >= goal) answer(id_of(mine), log_of((float)w, (float)sum), kept);
     return true;
   }
 
@@ -502,26 +543,36 @@ struct Sampler {
   }
   __device__ __forceinline__ bool finish(int n, u64 best, u64 whole) { return n <= kShort ? finish_short(n, best, whole) : finish_long(n, best, whole); }
 
+  // Units of a piece of a warp's range: whole steps.
+  static constexpr int kStep = 128;
+  static __device__ __forceinline__ int piece_units(int range) { return ((range + kStep - 1) / kStep + kPieces - 1) / kPieces * kStep; }
+
   // Rows without limits.  True: done; otherwise set_top is.
   __device__ __forceinline__ bool without_limits() {
     FastSum f;
     f.start(c_hi, c_lo);
-    const int each = ((w1 - w0 + 31) / 32 + 2 * kPieces - 1) / (2 * kPieces) * 64;  // units of a piece
+    const int each = piece_units(w1 - w0);
     {
-      float x[2][8];
-      if (w0 + lane < w1) row.load(w0 + lane, x[0]);
-      for (int i = 0; i < kPieces; ++i) {
-        const int end = min(w1, w0 + (i + 1) * each);
+      constexpr int kAhead = kStep / 32;
+      Unit<T> x[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (w0 + lane + 32 * i < w1) row.load(w0 + lane + 32 * i, x[i]);
+      for (int k = 0; k < kPieces; ++k) {
+        const int end = min(w1, w0 + (k + 1) * each);
         f.clear();
-        for (int w = w0 + i * each + lane; w < end; w += 64) {
-          if (w + 32 < w1) row.load(w + 32, x[1]);
-          f.add(x[0]);
-          if (w + 64 < w1) row.load(w + 64, x[0]);
-          if (w + 32 < end) f.add(x[1]);
-        }
+        for (int w = w0 + k * each + lane; w < end; w += kStep)
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            if (w + 32 * i < end) {
+              float y[8];
+              f.add(x[i].values(y));
+            }
+            if (w + kStep + 32 * i < w1) row.load(w + kStep + 32 * i, x[i]);
+          }
         __syncwarp();
-        if (w0 + i * each < w1) f.join_warp();
-        auto& piece = sm.pieces[warp * kPieces + i];
+        if (w0 + k * each < w1) f.join_warp();
+        auto& piece = sm.pieces[warp * kPieces + k];
         if (lane == 0) piece.sum = f.sum, piece.rest = f.rest, piece.ref = f.ref;
       }
     }
@@ -586,8 +637,7 @@ struct Sampler {
     if (piece >= 0) {
       // its tokens one after the other, 2,048 at a time
       const int s = warp_begin(piece / kPieces), e = warp_begin(piece / kPieces + 1);
-      const int piece_units = ((e - s + 31) / 32 + 2 * kPieces - 1) / (2 * kPieces) * 64;
-      const int s0 = s + piece % kPieces * piece_units, s1 = min(e, s0 + piece_units);
+      const int s0 = s + piece % kPieces * piece_units(e - s), s1 = min(e, s0 + piece_units(e - s));
       // from these sums' units to the weights', 2^-U of 2^(c m): to 2^-20
       const float up = exp2f(1.f - fmaf(m, c_lo, fmaf(m, c_hi, -(float)ref)));
       const u64 below = (u64)((float)sm.fast.below * up * (1.f - 0x1p-20f)), under = (u64)((float)sm.fast.under * up * (1.f + 0x1p-20f)) + 1;
@@ -595,9 +645,7 @@ struct Sampler {
       for (int w = s0; w < s1; w += kThreads) {
         float x[8];
         u64 v[8], own = 0, total;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = -INFINITY;
-        if (w + tid < s1) row.load(w + tid, x);
+        row.one(w + tid, s1, x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = weight(x[i]), own += v[i];
         u64 at = upto + block_scan(own, sm.scratch, &total) - own;
@@ -623,7 +671,7 @@ struct Sampler {
   __device__ __forceinline__ u64 first_token() {
     float m = -INFINITY;
     int at = 0;
-    row.each(w0, w1, lane, 32, [&](const float* x, int id) {
+    row.each(w0, w1, [&](const float* x, int id) {
       float y = x[0];
 #pragma unroll
       for (int i = 1; i < 8; ++i) y = fmaxf(y, x[i]);
@@ -649,10 +697,9 @@ struct Sampler {
   // Rows with limits by a list of the largest logits; false: it does not hold what it must.
   __device__ __forceinline__ bool by_list(u64 best) {
     const float each = per_bin();
-    const bool ranked = top_k || top_p < 1.f;
     int bin = kBins;
-    if (ranked) {
-      const int n = top_k ? top_k : kGuess;
+    if (top_k) {
+      const int n = top_k;
       int way = 0;
       if (part == 0) {
         for (int i = tid; i < kBins; i += kThreads) sm.bins.count[i] = 0;
@@ -677,35 +724,123 @@ struct Sampler {
       bin = (int)share(way, 0, 0)[0][0];
       if (bin >= kBins - 1 && blocks * kThreads < a.vocab) return false;  // (fewer threads than vocab: the last bin holds any number)
     }
-    const Kept limit(ranked ? 1 : least(best));
-    const bool sums = top_k == 0 && top_p < 1.f;
-    u64 whole = 0;
+    const Kept limit(top_k ? 1 : least(best));
     gather([&](const float* x, int id, auto name) {
-      if (sums) {
-        u64 w[8];
+      float m = x[0];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = weight(x[i]);
-        whole += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
-      }
-      if (limit.none(x)) return;
+      for (int i = 1; i < 8; ++i) m = fmaxf(m, x[i]);
+      if (!(m >= limit.z) || bin_of(m, each) > bin) return;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (limit.has(x[i], id + i) && (!ranked || bin_of(x[i], each) <= bin)) name(x[i], id + i);
+        if (limit.has(x[i], id + i) && bin_of(x[i], each) <= bin) name(x[i], id + i);
     });
-    if (sums) whole = block_sum(whole);
-    const u64(*got)[kBlocks] = share(whole, 0, 0);
-    whole = 0;
-    for (int i = 0; i < blocks; ++i) whole += got[0][i];
+    sync_all();
     bool done = true;
-    if (part == 0) done = sm.gathered <= kList && finish((int)sm.gathered, best, whole);
+    if (part == 0) done = sm.gathered <= kList && finish((int)sm.gathered, best, 0);
     return share(done, 0, 0)[0][0];
+  }
+
+  // Rows with top_p alone, or with min_p: bins of 1/22 of a power of two of weight, in each the
+  // sum of the weights in units of the bin's first (one addition a token, in 32 bits), name the
+  // bins in which the limit's last token can lie.  A second pass lists these, or, where they are few,
+  // all above their end, and sums all weights, and those above, as integers.
+  // 0: done; 1: no such luck; otherwise the last token that top_p keeps.
+  __device__ __forceinline__ u64 by_sums(u64 best) {
+    constexpr float kSpan = 46.f;
+    const float each = kBins / kSpan * c_hi;  // bins of a logit
+    const int bits = min(14, 31 - (32 - __clz(a.vocab - 1)));
+    if (!(each > 1e-3f && each < 1e30f) || bits < 8) return 1;
+    for (int i = tid; i < kBins; i += kThreads) sm.share[i] = 0;
+    __syncthreads();
+    const float m = top(), one = (float)(1 << bits);
+    row.each(w0, w1, [&](const float* x, int) {
+      int at[8];
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float y = (m - x[i]) * each, n = floorf(y);  // (NaN where x is)
+        at[i] = n < (float)(kBins - 1) ? (int)n : -1;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[i]) : "f"((n - y) * (kSpan / kBins)));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (at[i] >= 0) atomicAdd(&sm.share[at[i]], (uint32_t)__float2int_rn(v[i] * one));
+    });
+    sync_all();
+    if (blocks > 1) {
+      if (part > 0)
+        for (int i = tid; i < kBins; i += kThreads)
+          if (sm.share[i]) atomicAdd(cluster.map_shared_rank(sm.share, 0) + i, sm.share[i]);
+      cluster.sync();
+    }
+    u64 ends = 0, way = 0;
+    if (part == 0) {
+      constexpr int kPer = kBins / kThreads;
+      if (tid == 0) sm.ends.low = kBins - 1, sm.ends.high = kBins - 1, sm.ends.upto = ~0u;
+      u64 here[kPer], mass = 0, count = 0, all, total;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const uint32_t v = sm.share[tid * kPer + i];
+        here[i] = (u64)((float)v * exp2f(20.f - (tid * kPer + i) * (kSpan / kBins)));
+        mass += here[i], count += v;
+      }
+      u64 mass_to = block_scan(mass, sm.scratch, &all) - mass;
+      u64 count_to = block_scan(count, sm.scratch, &total) - count;
+      // sums are off by 2^-bits of themselves: a rounding of at most half of 2^-bits / 0.97, ex2 and what lies below the bins
+      const float goal = top_p * (float)all, off = goal * 4.f / one;
+      const u64 goal_lo = (u64)fmaxf(goal - off, 0.f), goal_hi = (u64)(goal + off) + 64;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const u64 next = mass_to + here[i], count_next = count_to + sm.share[tid * kPer + i];
+        if (mass_to <= goal_lo && next > goal_lo) sm.ends.low = tid * kPer + i;
+        if (mass_to <= goal_hi && next > goal_hi) sm.ends.high = tid * kPer + i, sm.ends.upto = (uint32_t)(count_next * 17 >> (bits + 4));
+        mass_to = next, count_to = count_next;
+      }
+      __syncthreads();
+      ends = (u64)sm.ends.low << 32 | sm.ends.high;
+      way = sm.ends.upto <= kList;  // (the tokens, from above: each is more than 0.96 of its bin's first)
+    }
+    const u64(*choice)[kBlocks] = share(ends, way, 0);
+    const int low = choice[1][0] ? 0 : (int)(choice[0][0] >> 32), high = (int)(uint32_t)choice[0][0];
+    u64 whole = 0, above = 0;
+    gather([&](const float* x, int id, auto name) {
+      u64 w[8];
+      int at[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        w[i] = weight(x[i]);
+        at[i] = (int)fminf((m - x[i]) * each, (float)(kBins - 1));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) whole += w[i], above += at[i] < low ? w[i] : 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (x[i] > -INFINITY && at[i] >= low && at[i] <= high) name(x[i], id + i);
+    });
+    whole = block_sum(whole), above = block_sum(above);
+    const u64(*got)[kBlocks] = share(whole, above, 0);
+    whole = above = 0;
+    for (int i = 0; i < blocks; ++i) whole += got[0][i], above += got[1][i];
+    u64 last = 1;
+    if (part == 0 && sm.gathered <= kList) {
+      const int n = (int)sm.gathered;
+      if (low == 0) {
+        last = finish(n, best, whole) ? 0 : 1;
+      } else {
+        const u64 goal = max(part_of(top_p, whole, true), 1ull);
+        sort_falling(sm.all, n);
+        if (above < goal && above + weigh_list(n) >= goal) last = sm.all[fewest(n, goal - above) - 1];
+      }
+    }
+    return share(last, 0, 0)[0][0];
   }
 };
 
 // Any row whose first token is known (without limits: whose largest logit is): rounds of bins for
-// each limit, then the sums of the kept tokens.
+// each limit, where `last`, from which on tokens are kept, is not known yet (1), then the sums of the
+// kept tokens.
 template <typename T>
-__device__ __noinline__ void slow_row(const SampleParams& p, Shared& sm, int turn, u64 best, float m) {
+__device__ __noinline__ void slow_row(const SampleParams& p, Shared& sm, int turn, u64 best, float m, u64 last) {
   Sampler<T> s(p, sm);
   s.turn = turn;
   s.set_top(m);
@@ -735,7 +870,7 @@ __device__ __noinline__ void slow_row(const SampleParams& p, Shared& sm, int tur
         const u64 comp = composite(z, id);
         return comp >= lo && comp <= hi ? (int)((hi - comp) >> shift) : -1;
       };
-      row.each(w0, w1, lane, 32, [&](const float* x, int id) {
+      row.each(w0, w1, [&](const float* x, int id) {
         if (from.none(x)) return;
         int at[8];
 #pragma unroll
@@ -790,7 +925,7 @@ __device__ __noinline__ void slow_row(const SampleParams& p, Shared& sm, int tur
       const bool take_all = got[1][0] == kWhole;
       if (!take_all && (uint32_t)got[0][0] > kList) {  // once more, in this bin
         u64 low = ~0ull, high = 0;
-        row.each(w0, w1, lane, 32, [&](const float* x, int id) {
+        row.each(w0, w1, [&](const float* x, int id) {
           if (from.none(x)) return;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -838,14 +973,11 @@ __device__ __noinline__ void slow_row(const SampleParams& p, Shared& sm, int tur
     }
   };
 
-  u64 last = 1;  // the kept tokens are those at or above it
-  if (s.top_k) {
-    last = s.top_k == 1 ? best : select(kCount, s.top_k, 1);
+  if (last == 1 && s.top_k) {
+    last = select(kCount, s.top_k, 1);
     if (last == 0) return;
   }
-  if (s.top_p <= 0.f) {
-    last = best;
-  } else if (s.top_p < 1.f && last != best) {
+  if ((last == 1 || s.top_k) && s.top_p < 1.f) {
     last = select(kMass, 0, last);
     if (last == 0) return;
   }
@@ -863,7 +995,7 @@ __device__ __noinline__ void slow_row(const SampleParams& p, Shared& sm, int tur
     return n;
   };
   u64 sum = 0, kept = 0;
-  row.each(w0, w1, lane, 32, [&](const float* x, int id) {
+  row.each(w0, w1, [&](const float* x, int id) {
     if (limit.none(x)) return;
     u64 w[8];
     kept += weigh(x, id, w);
@@ -892,9 +1024,7 @@ __device__ __noinline__ void slow_row(const SampleParams& p, Shared& sm, int tur
   for (int v = s0; v < s1; v += kThreads) {
     float x[8];
     u64 y[8], own = 0, total;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = -INFINITY;
-    if (v + tid < s1) row.load(v + tid, x);
+    row.one(v + tid, s1, x);
     const int id = (v + tid) * 8 - row.shift;
     weigh(x, id, y);
 #pragma unroll
@@ -922,7 +1052,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_token_kernel(const __grid_
   after_stream();
   Sampler<T> s(p, sm);
   if (s.blocks > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");  // waited for before another block's memory is touched
-  u64 best = 0;
+  u64 best = 0, last = 1;
   if (s.temperature > 0.f && s.top_k == 0 && !(s.top_p < 1.f) && !(s.min_p > 0.f) && s.c_hi > 1e-30f) {
     if (s.without_limits()) return;
   } else {
@@ -934,9 +1064,14 @@ __global__ void __launch_bounds__(kThreads, 3) sample_token_kernel(const __grid_
       return;
     }
     s.set_top(value_of((uint32_t)(best >> 32)));
-    if ((s.top_k || s.top_p < 1.f || s.min_p > 0.f) && s.by_list(best)) return;
+    if (s.top_k || !(s.top_p < 1.f)) {
+      if ((s.top_k || s.min_p > 0.f) && s.by_list(best)) return;
+    } else {
+      last = s.by_sums(best);
+      if (last == 0) return;
+    }
   }
-  slow_row<T>(p, sm, s.turn, best, s.top());
+  slow_row<T>(p, sm, s.turn, best, s.top(), last);
 }
 
 }  // namespace
