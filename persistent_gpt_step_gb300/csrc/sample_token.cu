@@ -48,6 +48,9 @@ struct SampleParams {
   u64 coarse[32], fine[32];   // 2^62 2^(i/32), 2^63 2^(i/1024)
 };
 
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
 // Ascends with z; 0: no token.  Both zeros are one value.
 __device__ __forceinline__ uint32_t key_of(float z) {
   const uint32_t b = __float_as_uint(z + 0.f);
@@ -59,6 +62,34 @@ __device__ __forceinline__ u64 composite(float z, int id) {
   return key ? (u64)key << 32 | ~(uint32_t)id : 0ull;
 }
 __device__ __forceinline__ int id_of(u64 comp) { return (int)~(uint32_t)comp; }
+
+// Two floats in one register pair, for operations on both at once.
+struct Pair {
+  u64 bits;
+  __device__ __forceinline__ Pair() {}
+  __device__ __forceinline__ Pair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(bits) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ explicit Pair(float a) : Pair(a, a) {}
+  __device__ __forceinline__ float2 both() const {
+    float2 x;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x.x), "=f"(x.y) : "l"(bits));
+    return x;
+  }
+};
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  Pair d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.bits) : "l"(a.bits), "l"(b.bits));
+  return d;
+}
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.bits) : "l"(a.bits), "l"(b.bits));
+  return d;
+}
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.bits) : "l"(a.bits), "l"(b.bits), "l"(c.bits));
+  return d;
+}
 
 // 2^U exp((z - m) / T) to 2^-42 of itself and half a unit, in fp32 and integer
 // operations: y = (z - m) c, c = log2 e / T, is kept in two floats (z - m and the product with
@@ -72,28 +103,44 @@ struct Weigher {
   int unit;
   bool infinite;  // m is
   __device__ __forceinline__ u64 operator()(float z) const {
+    u64 w[2];
+    two(z, -INFINITY, w);
+    return w[0];
+  }
+  __device__ __forceinline__ void eight(const float* x, u64* w) const {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) two(x[i], x[i + 1], w + i);
+  }
+  __device__ __forceinline__ void two(float z0, float z1, u64* w) const {
     constexpr double kLn2 = 0.69314718055994530942, kUp = 4398046511104.0;  // 2^42
     constexpr float kL = (float)kLn2, kL42 = (float)(kL * kUp), kRest42 = (float)((kLn2 - (double)kL) * kUp);
     constexpr float kC2 = (float)(kLn2 * kLn2 / 2 * kUp), kC3 = (float)(kLn2 * kLn2 * kLn2 / 6 * kUp);
     constexpr float kMagic = 12288.f;  // 1.5 2^13: sums with it are multiples of 2^-10
-    const float zh = __fmul_rn(z, 0.5f), s = __fsub_rn(zh, mh), t = __fsub_rn(s, zh);
-    const float e = __fsub_rn(__fsub_rn(zh, __fsub_rn(s, t)), __fadd_rn(mh, t));
-    const float p = fmaxf(__fmul_rn(s, c_hi), -100.f);  // (NaN too) nothing is left of 2^-100
-    const float up = __fadd_rn(p, kMagic), r = __fsub_rn(p, __fsub_rn(up, kMagic));
-    const float low = __fmaf_rn(s, c_lo, __fmaf_rn(e, c_hi, __fmaf_rn(s, c_hi, -p)));
-    const int J = (int)(__float_as_uint(up) - __float_as_uint(kMagic));
-    const float a = __fmul_rn(r, kL42);
-    const float rest = __fmaf_rn(__fmul_rn(r, r), __fmaf_rn(r, kC3, kC2), __fmaf_rn(r, kRest42, __fmaf_rn(low, kL42, __fmaf_rn(r, kL42, -a))));
-    const int more = __float2int_rn(a) + __float2int_rn(rest);
-    const u64 base = table[J & (kTable - 1)];
-    const u64 w = base + (u64)(((int64_t)more * (int)(base >> 32)) >> 10);
-    const u64 rounded = ((w >> min(61 - unit - (J >> 10), 63)) + 1) >> 1;
-    return infinite ? (z == INFINITY ? 1ull << unit : 0ull) : rounded;
+    const Pair half(0.5f), minus(-1.f), top(mh), hi(c_hi), z(z0, z1);
+    // s + e = (z - m) / 2
+    const Pair s = fma(z, half, Pair(-mh)), t = fma(z, Pair(-0.5f), s);
+    const Pair e = fma(add(top, t), minus, fma(z, half, fma(s, minus, t)));
+    const float2 q = mul(s, hi).both();
+    const Pair p(fmaxf(q.x, -100.f), fmaxf(q.y, -100.f));  // (NaN too) nothing is left of 2^-100
+    const Pair up = add(p, Pair(kMagic)), r = add(p, fma(up, minus, Pair(kMagic)));
+    const Pair low = fma(s, Pair(c_lo), fma(e, hi, fma(s, hi, mul(s, Pair(-c_hi)))));
+    const Pair a = mul(r, Pair(kL42)), a_low = fma(r, Pair(kL42), mul(r, Pair(-kL42)));
+    const Pair rest = fma(mul(r, r), fma(r, Pair(kC3), Pair(kC2)), fma(r, Pair(kRest42), fma(low, Pair(kL42), a_low)));
+    const float2 up2 = up.both(), a2 = a.both(), rest2 = rest.both();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int J = (int)(__float_as_uint(i ? up2.y : up2.x) - __float_as_uint(kMagic));
+      const int more = __float2int_rn(i ? a2.y : a2.x) + __float2int_rn(i ? rest2.y : rest2.x);
+      const u64 base = table[J & (kTable - 1)];
+      const u64 v = base + (u64)(((int64_t)more * (int)(base >> 32)) >> 10);
+      const u64 rounded = ((v >> min(61 - unit - (J >> 10), 63)) + 1) >> 1;
+      w[i] = infinite ? ((i ? z1 : z0) == INFINITY ? 1ull << unit : 0ull) : rounded;
+    }
   }
 };
 
 // The least integer that is at least f x, the largest that is at most f x, for 0 <= f < 1.
-__device__ __forceinline__ u64 part_of(float f, u64 x, bool up) {
+__device__ __noinline__ u64 part_of(float f, u64 x, bool up) {
   const uint32_t b = __float_as_uint(f), e = b >> 23;
   const uint32_t mant = e ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu;
   const int shift = 150 - (int)(e ? e : 1);  // f = mant 2^-shift
@@ -152,10 +199,14 @@ struct FastSum {
   }
   __device__ __forceinline__ void clear() { sum = rest = 0.f, low = high = -INFINITY, ref = -(1 << 24); }
   __device__ __forceinline__ void add(const float* x) {
-    float m = x[0], all = x[0];
+    float m = x[0];
+    Pair all(x[0], x[1]);
 #pragma unroll
-    for (int i = 1; i < 8; ++i) m = fmaxf(m, x[i]), all += x[i];
-    if (!(all > -INFINITY))
+    for (int i = 1; i < 8; ++i) m = fmaxf(m, x[i]);
+#pragma unroll
+    for (int i = 2; i < 8; i += 2) all = pgs::add(all, Pair(x[i], x[i + 1]));
+    const float2 sums = all.both();
+    if (!(sums.x + sums.y > -INFINITY))
 #pragma unroll
       for (int i = 0; i < 8; ++i) missing += !(x[i] > -INFINITY);
     if (!(m > low)) return;
@@ -171,22 +222,21 @@ struct FastSum {
       sum *= keep, rest *= keep, ref = now;
       low = (float)(now - 100) * inv_c, high = (float)(now + 40) * inv_c;
     }
-    constexpr float kMagic = 12582912.f;  // 1.5 2^23
-    const int less = __float_as_int(kMagic) + ref;
-    float w[8];
+    // up = c z to the next integer, over a number whose low bits are -ref: its own low bits are the exponent
+    const float magic = 12582912.f - (float)ref;  // 1.5 2^23
+    Pair w[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float z = fmaxf(x[i], low), up = __fmaf_rn(z, c_hi, kMagic), n = __fsub_rn(up, kMagic);
-      const float r = __fmaf_rn(z, c_lo, __fmaf_rn(z, c_hi, -n));
-      float f;
-      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(r));
-      w[i] = __int_as_float(__float_as_int(f) + ((__float_as_int(up) - less) << 23));
+    for (int i = 0; i < 4; ++i) {
+      const Pair z(fmaxf(x[2 * i], low), fmaxf(x[2 * i + 1], low)), hi(c_hi);
+      const Pair up = fma(z, hi, Pair(magic));
+      const float2 r = fma(z, Pair(c_lo), fma(z, hi, fma(up, Pair(-1.f), Pair(magic)))).both(), n = up.both();
+      float f, g;
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(r.x));
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(g) : "f"(r.y));
+      w[i] = Pair(__int_as_float(__float_as_int(f) + (__float_as_int(n.x) << 23)), __int_as_float(__float_as_int(g) + (__float_as_int(n.y) << 23)));
     }
-#pragma unroll
-    for (int k = 1; k < 8; k *= 2)
-#pragma unroll
-      for (int i = 0; i < 8; i += 2 * k) w[i] += w[i + k];
-    two_sum(w[0], 0.f);
+    const float2 v = pgs::add(pgs::add(w[0], w[1]), pgs::add(w[2], w[3])).both();
+    two_sum(v.x + v.y, 0.f);
   }
   __device__ __forceinline__ void two_sum(float v, float more) {  // sum + rest += v + more, exactly but for the rests' roundings
     const float s = __fadd_rn(sum, v), t = __fsub_rn(s, sum);
@@ -198,7 +248,7 @@ struct FastSum {
     const int all = __reduce_max_sync(0xffffffffu, ref);
     const float keep = power(ref - all);
     sum *= keep, rest *= keep, ref = all;
-#pragma unroll
+#pragma unroll 1
     for (int x = 16; x > 0; x >>= 1) {
       const float v = __shfl_xor_sync(0xffffffffu, sum, x), more = __shfl_xor_sync(0xffffffffu, rest, x);
       two_sum(v, more);
@@ -219,34 +269,37 @@ struct RowView {
       for (int i = 0; i < 8; ++i) x.set(i, z + id + i, id + i >= 0 && id + i < vocab);
     }
   }
-  // f(8 logits, the first's id) for units w0 + lane, w0 + lane + 32, ... below w1, four under way.
-  template <typename F>
+  // f(8 logits, the first's id) for units w0 + lane, w0 + lane + 32, ... below w1, kAhead more under
+  // way.  Code that runs once or twice costs its instructions' way from memory (61 % of the waits,
+  // with four copies of each f): one copy of a long f, the next unit under way; a few of a short one.
+  template <int kAhead = 1, typename F>
   __device__ __forceinline__ void each(int w0, int w1, F f) const {
-    constexpr int kAhead = 4;
     Unit<T> x[kAhead];
     int w = w0 + (threadIdx.x & 31);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
       if (w + 32 * i < w1) load(w + 32 * i, x[i]);
-    for (; w < w1; w += 32 * kAhead)
+#pragma unroll 1
+    for (; w < w1; w += 32 * kAhead) {
+      if constexpr (kAhead == 1) {
+        Unit<T> next;
+        float y[8];
+        if (w + 32 < w1) load(w + 32, next);
+        f(x[0].values(y), w * 8 - shift);
+        x[0] = next;
+      } else {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (w + 32 * i < w1) {
-          float y[8];
-          f(x[i].values(y), (w + 32 * i) * 8 - shift);
+        for (int i = 0; i < kAhead; ++i) {
+          if (w + 32 * i < w1) {
+            float y[8];
+            f(x[i].values(y), (w + 32 * i) * 8 - shift);
+          }
+          if (w + 32 * (kAhead + i) < w1) load(w + 32 * (kAhead + i), x[i]);
         }
-        if (w + 32 * (kAhead + i) < w1) load(w + 32 * (kAhead + i), x[i]);
       }
+    }
   }
-  // Unit w, nothing from w1 on.
-  __device__ __forceinline__ void one(int w, int w1, float* to) const {
-    Unit<T> x;
-    float y[8];
-    if (w < w1) load(w, x);
-    const float* v = x.values(y);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) to[i] = w < w1 ? v[i] : -INFINITY;
-  }
+  __device__ __forceinline__ float at(int id) const { return to_float(z[id]); }
 };
 
 // The tokens at or above a composite key (of 1: all of them).
@@ -300,7 +353,7 @@ __device__ __forceinline__ u64 warp_max(u64 v) {
   return v;
 }
 // The sum of v over the block's threads up to this one.
-__device__ __forceinline__ u64 block_scan(u64 v, u64* scratch, u64* total) {
+__device__ __noinline__ u64 block_scan(u64 v, u64* scratch, u64* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int y = 1; y < 32; y <<= 1) {
@@ -311,7 +364,7 @@ __device__ __forceinline__ u64 block_scan(u64 v, u64* scratch, u64* total) {
   if (lane == 31) scratch[warp] = v;
   __syncthreads();
   u64 sum = 0;
-#pragma unroll
+#pragma unroll 4
   for (int w = 0; w < kWarps; ++w) {
     if (w == warp) v += sum;
     sum += scratch[w];
@@ -320,7 +373,7 @@ __device__ __forceinline__ u64 block_scan(u64 v, u64* scratch, u64* total) {
   return v;
 }
 // Sorts the first n in falling order; what lies behind them up to a power of two is written over.
-__device__ __forceinline__ void sort_falling(u64* x, int n) {
+__device__ __noinline__ void sort_falling(u64* x, int n) {
   int m = 2;
   while (m < n) m *= 2;
   for (int i = n + threadIdx.x; i < m; i += kThreads) x[i] = 0;
@@ -336,9 +389,13 @@ __device__ __forceinline__ void sort_falling(u64* x, int n) {
   __syncthreads();
 }
 
+template <typename T>
+__device__ __noinline__ bool finish_long(const SampleParams& p, Shared& sm, int n, u64 best, u64 whole, float m, int top_k);
+
 // What a thread knows of its row.
 template <typename T>
 struct Sampler {
+  const SampleParams& p;
   const gpt_sample_token_args& a;
   Shared& sm;
   cg::cluster_group cluster;
@@ -351,7 +408,7 @@ struct Sampler {
   int turn;
   Weigher weight;
 
-  __device__ __forceinline__ Sampler(const SampleParams& p, Shared& shared) : a(p.a), sm(shared), cluster(cg::this_cluster()) {
+  __device__ __forceinline__ Sampler(const SampleParams& params, Shared& shared) : p(params), a(params.a), sm(shared), cluster(cg::this_cluster()) {
     tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     blocks = cluster.num_blocks(), part = cluster.block_rank(), turn = 0;
     b = blockIdx.x / blocks;
@@ -454,7 +511,7 @@ struct Sampler {
     u64 above = 0;
     int rank = 0;
     if (tid < n) {
-#pragma unroll 8
+#pragma unroll 4
       for (int i = 0; i < n; ++i) {
         const ulonglong2 x = entries[i];
         if (x.x > mine) ++rank, above += x.y;
@@ -476,7 +533,7 @@ struct Sampler {
     const u64 goal = goal_of(u, sum);
     u64 upto = 0;
     if (w) {
-#pragma unroll 8
+#pragma unroll 4
       for (int i = 0; i < kept; ++i) {
         const ulonglong2 x = entries[i];
         if ((uint32_t)x.x > (uint32_t)mine) upto += x.y;  // a smaller id
@@ -508,43 +565,10 @@ struct Sampler {
     __syncthreads();
     return sm.chosen;
   }
-  // As finish_short, for up to kList entries.
-  __device__ __forceinline__ bool finish_long(int n, u64 best, u64 whole) {
-    sort_falling(sm.all, n);
-    int keep = top_k ? min(top_k, n) : n;
-    u64 sum = weigh_list(keep);
-    if (top_p < 1.f) {
-      const u64 goal = max(top_p > 0.f ? part_of(top_p, top_k ? sum : whole, true) : 0, 1ull);
-      if (sum < goal) return false;
-      keep = fewest(keep, goal);
-    }
-    const u64 from = least(best);
-    int above = 0;
-    for (int i = tid; i < keep; i += kThreads) above += sm.all[i] >= from;
-    keep = (int)block_sum(above);
-    sum = 0;
-    for (int i = tid; i < keep; i += kThreads) sum += sm.weights[i];
-    sum = block_sum(sum);
-    // by rising ids: falling ~id
-    for (int i = tid; i < keep; i += kThreads) sm.all[i] = (u64)(uint32_t)sm.all[i] << 32 | (uint32_t)i;
-    __syncthreads();
-    sort_falling(sm.all, keep);
-    const u64 goal = goal_of(u, sum);
-    const int each = (keep + kThreads - 1) / kThreads;
-    u64 mine = 0, total;
-    for (int i = tid * each; i < min(keep, (tid + 1) * each); ++i) mine += sm.weights[(uint32_t)sm.all[i]];
-    u64 upto = block_scan(mine, sm.scratch, &total) - mine;
-    for (int i = tid * each; i < min(keep, (tid + 1) * each); ++i) {
-      const u64 w = sm.weights[(uint32_t)sm.all[i]];
-      if (upto < goal && upto + w >= goal) answer((int)~(uint32_t)(sm.all[i] >> 32), log_of((float)w, (float)sum), keep);
-      upto += w;
-    }
-    return true;
-  }
-  __device__ __forceinline__ bool finish(int n, u64 best, u64 whole) { return n <= kShort ? finish_short(n, best, whole) : finish_long(n, best, whole); }
+  __device__ __forceinline__ bool finish(int n, u64 best, u64 whole) { return n <= kShort ? finish_short(n, best, whole) : finish_long<T>(p, sm, n, best, whole, top(), top_k); }
 
   // Units of a piece of a warp's range: whole steps.
-  static constexpr int kStep = 128;
+  static constexpr int kStep = 32;
   static __device__ __forceinline__ int piece_units(int range) { return ((range + kStep - 1) / kStep + kPieces - 1) / kPieces * kStep; }
 
   // Rows without limits.  True: done; otherwise set_top is.
@@ -553,23 +577,20 @@ struct Sampler {
     f.start(c_hi, c_lo);
     const int each = piece_units(w1 - w0);
     {
-      constexpr int kAhead = kStep / 32;
-      Unit<T> x[kAhead];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-        if (w0 + lane + 32 * i < w1) row.load(w0 + lane + 32 * i, x[i]);
+      Unit<T> x;
+      if (w0 + lane < w1) row.load(w0 + lane, x);
+#pragma unroll 1
       for (int k = 0; k < kPieces; ++k) {
         const int end = min(w1, w0 + (k + 1) * each);
         f.clear();
-        for (int w = w0 + k * each + lane; w < end; w += kStep)
-#pragma unroll
-          for (int i = 0; i < kAhead; ++i) {
-            if (w + 32 * i < end) {
-              float y[8];
-              f.add(x[i].values(y));
-            }
-            if (w + kStep + 32 * i < w1) row.load(w + kStep + 32 * i, x[i]);
-          }
+#pragma unroll 1
+        for (int w = w0 + k * each + lane; w < end; w += 32) {
+          Unit<T> next;
+          float y[8];
+          if (w + 32 < w1) row.load(w + 32, next);
+          f.add(x.values(y));
+          x = next;
+        }
         __syncwarp();
         if (w0 + k * each < w1) f.join_warp();
         auto& piece = sm.pieces[warp * kPieces + k];
@@ -606,6 +627,7 @@ struct Sampler {
     uint32_t top_key = 0;
     int ref = -(1 << 22);
     flags = 0;
+#pragma unroll 1
     for (int i = 0; i < blocks; ++i) top_key = max(top_key, (uint32_t)got[1][i]), ref = max(ref, (int)(got[1][i] >> 32)), flags += got[2][i];
     if (top_key == 0) {
       if (part == 0 && tid == 0) answer(-1, -INFINITY, 0);
@@ -617,6 +639,7 @@ struct Sampler {
     int accepted = 0;
     auto moved = [&](u64 v, int from) { return ref - from < 64 ? v >> (ref - from) : 0ull; };
     u64 all = 0, before = 0;
+#pragma unroll 1
     for (int i = 0; i < blocks; ++i) {
       if (i == part) before = all;
       all += moved(got[0][i], (int)(got[1][i] >> 32));
@@ -642,27 +665,29 @@ struct Sampler {
       const float up = exp2f(1.f - fmaf(m, c_lo, fmaf(m, c_hi, -(float)ref)));
       const u64 below = (u64)((float)sm.fast.below * up * (1.f - 0x1p-20f)), under = (u64)((float)sm.fast.under * up * (1.f + 0x1p-20f)) + 1;
       u64 upto = 0;
+#pragma unroll 1
       for (int w = s0; w < s1; w += kThreads) {
-        float x[8];
-        u64 v[8], own = 0, total;
-        row.one(w + tid, s1, x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = weight(x[i]), own += v[i];
+        const int id = (w + tid) * 8 - row.shift, first_id = max(id, 0), end_id = w + tid < s1 ? min(id + 8, a.vocab) : 0;
+        u64 own = 0, total;
+#pragma unroll 1
+        for (int i = first_id; i < end_id; ++i) own += weight(row.at(i));
         u64 at = upto + block_scan(own, sm.scratch, &total) - own;
         if (at <= below && at + own > under)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (at <= below && at + v[i] > under) {
-              answer((w + tid) * 8 - row.shift + i, log_of((float)v[i], (float)all * up), units * 8 - (int)flags);
+#pragma unroll 1
+          for (int i = first_id; i < end_id; ++i) {
+            const u64 v = weight(row.at(i));
+            if (at <= below && at + v > under) {
+              answer(i, log_of((float)v, (float)all * up), units * 8 - (int)flags);
               accepted = 1;
             }
-            at += v[i];
+            at += v;
           }
         upto += total;
       }
     }
     accepted = __syncthreads_or(accepted);
     const u64(*verdict)[kBlocks] = share(accepted, 0, 0);
+#pragma unroll 1
     for (int i = 0; i < blocks; ++i) accepted |= (int)verdict[0][i];
     return accepted;
   }
@@ -671,7 +696,7 @@ struct Sampler {
   __device__ __forceinline__ u64 first_token() {
     float m = -INFINITY;
     int at = 0;
-    row.each(w0, w1, [&](const float* x, int id) {
+    row.template each<2>(w0, w1, [&](const float* x, int id) {
       float y = x[0];
 #pragma unroll
       for (int i = 1; i < 8; ++i) y = fmaxf(y, x[i]);
@@ -690,6 +715,7 @@ struct Sampler {
     if (blocks > 1) asm volatile("barrier.cluster.wait;" ::: "memory");
     cluster.map_shared_rank(sm.maxima, 0)[part * kThreads + tid] = m;
     const u64(*got)[kBlocks] = share(best, 0, 0);
+#pragma unroll 1
     for (int i = 0; i < blocks; ++i) best = max(best, got[0][i]);
     return best;
   }
@@ -777,21 +803,18 @@ struct Sampler {
     if (part == 0) {
       constexpr int kPer = kBins / kThreads;
       if (tid == 0) sm.ends.low = kBins - 1, sm.ends.high = kBins - 1, sm.ends.upto = ~0u;
-      u64 here[kPer], mass = 0, count = 0, all, total;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const uint32_t v = sm.share[tid * kPer + i];
-        here[i] = (u64)((float)v * exp2f(20.f - (tid * kPer + i) * (kSpan / kBins)));
-        mass += here[i], count += v;
-      }
+      u64 mass = 0, count = 0, all, total;
+      auto here = [&](int i) { return (u64)((float)sm.share[i] * exp2f(20.f - i * (kSpan / kBins))); };
+#pragma unroll 1
+      for (int i = 0; i < kPer; ++i) mass += here(tid * kPer + i), count += sm.share[tid * kPer + i];
       u64 mass_to = block_scan(mass, sm.scratch, &all) - mass;
       u64 count_to = block_scan(count, sm.scratch, &total) - count;
       // sums are off by 2^-bits of themselves: a rounding of at most half of 2^-bits / 0.97, ex2 and what lies below the bins
       const float goal = top_p * (float)all, off = goal * 4.f / one;
       const u64 goal_lo = (u64)fmaxf(goal - off, 0.f), goal_hi = (u64)(goal + off) + 64;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < kPer; ++i) {
-        const u64 next = mass_to + here[i], count_next = count_to + sm.share[tid * kPer + i];
+        const u64 next = mass_to + here(tid * kPer + i), count_next = count_to + sm.share[tid * kPer + i];
         if (mass_to <= goal_lo && next > goal_lo) sm.ends.low = tid * kPer + i;
         if (mass_to <= goal_hi && next > goal_hi) sm.ends.high = tid * kPer + i, sm.ends.upto = (uint32_t)(count_next * 17 >> (bits + 4));
         mass_to = next, count_to = count_next;
@@ -806,11 +829,9 @@ struct Sampler {
     gather([&](const float* x, int id, auto name) {
       u64 w[8];
       int at[8];
+      weight.eight(x, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        w[i] = weight(x[i]);
-        at[i] = (int)fminf((m - x[i]) * each, (float)(kBins - 1));
-      }
+      for (int i = 0; i < 8; ++i) at[i] = (int)fminf((m - x[i]) * each, (float)(kBins - 1));
 #pragma unroll
       for (int i = 0; i < 8; ++i) whole += w[i], above += at[i] < low ? w[i] : 0;
 #pragma unroll
@@ -820,6 +841,7 @@ struct Sampler {
     whole = block_sum(whole), above = block_sum(above);
     const u64(*got)[kBlocks] = share(whole, above, 0);
     whole = above = 0;
+#pragma unroll 1
     for (int i = 0; i < blocks; ++i) whole += got[0][i], above += got[1][i];
     u64 last = 1;
     if (part == 0 && sm.gathered <= kList) {
@@ -835,6 +857,44 @@ struct Sampler {
     return share(last, 0, 0)[0][0];
   }
 };
+
+// As finish_short, for up to kList entries.
+template <typename T>
+__device__ __noinline__ bool finish_long(const SampleParams& p, Shared& sm, int n, u64 best, u64 whole, float m, int top_k) {
+  Sampler<T> s(p, sm);
+  s.set_top(m);
+  const int tid = s.tid;
+    sort_falling(sm.all, n);
+  int keep = top_k ? min(top_k, n) : n;
+  u64 sum = s.weigh_list(keep);
+  if (s.top_p < 1.f) {
+    const u64 goal = max(s.top_p > 0.f ? part_of(s.top_p, top_k ? sum : whole, true) : 0, 1ull);
+    if (sum < goal) return false;
+    keep = s.fewest(keep, goal);
+  }
+  const u64 from = s.least(best);
+  int above = 0;
+  for (int i = tid; i < keep; i += kThreads) above += sm.all[i] >= from;
+  keep = (int)s.block_sum(above);
+  sum = 0;
+  for (int i = tid; i < keep; i += kThreads) sum += sm.weights[i];
+  sum = s.block_sum(sum);
+  // by rising ids: falling ~id
+  for (int i = tid; i < keep; i += kThreads) sm.all[i] = (u64)(uint32_t)sm.all[i] << 32 | (uint32_t)i;
+  __syncthreads();
+  sort_falling(sm.all, keep);
+  const u64 goal = goal_of(s.u, sum);
+  const int each = (keep + kThreads - 1) / kThreads;
+  u64 mine = 0, total;
+  for (int i = tid * each; i < min(keep, (tid + 1) * each); ++i) mine += sm.weights[(uint32_t)sm.all[i]];
+  u64 upto = block_scan(mine, sm.scratch, &total) - mine;
+  for (int i = tid * each; i < min(keep, (tid + 1) * each); ++i) {
+    const u64 w = sm.weights[(uint32_t)sm.all[i]];
+    if (upto < goal && upto + w >= goal) s.answer((int)~(uint32_t)(sm.all[i] >> 32), s.log_of((float)w, (float)sum), keep);
+    upto += w;
+  }
+  return true;
+}
 
 // Any row whose first token is known (without limits: whose largest logit is): rounds of bins for
 // each limit, where `last`, from which on tokens are kept, is not known yet (1), then the sums of the
@@ -880,8 +940,7 @@ __device__ __noinline__ void slow_row(const SampleParams& p, Shared& sm, int tur
           if (at[i] >= 0) atomicAdd(&sm.bins.count[at[i]], 1u);
         if (by == kMass) {
           u64 w[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = weight(x[i]);
+          weight.eight(x, w);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if (at[i] >= 0 && w[i]) atomicAdd(&sm.bins.mass[at[i]], w[i]);
@@ -937,6 +996,7 @@ __device__ __noinline__ void slow_row(const SampleParams& p, Shared& sm, int tur
         __syncthreads();
         for (int w = 0; w < kWarps; ++w) low = min(low, sm.parts[w]), high = max(high, sm.scratch[w]);
         const u64(*ends)[kBlocks] = s.share(low, high, 0);
+#pragma unroll 1
         for (int i = 0; i < blocks; ++i) low = min(low, ends[0][i]), high = max(high, ends[1][i]);
         lo = low, hi = high, shift = 0;
         while ((hi - lo) >> shift >= kBins) ++shift;
@@ -987,11 +1047,11 @@ __device__ __noinline__ void slow_row(const SampleParams& p, Shared& sm, int tur
   const Kept limit(last);
   auto weigh = [&](const float* x, int id, u64* w) {  // eight, 0 for those that are not kept; how many are
     int n = 0;
+    weight.eight(x, w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const bool in = limit.has(x[i], id + i);
-      w[i] = in ? weight(x[i]) : 0ull, n += in;
-    }
+    for (int i = 0; i < 8; ++i)
+      if (limit.has(x[i], id + i)) ++n;
+      else w[i] = 0;
     return n;
   };
   u64 sum = 0, kept = 0;
@@ -1011,6 +1071,7 @@ __device__ __noinline__ void slow_row(const SampleParams& p, Shared& sm, int tur
   const u64(*got)[kBlocks] = s.share(sum, kept, 0);
   u64 before = 0;
   sum = kept = 0;
+#pragma unroll 1
   for (int i = 0; i < blocks; ++i) {
     if (i == part) before = sum;
     sum += got[0][i], kept += got[1][i];
@@ -1022,19 +1083,21 @@ __device__ __noinline__ void slow_row(const SampleParams& p, Shared& sm, int tur
   // the warp's tokens one after the other, 2,048 at a time
   const int s0 = s.warp_begin(w), s1 = s.warp_begin(w + 1);
   for (int v = s0; v < s1; v += kThreads) {
-    float x[8];
-    u64 y[8], own = 0, total;
-    row.one(v + tid, s1, x);
-    const int id = (v + tid) * 8 - row.shift;
-    weigh(x, id, y);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) own += y[i];
+    const int id = (v + tid) * 8 - row.shift, first_id = max(id, 0), end_id = v + tid < s1 ? min(id + 8, s.a.vocab) : 0;
+    u64 own = 0, total;
+    auto one = [&](int i) {
+      const float x = row.at(i);
+      return limit.has(x, i) ? weight(x) : 0ull;
+    };
+#pragma unroll 1
+    for (int i = first_id; i < end_id; ++i) own += one(i);
     u64 upto = before + block_scan(own, sm.scratch, &total) - own;
     if (upto < goal && upto + own >= goal)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (upto < goal && upto + y[i] >= goal) s.answer(id + i, s.log_of((float)y[i], (float)sum), (int)kept);
-        upto += y[i];
+#pragma unroll 1
+      for (int i = first_id; i < end_id; ++i) {
+        const u64 y = one(i);
+        if (upto < goal && upto + y >= goal) s.answer(i, s.log_of((float)y, (float)sum), (int)kept);
+        upto += y;
       }
     before += total;
     if (before >= goal) return;
@@ -1109,7 +1172,7 @@ extern "C" int gpt_sample_token(const gpt_sample_token_args* a, void* cuda_strea
   std::copy(powers.coarse, powers.coarse + 32, p.coarse);
   std::copy(powers.fine, powers.fine + 32, p.fine);
   int blocks = 1;
-  while (blocks < kBlocks && a->vocab / (2 * blocks) >= 512 && (int64_t)a->rows * 2 * blocks <= 608) blocks *= 2;
+  while (blocks < kBlocks && a->vocab / (2 * blocks) >= 512 && ((int64_t)a->rows * 2 * blocks <= 456 || a->vocab / (2 * blocks) >= 32768)) blocks *= 2;
   if ((int64_t)a->rows * blocks > INT32_MAX) return call_error(GPT_ERR_UNSUPPORTED, "too many rows");
   const cudaStream_t st = (cudaStream_t)cuda_stream;
   return launch_after("gpt_sample_token", a->dtype == GPT_DTYPE_BF16 ? sample_token_kernel<__nv_bfloat16> : sample_token_kernel<float>,
