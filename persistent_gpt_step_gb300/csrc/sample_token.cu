@@ -39,7 +39,7 @@ constexpr int kBins = 1024;
 constexpr int kList = 1024;
 constexpr int kShort = 256;       // entries of a list that need no sorting
 constexpr int kTable = 1024;
-constexpr int kPieces = 8;        // of a warp's range, where sums are in fp32
+constexpr int kPieces = 4;        // of a warp's range, where sums are in fp32
 using u64 = unsigned long long;
 
 struct SampleParams {
@@ -400,7 +400,8 @@ struct Sampler {
   Shared& sm;
   cg::cluster_group cluster;
   RowView<T> row;
-  int tid, lane, warp, blocks, part;
+  int tid, lane, warp;
+  int blocks, part, home;     // of the row; the first block's rank in the cluster
   int units, b0, b1, w0, w1;  // of the row; the block's and the warp's
   int64_t b;
   float u, temperature, top_p, min_p, c_hi, c_lo;
@@ -408,10 +409,12 @@ struct Sampler {
   int turn;
   Weigher weight;
 
-  __device__ __forceinline__ Sampler(const SampleParams& params, Shared& shared) : p(params), a(params.a), sm(shared), cluster(cg::this_cluster()) {
+  // alone: the block does the whole row by itself
+  __device__ __forceinline__ Sampler(const SampleParams& params, Shared& shared, bool alone) : p(params), a(params.a), sm(shared), cluster(cg::this_cluster()) {
     tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    blocks = cluster.num_blocks(), part = cluster.block_rank(), turn = 0;
+    blocks = cluster.num_blocks(), part = cluster.block_rank(), home = 0, turn = 0;
     b = blockIdx.x / blocks;
+    if (alone) home = part, blocks = 1, part = 0;
     row.z = (const T*)a.logits + b * a.logits_stride, row.vocab = a.vocab;
     row.shift = (int)((reinterpret_cast<uintptr_t>(row.z) / sizeof(T)) & 7);
     units = (int)(((int64_t)a.vocab + row.shift + 7) / 8);
@@ -440,7 +443,7 @@ struct Sampler {
   // A value of each block to all of them; what the cluster's blocks wrote before is visible after it.
   __device__ __forceinline__ const u64 (*share(u64 x, u64 y, u64 z))[kBlocks] {  // (the first warp's threads' values)
     if (tid < blocks) {
-      u64(*to)[kBlocks] = cluster.map_shared_rank(sm.slots[turn & 1], tid);
+      u64(*to)[kBlocks] = cluster.map_shared_rank(sm.slots[turn & 1], home + tid);
       to[0][part] = x, to[1][part] = y, to[2][part] = z;
     }
     sync_all();
@@ -493,9 +496,9 @@ struct Sampler {
     });
     __syncthreads();
     const uint32_t n = sm.listed;
-    if (tid == 0 && n) sm.base = atomicAdd(cluster.map_shared_rank(&sm.gathered, 0), n);
+    if (tid == 0 && n) sm.base = atomicAdd(cluster.map_shared_rank(&sm.gathered, home), n);
     __syncthreads();
-    u64* all = cluster.map_shared_rank(sm.all, 0);
+    u64* all = cluster.map_shared_rank(sm.all, home);
     for (uint32_t i = tid; i < min(n, (uint32_t)kList); i += kThreads)
       if (sm.base + i < kList) all[sm.base + i] = sm.list[i];
   }
@@ -571,8 +574,12 @@ struct Sampler {
   static constexpr int kStep = 32;
   static __device__ __forceinline__ int piece_units(int range) { return ((range + kStep - 1) / kStep + kPieces - 1) / kPieces * kStep; }
 
-  // Rows without limits.  True: done; otherwise set_top is.
-  __device__ __forceinline__ bool without_limits() {
+  // What is left to slow_row: nothing, or the row, by all blocks or by this one alone.
+  enum { kDone, kTogether, kAlone };
+
+  // Rows without limits.  (A block alone took 45 us for the 131,072 integers of a row: all of them stay
+  // until the number's token is known.)
+  __device__ __forceinline__ int without_limits() {
     FastSum f;
     f.start(c_hi, c_lo);
     const int each = piece_units(w1 - w0);
@@ -612,14 +619,14 @@ struct Sampler {
         const float x = power(min(up, 0)), y = power(max(up, 0));
         return (u64)(__float2ll_rn(piece.sum * x * y) + __float2ll_rn(piece.rest * x * y));
       };
-      const u64 v0 = whole(sm.pieces[2 * lane]), v1 = whole(sm.pieces[2 * lane + 1]);
-      u64 upto = v0 + v1;
+      static_assert(kWarps * kPieces == 32, "a lane each");
+      u64 upto = whole(sm.pieces[lane]);
 #pragma unroll
       for (int y = 1; y < 32; y <<= 1) {
         const u64 t = __shfl_up_sync(0xffffffffu, upto, y);
         if (lane >= y) upto += t;
       }
-      sm.pieces[2 * lane].upto = upto - v1, sm.pieces[2 * lane + 1].upto = upto;
+      sm.pieces[lane].upto = upto;
       sum = __shfl_sync(0xffffffffu, upto, 31);
     }
     if (blocks > 1) asm volatile("barrier.cluster.wait;" ::: "memory");
@@ -631,11 +638,11 @@ struct Sampler {
     for (int i = 0; i < blocks; ++i) top_key = max(top_key, (uint32_t)got[1][i]), ref = max(ref, (int)(got[1][i] >> 32)), flags += got[2][i];
     if (top_key == 0) {
       if (part == 0 && tid == 0) answer(-1, -INFINITY, 0);
-      return true;
+      return kDone;
     }
     const float m = value_of(top_key);
     set_top(m);
-    if (flags >> 32) return false;
+    if (flags >> 32) return kTogether;
     int accepted = 0;
     auto moved = [&](u64 v, int from) { return ref - from < 64 ? v >> (ref - from) : 0ull; };
     u64 all = 0, before = 0;
@@ -644,16 +651,20 @@ struct Sampler {
       if (i == part) before = all;
       all += moved(got[0][i], (int)(got[1][i] >> 32));
     }
-    // The piece in which the number falls, surely: each sum is off by 2^-21 of itself and
-    // some units.
+    const u64 goal = u >= 1.f ? all : u > 0.f ? part_of(u, all, false) : 0;
+    // The piece in which the number falls, surely.  Sums are off by 2^-21 of themselves and some units: one
+    // from the row's start, S, less the number's share u of the whole one, W, by
+    // |(1 - u) dS - u d(W - S)| <= 2^-21 ((1 - u) S + u (W - S)).
+    auto off_by = [&](u64 from) {
+      return (u64)(((float)from * (1.f - u) + (float)(all - min(from, all)) * u) * (0x1p-21f * (1.f + 0x1p-18f))) + 256;
+    };
     if (tid == 0) sm.fast.piece = -1;
     __syncthreads();
-    const u64 goal = u >= 1.f ? all : u > 0.f ? part_of(u, all, false) : 0;
     if (tid < kWarps * kPieces) {
       const u64 from = before + (tid ? moved(sm.pieces[tid - 1].upto, mine) : 0), to = before + moved(sm.pieces[tid].upto, mine);
-      const u64 off = ((from + goal) >> 21) + 256, off_to = ((to + goal) >> 21) + 256;
-      if (goal >= from + off && to > goal + off_to)
-        sm.fast.piece = tid, sm.fast.below = goal - from - off, sm.fast.under = goal - from + off;
+      const u64 off = off_by(from), off_to = off_by(to);
+      if (u < 1.f && goal >= from + off && to > goal + off_to)
+        sm.fast.piece = tid, sm.fast.below = goal - from - off, sm.fast.under = goal - from + max(off, off_to);
     }
     __syncthreads();
     const int piece = sm.fast.piece;
@@ -689,7 +700,7 @@ struct Sampler {
     const u64(*verdict)[kBlocks] = share(accepted, 0, 0);
 #pragma unroll 1
     for (int i = 0; i < blocks; ++i) accepted |= (int)verdict[0][i];
-    return accepted;
+    return accepted ? kDone : kTogether;
   }
 
   // 1. of the other rows: the first token in order, and each thread's largest logit.
@@ -713,15 +724,15 @@ struct Sampler {
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) best = max(best, sm.scratch[w]);
     if (blocks > 1) asm volatile("barrier.cluster.wait;" ::: "memory");
-    cluster.map_shared_rank(sm.maxima, 0)[part * kThreads + tid] = m;
+    cluster.map_shared_rank(sm.maxima, home)[part * kThreads + tid] = m;
     const u64(*got)[kBlocks] = share(best, 0, 0);
 #pragma unroll 1
     for (int i = 0; i < blocks; ++i) best = max(best, got[0][i]);
     return best;
   }
 
-  // Rows with limits by a list of the largest logits; false: it does not hold what it must.
-  __device__ __forceinline__ bool by_list(u64 best) {
+  // Rows with limits by a list of the largest logits.
+  __device__ __forceinline__ int by_list(u64 best) {
     const float each = per_bin();
     int bin = kBins;
     if (top_k) {
@@ -748,7 +759,7 @@ struct Sampler {
         way = sm.chosen;
       }
       bin = (int)share(way, 0, 0)[0][0];
-      if (bin >= kBins - 1 && blocks * kThreads < a.vocab) return false;  // (fewer threads than vocab: the last bin holds any number)
+      if (bin >= kBins - 1 && blocks * kThreads < a.vocab) return kTogether;  // (fewer threads than vocab: the last bin holds any number)
     }
     const Kept limit(top_k ? 1 : least(best));
     gather([&](const float* x, int id, auto name) {
@@ -761,9 +772,8 @@ struct Sampler {
         if (limit.has(x[i], id + i) && bin_of(x[i], each) <= bin) name(x[i], id + i);
     });
     sync_all();
-    bool done = true;
-    if (part == 0) done = sm.gathered <= kList && finish((int)sm.gathered, best, 0);
-    return share(done, 0, 0)[0][0];
+    if (part > 0) return kDone;
+    return sm.gathered <= kList && finish((int)sm.gathered, best, 0) ? kDone : kAlone;
   }
 
   // Rows with top_p alone, or with min_p: bins of 1/22 of a power of two of weight, in each the
@@ -861,7 +871,7 @@ struct Sampler {
 // As finish_short, for up to kList entries.
 template <typename T>
 __device__ __noinline__ bool finish_long(const SampleParams& p, Shared& sm, int n, u64 best, u64 whole, float m, int top_k) {
-  Sampler<T> s(p, sm);
+  Sampler<T> s(p, sm, true);
   s.set_top(m);
   const int tid = s.tid;
     sort_falling(sm.all, n);
@@ -900,8 +910,8 @@ __device__ __noinline__ bool finish_long(const SampleParams& p, Shared& sm, int 
 // each limit, where `last`, from which on tokens are kept, is not known yet (1), then the sums of the
 // kept tokens.
 template <typename T>
-__device__ __noinline__ void slow_row(const SampleParams& p, Shared& sm, int turn, u64 best, float m, u64 last) {
-  Sampler<T> s(p, sm);
+__device__ __noinline__ void slow_row(const SampleParams& p, Shared& sm, bool alone, int turn, u64 best, float m, u64 last) {
+  Sampler<T> s(p, sm, alone);
   s.turn = turn;
   s.set_top(m);
   const Weigher weight = s.weight;
@@ -1105,7 +1115,7 @@ __device__ __noinline__ void slow_row(const SampleParams& p, Shared& sm, int tur
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) sample_token_kernel(const __grid_constant__ SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 4) sample_token_kernel(const __grid_constant__ SampleParams p) {
   __shared__ Shared sm;
   // what needs nothing of the stream before
   const u64 fine = p.fine[threadIdx.x & 31];
@@ -1113,11 +1123,12 @@ __global__ void __launch_bounds__(kThreads, 3) sample_token_kernel(const __grid_
   if (threadIdx.x == 0) sm.gathered = 0;
   __syncthreads();
   after_stream();
-  Sampler<T> s(p, sm);
+  Sampler<T> s(p, sm, false);
   if (s.blocks > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");  // waited for before another block's memory is touched
   u64 best = 0, last = 1;
+  int left = Sampler<T>::kTogether;
   if (s.temperature > 0.f && s.top_k == 0 && !(s.top_p < 1.f) && !(s.min_p > 0.f) && s.c_hi > 1e-30f) {
-    if (s.without_limits()) return;
+    left = s.without_limits();
   } else {
     // (doubles are slow: by one warp, while the logits are under way)
     if (s.min_p > 0.f && s.min_p <= 1.f && s.warp == kWarps - 1) sm.drop = log((double)s.min_p) * (double)s.temperature;
@@ -1127,14 +1138,15 @@ __global__ void __launch_bounds__(kThreads, 3) sample_token_kernel(const __grid_
       return;
     }
     s.set_top(value_of((uint32_t)(best >> 32)));
-    if (s.top_k || !(s.top_p < 1.f)) {
-      if ((s.top_k || s.min_p > 0.f) && s.by_list(best)) return;
-    } else {
+    if (s.top_k || (s.min_p > 0.f && !(s.top_p < 1.f))) {
+      left = s.by_list(best);
+    } else if (s.top_p < 1.f) {
       last = s.by_sums(best);
       if (last == 0) return;
     }
   }
-  slow_row<T>(p, sm, s.turn, best, s.top(), last);
+  if (left == Sampler<T>::kDone) return;
+  slow_row<T>(p, sm, left == Sampler<T>::kAlone, s.turn, best, s.top(), last);
 }
 
 }  // namespace
