@@ -17,8 +17,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxStrip = 64;   // rows of a block's strip
 constexpr int kStage = 1024;    // starts in shared memory
-constexpr int kHeld = 8;        // 16-byte pieces that a thread holds
-constexpr int kQueryHeld = 4;
+constexpr int kQueryHeld = 4;   // 16-byte pieces of queries that a thread has under way
 constexpr int kMaxTokens = 8;   // of a block of query rows
 constexpr int kNoRun = 255;
 
@@ -27,8 +26,9 @@ struct AppendParams {
   gpt_kv_append_fp8_args a;
   RotaryRates rates;
   int32_t strip;      // rows of a strip; a block has the runs that begin in one
-  int32_t kv_blocks;  // strips x key heads x 2; the blocks behind them have query rows
-  int32_t share;      // threads of a token of query rows are the block's >> share
+  int32_t heads;      // key heads of a block
+  int32_t kv_blocks;  // strips x groups of key heads x 2; the blocks behind them have query rows
+  int32_t tokens;     // of a block of query rows
 };
 
 // Where a row belongs.
@@ -102,10 +102,11 @@ __device__ __forceinline__ float scale_for(float top) {
   return __uint_as_float((uint32_t)(exponent - 7 + 127) << 23);
 }
 
-// Two numbers, rounded to nearest; what is not finite is NaN.
+// Two numbers, rounded to nearest; with kOdd what is not finite is NaN.
+template <bool kOdd>
 __device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
   uint16_t u;
-  a = fabsf(a) <= 448.f ? a : NAN, b = fabsf(b) <= 448.f ? b : NAN;
+  if (kOdd) a = fabsf(a) <= 448.f ? a : NAN, b = fabsf(b) <= 448.f ? b : NAN;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(u) : "f"(b), "f"(a));
   return u;
 }
@@ -115,52 +116,79 @@ __device__ __forceinline__ void unpack_e4m3(uint32_t u, float* x) {  // two
   asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}" : "=f"(x[0]), "=f"(x[1]) : "r"(h));
 }
 
-template <typename T>
-__device__ __forceinline__ float largest(const uint4& u) {
-  float x[Piece<T>::kN], m = 0.f;
-  Piece<T>::unpack(u, x);
+// The largest finite magnitude of a piece, as bits; *odd: there is one that is not finite.
+__device__ __forceinline__ uint32_t largest(const uint4& u, float, bool* odd) {
+  const uint32_t w[4] = {u.x & 0x7fffffffu, u.y & 0x7fffffffu, u.z & 0x7fffffffu, u.w & 0x7fffffffu};
+  uint32_t m = max(max(w[0], w[1]), max(w[2], w[3]));
+  if (__builtin_expect(m >= 0x7f800000u, 0)) {
+    *odd = true, m = 0;
 #pragma unroll
-  for (int i = 0; i < Piece<T>::kN; ++i) m = fabsf(x[i]) < INFINITY ? fmaxf(m, fabsf(x[i])) : m;
+    for (int i = 0; i < 4; ++i) m = w[i] < 0x7f800000u ? max(m, w[i]) : m;
+  }
   return m;
 }
-
-// Rotates the pairs of a piece whose first element is e of a head at position pos.
-template <int N>
-__device__ __forceinline__ void turn_piece(const AppendParams& p, float* x, int e, int pos) {
+__device__ __forceinline__ uint32_t largest(const uint4& u, __nv_bfloat16, bool* odd) {
+  const uint32_t w[4] = {u.x & 0x7fff7fffu, u.y & 0x7fff7fffu, u.z & 0x7fff7fffu, u.w & 0x7fff7fffu};
+  const uint32_t two = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
+  uint32_t m = max(two & 0xffffu, two >> 16);
+  if (__builtin_expect(m >= 0x7f80u, 0)) {
+    *odd = true, m = 0;
 #pragma unroll
-  for (int j = 0; j < N / 2; ++j)
-    if (e + 2 * j < p.a.rope_dims) {
-      float cs, sn;
-      pair_angle(p.rates, e / 2 + j, pos, &cs, &sn);
-      const float x0 = x[2 * j], x1 = x[2 * j + 1];
-      x[2 * j] = x0 * cs - x1 * sn;
-      x[2 * j + 1] = x0 * sn + x1 * cs;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = w[i] & 0xffffu, hi = w[i] >> 16;
+      m = lo < 0x7f80u ? max(m, lo) : m, m = hi < 0x7f80u ? max(m, hi) : m;
     }
+  }
+  return m << 16;
+}
+
+// Cosine and sine of the pairs of a piece whose first element is e of a head at position pos.
+template <int N>
+__device__ __forceinline__ void piece_angles(const AppendParams& p, int e, int pos, float2* turn) {
+#pragma unroll
+  for (int j = 0; j < N / 2; ++j) {
+    turn[j] = make_float2(1.f, 0.f);
+    if (e + 2 * j < p.a.rope_dims) pair_angle(p.rates, e / 2 + j, pos, &turn[j].x, &turn[j].y);
+  }
+}
+template <int N>
+__device__ __forceinline__ void turn_piece(float* x, const float2* turn) {
+#pragma unroll
+  for (int j = 0; j < N / 2; ++j) {
+    const float x0 = x[2 * j], x1 = x[2 * j + 1];
+    x[2 * j] = x0 * turn[j].x - x1 * turn[j].y;
+    x[2 * j + 1] = x0 * turn[j].y + x1 * turn[j].x;
+  }
 }
 
 struct Run {
   int begin, end;   // rows
   int page, slot;   // of the first row; page < 0: skipped
   int pos;          // of the first row
-  uint32_t top;     // largest magnitude, as bits
-  float old;        // the scale that was there
-  float inv, ratio; // 1 / scale, old / scale
 };
 
+// A block has a group of key heads, one after the other, of one side.  A thread has the same
+// rows and elements of each, so that it computes its sines and cosines once (of 8 heads of
+// 128 in 32,768 tokens each: as many instructions as all the rest).
 template <typename T>
 __device__ __forceinline__ void append_runs(const AppendParams& p, int* stage) {
-  constexpr int kN = Piece<T>::kN;
+  constexpr int kN = Piece<T>::kN, kHeld = 32 / kN;  // pieces that a thread holds: 32 elements
   __shared__ Run runs[kMaxStrip];
   __shared__ uint8_t run_of[kMaxStrip];
   __shared__ uint32_t begins[2];
-  __shared__ int rescale;
+  // of a head, in turns: largest magnitudes (as bits), 1 / scale, old scale / scale, whether one is not 1
+  __shared__ uint32_t tops[2][kMaxStrip];
+  __shared__ float inv[2][kMaxStrip], ratio[2][kMaxStrip];
+  __shared__ int rescale[2];
   const gpt_paged_cache& c = p.c.pages;
   const gpt_kv_append_fp8_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31;
-  const int unit = blockIdx.x, sides = 2 * c.n_kv_head;
-  const int strip0 = unit / sides * p.strip, side = unit % sides & 1, head = unit % sides >> 1;
+  const int groups = (c.n_kv_head + p.heads - 1) / p.heads, unit = blockIdx.x, sides = 2 * groups;
+  const int strip0 = unit / sides * p.strip, side = unit % sides & 1, head0 = (unit % sides >> 1) * p.heads;
+  const int head1 = min(head0 + p.heads, c.n_kv_head);
   const bool report = unit % sides == 0;
-  if (tid == 0) rescale = 0;
+  if (tid < 2) rescale[tid] = 0;
+  if (tid < 2 * kMaxStrip) tops[tid / kMaxStrip][tid % kMaxStrip] = 0;
   Row r{-1, 0, 0, 0};
   if (tid < p.strip && strip0 + tid < a.n_tokens) r = find_row(p, stage, strip0 + tid, report);
   const int slot = r.pos % c.page_size;
@@ -173,7 +201,6 @@ __device__ __forceinline__ void append_runs(const AppendParams& p, int* stage) {
   const uint64_t mask = begins[0] | (uint64_t)begins[1] << 32;
   if (mask == 0) return;
   const int n_runs = __popcll(mask);
-  float* scales = (side ? p.c.v_scale : p.c.k_scale) + head * p.c.scale_head;
   if (tid < kMaxStrip) {
     int mine = kNoRun;
     if (r.seq >= 0) {
@@ -184,142 +211,193 @@ __device__ __forceinline__ void append_runs(const AppendParams& p, int* stage) {
     if (begin) {
       Run& x = runs[mine];
       x.begin = strip0 + tid, x.end = (int)min((int64_t)r.end, (int64_t)strip0 + tid + c.page_size - slot);
-      x.page = page_of(p, r, report), x.slot = slot, x.pos = r.pos, x.top = 0;
-      x.old = x.page >= 0 && slot > 0 ? scales[x.page * p.c.scale_page] : 0.f;
+      x.page = page_of(p, r, report), x.slot = slot, x.pos = r.pos;
     }
   }
   __syncthreads();
   const int first = runs[0].begin, end = runs[n_runs - 1].end;
   const int pieces = c.head_dim / kN, per_pass = kThreads / pieces, window = kHeld * per_pass;
   const int group = tid / pieces, e = tid % pieces * kN;
-  const T* from = side ? (const T*)a.v + head * a.v_head + e : (const T*)a.k + head * a.k_head + e;
-  const int64_t stride = side ? a.v_row : a.k_row;
-  auto run_at = [&](int row) {  // of a row that is to be written
-    if (row >= end || group >= per_pass) return kNoRun;
-    const int x = row - strip0 < p.strip ? run_of[row - strip0] : n_runs - 1;
-    return x != kNoRun && runs[x].page >= 0 ? x : kNoRun;
-  };
+  const bool turns = side == 0 && e < a.rope_dims;
+  const T* from = (side ? (const T*)a.v : (const T*)a.k) + e;
+  const int64_t stride = side ? a.v_row : a.k_row, head_step = side ? a.v_head : a.k_head;
+  float* scales = side ? p.c.v_scale : p.c.k_scale;
+  uint8_t* cache = (uint8_t*)(side ? c.v : c.k);
+
   uint4 u[kHeld];
-  auto load = [&](int row0) {
+  int x[kHeld];          // run of a held row, kNoRun: not to be written
+  float2 turn[kHeld][kN / 2];
+  auto hold = [&](int row0) {
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
       const int row = row0 + i * per_pass + group;
-      if (run_at(row) != kNoRun) u[i] = __ldcs(reinterpret_cast<const uint4*>(from + row * stride));
+      x[i] = kNoRun;
+      if (row < end && group < per_pass) {
+        x[i] = row - strip0 < p.strip ? run_of[row - strip0] : n_runs - 1;
+        if (x[i] != kNoRun && runs[x[i]].page < 0) x[i] = kNoRun;
+      }
     }
   };
-  for (int row0 = first; row0 < end; row0 += window) {
-    load(row0);
+  auto load = [&](int row0, int head) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (x[i] != kNoRun) u[i] = __ldcs(reinterpret_cast<const uint4*>(from + head * head_step + (row0 + i * per_pass + group) * stride));
+  };
+  auto angles = [&](int row0) {
+    if (turns)
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        if (x[i] != kNoRun) piece_angles<kN>(p, e, runs[x[i]].pos + (row0 + i * per_pass + group - runs[x[i]].begin), turn[i]);
+  };
+  bool odd = false;
+  auto look = [&](uint32_t* top) {  // the held rows' largest magnitudes
     int now = kNoRun;
-    float top = 0.f;
+    uint32_t most = 0;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
-      const int x = run_at(row0 + i * per_pass + group);
-      if (x == kNoRun) continue;
-      if (x != now) {
-        if (now != kNoRun) atomicMax(&runs[now].top, __float_as_uint(top));
-        now = x, top = 0.f;
+      if (x[i] == kNoRun) continue;
+      if (x[i] != now) {
+        if (now != kNoRun) atomicMax(&top[now], most);
+        now = x[i], most = 0;
       }
-      top = fmaxf(top, largest<T>(u[i]));
+      most = max(most, largest(u[i], T(), &odd));
     }
     __syncwarp();
     const uint32_t same = __match_any_sync(0xffffffffu, now);
-    const uint32_t bits = __reduce_max_sync(same, __float_as_uint(top));
-    if (now != kNoRun && lane == __ffs(same) - 1) atomicMax(&runs[now].top, bits);
-  }
-  __syncthreads();
-  if (tid < n_runs && runs[tid].page >= 0) {
-    Run& x = runs[tid];
-    float scale = scale_for(__uint_as_float(x.top));
-    x.ratio = 1.f;
-    if (x.slot > 0) {
-      scale = fmaxf(scale, x.old);
-      if (scale != x.old) x.ratio = x.old / scale, rescale = 1;
+    most = __reduce_max_sync(same, most);
+    if (now != kNoRun && lane == __ffs(same) - 1) atomicMax(&top[now], most);
+  };
+  auto settle = [&](int turn_, int head) {  // the scales
+    if (tid == 0) rescale[turn_ ^ 1] = 0;
+    if (tid < n_runs && runs[tid].page >= 0) {
+      float* at = scales + runs[tid].page * p.c.scale_page + head * p.c.scale_head;
+      float scale = scale_for(__uint_as_float(tops[turn_][tid])), share = 1.f;
+      if (runs[tid].slot > 0) {
+        const float old = *at;
+        scale = fmaxf(scale, old);
+        if (scale != old) share = old / scale, rescale[turn_] = 1;
+      }
+      *at = scale;
+      inv[turn_][tid] = 1.f / scale, ratio[turn_][tid] = share;
+      tops[turn_ ^ 1][tid] = 0;
     }
-    x.inv = 1.f / scale;
-    scales[x.page * p.c.scale_page] = scale;
-  }
-  __syncthreads();
-  uint8_t* cache = (uint8_t*)(side ? c.v : c.k) + head * c.head_stride;
-  if (rescale)
-    for (int x = 0; x < n_runs; ++x) {
-      if (runs[x].page < 0 || runs[x].ratio == 1.f) continue;
-      const float ratio = runs[x].ratio;
-      for (int i = tid; i < runs[x].slot * (c.head_dim / 16); i += kThreads) {
-        uint4* at = reinterpret_cast<uint4*>(cache + runs[x].page * c.page_stride + i / (c.head_dim / 16) * c.slot_stride) + i % (c.head_dim / 16);
+  };
+  auto bring = [&](int turn_, int head) {  // the numbers before the new ones, to a larger scale
+    for (int y = 0; y < n_runs; ++y) {
+      const float by = ratio[turn_][y];
+      if (runs[y].page < 0 || by == 1.f) continue;
+      const int each = c.head_dim / 16;
+      for (int i = tid; i < runs[y].slot * each; i += kThreads) {
+        uint4* at = reinterpret_cast<uint4*>(cache + head * c.head_stride + runs[y].page * c.page_stride + i / each * c.slot_stride) + i % each;
         uint4 v = *at;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint32_t& w = (&v.x)[j];
-          float y[4];
-          unpack_e4m3(w & 0xffffu, y), unpack_e4m3(w >> 16, y + 2);
-          w = pack_e4m3(y[0] * ratio, y[1] * ratio) | pack_e4m3(y[2] * ratio, y[3] * ratio) << 16;
+          float z[4];
+          unpack_e4m3(w & 0xffffu, z), unpack_e4m3(w >> 16, z + 2);
+          w = pack_e4m3<true>(z[0] * by, z[1] * by) | pack_e4m3<true>(z[2] * by, z[3] * by) << 16;
         }
         *at = v;
       }
     }
-  for (int row0 = first; row0 < end; row0 += window) {
-    if (end - first > window) load(row0);
+  };
+  auto write = [&](int row0, int turn_, int head) {
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
-      const int row = row0 + i * per_pass + group, x = run_at(row);
-      if (x == kNoRun) continue;
-      const int into = row - runs[x].begin;
+      if (x[i] == kNoRun) continue;
+      const Run& run = runs[x[i]];
+      const float by = inv[turn_][x[i]];
       float y[kN];
       Piece<T>::unpack(u[i], y);
 #pragma unroll
-      for (int j = 0; j < kN; ++j) y[j] *= runs[x].inv;
-      if (side == 0) turn_piece<kN>(p, y, e, runs[x].pos + into);
+      for (int j = 0; j < kN; ++j) y[j] *= by;
+      if (turns) turn_piece<kN>(y, turn[i]);
       uint32_t w[kN / 4];
+      if (__builtin_expect(odd, 0)) {
 #pragma unroll
-      for (int j = 0; j < kN / 4; ++j) w[j] = pack_e4m3(y[4 * j], y[4 * j + 1]) | pack_e4m3(y[4 * j + 2], y[4 * j + 3]) << 16;
-      uint8_t* to = cache + runs[x].page * c.page_stride + (runs[x].slot + into) * c.slot_stride + e;
+        for (int j = 0; j < kN / 4; ++j) w[j] = pack_e4m3<true>(y[4 * j], y[4 * j + 1]) | pack_e4m3<true>(y[4 * j + 2], y[4 * j + 3]) << 16;
+      } else {
+#pragma unroll
+        for (int j = 0; j < kN / 4; ++j) w[j] = pack_e4m3<false>(y[4 * j], y[4 * j + 1]) | pack_e4m3<false>(y[4 * j + 2], y[4 * j + 3]) << 16;
+      }
+      uint8_t* to = cache + head * c.head_stride + run.page * c.page_stride + (run.slot + (row0 + i * per_pass + group - run.begin)) * c.slot_stride + e;
       if constexpr (kN == 8) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
       else *reinterpret_cast<uint32_t*>(to) = w[0];
+    }
+  };
+  const bool once = end - first <= window;
+  if (once) hold(first), load(first, head0), angles(first);
+#pragma unroll 1
+  for (int head = head0; head < head1; ++head) {
+    const int t = (head - head0) & 1;
+    if (once) {
+      if (head > head0) load(first, head);
+      look(tops[t]);
+    } else {
+      for (int row0 = first; row0 < end; row0 += window) hold(row0), load(row0, head), look(tops[t]);
+    }
+    __syncthreads();
+    settle(t, head);
+    __syncthreads();
+    if (rescale[t]) bring(t, head);
+    if (once) {
+      write(first, t, head);
+    } else {
+      for (int row0 = first; row0 < end; row0 += window) hold(row0), load(row0, head), angles(row0), write(row0, t, head);
     }
   }
 }
 
-// Query rows: as kv_append_kernel's, a token's sines and cosines once for all of its heads.
+// Query rows: a token's sines and cosines once for all of its heads.
 template <typename T>
 __device__ __forceinline__ void turn_queries(const AppendParams& p, const int* stage) {
   constexpr int kN = Piece<T>::kN;
   __shared__ __align__(16) float2 turns[kMaxTokens][kMaxPairs];  // cosine, sine
+  __shared__ int positions[kMaxTokens];                          // -1: left out
   const gpt_kv_append_fp8_args& a = p.a;
-  const int threads = kThreads >> p.share, tid = threadIdx.x % threads, sub = threadIdx.x / threads;
-  const int64_t n = ((int64_t)(blockIdx.x - p.kv_blocks) << p.share) + sub;
-  Row r{-1, 0, 0, 0};
-  if (n < a.n_tokens) r = find_row(p, stage, (int)n, false);
-  if (r.seq >= 0 && page_of(p, r, false) < 0) r.seq = -1;
-  if (r.seq >= 0)
-    for (int i = tid; i < a.rope_dims / 2; i += threads) pair_angle(p.rates, i, r.pos, &turns[sub][i].x, &turns[sub][i].y);
+  const int tid = threadIdx.x, n0 = (blockIdx.x - p.kv_blocks) * p.tokens, n = min(p.tokens, a.n_tokens - n0);
+  if (tid < n) {
+    const Row r = find_row(p, stage, n0 + tid, false);
+    positions[tid] = r.seq >= 0 && page_of(p, r, false) >= 0 ? r.pos : -1;
+  }
   __syncthreads();
-  if (r.seq < 0) return;
-  const int pieces = p.c.pages.head_dim / kN, groups = threads / pieces, group = tid / pieces, e = tid % pieces * kN;
+  const int pairs = a.rope_dims / 2;
+  for (int i = tid; i < n * kMaxPairs; i += kThreads)
+    if (i % kMaxPairs < pairs && positions[i / kMaxPairs] >= 0)
+      pair_angle(p.rates, i % kMaxPairs, positions[i / kMaxPairs], &turns[i / kMaxPairs][i % kMaxPairs].x, &turns[i / kMaxPairs][i % kMaxPairs].y);
+  __syncthreads();
+  const int pieces = p.c.pages.head_dim / kN, groups = kThreads / pieces, group = tid / pieces, e = tid % pieces * kN;
   if (group >= groups) return;
-  const T* from = (const T*)a.q + n * a.q_row + e;
-  T* to = (T*)a.q_out + n * a.qo_row + e;
-  for (int h0 = group; h0 < a.n_head; h0 += kQueryHeld * groups) {
+  const T* from = (const T*)a.q + (int64_t)n0 * a.q_row + e;
+  T* to = (T*)a.q_out + (int64_t)n0 * a.qo_row + e;
+  const int rows = n * a.n_head;
+  for (int row0 = group; row0 < rows; row0 += kQueryHeld * groups) {
     uint4 u[kQueryHeld];
-#pragma unroll
-    for (int i = 0; i < kQueryHeld; ++i)
-      if (h0 + i * groups < a.n_head) u[i] = __ldcs(reinterpret_cast<const uint4*>(from + (h0 + i * groups) * a.q_head));
+    int token[kQueryHeld], head[kQueryHeld];
 #pragma unroll
     for (int i = 0; i < kQueryHeld; ++i) {
-      if (h0 + i * groups >= a.n_head) break;
+      const int row = row0 + i * groups;
+      token[i] = row / a.n_head, head[i] = row % a.n_head;
+      if (row >= rows || positions[token[i]] < 0) token[i] = -1;
+      else u[i] = __ldcs(reinterpret_cast<const uint4*>(from + token[i] * a.q_row + head[i] * a.q_head));
+    }
+#pragma unroll
+    for (int i = 0; i < kQueryHeld; ++i) {
+      if (token[i] < 0) continue;
       if (e < a.rope_dims) {
         float x[kN];
         Piece<T>::unpack(u[i], x);
 #pragma unroll
         for (int j = 0; j < kN / 2; ++j)
           if (e + 2 * j < a.rope_dims) {
-            const float2 t = turns[sub][e / 2 + j];
+            const float2 t = turns[token[i]][e / 2 + j];
             const float x0 = x[2 * j], x1 = x[2 * j + 1];
             x[2 * j] = x0 * t.x - x1 * t.y;
             x[2 * j + 1] = x0 * t.y + x1 * t.x;
           }
         u[i] = Piece<T>::pack(x);
       }
-      *reinterpret_cast<uint4*>(to + (h0 + i * groups) * a.qo_head) = u[i];
+      *reinterpret_cast<uint4*>(to + token[i] * a.qo_row + head[i] * a.qo_head) = u[i];
     }
   }
 }
@@ -379,14 +457,15 @@ extern "C" int gpt_kv_append_fp8(const gpt_fp8_cache* cache, const gpt_kv_append
   p.c = *cache;
   p.a = *a;
   if (a->rope_dims > 0) set_rates(&p.rates, a->rope_base, a->rope_dims);
-  p.strip = a->n_tokens <= 4096 ? 16 : kMaxStrip;
-  const int64_t kv_blocks = ((int64_t)a->n_tokens + p.strip - 1) / p.strip * 2 * c->n_kv_head;
-  p.share = 0;
-  const int pieces = c->head_dim * es / 16;
-  while ((1 << p.share) < kMaxTokens && a->n_head * pieces << (p.share + 1) <= kThreads * kQueryHeld && kThreads >> (p.share + 1) >= pieces &&
-         a->n_tokens >> (p.share + 1) >= 608)
-    ++p.share;
-  const int64_t q_blocks = a->n_head > 0 ? ((int64_t)a->n_tokens + (1 << p.share) - 1) >> p.share : 0;
+  // Rows of a strip: as many as leave two units a block and SM (the window of a block's registers
+  // is 64 rows of 128), 16 at least; then heads of a block.
+  const auto units = [&](int rows) { return ((int64_t)a->n_tokens + rows - 1) / rows * 2 * c->n_kv_head; };
+  p.strip = kMaxStrip;
+  while (p.strip > 16 && units(p.strip) < 608) p.strip /= 2;
+  p.heads = (int32_t)std::max<int64_t>(1, std::min<int64_t>(c->n_kv_head, units(p.strip) / 1216));
+  const int64_t kv_blocks = units(p.strip) / c->n_kv_head * ((c->n_kv_head + p.heads - 1) / p.heads);
+  p.tokens = std::max(1, std::min(kMaxTokens, a->n_tokens / 1216));
+  const int64_t q_blocks = a->n_head > 0 ? ((int64_t)a->n_tokens + p.tokens - 1) / p.tokens : 0;
   if (kv_blocks + q_blocks > INT32_MAX) return call_error(GPT_ERR_UNSUPPORTED, "n_tokens x n_kv_head is too large for one call");
   p.kv_blocks = (int32_t)kv_blocks;
   const dim3 grid((unsigned)(kv_blocks + q_blocks));
