@@ -3,22 +3,23 @@
 // rotated on the way (rotary.h).
 //
 // A run: the new rows of one page.  Its scale needs the largest magnitude of all of them
-// before the first number is written, so one block has a run's rows of one key head and
-// side (keys or values), holds them in registers between the two passes, and owns the
-// scale: no atomics on global memory, no second kernel.  The scale comes from the
-// magnitudes before the rotation, which turns each pair by at most sqrt 2: it is then
-// exact, the same however sines are rounded, and no number reaches 448.
+// before the first number is written, so one warp has a run's rows of one key head and
+// side (keys or values), reads them twice (the second time from L2) and owns the scale: no
+// atomics on global memory, no barrier between the two passes, no second kernel.  The
+// scale comes from the magnitudes before the rotation, which turns each pair by at most
+// sqrt 2: it is then exact, the same however sines are rounded, and no number reaches 448.
 // Bound: HBM (rows read once, numbers and rotated queries written once).
 #include "rotary.h"
 
 namespace pgs {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxStrip = 64;   // rows of a block's strip
-constexpr int kStage = 1024;    // starts in shared memory
-constexpr int kQueryHeld = 4;   // 16-byte pieces of queries that a thread has under way
-constexpr int kMaxTokens = 8;   // of a block of query rows
+constexpr int kMostWarps = 8;
+constexpr int kMaxStrip = 64;    // rows of a block's strip, and of the table of sines and cosines
+constexpr int kStage = 1024;     // starts in shared memory
+constexpr int kUnder = 8;        // 16-byte pieces that a thread has under way
+constexpr int kQueryUnder = 4;   // the same of queries
+constexpr int kMaxTokens = 8;    // of a block of query rows
 constexpr int kNoRun = 255;
 
 struct AppendParams {
@@ -26,8 +27,9 @@ struct AppendParams {
   gpt_kv_append_fp8_args a;
   RotaryRates rates;
   int32_t strip;      // rows of a strip; a block has the runs that begin in one
-  int32_t heads;      // key heads of a block
-  int32_t kv_blocks;  // strips x groups of key heads x 2; the blocks behind them have query rows
+  int32_t groups;     // of key heads: a block has one,
+  int32_t warps;      // a warp for each head
+  int32_t kv_blocks;  // strips x groups x 2; the others have query rows
   int32_t tokens;     // of a block of query rows
 };
 
@@ -142,22 +144,20 @@ __device__ __forceinline__ uint32_t largest(const uint4& u, __nv_bfloat16, bool*
   return m << 16;
 }
 
-// Cosine and sine of the pairs of a piece whose first element is e of a head at position pos.
-template <int N>
-__device__ __forceinline__ void piece_angles(const AppendParams& p, int e, int pos, float2* turn) {
+// The numbers of a page's first slots, of one head, times `by`: by `threads` threads, the first of them 0.
+__device__ __forceinline__ void bring_numbers(const gpt_paged_cache& c, uint8_t* page, int slots, float by, int thread, int threads) {
+  const int each = c.head_dim / 16;
+  for (int i = thread; i < slots * each; i += threads) {
+    uint4* at = reinterpret_cast<uint4*>(page + i / each * c.slot_stride) + i % each;
+    uint4 v = *at;
 #pragma unroll
-  for (int j = 0; j < N / 2; ++j) {
-    turn[j] = make_float2(1.f, 0.f);
-    if (e + 2 * j < p.a.rope_dims) pair_angle(p.rates, e / 2 + j, pos, &turn[j].x, &turn[j].y);
-  }
-}
-template <int N>
-__device__ __forceinline__ void turn_piece(float* x, const float2* turn) {
-#pragma unroll
-  for (int j = 0; j < N / 2; ++j) {
-    const float x0 = x[2 * j], x1 = x[2 * j + 1];
-    x[2 * j] = x0 * turn[j].x - x1 * turn[j].y;
-    x[2 * j + 1] = x0 * turn[j].y + x1 * turn[j].x;
+    for (int j = 0; j < 4; ++j) {
+      uint32_t& w = (&v.x)[j];
+      float x[4];
+      unpack_e4m3(w & 0xffffu, x), unpack_e4m3(w >> 16, x + 2);
+      w = pack_e4m3<true>(x[0] * by, x[1] * by) | pack_e4m3<true>(x[2] * by, x[3] * by) << 16;
+    }
+    *at = v;
   }
 }
 
@@ -167,234 +167,295 @@ struct Run {
   int pos;          // of the first row
 };
 
-// A block has a group of key heads, one after the other, of one side.  A thread has the same
-// rows and elements of each, so that it computes its sines and cosines once (of 8 heads of
-// 128 in 32,768 tokens each: as many instructions as all the rest).
+// A block's strip of rows, of a group of heads and one side: the runs that begin in it.
 template <typename T>
-__device__ __forceinline__ void append_runs(const AppendParams& p, int* stage) {
-  constexpr int kN = Piece<T>::kN, kHeld = 32 / kN;  // pieces that a thread holds: 32 elements
+__device__ __forceinline__ void append_runs(const AppendParams& p, const RotaryRates& rates, const int* stage, float2* turns, int unit) {
+  constexpr int kN = Piece<T>::kN;
   __shared__ Run runs[kMaxStrip];
   __shared__ uint8_t run_of[kMaxStrip];
-  __shared__ uint32_t begins[2];
-  // of a head, in turns: largest magnitudes (as bits), 1 / scale, old scale / scale, whether one is not 1
-  __shared__ uint32_t tops[2][kMaxStrip];
-  __shared__ float inv[2][kMaxStrip], ratio[2][kMaxStrip];
-  __shared__ int rescale[2];
+  __shared__ int many;
+  // of a warp's head: largest magnitudes (as bits), 1 / scale
+  __shared__ uint32_t tops[kMostWarps][kMaxStrip];
+  __shared__ float invs[kMostWarps][kMaxStrip];
   const gpt_paged_cache& c = p.c.pages;
   const gpt_kv_append_fp8_args& a = p.a;
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int groups = (c.n_kv_head + p.heads - 1) / p.heads, unit = blockIdx.x, sides = 2 * groups;
-  const int strip0 = unit / sides * p.strip, side = unit % sides & 1, head0 = (unit % sides >> 1) * p.heads;
-  const int head1 = min(head0 + p.heads, c.n_kv_head);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sides = 2 * p.groups;
+  const int strip0 = unit / sides * p.strip, side = unit % sides & 1, head = (unit % sides >> 1) * p.warps + warp;
   const bool report = unit % sides == 0;
-  if (tid < 2) rescale[tid] = 0;
-  if (tid < 2 * kMaxStrip) tops[tid / kMaxStrip][tid % kMaxStrip] = 0;
-  Row r{-1, 0, 0, 0};
-  if (tid < p.strip && strip0 + tid < a.n_tokens) r = find_row(p, stage, strip0 + tid, report);
-  const int slot = r.pos % c.page_size;
-  const bool begin = r.seq >= 0 && (strip0 + tid == r.first || slot == 0);
-  if (tid < kMaxStrip) {
-    const uint32_t mask = __ballot_sync(0xffffffffu, begin);
-    if (lane == 0) begins[tid >> 5] = mask;
+  // the runs, by the first warp
+  if (warp == 0) {
+    uint64_t mask = 0;
+    Row r[2];
+    int slot[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = lane + 32 * k;
+      r[k] = Row{-1, 0, 0, 0};
+      if (i < p.strip && strip0 + i < a.n_tokens) r[k] = find_row(p, stage, strip0 + i, report);
+      slot[k] = r[k].pos % c.page_size;
+      mask |= (uint64_t)__ballot_sync(0xffffffffu, r[k].seq >= 0 && (strip0 + i == r[k].first || slot[k] == 0)) << (32 * k);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = lane + 32 * k;
+      int mine = kNoRun;
+      if (r[k].seq >= 0) {
+        const int at = i - min(slot[k], strip0 + i - r[k].first);  // where its run begins
+        if (at >= 0 && (mask >> at) & 1u) mine = __popcll(mask & ((1ull << at) - 1ull));
+      }
+      run_of[i] = (uint8_t)mine;
+      if ((mask >> i) & 1u) {
+        Run& x = runs[mine];
+        x.begin = strip0 + i, x.end = (int)min((int64_t)r[k].end, (int64_t)strip0 + i + c.page_size - slot[k]);
+        x.page = page_of(p, r[k], report), x.slot = slot[k], x.pos = r[k].pos;
+      }
+    }
+    if (lane == 0) many = __popcll(mask);
   }
   __syncthreads();
-  const uint64_t mask = begins[0] | (uint64_t)begins[1] << 32;
-  if (mask == 0) return;
-  const int n_runs = __popcll(mask);
-  if (tid < kMaxStrip) {
-    int mine = kNoRun;
-    if (r.seq >= 0) {
-      const int at = tid - min(slot, strip0 + tid - r.first);  // where its run begins
-      if (at >= 0 && (mask >> at) & 1u) mine = __popcll(mask & ((1ull << at) - 1ull));
-    }
-    run_of[tid] = (uint8_t)mine;
-    if (begin) {
-      Run& x = runs[mine];
-      x.begin = strip0 + tid, x.end = (int)min((int64_t)r.end, (int64_t)strip0 + tid + c.page_size - slot);
-      x.page = page_of(p, r, report), x.slot = slot, x.pos = r.pos;
-    }
-  }
-  __syncthreads();
+  const int n_runs = many;
+  if (n_runs == 0) return;
   const int first = runs[0].begin, end = runs[n_runs - 1].end;
-  const int pieces = c.head_dim / kN, per_pass = kThreads / pieces, window = kHeld * per_pass;
-  const int group = tid / pieces, e = tid % pieces * kN;
-  const bool turns = side == 0 && e < a.rope_dims;
-  const T* from = (side ? (const T*)a.v : (const T*)a.k) + e;
-  const int64_t stride = side ? a.v_row : a.k_row, head_step = side ? a.v_head : a.k_head;
-  float* scales = side ? p.c.v_scale : p.c.k_scale;
-  uint8_t* cache = (uint8_t*)(side ? c.v : c.k);
+  const bool works = warp < p.warps && head < c.n_kv_head;
+  auto run_at = [&](int row) {  // of a row below `end`, kNoRun: not to be written
+    const int x = n_runs == 1 ? 0 : row - strip0 < p.strip ? run_of[row - strip0] : n_runs - 1;
+    return x != kNoRun && runs[x].page >= 0 ? x : kNoRun;
+  };
 
-  uint4 u[kHeld];
-  int x[kHeld];          // run of a held row, kNoRun: not to be written
-  float2 turn[kHeld][kN / 2];
-  auto hold = [&](int row0) {
+  // A lane has a piece of every `side by side`-th row.
+  const int pieces = c.head_dim / kN, beside = 32 / pieces, sub = lane / pieces, e = (sub < beside ? lane % pieces : pieces - 1) * kN;
+  const int64_t stride = side ? a.v_row : a.k_row;
+  const T* from = (side ? (const T*)a.v + head * a.v_head : (const T*)a.k + head * a.k_head) + e;
+  bool odd = false;
+  uint4 u[kUnder];
+  auto load = [&](int row0, int stop) {
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int row = row0 + i * per_pass + group;
-      x[i] = kNoRun;
-      if (row < end && group < per_pass) {
-        x[i] = row - strip0 < p.strip ? run_of[row - strip0] : n_runs - 1;
-        if (x[i] != kNoRun && runs[x[i]].page < 0) x[i] = kNoRun;
-      }
+    for (int i = 0; i < kUnder; ++i) {
+      const int row = row0 + i * beside + sub;
+      u[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (sub < beside && row < stop && run_at(row) != kNoRun) u[i] = __ldcg(reinterpret_cast<const uint4*>(from + row * stride));
     }
   };
-  auto load = [&](int row0, int head) {
+  // Runs of eight rows and more on the average: one after the other, rows past the end as the last
+  // one again (and lanes past the pieces of a load as the last ones), so that nothing is conditional.
+  const bool runs_long = end - first >= 8 * n_runs;
+  const int sub_of = min(sub, beside - 1);
+  auto load_run = [&](const T* at, int row0, int last) {
+    const bool half = row0 + kUnder / 2 * beside > last;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-      if (x[i] != kNoRun) u[i] = __ldcs(reinterpret_cast<const uint4*>(from + head * head_step + (row0 + i * per_pass + group) * stride));
+    for (int i = 0; i < kUnder; ++i)
+      if (i < kUnder / 2 || !half) u[i] = __ldcg(reinterpret_cast<const uint4*>(at + min(row0 + i * beside + sub_of, last) * stride));
   };
-  auto angles = [&](int row0) {
-    if (turns)
+  if (works) {
+    // the first pass: magnitudes
+    if (runs_long) {
+#pragma unroll 1
+      for (int y = 0; y < n_runs; ++y) {
+        if (runs[y].page < 0) continue;
+        uint32_t top = 0;
+        const int last = runs[y].end - 1;
+#pragma unroll 1
+        for (int row0 = runs[y].begin; row0 <= last; row0 += kUnder * beside) {
+          load_run(from, row0, last);
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i)
-        if (x[i] != kNoRun) piece_angles<kN>(p, e, runs[x[i]].pos + (row0 + i * per_pass + group - runs[x[i]].begin), turn[i]);
-  };
-  bool odd = false;
-  auto look = [&](uint32_t* top) {  // the held rows' largest magnitudes
-    int now = kNoRun;
-    uint32_t most = 0;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      if (x[i] == kNoRun) continue;
-      if (x[i] != now) {
-        if (now != kNoRun) atomicMax(&top[now], most);
-        now = x[i], most = 0;
+          for (int i = 0; i < kUnder; ++i)
+            if (i < kUnder / 2 || row0 + kUnder / 2 * beside <= last) top = max(top, largest(u[i], T(), &odd));
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) tops[warp][y] = top;
       }
-      most = max(most, largest(u[i], T(), &odd));
+    } else {
+      for (int i = lane; i < n_runs; i += 32) tops[warp][i] = 0;
+      __syncwarp();
+      const uint32_t same = __match_any_sync(0xffffffffu, sub);
+      for (int row0 = first; row0 < end; row0 += kUnder * beside) {
+        load(row0, end);
+#pragma unroll
+        for (int i = 0; i < kUnder; ++i) {
+          const int row = row0 + i * beside + sub;
+          const uint32_t top = __reduce_max_sync(same, largest(u[i], T(), &odd));
+          if (sub < beside && e == 0 && row < end && top) {
+            const int x = run_at(row);
+            if (x != kNoRun) atomicMax(&tops[warp][x], top);
+          }
+        }
+      }
+    }
+    odd = __any_sync(0xffffffffu, odd);
+    __syncwarp();
+    // scales; the numbers before the new ones are brought to a larger one
+    float* scales = (side ? p.c.v_scale : p.c.k_scale) + head * p.c.scale_head;
+    uint8_t* cache = (uint8_t*)(side ? c.v : c.k) + head * c.head_stride;
+    for (int y0 = 0; y0 < n_runs; y0 += 32) {
+      const int y = y0 + lane;
+      float share = 1.f;
+      if (y < n_runs && runs[y].page >= 0) {
+        float* at = scales + runs[y].page * p.c.scale_page;
+        float scale = scale_for(__uint_as_float(tops[warp][y]));
+        if (runs[y].slot > 0) {
+          const float old = *at;
+          scale = fmaxf(scale, old);
+          if (scale != old) share = old / scale;
+        }
+        *at = scale;
+        invs[warp][y] = 1.f / scale;
+      }
+      for (uint32_t left = __ballot_sync(0xffffffffu, share != 1.f); left; left &= left - 1) {
+        const int z = y0 + __ffs(left) - 1;
+        const float by = __shfl_sync(0xffffffffu, share, z - y0);
+        bring_numbers(c, cache + runs[z].page * c.page_stride, runs[z].slot, by, lane, 32);
+      }
     }
     __syncwarp();
-    const uint32_t same = __match_any_sync(0xffffffffu, now);
-    most = __reduce_max_sync(same, most);
-    if (now != kNoRun && lane == __ffs(same) - 1) atomicMax(&top[now], most);
-  };
-  auto settle = [&](int turn_, int head) {  // the scales
-    if (tid == 0) rescale[turn_ ^ 1] = 0;
-    if (tid < n_runs && runs[tid].page >= 0) {
-      float* at = scales + runs[tid].page * p.c.scale_page + head * p.c.scale_head;
-      float scale = scale_for(__uint_as_float(tops[turn_][tid])), share = 1.f;
-      if (runs[tid].slot > 0) {
-        const float old = *at;
-        scale = fmaxf(scale, old);
-        if (scale != old) share = old / scale, rescale[turn_] = 1;
+  }
+  // the second pass, 64 rows at a time: sines and cosines by the block, numbers by the warps
+  const int pairs = side == 0 ? a.rope_dims / 2 : 0;
+  uint8_t* cache = (uint8_t*)(side ? c.v : c.k) + head * c.head_stride + e;
+  for (int chunk = first; chunk < end; chunk += kMaxStrip) {
+    const int stop = min(end, chunk + kMaxStrip);
+    if (pairs > 0) {
+      __syncthreads();
+      for (int i = tid; i < (stop - chunk) * kMaxPairs; i += blockDim.x) {
+        const int row = chunk + i / kMaxPairs, pair = i % kMaxPairs, x = run_at(row);
+        turns[i] = make_float2(1.f, 0.f);
+        if (pair < pairs && x != kNoRun) pair_angle(rates, pair, runs[x].pos + (row - runs[x].begin), &turns[i].x, &turns[i].y);
       }
-      *at = scale;
-      inv[turn_][tid] = 1.f / scale, ratio[turn_][tid] = share;
-      tops[turn_ ^ 1][tid] = 0;
+      __syncthreads();
     }
-  };
-  auto bring = [&](int turn_, int head) {  // the numbers before the new ones, to a larger scale
-    for (int y = 0; y < n_runs; ++y) {
-      const float by = ratio[turn_][y];
-      if (runs[y].page < 0 || by == 1.f) continue;
-      const int each = c.head_dim / 16;
-      for (int i = tid; i < runs[y].slot * each; i += kThreads) {
-        uint4* at = reinterpret_cast<uint4*>(cache + head * c.head_stride + runs[y].page * c.page_stride + i / each * c.slot_stride) + i % each;
-        uint4 v = *at;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t& w = (&v.x)[j];
-          float z[4];
-          unpack_e4m3(w & 0xffffu, z), unpack_e4m3(w >> 16, z + 2);
-          w = pack_e4m3<true>(z[0] * by, z[1] * by) | pack_e4m3<true>(z[2] * by, z[3] * by) << 16;
-        }
-        *at = v;
-      }
-    }
-  };
-  auto write = [&](int row0, int turn_, int head) {
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      if (x[i] == kNoRun) continue;
-      const Run& run = runs[x[i]];
-      const float by = inv[turn_][x[i]];
-      float y[kN];
-      Piece<T>::unpack(u[i], y);
-#pragma unroll
-      for (int j = 0; j < kN; ++j) y[j] *= by;
-      if (turns) turn_piece<kN>(y, turn[i]);
-      uint32_t w[kN / 4];
-      if (__builtin_expect(odd, 0)) {
-#pragma unroll
-        for (int j = 0; j < kN / 4; ++j) w[j] = pack_e4m3<true>(y[4 * j], y[4 * j + 1]) | pack_e4m3<true>(y[4 * j + 2], y[4 * j + 3]) << 16;
-      } else {
-#pragma unroll
-        for (int j = 0; j < kN / 4; ++j) w[j] = pack_e4m3<false>(y[4 * j], y[4 * j + 1]) | pack_e4m3<false>(y[4 * j + 2], y[4 * j + 3]) << 16;
-      }
-      uint8_t* to = cache + head * c.head_stride + run.page * c.page_stride + (run.slot + (row0 + i * per_pass + group - run.begin)) * c.slot_stride + e;
-      if constexpr (kN == 8) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
-      else *reinterpret_cast<uint32_t*>(to) = w[0];
-    }
-  };
-  const bool once = end - first <= window;
-  if (once) hold(first), load(first, head0), angles(first);
+    if (!works) continue;
+    if (runs_long && !odd) {
 #pragma unroll 1
-  for (int head = head0; head < head1; ++head) {
-    const int t = (head - head0) & 1;
-    if (once) {
-      if (head > head0) load(first, head);
-      look(tops[t]);
-    } else {
-      for (int row0 = first; row0 < end; row0 += window) hold(row0), load(row0, head), look(tops[t]);
+      for (int y = 0; y < n_runs; ++y) {
+        if (runs[y].page < 0) continue;
+        const int last = min(runs[y].end, stop) - 1;
+        const float by = invs[warp][y];
+        uint8_t* to = cache + runs[y].page * c.page_stride + (int64_t)(runs[y].slot - runs[y].begin) * c.slot_stride;
+#pragma unroll 1
+        for (int row0 = max(runs[y].begin, chunk); row0 <= last; row0 += kUnder * beside) {
+          load_run(from, row0, last);
+#pragma unroll
+          for (int i = 0; i < kUnder; ++i) {
+            if (i == kUnder / 2 && row0 + kUnder / 2 * beside > last) break;
+            const int row = min(row0 + i * beside + sub_of, last);
+            float x[kN];
+            Piece<T>::unpack(u[i], x);
+#pragma unroll
+            for (int j = 0; j < kN; j += 2) {
+              const float2 z = mul(Pair(x[j], x[j + 1]), Pair(by)).both();
+              x[j] = z.x, x[j + 1] = z.y;
+            }
+            if (pairs > 0) {
+              const float4* turn = reinterpret_cast<const float4*>(turns + (row - chunk) * kMaxPairs + e / 2);
+#pragma unroll
+              for (int j = 0; j < kN / 4; ++j) {
+                const float4 t = turn[j];
+                const float a0 = x[4 * j], a1 = x[4 * j + 1], b0 = x[4 * j + 2], b1 = x[4 * j + 3];
+                x[4 * j] = a0 * t.x - a1 * t.y, x[4 * j + 1] = a0 * t.y + a1 * t.x;
+                x[4 * j + 2] = b0 * t.z - b1 * t.w, x[4 * j + 3] = b0 * t.w + b1 * t.z;
+              }
+            }
+            uint32_t w[kN / 4];
+#pragma unroll
+            for (int j = 0; j < kN / 4; ++j) w[j] = pack_e4m3<false>(x[4 * j], x[4 * j + 1]) | pack_e4m3<false>(x[4 * j + 2], x[4 * j + 3]) << 16;
+            if constexpr (kN == 8) *reinterpret_cast<uint2*>(to + row * c.slot_stride) = make_uint2(w[0], w[1]);
+            else *reinterpret_cast<uint32_t*>(to + row * c.slot_stride) = w[0];
+          }
+        }
+      }
+      continue;
     }
-    __syncthreads();
-    settle(t, head);
-    __syncthreads();
-    if (rescale[t]) bring(t, head);
-    if (once) {
-      write(first, t, head);
-    } else {
-      for (int row0 = first; row0 < end; row0 += window) hold(row0), load(row0, head), angles(row0), write(row0, t, head);
+    for (int row0 = chunk; row0 < stop; row0 += kUnder * beside) {
+      load(row0, stop);
+#pragma unroll
+      for (int i = 0; i < kUnder; ++i) {
+        const int row = row0 + i * beside + sub;
+        if (sub >= beside || row >= stop) continue;
+        const int x = run_at(row);
+        if (x == kNoRun) continue;
+        const float by = invs[warp][x];
+        float y[kN];
+        Piece<T>::unpack(u[i], y);
+#pragma unroll
+        for (int j = 0; j < kN; j += 2) {
+          const float2 z = mul(Pair(y[j], y[j + 1]), Pair(by)).both();
+          y[j] = z.x, y[j + 1] = z.y;
+        }
+        if (e / 2 < pairs) {
+          const float2* turn = turns + (row - chunk) * kMaxPairs + e / 2;
+#pragma unroll
+          for (int j = 0; j < kN / 2; ++j)
+            if (e / 2 + j < pairs) {
+              const float2 t = turn[j];
+              const float x0 = y[2 * j], x1 = y[2 * j + 1];
+              y[2 * j] = x0 * t.x - x1 * t.y;
+              y[2 * j + 1] = x0 * t.y + x1 * t.x;
+            }
+        }
+        uint32_t w[kN / 4];
+        if (__builtin_expect(odd, 0)) {
+#pragma unroll
+          for (int j = 0; j < kN / 4; ++j) w[j] = pack_e4m3<true>(y[4 * j], y[4 * j + 1]) | pack_e4m3<true>(y[4 * j + 2], y[4 * j + 3]) << 16;
+        } else {
+#pragma unroll
+          for (int j = 0; j < kN / 4; ++j) w[j] = pack_e4m3<false>(y[4 * j], y[4 * j + 1]) | pack_e4m3<false>(y[4 * j + 2], y[4 * j + 3]) << 16;
+        }
+        uint8_t* to = cache + runs[x].page * c.page_stride + (runs[x].slot + (row - runs[x].begin)) * c.slot_stride;
+        if constexpr (kN == 8) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t*>(to) = w[0];
+      }
     }
   }
 }
 
 // Query rows: a token's sines and cosines once for all of its heads.
 template <typename T>
-__device__ __forceinline__ void turn_queries(const AppendParams& p, const int* stage) {
+__device__ __forceinline__ void turn_queries(const AppendParams& p, const RotaryRates& rates, const int* stage, float2* turns, int block) {
   constexpr int kN = Piece<T>::kN;
-  __shared__ __align__(16) float2 turns[kMaxTokens][kMaxPairs];  // cosine, sine
   __shared__ int positions[kMaxTokens];                          // -1: left out
   const gpt_kv_append_fp8_args& a = p.a;
-  const int tid = threadIdx.x, n0 = (blockIdx.x - p.kv_blocks) * p.tokens, n = min(p.tokens, a.n_tokens - n0);
+  const int tid = threadIdx.x, n0 = block * p.tokens, n = min(p.tokens, a.n_tokens - n0);
   if (tid < n) {
     const Row r = find_row(p, stage, n0 + tid, false);
     positions[tid] = r.seq >= 0 && page_of(p, r, false) >= 0 ? r.pos : -1;
   }
   __syncthreads();
   const int pairs = a.rope_dims / 2;
-  for (int i = tid; i < n * kMaxPairs; i += kThreads)
-    if (i % kMaxPairs < pairs && positions[i / kMaxPairs] >= 0)
-      pair_angle(p.rates, i % kMaxPairs, positions[i / kMaxPairs], &turns[i / kMaxPairs][i % kMaxPairs].x, &turns[i / kMaxPairs][i % kMaxPairs].y);
+  if (pairs > 0)
+    for (int i = tid; i < n * kMaxPairs; i += (int)blockDim.x)
+      if (i % kMaxPairs < pairs && positions[i / kMaxPairs] >= 0)
+        pair_angle(rates, i % kMaxPairs, positions[i / kMaxPairs], &turns[i].x, &turns[i].y);
   __syncthreads();
-  const int pieces = p.c.pages.head_dim / kN, groups = kThreads / pieces, group = tid / pieces, e = tid % pieces * kN;
+  const int pieces = p.c.pages.head_dim / kN, groups = (int)blockDim.x / pieces, group = tid / pieces, e = tid % pieces * kN;
   if (group >= groups) return;
   const T* from = (const T*)a.q + (int64_t)n0 * a.q_row + e;
   T* to = (T*)a.q_out + (int64_t)n0 * a.qo_row + e;
-  const int rows = n * a.n_head;
-  for (int row0 = group; row0 < rows; row0 += kQueryHeld * groups) {
-    uint4 u[kQueryHeld];
-    int token[kQueryHeld], head[kQueryHeld];
+  const bool whole = e + kN <= a.rope_dims;
+  int at = group / a.n_head, h = group % a.n_head;  // token and head, `groups` heads further each time
+  const int next_at = groups / a.n_head, next_h = groups % a.n_head;
+  while (at < n) {
+    uint4 u[kQueryUnder];
+    int token[kQueryUnder], head[kQueryUnder];
 #pragma unroll
-    for (int i = 0; i < kQueryHeld; ++i) {
-      const int row = row0 + i * groups;
-      token[i] = row / a.n_head, head[i] = row % a.n_head;
-      if (row >= rows || positions[token[i]] < 0) token[i] = -1;
-      else u[i] = __ldcs(reinterpret_cast<const uint4*>(from + token[i] * a.q_row + head[i] * a.q_head));
+    for (int i = 0; i < kQueryUnder; ++i) {
+      token[i] = at < n && positions[min(at, kMaxTokens - 1)] >= 0 ? at : -1, head[i] = h;
+      if (token[i] >= 0) u[i] = __ldcs(reinterpret_cast<const uint4*>(from + at * a.q_row + h * a.q_head));
+      at += next_at, h += next_h;
+      if (h >= a.n_head) h -= a.n_head, ++at;
     }
 #pragma unroll
-    for (int i = 0; i < kQueryHeld; ++i) {
+    for (int i = 0; i < kQueryUnder; ++i) {
       if (token[i] < 0) continue;
       if (e < a.rope_dims) {
         float x[kN];
         Piece<T>::unpack(u[i], x);
+        const float4* turn = reinterpret_cast<const float4*>(turns + token[i] * kMaxPairs + e / 2);
 #pragma unroll
-        for (int j = 0; j < kN / 2; ++j)
-          if (e + 2 * j < a.rope_dims) {
-            const float2 t = turns[token[i]][e / 2 + j];
-            const float x0 = x[2 * j], x1 = x[2 * j + 1];
-            x[2 * j] = x0 * t.x - x1 * t.y;
-            x[2 * j + 1] = x0 * t.y + x1 * t.x;
-          }
+        for (int j = 0; j < kN / 4; ++j) {
+          const float4 t = turn[j];
+          const float a0 = x[4 * j], a1 = x[4 * j + 1], b0 = x[4 * j + 2], b1 = x[4 * j + 3];
+          if (whole || e + 4 * j < a.rope_dims) x[4 * j] = a0 * t.x - a1 * t.y, x[4 * j + 1] = a0 * t.y + a1 * t.x;
+          if (whole || e + 4 * j + 2 < a.rope_dims) x[4 * j + 2] = b0 * t.z - b1 * t.w, x[4 * j + 3] = b0 * t.w + b1 * t.z;
+        }
         u[i] = Piece<T>::pack(x);
       }
       *reinterpret_cast<uint4*>(to + token[i] * a.qo_row + head[i] * a.qo_head) = u[i];
@@ -402,17 +463,119 @@ __device__ __forceinline__ void turn_queries(const AppendParams& p, const int* s
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) kv_append_fp8_kernel(const __grid_constant__ AppendParams p) {
-  __shared__ int stage[kStage];
+// What blocks of both kinds begin with.
+__device__ __forceinline__ void begin_block(const AppendParams& p, RotaryRates& rates, int* stage) {
+  // (rates are read by threads' own pairs: from the parameters one after the other)
+  for (int i = threadIdx.x; i < kMaxPairs; i += blockDim.x) rates.hi[i] = p.rates.hi[i], rates.lo[i] = p.rates.lo[i];
   after_stream();
   stage_starts(p, stage);
-  if (blockIdx.x == 0 && p.a.starts)
-    for (int i = threadIdx.x; i < p.c.pages.n_seq; i += kThreads)
-      if (p.a.starts[i] > p.a.starts[i + 1] || p.a.starts[i] < 0 || p.a.starts[i + 1] > p.a.n_tokens) set_status(p.a.status, GPT_STATUS_BAD_SEQ);
   __syncthreads();
-  if (blockIdx.x < p.kv_blocks) append_runs<T>(p, stage);
-  else turn_queries<T>(p, stage);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kMostWarps * 32, 3) kv_append_fp8_kernel(const __grid_constant__ AppendParams p) {
+  extern __shared__ __align__(16) float2 turns[];  // [kMaxStrip][kMaxPairs] cosine, sine; of queries [kMaxTokens][kMaxPairs]
+  __shared__ int stage[kStage];
+  __shared__ RotaryRates rates;
+  begin_block(p, rates, stage);
+  if (blockIdx.x == 0 && p.a.starts)
+    for (int i = threadIdx.x; i < p.c.pages.n_seq; i += blockDim.x)
+      if (p.a.starts[i] > p.a.starts[i + 1] || p.a.starts[i] < 0 || p.a.starts[i + 1] > p.a.n_tokens) set_status(p.a.status, GPT_STATUS_BAD_SEQ);
+  // Blocks of both kinds in even turns: the ones wait for memory while the others compute.
+  const int before = (int)((int64_t)blockIdx.x * p.kv_blocks / gridDim.x), kv = (int)((int64_t)(blockIdx.x + 1) * p.kv_blocks / gridDim.x) - before;
+  if (kv) append_runs<T>(p, rates, stage, turns, before);
+  else turn_queries<T>(p, rates, stage, turns, blockIdx.x - before);
+}
+
+// One new token of each sequence (no starts): every run is a row.  A block has a token, a warp
+// the pieces of as many heads as fit, each element once in registers.
+template <typename T, int kThreads, int kUnroll>
+__global__ void __launch_bounds__(kThreads) kv_append_fp8_step_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int kN = Piece<T>::kN;
+  __shared__ __align__(16) float2 turns[kMaxPairs];  // cosine, sine
+  const gpt_paged_cache& c = p.c.pages;
+  const gpt_kv_append_fp8_args& a = p.a;
+  after_stream();
+  const int tid = threadIdx.x, lane = tid & 31, pieces = c.head_dim / kN, beside = 32 / pieces, sub = lane / pieces;
+  const int group = sub < beside ? (tid >> 5) * beside + sub : 1 << 30, groups = kThreads / 32 * beside, e = lane % pieces * kN;
+  const int64_t n = blockIdx.x;
+  const int rows = a.n_head + 2 * c.n_kv_head;  // q heads, k heads, v heads
+  uint4 u[kUnroll];
+  auto load = [&](int row0) {
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      int row = row0 + i * groups;
+      if (row >= rows) continue;
+      const T* from;
+      if (row < a.n_head) from = (const T*)a.q + n * a.q_row + row * a.q_head;
+      else if ((row -= a.n_head) < c.n_kv_head) from = (const T*)a.k + n * a.k_row + row * a.k_head;
+      else from = (const T*)a.v + n * a.v_row + (row - c.n_kv_head) * a.v_head;
+      u[i] = __ldcs(reinterpret_cast<const uint4*>(from + e));
+    }
+  };
+  const Row r = find_row(p, nullptr, (int)n, tid == 0);
+  load(group);  // under way while the page is looked up
+  if (r.seq < 0) return;
+  const int page = page_of(p, r, tid == 0), slot = r.pos % c.page_size;
+  for (int i = tid; i < kMaxPairs; i += kThreads) {
+    turns[i] = make_float2(1.f, 0.f);
+    if (i < a.rope_dims / 2) pair_angle(p.rates, i, r.pos, &turns[i].x, &turns[i].y);
+  }
+  if (page < 0) return;
+  __syncthreads();
+  const uint32_t same = __match_any_sync(0xffffffffu, sub);
+  const int64_t scale_at = page * p.c.scale_page, at = page * c.page_stride;
+  const int passes = (rows + kUnroll * groups - 1) / (kUnroll * groups);
+  for (int pass = 0, row0 = group; pass < passes; ++pass, row0 += kUnroll * groups) {
+    if (pass > 0) load(row0);
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      int row = row0 + i * groups;
+      const bool there = row < rows, query = row < a.n_head;
+      if (!__any_sync(0xffffffffu, there)) break;
+      bool odd = false;
+      const uint32_t top = __reduce_max_sync(same, there && !query ? largest(u[i], T(), &odd) : 0u);
+      if (!there) continue;
+      float x[kN], by = 1.f;
+      Piece<T>::unpack(u[i], x);
+      const bool key = !query && (row -= a.n_head) < c.n_kv_head, value = !query && !key;
+      if (value) row -= c.n_kv_head;
+      uint8_t* numbers = (uint8_t*)(key ? c.k : c.v) + row * c.head_stride + at;
+      if (!query) {
+        float* scales = (key ? p.c.k_scale : p.c.v_scale) + scale_at + row * p.c.scale_head;
+        float scale = scale_for(__uint_as_float(top));
+        if (slot > 0) {
+          const float old = *scales;
+          __syncwarp(same);
+          scale = fmaxf(scale, old);
+          if (scale != old) bring_numbers(c, numbers, slot, old / scale, lane % pieces, pieces);
+        }
+        if (e == 0) *scales = scale;
+        by = 1.f / scale;
+#pragma unroll
+        for (int j = 0; j < kN; ++j) x[j] *= by;
+      }
+      if (!value && e < a.rope_dims)
+#pragma unroll
+        for (int j = 0; j < kN / 2; ++j)
+          if (e + 2 * j < a.rope_dims) {
+            const float2 t = turns[e / 2 + j];
+            const float x0 = x[2 * j], x1 = x[2 * j + 1];
+            x[2 * j] = x0 * t.x - x1 * t.y;
+            x[2 * j + 1] = x0 * t.y + x1 * t.x;
+          }
+      if (query) {
+        *reinterpret_cast<uint4*>((T*)a.q_out + n * a.qo_row + row * a.qo_head + e) = e < a.rope_dims ? Piece<T>::pack(x) : u[i];
+      } else {
+        uint32_t w[kN / 4];
+#pragma unroll
+        for (int j = 0; j < kN / 4; ++j) w[j] = pack_e4m3<true>(x[4 * j], x[4 * j + 1]) | pack_e4m3<true>(x[4 * j + 2], x[4 * j + 3]) << 16;
+        uint8_t* to = numbers + slot * c.slot_stride + e;
+        if constexpr (kN == 8) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t*>(to) = w[0];
+      }
+    }
+  }
 }
 
 }  // namespace
@@ -457,19 +620,26 @@ extern "C" int gpt_kv_append_fp8(const gpt_fp8_cache* cache, const gpt_kv_append
   p.c = *cache;
   p.a = *a;
   if (a->rope_dims > 0) set_rates(&p.rates, a->rope_base, a->rope_dims);
-  // Rows of a strip: as many as leave two units a block and SM (the window of a block's registers
-  // is 64 rows of 128), 16 at least; then heads of a block.
-  const auto units = [&](int rows) { return ((int64_t)a->n_tokens + rows - 1) / rows * 2 * c->n_kv_head; };
-  p.strip = kMaxStrip;
-  while (p.strip > 16 && units(p.strip) < 608) p.strip /= 2;
-  p.heads = (int32_t)std::max<int64_t>(1, std::min<int64_t>(c->n_kv_head, units(p.strip) / 1216));
-  const int64_t kv_blocks = units(p.strip) / c->n_kv_head * ((c->n_kv_head + p.heads - 1) / p.heads);
+  const cudaStream_t st = (cudaStream_t)cuda_stream;
+  const bool bf16 = c->dtype == GPT_DTYPE_BF16;
+  if (!a->starts) {
+    const bool few = a->n_tokens <= 608;
+    const auto kernel = bf16 ? (few ? kv_append_fp8_step_kernel<__nv_bfloat16, 256, 3> : kv_append_fp8_step_kernel<__nv_bfloat16, 128, 6>)
+                             : (few ? kv_append_fp8_step_kernel<float, 256, 3> : kv_append_fp8_step_kernel<float, 128, 6>);
+    return launch_after("gpt_kv_append_fp8", kernel, dim3((unsigned)a->n_tokens), few ? 256 : 128, 0, 0, st, p);
+  }
+  p.groups = (c->n_kv_head + kMostWarps - 1) / kMostWarps;
+  p.warps = (c->n_kv_head + p.groups - 1) / p.groups;
+  // Rows of a strip: about a page, for as many runs under way as there are.
+  const auto units = [&](int rows) { return ((int64_t)a->n_tokens + rows - 1) / rows * 2 * p.groups; };
+  p.strip = 16;
+  while (p.strip < kMaxStrip && p.strip < c->page_size) p.strip *= 2;
+  const int64_t kv_blocks = units(p.strip);
   p.tokens = std::max(1, std::min(kMaxTokens, a->n_tokens / 1216));
   const int64_t q_blocks = a->n_head > 0 ? ((int64_t)a->n_tokens + p.tokens - 1) / p.tokens : 0;
   if (kv_blocks + q_blocks > INT32_MAX) return call_error(GPT_ERR_UNSUPPORTED, "n_tokens x n_kv_head is too large for one call");
   p.kv_blocks = (int32_t)kv_blocks;
-  const dim3 grid((unsigned)(kv_blocks + q_blocks));
-  const cudaStream_t st = (cudaStream_t)cuda_stream;
-  return launch_after("gpt_kv_append_fp8", c->dtype == GPT_DTYPE_BF16 ? kv_append_fp8_kernel<__nv_bfloat16> : kv_append_fp8_kernel<float>, grid,
-                      kThreads, 0, 0, st, p);
+  const auto kernel = bf16 ? kv_append_fp8_kernel<__nv_bfloat16> : kv_append_fp8_kernel<float>;
+  const int turns = a->rope_dims ? kMaxStrip * kMaxPairs * (int)sizeof(float2) : 0;
+  return launch_after("gpt_kv_append_fp8", kernel, dim3((unsigned)(kv_blocks + q_blocks)), 32 * std::max(p.warps, 4), turns, 0, st, p);
 }

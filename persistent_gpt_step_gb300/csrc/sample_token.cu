@@ -63,34 +63,6 @@ __device__ __forceinline__ u64 composite(float z, int id) {
 }
 __device__ __forceinline__ int id_of(u64 comp) { return (int)~(uint32_t)comp; }
 
-// Two floats in one register pair, for operations on both at once.
-struct Pair {
-  u64 bits;
-  __device__ __forceinline__ Pair() {}
-  __device__ __forceinline__ Pair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(bits) : "f"(a), "f"(b)); }
-  __device__ __forceinline__ explicit Pair(float a) : Pair(a, a) {}
-  __device__ __forceinline__ float2 both() const {
-    float2 x;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x.x), "=f"(x.y) : "l"(bits));
-    return x;
-  }
-};
-__device__ __forceinline__ Pair add(Pair a, Pair b) {
-  Pair d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.bits) : "l"(a.bits), "l"(b.bits));
-  return d;
-}
-__device__ __forceinline__ Pair mul(Pair a, Pair b) {
-  Pair d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.bits) : "l"(a.bits), "l"(b.bits));
-  return d;
-}
-__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
-  Pair d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.bits) : "l"(a.bits), "l"(b.bits), "l"(c.bits));
-  return d;
-}
-
 // 2^U exp((z - m) / T) to 2^-42 of itself and half a unit, in fp32 and integer
 // operations: y = (z - m) c, c = log2 e / T, is kept in two floats (z - m and the product with
 // their rounding errors, from halves of z and m, so that nothing overflows), split into
