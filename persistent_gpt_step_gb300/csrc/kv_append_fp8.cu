@@ -18,8 +18,7 @@ constexpr int kMostWarps = 8;
 constexpr int kMaxStrip = 64;    // rows of a block's strip, and of the table of sines and cosines
 constexpr int kStage = 1024;     // starts in shared memory
 constexpr int kUnder = 8;        // 16-byte pieces that a thread has under way
-constexpr int kQueryUnder = 4;   // the same of queries
-constexpr int kMaxTokens = 8;    // of a block of query rows
+constexpr int kQueryUnder = 8;   // the same of queries
 constexpr int kNoRun = 255;
 
 struct AppendParams {
@@ -407,58 +406,50 @@ __device__ __forceinline__ void append_runs(const AppendParams& p, const RotaryR
   }
 }
 
-// Query rows: a token's sines and cosines once for all of its heads.
+// Query rows: a thread has a piece of every head of a token, for which it computes the sines and
+// cosines once.
 template <typename T>
-__device__ __forceinline__ void turn_queries(const AppendParams& p, const RotaryRates& rates, const int* stage, float2* turns, int block) {
+__device__ __forceinline__ void turn_queries(const AppendParams& p, const RotaryRates& rates, const int* stage, int block) {
   constexpr int kN = Piece<T>::kN;
-  __shared__ int positions[kMaxTokens];                          // -1: left out
   const gpt_kv_append_fp8_args& a = p.a;
-  const int tid = threadIdx.x, n0 = block * p.tokens, n = min(p.tokens, a.n_tokens - n0);
-  if (tid < n) {
-    const Row r = find_row(p, stage, n0 + tid, false);
-    positions[tid] = r.seq >= 0 && page_of(p, r, false) >= 0 ? r.pos : -1;
-  }
-  __syncthreads();
-  const int pairs = a.rope_dims / 2;
-  if (pairs > 0)
-    for (int i = tid; i < n * kMaxPairs; i += (int)blockDim.x)
-      if (i % kMaxPairs < pairs && positions[i / kMaxPairs] >= 0)
-        pair_angle(rates, i % kMaxPairs, positions[i / kMaxPairs], &turns[i].x, &turns[i].y);
-  __syncthreads();
-  const int pieces = p.c.pages.head_dim / kN, groups = (int)blockDim.x / pieces, group = tid / pieces, e = tid % pieces * kN;
-  if (group >= groups) return;
-  const T* from = (const T*)a.q + (int64_t)n0 * a.q_row + e;
-  T* to = (T*)a.q_out + (int64_t)n0 * a.qo_row + e;
-  const bool whole = e + kN <= a.rope_dims;
-  int at = group / a.n_head, h = group % a.n_head;  // token and head, `groups` heads further each time
-  const int next_at = groups / a.n_head, next_h = groups % a.n_head;
-  while (at < n) {
-    uint4 u[kQueryUnder];
-    int token[kQueryUnder], head[kQueryUnder];
+  const int pieces = p.c.pages.head_dim / kN, group = threadIdx.x / pieces, e = threadIdx.x % pieces * kN;
+  const int64_t n = (int64_t)block * p.tokens + group;
+  if (group >= p.tokens || n >= a.n_tokens) return;
+  const T* from = (const T*)a.q + n * a.q_row + e;
+  T* to = (T*)a.q_out + n * a.qo_row + e;
+  uint4 u[kQueryUnder];
+  auto load = [&](int head) {
+#pragma unroll
+    for (int i = 0; i < kQueryUnder; ++i)
+      if (head + i < a.n_head) u[i] = __ldcs(reinterpret_cast<const uint4*>(from + (head + i) * a.q_head));
+  };
+  load(0);  // under way while the row is looked up
+  const Row r = find_row(p, stage, (int)n, false);
+  if (r.seq < 0 || page_of(p, r, false) < 0) return;
+  float2 turn[kN / 2];
+#pragma unroll
+  for (int j = 0; j < kN / 2; ++j)
+    if (e + 2 * j < a.rope_dims) pair_angle(rates, e / 2 + j, r.pos, &turn[j].x, &turn[j].y);
+  const bool all = e + kN <= a.rope_dims;
+#pragma unroll 1
+  for (int head = 0; head < a.n_head; head += kQueryUnder) {
+    if (head > 0) load(head);
 #pragma unroll
     for (int i = 0; i < kQueryUnder; ++i) {
-      token[i] = at < n && positions[min(at, kMaxTokens - 1)] >= 0 ? at : -1, head[i] = h;
-      if (token[i] >= 0) u[i] = __ldcs(reinterpret_cast<const uint4*>(from + at * a.q_row + h * a.q_head));
-      at += next_at, h += next_h;
-      if (h >= a.n_head) h -= a.n_head, ++at;
-    }
-#pragma unroll
-    for (int i = 0; i < kQueryUnder; ++i) {
-      if (token[i] < 0) continue;
+      if (head + i >= a.n_head) break;
       if (e < a.rope_dims) {
         float x[kN];
         Piece<T>::unpack(u[i], x);
-        const float4* turn = reinterpret_cast<const float4*>(turns + token[i] * kMaxPairs + e / 2);
 #pragma unroll
-        for (int j = 0; j < kN / 4; ++j) {
-          const float4 t = turn[j];
-          const float a0 = x[4 * j], a1 = x[4 * j + 1], b0 = x[4 * j + 2], b1 = x[4 * j + 3];
-          if (whole || e + 4 * j < a.rope_dims) x[4 * j] = a0 * t.x - a1 * t.y, x[4 * j + 1] = a0 * t.y + a1 * t.x;
-          if (whole || e + 4 * j + 2 < a.rope_dims) x[4 * j + 2] = b0 * t.z - b1 * t.w, x[4 * j + 3] = b0 * t.w + b1 * t.z;
-        }
+        for (int j = 0; j < kN / 2; ++j)
+          if (all || e + 2 * j < a.rope_dims) {
+            const float x0 = x[2 * j], x1 = x[2 * j + 1];
+            x[2 * j] = x0 * turn[j].x - x1 * turn[j].y;
+            x[2 * j + 1] = x0 * turn[j].y + x1 * turn[j].x;
+          }
         u[i] = Piece<T>::pack(x);
       }
-      *reinterpret_cast<uint4*>(to + token[i] * a.qo_row + head[i] * a.qo_head) = u[i];
+      *reinterpret_cast<uint4*>(to + (head + i) * a.qo_head) = u[i];
     }
   }
 }
@@ -474,7 +465,7 @@ __device__ __forceinline__ void begin_block(const AppendParams& p, RotaryRates& 
 
 template <typename T>
 __global__ void __launch_bounds__(kMostWarps * 32, 3) kv_append_fp8_kernel(const __grid_constant__ AppendParams p) {
-  extern __shared__ __align__(16) float2 turns[];  // [kMaxStrip][kMaxPairs] cosine, sine; of queries [kMaxTokens][kMaxPairs]
+  extern __shared__ __align__(16) float2 turns[];  // [kMaxStrip][kMaxPairs] cosine, sine
   __shared__ int stage[kStage];
   __shared__ RotaryRates rates;
   begin_block(p, rates, stage);
@@ -484,7 +475,7 @@ __global__ void __launch_bounds__(kMostWarps * 32, 3) kv_append_fp8_kernel(const
   // Blocks of both kinds in even turns: the ones wait for memory while the others compute.
   const int before = (int)((int64_t)blockIdx.x * p.kv_blocks / gridDim.x), kv = (int)((int64_t)(blockIdx.x + 1) * p.kv_blocks / gridDim.x) - before;
   if (kv) append_runs<T>(p, rates, stage, turns, before);
-  else turn_queries<T>(p, rates, stage, turns, blockIdx.x - before);
+  else turn_queries<T>(p, rates, stage, blockIdx.x - before);
 }
 
 // One new token of each sequence (no starts): every run is a row.  A block has a token, a warp
@@ -635,11 +626,12 @@ extern "C" int gpt_kv_append_fp8(const gpt_fp8_cache* cache, const gpt_kv_append
   p.strip = 16;
   while (p.strip < kMaxStrip && p.strip < c->page_size) p.strip *= 2;
   const int64_t kv_blocks = units(p.strip);
-  p.tokens = std::max(1, std::min(kMaxTokens, a->n_tokens / 1216));
+  const int threads = 32 * std::max(p.warps, 4);
+  p.tokens = threads / (c->head_dim * es / 16);
   const int64_t q_blocks = a->n_head > 0 ? ((int64_t)a->n_tokens + p.tokens - 1) / p.tokens : 0;
   if (kv_blocks + q_blocks > INT32_MAX) return call_error(GPT_ERR_UNSUPPORTED, "n_tokens x n_kv_head is too large for one call");
   p.kv_blocks = (int32_t)kv_blocks;
   const auto kernel = bf16 ? kv_append_fp8_kernel<__nv_bfloat16> : kv_append_fp8_kernel<float>;
   const int turns = a->rope_dims ? kMaxStrip * kMaxPairs * (int)sizeof(float2) : 0;
-  return launch_after("gpt_kv_append_fp8", kernel, dim3((unsigned)(kv_blocks + q_blocks)), 32 * std::max(p.warps, 4), turns, 0, st, p);
+  return launch_after("gpt_kv_append_fp8", kernel, dim3((unsigned)(kv_blocks + q_blocks)), threads, turns, 0, st, p);
 }
