@@ -621,10 +621,12 @@ extern "C" int gpt_kv_append_fp8(const gpt_fp8_cache* cache, const gpt_kv_append
   }
   p.groups = (c->n_kv_head + kMostWarps - 1) / kMostWarps;
   p.warps = (c->n_kv_head + p.groups - 1) / p.groups;
-  // Rows of a strip: about a page, for as many runs under way as there are.
+  // Rows of a strip: about a page, 32 at least, where there are blocks enough (8,192 tokens of 16
+  // heads of 64 in pages of 16: 33.5 us, in strips of 16 38.6, of 64 36.4; 2,000 of 8 heads of 128
+  // in pages of 128: 30.4 in strips of 16, 37.7 of 64).
   const auto units = [&](int rows) { return ((int64_t)a->n_tokens + rows - 1) / rows * 2 * p.groups; };
   p.strip = 16;
-  while (p.strip < kMaxStrip && p.strip < c->page_size) p.strip *= 2;
+  while (p.strip < std::min(kMaxStrip, std::max(32, c->page_size)) && units(2 * p.strip) >= 304) p.strip *= 2;
   const int64_t kv_blocks = units(p.strip);
   const int threads = 32 * std::max(p.warps, 4);
   p.tokens = threads / (c->head_dim * es / 16);
