@@ -53,11 +53,11 @@ __device__ __forceinline__ uint2 load8(const void* p) {
 
 // As Walk, with the scales of each group's (or key's) page: table entries are read two
 // rounds ahead, the scales one.
-template <bool kFast>
+template <bool kFast, int kKeys>
 struct ScaledWalk {
   using Off = std::conditional_t<kFast, uint32_t, int64_t>;
   static constexpr Off kNoKey = (Off)-1;
-  static constexpr int kRound = kFast ? 256 : 32;  // keys
+  static constexpr int kRound = kFast ? 256 : kKeys;  // keys
   const DecodeParams& p;
   const int32_t* table;
   const float *ks_at, *vs_at;  // of the head
@@ -70,7 +70,7 @@ struct ScaledWalk {
         end(k1), lane_at(0) {
     const int lane = threadIdx.x & 31;
     head = kFast ? h * p.head16 : h * p.c.head_stride;
-    at1 = k0 + (kFast ? lane * 8 : lane);
+    at1 = k0 + (kFast ? lane * 8 : lane & (kKeys - 1));
     page1 = fetch(at1);
     scales();
     page2 = fetch(at1 + kRound);
@@ -112,7 +112,7 @@ struct Fp8Path {
   static constexpr bool kTwice = kFull && kMode == 4;
   static constexpr int kParts = kFull && !kTwice ? 2 : 1;  // products for a tile
   static constexpr int kBlocks = kMode == 16 ? 1 : 2;      // of an SM
-  static constexpr int KG = 2, kKeys = 16 * KG, kUnit = kKeys, kUnitStart = kStart;
+  static constexpr int KG = DP_ == 128 ? 1 : 2, kKeys = 16 * KG, kUnit = kKeys, kUnitStart = kStart;
   static constexpr int KP = DP / 64;                       // a lane's 16-byte pieces of a key
   static constexpr int VW = DP / 32;                       // a lane's words of a value
   static constexpr int kQuery = NT * kParts * KP * 256;    // a warp's queries: 32 bytes per lane, tile, part and piece
@@ -188,7 +188,7 @@ struct Fp8Path {
     }
     uint4 kr[KG][2][KP];
     uint32_t vr[KG][4][VW];
-    using Keys = ScaledWalk<kFast>;
+    using Keys = ScaledWalk<kFast, kKeys>;
     Keys walk(p, w.s, w.h, k0, k1);
     // Of the step's groups of 8: offsets, scales.  Without kFast: off[0][0] of the lane's key,
     // the scales of key g * 16 + u * 8 + r.
