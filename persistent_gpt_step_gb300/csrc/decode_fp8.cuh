@@ -7,11 +7,9 @@
 //    memory; the key scale of a page multiplies the score.  A query is brought below 2^15 by
 //    a power of two of its own (what falls under 2^-25 there is 2^-39 of its largest): bf16
 //    queries are then exact, fp32 ones enter as two fp16 parts (2^-23).
-//  - values: the weights enter as fp16 numbers below 2^15 (their reference lies 7 under the
-//    maximum, so that what falls under fp16's smallest number is 2^-32 of the largest), for
-//    fp32 results as two parts.  A product of 16 keys is summed apart and joined to the row's
-//    sums with the value scale of its page; where its keys have two scales, the smaller one's
-//    weights are brought to the larger.
+//  - values: the weights, times the value scale of their page over the largest one so far,
+//    enter as fp16 numbers below 2^15 (their reference lies 7 under the maximum, so that what
+//    falls under fp16's smallest number is 2^-32 of the largest), for fp32 results as two parts.
 // Bound: HBM, half the bytes of a bf16 cache; the conversions (a number of a key and a value
 // each, two at a time) are the pipe that is busiest beside it.
 #pragma once
@@ -186,6 +184,7 @@ struct Fp8Path {
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[t][b][i / 4][i % 4] = 0.f;
     }
+    float unit = 0x1p-126f, unit_inv = 0x1p126f;  // of the values' sums
     uint4 kr[KG][2][KP];
     uint32_t vr[KG][4][VW];
     using Keys = ScaledWalk<kFast, kKeys>;
@@ -265,18 +264,26 @@ struct Fp8Path {
       } else {
         there = __ballot_sync(0xffffffffu, off[0][0] >= 0);
       }
-      // the step's scales: of the scores; of a product of 16 keys, and what brings weights to it
-      float key_scale[KG][2], value_scale[KG], bring[KG][2];
+      // the step's scales: of the scores; what brings weights to the sums' unit, which is the largest so far
+      float key_scale[KG][2], bring[KG][2];
+      float top = 0.f;
 #pragma unroll
-      for (int g = 0; g < KG; ++g) {
-        key_scale[g][0] = ks[g][0], key_scale[g][1] = ks[g][1];
-        float top = fmaxf(vs[g][0], vs[g][1]);
-        if constexpr (!kFast)
+      for (int g = 0; g < KG; ++g) key_scale[g][0] = ks[g][0], key_scale[g][1] = ks[g][1], top = fmaxf(top, fmaxf(vs[g][0], vs[g][1]));
+      if constexpr (!kFast)
 #pragma unroll
-          for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        value_scale[g] = top;
-        bring[g][0] = vs[g][0] == top ? 1.f : vs[g][0] / top, bring[g][1] = vs[g][1] == top ? 1.f : vs[g][1] / top;
+        for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      if (top > unit) {
+        const float keep = unit / top;
+        unit = top, unit_inv = 1.f / top;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int b = 0; b < VW; ++b)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[t][b][i / 4][i % 4] *= keep;
       }
+#pragma unroll
+      for (int g = 0; g < KG; ++g) bring[g][0] = vs[g][0] * unit_inv, bring[g][1] = vs[g][1] * unit_inv;
       advance();
       // scores: 16 keys x 8 columns a tile
       float z[KG][NT][4];
@@ -386,11 +393,8 @@ struct Fp8Path {
             to_f16(__byte_perm(vr[g][2][b], vr[g][3][b], i ? 0x7362 : 0x5140), a2, a3);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-              float x[4] = {0.f, 0.f, 0.f, 0.f};
-              mma16816_f16(x, a0, a1, a2, a3, h0[t], h1[t]);
-              if (kParts == 2) mma16816_f16(x, a0, a1, a2, a3, l0[t], l1[t]);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) o[t][b][i][j] = fmaf(value_scale[g], x[j], o[t][b][i][j]);
+              mma16816_f16(o[t][b][i], a0, a1, a2, a3, h0[t], h1[t]);
+              if (kParts == 2) mma16816_f16(o[t][b][i], a0, a1, a2, a3, l0[t], l1[t]);
             }
           }
       }
@@ -410,6 +414,7 @@ struct Fp8Path {
           for (int i = 0; i < 4; ++i) {
             y[b][i] = o[t][b][i >> 1][e + 2 * (i & 1)];
             if (kTwice) y[b][i] += __shfl_xor_sync(0xffffffffu, y[b][i], 2);
+            y[b][i] *= unit;
           }
         if (qh >= w.n) continue;
         if (w.left) {
