@@ -84,8 +84,10 @@ struct ScaledWalk {
     ks1 = vs1 = 0.f;
     if (page1 >= 0) ks1 = __ldg(ks_at + page1 * p.scale_page), vs1 = __ldg(vs_at + page1 * p.scale_page);
   }
+  // kFast: the offset of the lane's group of the next round.
+  __device__ __forceinline__ Off next() const { return page1 < 0 ? kNoKey : page1 * p.page16 + (at1 % p.c.page_size) * p.slot16 + head; }
   __device__ __forceinline__ void turn() {
-    if constexpr (kFast) off = page1 < 0 ? kNoKey : page1 * p.page16 + (at1 % p.c.page_size) * p.slot16 + head;
+    if constexpr (kFast) off = next();
     else off = page1 < 0 ? kNoKey : page1 * p.c.page_stride + (at1 % p.c.page_size) * p.c.slot_stride + head;
     ks = ks1, vs = vs1;
     at1 += kRound, page1 = page2;
@@ -118,11 +120,12 @@ struct Fp8Path {
   // Dims of a lane's piece i of a key or query; those of its part of a value begin at r * 4 VW.
   static __device__ __forceinline__ int piece_dim(int i, int c) { return c * 16 * KP + i * 16; }
 
-  // Lane (r, c): query head r of a tile, its pieces, in fp16.  Returns 2^e of the head, by which
-  // its scores are to be multiplied.
-  static __device__ __forceinline__ float stage_query(const DecodeParams& p, uint4* query, const Part& w, int t) {
+  // Lane (r, c): query head r of a tile, its pieces, in fp16, eight words for each; put(part, piece,
+  // half, four words).  Returns 2^e of the head, by which its scores are to be multiplied.
+  template <typename Put>
+  static __device__ __forceinline__ float read_query(const DecodeParams& p, const Part& w, int t, Put put) {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const int qh = kTwice ? r & 3 : t * 8 + r;
+    const int qh = kTwice || kMode == 4 ? r & 3 : t * 8 + r;
     constexpr int kN = Piece<T>::kN, kLoads = 16 / kN;
     uint4 u[KP][kLoads];
 #pragma unroll
@@ -161,10 +164,42 @@ struct Fp8Path {
           if (kFull) l[k] = rest2_f16(x[2 * k], x[2 * k + 1], h[k]);
           if (kTwice && r >= 4) h[k] = l[k];
         }
-        query[((t * kParts * KP + i) * 2 + half) * 32] = make_uint4(h[0], h[1], h[2], h[3]);
-        if (kParts == 2) query[(((t * kParts + 1) * KP + i) * 2 + half) * 32] = make_uint4(l[0], l[1], l[2], l[3]);
+        put(0, i, half, make_uint4(h[0], h[1], h[2], h[3]));
+        if (kParts == 2) put(1, i, half, make_uint4(l[0], l[1], l[2], l[3]));
       }
     return __uint_as_float((uint32_t)(e + 127) << 23);
+  }
+  static __device__ __forceinline__ float stage_query(const DecodeParams& p, uint4* query, const Part& w, int t) {
+    return read_query(p, w, t, [&](int part, int i, int half, uint4 x) { query[(((t * kParts + part) * KP + i) * 2 + half) * 32] = x; });
+  }
+  template <int N>
+  static __device__ __forceinline__ float query_registers(const DecodeParams& p, uint32_t (&q)[N][8], const Part& w) {
+    return read_query(p, w, 0, [&](int, int i, int half, uint4 x) {
+      q[i][4 * half] = x.x, q[i][4 * half + 1] = x.y, q[i][4 * half + 2] = x.z, q[i][4 * half + 3] = x.w;
+    });
+  }
+
+  // What lane (r, c) has of query head qh: reference, sum of weights, its dims of their values' sum.
+  static __device__ __forceinline__ void finish(const DecodeParams& p, const Part& w, int qh, float m, float total, float (&y)[VW][4]) {
+    const int r = (threadIdx.x & 31) >> 2;
+    if (qh >= w.n) return;
+    if (w.left) {
+      if (r == 0) w.left[2 * qh] = m, w.left[2 * qh + 1] = total;
+      float* to = w.left + left_o(kHeads) + qh * DP + r * 4 * VW;
+#pragma unroll
+      for (int b = 0; b < VW; ++b) store4(to + 4 * b, y[b]);
+    } else {
+      const float inv = total == 0.f ? 0.f : 1.0f / total;
+      T* to = (T*)p.a.out + w.s * p.a.out_row + (w.hq + qh) * p.a.out_head + r * 4 * VW;
+#pragma unroll
+      for (int b = 0; b < VW; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[b][i] *= inv;
+      if (kExact || r * 4 * VW < p.c.head_dim)
+#pragma unroll
+        for (int b = 0; b < VW; ++b) store4(to + 4 * b, y[b]);
+      if (r == 0) store_lse(p, w.s, w.hq + qh, m, total);
+    }
   }
 
   static __device__ __forceinline__ void run(const DecodeParams& p, float* mine, const Part& w) {
@@ -416,32 +451,263 @@ struct Fp8Path {
             if (kTwice) y[b][i] += __shfl_xor_sync(0xffffffffu, y[b][i], 2);
             y[b][i] *= unit;
           }
-        if (qh >= w.n) continue;
-        if (w.left) {
-          if (r == 0) w.left[2 * qh] = m[t][e], w.left[2 * qh + 1] = total;
-          float* to = w.left + left_o(kHeads) + qh * DP + r * 4 * VW;
+        finish(p, w, qh, m[t][e], total, y);
+      }
+  }
+};
+
+// Up to 4 query heads, pages of whole 8-key groups: the same through shared memory.  The
+// registers of a step's keys and values are all that a warp has under way above, and it waits
+// for memory most of its time (long_scoreboard 6.2 of 10.6 clocks an instruction).  Here the next
+// step's are on their way into a ring of two stages while a step is at work, and the one's after it
+// as soon as its own are in registers: 8 KB a warp.  A stage's 16-byte pieces lie so that
+// neighbouring rows' are in other banks.  The queries stay in registers.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ uint4 shared16(uint32_t at) {
+  uint4 u;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(at));
+  return u;
+}
+__device__ __forceinline__ uint2 shared8(uint32_t at) {
+  uint2 u;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(u.x), "=r"(u.y) : "r"(at));
+  return u;
+}
+
+template <typename T_, int DP_, bool kExact>
+struct Fp8Ring {
+  using T = T_;
+  using Cache = E4m3;
+  using Path = Fp8Path<T, 4, DP_, true, kExact>;
+  static constexpr bool kFull = std::is_same_v<T, float>, kTwice = kFull;
+  static constexpr int DP = DP_, kHeads = 4, kBlocks = 2;
+  static constexpr int KP = Path::KP, VW = Path::VW, KG = Path::KG, kKeys = Path::kKeys, kUnit = kKeys, kUnitStart = kStart;
+  static constexpr int kStages = 2, kSide = kKeys * DP;  // bytes of a stage's keys
+  static constexpr int kQuery = kStages * 2 * kSide / 4;
+
+  static __device__ __forceinline__ void run(const DecodeParams& p, float* mine, const Part& w) {
+    const int k0 = w.k0, k1 = w.k1;
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const int d = p.c.head_dim;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(mine);
+    __syncwarp();  // the last part's reads of it
+    if (!kExact)
+      for (int i = lane; i < kQuery / 4; i += 32) reinterpret_cast<uint4*>(mine)[i] = make_uint4(0u, 0u, 0u, 0u);  // dims from d on
+    // A lane's pieces: copies (row and 16 bytes of it), operands of the products.
+    constexpr int kPer = DP / 16;                                // pieces of a row
+    const int row = lane / kPer, piece = lane % kPer;            // of the first copy; the others are 32 / kPer rows further
+    const uint32_t to = DP == 128 ? row * 128 + (piece ^ row) * 16
+                                  : (row >> 1) * 128 + (((row & 1) * 4 + piece) ^ (((row >> 1) & 3) * 2)) * 16;
+    const bool copies = kExact || piece * 16 < d;
+    const int64_t from = (int64_t)row * p.c.slot_stride + piece * 16;
+    const uint32_t key0 = DP == 128 ? r * 128 + ((2 * c) ^ r) * 16 : (r >> 1) * 128 + (((r & 1) * 4 + c) ^ (((r >> 1) & 3) * 2)) * 16;
+    const uint32_t key1 = r * 128 + ((2 * c + 1) ^ r) * 16;      // DP 128: the second 16 of its 32 dims
+    const uint32_t val0 = DP == 128 ? 2 * c * 128 + (r ^ (2 * c)) * 16 : c * 128 + ((r >> 1) ^ (c * 2)) * 16 + (r & 1) * 8;
+    const uint32_t val1 = DP == 128 ? (2 * c + 1) * 128 + (r ^ (2 * c + 1)) * 16 : c * 128 + ((4 + (r >> 1)) ^ (c * 2)) * 16 + (r & 1) * 8;
+
+    float o[VW][2][4], m[2], l[2], factor[2];
+    m[0] = m[1] = -INFINITY, l[0] = l[1] = 0.f;
 #pragma unroll
-          for (int b = 0; b < VW; ++b) store4(to + 4 * b, y[b]);
-        } else {
-          const float inv = total == 0.f ? 0.f : 1.0f / total;
-          T* to = (T*)p.a.out + w.s * p.a.out_row + (w.hq + qh) * p.a.out_head + r * 4 * VW;
+    for (int b = 0; b < VW; ++b)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[b][i / 4][i % 4] = 0.f;
+    float unit = 0x1p-126f, unit_inv = 0x1p126f;  // of the values' sums
+    using Keys = ScaledWalk<true, kKeys>;
+    Keys walk(p, w.s, w.h, k0, k1);
+    walk.turn();
+    __syncwarp();
+    // Copies of the step whose first group is the lane_at + ahead-th of the walk's round.
+    auto copy = [&](int ahead, int stage) {
+#pragma unroll
+      for (int g = 0; g < 2 * KG; ++g) {
+        const int j = walk.lane_at + ahead + g;
+        uint32_t off;
+        if (j < 32) off = __shfl_sync(0xffffffffu, walk.off, j);
+        else off = __shfl_sync(0xffffffffu, walk.next(), j - 32);
+        if (off == Keys::kNoKey || !copies) continue;
+        constexpr int kCopies = DP / 64;  // of a group of 8 rows
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+          const int64_t at = (int64_t)((unsigned long long)off * 16) + from + i * (8 / kCopies) * p.c.slot_stride;
+          // (4 rows on the pieces' places change by 4 of 8)
+          const uint32_t there = ring + stage * 2 * kSide + g * 8 * DP + (i ? (to ^ 64) + 4 * 128 : to);
+          copy16(there, (const uint8_t*)p.c.k + at);
+          copy16(there + kSide, (const uint8_t*)p.c.v + at);
+        }
+      }
+    };
+    auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+    copy(0, 0), commit();
+    if (k0 + kKeys < k1) copy(2 * KG, 1);
+    commit();
+    // queries
+    uint32_t q[KP][8];
+    {
+      const float up = Path::template query_registers<KP>(p, q, w);
+      factor[0] = __shfl_sync(0xffffffffu, up, 8 * c);
+      factor[1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
+    }
+    int stage = 0;
+    for (int k = k0; k < k1; k += kKeys, stage ^= 1) {
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncwarp();
+      uint4 kr[KG][2][KP];
+      uint32_t vr[KG][4][VW];
+      const uint32_t keys = ring + stage * 2 * kSide, values = keys + kSide;
+#pragma unroll
+      for (int g = 0; g < KG; ++g)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t at = (g * 16 + u * 8) * DP;
+          kr[g][u][0] = shared16(keys + at + key0);
+          if (KP == 2) kr[g][u][KP - 1] = shared16(keys + at + key1);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if constexpr (VW == 4) {
+              const uint4 v = shared16(values + at + (x ? val1 : val0));
+              vr[g][2 * u + x][0] = v.x, vr[g][2 * u + x][1] = v.y, vr[g][2 * u + x][2] = v.z, vr[g][2 * u + x][3] = v.w;
+            } else {
+              const uint2 v = shared8(values + at + (x ? val1 : val0));
+              vr[g][2 * u + x][0] = v.x, vr[g][2 * u + x][1] = v.y;
+            }
+          }
+        }
+      // the step's groups
+      uint32_t there = 0xffffffffu;  // keys that count
+      float ks[KG][2], vs[KG][2];
+      __syncwarp();
+      if (k + 2 * kKeys < k1) copy(4 * KG, stage);
+      commit();
+      float top = 0.f;
+#pragma unroll
+      for (int g = 0; g < KG; ++g)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint32_t off;
+          walk.group(off, ks[g][u], vs[g][u]);
+          if (off == Keys::kNoKey) there &= ~(0xffu << (g * 16 + u * 8));
+          top = fmaxf(top, vs[g][u]);
+        }
+      if (k1 - k < kKeys) there &= (1u << (k1 - k)) - 1u;
+      if (top > unit) {
+        const float keep = unit / top;
+        unit = top, unit_inv = 1.f / top;
+#pragma unroll
+        for (int b = 0; b < VW; ++b)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[b][i / 4][i % 4] *= keep;
+      }
+      // scores
+      float z[KG][4];
+#pragma unroll
+      for (int g = 0; g < KG; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[g][i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < KP; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int g = 0; g < KG; ++g) {
+            uint32_t a0, a1, a2, a3;
+            to_f16((&kr[g][0][i].x)[j], a0, a2);
+            to_f16((&kr[g][1][i].x)[j], a1, a3);
+            mma16816_f16(z[g], a0, a1, a2, a3, q[i][2 * j], q[i][2 * j + 1]);
+          }
+#pragma unroll
+      for (int g = 0; g < KG; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (kTwice) z[g][i] += __shfl_xor_sync(0xffffffffu, z[g][i], 2);
+          z[g][i] *= factor[i & 1] * ks[g][i >> 1] * p.scale2;
+        }
+      if (__builtin_expect(there != 0xffffffffu, 0)) {
+#pragma unroll
+        for (int g = 0; g < KG; ++g) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!((there >> (g * 16 + (i >> 1) * 8 + r)) & 1u)) z[g][i] = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < 4; ++u)  // what such a slot holds may be NaN
+            if (!((there >> (g * 16 + (u >> 1) * 8 + 2 * c + (u & 1))) & 1u))
+#pragma unroll
+              for (int b = 0; b < VW; ++b) vr[g][u][b] = 0u;
+        }
+      }
+      // softmax: the reference of a head moves only when a score passes the maximum by 2^8
+      bool move = false;
+#pragma unroll
+      for (int g = 0; g < KG; ++g) move |= fmaxf(z[g][0], z[g][2]) > m[0] + 15.f || fmaxf(z[g][1], z[g][3]) > m[1] + 15.f;
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float best = m[e] + 7.f;
+#pragma unroll
+          for (int g = 0; g < KG; ++g) best = fmaxf(best, fmaxf(z[g][e], z[g][e + 2]));
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, x));
+          best -= 7.f;
+          const float keep = weight(m[e], best);
+          m[e] = best;
+          l[e] *= keep;
 #pragma unroll
           for (int b = 0; b < VW; ++b)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[b][i] *= inv;
-          if (kExact || r * 4 * VW < d)
-#pragma unroll
-            for (int b = 0; b < VW; ++b) store4(to + 4 * b, y[b]);
-          if (r == 0) store_lse(p, w.s, w.hq + qh, m[t][e], total);
+            for (int i = 0; i < 2; ++i) o[b][i][e] *= keep, o[b][i][e + 2] *= keep;
         }
       }
+#pragma unroll
+      for (int g = 0; g < KG; ++g) {
+        const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
+        float p0 = exp2_fast(z[g][0] - m0), p1 = exp2_fast(z[g][1] - m1);
+        float p2 = exp2_fast(z[g][2] - m0), p3 = exp2_fast(z[g][3] - m1);
+        l[0] += p0 + p2, l[1] += p1 + p3;
+        const float b0 = vs[g][0] * unit_inv, b1 = vs[g][1] * unit_inv;
+        p0 *= b0, p1 *= b0, p2 *= b1, p3 *= b1;
+        uint32_t ha = pack2_f16(p0, p1), hb = pack2_f16(p2, p3);
+        if (kTwice) {
+          const uint32_t la = rest2_f16(p0, p1, ha), lb = rest2_f16(p2, p3, hb);
+          ha = c < 2 ? ha : la, hb = c < 2 ? hb : lb;
+        }
+        const uint32_t h0 = transpose8(ha), h1 = transpose8(hb);
+#pragma unroll
+        for (int b = 0; b < VW; ++b)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t a0, a1, a2, a3;
+            to_f16(__byte_perm(vr[g][0][b], vr[g][1][b], i ? 0x7362 : 0x5140), a0, a1);
+            to_f16(__byte_perm(vr[g][2][b], vr[g][3][b], i ? 0x7362 : 0x5140), a2, a3);
+            mma16816_f16(o[b][i], a0, a1, a2, a3, h0, h1);
+          }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int qh = 2 * c + e;
+      float total = l[e];
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
+      float y[VW][4];
+#pragma unroll
+      for (int b = 0; b < VW; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          y[b][i] = o[b][i >> 1][e + 2 * (i & 1)];
+          if (kTwice) y[b][i] += __shfl_xor_sync(0xffffffffu, y[b][i], 2);
+          y[b][i] *= unit;
+        }
+      Path::finish(p, w, qh, m[e], total, y);
+    }
   }
 };
 
 template <typename T, int N, int DP>
 int launch_fp8(const DecodeParams& p, const Plan& pl, cudaStream_t st) {
   if (!pl.fast) return launch<Fp8Path<T, N, DP, false, false>>(p, pl, st);
-  return pl.exact ? launch<Fp8Path<T, N, DP, true, true>>(p, pl, st) : launch<Fp8Path<T, N, DP, true, false>>(p, pl, st);
+  if constexpr (N == 4) return p.c.head_dim == DP ? launch<Fp8Ring<T, DP, true>>(p, pl, st) : launch<Fp8Ring<T, DP, false>>(p, pl, st);
+  else return pl.exact ? launch<Fp8Path<T, N, DP, true, true>>(p, pl, st) : launch<Fp8Path<T, N, DP, true, false>>(p, pl, st);
 }
 
 }  // namespace

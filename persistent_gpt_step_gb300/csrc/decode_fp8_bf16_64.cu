@@ -2,5 +2,6 @@
 #include "decode_fp8.cuh"
 
 int pgs::decode_fp8_bf16_64(const DecodeParams& p, const Plan& pl, cudaStream_t st) {
+  if (pl.chunk <= 4) return launch_fp8<__nv_bfloat16, 4, 64>(p, pl, st);
   return pl.chunk <= 8 ? launch_fp8<__nv_bfloat16, 8, 64>(p, pl, st) : launch_fp8<__nv_bfloat16, 16, 64>(p, pl, st);
 }
