@@ -476,7 +476,8 @@ __device__ __forceinline__ uint2 shared8(uint32_t at) {
   return u;
 }
 
-template <typename T_, int DP_, bool kExact>
+// kSame: pages of whole 16-key groups, one scale for each of these.
+template <typename T_, int DP_, bool kExact, bool kSame>
 struct Fp8Ring {
   using T = T_;
   using Cache = E4m3;
@@ -484,11 +485,12 @@ struct Fp8Ring {
   static constexpr bool kFull = std::is_same_v<T, float>, kTwice = kFull;
   static constexpr int DP = DP_, kHeads = 4, kBlocks = 2;
   static constexpr int KP = Path::KP, VW = Path::VW, KG = Path::KG, kKeys = Path::kKeys, kUnit = kKeys, kUnitStart = kStart;
-  static constexpr int kStages = 2, kSide = kKeys * DP;  // bytes of a stage's keys
+  static constexpr int kGroups = 2 * KG;                    // groups of 8 keys of a step
+  static constexpr int kStages = 2, kSide = kKeys * DP;     // bytes of a stage's keys
   static constexpr int kQuery = kStages * 2 * kSide / 4;
 
   static __device__ __forceinline__ void run(const DecodeParams& p, float* mine, const Part& w) {
-    const int k0 = w.k0, k1 = w.k1;
+    const int k1 = w.k1;
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const int d = p.c.head_dim;
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(mine);
@@ -497,50 +499,57 @@ struct Fp8Ring {
       for (int i = lane; i < kQuery / 4; i += 32) reinterpret_cast<uint4*>(mine)[i] = make_uint4(0u, 0u, 0u, 0u);  // dims from d on
     // A lane's pieces: copies (row and 16 bytes of it), operands of the products.
     constexpr int kPer = DP / 16;                                // pieces of a row
-    const int row = lane / kPer, piece = lane % kPer;            // of the first copy; the others are 32 / kPer rows further
-    const uint32_t to = DP == 128 ? row * 128 + (piece ^ row) * 16
-                                  : (row >> 1) * 128 + (((row & 1) * 4 + piece) ^ (((row >> 1) & 3) * 2)) * 16;
+    const int row = lane / kPer, piece = lane % kPer;            // of the first copy; the other is 4 rows further
+    const uint32_t to = ring + (DP == 128 ? row * 128 + (piece ^ row) * 16
+                                          : (row >> 1) * 128 + (((row & 1) * 4 + piece) ^ (((row >> 1) & 3) * 2)) * 16);
+    const uint32_t to4 = ring + (row + 4) * 128 + (piece ^ (row + 4)) * 16;  // DP 128
     const bool copies = kExact || piece * 16 < d;
     const int64_t from = (int64_t)row * p.c.slot_stride + piece * 16;
-    const uint32_t key0 = DP == 128 ? r * 128 + ((2 * c) ^ r) * 16 : (r >> 1) * 128 + (((r & 1) * 4 + c) ^ (((r >> 1) & 3) * 2)) * 16;
-    const uint32_t key1 = r * 128 + ((2 * c + 1) ^ r) * 16;      // DP 128: the second 16 of its 32 dims
-    const uint32_t val0 = DP == 128 ? 2 * c * 128 + (r ^ (2 * c)) * 16 : c * 128 + ((r >> 1) ^ (c * 2)) * 16 + (r & 1) * 8;
-    const uint32_t val1 = DP == 128 ? (2 * c + 1) * 128 + (r ^ (2 * c + 1)) * 16 : c * 128 + ((4 + (r >> 1)) ^ (c * 2)) * 16 + (r & 1) * 8;
+    const uint8_t *key_from = (const uint8_t*)p.c.k + from, *value_from = (const uint8_t*)p.c.v + from;
+    const uint32_t key0 = ring + (DP == 128 ? r * 128 + ((2 * c) ^ r) * 16 : (r >> 1) * 128 + (((r & 1) * 4 + c) ^ (((r >> 1) & 3) * 2)) * 16);
+    const uint32_t key1 = ring + r * 128 + ((2 * c + 1) ^ r) * 16;      // DP 128: the second 16 of its 32 dims
+    const uint32_t val0 = ring + kSide + (DP == 128 ? 2 * c * 128 + (r ^ (2 * c)) * 16 : c * 128 + ((r >> 1) ^ (c * 2)) * 16 + (r & 1) * 8);
+    const uint32_t val1 = ring + kSide + (DP == 128 ? (2 * c + 1) * 128 + (r ^ (2 * c + 1)) * 16 : c * 128 + ((4 + (r >> 1)) ^ (c * 2)) * 16 + (r & 1) * 8);
 
     float o[VW][2][4], m[2], l[2], factor[2];
     m[0] = m[1] = -INFINITY, l[0] = l[1] = 0.f;
+    float base[2] = {0.f, 0.f}, limit[2] = {-INFINITY, -INFINITY};  // m where it is finite; where it moves
 #pragma unroll
     for (int b = 0; b < VW; ++b)
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[b][i / 4][i % 4] = 0.f;
     float unit = 0x1p-126f, unit_inv = 0x1p126f;  // of the values' sums
+    // Rounds of 32 groups, one a lane: offsets (in 16 bytes) and scales of this one, offsets of the
+    // next, of which groups are there, a bit each.
     using Keys = ScaledWalk<true, kKeys>;
-    Keys walk(p, w.s, w.h, k0, k1);
-    walk.turn();
+    Keys walk(p, w.s, w.h, w.k0, k1);
+    uint32_t valid, valid_next = __ballot_sync(0xffffffffu, walk.page1 >= 0), next = walk.next();
+    auto turn = [&] {
+      valid = valid_next;
+      walk.turn();
+      valid_next = __ballot_sync(0xffffffffu, walk.page1 >= 0), next = walk.next();
+    };
+    turn();
     __syncwarp();
-    // Copies of the step whose first group is the lane_at + ahead-th of the walk's round.
-    auto copy = [&](int ahead, int stage) {
+    // Copies of the step whose first group is the j-th from the round's start.
+    auto copy = [&](int j, uint32_t stage) {
+      const uint32_t offs = j < 32 ? walk.off : next, there = (j < 32 ? valid : valid_next) >> (j & 31);
 #pragma unroll
-      for (int g = 0; g < 2 * KG; ++g) {
-        const int j = walk.lane_at + ahead + g;
-        uint32_t off;
-        if (j < 32) off = __shfl_sync(0xffffffffu, walk.off, j);
-        else off = __shfl_sync(0xffffffffu, walk.next(), j - 32);
-        if (off == Keys::kNoKey || !copies) continue;
-        constexpr int kCopies = DP / 64;  // of a group of 8 rows
-#pragma unroll
-        for (int i = 0; i < kCopies; ++i) {
-          const int64_t at = (int64_t)((unsigned long long)off * 16) + from + i * (8 / kCopies) * p.c.slot_stride;
-          // (4 rows on the pieces' places change by 4 of 8)
-          const uint32_t there = ring + stage * 2 * kSide + g * 8 * DP + (i ? (to ^ 64) + 4 * 128 : to);
-          copy16(there, (const uint8_t*)p.c.k + at);
-          copy16(there + kSide, (const uint8_t*)p.c.v + at);
+      for (int g = 0; g < kGroups; ++g) {
+        const uint32_t off = __shfl_sync(0xffffffffu, offs, (j + g) & 31);
+        if (!((there >> g) & 1u) || !copies) continue;
+        const uint8_t *key = key_from + (unsigned long long)off * 16, *value = value_from + (unsigned long long)off * 16;
+        copy16(to + stage + g * 8 * DP, key), copy16(to + stage + g * 8 * DP + kSide, value);
+        if constexpr (DP == 128) {
+          copy16(to4 + stage + g * 8 * DP, key + 4 * p.c.slot_stride);
+          copy16(to4 + stage + g * 8 * DP + kSide, value + 4 * p.c.slot_stride);
         }
       }
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
     copy(0, 0), commit();
-    if (k0 + kKeys < k1) copy(2 * KG, 1);
+    int left = k1 - w.k0;  // keys
+    if (left > kKeys) copy(kGroups, 2 * kSide);
     commit();
     // queries
     uint32_t q[KP][8];
@@ -549,48 +558,57 @@ struct Fp8Ring {
       factor[0] = __shfl_sync(0xffffffffu, up, 8 * c);
       factor[1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
     }
-    int stage = 0;
-    for (int k = k0; k < k1; k += kKeys, stage ^= 1) {
+    uint32_t stage = 0;
+#pragma unroll 1
+    for (int j = 0; left > 0; left -= kKeys, stage ^= 2 * kSide) {
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncwarp();
       uint4 kr[KG][2][KP];
       uint32_t vr[KG][4][VW];
-      const uint32_t keys = ring + stage * 2 * kSide, values = keys + kSide;
 #pragma unroll
       for (int g = 0; g < KG; ++g)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint32_t at = (g * 16 + u * 8) * DP;
-          kr[g][u][0] = shared16(keys + at + key0);
-          if (KP == 2) kr[g][u][KP - 1] = shared16(keys + at + key1);
+          constexpr int kGroup = 8 * DP;
+          kr[g][u][0] = shared16(key0 + stage + (g * 2 + u) * kGroup);
+          if (KP == 2) kr[g][u][KP - 1] = shared16(key1 + stage + (g * 2 + u) * kGroup);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if constexpr (VW == 4) {
-              const uint4 v = shared16(values + at + (x ? val1 : val0));
+              const uint4 v = shared16((x ? val1 : val0) + stage + (g * 2 + u) * kGroup);
               vr[g][2 * u + x][0] = v.x, vr[g][2 * u + x][1] = v.y, vr[g][2 * u + x][2] = v.z, vr[g][2 * u + x][3] = v.w;
             } else {
-              const uint2 v = shared8(values + at + (x ? val1 : val0));
+              const uint2 v = shared8((x ? val1 : val0) + stage + (g * 2 + u) * kGroup);
               vr[g][2 * u + x][0] = v.x, vr[g][2 * u + x][1] = v.y;
             }
           }
         }
-      // the step's groups
-      uint32_t there = 0xffffffffu;  // keys that count
-      float ks[KG][2], vs[KG][2];
       __syncwarp();
-      if (k + 2 * kKeys < k1) copy(4 * KG, stage);
+      if (left > 2 * kKeys) copy(j + 2 * kGroups, stage);
       commit();
-      float top = 0.f;
+      // the step's groups: scales, and which keys count
+      float ks[KG][2], vs[KG][2], top = 0.f;
 #pragma unroll
       for (int g = 0; g < KG; ++g)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          uint32_t off;
-          walk.group(off, ks[g][u], vs[g][u]);
-          if (off == Keys::kNoKey) there &= ~(0xffu << (g * 16 + u * 8));
-          top = fmaxf(top, vs[g][u]);
+          if (kSame && u == 1) {
+            ks[g][1] = ks[g][0], vs[g][1] = vs[g][0];
+          } else {
+            ks[g][u] = __shfl_sync(0xffffffffu, walk.ks, j + 2 * g + u) * p.scale2, vs[g][u] = __shfl_sync(0xffffffffu, walk.vs, j + 2 * g + u);
+            top = fmaxf(top, vs[g][u]);
+          }
         }
-      if (k1 - k < kKeys) there &= (1u << (k1 - k)) - 1u;
+      const bool whole = left >= kKeys && (valid >> j & ((1u << kGroups) - 1u)) == (1u << kGroups) - 1u;
+      uint32_t there = 0xffffffffu;
+      if (!whole) {
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+          if (!((valid >> (j + g)) & 1u)) there &= ~(0xffu << (8 * g));
+        if (left < kKeys) there &= (1u << left) - 1u;
+      }
+      j += kGroups;
+      if (j == 32) turn(), j = 0;
       if (top > unit) {
         const float keep = unit / top;
         unit = top, unit_inv = 1.f / top;
@@ -621,9 +639,9 @@ struct Fp8Ring {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (kTwice) z[g][i] += __shfl_xor_sync(0xffffffffu, z[g][i], 2);
-          z[g][i] *= factor[i & 1] * ks[g][i >> 1] * p.scale2;
+          z[g][i] *= factor[i & 1] * ks[g][i >> 1];
         }
-      if (__builtin_expect(there != 0xffffffffu, 0)) {
+      if (__builtin_expect(!whole, 0)) {
 #pragma unroll
         for (int g = 0; g < KG; ++g) {
 #pragma unroll
@@ -639,7 +657,7 @@ struct Fp8Ring {
       // softmax: the reference of a head moves only when a score passes the maximum by 2^8
       bool move = false;
 #pragma unroll
-      for (int g = 0; g < KG; ++g) move |= fmaxf(z[g][0], z[g][2]) > m[0] + 15.f || fmaxf(z[g][1], z[g][3]) > m[1] + 15.f;
+      for (int g = 0; g < KG; ++g) move |= fmaxf(z[g][0], z[g][2]) > limit[0] || fmaxf(z[g][1], z[g][3]) > limit[1];
       if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -651,6 +669,7 @@ struct Fp8Ring {
           best -= 7.f;
           const float keep = weight(m[e], best);
           m[e] = best;
+          base[e] = best == -INFINITY ? 0.f : best, limit[e] = best + 15.f;
           l[e] *= keep;
 #pragma unroll
           for (int b = 0; b < VW; ++b)
@@ -660,9 +679,8 @@ struct Fp8Ring {
       }
 #pragma unroll
       for (int g = 0; g < KG; ++g) {
-        const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
-        float p0 = exp2_fast(z[g][0] - m0), p1 = exp2_fast(z[g][1] - m1);
-        float p2 = exp2_fast(z[g][2] - m0), p3 = exp2_fast(z[g][3] - m1);
+        float p0 = exp2_fast(z[g][0] - base[0]), p1 = exp2_fast(z[g][1] - base[1]);
+        float p2 = exp2_fast(z[g][2] - base[0]), p3 = exp2_fast(z[g][3] - base[1]);
         l[0] += p0 + p2, l[1] += p1 + p3;
         const float b0 = vs[g][0] * unit_inv, b1 = vs[g][1] * unit_inv;
         p0 *= b0, p1 *= b0, p2 *= b1, p3 *= b1;
@@ -706,7 +724,10 @@ struct Fp8Ring {
 template <typename T, int N, int DP>
 int launch_fp8(const DecodeParams& p, const Plan& pl, cudaStream_t st) {
   if (!pl.fast) return launch<Fp8Path<T, N, DP, false, false>>(p, pl, st);
-  if constexpr (N == 4) return p.c.head_dim == DP ? launch<Fp8Ring<T, DP, true>>(p, pl, st) : launch<Fp8Ring<T, DP, false>>(p, pl, st);
+  if constexpr (N == 4) {
+    if (p.c.head_dim != DP) return launch<Fp8Ring<T, DP, false, false>>(p, pl, st);
+    return p.c.page_size % 16 == 0 ? launch<Fp8Ring<T, DP, true, true>>(p, pl, st) : launch<Fp8Ring<T, DP, true, false>>(p, pl, st);
+  }
   else return pl.exact ? launch<Fp8Path<T, N, DP, true, true>>(p, pl, st) : launch<Fp8Path<T, N, DP, true, false>>(p, pl, st);
 }
 
