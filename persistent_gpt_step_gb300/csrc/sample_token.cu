@@ -37,7 +37,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBlocks = 8;        // of a cluster at most
 constexpr int kBins = 1024;
 constexpr int kList = 1024;
-constexpr int kShort = 256;       // entries of a list that need no sorting
+// Entries of a list that are compared with one another, one a thread; longer ones go through bins.  (Rows of
+// 12,288 with a top_k of up to 200: 13.6 us, and 17.6 through bins; 512 of 131,072: 119 and 133.)
+constexpr int kShort = kThreads;
 constexpr int kTable = 1024;
 constexpr int kPieces = 4;        // of a warp's range, where sums are in fp32
 using u64 = unsigned long long;
@@ -309,6 +311,9 @@ struct Shared {
     struct { u64 before, all; uint32_t bin, count; int way; } found;  // (the first block's)
     struct { int low, high; uint32_t upto; } ends;                     // (the first block's)
   };
+  u64 bin_mass[kThreads], ends_of[kWarps][2], counts[kWarps];
+  uint32_t bin_count[kThreads];
+  struct { u64 before; int bin; uint32_t count; } crossed;
   double drop;
   uint32_t listed, gathered, base;
   int chosen;
@@ -344,21 +349,48 @@ __device__ __noinline__ u64 block_scan(u64 v, u64* scratch, u64* total) {
   *total = sum;
   return v;
 }
-// Sorts the first n in falling order; what lies behind them up to a power of two is written over.
-__device__ __noinline__ void sort_falling(u64* x, int n) {
-  int m = 2;
-  while (m < n) m *= 2;
-  for (int i = n + threadIdx.x; i < m; i += kThreads) x[i] = 0;
-  for (int k = 2; k <= m; k *= 2)
-    for (int j = k / 2; j > 0; j /= 2) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < m / 2; i += kThreads) {
-        const int a = (i & ~(j - 1)) * 2 + (i & (j - 1)), b = a + j;
-        const u64 u = x[a], v = x[b];
-        if ((u < v) == !(a & k)) x[a] = v, x[b] = u;
-      }
-    }
+// Of the n entries of sm.all at or above `floor`, in falling order or (kById) by rising ids: the one at
+// which the running sum of their weights (kCount: of ones) reaches `goal`, which it does.  The keys'
+// range is cut in 256 bins, and the bin where that happens again, until it holds one entry.  By all
+// threads of the block.
+enum { kCount, kMass, kById };
+__device__ __noinline__ int cross(Shared& sm, int n, int by, u64 goal, u64 floor) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  static_assert(kThreads == 256, "a bin each");
+  auto key_of_entry = [&](int i) { return by == kById ? (u64) ~(uint32_t)sm.all[i] : ~sm.all[i]; };
+  u64 lo = ~0ull, hi = 0, before = 0;
+  for (int i = tid; i < n; i += kThreads)
+    if (sm.all[i] >= floor) lo = min(lo, key_of_entry(i)), hi = max(hi, key_of_entry(i));
+  lo = ~warp_max(~lo), hi = warp_max(hi);
   __syncthreads();
+  if (lane == 0) sm.ends_of[warp][0] = lo, sm.ends_of[warp][1] = hi;
+  __syncthreads();
+  for (int w = 0; w < kWarps; ++w) lo = min(lo, sm.ends_of[w][0]), hi = max(hi, sm.ends_of[w][1]);
+  while (true) {
+    int shift = 0;
+    while ((hi - lo) >> shift >= kThreads) ++shift;
+    sm.bin_mass[tid] = 0, sm.bin_count[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) {
+      const u64 key = key_of_entry(i);
+      if (sm.all[i] < floor || key < lo || key > hi) continue;
+      atomicAdd(&sm.bin_count[(key - lo) >> shift], 1u);
+      if (by != kCount) atomicAdd(&sm.bin_mass[(key - lo) >> shift], sm.weights[i]);
+    }
+    __syncthreads();
+    u64 total;
+    const u64 here = by == kCount ? sm.bin_count[tid] : sm.bin_mass[tid], to = before + block_scan(here, sm.scratch, &total) - here;
+    if (to < goal && to + here >= goal) sm.crossed.before = to, sm.crossed.bin = tid, sm.crossed.count = sm.bin_count[tid];
+    __syncthreads();
+    before = sm.crossed.before;
+    lo += (u64)sm.crossed.bin << shift, hi = lo + (1ull << shift) - 1;
+    if (sm.crossed.count == 1) break;
+    __syncthreads();
+  }
+  for (int i = tid; i < n; i += kThreads)
+    if (sm.all[i] >= floor && key_of_entry(i) >= lo && key_of_entry(i) <= hi) sm.chosen = i;
+  __syncthreads();
+  return sm.chosen;
 }
 
 template <typename T>
@@ -518,7 +550,7 @@ struct Sampler {
     return true;
   }
 
-  // The entries of sm.all sorted, weights of the first n, and their sum.
+  // Weights of the n entries of sm.all, and their sum.
   __device__ __forceinline__ u64 weigh_list(int n) {
     u64 sum = 0;
     for (int i = tid; i < n; i += kThreads) {
@@ -527,19 +559,6 @@ struct Sampler {
     }
     return block_sum(sum);
   }
-  // How many of the first n it takes for a sum of at least `goal`.
-  __device__ __forceinline__ int fewest(int n, u64 goal) {
-    const int each = (n + kThreads - 1) / kThreads;
-    u64 mine = 0, total;
-    for (int i = tid * each; i < min(n, (tid + 1) * each); ++i) mine += sm.weights[i];
-    u64 upto = block_scan(mine, sm.scratch, &total) - mine;
-    for (int i = tid * each; i < min(n, (tid + 1) * each); ++i) {
-      if (upto < goal && upto + sm.weights[i] >= goal) sm.chosen = i + 1;
-      upto += sm.weights[i];
-    }
-    __syncthreads();
-    return sm.chosen;
-  }
   __device__ __forceinline__ bool finish(int n, u64 best, u64 whole) { return n <= kShort ? finish_short(n, best, whole) : finish_long<T>(p, sm, n, best, whole, top(), top_k); }
 
   // Units of a piece of a warp's range: whole steps.
@@ -547,7 +566,7 @@ struct Sampler {
   static __device__ __forceinline__ int piece_units(int range) { return ((range + kStep - 1) / kStep + kPieces - 1) / kPieces * kStep; }
 
   // What is left to slow_row: nothing, or the row, by all blocks or by this one alone.
-  enum { kDone, kTogether, kAlone };
+  enum { kDone, kTogether, kAlone, kDrawn };
 
   // Rows without limits.  (A block alone took 45 us for the 131,072 integers of a row: all of them stay
   // until the number's token is known.)
@@ -752,12 +771,13 @@ struct Sampler {
   // sum of the weights in units of the bin's first (one addition a token, in 32 bits), name the
   // bins in which the limit's last token can lie.  A second pass lists these, or, where they are few,
   // all above their end, and sums all weights, and those above, as integers.
-  // 0: done; 1: no such luck; otherwise the last token that top_p keeps.
-  __device__ __forceinline__ u64 by_sums(u64 best) {
+  // kDone; or, with *last the last token that top_p keeps or 1, what is left: kTogether, or kDrawn, the
+  // draw alone.
+  __device__ __forceinline__ int by_sums(u64 best, u64* last_kept) {
     constexpr float kSpan = 46.f;
     const float each = kBins / kSpan * c_hi;  // bins of a logit
     const int bits = min(14, 31 - (32 - __clz(a.vocab - 1)));
-    if (!(each > 1e-3f && each < 1e30f) || bits < 8) return 1;
+    if (!(each > 1e-3f && each < 1e30f) || bits < 8) return kTogether;
     for (int i = tid; i < kBins; i += kThreads) sm.share[i] = 0;
     __syncthreads();
     const float m = top(), one = (float)(1 << bits);
@@ -808,6 +828,7 @@ struct Sampler {
     const u64(*choice)[kBlocks] = share(ends, way, 0);
     const int low = choice[1][0] ? 0 : (int)(choice[0][0] >> 32), high = (int)(uint32_t)choice[0][0];
     u64 whole = 0, above = 0;
+    uint32_t many = 0;
     gather([&](const float* x, int id, auto name) {
       u64 w[8];
       int at[8];
@@ -815,12 +836,17 @@ struct Sampler {
 #pragma unroll
       for (int i = 0; i < 8; ++i) at[i] = (int)fminf((m - x[i]) * each, (float)(kBins - 1));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) whole += w[i], above += at[i] < low ? w[i] : 0;
+      for (int i = 0; i < 8; ++i) {
+        whole += w[i];
+        if (at[i] < low) above += w[i], ++many;
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (x[i] > -INFINITY && at[i] >= low && at[i] <= high) name(x[i], id + i);
     });
-    whole = block_sum(whole), above = block_sum(above);
+    above = warp_sum(above), many = __reduce_add_sync(0xffffffffu, many);
+    if (lane == 0) sm.parts[warp] = above, sm.counts[warp] = many;
+    whole = block_sum(whole), above = block_sum(lane == 0 ? above : 0);
     const u64(*got)[kBlocks] = share(whole, above, 0);
     whole = above = 0;
 #pragma unroll 1
@@ -832,11 +858,24 @@ struct Sampler {
         last = finish(n, best, whole) ? 0 : 1;
       } else {
         const u64 goal = max(part_of(top_p, whole, true), 1ull);
-        sort_falling(sm.all, n);
-        if (above < goal && above + weigh_list(n) >= goal) last = sm.all[fewest(n, goal - above) - 1];
+        if (above < goal && above + weigh_list(n) >= goal) last = sm.all[cross(sm, n, kMass, goal - above, 1)];
       }
     }
-    return share(last, 0, 0)[0][0];
+    last = share(last, 0, 0)[0][0];
+    if (last == 0) return kDone;
+    *last_kept = last;
+    if (last == 1 || least(best) > last) return kTogether;  // (a stricter min_p cuts what lies above the bins)
+    // what the limit keeps of this block's part of the list, to the sums of what lies above
+    for (uint32_t i = tid; i < sm.listed; i += kThreads) {
+      const u64 comp = sm.list[i];
+      if (comp < last) continue;
+      const int at = (id_of(comp) + row.shift) / 8;
+      int w = 0;
+      while (w < kWarps - 1 && at >= warp_begin(w + 1)) ++w;
+      atomicAdd(&sm.parts[w], weight(value_of((uint32_t)(comp >> 32)))), atomicAdd(&sm.counts[w], 1ull);
+    }
+    __syncthreads();
+    return kDrawn;
   }
 };
 
@@ -845,37 +884,72 @@ template <typename T>
 __device__ __noinline__ bool finish_long(const SampleParams& p, Shared& sm, int n, u64 best, u64 whole, float m, int top_k) {
   Sampler<T> s(p, sm, true);
   s.set_top(m);
-  const int tid = s.tid;
-    sort_falling(sm.all, n);
-  int keep = top_k ? min(top_k, n) : n;
-  u64 sum = s.weigh_list(keep);
+  u64 sum = s.weigh_list(n), kept, from = 1;
+  auto sum_from = [&] {
+    sum = kept = 0;
+    for (int i = s.tid; i < n; i += kThreads)
+      if (sm.all[i] >= from) sum += sm.weights[i], ++kept;
+    sum = s.block_sum(sum), kept = s.block_sum(kept);
+  };
+  if (top_k && top_k < n) from = sm.all[cross(sm, n, kCount, top_k, 1)], sum_from();
   if (s.top_p < 1.f) {
     const u64 goal = max(s.top_p > 0.f ? part_of(s.top_p, top_k ? sum : whole, true) : 0, 1ull);
     if (sum < goal) return false;
-    keep = s.fewest(keep, goal);
+    from = sm.all[cross(sm, n, kMass, goal, from)];
   }
-  const u64 from = s.least(best);
-  int above = 0;
-  for (int i = tid; i < keep; i += kThreads) above += sm.all[i] >= from;
-  keep = (int)s.block_sum(above);
-  sum = 0;
-  for (int i = tid; i < keep; i += kThreads) sum += sm.weights[i];
-  sum = s.block_sum(sum);
-  // by rising ids: falling ~id
-  for (int i = tid; i < keep; i += kThreads) sm.all[i] = (u64)(uint32_t)sm.all[i] << 32 | (uint32_t)i;
-  __syncthreads();
-  sort_falling(sm.all, keep);
-  const u64 goal = goal_of(s.u, sum);
-  const int each = (keep + kThreads - 1) / kThreads;
-  u64 mine = 0, total;
-  for (int i = tid * each; i < min(keep, (tid + 1) * each); ++i) mine += sm.weights[(uint32_t)sm.all[i]];
-  u64 upto = block_scan(mine, sm.scratch, &total) - mine;
-  for (int i = tid * each; i < min(keep, (tid + 1) * each); ++i) {
-    const u64 w = sm.weights[(uint32_t)sm.all[i]];
-    if (upto < goal && upto + w >= goal) s.answer((int)~(uint32_t)(sm.all[i] >> 32), s.log_of((float)w, (float)sum), keep);
-    upto += w;
-  }
+  from = max(from, s.least(best));
+  sum_from();
+  const int i = cross(sm, n, kById, goal_of(s.u, sum), from);
+  if (s.tid == 0) s.answer(id_of(sm.all[i]), s.log_of((float)sm.weights[i], (float)sum), (int)kept);
   return true;
+}
+
+// The draw, where sm.parts and sm.counts have the sums of the weights, and the numbers, of the kept
+// tokens of each warp's range.
+template <typename T>
+__device__ __noinline__ void draw_row(const SampleParams& p, Shared& sm, bool alone, int turn, float m, u64 last) {
+  Sampler<T> s(p, sm, alone);
+  s.turn = turn;
+  s.set_top(m);
+  const Weigher weight = s.weight;
+  const Kept limit(last);
+  u64 sum = 0, kept = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) sum += sm.parts[w], kept += sm.counts[w];
+  const u64(*got)[kBlocks] = s.share(sum, kept, 0);
+  u64 before = 0;
+  sum = kept = 0;
+#pragma unroll 1
+  for (int i = 0; i < s.blocks; ++i) {
+    if (i == s.part) before = sum;
+    sum += got[0][i], kept += got[1][i];
+  }
+  const u64 goal = goal_of(s.u, sum);
+  if (before >= goal || before + got[0][s.part] < goal) return;  // another block's
+  int w = 0;
+  while (before + sm.parts[w] < goal) before += sm.parts[w++];
+  // the warp's tokens one after the other, 2,048 at a time
+  const int s0 = s.warp_begin(w), s1 = s.warp_begin(w + 1);
+  for (int v = s0; v < s1; v += kThreads) {
+    const int id = (v + s.tid) * 8 - s.row.shift, first_id = max(id, 0), end_id = v + s.tid < s1 ? min(id + 8, s.a.vocab) : 0;
+    u64 own = 0, total;
+    auto one = [&](int i) {
+      const float x = s.row.at(i);
+      return limit.has(x, i) ? weight(x) : 0ull;
+    };
+#pragma unroll 1
+    for (int i = first_id; i < end_id; ++i) own += one(i);
+    u64 upto = before + block_scan(own, sm.scratch, &total) - own;
+    if (upto < goal && upto + own >= goal)
+#pragma unroll 1
+      for (int i = first_id; i < end_id; ++i) {
+        const u64 y = one(i);
+        if (upto < goal && upto + y >= goal) s.answer(i, s.log_of((float)y, (float)sum), (int)kept);
+        upto += y;
+      }
+    before += total;
+    if (before >= goal) return;
+  }
 }
 
 // Any row whose first token is known (without limits: whose largest logit is): rounds of bins for
@@ -894,7 +968,6 @@ __device__ __noinline__ void slow_row(const SampleParams& p, Shared& sm, bool al
   // The last token of the prefix of `target` tokens, or (kMass) of the fewest whose weights sum
   // to top_p of the sum of all, among those at or above `floor`; `floor` where there are not as many.
   // 0: the row is done (all that counts was in the list).
-  enum { kCount, kMass };
   enum { kBin, kWhole, kNoLimit };
   auto select = [&](int by, u64 target, u64 floor) -> u64 {
     u64 lo = 0, hi = 0;  // of the composite keys that are left, after the first round
@@ -1001,13 +1074,8 @@ __device__ __noinline__ void slow_row(const SampleParams& p, Shared& sm, bool al
           s.top_k = by == kCount ? s.top_k : 0;
           s.finish(n, best, sm.found.all);
         } else {
-          sort_falling(sm.all, n);
-          if (by == kCount) {
-            last = sm.all[target - before - 1];
-          } else {
-            s.weigh_list(n);
-            last = sm.all[s.fewest(n, target - before) - 1];
-          }
+          if (by == kMass) s.weigh_list(n);
+          last = sm.all[cross(sm, n, by, target - before, 1)];
         }
       }
       if (take_all) return 0;
@@ -1045,45 +1113,9 @@ __device__ __noinline__ void slow_row(const SampleParams& p, Shared& sm, bool al
   });
   sum = warp_sum(sum), kept = warp_sum(kept);
   __syncthreads();
-  if (lane == 0) sm.parts[warp] = sum, sm.scratch[warp] = kept;
+  if (lane == 0) sm.parts[warp] = sum, sm.counts[warp] = kept;
   __syncthreads();
-  sum = kept = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) sum += sm.parts[w], kept += sm.scratch[w];
-  const u64(*got)[kBlocks] = s.share(sum, kept, 0);
-  u64 before = 0;
-  sum = kept = 0;
-#pragma unroll 1
-  for (int i = 0; i < blocks; ++i) {
-    if (i == part) before = sum;
-    sum += got[0][i], kept += got[1][i];
-  }
-  const u64 goal = goal_of(s.u, sum);
-  if (before >= goal || before + got[0][part] < goal) return;  // another block's
-  int w = 0;
-  while (before + sm.parts[w] < goal) before += sm.parts[w++];
-  // the warp's tokens one after the other, 2,048 at a time
-  const int s0 = s.warp_begin(w), s1 = s.warp_begin(w + 1);
-  for (int v = s0; v < s1; v += kThreads) {
-    const int id = (v + tid) * 8 - row.shift, first_id = max(id, 0), end_id = v + tid < s1 ? min(id + 8, s.a.vocab) : 0;
-    u64 own = 0, total;
-    auto one = [&](int i) {
-      const float x = row.at(i);
-      return limit.has(x, i) ? weight(x) : 0ull;
-    };
-#pragma unroll 1
-    for (int i = first_id; i < end_id; ++i) own += one(i);
-    u64 upto = before + block_scan(own, sm.scratch, &total) - own;
-    if (upto < goal && upto + own >= goal)
-#pragma unroll 1
-      for (int i = first_id; i < end_id; ++i) {
-        const u64 y = one(i);
-        if (upto < goal && upto + y >= goal) s.answer(i, s.log_of((float)y, (float)sum), (int)kept);
-        upto += y;
-      }
-    before += total;
-    if (before >= goal) return;
-  }
+  draw_row<T>(p, sm, alone, s.turn, m, last);
 }
 
 template <typename T>
@@ -1113,11 +1145,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_token_kernel(const __grid_
     if (s.top_k || (s.min_p > 0.f && !(s.top_p < 1.f))) {
       left = s.by_list(best);
     } else if (s.top_p < 1.f) {
-      last = s.by_sums(best);
-      if (last == 0) return;
+      left = s.by_sums(best, &last);
     }
   }
   if (left == Sampler<T>::kDone) return;
+  if (left == Sampler<T>::kDrawn) return draw_row<T>(p, sm, false, s.turn, s.top(), last);
   slow_row<T>(p, sm, left == Sampler<T>::kAlone, s.turn, best, s.top(), last);
 }
 
