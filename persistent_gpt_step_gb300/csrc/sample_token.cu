@@ -311,9 +311,9 @@ struct Shared {
     struct { u64 before, all; uint32_t bin, count; int way; } found;  // (the first block's)
     struct { int low, high; uint32_t upto; } ends;                     // (the first block's)
   };
-  u64 bin_mass[kThreads], ends_of[kWarps][2], counts[kWarps];
-  uint32_t bin_count[kThreads];
-  struct { u64 before; int bin; uint32_t count; } crossed;
+  u64 ends_of[kWarps][2], counts[kWarps];
+  uint32_t words[3][kThreads];
+  struct { u64 before; int bin; } crossed;
   double drop;
   uint32_t listed, gathered, base;
   int chosen;
@@ -350,45 +350,53 @@ __device__ __noinline__ u64 block_scan(u64 v, u64* scratch, u64* total) {
   return v;
 }
 // Of the n entries of sm.all at or above `floor`, in falling order or (kById) by rising ids: the one at
-// which the running sum of their weights (kCount: of ones) reaches `goal`, which it does.  The keys'
-// range is cut in 256 bins, and the bin where that happens again, until it holds one entry.  By all
-// threads of the block.
+// which the running sum of their weights (kCount: of ones) reaches `goal`, which it does.  The range of
+// their keys is cut in 256 bins, and that of the bin where that happens again, until it holds one.
+// Bins' sums are in three words, for atomics of 32 bits: those of 64 go round for each thread that
+// meets another (20 us, of equal logits; 4 so).  By all threads of the block.
 enum { kCount, kMass, kById };
 __device__ __noinline__ int cross(Shared& sm, int n, int by, u64 goal, u64 floor) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  static_assert(kThreads == 256, "a bin each");
-  auto key_of_entry = [&](int i) { return by == kById ? (u64) ~(uint32_t)sm.all[i] : ~sm.all[i]; };
-  u64 lo = ~0ull, hi = 0, before = 0;
-  for (int i = tid; i < n; i += kThreads)
-    if (sm.all[i] >= floor) lo = min(lo, key_of_entry(i)), hi = max(hi, key_of_entry(i));
-  lo = ~warp_max(~lo), hi = warp_max(hi);
-  __syncthreads();
-  if (lane == 0) sm.ends_of[warp][0] = lo, sm.ends_of[warp][1] = hi;
-  __syncthreads();
-  for (int w = 0; w < kWarps; ++w) lo = min(lo, sm.ends_of[w][0]), hi = max(hi, sm.ends_of[w][1]);
+  static_assert(kThreads == 256 && kList <= 1024, "a bin each, words of 22 bits");
+  auto key_of_entry = [&](u64 comp) { return by == kById ? (u64) ~(uint32_t)comp : ~comp; };
+  u64 lo = 0, hi = ~0ull, before = 0;
   while (true) {
-    int shift = 0;
-    while ((hi - lo) >> shift >= kThreads) ++shift;
-    sm.bin_mass[tid] = 0, sm.bin_count[tid] = 0;
-    __syncthreads();
+    u64 first = ~0ull, last = 0;
+#pragma unroll 1
     for (int i = tid; i < n; i += kThreads) {
-      const u64 key = key_of_entry(i);
-      if (sm.all[i] < floor || key < lo || key > hi) continue;
-      atomicAdd(&sm.bin_count[(key - lo) >> shift], 1u);
-      if (by != kCount) atomicAdd(&sm.bin_mass[(key - lo) >> shift], sm.weights[i]);
+      const u64 comp = sm.all[i], key = key_of_entry(comp);
+      if (comp >= floor && key >= lo && key <= hi) first = min(first, key), last = max(last, key);
+    }
+    first = ~warp_max(~first), last = warp_max(last);
+    if (lane == 0) sm.ends_of[warp][0] = first, sm.ends_of[warp][1] = last;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) sm.words[k][tid] = 0;
+    __syncthreads();
+    lo = ~0ull, hi = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) lo = min(lo, sm.ends_of[w][0]), hi = max(hi, sm.ends_of[w][1]);
+    if (lo == hi) break;
+    const int shift = max(0, 56 - __clzll((long long)(hi - lo)));
+#pragma unroll 1
+    for (int i = tid; i < n; i += kThreads) {
+      const u64 comp = sm.all[i], key = key_of_entry(comp), w = by == kCount ? 1 : sm.weights[i];
+      if (comp < floor || key < lo || key > hi) continue;
+      const int at = (int)((key - lo) >> shift);
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if ((w >> 22 * k) & 0x3fffff) atomicAdd(&sm.words[k][at], (uint32_t)(w >> 22 * k) & 0x3fffff);
     }
     __syncthreads();
     u64 total;
-    const u64 here = by == kCount ? sm.bin_count[tid] : sm.bin_mass[tid], to = before + block_scan(here, sm.scratch, &total) - here;
-    if (to < goal && to + here >= goal) sm.crossed.before = to, sm.crossed.bin = tid, sm.crossed.count = sm.bin_count[tid];
+    const u64 here = sm.words[0][tid] + ((u64)sm.words[1][tid] << 22) + ((u64)sm.words[2][tid] << 44);
+    const u64 to = before + block_scan(here, sm.scratch, &total) - here;
+    if (to < goal && to + here >= goal) sm.crossed.before = to, sm.crossed.bin = tid;
     __syncthreads();
     before = sm.crossed.before;
     lo += (u64)sm.crossed.bin << shift, hi = lo + (1ull << shift) - 1;
-    if (sm.crossed.count == 1) break;
-    __syncthreads();
   }
   for (int i = tid; i < n; i += kThreads)
-    if (sm.all[i] >= floor && key_of_entry(i) >= lo && key_of_entry(i) <= hi) sm.chosen = i;
+    if (sm.all[i] >= floor && key_of_entry(sm.all[i]) == lo) sm.chosen = i;
   __syncthreads();
   return sm.chosen;
 }
