@@ -36,6 +36,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBlocks = 8;        // of a cluster at most
 constexpr int kBins = 1024;
+constexpr int kShares = 2048;     // bins of by_sums
 constexpr int kList = 1024;
 // Entries of a list that are compared with one another, one a thread; longer ones go through bins.  (Rows of
 // 12,288 with a top_k of up to 200: 13.6 us, and 17.6 through bins; 512 of 131,072: 119 and 133.)
@@ -296,7 +297,7 @@ struct Shared {
     struct { u64 mass[kBins]; uint32_t count[kBins]; } bins;
     u64 weights[kList];  // of the entries of `all`
     ulonglong2 entries[kShort];
-    uint32_t share[kBins];  // of a bin's weights, in units of its first
+    uint32_t share[kShares];  // of a bin's weights, in units of its first
   };
   union {
     float maxima[kBlocks * kThreads];  // of the cluster's threads (in the first block)
@@ -775,18 +776,18 @@ struct Sampler {
     return sm.gathered <= kList && finish((int)sm.gathered, best, 0) ? kDone : kAlone;
   }
 
-  // Rows with top_p alone, or with min_p: bins of 1/22 of a power of two of weight, in each the
+  // Rows with top_p alone, or with min_p: bins of 1/64 of a power of two of weight, in each the
   // sum of the weights in units of the bin's first (one addition a token, in 32 bits), name the
   // bins in which the limit's last token can lie.  A second pass lists these, or, where they are few,
   // all above their end, and sums all weights, and those above, as integers.
   // kDone; or, with *last the last token that top_p keeps or 1, what is left: kTogether, or kDrawn, the
   // draw alone.
   __device__ __forceinline__ int by_sums(u64 best, u64* last_kept) {
-    constexpr float kSpan = 46.f;
-    const float each = kBins / kSpan * c_hi;  // bins of a logit
+    constexpr float kSpan = 32.f;
+    const float each = kShares / kSpan * c_hi;  // bins of a logit
     const int bits = min(14, 31 - (32 - __clz(a.vocab - 1)));
     if (!(each > 1e-3f && each < 1e30f) || bits < 8) return kTogether;
-    for (int i = tid; i < kBins; i += kThreads) sm.share[i] = 0;
+    for (int i = tid; i < kShares; i += kThreads) sm.share[i] = 0;
     __syncthreads();
     const float m = top(), one = (float)(1 << bits);
     row.each(w0, w1, [&](const float* x, int) {
@@ -795,8 +796,8 @@ struct Sampler {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float y = (m - x[i]) * each, n = floorf(y);  // (NaN where x is)
-        at[i] = n < (float)(kBins - 1) ? (int)n : -1;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[i]) : "f"((n - y) * (kSpan / kBins)));
+        at[i] = n < (float)(kShares - 1) ? (int)n : -1;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[i]) : "f"((n - y) * (kSpan / kShares)));
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -805,22 +806,24 @@ struct Sampler {
     sync_all();
     if (blocks > 1) {
       if (part > 0)
-        for (int i = tid; i < kBins; i += kThreads)
+        for (int i = tid; i < kShares; i += kThreads)
           if (sm.share[i]) atomicAdd(cluster.map_shared_rank(sm.share, 0) + i, sm.share[i]);
       cluster.sync();
     }
     u64 ends = 0, way = 0;
     if (part == 0) {
-      constexpr int kPer = kBins / kThreads;
-      if (tid == 0) sm.ends.low = kBins - 1, sm.ends.high = kBins - 1, sm.ends.upto = ~0u;
+      constexpr int kPer = kShares / kThreads;
+      if (tid == 0) sm.ends.low = kShares - 1, sm.ends.high = kShares - 1, sm.ends.upto = ~0u;
       u64 mass = 0, count = 0, all, total;
-      auto here = [&](int i) { return (u64)((float)sm.share[i] * exp2f(20.f - i * (kSpan / kBins))); };
+      auto here = [&](int i) { return (u64)((float)sm.share[i] * exp2f(20.f - i * (kSpan / kShares))); };
 #pragma unroll 1
       for (int i = 0; i < kPer; ++i) mass += here(tid * kPer + i), count += sm.share[tid * kPer + i];
       u64 mass_to = block_scan(mass, sm.scratch, &all) - mass;
       u64 count_to = block_scan(count, sm.scratch, &total) - count;
-      // sums are off by 2^-bits of themselves: a rounding of at most half of 2^-bits / 0.97, ex2 and what lies below the bins
-      const float goal = top_p * (float)all, off = goal * 4.f / one;
+      // In units of 2^-bits: a sum of bins is off by 0.51 of itself (a rounding of half a unit of at least
+      // 0.98), so is the whole one, and what lies below the bins, 2^-32 of the first token each, is at most
+      // 0.5 of it.  ex2 and the roundings here are below 0.1, up to 2^14.
+      const float goal = top_p * (float)all, off = goal * 2.f / one;
       const u64 goal_lo = (u64)fmaxf(goal - off, 0.f), goal_hi = (u64)(goal + off) + 64;
 #pragma unroll 1
       for (int i = 0; i < kPer; ++i) {
@@ -831,7 +834,9 @@ struct Sampler {
       }
       __syncthreads();
       ends = (u64)sm.ends.low << 32 | sm.ends.high;
-      way = sm.ends.upto <= kList;  // (the tokens, from above: each is more than 0.96 of its bin's first)
+      // (the tokens, from above: each is more than 0.98 of its bin's first.  A list of more is slower than the
+      // rows' sums, 14 us and 10; but a min_p above the bins would need them all again)
+      way = sm.ends.upto <= (min_p > 0.f ? kList : kShort);
     }
     const u64(*choice)[kBlocks] = share(ends, way, 0);
     const int low = choice[1][0] ? 0 : (int)(choice[0][0] >> 32), high = (int)(uint32_t)choice[0][0];
@@ -842,7 +847,7 @@ struct Sampler {
       int at[8];
       weight.eight(x, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) at[i] = (int)fminf((m - x[i]) * each, (float)(kBins - 1));
+      for (int i = 0; i < 8; ++i) at[i] = (int)fminf((m - x[i]) * each, (float)(kShares - 1));
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         whole += w[i];
