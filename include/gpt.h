@@ -498,9 +498,11 @@ typedef struct gpt_fp8_cache {
  *     [0, n_tokens], or NULL: row s is the one new token of sequence s (n_tokens <=
  *     n_seq).  Other arguments as in gpt_kv_append; the scales' strides name no scale
  *     twice.
- *   A row at a position past the table's reach (status), on a bad page (status) or at
- *   a place where starts decreases or leaves its range (status BAD_SEQ) is skipped
- *   whole.  Two sequences that write to one page in a call leave it unspecified.
+ *   A row at a position past the table's reach (status) or on a bad page (status) is
+ *   skipped whole, and so are those of a sequence whose pair of starts decreases or
+ *   leaves its range (status BAD_SEQ).  Sequences whose rows overlap in such a table, or
+ *   that write to one page, leave these pages' numbers and scales, and these rows of
+ *   q_out, unspecified.
  */
 typedef struct gpt_kv_append_fp8_args {
   const void *q, *k, *v;
@@ -518,8 +520,9 @@ int gpt_kv_append_fp8(const gpt_fp8_cache* cache, const gpt_kv_append_fp8_args* 
  * gpt_decode_attention_fp8: gpt_decode_attention over such a cache (the same
  * arguments, q and out of type pages.dtype; strides of the scales may be 0: one scale
  * for all).  A NaN among the values of a key that counts is in the result however
- * small the key's weight is.  Weights enter the product with the values as fp16 numbers
- * (two of them for fp32 outputs), to 2^-32 of the largest; sums are fp32.
+ * small the key's weight is.  Weights, each times its page's value scale, enter the
+ * product with the values as fp16 numbers (two of them for fp32 outputs), down to 2^-32 of
+ * the largest of these; sums are fp32.
  */
 int gpt_decode_attention_fp8(const gpt_fp8_cache* cache, const gpt_decode_attention_args* args, void* cuda_stream);
 
@@ -544,10 +547,11 @@ size_t gpt_decode_attention_fp8_workspace(const gpt_fp8_cache* cache, int32_t n_
  * +infinity: the tokens of +infinity weigh 1 each, the others nothing.
  * logprob = log(w / sum) of the token among the kept ones; kept: their number.  A row
  * without tokens gives token -1, logprob -infinity, kept 0.
- * Weights are summed as 64-bit integers in units of 2^(ceil(log2 vocab) - 63) of the
- * largest, each off by 2^-40 of itself and a unit at most: the choices are those of the
- * definition in 64 bits but where a limit or the number lies that close to a border, and
- * do not depend on how a row is split.
+ * Weights are summed as 64-bit integers in units of 2^-min(48, 63 - ceil(log2 vocab)) of
+ * the largest, each off by 2^-40 of itself and a unit at most: the choices are those of
+ * the definition in 64 bits but where a limit or the number lies that close to a border,
+ * and do not depend on how a row is split.  T below 2^-126 counts as that.  logprob is good
+ * to 2^-19 in rows without limits, to 2^-21 in others, or to that part of itself.
  *   logits: DEVICE [rows, vocab] of type dtype; logits_stride: elements between rows, at
  *     least vocab or 0 (all rows read one); no alignment needed.  uniform,
  *     temperature (NULL: 1 each), top_p, min_p: DEVICE fp32 [rows]; top_k: DEVICE int32
