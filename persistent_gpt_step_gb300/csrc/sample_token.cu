@@ -51,9 +51,6 @@ struct SampleParams {
   u64 coarse[32], fine[32];   // 2^62 2^(i/32), 2^63 2^(i/1024)
 };
 
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-
 // Ascends with z; 0: no token.  Both zeros are one value.
 __device__ __forceinline__ uint32_t key_of(float z) {
   const uint32_t b = __float_as_uint(z + 0.f);
@@ -155,6 +152,14 @@ template <> struct Unit<__nv_bfloat16> {
   }
 };
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+  return m;
+}
+// Of eight; without NaN, if one is a number.
+__device__ __forceinline__ float max_of(const float* x) { return max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7])); }
+
 // 2^n, 0 and the largest power where that is too small or large.
 __device__ __forceinline__ float power(int n) { return __uint_as_float((uint32_t)min(max(n + 127, 0), 254) << 23); }
 
@@ -174,10 +179,8 @@ struct FastSum {
   }
   __device__ __forceinline__ void clear() { sum = rest = 0.f, low = high = -INFINITY, ref = -(1 << 24); }
   __device__ __forceinline__ void add(const float* x) {
-    float m = x[0];
+    const float m = max_of(x);
     Pair all(x[0], x[1]);
-#pragma unroll
-    for (int i = 1; i < 8; ++i) m = fmaxf(m, x[i]);
 #pragma unroll
     for (int i = 2; i < 8; i += 2) all = pgs::add(all, Pair(x[i], x[i + 1]));
     const float2 sums = all.both();
@@ -274,7 +277,6 @@ struct RowView {
       }
     }
   }
-  __device__ __forceinline__ float at(int id) const { return to_float(z[id]); }
 };
 
 // The tokens at or above a composite key (of 1: all of them).
@@ -284,10 +286,7 @@ struct Kept {
   __device__ __forceinline__ explicit Kept(u64 last) : z(last > 1 ? value_of((uint32_t)(last >> 32)) : -INFINITY), id(last > 1 ? id_of(last) : -1) {}
   __device__ __forceinline__ bool has(float x, int i) const { return x > z || (x == z && i <= id); }
   __device__ __forceinline__ bool none(const float* x) const {  // of eight
-    float m = x[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) m = fmaxf(m, x[i]);
-    return !(m >= z);
+    return !(max_of(x) >= z);
   }
 };
 
@@ -426,12 +425,13 @@ struct Sampler {
   __device__ __forceinline__ Sampler(const SampleParams& params, Shared& shared, bool alone) : p(params), a(params.a), sm(shared), cluster(cg::this_cluster()) {
     tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     blocks = cluster.num_blocks(), part = cluster.block_rank(), home = 0, turn = 0;
-    b = blockIdx.x / blocks;
-    if (alone) home = part, blocks = 1, part = 0;
+    int log_blocks = 31 - __clz(blocks);  // (a power of two)
+    b = blockIdx.x >> log_blocks;
+    if (alone) home = part, blocks = 1, part = 0, log_blocks = 0;
     row.z = (const T*)a.logits + b * a.logits_stride, row.vocab = a.vocab;
     row.shift = (int)((reinterpret_cast<uintptr_t>(row.z) / sizeof(T)) & 7);
     units = (int)(((int64_t)a.vocab + row.shift + 7) / 8);
-    b0 = (int)((int64_t)part * units / blocks), b1 = (int)((int64_t)(part + 1) * units / blocks);
+    b0 = (int)((int64_t)part * units >> log_blocks), b1 = (int)((int64_t)(part + 1) * units >> log_blocks);
     w0 = warp_begin(warp), w1 = warp_begin(warp + 1);
     u = a.uniform[b], temperature = a.temperature ? a.temperature[b] : 1.f;
     top_k = a.top_k ? a.top_k[b] : 0;
@@ -559,6 +559,22 @@ struct Sampler {
     return true;
   }
 
+  // The weights of a unit below w1, of the tokens at or above the limit.  (One load: one by one, the
+  // eight waited for memory each, 3 us of a row's 8.)
+  __device__ __forceinline__ void weigh_unit(int w, int w1, const Kept& limit, u64* v) const {
+    Unit<T> x;
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0;
+    if (w >= w1) return;
+    row.load(w, x);
+    const float* z = x.values(y);
+    weight.eight(z, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!limit.has(z[i], w * 8 - row.shift + i)) v[i] = 0;
+  }
+
   // Weights of the n entries of sm.all, and their sum.
   __device__ __forceinline__ u64 weigh_list(int n) {
     u64 sum = 0;
@@ -678,20 +694,19 @@ struct Sampler {
       u64 upto = 0;
 #pragma unroll 1
       for (int w = s0; w < s1; w += kThreads) {
-        const int id = (w + tid) * 8 - row.shift, first_id = max(id, 0), end_id = w + tid < s1 ? min(id + 8, a.vocab) : 0;
-        u64 own = 0, total;
-#pragma unroll 1
-        for (int i = first_id; i < end_id; ++i) own += weight(row.at(i));
+        u64 v[8], own = 0, total;
+        weigh_unit(w + tid, s1, Kept(1), v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) own += v[i];
         u64 at = upto + block_scan(own, sm.scratch, &total) - own;
         if (at <= below && at + own > under)
-#pragma unroll 1
-          for (int i = first_id; i < end_id; ++i) {
-            const u64 v = weight(row.at(i));
-            if (at <= below && at + v > under) {
-              answer(i, log_of((float)v, (float)all * up), units * 8 - (int)flags);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (at <= below && at + v[i] > under) {
+              answer((w + tid) * 8 - row.shift + i, log_of((float)v[i], (float)all * up), units * 8 - (int)flags);
               accepted = 1;
             }
-            at += v;
+            at += v[i];
           }
         upto += total;
       }
@@ -708,9 +723,7 @@ struct Sampler {
     float m = -INFINITY;
     int at = 0;
     row.template each<2>(w0, w1, [&](const float* x, int id) {
-      float y = x[0];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) y = fmaxf(y, x[i]);
+      const float y = max_of(x);
       if (y > m) {
         m = y;
 #pragma unroll
@@ -763,9 +776,7 @@ struct Sampler {
     }
     const Kept limit(top_k ? 1 : least(best));
     gather([&](const float* x, int id, auto name) {
-      float m = x[0];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) m = fmaxf(m, x[i]);
+      const float m = max_of(x);
       if (!(m >= limit.z) || bin_of(m, each) > bin) return;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -924,7 +935,6 @@ __device__ __noinline__ void draw_row(const SampleParams& p, Shared& sm, bool al
   Sampler<T> s(p, sm, alone);
   s.turn = turn;
   s.set_top(m);
-  const Weigher weight = s.weight;
   const Kept limit(last);
   u64 sum = 0, kept = 0;
 #pragma unroll
@@ -944,21 +954,16 @@ __device__ __noinline__ void draw_row(const SampleParams& p, Shared& sm, bool al
   // the warp's tokens one after the other, 2,048 at a time
   const int s0 = s.warp_begin(w), s1 = s.warp_begin(w + 1);
   for (int v = s0; v < s1; v += kThreads) {
-    const int id = (v + s.tid) * 8 - s.row.shift, first_id = max(id, 0), end_id = v + s.tid < s1 ? min(id + 8, s.a.vocab) : 0;
-    u64 own = 0, total;
-    auto one = [&](int i) {
-      const float x = s.row.at(i);
-      return limit.has(x, i) ? weight(x) : 0ull;
-    };
-#pragma unroll 1
-    for (int i = first_id; i < end_id; ++i) own += one(i);
+    u64 y[8], own = 0, total;
+    s.weigh_unit(v + s.tid, s1, limit, y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) own += y[i];
     u64 upto = before + block_scan(own, sm.scratch, &total) - own;
     if (upto < goal && upto + own >= goal)
-#pragma unroll 1
-      for (int i = first_id; i < end_id; ++i) {
-        const u64 y = one(i);
-        if (upto < goal && upto + y >= goal) s.answer(i, s.log_of((float)y, (float)sum), (int)kept);
-        upto += y;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (upto < goal && upto + y[i] >= goal) s.answer((v + s.tid) * 8 - s.row.shift + i, s.log_of((float)y[i], (float)sum), (int)kept);
+        upto += y[i];
       }
     before += total;
     if (before >= goal) return;
