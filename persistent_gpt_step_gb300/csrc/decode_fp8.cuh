@@ -112,7 +112,10 @@ struct Fp8Path {
   static constexpr bool kTwice = kFull && kMode == 4;
   static constexpr int kParts = kFull && !kTwice ? 2 : 1;  // products for a tile
   static constexpr int kBlocks = kMode == 16 ? 1 : 2;      // of an SM
-  static constexpr int KG = DP_ == 128 ? 1 : 2, kKeys = 16 * KG, kUnit = kKeys, kUnitStart = kStart;
+  static constexpr int KG = DP_ == 128 ? 1 : 2, kKeys = 16 * KG, kUnit = kKeys;
+  // A row's start, in units: 104 ragged sequences of 8 heads of 96 28.7 us with 2, 27.2 with 3, 27.0 with 4, 27.5 with 6;
+  // 200 of 16 heads of 64 (of 32 keys a unit) 48.1 48.2 49.0 49.3, 2 of up to 60,000 and 12 heads 40.8 39.2 38.1 39.7.
+  static constexpr int kUnitStart = DP_ == 128 ? 4 : 3;
   static constexpr int KP = DP / 64;                       // a lane's 16-byte pieces of a key
   static constexpr int VW = DP / 32;                       // a lane's words of a value
   static constexpr int kQuery = NT * kParts * KP * 256;    // a warp's queries: 32 bytes per lane, tile, part and piece
@@ -484,7 +487,7 @@ struct Fp8Ring {
   using Path = Fp8Path<T, 4, DP_, true, kExact>;
   static constexpr bool kFull = std::is_same_v<T, float>, kTwice = kFull;
   static constexpr int DP = DP_, kHeads = 4, kBlocks = 2;
-  static constexpr int KP = Path::KP, VW = Path::VW, KG = Path::KG, kKeys = Path::kKeys, kUnit = kKeys, kUnitStart = kStart;
+  static constexpr int KP = Path::KP, VW = Path::VW, KG = Path::KG, kKeys = Path::kKeys, kUnit = kKeys, kUnitStart = Path::kUnitStart;
   static constexpr int kGroups = 2 * KG;                    // groups of 8 keys of a step
   static constexpr int kStages = 2, kSide = kKeys * DP;     // bytes of a stage's keys
   static constexpr int kQuery = kStages * 2 * kSide / 4;
