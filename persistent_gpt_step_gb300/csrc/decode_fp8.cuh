@@ -112,6 +112,8 @@ struct Fp8Path {
   static constexpr bool kTwice = kFull && kMode == 4;
   static constexpr int kParts = kFull && !kTwice ? 2 : 1;  // products for a tile
   static constexpr int kBlocks = kMode == 16 ? 1 : 2;      // of an SM
+  // 16-key groups of a step: two of 128 dims leave too few registers (64 ragged sequences of 32 over 8 heads 144 us for 121),
+  // two of 64 are as long as one of those (200 sequences of 16 heads 48.2 us and 49.0, 32 of 14 over 2 heads 16.1 and 17.2).
   static constexpr int KG = DP_ == 128 ? 1 : 2, kKeys = 16 * KG, kUnit = kKeys;
   // A row's start, in units: 104 ragged sequences of 8 heads of 96 28.7 us with 2, 27.2 with 3, 27.0 with 4, 27.5 with 6;
   // 200 of 16 heads of 64 (of 32 keys a unit) 48.1 48.2 49.0 49.3, 2 of up to 60,000 and 12 heads 40.8 39.2 38.1 39.7.
@@ -479,7 +481,10 @@ __device__ __forceinline__ uint2 shared8(uint32_t at) {
   return u;
 }
 
-// kSame: pages of whole 16-key groups, one scale for each of these.
+// 64 ragged sequences of 32 over 8 heads of 128 104 us (117 without the ring), 200 of 16 heads of 64 48 (61), 131,071 keys
+// 61 (67).
+// kSame: pages of whole 16-key groups, one scale for each of these (300 ragged sequences of 8 heads of 128 93.3 us, 94.1
+// with two, 64 of 32 over 8 104.5 and 105.2).
 template <typename T_, int DP_, bool kExact, bool kSame>
 struct Fp8Ring {
   using T = T_;

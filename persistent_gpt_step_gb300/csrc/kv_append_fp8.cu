@@ -17,8 +17,9 @@ namespace {
 constexpr int kMostWarps = 8;
 constexpr int kMaxStrip = 64;    // rows of a block's strip, and of the table of sines and cosines
 constexpr int kStage = 1024;     // starts in shared memory
-constexpr int kUnder = 8;        // 16-byte pieces that a thread has under way
-constexpr int kQueryUnder = 8;   // the same of queries
+// 16-byte pieces that a thread has under way: 32,768 tokens of 32 + 8 + 8 heads of 128 132 us, with 4 140, with 16
+// 175 (8,192 of 16 + 16 + 16 of 64 33 32 60); of queries 132, 137 and 217.
+constexpr int kUnder = 8, kQueryUnder = 8;
 constexpr int kNoRun = 255;
 
 struct AppendParams {
@@ -472,10 +473,10 @@ __global__ void __launch_bounds__(kMostWarps * 32, 3) kv_append_fp8_kernel(const
   if (blockIdx.x == 0 && p.a.starts)
     for (int i = threadIdx.x; i < p.c.pages.n_seq; i += blockDim.x)
       if (p.a.starts[i] > p.a.starts[i + 1] || p.a.starts[i] < 0 || p.a.starts[i + 1] > p.a.n_tokens) set_status(p.a.status, GPT_STATUS_BAD_SEQ);
-  // Blocks of both kinds in even turns: the ones wait for memory while the others compute.
-  const int before = (int)((int64_t)blockIdx.x * p.kv_blocks / gridDim.x), kv = (int)((int64_t)(blockIdx.x + 1) * p.kv_blocks / gridDim.x) - before;
-  if (kv) append_runs<T>(p, rates, stage, turns, before);
-  else turn_queries<T>(p, rates, stage, blockIdx.x - before);
+  // The longer blocks first.  (In even turns 20,000 tokens of 4 + 1 + 1 heads of 96 take 42.6 us for 29.1, 8,192 of
+  // 16 + 16 + 16 of 64 33.4 for 30.0, 32,768 of 32 + 8 + 8 of 128 131.9 for 130.3.)
+  if ((int)blockIdx.x < p.kv_blocks) append_runs<T>(p, rates, stage, turns, blockIdx.x);
+  else turn_queries<T>(p, rates, stage, blockIdx.x - p.kv_blocks);
 }
 
 // One new token of each sequence (no starts): every run is a row.  A block has a token, a warp
@@ -614,9 +615,11 @@ extern "C" int gpt_kv_append_fp8(const gpt_fp8_cache* cache, const gpt_kv_append
   const cudaStream_t st = (cudaStream_t)cuda_stream;
   const bool bf16 = c->dtype == GPT_DTYPE_BF16;
   if (!a->starts) {
-    const bool few = a->n_tokens <= 608;
-    const auto kernel = bf16 ? (few ? kv_append_fp8_step_kernel<__nv_bfloat16, 256, 3> : kv_append_fp8_step_kernel<__nv_bfloat16, 128, 6>)
-                             : (few ? kv_append_fp8_step_kernel<float, 256, 3> : kv_append_fp8_step_kernel<float, 128, 6>);
+    // A wide block for a token, all under way at once, while four fit an SM; then narrow ones, that take turns (32 + 8 + 8
+    // heads of 128 in bf16, 256 600 1,000 2,000 4,000 tokens: 5.1 6.1 10.1 18.0 32.8 us and 7.1 7.9 9.4 16.7 31.6).
+    const bool few = a->n_tokens <= 4 * 152;
+    const auto kernel = bf16 ? (few ? kv_append_fp8_step_kernel<__nv_bfloat16, 256, 6> : kv_append_fp8_step_kernel<__nv_bfloat16, 128, 3>)
+                             : (few ? kv_append_fp8_step_kernel<float, 256, 6> : kv_append_fp8_step_kernel<float, 128, 3>);
     return launch_after("gpt_kv_append_fp8", kernel, dim3((unsigned)a->n_tokens), few ? 256 : 128, 0, 0, st, p);
   }
   p.groups = (c->n_kv_head + kMostWarps - 1) / kMostWarps;

@@ -781,6 +781,45 @@ def test_sample_few_values(cuda, kind):
 
 
 @gpu
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("vocab", [4096, 20011, 131072])
+def test_sample_counts_near_list_sizes(cuda, kind, vocab):
+    """top_k around the lengths at which lists are treated in other ways, logits all apart and of a few values."""
+    rng = _rng(kind, vocab)
+    k = np.array([1, 2, 255, 256, 257, 511, 1023, 1024, 1025, 2047, 4095, vocab - 1])
+    for z in (_logits(rng, len(k), vocab), rng.integers(-4, 4, (len(k), vocab)).astype(float)):
+        _run_sample(z, rng.random(len(k)), kind, t=1.3, k=k)
+        _run_sample(z, rng.random(len(k)), kind, t=0.8, k=k, p=0.9, mp=0.001)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("vocab,t,p,mp", [(131072, 2.0, 0.9, None), (131072, 5.0, 0.6, None), (50304, 2.0, 0.97, 1e-6), (50304, 2.0, 0.97, 0.01), (9999, 1.5, 0.9, None),
+                                          (20000, 50.0, 0.5, None), (20000, 3.0, 0.99999, None), (700, 2.0, 0.95, 1e-3)])
+def test_sample_wide_nucleus(cuda, kind, vocab, t, p, mp):
+    """top_p that keeps thousands: numbers across [0, 1) give tokens of every part of the row."""
+    rng = _rng(kind, vocab, t, p)
+    z = np.repeat(_logits(rng, 2, vocab), 33, axis=0)
+    _run_sample(z, np.tile((np.arange(33) + rng.random(33)) / 33, 2), kind, t=t, p=p, mp=mp)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+def test_sample_one_value_beside_thousands(cuda, kind):
+    """One token far above, all others at or near one value: a bin with most of the row in it."""
+    rng = _rng(kind)
+    z = np.full((12, 30000), -2.0)
+    z[4:8] += 2.0 ** -7 * rng.integers(0, 2, (4, 30000))
+    z[8:] += 1e-3 * rng.random((4, 30000))
+    z[np.arange(12), rng.integers(0, 30000, 12)] = 6.0
+    for p in (0.05, 0.5, 0.999):
+        _run_sample(z, rng.random(12), kind, p=p)
+    _run_sample(z, rng.random(12), kind, k=5000)
+    _run_sample(z, rng.random(12), kind, k=5000, p=0.7)
+    _run_sample(z, rng.random(12), kind, mp=1e-5)
+
+
+@gpu
 def test_sample_edge_rows(cuda):
     inf, nan = math.inf, math.nan
     z = np.zeros((14, 40))
