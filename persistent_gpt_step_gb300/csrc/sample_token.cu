@@ -312,7 +312,7 @@ struct Shared {
     struct { int low, high; uint32_t upto; } ends;                     // (the first block's)
   };
   u64 ends_of[kWarps][2], counts[kWarps];
-  uint32_t words[3][kThreads];
+  u64 sums[kThreads];
   struct { u64 before; int bin; } crossed;
   double drop;
   uint32_t listed, gathered, base;
@@ -349,15 +349,23 @@ __device__ __noinline__ u64 block_scan(u64 v, u64* scratch, u64* total) {
   *total = sum;
   return v;
 }
+// Adds to a sum in shared memory, a word and its carry after the other: atomics of 64 bits go round there for
+// each thread that meets another (131,072 equal logits with top_p 884 us; the limits of a list of them 20 us, 4 so).
+__device__ __forceinline__ void add64(u64* sum, u64 w) {
+  uint32_t* word = reinterpret_cast<uint32_t*>(sum);
+  const uint32_t low = (uint32_t)w;
+  uint32_t high = (uint32_t)(w >> 32);
+  if (low && atomicAdd(word, low) > ~low) ++high;
+  if (high) atomicAdd(word + 1, high);
+}
 // Of the n entries of sm.all at or above `floor`, in falling order or (kById) by rising ids: the one at
 // which the running sum of their weights (kCount: of ones) reaches `goal`, which it does.  The range of
 // their keys is cut in 256 bins, and that of the bin where that happens again, until it holds one.
-// Bins' sums are in three words, for atomics of 32 bits: those of 64 go round for each thread that
-// meets another (20 us, of equal logits; 4 so).  By all threads of the block.
+// By all threads of the block.
 enum { kCount, kMass, kById };
 __device__ __noinline__ int cross(Shared& sm, int n, int by, u64 goal, u64 floor) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  static_assert(kThreads == 256 && kList <= 1024, "a bin each, words of 22 bits");
+  static_assert(kThreads == 256, "a bin each");
   auto key_of_entry = [&](u64 comp) { return by == kById ? (u64) ~(uint32_t)comp : ~comp; };
   u64 lo = 0, hi = ~0ull, before = 0;
   while (true) {
@@ -369,8 +377,7 @@ __device__ __noinline__ int cross(Shared& sm, int n, int by, u64 goal, u64 floor
     }
     first = ~warp_max(~first), last = warp_max(last);
     if (lane == 0) sm.ends_of[warp][0] = first, sm.ends_of[warp][1] = last;
-#pragma unroll
-    for (int k = 0; k < 3; ++k) sm.words[k][tid] = 0;
+    sm.sums[tid] = 0;
     __syncthreads();
     lo = ~0ull, hi = 0;
 #pragma unroll
@@ -379,17 +386,12 @@ __device__ __noinline__ int cross(Shared& sm, int n, int by, u64 goal, u64 floor
     const int shift = max(0, 56 - __clzll((long long)(hi - lo)));
 #pragma unroll 1
     for (int i = tid; i < n; i += kThreads) {
-      const u64 comp = sm.all[i], key = key_of_entry(comp), w = by == kCount ? 1 : sm.weights[i];
-      if (comp < floor || key < lo || key > hi) continue;
-      const int at = (int)((key - lo) >> shift);
-#pragma unroll
-      for (int k = 0; k < 3; ++k)
-        if ((w >> 22 * k) & 0x3fffff) atomicAdd(&sm.words[k][at], (uint32_t)(w >> 22 * k) & 0x3fffff);
+      const u64 comp = sm.all[i], key = key_of_entry(comp);
+      if (comp >= floor && key >= lo && key <= hi) add64(&sm.sums[(key - lo) >> shift], by == kCount ? 1 : sm.weights[i]);
     }
     __syncthreads();
     u64 total;
-    const u64 here = sm.words[0][tid] + ((u64)sm.words[1][tid] << 22) + ((u64)sm.words[2][tid] << 44);
-    const u64 to = before + block_scan(here, sm.scratch, &total) - here;
+    const u64 here = sm.sums[tid], to = before + block_scan(here, sm.scratch, &total) - here;
     if (to < goal && to + here >= goal) sm.crossed.before = to, sm.crossed.bin = tid;
     __syncthreads();
     before = sm.crossed.before;
@@ -896,7 +898,7 @@ struct Sampler {
       const int at = (id_of(comp) + row.shift) / 8;
       int w = 0;
       while (w < kWarps - 1 && at >= warp_begin(w + 1)) ++w;
-      atomicAdd(&sm.parts[w], weight(value_of((uint32_t)(comp >> 32)))), atomicAdd(&sm.counts[w], 1ull);
+      add64(&sm.parts[w], weight(value_of((uint32_t)(comp >> 32)))), add64(&sm.counts[w], 1);
     }
     __syncthreads();
     return kDrawn;
@@ -1016,7 +1018,7 @@ __device__ __noinline__ void slow_row(const SampleParams& p, Shared& sm, bool al
           weight.eight(x, w);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (at[i] >= 0 && w[i]) atomicAdd(&sm.bins.mass[at[i]], w[i]);
+            if (at[i] >= 0 && w[i]) add64(&sm.bins.mass[at[i]], w[i]);
         }
       });
       s.sync_all();  // (the first block's bins have been cleared and filled)
