@@ -10,8 +10,10 @@
 //  - values: the weights, times the value scale of their page over the largest one so far,
 //    enter as fp16 numbers below 2^15 (their reference lies 7 under the maximum, so that what
 //    falls under fp16's smallest number is 2^-32 of the largest), for fp32 results as two parts.
-// Bound: HBM, half the bytes of a bf16 cache; the conversions (a number of a key and a value
-// each, two at a time) are the pipe that is busiest beside it.
+// Bound: HBM, half the bytes of a bf16 cache, and the instructions beside it: 322 for 16 keys of 128
+// dims, of these 64 conversions, 16 products and 109 on addresses and masks, and 1,900 for a row's
+// start and end (64 ragged sequences of 32 over 8 heads of 128 104 us, 5.2 TB/s; 131,071 keys 61 us,
+// 4.4 TB/s; 200 sequences of 16 heads of 64 48 us, 4.4 TB/s).
 #pragma once
 #include "decode_attention.cuh"
 

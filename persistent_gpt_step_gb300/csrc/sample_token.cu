@@ -21,6 +21,10 @@
 //  - with top_p alone: by_sums;
 //  - where a list does not hold what it must: slow_row, bins of counts and sums of all tokens, as
 //    many rounds as it takes, then the sums of the kept ones by warp.
+// Bound: a few rows by the chain of phases, 1 to 2 us each with a barrier of the cluster (1 row of
+// 12,288: 7.7 us without limits, 13 with; 64 of 50,304 15, 21, with top_p alone 40); many by
+// instructions (512 of 131,072 in fp32 without limits 88 us, 3.0 TB/s, 27 instructions a token; with
+// top_p alone 298).
 #include <cooperative_groups.h>
 
 #include <cmath>
