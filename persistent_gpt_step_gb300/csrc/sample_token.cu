@@ -287,7 +287,7 @@ struct RowView {
 struct Kept {
   float z;
   int id;
-  __device__ __forceinline__ explicit Kept(u64 last) : z(last > 1 ? value_of((uint32_t)(last >> 32)) : -INFINITY), id(last > 1 ? id_of(last) : -1) {}
+  __device__ __forceinline__ explicit Kept(u64 last) : z(last > 1 ? value_of((uint32_t)(last >> 32)) : -INFINITY), id(last > 1 ? id_of(last) : INT32_MIN) {}  // (not what a unit holds before the row's first token)
   __device__ __forceinline__ bool has(float x, int i) const { return x > z || (x == z && i <= id); }
   __device__ __forceinline__ bool none(const float* x) const {  // of eight
     return !(max_of(x) >= z);

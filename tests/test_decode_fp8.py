@@ -871,6 +871,22 @@ def test_sample_strides(cuda, kind, offset, width):
 
 
 @gpu
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("vocab", [1, 54, 1821, 13395])
+def test_sample_number_zero_in_rows_off_boundaries(cuda, kind, vocab):
+    """Rows that begin anywhere between boundaries of eight logits; the number 0 lies at a border, and half the tokens
+    of some rows are not there."""
+    rng = _rng(kind, vocab)
+    z = _logits(rng, 24, vocab)
+    z[8:16, 1::2] = -np.inf
+    u = np.where(np.arange(24) % 3 < 2, 0.0, 0.7)
+    _run_sample(z, u, kind)
+    for k in (vocab // 2, (vocab + 1) // 2 + 2, vocab - 1):
+        _run_sample(z, u, kind, t=3.0, k=max(k, 1))
+        _run_sample(z, u, kind, t=3.0, k=max(k, 1), p=0.9999)
+
+
+@gpu
 def test_sample_rows_past_32_bits(cuda):
     rng = _rng(9)
     wide = torch.empty(3, (1 << 31) + 64, dtype=torch.bfloat16, device="cuda")
