@@ -10,13 +10,15 @@
 // sqrt 2: it is then exact, the same however sines are rounded, and no number reaches 448.
 // Bound: HBM (rows read once, numbers and rotated queries written once): 32,768 tokens of 32 + 8 + 8
 // heads of 128 in bf16 130 us, 5.7 TB/s; a few thousand tokens by the chain of loads and the sines
-// (4,095 of 12 + 12 + 12 of 64 in fp32 20 us, 2.8 TB/s).
+// (4,095 of 12 + 12 + 12 of 64 in fp32 16 us, 3.5 TB/s).
 #include "rotary.h"
 
 namespace pgs {
 namespace {
 
-constexpr int kMostWarps = 8;
+// Of a block, a head each; two such blocks fit an SM.  (4,095 tokens of 12 + 12 + 12 heads of 64 in fp32: 16.4 us, with 4,
+// 8 and 16 at the same warps of an SM 23.0, 20.0, 25.0; 8 heads of 128: 130.5 with 8 or 12, 164 with 4.)
+constexpr int kMostWarps = 12;
 constexpr int kMaxStrip = 64;    // rows of a block's strip, and of the table of sines and cosines
 constexpr int kStage = 1024;     // starts in shared memory
 // 16-byte pieces that a thread has under way: 32,768 tokens of 32 + 8 + 8 heads of 128 132 us, with 4 140, with 16
@@ -467,7 +469,7 @@ __device__ __forceinline__ void begin_block(const AppendParams& p, RotaryRates& 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kMostWarps * 32, 3) kv_append_fp8_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kMostWarps * 32, 2) kv_append_fp8_kernel(const __grid_constant__ AppendParams p) {
   extern __shared__ __align__(16) float2 turns[];  // [kMaxStrip][kMaxPairs] cosine, sine
   __shared__ int stage[kStage];
   __shared__ RotaryRates rates;
