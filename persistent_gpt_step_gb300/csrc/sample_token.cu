@@ -22,8 +22,8 @@
 //  - where a list does not hold what it must: slow_row, bins of counts and sums of all tokens, as
 //    many rounds as it takes, then the sums of the kept ones by warp.
 // Bound: a few rows by the chain of phases, 1 to 2 us each with a barrier of the cluster (1 row of
-// 12,288: 7.7 us without limits, 13 with; 64 of 50,304 15, 21, with top_p alone 40); many by
-// instructions (512 of 131,072 in fp32 without limits 88 us, 3.0 TB/s, 27 instructions a token; with
+// 12,288: 7.6 us without limits, 13 with; 64 of 50,304 15, 21, with top_p alone 40); many by
+// instructions (512 of 131,072 in fp32 without limits 90 us, 3.0 TB/s, 27 instructions a token; with
 // top_p alone 298).
 #include <cooperative_groups.h>
 
@@ -46,7 +46,7 @@ constexpr int kList = 1024;
 // 12,288 with a top_k of up to 200: 13.6 us, and 17.6 through bins; 512 of 131,072: 119 and 133.)
 constexpr int kShort = kThreads;
 constexpr int kTable = 1024;
-constexpr int kPieces = 4;        // of a warp's range, where sums are in fp32
+constexpr int kPieces = 2;        // of a warp's range, where sums are in fp32 (with 4 a row of 131,072 10.4 us, 9.7 so)
 using u64 = unsigned long long;
 
 struct SampleParams {
@@ -606,13 +606,14 @@ struct Sampler {
     f.start(c_hi, c_lo);
     const int each = piece_units(w1 - w0);
     {
+      constexpr int kTurns = sizeof(T) == 2 ? 2 : 1;  // (512 rows of 131,072 in bf16 80 us, one at a time 86; in fp32 92 both)
       Unit<T> x;
       if (w0 + lane < w1) row.load(w0 + lane, x);
 #pragma unroll 1
       for (int k = 0; k < kPieces; ++k) {
         const int end = min(w1, w0 + (k + 1) * each);
         f.clear();
-#pragma unroll 1
+#pragma unroll(kTurns)
         for (int w = w0 + k * each + lane; w < end; w += 32) {
           Unit<T> next;
           float y[8];
@@ -641,14 +642,14 @@ struct Sampler {
         const float x = power(min(up, 0)), y = power(max(up, 0));
         return (u64)(__float2ll_rn(piece.sum * x * y) + __float2ll_rn(piece.rest * x * y));
       };
-      static_assert(kWarps * kPieces == 32, "a lane each");
-      u64 upto = whole(sm.pieces[lane]);
+      static_assert(kWarps * kPieces <= 32, "a lane each");
+      u64 upto = lane < kWarps * kPieces ? whole(sm.pieces[lane]) : 0;
 #pragma unroll
       for (int y = 1; y < 32; y <<= 1) {
         const u64 t = __shfl_up_sync(0xffffffffu, upto, y);
         if (lane >= y) upto += t;
       }
-      sm.pieces[lane].upto = upto;
+      if (lane < kWarps * kPieces) sm.pieces[lane].upto = upto;
       sum = __shfl_sync(0xffffffffu, upto, 31);
     }
     if (blocks > 1) asm volatile("barrier.cluster.wait;" ::: "memory");
