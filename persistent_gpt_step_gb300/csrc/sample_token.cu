@@ -677,9 +677,9 @@ struct Sampler {
     const u64 goal = u >= 1.f ? all : u > 0.f ? part_of(u, all, false) : 0;
     // The piece in which the number falls, surely.  Sums are off by 2^-21 of themselves and some units: one
     // from the row's start, S, less the number's share u of the whole one, W, by
-    // |(1 - u) dS - u d(W - S)| <= 2^-21 ((1 - u) S + u (W - S)).
+    // |(1 - u) dS - u d(W - S)| <= 2^-21 ((1 - u) S + u (W - S)); the weights as integers by half a unit each.
     auto off_by = [&](u64 from) {
-      return (u64)(((float)from * (1.f - u) + (float)(all - min(from, all)) * u) * (0x1p-21f * (1.f + 0x1p-18f))) + 256;
+      return (u64)(((float)from * (1.f - u) + (float)(all - min(from, all)) * u) * (0x1p-21f * (1.f + 0x1p-18f))) + 256 + a.vocab;
     };
     if (tid == 0) sm.fast.piece = -1;
     __syncthreads();
