@@ -521,8 +521,8 @@ int gpt_kv_append_fp8(const gpt_fp8_cache* cache, const gpt_kv_append_fp8_args* 
  * arguments, q and out of type pages.dtype; strides of the scales may be 0: one scale
  * for all).  A NaN among the values of a key that counts is in the result however
  * small the key's weight is.  Weights, each times its page's value scale, enter the
- * product with the values as fp16 numbers (two of them for fp32 outputs), down to 2^-32 of
- * the largest of these; sums are fp32.
+ * product with the values as two fp16 parts (2^-22), down to 2^-32 of the largest of
+ * these; sums are fp32.
  */
 int gpt_decode_attention_fp8(const gpt_fp8_cache* cache, const gpt_decode_attention_args* args, void* cuda_stream);
 

@@ -8,8 +8,8 @@
 //    a power of two of its own (what falls under 2^-25 there is 2^-39 of its largest): bf16
 //    queries are then exact, fp32 ones enter as two fp16 parts (2^-23).
 //  - values: the weights, times the value scale of their page over the largest one so far,
-//    enter as fp16 numbers below 2^15 (their reference lies 7 under the maximum, so that what
-//    falls under fp16's smallest number is 2^-32 of the largest), for fp32 results as two parts.
+//    enter as two fp16 parts (2^-22 left over) below 2^15 (their reference lies 7 under the
+//    maximum, so that what falls under fp16's smallest number is 2^-32 of the largest).
 // Bound: HBM, half the bytes of a bf16 cache, and the instructions beside it: 322 for 16 keys of 128
 // dims, of these 64 conversions, 16 products and 109 on addresses and masks, and 1,900 for a row's
 // start and end (64 ragged sequences of 32 over 8 heads of 128 104 us, 5.2 TB/s; 131,071 keys 61 us,
@@ -40,8 +40,13 @@ __device__ __forceinline__ float2 unpack2_f16(uint32_t u) {
   asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(x.x), "=f"(x.y) : "r"(u));
   return x;
 }
-// What two numbers leave over of their fp16 parts; nothing of an infinity.
+// What two numbers leave over of their fp16 parts.
 __device__ __forceinline__ uint32_t rest2_f16(float lo, float hi, uint32_t parts) {
+  const float2 x = unpack2_f16(parts);
+  return pack2_f16(lo - x.x, hi - x.y);
+}
+// The same, nothing of an infinity.
+__device__ __forceinline__ uint32_t finite_rest2_f16(float lo, float hi, uint32_t parts) {
   const float2 x = unpack2_f16(parts);
   return pack2_f16(fabsf(x.x) == INFINITY ? 0.f : lo - x.x, fabsf(x.y) == INFINITY ? 0.f : hi - x.y);
 }
@@ -103,16 +108,16 @@ struct ScaledWalk {
   }
 };
 
-// kMode: query heads of a row.  fp32 with 4: columns 4..7 of the products take the low parts
-// of queries and weights; with 8: products of their own.  bf16: 8, or 16 in two tiles.
+// kMode: query heads of a row, 16 of them in two tiles.  With 4, columns 4..7 of the products take
+// the low parts of weights and fp32 queries (and bf16 ones once more); otherwise products of their own do.
 template <typename T_, int kMode, int DP_, bool kFast, bool kExact>
 struct Fp8Path {
   using T = T_;
   using Cache = E4m3;
   static constexpr bool kFull = std::is_same_v<T, float>;
   static constexpr int NT = kMode == 16 ? 2 : 1, DP = DP_, kHeads = kMode;
-  static constexpr bool kTwice = kFull && kMode == 4;
-  static constexpr int kParts = kFull && !kTwice ? 2 : 1;  // products for a tile
+  static constexpr bool kTwice = kMode == 4;
+  static constexpr int kParts = kFull && !kTwice ? 2 : 1;  // of a query, a product each
   static constexpr int kBlocks = kMode == 16 ? 1 : 2;      // of an SM
   // 16-key groups of a step: two of 128 dims leave too few registers (64 ragged sequences of 32 over 8 heads 144 us for 121),
   // two of 64 are as long as one of those (200 sequences of 16 heads 48.2 us and 49.0, 32 of 14 over 2 heads 16.1 and 17.2).
@@ -132,7 +137,7 @@ struct Fp8Path {
   template <typename Put>
   static __device__ __forceinline__ float read_query(const DecodeParams& p, const Part& w, int t, Put put) {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const int qh = kTwice || kMode == 4 ? r & 3 : t * 8 + r;
+    const int qh = kTwice ? r & 3 : t * 8 + r;
     constexpr int kN = Piece<T>::kN, kLoads = 16 / kN;
     uint4 u[KP][kLoads];
 #pragma unroll
@@ -168,8 +173,8 @@ struct Fp8Path {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           h[k] = pack2_f16(x[2 * k], x[2 * k + 1]);
-          if (kFull) l[k] = rest2_f16(x[2 * k], x[2 * k + 1], h[k]);
-          if (kTwice && r >= 4) h[k] = l[k];
+          if (kFull) l[k] = finite_rest2_f16(x[2 * k], x[2 * k + 1], h[k]);
+          if (kFull && kTwice && r >= 4) h[k] = l[k];
         }
         put(0, i, half, make_uint4(h[0], h[1], h[2], h[3]));
         if (kParts == 2) put(1, i, half, make_uint4(l[0], l[1], l[2], l[3]));
@@ -364,7 +369,7 @@ struct Fp8Path {
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if (kTwice) z[g][t][i] += __shfl_xor_sync(0xffffffffu, z[g][t][i], 2);
+            if (kFull && kTwice) z[g][t][i] += __shfl_xor_sync(0xffffffffu, z[g][t][i], 2);
             z[g][t][i] *= factor[t][i & 1] * key_scale[g][i >> 1] * p.scale2;
           }
       if (__builtin_expect(there != 0xffffffffu, 0)) {
@@ -420,11 +425,11 @@ struct Fp8Path {
           float p2 = exp2_fast(z[g][t][2] - m0), p3 = exp2_fast(z[g][t][3] - m1);
           l[t][0] += p0 + p2, l[t][1] += p1 + p3;
           p0 *= bring[g][0], p1 *= bring[g][0], p2 *= bring[g][1], p3 *= bring[g][1];
-          uint32_t ha = pack2_f16(p0, p1), hb = pack2_f16(p2, p3), la = 0u, lb = 0u;
-          if (kFull) la = rest2_f16(p0, p1, ha), lb = rest2_f16(p2, p3, hb);
+          uint32_t ha = pack2_f16(p0, p1), hb = pack2_f16(p2, p3);
+          const uint32_t la = rest2_f16(p0, p1, ha), lb = rest2_f16(p2, p3, hb);
           if (kTwice) ha = c < 2 ? ha : la, hb = c < 2 ? hb : lb;
           h0[t] = transpose8(ha), h1[t] = transpose8(hb);
-          if (kParts == 2) l0[t] = transpose8(la), l1[t] = transpose8(lb);
+          if (!kTwice) l0[t] = transpose8(la), l1[t] = transpose8(lb);
         }
 #pragma unroll
         for (int b = 0; b < VW; ++b)
@@ -436,7 +441,7 @@ struct Fp8Path {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               mma16816_f16(o[t][b][i], a0, a1, a2, a3, h0[t], h1[t]);
-              if (kParts == 2) mma16816_f16(o[t][b][i], a0, a1, a2, a3, l0[t], l1[t]);
+              if (!kTwice) mma16816_f16(o[t][b][i], a0, a1, a2, a3, l0[t], l1[t]);
             }
           }
       }
@@ -492,7 +497,7 @@ struct Fp8Ring {
   using T = T_;
   using Cache = E4m3;
   using Path = Fp8Path<T, 4, DP_, true, kExact>;
-  static constexpr bool kFull = std::is_same_v<T, float>, kTwice = kFull;
+  static constexpr bool kFull = std::is_same_v<T, float>;
   static constexpr int DP = DP_, kHeads = 4, kBlocks = 2;
   static constexpr int KP = Path::KP, VW = Path::VW, KG = Path::KG, kKeys = Path::kKeys, kUnit = kKeys, kUnitStart = Path::kUnitStart;
   static constexpr int kGroups = 2 * KG;                    // groups of 8 keys of a step
@@ -648,7 +653,7 @@ struct Fp8Ring {
       for (int g = 0; g < KG; ++g)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (kTwice) z[g][i] += __shfl_xor_sync(0xffffffffu, z[g][i], 2);
+          if (kFull) z[g][i] += __shfl_xor_sync(0xffffffffu, z[g][i], 2);
           z[g][i] *= factor[i & 1] * ks[g][i >> 1];
         }
       if (__builtin_expect(!whole, 0)) {
@@ -694,12 +699,9 @@ struct Fp8Ring {
         l[0] += p0 + p2, l[1] += p1 + p3;
         const float b0 = vs[g][0] * unit_inv, b1 = vs[g][1] * unit_inv;
         p0 *= b0, p1 *= b0, p2 *= b1, p3 *= b1;
-        uint32_t ha = pack2_f16(p0, p1), hb = pack2_f16(p2, p3);
-        if (kTwice) {
-          const uint32_t la = rest2_f16(p0, p1, ha), lb = rest2_f16(p2, p3, hb);
-          ha = c < 2 ? ha : la, hb = c < 2 ? hb : lb;
-        }
-        const uint32_t h0 = transpose8(ha), h1 = transpose8(hb);
+        const uint32_t ha = pack2_f16(p0, p1), hb = pack2_f16(p2, p3);
+        const uint32_t la = rest2_f16(p0, p1, ha), lb = rest2_f16(p2, p3, hb);
+        const uint32_t h0 = transpose8(c < 2 ? ha : la), h1 = transpose8(c < 2 ? hb : lb);
 #pragma unroll
         for (int b = 0; b < VW; ++b)
 #pragma unroll
@@ -723,7 +725,7 @@ struct Fp8Ring {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           y[b][i] = o[b][i >> 1][e + 2 * (i & 1)];
-          if (kTwice) y[b][i] += __shfl_xor_sync(0xffffffffu, y[b][i], 2);
+          y[b][i] += __shfl_xor_sync(0xffffffffu, y[b][i], 2);
           y[b][i] *= unit;
         }
       Path::finish(p, w, qh, m[e], total, y);

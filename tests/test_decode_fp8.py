@@ -528,6 +528,25 @@ def test_attention_scales_far_apart(cuda, kind, page):
 
 
 @gpu
+@pytest.mark.parametrize("reach", [0, 400000])
+@pytest.mark.parametrize("page", [16, 8, 5])
+@pytest.mark.parametrize("heads,dim", [(4, 64), (3, 128), (8, 64), (7, 128), (16, 64), (17, 96)])
+def test_attention_rounds_bf16_results_once(cuda, heads, dim, page, reach):
+    """Results in bf16 are those in fp32 and one rounding: half a step of the binade.  (Small scores, so that
+    their own errors do not hide what the weights lose.)"""
+    rng = _rng(heads, dim, page)
+    lens, scale = [1, 2, 3, 5, 9, 30, 70], 2.0 ** -8
+    table, n_pages = _pages(rng, lens, page, width=-(-reach // page))
+    cache = _pool8(rng, n_pages, page, 1, dim, "slot")
+    parts = _fill8(rng, lens, table, page, cache)
+    q = _t(rng.standard_normal((len(lens), heads, dim)), "bf16")
+    out, _ = B.decode_attention_fp8(q, *cache, _i(table), _i(lens), scale=scale)
+    for s, (k, v) in enumerate(parts):
+        want, _, tol, _ = _attention8(_np(q)[s], k, v, scale, "fp32")
+        _check(out[s], want, tol + 2.0 ** (np.floor(np.log2(np.abs(want) + tol)) - 8))
+
+
+@gpu
 @pytest.mark.parametrize("kind", ["fp32", "bf16"])
 def test_attention_strided_and_scaled(cuda, kind):
     _run_attention8(_rng(kind), [70, 0, 9], 6, 2, 64, 16, kind, "gaps", scale=0.3, strided=True)
