@@ -522,7 +522,7 @@ int gpt_kv_append_fp8(const gpt_fp8_cache* cache, const gpt_kv_append_fp8_args* 
  * for all).  A NaN among the values of a key that counts is in the result however
  * small the key's weight is.  Weights, each times its page's value scale, enter the
  * product with the values as two fp16 parts (2^-22), down to 2^-32 of the largest of
- * these; sums are fp32.
+ * these; weights below 2^-119 of the largest may count as nothing; sums are fp32.
  */
 int gpt_decode_attention_fp8(const gpt_fp8_cache* cache, const gpt_decode_attention_args* args, void* cuda_stream);
 

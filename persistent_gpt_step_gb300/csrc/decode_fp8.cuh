@@ -7,9 +7,12 @@
 //    memory; the key scale of a page multiplies the score.  A query is brought below 2^15 by
 //    a power of two of its own (what falls under 2^-25 there is 2^-39 of its largest): bf16
 //    queries are then exact, fp32 ones enter as two fp16 parts (2^-23).
-//  - values: the weights, times the value scale of their page over the largest one so far,
-//    enter as two fp16 parts (2^-22 left over) below 2^15 (their reference lies 7 under the
-//    maximum, so that what falls under fp16's smallest number is 2^-32 of the largest).
+//  - values: the weights, each times the value scale of its page, enter as two fp16 parts (2^-22
+//    left over) below 2^15.  Scales may lie further apart than fp16 reaches, and a key of the
+//    largest weight in a page of a small one, so that these products have a reference of their
+//    own beside the weights': 9 under a bound of their largest that is at most two above it, so
+//    that what falls under fp16's smallest number is 2^-32 of the largest product.  Both are
+//    integers, and what brings weights from one to the other a power of two.
 // Bound: HBM, half the bytes of a bf16 cache, and the instructions beside it: 322 for 16 keys of 128
 // dims, of these 64 conversions, 16 products and 109 on addresses and masks, and 1,900 for a row's
 // start and end (64 ragged sequences of 32 over 8 heads of 128 104 us, 5.2 TB/s; 131,071 keys 61 us,
@@ -55,6 +58,10 @@ __device__ __forceinline__ uint2 load8(const void* p) {
   asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(u.x), "=r"(u.y) : "l"(p));
   return u;
 }
+
+__device__ __forceinline__ float power2(int n) { return __uint_as_float((uint32_t)(n + 127) << 23); }
+// log2 of a scale is below this (0: -126).
+__device__ __forceinline__ float log2_above(float scale) { return (float)((int)(__float_as_uint(scale) >> 23) - 126); }
 
 // As Walk, with the scales of each group's (or key's) page: table entries are read two
 // rounds ahead, the scales one.
@@ -191,6 +198,30 @@ struct Fp8Path {
     });
   }
 
+  // What a weight is multiplied by; finite, so that nothing is left of a weight of zero.
+  static __device__ __forceinline__ float bring(float scale, float rate) { return fminf(scale * rate, 0x1.fffffep127f); }
+
+  // New references of a column from its largest score, and bound of a product's log2, best and best_w of
+  // a lane; m, mw, rate, l and o as in run.
+  static __device__ __forceinline__ void move(float best, float best_w, float& m, float& mw, float& rate, float& l, float (&o)[VW][2][4], int e) {
+    best = fmaxf(best, m + 7.f), best_w = fmaxf(best_w, mw + 9.f);
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) {
+      best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, x));
+      best_w = fmaxf(best_w, __shfl_xor_sync(0xffffffffu, best_w, x));
+    }
+    best = ceilf(best) - 7.f, best_w = ceilf(best_w) - 9.f;
+    const float keep = weight(m, best), n = fminf(fmaxf(best - best_w, -126.f), 126.f);
+    const int more = (int)n - ((int)(__float_as_uint(rate) >> 23) - 127);
+    const float keep_w = keep * power2(more / 2) * power2(more - more / 2);
+    m = best, mw = best - n, rate = power2((int)n);
+    l *= keep;
+#pragma unroll
+    for (int b = 0; b < VW; ++b)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) o[b][i][e] *= keep_w, o[b][i][e + 2] *= keep_w;
+  }
+
   // What lane (r, c) has of query head qh: reference, sum of weights, its dims of their values' sum.
   static __device__ __forceinline__ void finish(const DecodeParams& p, const Part& w, int qh, float m, float total, float (&y)[VW][4]) {
     const int r = (threadIdx.x & 31) >> 2;
@@ -222,16 +253,16 @@ struct Fp8Path {
     const uint8_t* kb = (const uint8_t*)p.c.k + (kFast ? r * row : 0);
     const uint8_t* vb = (const uint8_t*)p.c.v + r * 4 * VW + (kFast ? 2 * c * row : 0);
     uint4* query = reinterpret_cast<uint4*>(mine) + lane;
-    float o[NT][VW][2][4], m[NT][2], l[NT][2], factor[NT][2];
+    // m, mw: references of the weights, and of their products with scales; rate: 2^(m - mw)
+    float o[NT][VW][2][4], m[NT][2], mw[NT][2], rate[NT][2], l[NT][2], factor[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      m[t][0] = m[t][1] = -INFINITY, l[t][0] = l[t][1] = 0.f;
+      m[t][0] = m[t][1] = mw[t][0] = mw[t][1] = -INFINITY, rate[t][0] = rate[t][1] = 1.f, l[t][0] = l[t][1] = 0.f;
 #pragma unroll
       for (int b = 0; b < VW; ++b)
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[t][b][i / 4][i % 4] = 0.f;
     }
-    float unit = 0x1p-126f, unit_inv = 0x1p126f;  // of the values' sums
     uint4 kr[KG][2][KP];
     uint32_t vr[KG][4][VW];
     using Keys = ScaledWalk<kFast, kKeys>;
@@ -311,26 +342,12 @@ struct Fp8Path {
       } else {
         there = __ballot_sync(0xffffffffu, off[0][0] >= 0);
       }
-      // the step's scales: of the scores; what brings weights to the sums' unit, which is the largest so far
-      float key_scale[KG][2], bring[KG][2];
-      float top = 0.f;
+      // the step's scales, and the largest of the values'
+      float key_scale[KG][2], value_scale[KG][2], top = 0.f;
 #pragma unroll
-      for (int g = 0; g < KG; ++g) key_scale[g][0] = ks[g][0], key_scale[g][1] = ks[g][1], top = fmaxf(top, fmaxf(vs[g][0], vs[g][1]));
-      if constexpr (!kFast)
+      for (int g = 0; g < KG; ++g)
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      if (top > unit) {
-        const float keep = unit / top;
-        unit = top, unit_inv = 1.f / top;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int b = 0; b < VW; ++b)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[t][b][i / 4][i % 4] *= keep;
-      }
-#pragma unroll
-      for (int g = 0; g < KG; ++g) bring[g][0] = vs[g][0] * unit_inv, bring[g][1] = vs[g][1] * unit_inv;
+        for (int u = 0; u < 2; ++u) key_scale[g][u] = ks[g][u], value_scale[g][u] = vs[g][u], top = fmaxf(top, vs[g][u]);
       advance();
       // scores: 16 keys x 8 columns a tile
       float z[KG][NT][4];
@@ -388,31 +405,29 @@ struct Fp8Path {
                 for (int b = 0; b < VW; ++b) vr[g][u][b] = 0u;
         }
       }
-      // softmax: the reference of a head moves only when a score passes the maximum by 2^8
+      // softmax: the references of a head move only when a weight, or its product with a scale, could pass 2^15
       bool move = false;
+      const float above = log2_above(top);
 #pragma unroll
-      for (int g = 0; g < KG; ++g)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-          move |= fmaxf(z[g][t][0], z[g][t][2]) > m[t][0] + 15.f || fmaxf(z[g][t][1], z[g][t][3]) > m[t][1] + 15.f;
+        for (int e = 0; e < 2; ++e) {
+          const float most = fminf(m[t][e], mw[t][e] - above) + 15.f;
+#pragma unroll
+          for (int g = 0; g < KG; ++g) move |= fmaxf(z[g][t][e], z[g][t][e + 2]) > most;
+        }
       if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = m[t][e] + 7.f;
+            float best = -INFINITY, best_w = -INFINITY;
 #pragma unroll
-            for (int g = 0; g < KG; ++g) top = fmaxf(top, fmaxf(z[g][t][e], z[g][t][e + 2]));
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-            top -= 7.f;
-            const float keep = weight(m[t][e], top);
-            m[t][e] = top;
-            l[t][e] *= keep;
-#pragma unroll
-            for (int b = 0; b < VW; ++b)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) o[t][b][i][e] *= keep, o[t][b][i][e + 2] *= keep;
+            for (int g = 0; g < KG; ++g) {
+              best = fmaxf(best, fmaxf(z[g][t][e], z[g][t][e + 2]));
+              best_w = fmaxf(best_w, fmaxf(z[g][t][e] + log2_above(value_scale[g][0]), z[g][t][e + 2] + log2_above(value_scale[g][1])));
+            }
+            Fp8Path::move(best, best_w, m[t][e], mw[t][e], rate[t][e], l[t][e], o[t], e);
           }
       }
 #pragma unroll
@@ -420,11 +435,12 @@ struct Fp8Path {
         uint32_t h0[NT], h1[NT], l0[NT], l1[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const float m0 = m[t][0] == -INFINITY ? 0.f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+          const float m0 = fmaxf(m[t][0], -0x1.fffffep127f), m1 = fmaxf(m[t][1], -0x1.fffffep127f);
           float p0 = exp2_fast(z[g][t][0] - m0), p1 = exp2_fast(z[g][t][1] - m1);
           float p2 = exp2_fast(z[g][t][2] - m0), p3 = exp2_fast(z[g][t][3] - m1);
           l[t][0] += p0 + p2, l[t][1] += p1 + p3;
-          p0 *= bring[g][0], p1 *= bring[g][0], p2 *= bring[g][1], p3 *= bring[g][1];
+          p0 *= bring(value_scale[g][0], rate[t][0]), p1 *= bring(value_scale[g][0], rate[t][1]);
+          p2 *= bring(value_scale[g][1], rate[t][0]), p3 *= bring(value_scale[g][1], rate[t][1]);
           uint32_t ha = pack2_f16(p0, p1), hb = pack2_f16(p2, p3);
           const uint32_t la = rest2_f16(p0, p1, ha), lb = rest2_f16(p2, p3, hb);
           if (kTwice) ha = c < 2 ? ha : la, hb = c < 2 ? hb : lb;
@@ -461,7 +477,7 @@ struct Fp8Path {
           for (int i = 0; i < 4; ++i) {
             y[b][i] = o[t][b][i >> 1][e + 2 * (i & 1)];
             if (kTwice) y[b][i] += __shfl_xor_sync(0xffffffffu, y[b][i], 2);
-            y[b][i] *= unit;
+            y[b][i] *= 1.f / rate[t][e];
           }
         finish(p, w, qh, m[t][e], total, y);
       }
@@ -526,14 +542,12 @@ struct Fp8Ring {
     const uint32_t val0 = ring + kSide + (DP == 128 ? 2 * c * 128 + (r ^ (2 * c)) * 16 : c * 128 + ((r >> 1) ^ (c * 2)) * 16 + (r & 1) * 8);
     const uint32_t val1 = ring + kSide + (DP == 128 ? (2 * c + 1) * 128 + (r ^ (2 * c + 1)) * 16 : c * 128 + ((4 + (r >> 1)) ^ (c * 2)) * 16 + (r & 1) * 8);
 
-    float o[VW][2][4], m[2], l[2], factor[2];
-    m[0] = m[1] = -INFINITY, l[0] = l[1] = 0.f;
-    float base[2] = {0.f, 0.f}, limit[2] = {-INFINITY, -INFINITY};  // m where it is finite; where it moves
+    float o[VW][2][4], m[2], mw[2], rate[2], l[2], factor[2];
+    m[0] = m[1] = mw[0] = mw[1] = -INFINITY, rate[0] = rate[1] = 1.f, l[0] = l[1] = 0.f;
 #pragma unroll
     for (int b = 0; b < VW; ++b)
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[b][i / 4][i % 4] = 0.f;
-    float unit = 0x1p-126f, unit_inv = 0x1p126f;  // of the values' sums
     // Rounds of 32 groups, one a lane: offsets (in 16 bytes) and scales of this one, offsets of the
     // next, of which groups are there, a bit each.
     using Keys = ScaledWalk<true, kKeys>;
@@ -624,14 +638,6 @@ struct Fp8Ring {
       }
       j += kGroups;
       if (j == 32) turn(), j = 0;
-      if (top > unit) {
-        const float keep = unit / top;
-        unit = top, unit_inv = 1.f / top;
-#pragma unroll
-        for (int b = 0; b < VW; ++b)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[b][i / 4][i % 4] *= keep;
-      }
       // scores
       float z[KG][4];
 #pragma unroll
@@ -669,36 +675,35 @@ struct Fp8Ring {
               for (int b = 0; b < VW; ++b) vr[g][u][b] = 0u;
         }
       }
-      // softmax: the reference of a head moves only when a score passes the maximum by 2^8
+      // softmax: as above
       bool move = false;
+      const float above = log2_above(top);
 #pragma unroll
-      for (int g = 0; g < KG; ++g) move |= fmaxf(z[g][0], z[g][2]) > limit[0] || fmaxf(z[g][1], z[g][3]) > limit[1];
+      for (int e = 0; e < 2; ++e) {
+        const float most = fminf(m[e], mw[e] - above) + 15.f;
+#pragma unroll
+        for (int g = 0; g < KG; ++g) move |= fmaxf(z[g][e], z[g][e + 2]) > most;
+      }
       if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float best = m[e] + 7.f;
+          float best = -INFINITY, best_w = -INFINITY;
 #pragma unroll
-          for (int g = 0; g < KG; ++g) best = fmaxf(best, fmaxf(z[g][e], z[g][e + 2]));
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, x));
-          best -= 7.f;
-          const float keep = weight(m[e], best);
-          m[e] = best;
-          base[e] = best == -INFINITY ? 0.f : best, limit[e] = best + 15.f;
-          l[e] *= keep;
-#pragma unroll
-          for (int b = 0; b < VW; ++b)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) o[b][i][e] *= keep, o[b][i][e + 2] *= keep;
+          for (int g = 0; g < KG; ++g) {
+            best = fmaxf(best, fmaxf(z[g][e], z[g][e + 2]));
+            best_w = fmaxf(best_w, fmaxf(z[g][e] + log2_above(vs[g][0]), z[g][e + 2] + log2_above(vs[g][1])));
+          }
+          Path::move(best, best_w, m[e], mw[e], rate[e], l[e], o, e);
         }
       }
+      const float m0 = fmaxf(m[0], -0x1.fffffep127f), m1 = fmaxf(m[1], -0x1.fffffep127f);
 #pragma unroll
       for (int g = 0; g < KG; ++g) {
-        float p0 = exp2_fast(z[g][0] - base[0]), p1 = exp2_fast(z[g][1] - base[1]);
-        float p2 = exp2_fast(z[g][2] - base[0]), p3 = exp2_fast(z[g][3] - base[1]);
+        float p0 = exp2_fast(z[g][0] - m0), p1 = exp2_fast(z[g][1] - m1);
+        float p2 = exp2_fast(z[g][2] - m0), p3 = exp2_fast(z[g][3] - m1);
         l[0] += p0 + p2, l[1] += p1 + p3;
-        const float b0 = vs[g][0] * unit_inv, b1 = vs[g][1] * unit_inv;
-        p0 *= b0, p1 *= b0, p2 *= b1, p3 *= b1;
+        p0 *= Path::bring(vs[g][0], rate[0]), p1 *= Path::bring(vs[g][0], rate[1]);
+        p2 *= Path::bring(vs[g][1], rate[0]), p3 *= Path::bring(vs[g][1], rate[1]);
         const uint32_t ha = pack2_f16(p0, p1), hb = pack2_f16(p2, p3);
         const uint32_t la = rest2_f16(p0, p1, ha), lb = rest2_f16(p2, p3, hb);
         const uint32_t h0 = transpose8(c < 2 ? ha : la), h1 = transpose8(c < 2 ? hb : lb);
@@ -726,7 +731,7 @@ struct Fp8Ring {
         for (int i = 0; i < 4; ++i) {
           y[b][i] = o[b][i >> 1][e + 2 * (i & 1)];
           y[b][i] += __shfl_xor_sync(0xffffffffu, y[b][i], 2);
-          y[b][i] *= unit;
+          y[b][i] *= 1.f / rate[e];
         }
       Path::finish(p, w, qh, m[e], total, y);
     }

@@ -528,6 +528,72 @@ def test_attention_scales_far_apart(cuda, kind, page):
 
 
 @gpu
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("reach", [0, 400000])
+@pytest.mark.parametrize("page", [16, 8, 5])
+@pytest.mark.parametrize("heads,dim", [(4, 64), (3, 128), (8, 64), (7, 128), (16, 64), (17, 96)])
+def test_attention_weight_in_pages_of_small_scales(cuda, kind, heads, dim, page, reach):
+    """One page has the weight, the others a larger value scale: what is lost is 2^-32 of the largest product of a weight and
+    a scale, not of the largest weight times the largest scale.  Scores are one exact product: off by the roundings of its
+    factors, 4 u of itself."""
+    rng = _rng(kind, heads, dim, page)
+    cases = [(gap, up, at) for gap, up in ((80, 10), (80, 20), (80, 28), (80, 33), (80, 40), (80, 90), (20, 28), (20, 40), (0, 40), (0, -40))
+             for at in (0, 2, 5)]
+    lens = [5 * page + 1 + i % page for i in range(len(cases))]
+    table, n_pages = _pages(rng, lens, page, width=-(-reach // page))
+    kc, vc, ks, vs = cache = _pool8(rng, n_pages, page, 1, dim, "slot")
+    _fill8(rng, lens, table, page, cache)
+    ks.fill_(2.0 ** -6), vs.fill_(1.0)
+    first = torch.full((n_pages, page), -320.0, device="cuda")
+    for s, (gap, up, at) in enumerate(cases):
+        pages = table[s, :6]
+        vs[torch.from_numpy(pages).cuda().long()] = 2.0 ** up * float(rng.uniform(1, 2))
+        vs[int(pages[at])] = float(rng.uniform(1, 2))
+        first[torch.from_numpy(pages).cuda().long()] = -4.0 * gap  # (gap 80: -320 / 64 * 8 = -40)
+        first[int(pages[at])] = 4.0 * gap
+    kc[:, :, 0, 0] = (first * torch.from_numpy(rng.choice([1.0, 0.9375], (n_pages, page))).cuda().float()).to(F8)
+    q = torch.zeros(len(cases), heads, dim, device="cuda", dtype=DT[kind])
+    q[:, :, 0] = 8.0
+    out, lse = B.decode_attention_fp8(q, *cache, _i(table), _i(lens), scale=1.0)
+    for s, n in enumerate(lens):
+        at = np.arange(n)
+        where = table[s, at // page], at % page
+        z = 8 * _number(_codes(kc))[where][:, 0, 0] / 64
+        numbers, scale = _number(_codes(vc))[where][:, 0], _np(vs)[where[0], 0]
+        w = np.exp(z - z.max())
+        total, w = w.sum(), w / w.sum()
+        want = (w * scale) @ numbers
+        dw = 4 * U * 1.5 * np.abs(z).max() + 2.0 ** -20 + 2.0 ** -22
+        tol = (w * scale) @ np.abs(numbers) * (2 * dw + 2 * (n + 8) * U) + 2.0 ** -32 * n * 448 * (w * scale).max()
+        step = 2.0 ** (np.floor(np.log2(np.abs(want) + tol)) - 8) if kind == "bf16" else 0
+        _check(out[s], np.tile(want, (heads, 1)), np.tile(tol + step, (heads, 1)))
+        _check(lse[s], np.full(heads, z.max() + np.log(total)), dw + (n + 8) * U + 4 * U * abs(z).max())
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("size", [0.0, 2.0 ** -126, 2.0 ** -140, 2.0 ** 118])
+def test_attention_value_scales_at_the_ends(cuda, kind, size):
+    """Pages whose value scales are 0, subnormal or near the largest, beside ordinary ones and alone."""
+    rng = _rng(kind, str(size))
+    lens, heads, kv, dim, page = [64, 40, 64], 4, 1, 64, 16
+    table, n_pages = _pages(rng, lens, page)
+    cache = _pool8(rng, n_pages, page, kv, dim, "slot")
+    parts = _fill8(rng, lens, table, page, cache)
+    vs = cache[3]
+    for s, pages in ((0, [0, 1, 2, 3]), (1, [1]), (2, [0, 3])):
+        for i in pages:
+            p = int(table[s, i])
+            at = slice(16 * i, min(16 * i + 16, lens[s]))
+            parts[s][1][at] *= float(np.float32(size)) / float(vs[p, 0])
+            vs[p] = size
+    q = _t(rng.standard_normal((3, heads, dim)), kind)
+    out, lse = B.decode_attention_fp8(q, *cache, _i(table), _i(lens))
+    # (half a step of subnormal results, 2^-150, in bf16 2^-134)
+    _check_attention(out, lse, q, parts, dim ** -0.5, kind, 2.0 ** -134 if kind == "bf16" else 2.0 ** -150)
+
+
+@gpu
 @pytest.mark.parametrize("reach", [0, 400000])
 @pytest.mark.parametrize("page", [16, 8, 5])
 @pytest.mark.parametrize("heads,dim", [(4, 64), (3, 128), (8, 64), (7, 128), (16, 64), (17, 96)])
