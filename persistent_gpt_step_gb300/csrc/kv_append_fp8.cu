@@ -203,10 +203,10 @@ __device__ __forceinline__ void append_runs(const AppendParams& p, const RotaryR
     for (int k = 0; k < 2; ++k) {
       const int i = lane + 32 * k;
       int mine = kNoRun;
-      if (r[k].seq >= 0) {
-        const int at = i - min(slot[k], strip0 + i - r[k].first);  // where its run begins
-        if (at >= 0 && (mask >> at) & 1u) mine = __popcll(mask & ((1ull << at) - 1ull));
-      }
+      const int at = i - min(slot[k], strip0 + i - r[k].first);  // where its run begins
+      // (Where starts decrease, a row can be another sequence's than the one before it, whose run would take it past the page.)
+      const int seq0 = __shfl_sync(0xffffffffu, r[0].seq, at & 31), seq1 = __shfl_sync(0xffffffffu, r[1].seq, at & 31);
+      if (r[k].seq >= 0 && at >= 0 && (mask >> at) & 1u && (at < 32 ? seq0 : seq1) == r[k].seq) mine = __popcll(mask & ((1ull << at) - 1ull));
       run_of[i] = (uint8_t)mine;
       if ((mask >> i) & 1u) {
         Run& x = runs[mine];

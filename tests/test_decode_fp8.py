@@ -416,6 +416,32 @@ def test_append_bad_indices_are_skipped_and_reported(cuda, what, bit):
             assert (np.abs(got - want) <= np.maximum(np.abs(want) * 2.0 ** -4, 2.0 ** -10 * _np(vs).max())).all()
 
 
+@gpu
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+def test_append_starts_that_decrease_stay_inside_their_pages(cuda, kind):
+    """Row 5 is found in sequence 3, at the last slot of a page, rows 6 to 8 in sequence 5, which begins at row 5 too: they
+    are not the slots after that page's last one.  Sequences that nothing overlaps are written."""
+    rng = _rng(kind)
+    page, kv, dim, heads = 16, 2, 32, 2
+    starts, before = [0, 2, 4, 5, 6, 5, 9, 12], [0, 3, 0, 15, 0, 0, 14]
+    table = np.array([[0, 9], [1, 9], [2, 9], [7, 9], [3, 9], [4, 9], [5, 6]])  # 7: the last of the pool
+    pools = [torch.full((9, page, kv, dim), 0x33, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    kc, vc = (x[:8].view(F8) for x in pools)
+    ks, vs = torch.full((8, kv), 0.5, device="cuda"), torch.full((8, kv), 0.5, device="cuda")
+    x = _t(rng.standard_normal((12, 2 * kv + heads, dim)), kind)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.kv_append_fp8(x[:, :kv], x[:, kv:2 * kv], kc, vc, ks, vs, _i(table), _i(before), starts=_i(starts), q=x[:, 2 * kv:], status=status)
+    torch.cuda.synchronize()
+    assert int(status) == B.STATUS_BAD_SEQ
+    for pool in pools:
+        assert bool((pool[8] == 0x33).all()) and bool((pool[3] == 0x33).all())  # behind the pool; the sequence whose pair decreases
+    for s in (0, 1, 2, 6):
+        rows, at = np.arange(starts[s], starts[s + 1]), before[s] + np.arange(starts[s + 1] - starts[s])
+        got = (_number(_codes(vc)) * _np(vs)[:, None, :, None])[table[s, at // page], at % page]
+        want = _np(x)[rows, kv:2 * kv]
+        assert (np.abs(got - want) <= np.maximum(np.abs(want) * 2.0 ** -4, 2.0 ** -10 * _np(vs).max())).all()
+
+
 # ----------------------------------------------------------------- decode_attention_fp8
 
 def _fill8(rng, lens, table, page, cache, spread=1):
