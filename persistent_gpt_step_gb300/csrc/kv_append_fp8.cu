@@ -122,6 +122,23 @@ __device__ __forceinline__ void unpack_e4m3(uint32_t u, float* x) {  // two
   asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}" : "=f"(x[0]), "=f"(x[1]) : "r"(h));
 }
 
+// A scale that a page had may be any number, where ours are powers of two.  What is multiplied or divided by one that is
+// not goes to 24 bits towards zero first, the last bit set where anything is left, so that the rounding to 4 bits is
+// that of the exact product or quotient.
+__device__ __forceinline__ bool uneven(float scale) { return __float_as_uint(scale) & 0x7fffffu; }
+__device__ __forceinline__ float with_rest(float x, float rest) { return rest != 0.f ? __uint_as_float(__float_as_uint(x) | 1u) : x; }
+__device__ __forceinline__ float times(float x, float by) {
+  const float y = __fmul_rz(x, by);
+  return with_rest(y, __fmaf_rn(x, by, -y));
+}
+__device__ __forceinline__ float over(float x, float by) {
+  const float y = __fdiv_rz(x, by);
+  return with_rest(y, __fmaf_rn(-y, by, x));
+}
+// 1 / scale without its fraction, a power of two; the fraction, in [1, 2).
+__device__ __forceinline__ float whole_inverse(float scale) { return 1.f / __uint_as_float(__float_as_uint(scale) & 0x7f800000u); }
+__device__ __forceinline__ float fraction(float scale) { return __uint_as_float((__float_as_uint(scale) & 0x7fffffu) | 0x3f800000u); }
+
 // The largest finite magnitude of a piece, as bits; *odd: there is one that is not finite.
 __device__ __forceinline__ uint32_t largest(const uint4& u, float, bool* odd) {
   const uint32_t w[4] = {u.x & 0x7fffffffu, u.y & 0x7fffffffu, u.z & 0x7fffffffu, u.w & 0x7fffffffu};
@@ -159,7 +176,9 @@ __device__ __forceinline__ void bring_numbers(const gpt_paged_cache& c, uint8_t*
       uint32_t& w = (&v.x)[j];
       float x[4];
       unpack_e4m3(w & 0xffffu, x), unpack_e4m3(w >> 16, x + 2);
-      w = pack_e4m3<true>(x[0] * by, x[1] * by) | pack_e4m3<true>(x[2] * by, x[3] * by) << 16;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = uneven(by) ? times(x[k], by) : x[k] * by;
+      w = pack_e4m3<true>(x[0], x[1]) | pack_e4m3<true>(x[2], x[3]) << 16;
     }
     *at = v;
   }
@@ -178,7 +197,7 @@ __device__ __forceinline__ void append_runs(const AppendParams& p, const RotaryR
   __shared__ Run runs[kMaxStrip];
   __shared__ uint8_t run_of[kMaxStrip];
   __shared__ int many;
-  // of a warp's head: largest magnitudes (as bits), 1 / scale
+  // of a warp's head: largest magnitudes (as bits), then the scales' fractions; 1 / scale without these
   __shared__ uint32_t tops[kMostWarps][kMaxStrip];
   __shared__ float invs[kMostWarps][kMaxStrip];
   const gpt_paged_cache& c = p.c.pages;
@@ -290,6 +309,7 @@ __device__ __forceinline__ void append_runs(const AppendParams& p, const RotaryR
     // scales; the numbers before the new ones are brought to a larger one
     float* scales = (side ? p.c.v_scale : p.c.k_scale) + head * p.c.scale_head;
     uint8_t* cache = (uint8_t*)(side ? c.v : c.k) + head * c.head_stride;
+    bool other = false;  // a scale is no power of two
     for (int y0 = 0; y0 < n_runs; y0 += 32) {
       const int y = y0 + lane;
       float share = 1.f;
@@ -302,7 +322,9 @@ __device__ __forceinline__ void append_runs(const AppendParams& p, const RotaryR
           if (scale != old) share = old / scale;
         }
         *at = scale;
-        invs[warp][y] = 1.f / scale;
+        invs[warp][y] = whole_inverse(scale);
+        tops[warp][y] = __float_as_uint(fraction(scale));
+        other |= uneven(scale);
       }
       for (uint32_t left = __ballot_sync(0xffffffffu, share != 1.f); left; left &= left - 1) {
         const int z = y0 + __ffs(left) - 1;
@@ -310,6 +332,7 @@ __device__ __forceinline__ void append_runs(const AppendParams& p, const RotaryR
         bring_numbers(c, cache + runs[z].page * c.page_stride, runs[z].slot, by, lane, 32);
       }
     }
+    odd |= __any_sync(0xffffffffu, other);
     __syncwarp();
   }
   // the second pass, 64 rows at a time: sines and cosines by the block, numbers by the warps
@@ -397,6 +420,10 @@ __device__ __forceinline__ void append_runs(const AppendParams& p, const RotaryR
         }
         uint32_t w[kN / 4];
         if (__builtin_expect(odd, 0)) {
+          const float part = __uint_as_float(tops[warp][x]);
+          if (part != 1.f)
+#pragma unroll
+            for (int j = 0; j < kN; ++j) y[j] = over(y[j], part);
 #pragma unroll
           for (int j = 0; j < kN / 4; ++j) w[j] = pack_e4m3<true>(y[4 * j], y[4 * j + 1]) | pack_e4m3<true>(y[4 * j + 2], y[4 * j + 3]) << 16;
         } else {
@@ -532,7 +559,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp8_step_kernel(const __gr
       bool odd = false;
       const uint32_t top = __reduce_max_sync(same, there && !query ? largest(u[i], T(), &odd) : 0u);
       if (!there) continue;
-      float x[kN], by = 1.f;
+      float x[kN], by = 1.f, part = 1.f;
       Piece<T>::unpack(u[i], x);
       const bool key = !query && (row -= a.n_head) < c.n_kv_head, value = !query && !key;
       if (value) row -= c.n_kv_head;
@@ -547,7 +574,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp8_step_kernel(const __gr
           if (scale != old) bring_numbers(c, numbers, slot, old / scale, lane % pieces, pieces);
         }
         if (e == 0) *scales = scale;
-        by = 1.f / scale;
+        by = whole_inverse(scale), part = fraction(scale);
 #pragma unroll
         for (int j = 0; j < kN; ++j) x[j] *= by;
       }
@@ -563,6 +590,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp8_step_kernel(const __gr
       if (query) {
         *reinterpret_cast<uint4*>((T*)a.q_out + n * a.qo_row + row * a.qo_head + e) = e < a.rope_dims ? Piece<T>::pack(x) : u[i];
       } else {
+        if (part != 1.f)
+#pragma unroll
+          for (int j = 0; j < kN; ++j) x[j] = over(x[j], part);
         uint32_t w[kN / 4];
 #pragma unroll
         for (int j = 0; j < kN / 4; ++j) w[j] = pack_e4m3<true>(x[4 * j], x[4 * j + 1]) | pack_e4m3<true>(x[4 * j + 2], x[4 * j + 3]) << 16;

@@ -418,6 +418,70 @@ def test_append_bad_indices_are_skipped_and_reported(cuda, what, bit):
 
 @gpu
 @pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("many", [None, 1, 12])
+def test_append_to_pages_of_any_scale(cuda, kind, many):
+    """Pages begun by other code, with scales that are no powers of two: elements at (and near) the middle between two numbers
+    of their page's scale, and numbers whose product with the old scale over the new one is near the middle, are
+    rounded as the exact quotients.  many: rows of each sequence; None: one each, without starts."""
+    rng = _rng(kind, str(many))
+    n_seq, kv, dim, page, slot = 300, 2, 32, 16, 3
+    n = many or 1
+    bits = 19 if kind == "fp32" else 3  # 5 bits of the middle and these are the element's
+    mant = 1 + rng.integers(1, 1 << bits, (n_seq, kv)) / 2.0 ** bits
+    scale = mant * 2.0 ** rng.integers(-3, 4, (n_seq, kv))
+    grown = np.arange(n_seq) % 3 == 0  # the others keep their scales
+    middle = (2 * rng.integers(8, 16, (n_seq, n, kv, dim)) + 1) * 2.0 ** rng.integers(-6, 3, (n_seq, n, kv, dim))
+    x = middle * scale[:, None, :, None] * rng.choice([-1.0, 1.0], middle.shape)
+    x += np.where(rng.random(x.shape) < 0.3, x * 2.0 ** -23, 0)
+    x[grown] *= 2.0 ** 10
+    number = rng.integers(9, 16, (n_seq, kv))  # n m is within n / 2 of a middle of 5 bits, m the old scale's 24 bits
+    m = (2 * rng.integers(8, 16, (n_seq, kv)) + 1) * 2.0 ** 23 / number
+    m = np.rint(np.where(m < 2 ** 24, m, m / 2))
+    scale[grown] = (m * 2.0 ** -24)[grown]
+    scale = scale.astype(np.float32)
+    kc, vc, ks, vs = _pool8(rng, n_seq, page, kv, dim, "slot")
+    ks.copy_(torch.from_numpy(scale)), vs.copy_(torch.from_numpy(scale))
+    for c in (kc, vc):
+        c[:, 0] = torch.from_numpy(number[:, :, None] * np.ones(dim)).cuda().float().to(F8)
+    was = [_codes(c) for c in (kc, vc)]
+    rows = _t(x.reshape(n_seq * n, kv, dim), kind)
+    table, before, starts = np.arange(n_seq)[:, None], [slot] * n_seq, [n * s for s in range(n_seq + 1)]
+    B.kv_append_fp8(rows, rows, kc, vc, ks, vs, _i(table), _i(before), starts=_i(starts) if many else None)
+    for c, s, old in ((kc, ks, was[0]), (vc, vs, was[1])):
+        want, ws, written = _expect_append(_np(rows), _np(rows), old, scale, table, page, starts, before, page)
+        assert np.array_equal(_np(s), ws) and bool((ws[grown] != scale[grown]).all()) and bool((ws[~grown] == scale[~grown]).all())
+        have = _number(_codes(c))
+        assert np.array_equal(have[~written], want[~written])
+        assert np.array_equal(have[written], _nearest(want[written]))
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("many", [None, 2, 12])
+def test_append_rotated_to_pages_of_any_scale(cuda, kind, many):
+    rng = _rng(kind, str(many), 1)
+    n_seq, kv, dim, page, slot, n = 60, 2, 64, 16, 3, many or 1
+    kc, vc, ks, vs = _pool8(rng, n_seq, page, kv, dim, "slot")
+    scale = rng.uniform(0.01, 0.04, (n_seq, kv)).astype(np.float32)
+    scale[0] = 1.5 * 2.0 ** 127
+    ks.copy_(torch.from_numpy(scale)), vs.copy_(torch.from_numpy(scale))
+    was, rows = _codes(kc), _t(rng.standard_normal((n_seq * n, kv, dim)), kind)
+    rows[:n] *= 2.0 ** 124
+    table, before, starts = np.arange(n_seq)[:, None], [slot] * n_seq, [n * s for s in range(n_seq + 1)]
+    B.kv_append_fp8(rows, rows, kc, vc, ks, vs, _i(table), _i(before), starts=_i(starts) if many else None, rope_dims=dim)
+    pos = slot + np.arange(n_seq * n) % n
+    turned = _turned(_np(rows), pos, dim, 10000.0)
+    want, ws, written = _expect_append(_np(rows), turned, was, scale, table, page, starts, before, page)
+    assert np.array_equal(_np(ks), ws)
+    have, off = _number(_codes(kc)), _turn_tolerance(_np(rows), turned, dim, "fp32", 2.0 ** -24)
+    off = _expect_append(_np(rows), off, was, scale, table, page, starts, before, page)[0]
+    assert np.array_equal(have[~written], want[~written])
+    x, y, off = have[written], want[written], off[written]
+    assert (np.abs(x - y) <= off + np.maximum((np.abs(y) + off) * 2.0 ** -4, 2.0 ** -10)).all()
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
 def test_append_starts_that_decrease_stay_inside_their_pages(cuda, kind):
     """Row 5 is found in sequence 3, at the last slot of a page, rows 6 to 8 in sequence 5, which begins at row 5 too: they
     are not the slots after that page's last one.  Sequences that nothing overlaps are written."""
