@@ -455,9 +455,10 @@ __device__ __forceinline__ void turn_queries(const AppendParams& p, const Rotary
     for (int i = 0; i < kQueryUnder; ++i)
       if (head + i < a.n_head) u[i] = __ldcs(reinterpret_cast<const uint4*>(from + (head + i) * a.q_head));
   };
-  load(0);  // under way while the row is looked up
   const Row r = find_row(p, stage, (int)n, false);
-  if (r.seq < 0 || page_of(p, r, false) < 0) return;
+  if (r.seq < 0) return;
+  load(0);  // under way while the page is looked up
+  if (page_of(p, r, false) < 0) return;
   float2 turn[kN / 2];
 #pragma unroll
   for (int j = 0; j < kN / 2; ++j)
@@ -537,8 +538,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp8_step_kernel(const __gr
     }
   };
   const Row r = find_row(p, nullptr, (int)n, tid == 0);
-  load(group);  // under way while the page is looked up
   if (r.seq < 0) return;
+  load(group);  // under way while the page is looked up
   const int page = page_of(p, r, tid == 0), slot = r.pos % c.page_size;
   for (int i = tid; i < kMaxPairs; i += kThreads) {
     turns[i] = make_float2(1.f, 0.f);
