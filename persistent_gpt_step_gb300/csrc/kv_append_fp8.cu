@@ -171,9 +171,9 @@ __device__ __forceinline__ uint32_t largest(const uint4& u, __nv_bfloat16, bool*
 // The numbers of a page's first slots, of one head, times `by`: by `threads` threads, the first of them 0.  (Not inlined:
 // 32,768 tokens 131.0 us, 133.6 so, for the registers.)
 __device__ __noinline__ void bring_numbers(const gpt_paged_cache& c, uint8_t* page, int slots, float by, int thread, int threads) {
-  const int each = c.head_dim / 16;
-  for (int i = thread; i < slots * each; i += threads) {
-    uint4* at = reinterpret_cast<uint4*>(page + i / each * c.slot_stride) + i % each;
+  const int each = c.head_dim / 16, beside = threads / each, sub = thread / each;  // (slots x each can pass 32 bits)
+  for (int slot = sub; sub < beside && slot < slots; slot += beside) {
+    uint4* at = reinterpret_cast<uint4*>(page + slot * c.slot_stride) + thread % each;
     uint4 v = *at;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
