@@ -487,7 +487,13 @@ struct Sampler {
     if (a.logprob) a.logprob[b] = logprob;
     if (a.kept) a.kept[b] = kept;
   }
-  __device__ __forceinline__ float log_of(float w, float sum) { return logf(__fdiv_rn(w, sum)); }
+  // The log probability of token `id`, of weight w, from a sum in the same units.  A weight of few units is rounded by much
+  // of itself: there its logit gives it.
+  __device__ __forceinline__ float log_of(u64 w, float sum, int id) const {
+    float part = (float)w, log_w = 0.f;
+    if (w < 1u << 22) part = (float)(1ull << weight.unit), log_w = fmaf(0.5f, (float)row.z[id], -weight.mh) * weight.c_hi * 0.693147181f;
+    return log_w + logf(__fdiv_rn(part, sum));
+  }
 
   // Bins of equal width from the largest logit down; the last one goes on to the end.
   __device__ __forceinline__ float per_bin() const { return kBins / (32.f * fmaxf(1.f, fminf(temperature, 1e30f))); }
@@ -561,7 +567,7 @@ struct Sampler {
         if ((uint32_t)x.x > (uint32_t)mine) upto += x.y;  // a smaller id
       }
     }
-    if (w && upto < goal && upto + w >= goal) answer(id_of(mine), log_of((float)w, (float)sum), kept);
+    if (w && upto < goal && upto + w >= goal) answer(id_of(mine), log_of(w, (float)sum, id_of(mine)), kept);
     return true;
   }
 
@@ -710,7 +716,7 @@ struct Sampler {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             if (at <= below && at + v[i] > under) {
-              answer((w + tid) * 8 - row.shift + i, log_of((float)v[i], (float)all * up), units * 8 - (int)flags);
+              answer((w + tid) * 8 - row.shift + i, log_of(v[i], (float)all * up, (w + tid) * 8 - row.shift + i), units * 8 - (int)flags);
               accepted = 1;
             }
             at += v[i];
@@ -931,7 +937,7 @@ __device__ __noinline__ bool finish_long(const SampleParams& p, Shared& sm, int 
   from = max(from, s.least(best));
   sum_from();
   const int i = cross(sm, n, kById, goal_of(s.u, sum), from);
-  if (s.tid == 0) s.answer(id_of(sm.all[i]), s.log_of((float)sm.weights[i], (float)sum), (int)kept);
+  if (s.tid == 0) s.answer(id_of(sm.all[i]), s.log_of(sm.weights[i], (float)sum, id_of(sm.all[i])), (int)kept);
   return true;
 }
 
@@ -969,7 +975,7 @@ __device__ __noinline__ void draw_row(const SampleParams& p, Shared& sm, bool al
     if (upto < goal && upto + own >= goal)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (upto < goal && upto + y[i] >= goal) s.answer((v + s.tid) * 8 - s.row.shift + i, s.log_of((float)y[i], (float)sum), (int)kept);
+        if (upto < goal && upto + y[i] >= goal) s.answer((v + s.tid) * 8 - s.row.shift + i, s.log_of(y[i], (float)sum, (v + s.tid) * 8 - s.row.shift + i), (int)kept);
         upto += y[i];
       }
     before += total;

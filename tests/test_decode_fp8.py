@@ -1062,6 +1062,34 @@ def test_sample_number_zero_in_rows_off_boundaries(cuda, kind, vocab):
 
 
 @gpu
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("vocab,filters", [(300, {}), (131072, {}), (40, dict(k=39)), (40, dict(mp=1e-16)), (600, dict(k=599)), (5000, dict(k=4999)),
+                                           (5000, dict(mp=1e-16)), (131072, dict(mp=1e-16))])
+def test_sample_logprob_of_hardly_any_weight(cuda, kind, vocab, filters):
+    """The number 0 draws the first token that has a weight, here one of a few units (2^-48 of the largest and more): its
+    log probability is its logit's.  Bounds as in _run_sample; the weight's log2, up to 64, by three roundings of fp32."""
+    rng = _rng(kind, vocab, str(filters))
+    rows, t = 24, 0.7
+    z = rng.uniform(-1.0, 0.0, (rows, vocab))
+    z[:, 5] = 0.0
+    z[:, 0] = -t * math.log(2.0) * rng.uniform(40.0, 48.5, rows)
+    z[:, 1] = -80.0  # (no weight, and not among the first top_k)
+    zt = _t(z, kind)
+    f = lambda x: _t(np.full(rows, x))  # noqa: E731
+    token, logprob, kept = B.sample_token(zt, f(0.0), temperature=f(t), top_k=_i([filters["k"]] * rows) if "k" in filters else None,
+                                          min_p=f(filters["mp"]) if "mp" in filters else None)
+    z, small = _np(zt), 0
+    for i in range(rows):
+        at = int(token[i])
+        assert at in (0, 2)  # (a weight of less than half a unit is none)
+        small += at == 0
+        want = z[i] / np.float64(np.float32(t))
+        want = want[at] - np.log(np.exp(want).sum())
+        assert abs(float(logprob[i]) - want) <= 2.0 ** (-21 if filters else -19) * max(1.0, abs(want)), (i, at, float(logprob[i]), want)
+    assert small > rows // 2
+
+
+@gpu
 def test_sample_rows_past_32_bits(cuda):
     rng = _rng(9)
     wide = torch.empty(3, (1 << 31) + 64, dtype=torch.bfloat16, device="cuda")
