@@ -492,7 +492,7 @@ struct Sampler {
   __device__ __forceinline__ float log_of(u64 w, float sum, int id) const {
     float part = (float)w, log_w = 0.f;
     if (w < 1u << 22) part = (float)(1ull << weight.unit), log_w = fmaf(0.5f, (float)row.z[id], -weight.mh) * weight.c_hi * 0.693147181f;
-    return log_w + logf(__fdiv_rn(part, sum));
+    return log_w + logf(__fdiv_rn(part, fmaxf(sum, part)));  // (a sum in fp32 can lie below the one weight in it)
   }
 
   // Bins of equal width from the largest logit down; the last one goes on to the end.

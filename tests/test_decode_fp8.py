@@ -1090,6 +1090,21 @@ def test_sample_logprob_of_hardly_any_weight(cuda, kind, vocab, filters):
 
 
 @gpu
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("vocab", [1, 50, 5000, 131072])
+def test_sample_logprob_of_all_the_weight(cuda, kind, vocab):
+    """Rows of one token, or of one far above all others: no probability above 1."""
+    rng = _rng(kind, vocab)
+    z = np.full((96, vocab), -np.inf)
+    z[1::2] = -200.0
+    z[np.arange(96), rng.integers(0, vocab, 96)] = rng.uniform(-9, 9, 96)
+    t, u = rng.uniform(0.3, 3.0, 96), 0.1 + 0.8 * rng.random(96)
+    for filters in ({}, dict(k=30), dict(p=0.9), dict(mp=0.5)):
+        _, logprob, _ = _run_sample(z, u, kind, t=t, **filters)
+        assert bool((logprob <= 0).all())
+
+
+@gpu
 def test_sample_rows_past_32_bits(cuda):
     rng = _rng(9)
     wide = torch.empty(3, (1 << 31) + 64, dtype=torch.bfloat16, device="cuda")
