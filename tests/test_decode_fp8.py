@@ -1127,6 +1127,22 @@ def test_sample_repeats(cuda):
         assert all(torch.equal(a[i:i + 1], b) for a, b in zip(first, one))
 
 
+@gpu
+@pytest.mark.parametrize("rows,vocab", [(64, 30011), (400, 20000)])
+def test_sample_repeats_without_limits(cuda, rows, vocab):
+    """The same bits every time; alone, in other numbers of blocks, the same tokens and counts, and log probabilities within
+    both sides' bounds."""
+    rng = _rng(rows)
+    z, u = _t(_logits(rng, rows, vocab)), _t(rng.random(rows))
+    first = B.sample_token(z, u)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(first, B.sample_token(z, u)))
+    for i in range(0, rows, rows // 8):
+        token, logprob, kept = B.sample_token(z[i:i + 1], u[i:i + 1])
+        assert int(token) == int(first[0][i]) and int(kept) == int(first[2][i])
+        assert abs(float(logprob) - float(first[1][i])) <= 2.0 ** -18 * max(1.0, abs(float(logprob)))
+
+
 # ----------------------------------------------------------------- together
 
 @gpu
