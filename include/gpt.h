@@ -487,8 +487,8 @@ typedef struct gpt_fp8_cache {
  *  - a page whose slot 0 gets a row starts anew: its scale becomes s_new;
  *  - otherwise it becomes the larger, s', of s_new and the scale s that is there,
  *    and the numbers in the slots before the first new one become e4m3(number * s / s');
- * then each new element x (keys: rotated, in fp32) is written as e4m3(x / scale),
- * rounded to nearest, ties to even; infinities and NaN become NaN.  With s_new all
+ * then each new element x (keys: rotated, in fp32, the angle accurate to 2^-25 of a turn
+ * below position 2^24, 2^-18 from there on) is written as e4m3(x / scale), rounded to nearest, ties to even; infinities and NaN become NaN.  With s_new all
  * elements lie below 2^8 (rotated ones below 2^8.5) and none reaches 448, the largest
  * number; scales are powers of two, so that bringing numbers to a larger one loses nothing
  * but what falls under the smallest number, 2^-9.  Slots behind the new rows are left

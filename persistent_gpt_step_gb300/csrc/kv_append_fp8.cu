@@ -349,7 +349,7 @@ __device__ __forceinline__ void append_runs(const AppendParams& p, const RotaryR
       for (int i = tid; i < (stop - chunk) * kMaxPairs; i += blockDim.x) {
         const int row = chunk + i / kMaxPairs, pair = i % kMaxPairs, x = run_at(row);
         turns[i] = make_float2(1.f, 0.f);
-        if (pair < pairs && x != kNoRun) pair_angle(rates, pair, runs[x].pos + (row - runs[x].begin), &turns[i].x, &turns[i].y);
+        if (pair < pairs && x != kNoRun) pair_angle_fine(rates, pair, runs[x].pos + (row - runs[x].begin), &turns[i].x, &turns[i].y);
       }
       __syncthreads();
     }
@@ -466,7 +466,7 @@ __device__ __forceinline__ void turn_queries(const AppendParams& p, const Rotary
   float2 turn[kN / 2];
 #pragma unroll
   for (int j = 0; j < kN / 2; ++j)
-    if (e + 2 * j < a.rope_dims) pair_angle(rates, e / 2 + j, r.pos, &turn[j].x, &turn[j].y);
+    if (e + 2 * j < a.rope_dims) pair_angle_fine(rates, e / 2 + j, r.pos, &turn[j].x, &turn[j].y);
   const bool all = e + kN <= a.rope_dims;
 #pragma unroll 1
   for (int head = 0; head < a.n_head; head += kQueryUnder) {
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp8_step_kernel(const __gr
   const int page = page_of(p, r, tid == 0), slot = r.pos % c.page_size;
   for (int i = tid; i < kMaxPairs; i += kThreads) {
     turns[i] = make_float2(1.f, 0.f);
-    if (i < a.rope_dims / 2) pair_angle(p.rates, i, r.pos, &turns[i].x, &turns[i].y);
+    if (i < a.rope_dims / 2) pair_angle_fine(p.rates, i, r.pos, &turns[i].x, &turns[i].y);
   }
   if (page < 0) return;
   __syncthreads();

@@ -417,6 +417,24 @@ def test_append_bad_indices_are_skipped_and_reported(cuda, what, bit):
 
 
 @gpu
+@pytest.mark.parametrize("plain", [False, True])
+@pytest.mark.parametrize("pos,turn", [(0, 0.0), (60000, 2.0 ** -32), ((1 << 24) - 2100, 2.0 ** -25)])
+def test_append_angles(cuda, pos, turn, plain):
+    """Queries (1, 0) become cosine and sine: off by the angle (a turn's part), one step of 2^-24, a rounding."""
+    dim, n = 128, 2000
+    kc, vc = (torch.zeros(1, 16, 1, dim, dtype=torch.uint8, device="cuda").view(F8) for _ in range(2))
+    ks, vs = torch.ones(1, 1, device="cuda"), torch.ones(1, 1, device="cuda")
+    table = torch.zeros(1, 1 << 20, dtype=torch.int32, device="cuda").expand(n if plain else 1, -1)  # (every position in one page)
+    x = torch.zeros(n, 1, dim, device="cuda")
+    q = torch.zeros(n, 1, dim, device="cuda")
+    q[..., ::2] = 1.0
+    at = pos + np.arange(n)
+    got = B.kv_append_fp8(x, x, kc, vc, ks, vs, table, _i(at if plain else [pos]), starts=None if plain else _i([0, n]), q=q, rope_dims=dim)
+    want = _turned(_np(q), at, dim, 10000.0)
+    _check(got, want, 2 * math.pi * turn + 2.0 ** -24 + 2.0 ** -25)
+
+
+@gpu
 @pytest.mark.parametrize("kind", ["fp32", "bf16"])
 @pytest.mark.parametrize("many", [None, 1, 12])
 def test_append_to_pages_of_any_scale(cuda, kind, many):
