@@ -60,11 +60,13 @@ __device__ __forceinline__ uint2 load8(const void* p) {
 }
 
 __device__ __forceinline__ float power2(int n) { return __uint_as_float((uint32_t)(n + 127) << 23); }
+__device__ __forceinline__ float power2_inverse(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }  // of a power of two
 // log2 of a scale is below this (0: -126).
 __device__ __forceinline__ float log2_above(float scale) { return (float)((int)(__float_as_uint(scale) >> 23) - 126); }
 
 // As Walk, with the scales of each group's (or key's) page: table entries are read two
-// rounds ahead, the scales one.
+// rounds ahead and looked at one round ahead (where a round is one step, pages of 5 slots, 87 us for
+// 100 with both two ahead), when the scales are read.
 template <bool kFast, int kKeys>
 struct ScaledWalk {
   using Off = std::conditional_t<kFast, uint32_t, int64_t>;
@@ -83,15 +85,14 @@ struct ScaledWalk {
     const int lane = threadIdx.x & 31;
     head = kFast ? h * p.head16 : h * p.c.head_stride;
     at1 = k0 + (kFast ? lane * 8 : lane & (kKeys - 1));
-    page1 = fetch(at1);
+    page1 = checked(entry(at1));
     scales();
-    page2 = fetch(at1 + kRound);
+    page2 = entry(at1 + kRound);
   }
-  __device__ __forceinline__ int fetch(int at) const {
-    if (at >= end) return -1;
-    const int id = table[at / p.c.page_size];
+  __device__ __forceinline__ int entry(int at) const { return at < end ? table[at / p.c.page_size] : -1; }
+  __device__ __forceinline__ int checked(int id) const {  // the entry of at1
     if (id >= 0 && id < p.c.n_pages) return id;
-    set_status(p.a.status, GPT_STATUS_BAD_PAGE);
+    if (at1 < end) set_status(p.a.status, GPT_STATUS_BAD_PAGE);
     return -1;
   }
   __device__ __forceinline__ void scales() {
@@ -104,9 +105,9 @@ struct ScaledWalk {
     if constexpr (kFast) off = next();
     else off = page1 < 0 ? kNoKey : page1 * p.c.page_stride + (at1 % p.c.page_size) * p.c.slot_stride + head;
     ks = ks1, vs = vs1;
-    at1 += kRound, page1 = page2;
+    at1 += kRound, page1 = checked(page2);
     scales();
-    page2 = fetch(at1 + kRound);
+    page2 = entry(at1 + kRound);
   }
   // kFast: the next group of 8 keys.
   __device__ __forceinline__ void group(Off& o, float& k, float& v) {
@@ -477,7 +478,7 @@ struct Fp8Path {
           for (int i = 0; i < 4; ++i) {
             y[b][i] = o[t][b][i >> 1][e + 2 * (i & 1)];
             if (kTwice) y[b][i] += __shfl_xor_sync(0xffffffffu, y[b][i], 2);
-            y[b][i] *= 1.f / rate[t][e];
+            y[b][i] *= power2_inverse(rate[t][e]);
           }
         finish(p, w, qh, m[t][e], total, y);
       }
@@ -731,7 +732,7 @@ struct Fp8Ring {
         for (int i = 0; i < 4; ++i) {
           y[b][i] = o[b][i >> 1][e + 2 * (i & 1)];
           y[b][i] += __shfl_xor_sync(0xffffffffu, y[b][i], 2);
-          y[b][i] *= 1.f / rate[e];
+          y[b][i] *= power2_inverse(rate[e]);
         }
       Path::finish(p, w, qh, m[e], total, y);
     }
