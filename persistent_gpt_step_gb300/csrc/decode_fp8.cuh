@@ -10,9 +10,9 @@
 //  - values: the weights, each times the value scale of its page, enter as two fp16 parts (2^-22
 //    left over) below 2^15.  Scales may lie further apart than fp16 reaches, and a key of the
 //    largest weight in a page of a small one, so that these products have a reference of their
-//    own beside the weights': 9 under a bound of their largest that is at most two above it, so
-//    that what falls under fp16's smallest number is 2^-32 of the largest product.  Both are
-//    integers, and what brings weights from one to the other a power of two.
+//    own beside the weights' (7 under the maximum): an integer, 10 under a bound of their largest
+//    that is at most two above it.  What brings weights from one to the other is a power of two,
+//    rounded down, so that what falls under fp16's smallest number is 2^-32 of the largest product.
 // Bound: HBM, half the bytes of a bf16 cache, and the instructions beside it: 322 for 16 keys of 128
 // dims, of these 64 conversions, 16 products and 109 on addresses and masks, and 1,900 for a row's
 // start and end (64 ragged sequences of 32 over 8 heads of 128 104 us, 5.2 TB/s; 131,071 keys 61 us,
@@ -205,17 +205,17 @@ struct Fp8Path {
   // New references of a column from its largest score, and bound of a product's log2, best and best_w of
   // a lane; m, mw, rate, l and o as in run.
   static __device__ __forceinline__ void move(float best, float best_w, float& m, float& mw, float& rate, float& l, float (&o)[VW][2][4], int e) {
-    best = fmaxf(best, m + 7.f), best_w = fmaxf(best_w, mw + 9.f);
+    best = fmaxf(best, m + 7.f), best_w = fmaxf(best_w, mw + 10.f);
 #pragma unroll
     for (int x = 4; x < 32; x <<= 1) {
       best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, x));
       best_w = fmaxf(best_w, __shfl_xor_sync(0xffffffffu, best_w, x));
     }
-    best = ceilf(best) - 7.f, best_w = ceilf(best_w) - 9.f;
-    const float keep = weight(m, best), n = fminf(fmaxf(best - best_w, -126.f), 126.f);
+    best -= 7.f, best_w = ceilf(best_w) - 10.f;
+    const float keep = weight(m, best), n = fminf(fmaxf(floorf(best - best_w), -126.f), 126.f);
     const int more = (int)n - ((int)(__float_as_uint(rate) >> 23) - 127);
     const float keep_w = keep * power2(more / 2) * power2(more - more / 2);
-    m = best, mw = best - n, rate = power2((int)n);
+    m = best, mw = best_w, rate = power2((int)n);
     l *= keep;
 #pragma unroll
     for (int b = 0; b < VW; ++b)
@@ -254,7 +254,7 @@ struct Fp8Path {
     const uint8_t* kb = (const uint8_t*)p.c.k + (kFast ? r * row : 0);
     const uint8_t* vb = (const uint8_t*)p.c.v + r * 4 * VW + (kFast ? 2 * c * row : 0);
     uint4* query = reinterpret_cast<uint4*>(mine) + lane;
-    // m, mw: references of the weights, and of their products with scales; rate: 2^(m - mw)
+    // m, mw: references of the weights, and of their products with scales; rate: 2^(m - mw), rounded down to a power of two
     float o[NT][VW][2][4], m[NT][2], mw[NT][2], rate[NT][2], l[NT][2], factor[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
