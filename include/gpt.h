@@ -488,12 +488,13 @@ typedef struct gpt_fp8_cache {
  *  - otherwise it becomes the larger, s', of s_new and the scale s that is there,
  *    and the numbers in the slots before the first new one become e4m3(number * s / s');
  * then each new element x (keys: rotated, in fp32, the angle accurate to 2^-25 of a turn
- * below position 2^24, 2^-18 from there on) is written as e4m3(x / scale), rounded to nearest, ties to even; infinities and NaN become NaN.  With s_new all
- * elements lie below 2^8 (rotated ones below 2^8.5) and none reaches 448, the largest
- * number; scales are powers of two, so that bringing numbers to a larger one loses nothing
- * but what falls under the smallest number, 2^-9.  Slots behind the new rows are left
- * as they are.  Rows before starts[0] and from starts[n_seq] on are neither read nor
- * written (rows of q_out too), nor are the rows of a sequence of negative before[s].
+ * below position 2^24, 2^-18 from there on) is written as e4m3(x / scale), rounded to
+ * nearest, ties to even; infinities and NaN become NaN.  With s_new all elements lie
+ * below 2^8 (rotated ones below 2^8.5) and none reaches 448, the largest number; s_new is a
+ * power of two, so that bringing numbers from one to a larger one loses nothing but what
+ * falls under the smallest number, 2^-9.  Slots behind the new rows are left as they are.
+ * Rows before starts[0] and from starts[n_seq] on are neither read nor written (rows of
+ * q_out too), nor are the rows of a sequence of negative before[s].
  *   before: DEVICE int32 [n_seq]; starts: DEVICE int32 [n_seq + 1], not decreasing, in
  *     [0, n_tokens], or NULL: row s is the one new token of sequence s (n_tokens <=
  *     n_seq).  Other arguments as in gpt_kv_append; the scales' strides name no scale

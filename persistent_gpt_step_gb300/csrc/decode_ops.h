@@ -1,5 +1,5 @@
 // decode_ops.h — what the operators of a batched decode step (kv_append.cu, kv_append_fp8.cu,
-// decode_attention.cu, decode_attention_fp8.cu, next_token.cu, sample_token.cu) share: error texts, argument checks, the
+// decode_attention.cu, next_token.cu, sample_token.cu) share: error texts, argument checks, the
 // device view of a paged cache and element conversions.
 #pragma once
 #include <cuda_bf16.h>

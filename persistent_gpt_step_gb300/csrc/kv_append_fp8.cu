@@ -9,8 +9,9 @@
 // scale comes from the magnitudes before the rotation, which turns each pair by at most
 // sqrt 2: it is then exact, the same however sines are rounded, and no number reaches 448.
 // Bound: HBM (rows read once, numbers and rotated queries written once): 32,768 tokens of 32 + 8 + 8
-// heads of 128 in bf16 130 us, 5.7 TB/s; a few thousand tokens by the chain of loads and the sines
-// (4,095 of 12 + 12 + 12 of 64 in fp32 16 us, 3.5 TB/s).
+// heads of 128 in bf16 131 us, 5.6 TB/s; a few thousand tokens by the chain of loads and the sines
+// (4,095 of 12 + 12 + 12 of 64 in fp32 16.8 us, 3.4 TB/s).  Pages of hundreds of slots and more leave few
+// warps at work: 32,768 tokens of 4 sequences take 132 us in pages of 64, 210 of 512, 1,025 of 4,096.
 #include "rotary.h"
 
 namespace pgs {

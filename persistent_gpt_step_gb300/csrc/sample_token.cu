@@ -21,10 +21,11 @@
 //  - with top_p alone: by_sums;
 //  - where a list does not hold what it must: slow_row, bins of counts and sums of all tokens, as
 //    many rounds as it takes, then the sums of the kept ones by warp.
-// Bound: a few rows by the chain of phases, 1 to 2 us each with a barrier of the cluster (1 row of
-// 12,288: 7.6 us without limits, 13 with; 64 of 50,304 15, 21, with top_p alone 40); many by
-// instructions (512 of 131,072 in fp32 without limits 90 us, 3.0 TB/s, 27 instructions a token; with
-// top_p alone 298).
+// Bound: a few rows by the chain of phases, each with a barrier of the cluster (0.7 us): 1 row of 12,288 7.5 us without
+// limits, 12 with top_k, 64 of 50,304 14.5 and 22; with top_p alone by passes over the row (14 and 40).  Many rows by
+// instructions: 512 of 131,072 in fp32 without limits 90 us, 3.0 TB/s, 25 instructions a token; in bf16 79; with top_p
+// alone 296.  Lists that overflow are finished by one block: 1 row of 131,072 with a top_k of 900 to 2,000 takes 160 to
+// 220 us (of 200 19, of 5,000, where all blocks stay, 50), with a min_p that keeps 20,000 97.
 #include <cooperative_groups.h>
 
 #include <cmath>
