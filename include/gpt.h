@@ -333,8 +333,8 @@ int gpt_serve_end(gpt* h);
  * page*page_stride + slot*slot_stride + head*head_stride + i (elements, k and v
  * alike; any order of pages, slots and heads).  Base addresses and strides are
  * multiples of 16 bytes, strides are not negative; head_dim is a multiple of 16
- * bytes and <= 128, n_kv_head <= 65536; max_pages * page_size stays 4096 below
- * 2^31.  Sequences may share pages (table_stride 0: all of them one row of the
+ * bytes and <= 128, n_kv_head <= 65536; max_pages * page_size and n_seq stay 4096
+ * below 2^31.  Sequences may share pages (table_stride 0: all of them one row of the
  * table).
  *
  * The attention's kernel is chosen by what the table can name, max_pages *

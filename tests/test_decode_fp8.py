@@ -122,6 +122,16 @@ def test_head_and_token_counts_beyond_32_bits_of_work_are_refused(lib):
     assert lib.gpt_decode_attention_fp8(ctypes.byref(_cache8()), ctypes.byref(_attend(n_head=heads)), None) == -8
 
 
+def test_sequence_counts_at_the_end_of_32_bits_are_refused(lib):
+    for n in (2 ** 31 - 1, 2 ** 31 - 4096):
+        for rc in (lib.gpt_kv_append_fp8(ctypes.byref(_cache8(n_seq=n)), ctypes.byref(_append8()), None),
+                   lib.gpt_decode_attention_fp8(ctypes.byref(_cache8(n_seq=n)), ctypes.byref(_attend()), None),
+                   lib.gpt_kv_append(ctypes.byref(_cache(n_seq=n)), ctypes.byref(_append()), None),
+                   lib.gpt_decode_attention(ctypes.byref(_cache(n_seq=n)), ctypes.byref(_attend()), None)):
+            assert rc == -8 and "n_seq" in lib.gpt_last_error(None).decode()
+        assert lib.gpt_decode_attention_fp8_workspace(ctypes.byref(_cache8(n_seq=n)), 8) == 0
+
+
 def test_nothing_to_do_is_no_error(lib):
     assert lib.gpt_kv_append_fp8(ctypes.byref(_cache8()), ctypes.byref(_append8(n_tokens=0)), None) == 0
     assert lib.gpt_decode_attention_fp8(ctypes.byref(_cache8(n_seq=0)), ctypes.byref(_attend()), None) == 0
