@@ -13,8 +13,8 @@
 //    own beside the weights' (7 under the maximum): an integer, 10 under a bound of their largest
 //    that is at most two above it.  What brings weights from one to the other is a power of two,
 //    rounded down, so that what falls under fp16's smallest number is 2^-32 of the largest product.
-// Bound: HBM, half the bytes of a bf16 cache, and the instructions beside it: 330 for 16 keys of 128
-// dims, of these 69 conversions, 16 products and 98 on integers, and 1,900 for a row's start and end
+// Bound: HBM, half the bytes of a bf16 cache, and the instructions beside it: 328 for 16 keys of 128
+// dims, of these 69 conversions, 16 products and 95 on integers, and 1,900 for a row's start and end
 // (64 ragged sequences of 32 over 8 heads of 128 104 us, 5.2 TB/s; 131,071 keys 61 us, 4.4 TB/s;
 // 200 sequences of 16 heads of 64 48 us, 4.4 TB/s).  With 8 query heads to a key head 73 us (64 ragged
 // sequences of 32 over 4 heads of 128, floor 40; for fp32 results 81); pages that are not of whole
