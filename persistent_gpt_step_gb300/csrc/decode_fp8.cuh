@@ -18,7 +18,7 @@
 // (64 ragged sequences of 32 over 8 heads of 128 104 us, 5.2 TB/s; 131,071 keys 61 us, 4.4 TB/s;
 // 200 sequences of 16 heads of 64 48 us, 4.4 TB/s).  With 8 query heads to a key head 73 us (64 ragged
 // sequences of 32 over 4 heads of 128, floor 40; for fp32 results 81); pages that are not of whole
-// 8-key groups 86 us (64 of up to 4,096 keys, 32 over 8 heads, pages of 5; floor 40).
+// 8-key groups 78 us (64 of up to 4,096 keys, 32 over 8 heads, pages of 5; floor 40).
 #pragma once
 #include "decode_attention.cuh"
 
@@ -67,8 +67,7 @@ __device__ __forceinline__ float power2_inverse(float x) { return __uint_as_floa
 __device__ __forceinline__ float log2_above(float scale) { return (float)((int)(__float_as_uint(scale) >> 23) - 126); }
 
 // As Walk, with the scales of each group's (or key's) page: table entries are read two
-// rounds ahead and looked at one round ahead (where a round is one step, pages of 5 slots, 87 us for
-// 100 with both two ahead), when the scales are read.
+// rounds ahead and looked at one round ahead, when the scales are read.
 template <bool kFast, int kKeys>
 struct ScaledWalk {
   using Off = std::conditional_t<kFast, uint32_t, int64_t>;
@@ -289,7 +288,6 @@ struct Fp8Path {
             ks[g][u] = __shfl_sync(0xffffffffu, walk.ks, g * 16 + u * 8 + r);
             vs[g][u] = __shfl_sync(0xffffffffu, walk.vs, g * 16 + u * 8 + r);
           }
-        walk.turn();
       }
     };
     auto load_keys = [&] {
@@ -326,6 +324,7 @@ struct Fp8Path {
     }
     walk.turn();
     advance();
+    if constexpr (!kFast) walk.turn();
     load_keys();
     for (int k = k0; k < k1; k += kKeys) {
       uint32_t there = 0xffffffffu;  // keys that count
@@ -464,6 +463,8 @@ struct Fp8Path {
             }
           }
       }
+      // (At the end: next to the step's other loads it waits for them.  64 sequences in pages of 5 slots 78 us for 86.)
+      if constexpr (!kFast) walk.turn();
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t)
